@@ -13,6 +13,9 @@ raises.
     q8h, sqh = fa.attn_quantize_fp8_hadamard(q)              # rotate rows, then quantise (Q, K)
     o, lse = fa.attn_fwd_bf16_varlen(qp, kp, vp, cu, max_len) # packed [T, H, d], int32 offsets
     o, lse = fa.attn_decode_bf16_paged(q1, kc, vc, table, lens) # decoding step, paged KV cache
+    lens, free, cu, slots, pos, ok = fa.attn_paged_plan(new, lens, table, pages, free, 64, T)
+    fa.attn_cache_append_fp8(k, v, kc8, vc8, ks, vs, slots)  # k, v: [T, Hkv, d], 8-bit paged cache
+    o, lse = fa.attn_decode_fp8_paged(q1, kc8, vc8, ks, vs, table, lens)
 """
 from __future__ import annotations
 
@@ -30,6 +33,8 @@ __all__ = [
     "attn_bwd_bf16", "attn_bwd_workspace_bytes", "attn_bwd_bf16_varlen",
     "attn_fwd_bf16_varlen", "attn_decode_bf16_paged", "attn_decode_bf16_paged_noalloc",
     "attn_decode_workspace_bytes",
+    "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
+    "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes",
     "attn_quantize_fp8_blockwise", "attn_quantize_fp8_hadamard", "attn_fwd_fp8",
     "attn_quantize_fp8_blockwise_fmt", "attn_fwd_fp8_fmt", "attn_fwd_fp8_blocks",
     "attn_fp8_qk_block_rows", "attn_fwd_schedule", "ATTN_FP8_E4M3", "ATTN_FP8_E5M2",
@@ -58,6 +63,8 @@ EXPORTED_SYMBOLS = (
     "attn_fwd_bf16_varlen",
     "attn_decode_bf16_paged",
     "attn_decode_bf16_paged_noalloc", "attn_decode_workspace_bytes",
+    "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
+    "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes",
     "attn_quantize_fp8_blockwise", "attn_quantize_fp8_blockwise_fmt",
     "attn_quantize_fp8_hadamard",
     "attn_fwd_fp8", "attn_fwd_fp8_fmt", "attn_fwd_fp8_blocks", "attn_fp8_qk_block_rows",
@@ -113,6 +120,17 @@ def load_library(path: str | None = None):
         lib.attn_decode_bf16_paged_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i,
                                                        i, i, f, i, vp]
         lib.attn_decode_bf16_paged_noalloc.restype = i
+        ll = ctypes.c_longlong
+        lib.attn_paged_plan.argtypes = [vp] * 11 + [i, i, i, i, i, vp]
+        lib.attn_paged_plan.restype = i
+        lib.attn_cache_append_bf16.argtypes = [vp] * 5 + [i, i, i, ll, ll, i, i, vp]
+        lib.attn_cache_append_bf16.restype = i
+        lib.attn_cache_append_fp8.argtypes = [vp] * 7 + [i, i, i, ll, ll, i, i, i, i, vp]
+        lib.attn_cache_append_fp8.restype = i
+        lib.attn_decode_fp8_workspace_bytes.argtypes = [i, i, i, i]
+        lib.attn_decode_fp8_workspace_bytes.restype = ctypes.c_size_t
+        lib.attn_decode_fp8_paged.argtypes = ([vp] * 9 + [i] * 10 + [f, i, vp, ctypes.c_size_t, vp])
+        lib.attn_decode_fp8_paged.restype = i
         lib.attn_quantize_fp8_blockwise.argtypes = [vp, vp, vp, i, i, i, i, i, vp]
         lib.attn_quantize_fp8_blockwise.restype = i
         lib.attn_quantize_fp8_hadamard.argtypes = [vp, vp, vp, i, i, i, i, i, vp]
@@ -382,6 +400,201 @@ def attn_decode_bf16_paged_noalloc(q, k_cache, v_cache, page_table, seq_lens,
         seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, nq, d, page_size, num_pages,
         max_pages, float(scale), int(num_splits), _stream_handle(stream))
     _raise_if(st, "attn_decode_bf16_paged_noalloc")
+    return o, lse
+
+
+def _on(device, stream):
+    """The guard and stream handle of a call whose tensors live on `device`: the library
+    launches on the current device, on the given stream or that device's current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.device(device), int(stream.cuda_stream)
+
+
+def _check_cuda(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+
+
+def attn_paged_plan(new_lens, seq_lens, page_table, free_pages, free_count, page_size: int,
+                    num_tokens: int, seq_lens_out=None, free_count_out=None, cu_new=None,
+                    slot_map=None, positions=None, served=None, stream=None):
+    """Pages, slots, positions and lengths of one serving step.  new_lens, seq_lens: int32
+    [B] (tokens each request adds, and has cached); page_table: int32 [B, max_pages],
+    updated in place; free_pages: int32 stack of free pages of which free_count (int32 [1])
+    are left; num_tokens: packed rows of the step, at least the sum of new_lens.  Returns
+    (seq_lens_out, free_count_out, cu_new, slot_map int64 [num_tokens], positions, served).
+    seq_lens_out may be seq_lens and free_count_out free_count (in place)."""
+    _check_cuda(new_lens, "new_lens")
+    dev, i32 = new_lens.device, torch.int32
+    B, T = new_lens.numel(), int(num_tokens)
+    _check_out(new_lens, (B,), i32, dev, "new_lens")
+    _check_out(seq_lens, (B,), i32, dev, "seq_lens")
+    _check_out(free_count, (1,), i32, dev, "free_count")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise TypeError("page_table must be an int32 [B, max_pages] tensor")
+    max_pages = page_table.shape[1]
+    _check_out(page_table, (B, max_pages), i32, dev, "page_table")
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise TypeError("free_pages must be an int32 [capacity] tensor")
+    _check_out(free_pages, (free_pages.numel(),), i32, dev, "free_pages")
+    if T < 0:
+        raise ValueError("num_tokens must not be negative")
+    outs = []
+    for name, t, shape, dtype in (("seq_lens_out", seq_lens_out, (B,), i32),
+                                  ("free_count_out", free_count_out, (1,), i32),
+                                  ("cu_new", cu_new, (B + 1,), i32),
+                                  ("slot_map", slot_map, (T,), torch.int64),
+                                  ("positions", positions, (T,), i32),
+                                  ("served", served, (B,), i32)):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _check_out(t, shape, dtype, dev, name)
+        outs.append(t)
+    guard, s = _on(dev, stream)
+    with guard:
+        st = load_library().attn_paged_plan(
+            new_lens.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), free_pages.data_ptr(),
+            free_count.data_ptr(), *(t.data_ptr() for t in outs), B, int(page_size), max_pages,
+            free_pages.numel(), T, s)
+    _raise_if(st, "attn_paged_plan")
+    return tuple(outs)
+
+
+def _append_args(k, v, k_cache, v_cache, slot_map, cache_dtype):
+    _check_cuda(k, "k")
+    dev = k.device
+    for n, t in (("k", k), ("v", v)):
+        if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != dev
+                or t.dim() != 3):
+            raise TypeError(f"{n} must be a bf16 [T, Hkv, d] tensor on {dev}")
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    T, H, d = k.shape
+    strides = []
+    for n, t in (("k", k), ("v", v)):
+        if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+            raise ValueError(f"{n}: the heads of a token must be contiguous")
+        strides.append(t.stride(0) if T > 1 else max(H * d, 8))
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if (not isinstance(t, torch.Tensor) or t.dtype not in cache_dtype or t.device != dev
+                or t.dim() != 4 or not t.is_contiguous()):
+            raise TypeError(f"{n} must be a contiguous [num_pages, Hkv, page_size, d] tensor of "
+                            f"{cache_dtype[0]} on {dev}")
+    if v_cache.shape != k_cache.shape or k_cache.shape[1] != H or k_cache.shape[3] != d:
+        raise ValueError("the caches must be [num_pages, Hkv, page_size, d] with k's heads and d")
+    _check_out(slot_map, (T,), torch.int64, dev, "slot_map")
+    return dev, T, H, d, strides, k_cache.shape[2], k_cache.shape[0]
+
+
+def attn_cache_append_bf16(k, v, k_cache, v_cache, slot_map, stream=None):
+    """Write new keys and values (bf16 [T, Hkv, d]; tokens may be strided) to their slots
+    (int64 [T], page * page_size + row; -1 skips a token) in the bf16 caches
+    [num_pages, Hkv, page_size, d], in place.  Returns (k_cache, v_cache)."""
+    dev, T, H, d, strides, ps, pages = _append_args(k, v, k_cache, v_cache, slot_map,
+                                                    (torch.bfloat16,))
+    guard, s = _on(dev, stream)
+    with guard:
+        st = load_library().attn_cache_append_bf16(
+            k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            slot_map.data_ptr(), T, H, d, strides[0], strides[1], ps, pages, s)
+    _raise_if(st, "attn_cache_append_bf16")
+    return k_cache, v_cache
+
+
+_FP8_CACHE = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
+
+
+def _cache_block(k_cache, v_cache, k_scales, v_scales, fmt, dev):
+    """Rows per scale block, from the scales' shape; a typed cache has to hold fmt's codes."""
+    typed = torch.float8_e5m2 if _fp8_format(fmt) == ATTN_FP8_E5M2 else torch.float8_e4m3fn
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype not in (torch.uint8, typed):
+            raise TypeError(f"{n} holds {t.dtype}, not codes of {fmt!r}")
+    pages, H, ps, _ = k_cache.shape
+    if not isinstance(k_scales, torch.Tensor) or k_scales.dim() != 3 or k_scales.shape[2] < 1:
+        raise TypeError("k_scales must be a float32 [num_pages, Hkv, page_size / block] tensor")
+    nblk = k_scales.shape[2]
+    for n, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        _check_out(t, (pages, H, nblk), torch.float32, dev, n)
+    if ps % nblk:
+        raise ValueError("the scales' blocks must divide the page")
+    return ps // nblk
+
+
+def attn_cache_append_fp8(k, v, k_cache, v_cache, k_scales, v_scales, slot_map, fmt="e4m3",
+                          stream=None):
+    """Quantise new keys and values (bf16 [T, Hkv, d]) into their slots of an 8-bit paged
+    cache (codes [num_pages, Hkv, page_size, d], float32 scales [num_pages, Hkv,
+    page_size / block]), in place.  A block's scale grows with its largest value; its
+    earlier rows are then requantised.  Returns (k_cache, v_cache, k_scales, v_scales)."""
+    dev, T, H, d, strides, ps, pages = _append_args(k, v, k_cache, v_cache, slot_map, _FP8_CACHE)
+    block = _cache_block(k_cache, v_cache, k_scales, v_scales, fmt, dev)
+    guard, s = _on(dev, stream)
+    with guard:
+        st = load_library().attn_cache_append_fp8(
+            k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), slot_map.data_ptr(), T, H, d, strides[0],
+            strides[1], ps, pages, block, _fp8_format(fmt), s)
+    _raise_if(st, "attn_cache_append_fp8")
+    return k_cache, v_cache, k_scales, v_scales
+
+
+def attn_decode_fp8_workspace_bytes(H: int, Hkv: int, nq: int, d: int) -> int:
+    """Workspace bytes attn_decode_fp8_paged needs on the current device."""
+    return int(load_library().attn_decode_fp8_workspace_bytes(int(H), int(Hkv), int(nq), int(d)))
+
+
+def attn_decode_fp8_paged(q, k_cache, v_cache, k_scales, v_scales, page_table, seq_lens,
+                          fmt="e4m3", scale: float | None = None, window: int = 0,
+                          workspace=None, o=None, lse=None, stream=None):
+    """One decoding step over an 8-bit paged cache.  q: bf16 [B, H, nq, d] (the nq newest
+    tokens, nq <= 8); caches and scales as attn_cache_append_fp8 leaves them, with Hkv heads
+    (H a multiple of Hkv); page_table int32 [B, max_pages], seq_lens int32 [B] (the new
+    tokens included); window > 0: a query sees the last window + 1 keys.  Returns
+    O [B, H, nq, d] and the natural-log LSE [B, H, nq]."""
+    _check_bhnd("q", q, torch.bfloat16)
+    dev = q.device
+    B, H, nq, d = q.shape
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if (not isinstance(t, torch.Tensor) or t.dtype not in _FP8_CACHE or t.device != dev
+                or t.dim() != 4 or not t.is_contiguous()):
+            raise TypeError(f"{n} must be a contiguous 8-bit [num_pages, Hkv, page_size, d] tensor on {dev}")
+    if v_cache.shape != k_cache.shape or k_cache.shape[3] != d:
+        raise ValueError("the caches must be [num_pages, Hkv, page_size, d] with q's d")
+    pages, Hkv, ps, _ = k_cache.shape
+    block = _cache_block(k_cache, v_cache, k_scales, v_scales, fmt, dev)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise TypeError("page_table must be an int32 [B, max_pages] tensor")
+    _check_out(page_table, (B, page_table.shape[1]), torch.int32, dev, "page_table")
+    _check_out(seq_lens, (B,), torch.int32, dev, "seq_lens")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _check_out(o, (B, H, nq, d), torch.bfloat16, dev, "o")
+    if lse is None:
+        lse = torch.empty((B, H, nq), dtype=torch.float32, device=dev)
+    else:
+        _check_out(lse, (B, H, nq), torch.float32, dev, "lse")
+    guard, s = _on(dev, stream)
+    with guard:
+        if workspace is None:
+            nbytes = attn_decode_fp8_workspace_bytes(H, Hkv, nq, d)
+            workspace = torch.empty(max(nbytes // 4, 4), dtype=torch.float32, device=dev)
+        elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != dev:
+            raise TypeError(f"workspace must be a contiguous CUDA tensor on {dev}")
+        st = load_library().attn_decode_fp8_paged(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+            lse.data_ptr(), B, H, Hkv, nq, d, ps, pages, page_table.shape[1], block,
+            _fp8_format(fmt), float(scale), int(window), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), s)
+    _raise_if(st, "attn_decode_fp8_paged")
     return o, lse
 
 

@@ -16,6 +16,7 @@
 #include "../../include/attn.h"
 #include "attn_fwd.cuh"
 #include "attn_params.h"
+#include "paged_params.h"
 
 namespace gb300 {
 
@@ -25,6 +26,10 @@ cudaError_t launch_fp8_convert(uint32_t first, size_t count, int fmt, void* code
 cudaError_t launch_decode(const DecodeParams& p, int d, cudaStream_t stream);
 cudaError_t launch_decode_tc(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                              const DecodeParams& p, int d, int sm_count, cudaStream_t stream);
+cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream);
+cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_cache_append_fp8(const AppendParams& p, bool e5m2, cudaStream_t stream);
+cudaError_t launch_decode_fp8(const DecodeFp8Params& p, int d, bool e5m2, cudaStream_t stream);
 cudaError_t launch_bwd(const BwdMaps& m, const BwdParams& p, int d, int sm_count, cudaStream_t stream);
 
 // One status word per device: kernels write kStatusTimeout here when they give up.
@@ -898,4 +903,182 @@ extern "C" attn_status_t attn_bwd_bf16(const void* q, const void* k, const void*
 {
     return bwd_batched(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, B, H, N, d,
                        scale, causal, window, stream, kWaitTimeoutNs, 0);
+}
+
+// ------------------------------------------------------------------ paged 8-bit cache
+namespace {
+
+constexpr int kPlanMaxRequests = 16384;   // three ints of shared memory per request
+
+bool page_size_ok(int page_size, int least)
+{
+    return page_size >= least && page_size <= 65536 && (page_size & (page_size - 1)) == 0;
+}
+
+bool block_ok(int block, int page_size)
+{
+    return (block == 16 || block == 32 || block == 64 || block == 128) && block <= page_size;
+}
+
+bool format_ok(int format)
+{
+    return format == ATTN_FP8_E4M3 || format == ATTN_FP8_E5M2 || format == ATTN_FP8_E4M3_POW2;
+}
+
+// The checks both appends share; fills the shared fields.
+attn_status_t append_args(const void* k, const void* v, const void* k_cache, const void* v_cache,
+                          const long long* slot_map, int T, int Hkv, int d, long long k_stride,
+                          long long v_stride, int page_size, int num_pages, int least_page,
+                          AppendParams* p)
+{
+    if (T < 0 || Hkv < 1 || num_pages < 1) return ATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
+    if (!page_size_ok(page_size, least_page)) return ATTN_ERR_UNSUPPORTED;
+    if (Hkv > 65535 || (long long)num_pages * Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+    if (T == 0) return ATTN_OK;
+    if (!k || !v || !k_cache || !v_cache || !slot_map) return ATTN_ERR_INVALID_ARG;
+    if (k_stride < (long long)Hkv * d || v_stride < (long long)Hkv * d) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(slot_map, 8) || k_stride % 8 != 0 || v_stride % 8 != 0)
+        return ATTN_ERR_MISALIGNED;
+    std::memset(p, 0, sizeof(*p));
+    p->k = k;
+    p->v = v;
+    p->kc = const_cast<void*>(k_cache);
+    p->vc = const_cast<void*>(v_cache);
+    p->slot_map = slot_map;
+    p->k_stride = k_stride;
+    p->v_stride = v_stride;
+    p->T = T;
+    p->H = Hkv;
+    p->d = d;
+    p->log2_ps = page_log2(page_size);
+    p->num_slots = (long long)num_pages << p->log2_ps;
+    return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" attn_status_t attn_paged_plan(const int* new_lens, const int* seq_lens, int* page_table,
+                                         const int* free_pages, const int* free_count,
+                                         int* seq_lens_out, int* free_count_out, int* cu_new,
+                                         long long* slot_map, int* positions, int* served, int B,
+                                         int page_size, int max_pages, int free_capacity,
+                                         int num_tokens, void* stream)
+{
+    if (B < 1 || max_pages < 1 || free_capacity < 0 || num_tokens < 0) return ATTN_ERR_INVALID_ARG;
+    if (!new_lens || !seq_lens || !page_table || !free_count || !seq_lens_out || !free_count_out ||
+        !cu_new || !served || (free_capacity > 0 && !free_pages) ||
+        (num_tokens > 0 && (!slot_map || !positions)))
+        return ATTN_ERR_INVALID_ARG;
+    if (B > kPlanMaxRequests || !page_size_ok(page_size, 1)) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+    if (!aligned(new_lens, 4) || !aligned(seq_lens, 4) || !aligned(page_table, 4) ||
+        !aligned(free_pages, 4) || !aligned(free_count, 4) || !aligned(seq_lens_out, 4) ||
+        !aligned(free_count_out, 4) || !aligned(cu_new, 4) || !aligned(slot_map, 8) ||
+        !aligned(positions, 4) || !aligned(served, 4))
+        return ATTN_ERR_MISALIGNED;
+    const PlanParams p = {new_lens, seq_lens, page_table, free_pages, free_count, seq_lens_out,
+                          free_count_out, cu_new, slot_map, positions, served, B,
+                          page_log2(page_size), max_pages, free_capacity, num_tokens};
+    return launch_paged_plan(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK
+                                                                                   : ATTN_ERR_CUDA;
+}
+
+extern "C" attn_status_t attn_cache_append_bf16(const void* k, const void* v, void* k_cache,
+                                                void* v_cache, const long long* slot_map, int T,
+                                                int Hkv, int d, long long k_stride,
+                                                long long v_stride, int page_size, int num_pages,
+                                                void* stream)
+{
+    AppendParams p;
+    const attn_status_t st = append_args(k, v, k_cache, v_cache, slot_map, T, Hkv, d, k_stride,
+                                         v_stride, page_size, num_pages, 1, &p);
+    if (st != ATTN_OK || T == 0) return st;
+    return launch_cache_append_bf16(p, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" attn_status_t attn_cache_append_fp8(const void* k, const void* v, void* k_cache,
+                                               void* v_cache, float* k_scales, float* v_scales,
+                                               const long long* slot_map, int T, int Hkv, int d,
+                                               long long k_stride, long long v_stride,
+                                               int page_size, int num_pages, int block,
+                                               int format, void* stream)
+{
+    if (!format_ok(format)) return ATTN_ERR_INVALID_ARG;
+    AppendParams p;
+    const attn_status_t st = append_args(k, v, k_cache, v_cache, slot_map, T, Hkv, d, k_stride,
+                                         v_stride, page_size, num_pages, 16, &p);
+    if (st != ATTN_OK) return st;
+    if (!block_ok(block, page_size)) return ATTN_ERR_UNSUPPORTED;
+    if (T == 0) return ATTN_OK;
+    if (!k_scales || !v_scales) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(k_scales, 4) || !aligned(v_scales, 4)) return ATTN_ERR_MISALIGNED;
+    p.ks = k_scales;
+    p.vs = v_scales;
+    p.log2_blk = page_log2(block);
+    p.pow2 = format == ATTN_FP8_E4M3_POW2 ? 1 : 0;
+    return launch_cache_append_fp8(p, format == ATTN_FP8_E5M2, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" size_t attn_decode_fp8_workspace_bytes(int H, int Hkv, int nq, int d)
+{
+    if (H < 1 || Hkv < 1 || nq < 1 || d < 1) return 0;
+    return 0;
+}
+
+extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cache,
+                                               const void* v_cache, const float* k_scales,
+                                               const float* v_scales, const int* page_table,
+                                               const int* seq_lens, void* o, float* lse, int B,
+                                               int H, int Hkv, int nq, int d, int page_size,
+                                               int num_pages, int max_pages, int block, int format,
+                                               float scale, int window, void* workspace,
+                                               size_t workspace_bytes, void* stream)
+{
+    if (!q || !k_cache || !v_cache || !k_scales || !v_scales || !page_table || !seq_lens || !o || !lse)
+        return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || H < 1 || Hkv < 1 || nq < 1 || num_pages < 1 || max_pages < 1 || H % Hkv != 0 ||
+        !format_ok(format))
+        return ATTN_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
+    if (nq > 8 || !page_size_ok(page_size, 16) || !block_ok(block, page_size))
+        return ATTN_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page_size > 0x7fffffffLL ||
+        (long long)num_pages * Hkv > 0x7fffffffLL || (long long)B * H > 0x7fffffffLL / nq)
+        return ATTN_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) ||
+        !aligned(lse, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
+        !aligned(k_scales, 4) || !aligned(v_scales, 4) || (workspace && !aligned(workspace, 16)))
+        return ATTN_ERR_MISALIGNED;
+    if (attn_decode_fp8_workspace_bytes(H, Hkv, nq, d) > (workspace ? workspace_bytes : 0))
+        return ATTN_ERR_INVALID_ARG;
+    DecodeFp8Params p;
+    std::memset(&p, 0, sizeof(p));
+    p.q = q;
+    p.kc = static_cast<const uint8_t*>(k_cache);
+    p.vc = static_cast<const uint8_t*>(v_cache);
+    p.ks = k_scales;
+    p.vs = v_scales;
+    p.page_table = page_table;
+    p.seq_lens = seq_lens;
+    p.o = o;
+    p.lse = lse;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.nq = nq;
+    p.rows = H / Hkv * nq;
+    p.log2_ps = page_log2(page_size);
+    p.log2_blk = page_log2(block);
+    p.num_pages = num_pages;
+    p.max_pages = max_pages;
+    p.window = window > 0 ? window : 0;
+    p.c_log2 = (float)((double)scale * 1.4426950408889634);
+    return launch_decode_fp8(p, d, format == ATTN_FP8_E5M2, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? ATTN_OK : ATTN_ERR_CUDA;
 }

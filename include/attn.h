@@ -350,6 +350,120 @@ attn_status_t attn_fwd_fp8_blocks(const void* q8, const void* k8, const void* v8
                                   int N, int d, float scale, int causal, int window,
                                   int qk_format, int v_format, int qk_block, void* stream);
 
+/*
+ * attn_paged_plan -- the pages, slots, positions and lengths of one serving step over a
+ * paged KV cache, from the lengths of its requests, on the device.
+ *
+ * [WGC] 局限性与后续方向 item 2 (PagedAttention KV-cache management).  Request b has
+ * L = seq_lens[b] cached tokens and adds n = new_lens[b] (0 allowed, a negative count is 0);
+ * the step's new tokens are packed request after request.  Requests take pages from the top
+ * of a stack of free ones, in order: the k-th page taken is free_pages[count - 1 - k].  A
+ * request is served when its tokens fit into its row of the table and into num_tokens and
+ * its pages are there; one that is not keeps its length and takes no page, and its tokens
+ * get no slot (the ones behind it that need no page are still served).
+ *   new_lens, seq_lens : const int32 [B]; L is clamped to [0, max_pages * page_size]
+ *   page_table     : int32 [B, max_pages]; the entries of the pages taken are written, the
+ *                    others left as they are
+ *   free_pages     : const int32 [free_capacity]; free_count : const int32 [1], clamped to
+ *                    [0, free_capacity]
+ *   seq_lens_out   : int32 [B], written: L + n, or L when not served (may be seq_lens)
+ *   free_count_out : int32 [1], written: free pages left (may be free_count)
+ *   cu_new         : int32 [B + 1], written: first packed row of each request (at most
+ *                    num_tokens), as attn_fwd_bf16_varlen's cu_seqlens
+ *   slot_map       : int64 [num_tokens], written: page * page_size + row of each packed
+ *                    token, -1 for tokens not served and for rows behind the last request
+ *   positions      : int32 [num_tokens], written: position in the request, or -1 likewise
+ *   served         : int32 [B], written: 1 or 0
+ *   B <= 16384, page_size a power of two <= 65536 (else ATTN_ERR_UNSUPPORTED)
+ * Besides the two pairs named, no output may overlap an input.  Called again on the same
+ * inputs (outputs elsewhere) it gives the same outputs.  slot_map is 8-byte aligned.
+ */
+attn_status_t attn_paged_plan(const int* new_lens, const int* seq_lens, int* page_table,
+                              const int* free_pages, const int* free_count, int* seq_lens_out,
+                              int* free_count_out, int* cu_new, long long* slot_map,
+                              int* positions, int* served, int B, int page_size, int max_pages,
+                              int free_capacity, int num_tokens, void* stream);
+
+/*
+ * attn_cache_append_bf16 -- writes new keys and values into the cache that
+ * attn_decode_bf16_paged reads ([JJ] §3 总结: the cache of earlier keys and values).
+ *   k, v     : const bf16 [T, Hkv, d], token rows k_stride and v_stride elements apart
+ *              (at least Hkv * d, multiples of 8: columns of a larger matrix are fine)
+ *   k_cache, v_cache : bf16 [num_pages, Hkv, page_size, d], written at the slots
+ *   slot_map : const int64 [T]: token t goes to row slot % page_size of page
+ *              slot / page_size; a slot outside the cache (-1 for padding) is skipped
+ *   d in {64, 128, 256}; page_size a power of two <= 65536; T == 0 returns ATTN_OK
+ * A slot named twice holds one of its tokens' rows, K and V not necessarily the same one's.
+ */
+attn_status_t attn_cache_append_bf16(const void* k, const void* v, void* k_cache, void* v_cache,
+                                     const long long* slot_map, int T, int Hkv, int d,
+                                     long long k_stride, long long v_stride, int page_size,
+                                     int num_pages, void* stream);
+
+/*
+ * attn_cache_append_fp8 -- quantises new keys and values into an 8-bit cache with one scale
+ * per head and block of `block` slots, which grows as the block fills.
+ *
+ * [WGC] §3 FP8 量化与精度保持 and [JJ] §1 item 3 (a scale per block), for a cache that is
+ * filled a few tokens at a time.  For each head, tensor and block that the call writes, let
+ * o be the first row written in the block and a the largest finite |x| of the rows written:
+ *     need = a / 448 (E5M2: a / 57344), IEEE fp32; for ATTN_FP8_E4M3_POW2 the smallest
+ *            power of two at or above it
+ *     s    = max(need, o > 0 ? the block's scale : 0)
+ *     if o > 0 and the scale grew: rows 0 .. o - 1 become code((code * old scale) / s)
+ *     the rows written become code(x / s), the block's scale s (0 while all rows are 0)
+ * with IEEE fp32 products and quotients and code() rounding to nearest even, saturating
+ * (an infinity saturates too, NaN stays NaN; neither enters the scale).  Rows behind the
+ * ones written are left as they were; a block's scale is read only when o > 0, so a new
+ * page needs no clearing.
+ *   k, v, slot_map, T, Hkv, d, k_stride, v_stride : as attn_cache_append_bf16
+ *   k_cache, v_cache   : uint8 codes [num_pages, Hkv, page_size, d]
+ *   k_scales, v_scales : float [num_pages, Hkv, page_size / block]
+ *   block  : 16, 32, 64 or 128, at most page_size; page_size a power of two, 16 .. 65536
+ *   format : an attn_fp8_format_t, the same in every call on a cache
+ * The tokens of one block must be consecutive in the call, in ascending slots, as
+ * attn_paged_plan packs them; otherwise that block's rows and scale are unspecified (no
+ * other block's are).
+ */
+attn_status_t attn_cache_append_fp8(const void* k, const void* v, void* k_cache, void* v_cache,
+                                    float* k_scales, float* v_scales, const long long* slot_map,
+                                    int T, int Hkv, int d, long long k_stride, long long v_stride,
+                                    int page_size, int num_pages, int block, int format,
+                                    void* stream);
+
+/*
+ * attn_decode_fp8_paged -- attn_decode_bf16_paged over the cache attn_cache_append_fp8
+ * fills, with query heads that may share key heads and an optional sliding window.
+ *
+ * [JJ] §3 总结, §1.5; [WGC] 局限性与后续方向 item 2.  Query head h reads key head
+ * h / (H / Hkv).  For sequence b with seq_lens[b] = L, query i is the token at position
+ * p = L - nq + i and attends to keys 0 .. p, or max(0, p - window) .. p when window > 0:
+ *     s_j = scale * k_scale(j) * (q . k8_j),  O = softmax(s) (v_scale v8),  LSE = ln sum e^s
+ *   q          : const bf16 [B, H, nq, d]; 1 <= nq <= 8; H a multiple of Hkv
+ *   k_cache, v_cache, k_scales, v_scales, block, format : as attn_cache_append_fp8 left
+ *                them; scales are finite and >= 0
+ *   page_table, seq_lens, max_pages, num_pages : as attn_decode_bf16_paged
+ *   o, lse     : bf16 [B, H, nq, d], float [B, H, nq], written; a query that sees no key
+ *                gets O = 0, LSE = -inf
+ *   d in {64, 128, 256}
+ *   workspace  : device memory of attn_decode_fp8_workspace_bytes(...) bytes, 16-byte
+ *                aligned (may be NULL when that is 0); its contents before and after do
+ *                not matter.  Calls that may overlap need one each.
+ * What the cache holds at keys a query does not see (rows behind the sequence, pages
+ * behind it or before its window) never reaches that query's outputs, NaN codes and
+ * scales included.  The queries and the codes enter the products exactly; scores, sums and
+ * O are fp32, the weights of the second product are rounded to fp16.
+ * HBM-bound: every key and value code that a query sees is read once per call.
+ */
+size_t attn_decode_fp8_workspace_bytes(int H, int Hkv, int nq, int d);
+attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cache, const void* v_cache,
+                                    const float* k_scales, const float* v_scales,
+                                    const int* page_table, const int* seq_lens, void* o,
+                                    float* lse, int B, int H, int Hkv, int nq, int d,
+                                    int page_size, int num_pages, int max_pages, int block,
+                                    int format, float scale, int window, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 /* Static English text for a status code (never NULL). */
 const char* attn_status_string(attn_status_t status);
 

@@ -1,0 +1,546 @@
+"""GPU parity of the paged-cache operators (attn_paged_plan, attn_cache_append_bf16,
+attn_cache_append_fp8, attn_decode_fp8_paged) against plain implementations, at the sizes,
+masks and contents where they can go wrong."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import paged_reference as ref
+from tests.conftest import require_gpu
+
+pytestmark = pytest.mark.gpu
+FORMATS = ["e4m3", "e5m2", "e4m3_pow2"]
+
+
+@pytest.fixture(scope="module")
+def fa():
+    require_gpu()
+    import exact_attention_55_gb300 as fa
+    fa.load_library()
+    return fa
+
+
+def cuda(a, dtype=None):
+    t = torch.from_numpy(np.array(a))
+    return (t if dtype is None else t.to(dtype)).cuda()
+
+
+# ------------------------------------------------------------------ plan
+def plan_case(rng, B, ps, max_pages, hi_len, hi_new, free, pad):
+    seq = rng.integers(0, hi_len + 1, B).astype(np.int32)
+    new = rng.integers(0, hi_new + 1, B).astype(np.int32)
+    owned = B * max_pages
+    table = rng.permutation(owned).astype(np.int32).reshape(B, max_pages)
+    stack = (owned + rng.permutation(max(free, 1))).astype(np.int32)
+    return new, seq, table, stack, np.array([free], np.int32), ps, int(new.sum()) + pad
+
+
+def run_plan(fa, new, seq, table, stack, count, ps, T, **kw):
+    t = [cuda(a) for a in (new, seq, table, stack, count)]
+    outs = fa.attn_paged_plan(*t, ps, T, **kw)
+    got = dict(zip(("seq_lens", "free_count", "cu_new", "slot_map", "positions", "served"), outs), page_table=t[2])
+    torch.cuda.synchronize()
+    return {k: v.cpu().numpy() for k, v in got.items()}
+
+
+def check_plan(fa, case):
+    want, got = ref.plan(*case), run_plan(fa, *case)
+    for k in want:
+        np.testing.assert_array_equal(got[k], want[k], err_msg=k)
+
+
+@pytest.mark.parametrize("B", [1, 2, 31, 129, 700, 5000, 16384])
+@pytest.mark.parametrize("ps", [1, 16, 64])
+def test_plan(fa, B, ps):
+    rng = np.random.default_rng(B + ps)
+    width = -(-70 // ps)
+    check_plan(fa, plan_case(rng, B, ps, width, 40, 30, B * width, pad=B % 3))
+
+
+@pytest.mark.parametrize("free", [0, 1, 7, 40, 41])
+def test_plan_with_too_few_pages(fa, free):
+    """The pool runs out on the way: later requests that need no page are still served."""
+    rng = np.random.default_rng(free)
+    check_plan(fa, plan_case(rng, 60, 16, 8, 90, 30, free, pad=5))
+
+
+def test_plan_of_long_requests(fa):
+    """Many tokens of few requests (several CTAs), a request that overruns its table, one
+    that adds nothing, negative lengths and counts, a page table entry below zero."""
+    rng = np.random.default_rng(3)
+    new = np.array([9000, 0, 20000, -5, 12345, 1, 6], np.int32)
+    seq = np.array([17, 30, 64, 12, -9, 2 ** 31 - 1, 20], np.int32)
+    table = rng.permutation(7 * 400).astype(np.int32).reshape(7, 400)
+    table[6, 1] = -1
+    stack = (5000 + rng.permutation(4000)).astype(np.int32)
+    for T in (int(new.clip(0).sum()), int(new.clip(0).sum()) + 1000, 29001, 0):
+        check_plan(fa, (new, seq, table, stack, np.array([3900], np.int32), 64, T))
+    check_plan(fa, (new, seq, table, stack, np.array([99999], np.int32), 64, 41352))
+    check_plan(fa, (new, seq, table, stack, np.array([-4], np.int32), 64, 41352))
+
+
+def test_plan_in_place_and_again(fa):
+    """seq_lens and free_count may be their own outputs; steps follow one another."""
+    rng = np.random.default_rng(4)
+    new, seq, table, stack, count, ps, _ = plan_case(rng, 300, 16, 30, 40, 20, 3000, 0)
+    t = [cuda(a) for a in (new, seq, table, stack, count)]
+    for step in range(4):
+        T = int(new.sum())
+        want = ref.plan(new, seq, table, stack, count, ps, T)
+        outs = fa.attn_paged_plan(*t, ps, T, seq_lens_out=t[1], free_count_out=t[4])
+        torch.cuda.synchronize()
+        seq, table, count = want["seq_lens"], want["page_table"], want["free_count"]
+        np.testing.assert_array_equal(t[1].cpu().numpy(), seq)
+        np.testing.assert_array_equal(t[2].cpu().numpy(), table)
+        np.testing.assert_array_equal(t[4].cpu().numpy(), count)
+        np.testing.assert_array_equal(outs[3].cpu().numpy(), want["slot_map"])
+
+
+# ------------------------------------------------------------------ appends
+def slots_of(rng, lens, news, ps, pad=0, spare=3):
+    need = [-(-(L + n) // ps) for L, n in zip(lens, news)]
+    pages, used, slots = sum(need) + spare, 0, []
+    perm = rng.permutation(pages)
+    for L, n, c in zip(lens, news, need):
+        own = perm[used:used + c]
+        used += c
+        pos = np.arange(L, L + n)
+        slots.append(own[pos // ps] * ps + pos % ps)
+    return pages, np.concatenate(slots + [np.full(pad, -1)]).astype(np.int64)
+
+
+def rows_of(rng, T, H, d, outliers=True):
+    x = rng.standard_normal((T, H, d)).astype(np.float32)
+    if outliers:
+        x[rng.random(x.shape) < 2e-3] *= 30
+    return torch.from_numpy(x).bfloat16()
+
+
+def strided(k, v, how):
+    """K and V as separate tensors, or as columns of one wider matrix."""
+    if how == "whole":
+        return k.cuda(), v.cuda()
+    T, H, d = k.shape
+    wide = torch.full((T, 2 * H * d + 8), float("nan"), dtype=torch.bfloat16)
+    wide[:, :H * d], wide[:, H * d + 8:] = k.reshape(T, -1), v.reshape(T, -1)
+    wide = wide.cuda()
+    return wide[:, :H * d].unflatten(1, (H, d)), wide[:, H * d + 8:].unflatten(1, (H, d))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("ps", [1, 16, 128])
+@pytest.mark.parametrize("how", ["whole", "columns"])
+def test_append_bf16(fa, d, ps, how):
+    rng = np.random.default_rng(d + ps)
+    pages, slots = slots_of(rng, [0, 5, 130, 17], [1, 40, 3, 200], ps, pad=2)
+    slots[3] = pages * ps            # outside the cache: skipped
+    k, v = rows_of(rng, len(slots), 3, d), rows_of(rng, len(slots), 3, d)
+    kc, vc = (torch.randn(pages, 3, ps, d).bfloat16() for _ in range(2))
+    want = [kc.clone(), vc.clone()]
+    for t, s in enumerate(slots):
+        if 0 <= s < pages * ps:
+            want[0][s // ps, :, s % ps], want[1][s // ps, :, s % ps] = k[t], v[t]
+    kd, vd = strided(k, v, how)
+    got = fa.attn_cache_append_bf16(kd, vd, kc.cuda(), vc.cuda(), cuda(slots))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0].cpu(), want[0]) and torch.equal(got[1].cpu(), want[1])
+
+
+def check_append_fp8(fa, rng, slots, pages, H, d, ps, block, fmt, how="whole", k=None, v=None, prior=None):
+    T = len(slots)
+    k = rows_of(rng, T, H, d) if k is None else k
+    v = rows_of(rng, T, H, d) if v is None else v
+    if prior is None:
+        codes = [rng.integers(0, 256, (pages, H, ps, d)).astype(np.uint8) for _ in range(2)]
+        scales = [np.exp2(rng.uniform(-12, -4, (pages, H, ps // block))).astype(np.float32) for _ in range(2)]
+        for c in codes:       # old rows hold finite codes
+            c[(c & 0x7F) >= (0x7C if fmt == "e5m2" else 0x7F)] = 0x11
+        if fmt == "e4m3_pow2":
+            scales = [np.exp2(np.round(np.log2(s))).astype(np.float32) for s in scales]
+    else:
+        codes, scales = prior
+    dev = [cuda(c) for c in codes + scales]
+    kd, vd = strided(k, v, how)
+    fa.attn_cache_append_fp8(kd, vd, dev[0], dev[1], dev[2], dev[3], cuda(slots), fmt=fmt)
+    torch.cuda.synchronize()
+    for x, c, s in ((k, codes[0], scales[0]), (v, codes[1], scales[1])):
+        ref.append_fp8(x.float().numpy(), c, s, slots, fmt)
+    for n, got, want in zip(("k_scales", "v_scales", "k", "v"), (dev[2], dev[3], dev[0], dev[1]),
+                            (scales[0], scales[1], codes[0], codes[1])):
+        np.testing.assert_array_equal(got.cpu().numpy(), want, err_msg=n)
+    return codes, scales
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("d,ps,block", [(64, 16, 16), (64, 64, 32), (128, 64, 64), (128, 256, 128), (256, 128, 128),
+                                        (256, 32, 16)])
+def test_append_fp8(fa, fmt, d, ps, block):
+    rng = np.random.default_rng(d + ps + block)
+    lens = [0, 1, 15, 16, 17, 63, 100, 127, 128, 200, 31]
+    news = [1, 1, 1, 1, 30, 2, 1, 1, 128, 77, 300]
+    pages, slots = slots_of(rng, lens, news, ps, pad=3)
+    check_append_fp8(fa, rng, slots, pages, 3, d, ps, block, fmt, how="columns" if d == 128 else "whole")
+
+
+@pytest.mark.parametrize("block", [16, 64, 128])
+def test_append_fp8_one_token_each(fa, block):
+    """A decoding step: every token is a run of its own, some slots are padding in between."""
+    rng = np.random.default_rng(block)
+    lens = list(rng.integers(0, 300, 150))
+    pages, slots = slots_of(rng, lens, [1] * 150, 128)
+    slots[::7] = -1
+    slots[3] = pages * 128
+    slots[4] = 2 ** 40
+    check_append_fp8(fa, rng, slots, pages, 2, 128, 128, block, "e4m3")
+
+
+def test_append_fp8_step_by_step_is_deterministic(fa):
+    """A block that fills token by token, growing its scale on the way."""
+    rng = np.random.default_rng(9)
+    ps, H, d = 64, 2, 64
+    codes = [np.full((3, H, ps, d), 0x7F, np.uint8) for _ in range(2)]
+    scales = [np.full((3, H, 1), np.nan, np.float32) for _ in range(2)]
+    for t in range(70):
+        x = (rows_of(rng, 1, H, d).float() * 1.07 ** t).bfloat16()
+        slot = np.array([t if t < 64 else 2 * 64 + t - 64])
+        codes, scales = check_append_fp8(fa, rng, slot, 3, H, d, ps, ps, "e4m3", k=x, v=x * 3, prior=(codes, scales))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_append_fp8_unusual_values(fa, fmt):
+    """Zeros, infinities, NaN, the largest and the smallest bf16 values, and a block that is
+    all zero before its first other value."""
+    rng = np.random.default_rng(10)
+    T, H, d, ps = 96, 2, 64, 32
+    k = rows_of(rng, T, H, d)
+    k[0:32] = 0
+    k[33, 0, 5], k[34, 1, 6], k[35, 0, 7] = float("inf"), float("-inf"), float("nan")
+    k[64:80] *= 1e-38
+    k[80:96] = k[80:96].sign() * 3.3e38
+    v = k.flip(0).contiguous()
+    check_append_fp8(fa, rng, np.arange(T), 4, H, d, ps, 16, fmt, k=k, v=v)
+    zero = torch.zeros(4, H, d, dtype=torch.bfloat16)
+    prior = check_append_fp8(fa, rng, np.arange(4), 4, H, d, ps, 32, fmt, k=zero, v=zero)
+    check_append_fp8(fa, rng, np.arange(4, 12), 4, H, d, ps, 32, fmt, prior=prior)
+
+
+# ------------------------------------------------------------------ decoding
+def check_decode(fa, lens, H, Hkv, nq, d, ps, block, fmt, window=0, seed=0, qmul=1.0, stale=True, scale=None):
+    rng = np.random.default_rng(seed)
+    kc, vc, ks, vs, table = ref.make_cache(rng, lens, Hkv, d, ps, block, fmt, stale=stale)
+    q = (torch.from_numpy(rng.standard_normal((len(lens), H, nq, d)).astype(np.float32)) * qmul).bfloat16()
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    o, lse = fa.attn_decode_fp8_paged(q.cuda(), cuda(kc), cuda(vc), cuda(ks), cuda(vs), cuda(table),
+                                      cuda(np.array(lens, np.int32)), fmt=fmt, scale=scale, window=window)
+    assert fa.attn_get_device_status() == fa.ATTN_OK
+    compare_decode(o, lse, ref.decode_fp8(q.double().numpy(), kc, vc, ks, vs, table, lens, fmt, scale, window))
+
+
+def compare_decode(o, lse, want):
+    o, lse = o.cpu().double().numpy(), lse.cpu().double().numpy()
+    ro, rl, o_tol, l_tol = want
+    empty = np.isneginf(rl)
+    assert (np.isneginf(lse) == empty).all() and (o[empty] == 0).all()
+    assert np.isfinite(o).all()
+    off = np.abs(o - ro)
+    assert (off <= o_tol).all(), f"O: {(off / np.maximum(o_tol, 1e-300)).max()} of the bound"
+    off = np.abs(lse[~empty] - rl[~empty])
+    assert (off <= l_tol[~empty]).all(), f"LSE: {(off / l_tol[~empty]).max()} of the bound"
+
+
+LENS = [1, 0, 2, 15, 16, 17, 63, 64, 65, 127, 130, 500]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("nq,group", [(1, 1), (1, 4), (3, 2), (8, 1), (2, 8), (8, 5)])
+def test_decode_fp8(fa, d, fmt, nq, group):
+    check_decode(fa, LENS, 2 * group, 2, nq, d, 32, 16, fmt, seed=d + nq)
+
+
+@pytest.mark.parametrize("ps,block", [(16, 16), (64, 16), (64, 64), (128, 128), (256, 64), (1024, 128)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_decode_fp8_page_sizes(fa, ps, block, d):
+    check_decode(fa, [700, 33, 1025, 0, 1], 6, 3, 2, d, ps, block, "e4m3", seed=ps + block)
+
+
+@pytest.mark.parametrize("window", [1, 5, 16, 100, 127, 128, 400, 100000])
+@pytest.mark.parametrize("nq", [1, 4])
+def test_decode_fp8_window(fa, window, nq):
+    """Sliding windows; the pages before a window hold NaN codes and scales, as freed ones may."""
+    lens, d, ps, block = [1, 3, 100, 129, 600, 1111], 64, 32, 16
+    rng = np.random.default_rng(window)
+    kc, vc, ks, vs, table = ref.make_cache(rng, lens, 2, d, ps, block, "e4m3")
+    for b, L in enumerate(lens):
+        lo = max(0, L - nq - window)
+        for t in range(lo):
+            kc[table[b, t // ps], :, t % ps], vc[table[b, t // ps], :, t % ps] = 0x7F, 0xFF
+        for blk in range(lo // block):
+            ks[table[b, blk * block // ps], :, blk % (ps // block)] = np.nan
+            vs[table[b, blk * block // ps], :, blk % (ps // block)] = np.inf
+        table[b, :lo // ps] = -1
+    q = torch.from_numpy(rng.standard_normal((len(lens), 6, nq, d)).astype(np.float32)).bfloat16()
+    o, lse = fa.attn_decode_fp8_paged(q.cuda(), cuda(kc), cuda(vc), cuda(ks), cuda(vs), cuda(table),
+                                      cuda(np.array(lens, np.int32)), scale=0.125, window=window)
+    assert fa.attn_get_device_status() == fa.ATTN_OK
+    compare_decode(o, lse, ref.decode_fp8(q.double().numpy(), kc, vc, ks, vs, table, lens, "e4m3", 0.125, window))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 16, 17, 32, 33, 48, 100])
+def test_decode_fp8_many_query_heads(fa, rows, d):
+    """One key head under any number of query heads."""
+    check_decode(fa, [300, 64, 5], rows, 1, 1, d, 64, 64, "e4m3", seed=rows)
+
+
+def test_decode_fp8_long_and_ragged(fa):
+    """Sequences of very different lengths, many CTAs on one of them."""
+    check_decode(fa, [40001, 3, 7000, 1, 129, 12345], 4, 2, 1, 128, 64, 64, "e4m3_pow2", seed=11)
+    check_decode(fa, [20000], 8, 1, 2, 256, 128, 128, "e4m3", seed=12)
+    check_decode(fa, [9001] * 3, 3, 3, 1, 64, 16, 16, "e5m2", seed=13)
+
+
+@pytest.mark.parametrize("qmul", [0.0, 1e-30, 1e-4, 300.0, 1e30])
+def test_decode_fp8_query_magnitudes(fa, qmul):
+    """Queries far outside fp16's range keep their scores (softmax scale chosen to match)."""
+    check_decode(fa, [100, 17], 4, 2, 2, 128, 32, 32, "e4m3", qmul=qmul, seed=14,
+                 scale=0.1 / max(qmul, 1e-30) if qmul else 0.1)
+
+
+def test_decode_fp8_query_rows_of_mixed_magnitude(fa):
+    """Within a row: values down to 2^-20 of the row's largest still count."""
+    rng = np.random.default_rng(15)
+    d, lens = 128, [200]
+    kc, vc, ks, vs, table = ref.make_cache(rng, lens, 1, d, 32, 32, "e4m3")
+    q = rng.standard_normal((1, 4, 1, d)).astype(np.float32)
+    q[..., 1:] *= np.exp2(-rng.integers(0, 21, d - 1)).astype(np.float32)
+    q = torch.from_numpy(q).bfloat16()
+    o, lse = fa.attn_decode_fp8_paged(q.cuda(), cuda(kc), cuda(vc), cuda(ks), cuda(vs), cuda(table),
+                                      cuda(np.array(lens, np.int32)), scale=0.3)
+    compare_decode(o, lse, ref.decode_fp8(q.double().numpy(), kc, vc, ks, vs, table, lens, "e4m3", 0.3))
+
+
+def test_decode_fp8_scales_far_apart(fa):
+    """Blocks whose scales lie 2^40 apart, zero scales among them, in K and in V."""
+    rng = np.random.default_rng(16)
+    d, lens, fmt = 64, [300, 70], "e4m3"
+    kc, vc, ks, vs, table = ref.make_cache(rng, lens, 2, d, 32, 16, fmt)
+    ks[:], vs[:] = np.nan_to_num(ks, nan=0.01), np.nan_to_num(vs, nan=0.01)
+    vs *= np.exp2(rng.integers(-20, 21, vs.shape)).astype(np.float32)
+    vs[rng.random(vs.shape) < 0.2] = 0
+    ks[rng.random(ks.shape) < 0.2] = 0
+    q = torch.from_numpy(rng.standard_normal((2, 4, 1, d)).astype(np.float32)).bfloat16()
+    o, lse = fa.attn_decode_fp8_paged(q.cuda(), cuda(kc), cuda(vc), cuda(ks), cuda(vs), cuda(table),
+                                      cuda(np.array(lens, np.int32)), scale=0.125)
+    compare_decode(o, lse, ref.decode_fp8(q.double().numpy(), kc, vc, ks, vs, table, lens, fmt, 0.125))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_decode_fp8_nan_at_a_key_only_later_queries_see(fa, fmt, d):
+    """A NaN value at the newest token reaches the last query alone (and there only its own
+    coordinate); a NaN key reaches every query that sees it."""
+    rng = np.random.default_rng(17)
+    lens, nq, ps = [70, 64], 3, 32
+    kc, vc, ks, vs, table = ref.make_cache(rng, lens, 1, d, ps, 32, fmt)
+    clean = (vc.copy(), kc.copy())
+    for b, L in enumerate(lens):
+        vc[table[b, (L - 1) // ps], 0, (L - 1) % ps, 7] = 0x7F
+    kc[table[1, (lens[1] - 2) // ps], 0, (lens[1] - 2) % ps, 3] = 0xFF
+    q = torch.from_numpy(rng.standard_normal((2, 2, nq, d)).astype(np.float32)).bfloat16()
+    o, lse = fa.attn_decode_fp8_paged(q.cuda(), cuda(kc), cuda(vc), cuda(ks), cuda(vs), cuda(table),
+                                      cuda(np.array(lens, np.int32)), fmt=fmt, scale=0.1)
+    want = ref.decode_fp8(q.double().numpy(), clean[1], clean[0], ks, vs, table, lens, fmt, 0.1)
+    o, lse = o.cpu().double().numpy(), lse.cpu().double().numpy()
+    nan = np.zeros(o.shape, bool)
+    nan[0, :, 2, 7] = True
+    nan[1, :, 1:] = True
+    assert (np.isnan(o) == nan).all()
+    assert (np.abs(o - want[0]) <= want[2])[~nan].all()
+    seen = np.zeros(lse.shape, bool)
+    seen[1, :, 1:] = True
+    assert (np.isnan(lse) == seen).all() and (np.abs(lse - want[1]) <= want[3])[~seen].all()
+
+
+def test_decode_fp8_bad_page_numbers_stay_inside(fa):
+    """Page numbers far outside the cache and lengths beyond the table are clamped: values
+    are then unspecified, the call finishes, and later calls are right."""
+    rng = np.random.default_rng(18)
+    kc, vc, ks, vs, table = ref.make_cache(rng, [100, 40], 2, 64, 32, 32, "e4m3")
+    bad = table.copy()
+    bad[0, 1], bad[1, 0] = 2 ** 31 - 1, -2 ** 31
+    q = torch.randn(2, 2, 1, 64).bfloat16().cuda()
+    dev = [cuda(a) for a in (kc, vc, ks, vs)]
+    fa.attn_decode_fp8_paged(q, *dev, cuda(bad), cuda(np.array([2 ** 31 - 1, -7], np.int32)))
+    assert fa.attn_get_device_status() == fa.ATTN_OK
+    check_decode(fa, [100, 40], 2, 2, 1, 64, 32, 32, "e4m3", seed=19)
+
+
+# ------------------------------------------------------------------ together
+def serve(fa, fmt, steps, seed=0, graph=False):
+    """A small serving loop: a prefill step, then decoding steps; returns the outputs of every
+    step, the cache, and the keys and values that went in."""
+    rng = np.random.default_rng(seed)
+    B, H, Hkv, d, ps, block, pages, width = 5, 8, 2, 128, 32, 16, 64, 8
+    st = dict(seq=cuda(np.zeros(B, np.int32)), table=cuda(np.full((B, width), -1, np.int32)),
+              stack=cuda(rng.permutation(pages).astype(np.int32)), count=cuda(np.array([pages], np.int32)))
+    kc, vc = (torch.full((pages, Hkv, ps, d), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((pages, Hkv, ps // block), float("nan"), device="cuda") for _ in range(2))
+    history, outs = [[] for _ in range(B)], []
+    for step in range(steps):
+        new = np.array([70, 1, 33, 0, 128] if step == 0 else [1, 1, 1, 1, 1], np.int32)
+        T = int(new.sum()) + 2
+        k, v = rows_of(rng, T, Hkv, d), rows_of(rng, T, Hkv, d)
+        q = torch.from_numpy(rng.standard_normal((B, H, 1, d)).astype(np.float32)).bfloat16()
+        seq, count, cu, slots, pos, served = fa.attn_paged_plan(
+            cuda(new), st["seq"], st["table"], st["stack"], st["count"], ps, T,
+            seq_lens_out=st["seq"], free_count_out=st["count"])
+        fa.attn_cache_append_fp8(k.cuda(), v.cuda(), kc, vc, ks, vs, slots, fmt=fmt)
+        outs.append((q, *fa.attn_decode_fp8_paged(q.cuda(), kc, vc, ks, vs, st["table"], seq, fmt=fmt), seq.cpu()))
+        row = 0
+        for b in range(B):
+            history[b] += [(k[row + j], v[row + j]) for j in range(new[b])]
+            row += new[b]
+        assert served.all()
+    torch.cuda.synchronize()
+    return st, (kc, vc, ks, vs), outs, history
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_serving_loop(fa, fmt):
+    """Plan, append and decode as they are used together: the last step against attention over
+    the cache's own values, and those values against the keys and values that went in, off by
+    at most half a step of the format per rewriting of a block."""
+    steps = 20
+    st, cache, outs, history = serve(fa, fmt, steps)
+    kc, vc, ks, vs = (t.cpu().numpy() for t in cache)
+    table = st["table"].cpu().numpy()
+    q, o, lse, seq = outs[-1]
+    lens = seq.numpy()
+    assert lens.tolist() == [70 + 19, 1 + 19, 33 + 19, 19, 128 + 19]
+    compare_decode(o, lse, ref.decode_fp8(q.double().numpy(), kc, vc, ks, vs, table, lens, fmt, 1 / math.sqrt(128)))
+    half = 2.0 ** -3 if fmt == "e5m2" else 2.0 ** -4       # half a step relative to the value
+    least = 2.0 ** -17 if fmt == "e5m2" else 2.0 ** -10    # and below the normal numbers
+    for b, L in enumerate(lens):
+        t = np.arange(L)
+        page, row = table[b, t // 32], t % 32
+        for codes, s, which in ((kc, ks, 0), (vc, vs, 1)):
+            got = ref.decode(codes[page, :, row], fmt) * s[page, :, row // 16][..., None]
+            x = np.stack([h[which].float().numpy() for h in history[b]])
+            sc = s[page, :, row // 16][..., None]
+            assert (np.abs(got - x) <= 16 * (half * np.abs(x) + least * sc)).all()
+
+
+def test_serving_step_in_a_graph(fa):
+    """One captured step (plan, append, decode, all in place) replayed token after token gives
+    what the same steps give eagerly, and a second graph may share its buffers when they are
+    replayed in turn."""
+    B, H, Hkv, d, ps, pages, width = 6, 4, 2, 64, 16, 80, 12
+
+    def fresh():
+        rng = np.random.default_rng(21)
+        return dict(new=cuda(np.array([1, 1, 0, 1, 1, 1], np.int32)), seq=cuda(rng.integers(0, 40, B).astype(np.int32)),
+                    table=cuda(np.arange(B * width, dtype=np.int32).reshape(B, width) % 40),
+                    stack=cuda((40 + rng.permutation(40)).astype(np.int32)), count=cuda(np.array([40], np.int32)),
+                    kc=torch.full((pages, Hkv, ps, d), 0x20, dtype=torch.uint8, device="cuda"),
+                    vc=torch.full((pages, Hkv, ps, d), 0x21, dtype=torch.uint8, device="cuda"),
+                    ks=torch.full((pages, Hkv, 1), 0.01, device="cuda"), vs=torch.full((pages, Hkv, 1), 0.02, device="cuda"),
+                    k=torch.zeros(B, Hkv, d, dtype=torch.bfloat16, device="cuda"),
+                    v=torch.zeros(B, Hkv, d, dtype=torch.bfloat16, device="cuda"),
+                    q=torch.zeros(B, H, 1, d, dtype=torch.bfloat16, device="cuda"),
+                    o=torch.zeros(B, H, 1, d, dtype=torch.bfloat16, device="cuda"),
+                    lse=torch.zeros(B, H, 1, device="cuda"),
+                    ws=torch.empty(max(4, fa.attn_decode_fp8_workspace_bytes(H, Hkv, 1, d) // 4), device="cuda"))
+
+    def step(s):
+        out = fa.attn_paged_plan(s["new"], s["seq"], s["table"], s["stack"], s["count"], ps, B,
+                                 seq_lens_out=s["seq"], free_count_out=s["count"])
+        fa.attn_cache_append_fp8(s["k"], s["v"], s["kc"], s["vc"], s["ks"], s["vs"], out[3])
+        fa.attn_decode_fp8_paged(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["seq"], workspace=s["ws"],
+                                 o=s["o"], lse=s["lse"])
+
+    gen = torch.Generator().manual_seed(5)
+    inputs = [[torch.randn(t, generator=gen).bfloat16().cuda() for t in ((B, Hkv, d), (B, Hkv, d), (B, H, 1, d))]
+              for _ in range(12)]
+    eager, want = fresh(), []
+    for kvq in inputs:
+        for n, t in zip(("k", "v", "q"), kvq):
+            eager[n].copy_(t)
+        step(eager)
+        want.append((eager["o"].clone(), eager["lse"].clone()))
+    s = fresh()
+    warm = fresh()
+    step(warm)                                   # first calls outside capture
+    graphs = []
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(s)
+        graphs.append(g)
+    for i, kvq in enumerate(inputs):
+        for n, t in zip(("k", "v", "q"), kvq):
+            s[n].copy_(t)
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(s["o"], want[i][0]) and torch.equal(s["lse"], want[i][1]), i
+    for n in ("kc", "vc", "ks", "vs", "seq", "table", "count"):
+        assert torch.equal(s[n], eager[n]), n
+    assert fa.attn_get_device_status() == fa.ATTN_OK
+
+
+def test_calls_on_other_streams(fa):
+    """Concurrent streams, each with its own workspace, give the sequential results; a call
+    takes the stream it is given."""
+    rng = np.random.default_rng(22)
+    cases = []
+    for seed, (H, Hkv, d) in enumerate([(4, 2, 64), (8, 1, 128), (3, 3, 256)]):
+        lens = [3000, 17, 900]
+        kc, vc, ks, vs, table = ref.make_cache(rng, lens, Hkv, d, 32, 32, "e4m3")
+        q = torch.randn(3, H, 1, d, generator=torch.Generator().manual_seed(seed)).bfloat16()
+        cases.append([t.cuda() if isinstance(t, torch.Tensor) else cuda(t)
+                      for t in (q, kc, vc, ks, vs, table, np.array(lens, np.int32))])
+    want = [fa.attn_decode_fp8_paged(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    ws = [torch.empty(max(4, fa.attn_decode_fp8_workspace_bytes(c[0].shape[1], c[1].shape[1], 1, c[0].shape[3]) // 4),
+                      device="cuda") for c in cases]
+    for _ in range(3):
+        got = [fa.attn_decode_fp8_paged(*c, workspace=w, stream=s) for c, w, s in zip(cases, ws, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_refusals(fa):
+    """What the binding refuses on the device: types, shapes, a cache of the other format."""
+    q = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    c = torch.zeros(5, 2, 32, 64, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(5, 2, 2, device="cuda")
+    table, lens = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    ok = [q, c, c, s, s, table, lens]
+    fa.attn_decode_fp8_paged(*ok)
+    for i, t in ((0, q.float()), (0, q.transpose(1, 2)), (1, c[:, :1]), (1, c.view(torch.float8_e5m2)), (3, s[:, :, :1]),
+                 (4, s.double()), (5, table.long()), (5, table[:1]), (6, lens[:1]), (6, lens.cpu())):
+        bad = list(ok)
+        bad[i] = t
+        with pytest.raises((TypeError, ValueError, fa.AttnError)):   # AttnError: [2, 1, 4, 64] has 1 head over 2
+            fa.attn_decode_fp8_paged(*bad)
+    with pytest.raises(ValueError):
+        fa.attn_decode_fp8_paged(*ok, fmt="int8")
+    with pytest.raises(fa.AttnError):
+        fa.attn_decode_fp8_paged(q[:, :3].contiguous(), *ok[1:])             # 3 heads over 2
+    x, slots = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        fa.attn_cache_append_fp8(x.transpose(0, 1), x.transpose(0, 1), c, c, s, s, slots[:2])
+    with pytest.raises(TypeError):
+        fa.attn_cache_append_fp8(x, x, c, c, s, s, slots.int())
+    with pytest.raises(fa.AttnError):
+        fa.attn_cache_append_fp8(x[:1].expand(3, 2, 64), x, c, c, s, s, slots)  # tokens that overlap
+    with pytest.raises(TypeError):
+        fa.attn_cache_append_bf16(x, x, c, c, slots)
+    with pytest.raises(TypeError):
+        fa.attn_paged_plan(lens.long(), lens, table, lens, lens[:1], 16, 4)
+    assert fa.attn_get_device_status() == fa.ATTN_OK
