@@ -29,7 +29,9 @@ cudaError_t launch_decode_tc(const CUtensorMap& mq, const CUtensorMap& mk, const
 cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append_fp8(const AppendParams& p, bool e5m2, cudaStream_t stream);
-cudaError_t launch_decode_fp8(const DecodeFp8Params& p, int d, bool e5m2, cudaStream_t stream);
+int decode_fp8_row_tiles(int rows, int d);
+cudaError_t launch_decode_fp8(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeFp8Params& p,
+                              int d, bool e5m2, cudaStream_t stream);
 cudaError_t launch_bwd(const BwdMaps& m, const BwdParams& p, int d, int sm_count, cudaStream_t stream);
 
 // One status word per device: kernels write kStatusTimeout here when they give up.
@@ -1024,10 +1026,28 @@ extern "C" attn_status_t attn_cache_append_fp8(const void* k, const void* v, voi
                ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// The grid of an 8-bit decoding step: two CTAs per SM, shared out among the groups of rows.
+static void decode_fp8_grid(int rows, int d, int sm_count, int* ranges, int* row_groups)
+{
+    const int per = 8 * decode_fp8_row_tiles(rows, d);
+    *row_groups = (rows + per - 1) / per;
+    *ranges = 2 * sm_count / *row_groups > 1 ? 2 * sm_count / *row_groups : 1;
+}
+
+static size_t decode_fp8_ws_bytes(int rows, int d, int ranges, int row_groups)
+{
+    return (size_t)2 * ranges * row_groups * 8 * decode_fp8_row_tiles(rows, d) * (d + 2) * sizeof(float);
+}
+
 extern "C" size_t attn_decode_fp8_workspace_bytes(int H, int Hkv, int nq, int d)
 {
-    if (H < 1 || Hkv < 1 || nq < 1 || d < 1) return 0;
-    return 0;
+    if (H < 1 || Hkv < 1 || nq < 1 || nq > 8 || H % Hkv != 0) return 0;
+    if (d != 64 && d != 128 && d != 256) return 0;
+    DeviceInfo* dev = nullptr;
+    if (H / Hkv > 0x7fffffff / 8 || device_info(&dev) != ATTN_OK) return 0;
+    int ranges = 1, row_groups = 1;
+    decode_fp8_grid(H / Hkv * nq, d, dev->sm_count, &ranges, &row_groups);
+    return decode_fp8_ws_bytes(H / Hkv * nq, d, ranges, row_groups);
 }
 
 extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cache,
@@ -1055,8 +1075,20 @@ extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cach
         !aligned(lse, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
         !aligned(k_scales, 4) || !aligned(v_scales, 4) || (workspace && !aligned(workspace, 16)))
         return ATTN_ERR_MISALIGNED;
-    if (attn_decode_fp8_workspace_bytes(H, Hkv, nq, d) > (workspace ? workspace_bytes : 0))
+    DeviceInfo* dev = nullptr;
+    const attn_status_t st = device_info(&dev);
+    if (st != ATTN_OK) return st;
+    const int rows = H / Hkv * nq;
+    int ranges = 1, row_groups = 1;
+    decode_fp8_grid(rows, d, dev->sm_count, &ranges, &row_groups);
+    if (decode_fp8_ws_bytes(rows, d, ranges, row_groups) > (workspace ? workspace_bytes : 0))
         return ATTN_ERR_INVALID_ARG;
+    // the caches as (d, page_size, pages * Hkv), boxes of one page or 64 rows of a larger one
+    alignas(64) CUtensorMap mk, mv;
+    const int box = page_size < 64 ? page_size : 64, swz = d < 128 ? 64 : 128;
+    if (!encode_3d(&mk, k_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d, page_size, num_pages * Hkv, box, swz) ||
+        !encode_3d(&mv, v_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d, page_size, num_pages * Hkv, box, swz))
+        return ATTN_ERR_CUDA;
     DecodeFp8Params p;
     std::memset(&p, 0, sizeof(p));
     p.q = q;
@@ -1071,14 +1103,19 @@ extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cach
     p.B = B;
     p.Hkv = Hkv;
     p.nq = nq;
-    p.rows = H / Hkv * nq;
+    p.rows = rows;
     p.log2_ps = page_log2(page_size);
     p.log2_blk = page_log2(block);
     p.num_pages = num_pages;
     p.max_pages = max_pages;
     p.window = window > 0 ? window : 0;
     p.c_log2 = (float)((double)scale * 1.4426950408889634);
-    return launch_decode_fp8(p, d, format == ATTN_FP8_E5M2, static_cast<cudaStream_t>(stream)) ==
+    p.ws = static_cast<float*>(workspace);
+    p.ranges = ranges;
+    p.row_groups = row_groups;
+    p.status = dev->status;
+    p.timeout_ns = kWaitTimeoutNs;
+    return launch_decode_fp8(mk, mv, p, d, format == ATTN_FP8_E5M2, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
                ? ATTN_OK : ATTN_ERR_CUDA;
 }

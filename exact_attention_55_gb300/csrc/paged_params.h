@@ -54,6 +54,11 @@ struct DecodeFp8Params {
     int num_pages, max_pages;
     int window;
     float c_log2;           // softmax scale * log2(e)
+    float* ws;              // parts of units that several CTAs share, two per CTA
+    int ranges;             // CTAs of one row group: at most this many ranges of tiles
+    int row_groups;         // groups of query rows, each a CTA's share
+    int* status;            // device status word (bounded waits)
+    unsigned long long timeout_ns;
 };
 
 }  // namespace gb300
