@@ -382,14 +382,6 @@ __global__ void __launch_bounds__(kD8Threads, 2)
             if constexpr (!C::Q_REGS) {
                 if (!meet()) break;
             }
-            // positions of this lane's rows 8 nt + 2 t + {0, 1}
-            int pos[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    pos[nt][e] = seq.L - p.nq + (row0 + nt * 8 + 2 * t + e) % p.nq;
-
             float acc[NT][D / 16][4], m[NT][2], l[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -401,6 +393,43 @@ __global__ void __launch_bounds__(kD8Threads, 2)
                 l[nt][0] = l[nt][1] = 0.0f;
             }
             int v_top = 0;                                       // largest value exponent so far
+            // Non-finite values of column box c at keys that only some rows see: O becomes NaN
+            // where a row sees one (a product of two indicators), and the codes become 0.
+            constexpr int VW = C::CB / 32;                       // words of a key in this lane
+            auto keep_nan = [&](int c, uint32_t (&v)[4][VW], const float (&xs)[NT][4]) {
+                constexpr uint32_t one = kE5M2 ? 0x3C : 0x38;
+                uint32_t seen[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        seen[nt][h] = dec8_transpose(dec8_pack_half2(xs[nt][2 * h] == NEG_INF ? 0.0f : 1.0f,
+                                                                     xs[nt][2 * h + 1] == NEG_INF ? 0.0f : 1.0f));
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    uint32_t n[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        n[k] = dec8_nonfinite<kE5M2>(v[k][i]) >> 7;
+                        v[k][i] &= ~(n[k] * 0xFFu);
+                        n[k] *= one;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t sel = h ? 0x7362 : 0x5140;
+                        const uint32_t a = __byte_perm(n[0], n[1], sel), d = __byte_perm(n[2], n[3], sel);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            dec8_mma(hit, dec8_half2<kE5M2>(a & 0xFFFF), dec8_half2<kE5M2>(a >> 16),
+                                     dec8_half2<kE5M2>(d & 0xFFFF), dec8_half2<kE5M2>(d >> 16), seen[nt][0], seen[nt][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (hit[e] > 0.0f) acc[nt][(c * VW + i) * 2 + h][e] = __int_as_float(0x7fc00000);
+                        }
+                    }
+                }
+            };
 
             for (int jj = 0; jj < part; ++jj) {
                 const int key0 = (seq.t0 + j + jj) * kD8Tile + warp * 16;
@@ -448,6 +477,7 @@ __global__ void __launch_bounds__(kD8Threads, 2)
                     const int ve = min(max((int)((__float_as_uint(vsc) >> 23) & 0xFF) - 127, v_top - 60), 126);
                     v_top = max(v_top, ve);
                     const float vf = vsc * __int_as_float((127 - ve) << 23), vinv = __int_as_float((127 - ve) << 23);
+                    const float vef = (float)ve;
                     float xs[NT][4];
                     bool raise = false;
 #pragma unroll
@@ -455,13 +485,21 @@ __global__ void __launch_bounds__(kD8Threads, 2)
                         const float k0 = ksc * rowc[nt][0], k1 = ksc * rowc[nt][1];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float v = fmaf(s[nt][0][e] + s[nt][1][e], (e & 1) ? k1 : k0, (float)ve);
-                            if (edge) {
-                                const int key = key0 + g + (e & 2) * 4, last = pos[nt][e & 1];
-                                if (key > last || (p.window > 0 && key < last - p.window)) v = NEG_INF;
-                            }
-                            xs[nt][e] = v;
+                            xs[nt][e] = fmaf(s[nt][0][e] + s[nt][1][e], (e & 1) ? k1 : k0, vef);
                         }
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int key = key0 + g + (e & 2) * 4;
+                                const int last = seq.L - p.nq + (row0 + nt * 8 + 2 * t + (e & 1)) % p.nq;
+                                if (key > last || (p.window > 0 && key < last - p.window)) xs[nt][e] = NEG_INF;
+                            }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
                         raise |= fmaxf(xs[nt][0], xs[nt][2]) > m[nt][0] + kD8Tau ||
                                  fmaxf(xs[nt][1], xs[nt][3]) > m[nt][1] + kD8Tau;
                     }
@@ -502,7 +540,6 @@ __global__ void __launch_bounds__(kD8Threads, 2)
                     // ---- O^T += V^T P^T: this lane's keys 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
                     for (int c = 0; c < C::NCB; ++c) {
-                        constexpr int VW = C::CB / 32;           // words of a key in this lane
                         uint32_t v[4][VW];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -516,59 +553,26 @@ __global__ void __launch_bounds__(kD8Threads, 2)
                                 v[k][0] = u.x, v[k][1] = u.y;
                             }
                         }
-                        uint32_t odd = 0;                        // non-finite codes among this lane's
                         if (edge) {
+                            uint32_t odd = 0;                    // non-finite codes among this lane's
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const int key = key0 + 2 * t + (k & 1) + (k & 2) * 4;
+                                const bool out = key >= seq.L || key < seq.lo;
 #pragma unroll
                                 for (int i = 0; i < VW; ++i) {
-                                    if (key >= seq.L || key < seq.lo) v[k][i] = 0;
+                                    v[k][i] = out ? 0u : v[k][i];
                                     odd |= dec8_nonfinite<kE5M2>(v[k][i]);
                                 }
                             }
-                        }
-                        const bool keep_nan = edge && __any_sync(0xffffffffu, odd != 0);
-                        uint32_t seen[NT][2];
-                        if (keep_nan) {                          // 1 where the row sees the key
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    seen[nt][h] = dec8_transpose(
-                                        dec8_pack_half2(xs[nt][2 * h] == NEG_INF ? 0.0f : 1.0f,
-                                                        xs[nt][2 * h + 1] == NEG_INF ? 0.0f : 1.0f));
+                            if (__any_sync(0xffffffffu, odd != 0)) keep_nan(c, v, xs);
                         }
 #pragma unroll
                         for (int i = 0; i < VW; ++i) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {        // two values of d per product
                                 const uint32_t sel = h ? 0x7362 : 0x5140;
-                                if (keep_nan) {
-                                    constexpr uint32_t one = kE5M2 ? 0x3C : 0x38;
-                                    uint32_t n[4];
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) n[k] = (dec8_nonfinite<kE5M2>(v[k][i]) >> 7) * one;
-                                    const uint32_t a = __byte_perm(n[0], n[1], sel), d = __byte_perm(n[2], n[3], sel);
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) {
-                                        float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                        dec8_mma(hit, dec8_half2<kE5M2>(a & 0xFFFF), dec8_half2<kE5M2>(a >> 16),
-                                                 dec8_half2<kE5M2>(d & 0xFFFF), dec8_half2<kE5M2>(d >> 16),
-                                                 seen[nt][0], seen[nt][1]);
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e)
-                                            if (hit[e] > 0.0f)
-                                                acc[nt][(c * VW + i) * 2 + h][e] = __int_as_float(0x7fc00000);
-                                    }
-                                }
-                                uint32_t u[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    u[k] = v[k][i];
-                                    if (keep_nan) u[k] &= ~((dec8_nonfinite<kE5M2>(u[k]) >> 7) * 0xFFu);
-                                }
-                                const uint32_t a = __byte_perm(u[0], u[1], sel), d = __byte_perm(u[2], u[3], sel);
+                                const uint32_t a = __byte_perm(v[0][i], v[1][i], sel), d = __byte_perm(v[2][i], v[3][i], sel);
                                 const uint32_t a0 = dec8_half2<kE5M2>(a & 0xFFFF), a1 = dec8_half2<kE5M2>(a >> 16);
                                 const uint32_t a2 = dec8_half2<kE5M2>(d & 0xFFFF), a3 = dec8_half2<kE5M2>(d >> 16);
 #pragma unroll
