@@ -1036,7 +1036,8 @@ static void decode_fp8_grid(int rows, int d, int sm_count, int* ranges, int* row
 
 static size_t decode_fp8_ws_bytes(int rows, int d, int ranges, int row_groups)
 {
-    return (size_t)2 * ranges * row_groups * 8 * decode_fp8_row_tiles(rows, d) * (d + 2) * sizeof(float);
+    // per CTA: what the joining kernel has to do (16 bytes), and two parts
+    return (size_t)ranges * row_groups * (4 + 2 * 8 * decode_fp8_row_tiles(rows, d) * (d + 2)) * sizeof(float);
 }
 
 extern "C" size_t attn_decode_fp8_workspace_bytes(int H, int Hkv, int nq, int d)

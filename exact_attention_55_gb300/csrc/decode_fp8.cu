@@ -17,11 +17,13 @@
 // conversion.  The design is about keeping the loads in flight and the work even:
 //   * The tiles (64 keys of one head) of all sequences form one line that is cut into equal
 //     ranges, one per resident CTA (two per SM), so a ragged batch and a single long sequence
-//     both keep every SM busy to the end; a range may end inside a sequence, and then its
-//     part goes to the workspace and decode_fp8_combine_kernel joins the parts.  It is
-//     launched as a dependent of the main grid, its set-up hidden behind it.
+//     both keep every SM busy to the end.  A head counts kD8UnitCost tiles more than it has,
+//     what starting and joining it costs.  A range may end inside a head; its part then goes
+//     to the workspace and decode_fp8_combine_kernel, launched as a dependent of the main
+//     grid, joins the parts.
 //   * Warp 4 walks the range ahead of the others: TMA boxes (one per page or 64 rows) into a
-//     ring of stages, the blocks' scales beside them by cp.async on the same barrier.
+//     ring of stages, the blocks' scales beside them by cp.async on the same barrier, and the
+//     next head's queries as product fragments.
 //   * Warps 0-3 take 16 keys of each tile.  The codes are exact in fp16 and a query row
 //     scaled by a power of two is too, so S^T = K Q^T and O^T += V^T P^T run as
 //     mma.m16n8k16 fp16 with fp32 sums: 16 keys (or 16 values of d) by 8 query rows, which
@@ -52,7 +54,8 @@ constexpr int kD8Tile = 64;            // keys of a tile, 16 per consumer warp
 constexpr int kD8Warps = 4;            // consumer warps
 constexpr int kD8Threads = (kD8Warps + 1) * 32;
 constexpr float kD8Tau = 8.0f;         // the running maximum is raised when passed by this (log2)
-constexpr int kD8CombineThreads = 256;
+constexpr int kD8UnitCost = 4;         // tiles a head's start and end are worth
+constexpr int kD8CombineThreads = 128;
 
 template <int D, int NT>
 struct Dec8Cfg {
@@ -61,26 +64,30 @@ struct Dec8Cfg {
     static constexpr int NCB = D / CB;                    // column boxes of a row
     static constexpr int HALF = kD8Tile * D;              // K or V of a tile
     static constexpr int STAGE = 2 * HALF;
-    static constexpr bool Q_REGS = NT * D <= 256;         // query fragments in registers
-    static constexpr int Q_BYTES = Q_REGS ? 0 : NT * (D / 16) * 32 * 8;
+    static constexpr bool Q_REGS = NT * D <= 128;         // query fragments held in registers
+    static constexpr int Q_FRAGS = NT * (D / 16) * 32;    // 8 bytes each, two heads' worth
     static constexpr int PAD = 4;
-    static constexpr int MERGE = 2 * ROWS * (D + PAD) * 4;
+    static constexpr int MERGE = kD8Warps * 8 * (D + PAD) * 4;
     static constexpr int CAP = 112 * 1024;                // two CTAs per SM
-    static constexpr int FIXED = 1024 + Q_BYTES + MERGE + 4096;   // alignment, barriers, statistics
+    static constexpr int FIXED = 1024 + 2 * Q_FRAGS * 8 + MERGE + 2048;   // 1024: alignment
     static constexpr int FIT = (CAP - FIXED) / STAGE;
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
+    static constexpr int PART = ROWS * (D + 2);           // floats of a part: O, maxima, sums
     static_assert(STAGES >= 2, "ring");
 };
 
-template <int STAGES>
+template <int D, int NT>
 struct alignas(16) Dec8Shared {
-    uint64_t full[STAGES], empty[STAGES];
+    using C = Dec8Cfg<D, NT>;
+    uint64_t full[C::STAGES], empty[C::STAGES];
+    uint64_t q_full[2], q_empty[2];
     uint64_t meet;                     // the consumer warps' barrier
-    float scale[STAGES][8];            // K scales of the tile's four 16-key parts, then V's
-    float m[kD8Warps][64], l[kD8Warps][64];
-    long long sum[kD8Threads / 32];    // set-up: tiles per warp's sequences
-    long long first;                   // tiles before sequence b0
+    float scale[C::STAGES][8];         // K scales of the tile's four 16-key parts, then V's
+    float rowc[2][C::ROWS];            // per query row: softmax scale over its fragments' factor
+    float m[kD8Warps][C::ROWS], l[kD8Warps][C::ROWS];
+    long long sum[kD8Threads / 32][2]; // set-up: tiles and sequences of each warp's share
+    long long first;                   // cost before sequence b0
     int b0;
     int abort_flag;
 };
@@ -100,36 +107,78 @@ __device__ __forceinline__ Dec8Seq dec8_seq(const DecodeFp8Params& p, int b)
     return s;
 }
 
-// Set-up of main and combine kernel: the sum of all sequences' tiles, and the tiles before
-// the sequence that `pick` chooses from (tiles before it, its own).  All threads call it.
-template <int kThreads, class Pick>
-__device__ __forceinline__ long long dec8_scan(const DecodeFp8Params& p, long long* warp_sum, Pick pick)
+// The line that the ranges are cut from: `tiles` in all, `cost` long; a unit (sequence, key
+// head) of n tiles covers n + unit_cost of it, its tiles at the end; x cuts it at x cost / X.
+struct Dec8Line {
+    long long tiles, cost, X;
+    int unit_cost;
+
+    __device__ __forceinline__ Dec8Line(const DecodeFp8Params& p, long long seq_tiles, long long seqs)
+    {
+        tiles = seq_tiles * p.Hkv;
+        unit_cost = tiles <= p.ranges ? 0 : kD8UnitCost;   // few tiles: one per range
+        cost = tiles + seqs * p.Hkv * unit_cost;
+        X = tiles < p.ranges ? tiles : p.ranges;
+    }
+    __device__ __forceinline__ long long cut(int x) const { return x * cost / X; }
+    __device__ __forceinline__ int owner(long long at) const { return (int)(((at + 1) * X - 1) / cost); }
+};
+
+// Finds the sequence that range x starts in (its number and the cost before it).  All
+// threads of the main kernel call it.
+template <class Shared>
+__device__ __forceinline__ Dec8Line dec8_line(const DecodeFp8Params& p, Shared* sh, int x)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.B + kThreads - 1) / kThreads;
+    const int per = (p.B + kD8Threads - 1) / kD8Threads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += dec8_seq(p, b).n;
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    long long before = inc - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        total += warp_sum[w];
-    }
+    long long mine = 0, seqs = 0;
     for (int b = b0; b < b1; ++b) {
         const int n = dec8_seq(p, b).n;
-        pick(b, before, n, total);
-        before += n;
+        mine += n;
+        seqs += n > 0;
     }
-    return total;
+    long long inc = mine, inc_s = seqs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o), z = __shfl_up_sync(0xffffffffu, inc_s, o);
+        if (lane >= o) {
+            inc += y;
+            inc_s += z;
+        }
+    }
+    if (lane == 31) {
+        sh->sum[warp][0] = inc;
+        sh->sum[warp][1] = inc_s;
+    }
+    __syncthreads();
+    long long before = inc - mine, before_s = inc_s - seqs, total = 0, total_s = 0;
+#pragma unroll
+    for (int w = 0; w < kD8Threads / 32; ++w) {
+        if (w < warp) {
+            before += sh->sum[w][0];
+            before_s += sh->sum[w][1];
+        }
+        total += sh->sum[w][0];
+        total_s += sh->sum[w][1];
+    }
+    const Dec8Line line(p, total, total_s);
+    if (x < line.X) {
+        const long long at = line.cut(x);
+        long long s0 = (before + before_s * line.unit_cost) * p.Hkv;
+        if (s0 <= at && at < s0 + (mine + seqs * line.unit_cost) * p.Hkv)
+            for (int b = b0; b < b1; ++b) {
+                const int n = dec8_seq(p, b).n;
+                const long long len = n > 0 ? (long long)(n + line.unit_cost) * p.Hkv : 0;
+                if (s0 <= at && at < s0 + len) {
+                    sh->b0 = b;
+                    sh->first = s0;
+                }
+                s0 += len;
+            }
+    }
+    __syncthreads();
+    return line;
 }
 
 template <bool kE5M2>
@@ -199,12 +248,14 @@ __global__ void __launch_bounds__(kD8Threads, 2)
     using C = Dec8Cfg<D, NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* q_smem = smem + C::STAGES * C::STAGE;
-    float* merge = reinterpret_cast<float*>(q_smem + C::Q_BYTES);
-    auto* sh = reinterpret_cast<Dec8Shared<C::STAGES>*>(q_smem + C::Q_BYTES + C::MERGE);
-    static_assert(sizeof(Dec8Shared<C::STAGES>) <= 3072, "shared memory");
+    uint2* qs = reinterpret_cast<uint2*>(smem + C::STAGES * C::STAGE);       // [2][Q_FRAGS]
+    float* merge = reinterpret_cast<float*>(qs + 2 * C::Q_FRAGS);
+    auto* sh = reinterpret_cast<Dec8Shared<D, NT>*>(merge + C::MERGE / 4);
+    static_assert(sizeof(Dec8Shared<D, NT>) <= 2048, "shared memory");
     const volatile int* abort_flag = &sh->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float NEG_INF = -__int_as_float(0x7f800000);
+    int4* todo = reinterpret_cast<int4*>(p.ws) + blockIdx.x;   // for the combine kernel
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (threadIdx.x == 0) {
@@ -212,40 +263,59 @@ __global__ void __launch_bounds__(kD8Threads, 2)
             mbar_init(smem_u32(&sh->full[s]), 9);        // lane 0's bytes, eight lanes' scales
             mbar_init(smem_u32(&sh->empty[s]), kD8Warps);
         }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&sh->q_full[s]), 1);
+            mbar_init(smem_u32(&sh->q_empty[s]), kD8Warps);
+        }
         mbar_init(smem_u32(&sh->meet), kD8Warps);
         sh->abort_flag = 0;
         fence_mbar_init();
+        *todo = make_int4(-1, 0, 0, 0);
     }
-    // this CTA's range [f0, f_end) of the line of tiles (sequence, key head, tile)
-    const int x = blockIdx.x / p.row_groups, rg = blockIdx.x - x * p.row_groups;
-    const long long total = p.Hkv * dec8_scan<kD8Threads>(
-        p, sh->sum, [&](int b, long long before, int n, long long all) {
-            const long long T = all * p.Hkv, X = T < p.ranges ? T : p.ranges;
-            if (x >= X) return;
-            const long long f = x * T / X;
-            if (n > 0 && before * p.Hkv <= f && f < (before + n) * p.Hkv) {
-                sh->b0 = b;
-                sh->first = before;
-            }
-        });
-    __syncthreads();
-    const long long X = total < p.ranges ? total : p.ranges;
-    if (x >= X) return;
-    long long f = x * total / X;
-    const long long f_end = (x + 1) * total / X;
-    int b = sh->b0;
-    Dec8Seq seq = dec8_seq(p, b);
-    const long long in_seq = f - sh->first * p.Hkv;
-    int hk = (int)(in_seq / seq.n), j = (int)(in_seq - (long long)hk * seq.n);
-    // to the next unit (sequence, key head) of the line
-    auto next_unit = [&]() {
-        j = 0;
-        if (++hk == p.Hkv) {
-            hk = 0;
-            do seq = dec8_seq(p, ++b);
-            while (seq.n == 0);
+    const int x = blockIdx.x / p.row_groups, rg = blockIdx.x - x * p.row_groups, row0 = rg * C::ROWS;
+    const Dec8Line line = dec8_line(p, sh, x);
+    // sequences without a key: O = 0, LSE = -inf
+    auto write_empty = [&](int threads) {
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+            if (dec8_seq(p, b).n > 0) continue;
+            const size_t r0 = (size_t)b * p.Hkv * p.rows, rows = (size_t)p.Hkv * p.rows;
+            uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + r0 * D);
+            for (size_t i = threadIdx.x; i < rows * (D / 8); i += threads) o[i] = make_uint4(0, 0, 0, 0);
+            for (size_t i = threadIdx.x; i < rows; i += threads) p.lse[r0 + i] = NEG_INF;
         }
     };
+    if (x >= line.X) {
+        write_empty(kD8Threads);
+        return;
+    }
+    // this CTA's range [a, e) of the line; unit (b, hk) starts at s0 and has seq.n tiles
+    const long long a = line.cut(x), e = line.cut(x + 1);
+    int b = sh->b0;
+    Dec8Seq seq = dec8_seq(p, b);
+    int hk = (int)((a - sh->first) / (seq.n + line.unit_cost));
+    long long s0 = sh->first + (long long)hk * (seq.n + line.unit_cost);
+    // the unit's tiles of this range: [k0, k1)
+    int k0 = 0, k1 = 0;
+    auto take = [&]() {
+        k0 = (int)max(0LL, a - s0 - line.unit_cost);
+        k1 = (int)max((long long)k0, min((long long)seq.n, e - s0 - line.unit_cost));
+    };
+    // to the next unit with tiles of this range; false when there is none
+    auto next_unit = [&]() -> bool {
+        do {
+            s0 += seq.n + line.unit_cost;
+            if (s0 + line.unit_cost >= e) return false;
+            if (++hk == p.Hkv) {
+                hk = 0;
+                do seq = dec8_seq(p, ++b);
+                while (seq.n == 0);
+            }
+            take();
+        } while (k1 <= k0);
+        return true;
+    };
+    take();
+    bool more = k1 > k0 || next_unit();
 
     if (warp == kD8Warps) {
         // ------------------------------------------------------------ producer
@@ -254,28 +324,48 @@ __global__ void __launch_bounds__(kD8Threads, 2)
             tma_prefetch_desc(&tmV);
         }
         const uint64_t pol = l2_policy_evict_first();
+        const int g = lane >> 2, t = lane & 3;
         const int log2_r = p.log2_ps < 6 ? p.log2_ps : 6;       // rows per TMA box: a page, or 64
         const int nbox = kD8Tile >> log2_r;
         const int ps_mask = (1 << p.log2_ps) - 1;
-        int stage = 0, filled = 0;
-        uint32_t parity = 1;
+        int stage = 0, filled = 0, q_slot = 0;
+        uint32_t parity = 1, q_parity = 1;
         bool ok = true;
-        while (f < f_end && ok) {
-            const int part = (int)min((long long)(seq.n - j), f_end - f);
+        auto wait_lane0 = [&](uint64_t* bar, uint32_t par) {
+            int r = 1;
+            if (lane == 0) r = mbar_wait(smem_u32(bar), par, abort_flag, p.timeout_ns);
+            ok = __shfl_sync(0xffffffffu, r, 0) != 0;
+            return ok;
+        };
+        while (more && ok) {
+            // this head's queries: lane (g, t) holds row 8 nt + g, 16-byte pieces of its share of d
+            constexpr int PER = D / 8;                           // words of a row in a lane
+            uint32_t w[NT][PER];
+            const size_t unit_row = ((size_t)b * p.Hkv + hk) * p.rows + row0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < C::NCB; ++c)
+#pragma unroll
+                    for (int v = 0; v < C::CB / 32; ++v) {
+                        const int r = nt * 8 + g, o = (c * (C::CB / 32) + v) * 4;
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (row0 + r < p.rows)
+                            u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                                     (unit_row + r) * D + c * C::CB + t * (C::CB / 4) + v * 8));
+                        w[nt][o] = u.x, w[nt][o + 1] = u.y, w[nt][o + 2] = u.z, w[nt][o + 3] = u.w;
+                    }
             const int* ptab = p.page_table + (size_t)b * p.max_pages;
             int held = 0, pg = 0;                                // 32 boxes' pages from box `held` on
-            for (int jj = 0; jj < part && ok; ++jj) {
-                const int key0 = (seq.t0 + j + jj) * kD8Tile, box0 = key0 >> log2_r;
-                if (jj == 0 || box0 - held >= 32) {
+            for (int k = k0; k < k1 && ok; ++k) {
+                const int key0 = (seq.t0 + k) * kD8Tile, box0 = key0 >> log2_r;
+                if (k == k0 || box0 - held >= 32) {
                     held = box0;
                     const long long key = (long long)(box0 + lane) << log2_r;
                     const int pi = (int)min(key >> p.log2_ps, (long long)p.max_pages - 1);
                     pg = min(max(__ldg(ptab + pi), 0), p.num_pages - 1);
                 }
-                int r = 1;
-                if (lane == 0) r = mbar_wait(smem_u32(&sh->empty[stage]), parity, abort_flag, p.timeout_ns);
-                ok = __shfl_sync(0xffffffffu, r, 0) != 0;
-                if (!ok) break;
+                if (!wait_lane0(&sh->empty[stage], parity)) break;
                 const uint32_t fb = smem_u32(&sh->full[stage]);
                 if (lane == 0) mbar_arrive_expect_tx(fb, C::STAGE);
                 __syncwarp();
@@ -305,9 +395,36 @@ __global__ void __launch_bounds__(kD8Threads, 2)
                     stage = 0;
                     parity ^= 1;
                 }
+                if (k > k0) continue;
+                // fragments: a row scaled by a power of two so that its largest value is just
+                // below 2^15 in fp16; what is 2^-38 of that and less is rounded
+                if (!wait_lane0(&sh->q_empty[q_slot], q_parity)) break;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    uint32_t big = 0;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) big = max(big, max((w[nt][i] << 16) & 0x7FFF0000u, w[nt][i] & 0x7FFF0000u));
+                    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                    big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                    const int ex = max((int)(big >> 23), 15) - 14;   // biased exponent of the factor's inverse
+                    const float down = __int_as_float((254 - ex) << 23);
+                    if (t == 0) sh->rowc[q_slot][nt * 8 + g] = __int_as_float(ex << 23) * p.c_log2;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t u = w[nt][2 * i], v = w[nt][2 * i + 1];
+                        qs[q_slot * C::Q_FRAGS + (nt * (D / 16) + i) * 32 + lane] = make_uint2(
+                            dec8_pack_half2(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xFFFF0000u) * down),
+                            dec8_pack_half2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down));
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh->q_full[q_slot]));
+                if (++q_slot == 2) {
+                    q_slot = 0;
+                    q_parity ^= 1;
+                }
             }
-            f += part;
-            if (ok && f < f_end) next_unit();
+            if (ok) more = next_unit();
         }
         if (!ok && lane == 0) dec8_timeout(p, &sh->abort_flag);
         // every copy issued lands before shared memory is released
@@ -318,11 +435,9 @@ __global__ void __launch_bounds__(kD8Threads, 2)
     } else {
         // ------------------------------------------------------------ consumers
         const int g = lane >> 2, t = lane & 3;
-        const float NEG_INF = -__int_as_float(0x7f800000);
-        const int row0 = rg * C::ROWS;
-        int stage = 0;
-        uint32_t parity = 0, meet_parity = 0;
-        bool ok = true;
+        int stage = 0, q_slot = 0;
+        uint32_t parity = 0, q_parity = 0, meet_parity = 0;
+        bool ok = true, merged = false;
         auto wait_all = [&](uint64_t* bar, uint32_t par) {
             const bool r = mbar_wait(smem_u32(bar), par, abort_flag, p.timeout_ns);
             ok = __all_sync(0xffffffffu, r);
@@ -335,60 +450,28 @@ __global__ void __launch_bounds__(kD8Threads, 2)
             meet_parity ^= 1;
             return r;
         };
-        while (f < f_end && ok) {
-            const int part = (int)min((long long)(seq.n - j), f_end - f);
+        while (more) {
             const size_t unit_row = ((size_t)b * p.Hkv + hk) * p.rows + row0;
-
-            // query fragments: row 8 nt + g, scaled by a power of two so that its largest
-            // value is just below 2^15; what is 2^-38 of that and less rounds in fp16
-            uint2 qf[C::Q_REGS ? NT : 1][C::Q_REGS ? D / 16 : 1];
+            if (!wait_all(&sh->q_full[q_slot], q_parity)) break;
+            const uint2* frag = qs + q_slot * C::Q_FRAGS + lane;
+            uint2 qf[C::Q_REGS ? NT * (D / 16) : 1];
+            if constexpr (C::Q_REGS) {
+#pragma unroll
+                for (int i = 0; i < NT * (D / 16); ++i) qf[i] = frag[i * 32];
+            }
             float rowc[NT][2];
-            uint2* qs = reinterpret_cast<uint2*>(q_smem);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int r = nt * 8 + g;
-                constexpr int PER = D / 4;                       // values of a lane: D/4 in NCB pieces
-                uint32_t w[PER / 2];
-                uint32_t big = 0;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < C::NCB; ++c)
-#pragma unroll
-                    for (int v = 0; v < C::CB / 32; ++v) {       // 8 values each
-                        uint4 u = make_uint4(0, 0, 0, 0);
-                        if (row0 + r < p.rows)
-                            u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                                     (unit_row + r) * D + c * C::CB + t * (C::CB / 4) + v * 8));
-                        const int o = (c * (C::CB / 32) + v) * 4;
-                        w[o] = u.x, w[o + 1] = u.y, w[o + 2] = u.z, w[o + 3] = u.w;
-                    }
-#pragma unroll
-                for (int i = 0; i < PER / 2; ++i) big = max(big, max((w[i] << 16) & 0x7FFF0000u, w[i] & 0x7FFF0000u));
-                big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                const int e = max((int)(big >> 23), 15) - 14;    // biased exponent of the factor's inverse
-                const float down = __int_as_float((254 - e) << 23), up = __int_as_float(e << 23);
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t a = w[2 * i], d = w[2 * i + 1];
-                    const uint2 fr = make_uint2(
-                        dec8_pack_half2(__uint_as_float(a << 16) * down, __uint_as_float(a & 0xFFFF0000u) * down),
-                        dec8_pack_half2(__uint_as_float(d << 16) * down, __uint_as_float(d & 0xFFFF0000u) * down));
-                    if constexpr (C::Q_REGS) qf[nt][i] = fr;
-                    else if (warp == (nt & 3)) qs[(nt * (D / 16) + i) * 32 + lane] = fr;
-                }
-                rowc[nt][0] = __shfl_sync(0xffffffffu, up, (2 * t) * 4) * p.c_log2;
-                rowc[nt][1] = __shfl_sync(0xffffffffu, up, (2 * t + 1) * 4) * p.c_log2;
-            }
-            if constexpr (!C::Q_REGS) {
-                if (!meet()) break;
-            }
+                for (int h = 0; h < 2; ++h) rowc[nt][h] = sh->rowc[q_slot][nt * 8 + 2 * t + h];
+
             float acc[NT][D / 16][4], m[NT][2], l[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.0f;
+                    for (int h = 0; h < 4; ++h) acc[nt][i][h] = 0.0f;
                 m[nt][0] = m[nt][1] = NEG_INF;
                 l[nt][0] = l[nt][1] = 0.0f;
             }
@@ -431,8 +514,8 @@ __global__ void __launch_bounds__(kD8Threads, 2)
                 }
             };
 
-            for (int jj = 0; jj < part; ++jj) {
-                const int key0 = (seq.t0 + j + jj) * kD8Tile + warp * 16;
+            for (int k = k0; k < k1; ++k) {
+                const int key0 = (seq.t0 + k) * kD8Tile + warp * 16;
                 if (!wait_all(&sh->full[stage], parity)) break;
                 // this warp's keys: some row sees one of them; all rows see all of them
                 const bool any = key0 < seq.L && key0 + 15 >= seq.lo;
@@ -464,8 +547,8 @@ __global__ void __launch_bounds__(kD8Threads, 2)
                             const uint32_t a1 = dec8_half2<kE5M2>(hi[i] & 0xFFFF), a3 = dec8_half2<kE5M2>(hi[i] >> 16);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                const uint2 q2 = C::Q_REGS ? qf[C::Q_REGS ? nt : 0][C::Q_REGS ? c * KW + i : 0]
-                                                           : qs[(nt * (D / 16) + c * KW + i) * 32 + lane];
+                                const int at = nt * (D / 16) + c * KW + i;
+                                const uint2 q2 = C::Q_REGS ? qf[C::Q_REGS ? at : 0] : frag[at * 32];
                                 dec8_mma(s[nt][i & 1], a0, a1, a2, a3, q2.x, q2.y);
                             }
                         }
@@ -591,139 +674,104 @@ __global__ void __launch_bounds__(kD8Threads, 2)
             }
             if (!ok) break;
 
-            // ---- join the four warps: statistics, then O in two steps
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh->q_empty[q_slot]));
+            if (++q_slot == 2) {
+                q_slot = 0;
+                q_parity ^= 1;
+            }
+
+            // ---- join the four warps, eight rows at a time
+            const bool whole = k1 - k0 == seq.n;
+            float* part = p.ws + 4 * gridDim.x + (size_t)(2 * blockIdx.x + (k0 == 0 ? 1 : 0)) * C::PART;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                if (merged && !meet()) break;                    // the areas have been read
+                merged = true;
+                // value d of acc[..][i][h]: group g holds CB/8 consecutive ones of a column box
+                constexpr int VT = C::CB / 16;                   // products per column box
+                float* area = merge + warp * 8 * (D + C::PAD) + g * (C::CB / 8);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int i = 0; i < D / 16; i += 2)
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<float4*>(area + (2 * t + h) * (D + C::PAD) + (i / VT) * C::CB + (i % VT) * 2) =
+                            make_float4(acc[nt][i][h], acc[nt][i][h + 2], acc[nt][i + 1][h], acc[nt][i + 1][h + 2]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], o);
                     if (g == 0) {
-                        sh->m[warp][nt * 8 + 2 * t + e] = m[nt][e];
-                        sh->l[warp][nt * 8 + 2 * t + e] = l[nt][e];
+                        sh->m[warp][nt * 8 + 2 * t + h] = m[nt][h];
+                        sh->l[warp][nt * 8 + 2 * t + h] = l[nt][h];
                     }
                 }
-            if (!meet()) break;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = nt * 8 + 2 * t + e;
+                if (!meet()) break;
+                for (int idx = threadIdx.x; idx < 8 * (D / 4); idx += kD8Warps * 32) {
+                    const int r8 = idx / (D / 4), d4 = idx - r8 * (D / 4), r = nt * 8 + r8;
+                    if (row0 + r >= p.rows) break;
                     const float M = fmaxf(fmaxf(sh->m[0][r], sh->m[1][r]), fmaxf(sh->m[2][r], sh->m[3][r]));
-                    const float fac = ex2(m[nt][e] - (M == NEG_INF ? 0.0f : M));   // ex2(-inf) = 0
+                    const float mb = M == NEG_INF ? 0.0f : M;
+                    float sum = 0.0f;
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        acc[nt][i][e] *= fac;
-                        acc[nt][i][e + 2] *= fac;
+                    for (int w = 0; w < kD8Warps; ++w) {
+                        const float fac = ex2(sh->m[w][r] - mb);     // ex2(-inf) = 0
+                        const float4 u = *reinterpret_cast<const float4*>(merge + (w * 8 + r8) * (D + C::PAD) + d4 * 4);
+                        sum = fmaf(sh->l[w][r], fac, sum);
+                        v.x = fmaf(u.x, fac, v.x), v.y = fmaf(u.y, fac, v.y);
+                        v.z = fmaf(u.z, fac, v.z), v.w = fmaf(u.w, fac, v.w);
                     }
-                }
-            // value d of acc[..][i][e]: lane group g holds CB/8 consecutive ones of a column box
-            constexpr int VT = C::CB / 16;                       // products per column box
-            float* area = merge + (warp & 1) * C::ROWS * (D + C::PAD);
-            auto place = [&](int nt, int i, int e) {             // float4 over i, i + 1
-                return area + (nt * 8 + 2 * t + e) * (D + C::PAD) + (i / VT) * C::CB + g * (C::CB / 8) + (i % VT) * 2;
-            };
-            if (warp >= 2) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < D / 16; i += 2)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<float4*>(place(nt, i, e)) =
-                                make_float4(acc[nt][i][e], acc[nt][i][e + 2], acc[nt][i + 1][e], acc[nt][i + 1][e + 2]);
-            }
-            if (!meet()) break;
-            if (warp < 2) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < D / 16; i += 2)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float4* at = reinterpret_cast<float4*>(place(nt, i, e));
-                            float4 v = *at;
-                            v.x += acc[nt][i][e], v.y += acc[nt][i][e + 2];
-                            v.z += acc[nt][i + 1][e], v.w += acc[nt][i + 1][e + 2];
-                            *at = v;
+                    if (whole) {
+                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (unit_row + r) * D + d4 * 4) =
+                            make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+                        if (d4 == 0)
+                            p.lse[unit_row + r] = sum == 0.0f ? NEG_INF : (mb + __log2f(sum)) * 0.69314718055994531f;
+                    } else {
+                        *reinterpret_cast<float4*>(part + r * D + d4 * 4) = v;
+                        if (d4 == 0) {
+                            part[C::ROWS * D + r] = M;
+                            part[C::ROWS * D + C::ROWS + r] = sum;
                         }
-            }
-            if (!meet()) break;
-            const bool whole = part == seq.n;
-            const int slot = 2 * blockIdx.x + (j == 0 ? 1 : 0);
-            float* ws = p.ws + (size_t)slot * C::ROWS * (D + 2);
-            for (int idx = threadIdx.x; idx < C::ROWS * (D / 4); idx += kD8Warps * 32) {
-                const int r = idx / (D / 4), d4 = idx - r * (D / 4);
-                if (row0 + r >= p.rows) break;
-                const float4 a = *reinterpret_cast<const float4*>(merge + r * (D + C::PAD) + d4 * 4);
-                const float4 d = *reinterpret_cast<const float4*>(merge + (C::ROWS + r) * (D + C::PAD) + d4 * 4);
-                float4 v = make_float4(a.x + d.x, a.y + d.y, a.z + d.z, a.w + d.w);
-                const float M = fmaxf(fmaxf(sh->m[0][r], sh->m[1][r]), fmaxf(sh->m[2][r], sh->m[3][r]));
-                const float mb = M == NEG_INF ? 0.0f : M;
-                float sum = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kD8Warps; ++w) sum = fmaf(sh->l[w][r], ex2(sh->m[w][r] - mb), sum);
-                if (whole) {
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (unit_row + r) * D + d4 * 4) =
-                        make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-                    if (d4 == 0)
-                        p.lse[unit_row + r] = sum == 0.0f ? NEG_INF : (mb + __log2f(sum)) * 0.69314718055994531f;
-                } else {
-                    *reinterpret_cast<float4*>(ws + r * D + d4 * 4) = v;
-                    if (d4 == 0) {
-                        ws[C::ROWS * D + r] = M;
-                        ws[C::ROWS * D + C::ROWS + r] = sum;
                     }
                 }
             }
-            f += part;
-            if (f < f_end) {
-                next_unit();
-                if (!meet()) break;      // the statistics and areas have been read
-            }
+            if (!ok) break;
+            if (!whole && k0 == 0 && threadIdx.x == 0)           // the unit's first part: name the others
+                *todo = make_int4(line.owner(s0 + line.unit_cost + seq.n - 1), (int)(unit_row & 0x7fffffff),
+                                  (int)(unit_row >> 31), 0);
+            more = next_unit();
         }
         if (!ok) dec8_timeout(p, &sh->abort_flag);
+        else write_empty(kD8Warps * 32);
     }
 }
 
-// Joins the parts of the units that several CTAs shared, one CTA per query row: with M the
-// largest part maximum, O = sum_x 2^(M_x - M) a_x / sum_x 2^(M_x - M) l_x.  Units of one CTA
-// are done already; rows of an empty sequence get O = 0, LSE = -inf here.
+// Joins the parts of a unit that several ranges shared: with M the largest part maximum,
+// O = sum_x 2^(M_x - M) a_x / sum_x 2^(M_x - M) l_x.  One CTA per range and row; those of a
+// range that no unit leaves have nothing to do.
 template <int D, int NT>
 __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(const DecodeFp8Params p)
 {
-    constexpr int ROWS = 8 * NT, COLS = D / 4, GROUPS = kD8CombineThreads / COLS;
-    __shared__ long long warp_sum[kD8CombineThreads / 32], first;
+    using C = Dec8Cfg<D, NT>;
+    constexpr int COLS = D / 4, GROUPS = kD8CombineThreads / COLS;
     __shared__ float4 sm_a[GROUPS][COLS];
     __shared__ float sm_m[kD8CombineThreads / 32], sm_l[GROUPS];
     const float NEG_INF = -__int_as_float(0x7f800000);
-    const int tid = threadIdx.x;
-    const long long row = blockIdx.x;
-    const int r = (int)(row % p.rows);
-    const long long bh = row / p.rows;
-    const int my_b = (int)(bh / p.Hkv), hk = (int)(bh - (long long)my_b * p.Hkv);
-    const long long T = p.Hkv * dec8_scan<kD8CombineThreads>(p, warp_sum, [&](int b, long long before, int, long long) {
-        if (b == my_b) first = before;
-    });
-    __syncthreads();
+    const int tid = threadIdx.x, r = blockIdx.y, ctas = p.ranges * p.row_groups;
+    const int x0 = blockIdx.x / p.row_groups, rg = blockIdx.x - x0 * p.row_groups;
+    if (rg * C::ROWS + r >= p.rows) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int n = dec8_seq(p, my_b).n;
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + row * D;
-    if (n == 0) {
-        if (tid < D / 8) reinterpret_cast<uint4*>(o)[tid] = make_uint4(0, 0, 0, 0);
-        if (tid == 0) p.lse[row] = NEG_INF;
-        return;
-    }
-    const long long X = T < p.ranges ? T : p.ranges, s0 = first * p.Hkv + (long long)hk * n;
-    const int x0 = (int)(((s0 + 1) * X - 1) / T), x1 = (int)(((s0 + n) * X - 1) / T);
-    if (x0 == x1) return;
-    const int rg = r / ROWS, rr = r - rg * ROWS;
+    const int4 todo = reinterpret_cast<const int4*>(p.ws)[blockIdx.x];
+    if (todo.x < 0) return;
+    const int x1 = min(todo.x, p.ranges - 1);
+    const size_t row = (((size_t)todo.z << 31) | (size_t)todo.y) + r;
     auto part_of = [&](int x) {
-        return p.ws + (size_t)(2 * (x * p.row_groups + rg) + (x == x0 ? 1 : 0)) * ROWS * (D + 2);
+        return p.ws + 4 * ctas + (size_t)(2 * (x * p.row_groups + rg) + (x == x0 ? 1 : 0)) * C::PART;
     };
     float M = NEG_INF;
-    for (int x = x0 + tid; x <= x1; x += kD8CombineThreads) M = fmaxf(M, part_of(x)[ROWS * D + rr]);
+    for (int x = x0 + tid; x <= x1; x += kD8CombineThreads) M = fmaxf(M, part_of(x)[C::ROWS * D + r]);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
     if ((tid & 31) == 0) sm_m[tid >> 5] = M;
@@ -738,9 +786,9 @@ __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(c
 #pragma unroll 4
     for (int x = x0 + grp; x <= x1; x += GROUPS) {
         const float* w = part_of(x);
-        const float fac = ex2(w[ROWS * D + rr] - mb);
-        const float4 v = *reinterpret_cast<const float4*>(w + rr * D + col * 4);
-        l = fmaf(fac, w[ROWS * D + ROWS + rr], l);
+        const float fac = ex2(w[C::ROWS * D + r] - mb);
+        const float4 v = *reinterpret_cast<const float4*>(w + r * D + col * 4);
+        l = fmaf(fac, w[C::ROWS * D + C::ROWS + r], l);
         a.x = fmaf(fac, v.x, a.x), a.y = fmaf(fac, v.y, a.y);
         a.z = fmaf(fac, v.z, a.z), a.w = fmaf(fac, v.w, a.w);
     }
@@ -757,20 +805,15 @@ __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(c
             sum += sm_l[k];
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        reinterpret_cast<uint2*>(o)[tid] =
+        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * D)[tid] =
             make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
         if (tid == 0) p.lse[row] = sum == 0.0f ? NEG_INF : (mb + __log2f(sum)) * 0.69314718055994531f;
     }
 }
 
-// Query rows of a CTA, in eights: as many as the accumulators allow (128 registers of them),
-// so that a key head under up to 32 rows (16 at d = 256) is read once.
-int decode_fp8_row_tiles(int rows, int d)
-{
-    const int most = d == 256 ? 2 : 4;
-    const int want = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-    return want < most ? want : most;
-}
+// Query rows of a CTA, in eights.  More rows under one key head go to more CTAs, which read
+// the same tiles at the same time (the second read comes from L2).
+int decode_fp8_row_tiles(int rows, int d) { return rows <= 8 || d == 256 ? 1 : 2; }
 
 template <int D, bool kE5M2, int NT>
 static cudaError_t launch_decode_fp8_n(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeFp8Params& p,
@@ -784,7 +827,7 @@ static cudaError_t launch_decode_fp8_n(const CUtensorMap& mk, const CUtensorMap&
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * p.rows));
+    cfg.gridDim = dim3(p.ranges * p.row_groups, p.rows < C::ROWS ? p.rows : C::ROWS);
     cfg.blockDim = dim3(kD8CombineThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -799,13 +842,9 @@ template <int D, bool kE5M2>
 static cudaError_t launch_decode_fp8_d(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeFp8Params& p,
                                        cudaStream_t stream)
 {
-    switch (decode_fp8_row_tiles(p.rows, D)) {
-    case 1: return launch_decode_fp8_n<D, kE5M2, 1>(mk, mv, p, stream);
-    case 2: return launch_decode_fp8_n<D, kE5M2, 2>(mk, mv, p, stream);
-    default:
-        if constexpr (D < 256) return launch_decode_fp8_n<D, kE5M2, 4>(mk, mv, p, stream);
-        return cudaErrorInvalidValue;
-    }
+    if constexpr (D < 256)
+        if (decode_fp8_row_tiles(p.rows, D) == 2) return launch_decode_fp8_n<D, kE5M2, 2>(mk, mv, p, stream);
+    return launch_decode_fp8_n<D, kE5M2, 1>(mk, mv, p, stream);
 }
 
 cudaError_t launch_decode_fp8(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeFp8Params& p, int d,

@@ -54,7 +54,7 @@ struct DecodeFp8Params {
     int num_pages, max_pages;
     int window;
     float c_log2;           // softmax scale * log2(e)
-    float* ws;              // parts of units that several CTAs share, two per CTA
+    float* ws;              // per CTA: int4 for the joining kernel; then two parts per CTA
     int ranges;             // CTAs of one row group: at most this many ranges of tiles
     int row_groups;         // groups of query rows, each a CTA's share
     int* status;            // device status word (bounded waits)
