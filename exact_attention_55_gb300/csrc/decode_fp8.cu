@@ -255,7 +255,10 @@ __global__ void __launch_bounds__(kD8Threads, 2)
     const volatile int* abort_flag = &sh->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float NEG_INF = -__int_as_float(0x7f800000);
-    int4* todo = reinterpret_cast<int4*>(p.ws) + blockIdx.x;   // for the combine kernel
+    // what the combine kernel finds: an entry per unit, or where there are more units than CTAs
+    // one per CTA, for the one unit that it may begin and not end
+    const bool per_unit = (long long)p.B * p.Hkv * p.row_groups <= gridDim.x;
+    int4* todo = reinterpret_cast<int4*>(p.ws);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (threadIdx.x == 0) {
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(kD8Threads, 2)
         mbar_init(smem_u32(&sh->meet), kD8Warps);
         sh->abort_flag = 0;
         fence_mbar_init();
-        *todo = make_int4(-1, 0, 0, 0);
+        if (!per_unit) todo[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
     const int x = blockIdx.x / p.row_groups, rg = blockIdx.x - x * p.row_groups, row0 = rg * C::ROWS;
     const Dec8Line line = dec8_line(p, sh, x);
@@ -282,6 +285,9 @@ __global__ void __launch_bounds__(kD8Threads, 2)
             uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + r0 * D);
             for (size_t i = threadIdx.x; i < rows * (D / 8); i += threads) o[i] = make_uint4(0, 0, 0, 0);
             for (size_t i = threadIdx.x; i < rows; i += threads) p.lse[r0 + i] = NEG_INF;
+            if (per_unit)
+                for (int i = threadIdx.x; i < p.Hkv * p.row_groups; i += threads)
+                    todo[b * p.Hkv * p.row_groups + i] = make_int4(-1, 0, 0, 0);
         }
     };
     if (x >= line.X) {
@@ -738,9 +744,10 @@ __global__ void __launch_bounds__(kD8Threads, 2)
                 }
             }
             if (!ok) break;
-            if (!whole && k0 == 0 && threadIdx.x == 0)           // the unit's first part: name the others
-                *todo = make_int4(line.owner(s0 + line.unit_cost + seq.n - 1), (int)(unit_row & 0x7fffffff),
-                                  (int)(unit_row >> 31), 0);
+            if (k0 == 0 && threadIdx.x == 0 && (per_unit || !whole))   // the unit's first part names the last
+                todo[per_unit ? (b * p.Hkv + hk) * p.row_groups + rg : blockIdx.x] =
+                    whole ? make_int4(-1, 0, 0, 0)
+                          : make_int4(x, line.owner(s0 + line.unit_cost + seq.n - 1), rg, (int)unit_row);
             more = next_unit();
         }
         if (!ok) dec8_timeout(p, &sh->abort_flag);
@@ -749,65 +756,86 @@ __global__ void __launch_bounds__(kD8Threads, 2)
 }
 
 // Joins the parts of a unit that several ranges shared: with M the largest part maximum,
-// O = sum_x 2^(M_x - M) a_x / sum_x 2^(M_x - M) l_x.  One CTA per range and row; those of a
-// range that no unit leaves have nothing to do.
+// O = sum_x 2^(M_x - M) a_x / sum_x 2^(M_x - M) l_x.  grid.x: the units, or where there are
+// more of them the ranges (each leaves at most one unit to its successors); grid.y shares
+// a unit's rows and columns.  Few parts (the usual batch): a thread joins one float4 of one
+// row.  Many (one long sequence): 64 columns of a row at a time, eight threads a float4.
 template <int D, int NT>
 __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(const DecodeFp8Params p)
 {
     using C = Dec8Cfg<D, NT>;
-    constexpr int COLS = D / 4, GROUPS = kD8CombineThreads / COLS;
+    constexpr int COLS = 16, GROUPS = kD8CombineThreads / COLS, SLICES = D / 64;
     __shared__ float4 sm_a[GROUPS][COLS];
     __shared__ float sm_m[kD8CombineThreads / 32], sm_l[GROUPS];
     const float NEG_INF = -__int_as_float(0x7f800000);
-    const int tid = threadIdx.x, r = blockIdx.y, ctas = p.ranges * p.row_groups;
-    const int x0 = blockIdx.x / p.row_groups, rg = blockIdx.x - x0 * p.row_groups;
-    if (rg * C::ROWS + r >= p.rows) return;
+    const int tid = threadIdx.x, ctas = p.ranges * p.row_groups;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 todo = reinterpret_cast<const int4*>(p.ws)[blockIdx.x];
-    if (todo.x < 0) return;
-    const int x1 = min(todo.x, p.ranges - 1);
-    const size_t row = (((size_t)todo.z << 31) | (size_t)todo.y) + r;
+    const int x0 = todo.x, x1 = min(todo.y, p.ranges - 1), rg = todo.z;
+    if (x0 < 0) return;
+    const size_t row0 = (size_t)todo.w;
+    const int rows = min(C::ROWS, p.rows - rg * C::ROWS);
     auto part_of = [&](int x) {
         return p.ws + 4 * ctas + (size_t)(2 * (x * p.row_groups + rg) + (x == x0 ? 1 : 0)) * C::PART;
     };
-    float M = NEG_INF;
-    for (int x = x0 + tid; x <= x1; x += kD8CombineThreads) M = fmaxf(M, part_of(x)[C::ROWS * D + r]);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-    if ((tid & 31) == 0) sm_m[tid >> 5] = M;
-    __syncthreads();
-    M = sm_m[0];
-#pragma unroll
-    for (int w = 1; w < kD8CombineThreads / 32; ++w) M = fmaxf(M, sm_m[w]);
-    const float mb = M == NEG_INF ? 0.0f : M;
-    const int grp = tid / COLS, col = tid - grp * COLS;
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
-#pragma unroll 4
-    for (int x = x0 + grp; x <= x1; x += GROUPS) {
+    auto finish = [&](int r, int col, float4 a, float sum, float mb) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (row0 + r) * D)[col] =
+            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        if (col == 0) p.lse[row0 + r] = sum == 0.0f ? NEG_INF : (mb + __log2f(sum)) * 0.69314718055994531f;
+    };
+    auto add = [&](int x, int r, int col, float mb, float4& a, float& l) {
         const float* w = part_of(x);
         const float fac = ex2(w[C::ROWS * D + r] - mb);
         const float4 v = *reinterpret_cast<const float4*>(w + r * D + col * 4);
         l = fmaf(fac, w[C::ROWS * D + C::ROWS + r], l);
         a.x = fmaf(fac, v.x, a.x), a.y = fmaf(fac, v.y, a.y);
         a.z = fmaf(fac, v.z, a.z), a.w = fmaf(fac, v.w, a.w);
-    }
-    sm_a[grp][col] = a;
-    if (col == 0) sm_l[grp] = l;
-    __syncthreads();
-    if (tid < COLS) {
-        float sum = 0.0f;
-        a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int k = 0; k < GROUPS; ++k) {
-            const float4 v = sm_a[k][tid];
-            a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-            sum += sm_l[k];
+    };
+    if (x1 - x0 < 4) {
+        for (int i = blockIdx.y * kD8CombineThreads + tid; i < rows * (D / 4); i += gridDim.y * kD8CombineThreads) {
+            const int r = i / (D / 4), col = i - r * (D / 4);
+            float M = NEG_INF, l = 0.0f;
+            for (int x = x0; x <= x1; ++x) M = fmaxf(M, part_of(x)[C::ROWS * D + r]);
+            const float mb = M == NEG_INF ? 0.0f : M;
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int x = x0; x <= x1; ++x) add(x, r, col, mb, a, l);
+            finish(r, col, a, l, mb);
         }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * D)[tid] =
-            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-        if (tid == 0) p.lse[row] = sum == 0.0f ? NEG_INF : (mb + __log2f(sum)) * 0.69314718055994531f;
+        return;
+    }
+    const int grp = tid / COLS;
+    for (int i = blockIdx.y; i < rows * SLICES; i += gridDim.y) {
+        const int r = i / SLICES, col = (i - r * SLICES) * COLS + tid % COLS;
+        float M = NEG_INF;
+        for (int x = x0 + tid; x <= x1; x += kD8CombineThreads) M = fmaxf(M, part_of(x)[C::ROWS * D + r]);
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+        if ((tid & 31) == 0) sm_m[tid >> 5] = M;
+        __syncthreads();
+        M = sm_m[0];
+#pragma unroll
+        for (int w = 1; w < kD8CombineThreads / 32; ++w) M = fmaxf(M, sm_m[w]);
+        const float mb = M == NEG_INF ? 0.0f : M;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float l = 0.0f;
+#pragma unroll 8
+        for (int x = x0 + grp; x <= x1; x += GROUPS) add(x, r, col, mb, a, l);
+        sm_a[grp][tid % COLS] = a;
+        if (tid % COLS == 0) sm_l[grp] = l;
+        __syncthreads();
+        if (tid < COLS) {
+            float sum = 0.0f;
+            a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < GROUPS; ++k) {
+                const float4 v = sm_a[k][tid];
+                a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+                sum += sm_l[k];
+            }
+            finish(r, col, a, sum, mb);
+        }
+        __syncthreads();
     }
 }
 
@@ -827,7 +855,11 @@ static cudaError_t launch_decode_fp8_n(const CUtensorMap& mk, const CUtensorMap&
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.ranges * p.row_groups, p.rows < C::ROWS ? p.rows : C::ROWS);
+    // as many CTAs for a unit as it has parts on average, up to one for 64 columns of a row
+    const long long units = (long long)p.B * p.Hkv * p.row_groups, ctas = p.ranges * p.row_groups;
+    const int items = (p.rows < C::ROWS ? p.rows : C::ROWS) * (D / 64);
+    const int share = units < ctas ? (int)(4 * ctas / units) : 2;
+    cfg.gridDim = dim3((unsigned)(units < ctas ? units : ctas), share < items ? share : items);
     cfg.blockDim = dim3(kD8CombineThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
