@@ -2,9 +2,10 @@
 
 The functions below carry the C entry points' names (``include/attn.h``) and do
 argument marshalling only: every arithmetic step runs in the CUDA library
-``_build/libgb300attn.so``.  PyTorch supplies device memory and the stream.
-There is no fallback: if the library is missing or fails to load, every call
-raises.
+``_build/libgb300attn.so``.  PyTorch supplies device memory and the stream.  The
+paged-cache calls of a serving step are marshalled natively (``csrc/binding.cpp``),
+the others through ctypes.  There is no fallback: if a library is missing or fails
+to load, every call raises.
 
     import exact_attention_55_gb300 as fa
     o, lse = fa.attn_fwd_bf16(q, k, v, causal=True)          # q, k, v: cuda bf16 [B,H,N,d]
@@ -76,6 +77,7 @@ EXPORTED_SYMBOLS = (
 
 _lock = threading.Lock()
 _lib = None
+_binding = None
 
 
 class AttnError(RuntimeError):
@@ -89,8 +91,9 @@ def library_path() -> str:
 
 
 def load_library(path: str | None = None):
-    """Load (once) and return the ctypes handle of the CUDA library.  Raises if absent."""
-    global _lib
+    """Load (once) and return the ctypes handle of the CUDA library, with the native binding
+    of the paged-cache calls.  Raises if either is absent."""
+    global _lib, _binding
     with _lock:
         if _lib is not None:
             return _lib
@@ -164,6 +167,12 @@ def load_library(path: str | None = None):
         lib.attn_selftest_bwd_withheld_load.restype = i
         lib.attn_selftest_fp8_convert.argtypes = [ctypes.c_uint, ctypes.c_size_t, i, vp, vp]
         lib.attn_selftest_fp8_convert.restype = i
+        if _binding is None:
+            binding = _build.load_binding()
+            binding.bind(*(ctypes.cast(getattr(lib, name), vp).value for name in (
+                "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
+                "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes")))
+            _binding = binding
         _lib = lib
         return lib
 
@@ -403,19 +412,20 @@ def attn_decode_bf16_paged_noalloc(q, k_cache, v_cache, page_table, seq_lens,
     return o, lse
 
 
-def _on(device, stream):
-    """The guard and stream handle of a call whose tensors live on `device`: the library
-    launches on the current device, on the given stream or that device's current one."""
+def _native():
+    """The native binding of the paged-cache calls (checks, outputs and the C call in one step)."""
+    if _binding is None:
+        load_library()
+    return _binding
+
+
+def _stream_on(stream, t):
+    """The handle of a given stream, which has to be on t's device (None: its current one)."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-    return torch.cuda.device(device), int(stream.cuda_stream)
-
-
-def _check_cuda(t, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+        return None
+    if isinstance(t, torch.Tensor) and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
+    return int(stream.cuda_stream)
 
 
 def attn_paged_plan(new_lens, seq_lens, page_table, free_pages, free_count, page_size: int,
@@ -427,102 +437,21 @@ def attn_paged_plan(new_lens, seq_lens, page_table, free_pages, free_count, page
     are left; num_tokens: packed rows of the step, at least the sum of new_lens.  Returns
     (seq_lens_out, free_count_out, cu_new, slot_map int64 [num_tokens], positions, served).
     seq_lens_out may be seq_lens and free_count_out free_count (in place)."""
-    _check_cuda(new_lens, "new_lens")
-    dev, i32 = new_lens.device, torch.int32
-    B, T = new_lens.numel(), int(num_tokens)
-    _check_out(new_lens, (B,), i32, dev, "new_lens")
-    _check_out(seq_lens, (B,), i32, dev, "seq_lens")
-    _check_out(free_count, (1,), i32, dev, "free_count")
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise TypeError("page_table must be an int32 [B, max_pages] tensor")
-    max_pages = page_table.shape[1]
-    _check_out(page_table, (B, max_pages), i32, dev, "page_table")
-    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
-        raise TypeError("free_pages must be an int32 [capacity] tensor")
-    _check_out(free_pages, (free_pages.numel(),), i32, dev, "free_pages")
-    if T < 0:
-        raise ValueError("num_tokens must not be negative")
-    outs = []
-    for name, t, shape, dtype in (("seq_lens_out", seq_lens_out, (B,), i32),
-                                  ("free_count_out", free_count_out, (1,), i32),
-                                  ("cu_new", cu_new, (B + 1,), i32),
-                                  ("slot_map", slot_map, (T,), torch.int64),
-                                  ("positions", positions, (T,), i32),
-                                  ("served", served, (B,), i32)):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            _check_out(t, shape, dtype, dev, name)
-        outs.append(t)
-    guard, s = _on(dev, stream)
-    with guard:
-        st = load_library().attn_paged_plan(
-            new_lens.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), free_pages.data_ptr(),
-            free_count.data_ptr(), *(t.data_ptr() for t in outs), B, int(page_size), max_pages,
-            free_pages.numel(), T, s)
-    _raise_if(st, "attn_paged_plan")
-    return tuple(outs)
-
-
-def _append_args(k, v, k_cache, v_cache, slot_map, cache_dtype):
-    _check_cuda(k, "k")
-    dev = k.device
-    for n, t in (("k", k), ("v", v)):
-        if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != dev
-                or t.dim() != 3):
-            raise TypeError(f"{n} must be a bf16 [T, Hkv, d] tensor on {dev}")
-    if v.shape != k.shape:
-        raise ValueError("k and v must have the same shape")
-    T, H, d = k.shape
-    strides = []
-    for n, t in (("k", k), ("v", v)):
-        if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
-            raise ValueError(f"{n}: the heads of a token must be contiguous")
-        strides.append(t.stride(0) if T > 1 else max(H * d, 8))
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if (not isinstance(t, torch.Tensor) or t.dtype not in cache_dtype or t.device != dev
-                or t.dim() != 4 or not t.is_contiguous()):
-            raise TypeError(f"{n} must be a contiguous [num_pages, Hkv, page_size, d] tensor of "
-                            f"{cache_dtype[0]} on {dev}")
-    if v_cache.shape != k_cache.shape or k_cache.shape[1] != H or k_cache.shape[3] != d:
-        raise ValueError("the caches must be [num_pages, Hkv, page_size, d] with k's heads and d")
-    _check_out(slot_map, (T,), torch.int64, dev, "slot_map")
-    return dev, T, H, d, strides, k_cache.shape[2], k_cache.shape[0]
+    r = _native().plan(new_lens, seq_lens, page_table, free_pages, free_count, page_size, num_tokens,
+                       seq_lens_out, free_count_out, cu_new, slot_map, positions, served,
+                       _stream_on(stream, new_lens))
+    if type(r) is int:
+        raise AttnError(r, "attn_paged_plan")
+    return r
 
 
 def attn_cache_append_bf16(k, v, k_cache, v_cache, slot_map, stream=None):
     """Write new keys and values (bf16 [T, Hkv, d]; tokens may be strided) to their slots
     (int64 [T], page * page_size + row; -1 skips a token) in the bf16 caches
     [num_pages, Hkv, page_size, d], in place.  Returns (k_cache, v_cache)."""
-    dev, T, H, d, strides, ps, pages = _append_args(k, v, k_cache, v_cache, slot_map,
-                                                    (torch.bfloat16,))
-    guard, s = _on(dev, stream)
-    with guard:
-        st = load_library().attn_cache_append_bf16(
-            k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            slot_map.data_ptr(), T, H, d, strides[0], strides[1], ps, pages, s)
+    st = _native().append_bf16(k, v, k_cache, v_cache, slot_map, _stream_on(stream, k))
     _raise_if(st, "attn_cache_append_bf16")
     return k_cache, v_cache
-
-
-_FP8_CACHE = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
-
-
-def _cache_block(k_cache, v_cache, k_scales, v_scales, fmt, dev):
-    """Rows per scale block, from the scales' shape; a typed cache has to hold fmt's codes."""
-    typed = torch.float8_e5m2 if _fp8_format(fmt) == ATTN_FP8_E5M2 else torch.float8_e4m3fn
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype not in (torch.uint8, typed):
-            raise TypeError(f"{n} holds {t.dtype}, not codes of {fmt!r}")
-    pages, H, ps, _ = k_cache.shape
-    if not isinstance(k_scales, torch.Tensor) or k_scales.dim() != 3 or k_scales.shape[2] < 1:
-        raise TypeError("k_scales must be a float32 [num_pages, Hkv, page_size / block] tensor")
-    nblk = k_scales.shape[2]
-    for n, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        _check_out(t, (pages, H, nblk), torch.float32, dev, n)
-    if ps % nblk:
-        raise ValueError("the scales' blocks must divide the page")
-    return ps // nblk
 
 
 def attn_cache_append_fp8(k, v, k_cache, v_cache, k_scales, v_scales, slot_map, fmt="e4m3",
@@ -531,14 +460,8 @@ def attn_cache_append_fp8(k, v, k_cache, v_cache, k_scales, v_scales, slot_map, 
     cache (codes [num_pages, Hkv, page_size, d], float32 scales [num_pages, Hkv,
     page_size / block]), in place.  A block's scale grows with its largest value; its
     earlier rows are then requantised.  Returns (k_cache, v_cache, k_scales, v_scales)."""
-    dev, T, H, d, strides, ps, pages = _append_args(k, v, k_cache, v_cache, slot_map, _FP8_CACHE)
-    block = _cache_block(k_cache, v_cache, k_scales, v_scales, fmt, dev)
-    guard, s = _on(dev, stream)
-    with guard:
-        st = load_library().attn_cache_append_fp8(
-            k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scales.data_ptr(), v_scales.data_ptr(), slot_map.data_ptr(), T, H, d, strides[0],
-            strides[1], ps, pages, block, _fp8_format(fmt), s)
+    st = _native().append_fp8(k, v, k_cache, v_cache, k_scales, v_scales, slot_map,
+                              _fp8_format(fmt), _stream_on(stream, k))
     _raise_if(st, "attn_cache_append_fp8")
     return k_cache, v_cache, k_scales, v_scales
 
@@ -555,47 +478,13 @@ def attn_decode_fp8_paged(q, k_cache, v_cache, k_scales, v_scales, page_table, s
     tokens, nq <= 8); caches and scales as attn_cache_append_fp8 leaves them, with Hkv heads
     (H a multiple of Hkv); page_table int32 [B, max_pages], seq_lens int32 [B] (the new
     tokens included); window > 0: a query sees the last window + 1 keys.  Returns
-    O [B, H, nq, d] and the natural-log LSE [B, H, nq]."""
-    _check_bhnd("q", q, torch.bfloat16)
-    dev = q.device
-    B, H, nq, d = q.shape
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if (not isinstance(t, torch.Tensor) or t.dtype not in _FP8_CACHE or t.device != dev
-                or t.dim() != 4 or not t.is_contiguous()):
-            raise TypeError(f"{n} must be a contiguous 8-bit [num_pages, Hkv, page_size, d] tensor on {dev}")
-    if v_cache.shape != k_cache.shape or k_cache.shape[3] != d:
-        raise ValueError("the caches must be [num_pages, Hkv, page_size, d] with q's d")
-    pages, Hkv, ps, _ = k_cache.shape
-    block = _cache_block(k_cache, v_cache, k_scales, v_scales, fmt, dev)
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise TypeError("page_table must be an int32 [B, max_pages] tensor")
-    _check_out(page_table, (B, page_table.shape[1]), torch.int32, dev, "page_table")
-    _check_out(seq_lens, (B,), torch.int32, dev, "seq_lens")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    if o is None:
-        o = torch.empty_like(q)
-    else:
-        _check_out(o, (B, H, nq, d), torch.bfloat16, dev, "o")
-    if lse is None:
-        lse = torch.empty((B, H, nq), dtype=torch.float32, device=dev)
-    else:
-        _check_out(lse, (B, H, nq), torch.float32, dev, "lse")
-    guard, s = _on(dev, stream)
-    with guard:
-        if workspace is None:
-            nbytes = attn_decode_fp8_workspace_bytes(H, Hkv, nq, d)
-            workspace = torch.empty(max(nbytes // 4, 4), dtype=torch.float32, device=dev)
-        elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != dev:
-            raise TypeError(f"workspace must be a contiguous CUDA tensor on {dev}")
-        st = load_library().attn_decode_fp8_paged(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
-            v_scales.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
-            lse.data_ptr(), B, H, Hkv, nq, d, ps, pages, page_table.shape[1], block,
-            _fp8_format(fmt), float(scale), int(window), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), s)
-    _raise_if(st, "attn_decode_fp8_paged")
-    return o, lse
+    O [B, H, nq, d] and the natural-log LSE [B, H, nq].  A workspace of
+    attn_decode_fp8_workspace_bytes(...) is allocated when none is given."""
+    r = _native().decode(q, k_cache, v_cache, k_scales, v_scales, page_table, seq_lens,
+                         _fp8_format(fmt), scale, window, workspace, o, lse, _stream_on(stream, q))
+    if type(r) is int:
+        raise AttnError(r, "attn_decode_fp8_paged")
+    return r
 
 
 def _quant_outputs(x, block, x8, scales):

@@ -3,20 +3,27 @@
 Every translation unit is compiled for sm_103a only
 (``-gencode arch=compute_103a,code=sm_103a``), in parallel, then linked into
 one shared library with the CUDA runtime linked statically.  The kernel file
-``attn_fwd_inst.cu`` is compiled once per (head dim, operand type) pair.
+``attn_fwd_inst.cu`` is compiled once per (head dim, operand type) pair.  Beside it,
+``csrc/binding.cpp`` becomes a Python extension against the installed PyTorch
+(``_build/_gb300attn_binding.so``): host code only, compiled by the host compiler.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.machinery
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB_NAME = "libgb300attn.so"
 LIB_PATH = os.path.join(BUILD, LIB_NAME)
+BINDING_NAME = "_gb300attn_binding"
+BINDING_PATH = os.path.join(BUILD, BINDING_NAME + ".so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -55,9 +62,37 @@ def _sources_mtime() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
+def _compile_binding() -> None:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *("-I" + i for i in inc),
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
+def load_binding():
+    """The native binding's module; raises if it is not built."""
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"binding not built: {BINDING_PATH} is missing "
+                           "(run exact_attention_55_gb300.build.build())")
+    loader = importlib.machinery.ExtensionFileLoader(BINDING_NAME, BINDING_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader(BINDING_NAME, loader))
+    loader.exec_module(module)
+    return module
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if stale) and return the path of the shared library."""
-    if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= _sources_mtime():
+    built = (LIB_PATH, BINDING_PATH)
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _sources_mtime() for p in built):
         return LIB_PATH
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -73,8 +108,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {name}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(UNITS)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(UNITS) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(compile_unit, UNITS))
+        binding.result()
     if verbose:
         for obj, log in results:
             print(f"== {os.path.basename(obj)}\n{log}")
