@@ -1017,6 +1017,10 @@ extern "C" attn_status_t attn_cache_append_fp8(const void* k, const void* v, voi
     if (T == 0) return ATTN_OK;
     if (!k_scales || !v_scales) return ATTN_ERR_INVALID_ARG;
     if (!aligned(k_scales, 4) || !aligned(v_scales, 4)) return ATTN_ERR_MISALIGNED;
+    DeviceInfo* dev = nullptr;
+    const attn_status_t info = device_info(&dev);
+    if (info != ATTN_OK) return info;
+    p.sm_count = dev->sm_count;
     p.ks = k_scales;
     p.vs = v_scales;
     p.log2_blk = page_log2(block);

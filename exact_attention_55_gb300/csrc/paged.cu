@@ -190,31 +190,44 @@ cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream)
 
 // ------------------------------------------------------------------ bf16 append
 //
-// cache[slot / ps][h][slot % ps] = row (t, h), 16 bytes a thread; slots outside the cache
-// (padding) are skipped.  HBM-bound: each row is read once and written once.
+// cache[slot / ps][h][slot % ps] = row (t, h); slots outside the cache (padding) are
+// skipped.  HBM-bound: each row is read once and written once.  A CTA takes kTokens tokens of
+// K or V, all heads; a token's heads are one run of memory on the input side, so a thread
+// copies the same 16-byte piece of each token, the loads of its tokens in flight together.
+template <int kTokens>
 __global__ void __launch_bounds__(256) cache_append_bf16_kernel(const AppendParams p)
 {
-    const int chunks = p.d / 8;                    // 16-byte pieces of a row
-    const long long total = (long long)p.T * p.H * chunks;
-    const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (idx >= total) return;
-    const int c = (int)(idx % chunks);
-    const long long row = idx / chunks;
-    const int t = (int)(row / p.H), h = (int)(row - (long long)t * p.H);
-    const long long slot = p.slot_map[t];
-    if (slot < 0 || slot >= p.num_slots) return;
     const bool is_v = blockIdx.y != 0;
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k) +
-                               (long long)t * (is_v ? p.v_stride : p.k_stride) + h * p.d + c * 8;
-    const long long to = ((((slot >> p.log2_ps) * p.H + h) << p.log2_ps) + (slot & ((1 << p.log2_ps) - 1))) * p.d;
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.vc : p.kc) + to + c * 8) =
-        *reinterpret_cast<const uint4*>(src);
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k);
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.vc : p.kc);
+    const long long stride = is_v ? p.v_stride : p.k_stride;
+    const int t0 = blockIdx.x * kTokens, ps_mask = (1 << p.log2_ps) - 1;
+    const int log2_d = p.d == 64 ? 6 : p.d == 128 ? 7 : 8;
+    long long at[kTokens];                         // row of (page, head 0, slot % ps), or -1
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const long long slot = t0 + i < p.T ? __ldg(p.slot_map + t0 + i) : -1;
+        at[i] = slot < 0 || slot >= p.num_slots
+                    ? -1 : (((slot >> p.log2_ps) * p.H) << p.log2_ps) + (slot & ps_mask);
+    }
+    for (int e = threadIdx.x * 8; e < p.H << log2_d; e += 256 * 8) {
+        const long long head = (long long)(e >> log2_d) << p.log2_ps;
+        uint4 x[kTokens];
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i)
+            if (at[i] >= 0) x[i] = __ldcs(reinterpret_cast<const uint4*>(src + (t0 + i) * stride + e));
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i)
+            if (at[i] >= 0)
+                *reinterpret_cast<uint4*>(dst + ((at[i] + head) << log2_d) + (e & (p.d - 1))) = x[i];
+    }
 }
 
 cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream)
 {
-    const long long total = (long long)p.T * p.H * (p.d / 8);
-    cache_append_bf16_kernel<<<dim3((unsigned)((total + 255) / 256), 2), 256, 0, stream>>>(p);
+    // one token a CTA while that is what spreads the work, else four
+    if (p.T <= 1024) cache_append_bf16_kernel<1><<<dim3(p.T, 2), 256, 0, stream>>>(p);
+    else cache_append_bf16_kernel<4><<<dim3((unsigned)(((long long)p.T + 3) / 4), 2), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -231,22 +244,16 @@ cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream)
 // bytes are a pure function of the inputs.
 //
 // A CTA takes the runs whose first token lies in its tile of packed tokens, for one head
-// of K or V: a run is at most one block long, so it reads at most tile + block - 1 tokens.
-// First pass: row maxima, joined per run in shared memory (a maximum does not depend on
-// the order).  Then one thread per run settles the scale, and the second pass reads the
-// rows again (from L1 or L2) and writes the codes.
-constexpr int kAppendThreads = 256;
+// (K, V, or one after the other): a run is at most one block long, so the runs of a tile
+// span at most tile + block - 1 tokens.  Row maxima are joined per run in shared memory (a
+// maximum does not depend on the order), one thread per run settles the scale, and the rows
+// are converted.  HBM-bound when it prefills: the rows stay in registers in between, 128 of
+// them (what a tile holds unless short runs and one of a whole block meet in it; rows past
+// that are read again).  The quotient is formed from the reciprocal with one residual
+// correction, as in the block quantiser; values that this cannot take (infinities, scales
+// near fp32's limits) go through the division itself.
 constexpr int kAppendWindow = 256;     // tokens a CTA looks at: tile + block - 1 < 256
-
-__device__ __forceinline__ float append_pow2_at_least(float s)
-{
-    const uint32_t b = __float_as_uint(s);
-    if ((b & 0x7F800000u) == 0) {      // zero or subnormal
-        const uint32_t m = b & 0x7FFFFFu;
-        return __uint_as_float((m & (m - 1)) == 0 ? m : (1u << (32 - __clz(m))));
-    }
-    return (b & 0x7FFFFFu) == 0 ? s : __uint_as_float((b & 0x7F800000u) + 0x00800000u);
-}
+constexpr int kAppendHeld = 128;       // rows held in registers
 
 template <bool kE5M2>
 __device__ __forceinline__ uint32_t pack4_fp8(float a, float b, float c, float d)
@@ -269,38 +276,45 @@ __device__ __forceinline__ float2 unpack2_fp8(uint32_t two)
     return make_float2(lo, hi);
 }
 
+template <int D> struct AppendCfg {
+    static constexpr int LPR = D / 8;                       // lanes of a row, 8 values each
+    static constexpr int THREADS = D == 256 ? 512 : 256;
+    static constexpr int RPP = THREADS / LPR;               // rows of a pass
+    static constexpr int HELD = kAppendHeld / RPP;          // passes whose rows stay in registers
+};
+
 template <int D, bool kE5M2>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_fp8_kernel(const AppendParams p)
+__global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
+    cache_append_fp8_kernel(const AppendParams p)
 {
-    constexpr int LPR = D / 8;                       // lanes of a row, 8 values each
-    constexpr int RPP = kAppendThreads / LPR;        // rows of a pass
+    using C = AppendCfg<D>;
     __shared__ long long slots[kAppendWindow];
     __shared__ int run_of[kAppendWindow];            // window index of the token's run, or -1
-    __shared__ unsigned run_max[kAppendWindow];      // bits of the run's largest |x|
+    __shared__ unsigned run_max[kAppendWindow];      // bits of the run's largest finite |x|
     __shared__ float run_scale[kAppendWindow], run_old[kAppendWindow];
     __shared__ int grown[kAppendWindow];
-    __shared__ int num_grown, warp_last[kAppendThreads / 32], num_rows;
+    __shared__ int num_grown, warp_last[kAppendWindow / 32], first_row, end_row;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int block = 1 << p.log2_blk, tile = block < 64 ? 64 : block;
+    const int block = 1 << p.log2_blk, tile = block < 64 ? 64 : block, ps_mask = (1 << p.log2_ps) - 1;
     const int h = blockIdx.y;
-    const bool is_v = blockIdx.z != 0;
     const long long t0 = (long long)blockIdx.x * tile;
     const int window = (int)min((long long)(tile + block - 1), p.T - t0);
 
     auto slot_at = [&](long long t) -> long long {
-        const long long s = p.slot_map[t];
+        const long long s = __ldg(p.slot_map + t);
         return s >= 0 && s < p.num_slots ? s : -1;
     };
     // heads of runs, then the nearest head at or before each token
-    {
-        const int i = tid;
-        long long s = -1, before = -1;
-        if (i < window) {
-            s = slot_at(t0 + i);
-            if (t0 + i > 0) before = slot_at(t0 + i - 1);
+    int last = -1;
+    long long slot = -1;
+    if (tid < kAppendWindow) {
+        long long before = -1;
+        if (tid < window) {
+            slot = slot_at(t0 + tid);
+            if (t0 + tid > 0) before = slot_at(t0 + tid - 1);
         }
-        const bool head = s >= 0 && (before < 0 || s != before + 1 || (s & (block - 1)) == 0);
-        int last = head ? i : -1;
+        const bool head = slot >= 0 && (before < 0 || slot != before + 1 || (slot & (block - 1)) == 0);
+        last = head ? tid : -1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, last, o);
@@ -308,93 +322,132 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_fp8_kernel(const 
         }
         if (lane == 31) warp_last[warp] = last;
         if (tid == 0) {
-            num_grown = 0;
-            num_rows = 0;
+            first_row = kAppendWindow;
+            end_row = 0;
         }
-        run_max[i] = 0;
-        slots[i] = s;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) last = max(last, warp_last[w]);
-        const int run = s >= 0 && last < tile ? last : -1;
-        run_of[i] = run;
-        if (run >= 0) atomicMax(&num_rows, i + 1);
-        __syncthreads();
+        slots[tid] = slot;
     }
-    const int rows = num_rows;
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k) + h * D;
-    const long long stride = is_v ? p.v_stride : p.k_stride;
-    uint8_t* cache = static_cast<uint8_t*>(is_v ? p.vc : p.kc);
-    float* scales = is_v ? p.vs : p.ks;
-    const int c = tid % LPR;
-    auto load = [&](int i, float (&x)[8]) {
-        const uint4 w = *reinterpret_cast<const uint4*>(src + (t0 + i) * stride + c * 8);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[2 * e] = __uint_as_float(u[e] << 16);
-            x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+    __syncthreads();
+    if (tid < kAppendWindow) {
+        for (int w = 0; w < warp; ++w) last = max(last, warp_last[w]);
+        const int run = slot >= 0 && last < tile ? last : -1;
+        run_of[tid] = run;
+        run_max[tid] = 0;
+        const unsigned mine = __ballot_sync(0xffffffffu, run >= 0);
+        if (lane == 0 && mine) {
+            atomicMin(&first_row, tid + __ffs(mine) - 1);
+            atomicMax(&end_row, tid + 32 - __clz(mine));
         }
+    }
+    if (tid == 0) num_grown = 0;
+    __syncthreads();
+    const int begin = first_row, end = end_row;
+    if (end <= begin) return;
+    const int c = tid % C::LPR, row_in_pass = tid / C::LPR;
+    auto row_address = [&](long long s) {
+        return ((((s >> p.log2_ps) * p.H + h) << p.log2_ps) + (s & ps_mask)) * D;
     };
-    auto row_address = [&](long long slot) {
-        return ((((slot >> p.log2_ps) * p.H + h) << p.log2_ps) + (slot & ((1 << p.log2_ps) - 1))) * D;
-    };
-    for (int i0 = 0; i0 < rows; i0 += RPP) {
-        const int i = i0 + tid / LPR;
-        const int run = i < rows ? run_of[i] : -1;
-        float a = 0.0f;
-        if (run >= 0) {
-            float x[8];
-            load(i, x);
+    // eight values' largest finite magnitude; NaN and infinities are left out
+    auto magnitude = [](const uint4& w) -> float {
+        const uint32_t a[4] = {w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu, w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu};
+        const uint32_t m2 = __vmaxu2(__vmaxu2(a[0], a[1]), __vmaxu2(a[2], a[3]));
+        uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+        if (m >= 0x7F80u) {
+            m = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float m = fabsf(x[e]);
-                a = fmaxf(a, m < __int_as_float(0x7f800000) ? m : 0.0f);   // finite values only
+            for (int i = 0; i < 4; ++i) {
+                if ((a[i] & 0xFFFFu) < 0x7F80u) m = max(m, a[i] & 0xFFFFu);
+                if ((a[i] >> 16) < 0x7F80u) m = max(m, a[i] >> 16);
             }
         }
+        return __uint_as_float(m << 16);
+    };
+
+    for (int z = blockIdx.z; z < 2; z += gridDim.z) {
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(z ? p.v : p.k) + h * D + c * 8;
+        const long long stride = z ? p.v_stride : p.k_stride;
+        uint8_t* cache = static_cast<uint8_t*>(z ? p.vc : p.kc);
+        float* scales = z ? p.vs : p.ks;
+        auto load = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(src + (t0 + i) * stride)); };
+        auto run_at = [&](int i) { return i < end ? run_of[i] : -1; };
+        auto join = [&](int run, const uint4& w) {
+            float a = run >= 0 ? magnitude(w) : 0.0f;
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        if (run >= 0 && c == 0) atomicMax(&run_max[run], __float_as_uint(a));
-    }
-    __syncthreads();
-    if (tid < tile && run_of[tid] == tid) {
-        const long long slot = slots[tid];
-        const int row = (int)(slot & (block - 1));
-        float* sc = scales + ((((slot >> p.log2_ps) * p.H + h) << (p.log2_ps - p.log2_blk)) +
-                              ((slot & ((1 << p.log2_ps) - 1)) >> p.log2_blk));
-        float need = __fdiv_rn(__uint_as_float(run_max[tid]), kE5M2 ? 57344.0f : 448.0f);
-        if (p.pow2) need = append_pow2_at_least(need);
-        const float old = row > 0 ? *sc : 0.0f;
-        const float s = fmaxf(old, need);
-        run_old[tid] = old;
-        run_scale[tid] = s;
-        if (row == 0 || s > old) *sc = s;
-        if (row > 0 && s > old) grown[atomicAdd(&num_grown, 1)] = tid;
-    }
-    __syncthreads();
-    for (int i0 = 0; i0 < rows; i0 += RPP) {
-        const int i = i0 + tid / LPR;
-        const int run = i < rows ? run_of[i] : -1;
-        if (run < 0) continue;
-        float x[8];
-        load(i, x);
-        const float s = run_scale[run] > 0.0f ? run_scale[run] : 1.0f;
+            for (int o = C::LPR / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            if (run >= 0 && c == 0) atomicMax(&run_max[run], __float_as_uint(a));
+        };
+        uint4 x[C::HELD];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(x[e], s);
-        *reinterpret_cast<uint2*>(cache + row_address(slots[i]) + c * 8) =
-            make_uint2(pack4_fp8<kE5M2>(x[0], x[1], x[2], x[3]), pack4_fp8<kE5M2>(x[4], x[5], x[6], x[7]));
-    }
-    // blocks whose scale grew: their earlier rows, one warp a block
-    for (int g = warp; g < num_grown; g += kAppendThreads / 32) {
-        const int run = grown[g];
-        const long long slot = slots[run];
-        const int row = (int)(slot & (block - 1));
-        const float old = run_old[run], s = run_scale[run];
-        uint32_t* base = reinterpret_cast<uint32_t*>(cache + row_address(slot - row));
-        for (int w = lane; w < row * (D / 4); w += 32) {
-            const uint32_t codes = base[w];
-            const float2 a = unpack2_fp8<kE5M2>(codes & 0xFFFFu), b = unpack2_fp8<kE5M2>(codes >> 16);
-            base[w] = pack4_fp8<kE5M2>(__fdiv_rn(a.x * old, s), __fdiv_rn(a.y * old, s),
-                                       __fdiv_rn(b.x * old, s), __fdiv_rn(b.y * old, s));
+        for (int k = 0; k < C::HELD; ++k) {
+            const int i = begin + k * C::RPP + row_in_pass;
+            if (run_at(i) >= 0) x[k] = load(i);
+        }
+#pragma unroll
+        for (int k = 0; k < C::HELD; ++k) join(run_at(begin + k * C::RPP + row_in_pass), x[k]);
+        for (int i0 = begin + kAppendHeld; i0 < end; i0 += C::RPP) {
+            const int i = i0 + row_in_pass, run = run_at(i);
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (run >= 0) w = load(i);
+            join(run, w);
+        }
+        __syncthreads();
+        if (tid < tile && run_of[tid] == tid) {
+            const long long s0 = slots[tid];
+            const int row = (int)(s0 & (block - 1));
+            float* sc = scales + ((((s0 >> p.log2_ps) * p.H + h) << (p.log2_ps - p.log2_blk)) +
+                                  ((s0 & ps_mask) >> p.log2_blk));
+            float need = __fdiv_rn(__uint_as_float(run_max[tid]), kE5M2 ? 57344.0f : 448.0f);
+            if (p.pow2) need = pow2_at_least(need);
+            const float old = row > 0 ? *sc : 0.0f;
+            const float s = fmaxf(old, need);
+            run_old[tid] = old;
+            run_scale[tid] = s;
+            if (row == 0 || s > old) *sc = s;
+            if (row > 0 && s > old) grown[atomicAdd(&num_grown, 1)] = tid;
+        }
+        __syncthreads();
+        auto write = [&](int i, int run, const uint4& w) {
+            const float s = run_scale[run] > 0.0f ? run_scale[run] : 1.0f;
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            float2 v[4];
+            const uint32_t m2 = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu),
+                                         __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
+            const bool plain = max(m2 & 0xFFFFu, m2 >> 16) < 0x7F80u && s > 1e-30f && s < 1e30f;
+            const float2 y = make_float2(__frcp_rn(s), __frcp_rn(s)), neg = make_float2(-s, -s);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 a = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xFFFF0000u));
+                v[k] = plain ? div2_by_scale(a, neg, y) : make_float2(__fdiv_rn(a.x, s), __fdiv_rn(a.y, s));
+            }
+            *reinterpret_cast<uint2*>(cache + row_address(slots[i]) + c * 8) =
+                make_uint2(pack4_fp8<kE5M2>(v[0].x, v[0].y, v[1].x, v[1].y),
+                           pack4_fp8<kE5M2>(v[2].x, v[2].y, v[3].x, v[3].y));
+        };
+#pragma unroll
+        for (int k = 0; k < C::HELD; ++k) {
+            const int i = begin + k * C::RPP + row_in_pass, run = run_at(i);
+            if (run >= 0) write(i, run, x[k]);
+        }
+        for (int i = begin + kAppendHeld + row_in_pass; i < end; i += C::RPP)
+            if (run_of[i] >= 0) write(i, run_of[i], load(i));
+        // blocks whose scale grew: their earlier rows, one warp a block
+        for (int k = warp; k < num_grown; k += C::THREADS / 32) {
+            const int run = grown[k];
+            const int row = (int)(slots[run] & (block - 1));
+            const float old = run_old[run], s = run_scale[run];
+            uint32_t* base = reinterpret_cast<uint32_t*>(cache + row_address(slots[run] - row));
+            for (int w = lane; w < row * (D / 4); w += 32) {
+                const uint32_t codes = base[w];
+                const float2 a = unpack2_fp8<kE5M2>(codes & 0xFFFFu), b = unpack2_fp8<kE5M2>(codes >> 16);
+                base[w] = pack4_fp8<kE5M2>(__fdiv_rn(a.x * old, s), __fdiv_rn(a.y * old, s),
+                                           __fdiv_rn(b.x * old, s), __fdiv_rn(b.y * old, s));
+            }
+        }
+        if (z + gridDim.z < 2) {
+            __syncthreads();
+            if (tid < kAppendWindow) run_max[tid] = 0;
+            if (tid == 0) num_grown = 0;
+            __syncthreads();
         }
     }
 }
@@ -403,9 +456,12 @@ template <int D>
 static cudaError_t launch_append_fp8_d(const AppendParams& p, bool e5m2, cudaStream_t stream)
 {
     const int block = 1 << p.log2_blk, tile = block < 64 ? 64 : block;
-    const dim3 grid((unsigned)((p.T + tile - 1) / tile), p.H, 2);
-    if (e5m2) cache_append_fp8_kernel<D, true><<<grid, kAppendThreads, 0, stream>>>(p);
-    else cache_append_fp8_kernel<D, false><<<grid, kAppendThreads, 0, stream>>>(p);
+    const long long tiles = ((long long)p.T + tile - 1) / tile;
+    // K and V in CTAs of their own while there are few, else one after the other
+    const dim3 grid((unsigned)tiles, p.H, tiles * p.H <= 2 * p.sm_count ? 2 : 1);
+    constexpr int threads = AppendCfg<D>::THREADS;
+    if (e5m2) cache_append_fp8_kernel<D, true><<<grid, threads, 0, stream>>>(p);
+    else cache_append_fp8_kernel<D, false><<<grid, threads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -35,6 +35,7 @@ struct AppendParams {
     int T, H, d;
     int log2_ps, log2_blk;
     int pow2;               // scales are rounded up to powers of two
+    int sm_count;
 };
 
 // One decoding step over an 8-bit paged cache.

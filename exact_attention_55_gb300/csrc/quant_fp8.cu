@@ -78,18 +78,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
-// RN(x / s) for two values at once, s > 0 finite and the quotients normal, from
-// y = RN(1/s) and s_neg = -s: q = RN(x y), r = x - q s (exact), RN(q + r y).
-__device__ __forceinline__ float2 div2_by_scale(float2 x, float2 s_neg, float2 y)
-{
-    const float2 q = __fmul2_rn(x, y);
-    const float2 r = __ffma2_rn(q, s_neg, x);  // x - q s, exact
-    const float2 c = __ffma2_rn(r, y, q);
-    // c equals q when r == 0, except that q = -0 (x = -0) would come back as +0;
-    // the quotient's sign is x's in every case
-    return make_float2(copysignf(c.x, x.x), copysignf(c.y, x.y));
-}
-
 // a + b and a - b of two pairs, each rounded once (a - b as fma(b, -1, a)).
 __device__ __forceinline__ void butterfly2(float& a0, float& a1, float& b0, float& b1)
 {
@@ -115,16 +103,6 @@ template <int DR> struct QuantShape {
 // DR = 0: plain per-block quantisation (any d); DR = d in {64, 128, 256}: rotate first.
 // FMT = 0: E4M3; FMT = 1: E5M2; FMT = 2: E4M3 with power-of-two scales (plain only).
 
-// The smallest power of two >= s (s > 0 finite), normal or subnormal.
-__device__ __forceinline__ float pow2_at_least(float s)
-{
-    const uint32_t b = __float_as_uint(s);
-    if ((b & 0x7F800000u) == 0) {  // subnormal: 2^k >= m * 2^-149 from m's highest bit
-        const uint32_t m = b & 0x7FFFFFu;
-        return __uint_as_float((m & (m - 1)) == 0 ? m : (1u << (32 - __clz(m))));
-    }
-    return (b & 0x7FFFFFu) == 0 ? s : __uint_as_float((b & 0x7F800000u) + 0x00800000u);
-}
 template <int DR, int FMT = 0>
 __global__ void __launch_bounds__(QuantShape<DR>::kThreads, QuantShape<DR>::kMinBlocks)
     quant_fp8_kernel(const QuantParams p)
