@@ -243,8 +243,8 @@ cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream)
 // where code() rounds to nearest even and saturates.  All divisions are IEEE fp32, so the
 // bytes are a pure function of the inputs.
 //
-// A CTA takes the runs whose first token lies in its tile of packed tokens, for one head
-// (K, V, or one after the other): a run is at most one block long, so the runs of a tile
+// A CTA takes the runs whose first token lies in its tile of packed tokens, for some of the
+// heads of K and V, one after the other: a run is at most one block long, so the runs of a tile
 // span at most tile + block - 1 tokens.  Row maxima are joined per run in shared memory (a
 // maximum does not depend on the order), one thread per run settles the scale, and the rows
 // are converted.  HBM-bound when it prefills: the rows stay in registers in between, 128 of
@@ -276,6 +276,42 @@ __device__ __forceinline__ float2 unpack2_fp8(uint32_t two)
     return make_float2(lo, hi);
 }
 
+// Per half: the larger of two bf16 magnitudes (its sign is of no use), NaN if one is NaN.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// RN(x / s) of four values as codes, from their bf16 words, s and RN(1 / s).  The residual
+// correction loses the sign of a zero; it is put back on the codes.
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t quotient4(uint32_t a, uint32_t b, float s, float inv)
+{
+    const float2 neg = make_float2(-s, -s), y = make_float2(inv, inv);
+    const float2 xa = make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+    const float2 xb = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
+    const float2 qa = __fmul2_rn(xa, y), qb = __fmul2_rn(xb, y);
+    const float2 ca = __ffma2_rn(__ffma2_rn(qa, neg, xa), y, qa), cb = __ffma2_rn(__ffma2_rn(qb, neg, xb), y, qb);
+    return pack4_fp8<kE5M2>(ca.x, ca.y, cb.x, cb.y) | (__byte_perm(a, b, 0x7531) & 0x80808080u);
+}
+
+// Eight codes by division, out of line: the rare runs that the reciprocal cannot take.
+template <bool kE5M2>
+__device__ __noinline__ uint2 divide8(uint4 w, float s)
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t out[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        out[k] = pack4_fp8<kE5M2>(__fdiv_rn(__uint_as_float(u[2 * k] << 16), s),
+                                  __fdiv_rn(__uint_as_float(u[2 * k] & 0xFFFF0000u), s),
+                                  __fdiv_rn(__uint_as_float(u[2 * k + 1] << 16), s),
+                                  __fdiv_rn(__uint_as_float(u[2 * k + 1] & 0xFFFF0000u), s));
+    return make_uint2(out[0], out[1]);
+}
+
 template <int D> struct AppendCfg {
     static constexpr int LPR = D / 8;                       // lanes of a row, 8 values each
     static constexpr int THREADS = D == 256 ? 512 : 256;
@@ -292,11 +328,12 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
     __shared__ int run_of[kAppendWindow];            // window index of the token's run, or -1
     __shared__ unsigned run_max[kAppendWindow];      // bits of the run's largest finite |x|
     __shared__ float run_scale[kAppendWindow], run_old[kAppendWindow];
+    __shared__ float run_inv[kAppendWindow];         // 1 / scale, or 0: divide
+    __shared__ int run_odd[kAppendWindow];           // the run has a value that is not finite
     __shared__ int grown[kAppendWindow];
-    __shared__ int num_grown, warp_last[kAppendWindow / 32], first_row, end_row;
+    __shared__ int num_grown[2], warp_last[kAppendWindow / 32], first_row, end_row;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int block = 1 << p.log2_blk, tile = block < 64 ? 64 : block, ps_mask = (1 << p.log2_ps) - 1;
-    const int h = blockIdx.y;
     const long long t0 = (long long)blockIdx.x * tile;
     const int window = (int)min((long long)(tile + block - 1), p.T - t0);
 
@@ -333,37 +370,40 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
         const int run = slot >= 0 && last < tile ? last : -1;
         run_of[tid] = run;
         run_max[tid] = 0;
+        run_odd[tid] = 0;
         const unsigned mine = __ballot_sync(0xffffffffu, run >= 0);
         if (lane == 0 && mine) {
             atomicMin(&first_row, tid + __ffs(mine) - 1);
             atomicMax(&end_row, tid + 32 - __clz(mine));
         }
     }
-    if (tid == 0) num_grown = 0;
+    if (tid == 0) num_grown[0] = 0;
     __syncthreads();
     const int begin = first_row, end = end_row;
     if (end <= begin) return;
     const int c = tid % C::LPR, row_in_pass = tid / C::LPR;
-    auto row_address = [&](long long s) {
-        return ((((s >> p.log2_ps) * p.H + h) << p.log2_ps) + (s & ps_mask)) * D;
+    // eight values' largest magnitude as bf16 bits, and the largest finite one
+    auto largest = [](const uint4& w) -> uint32_t {
+        const uint32_t m2 = max_abs_bf16x2(max_abs_bf16x2(w.x, w.y), max_abs_bf16x2(w.z, w.w));
+        return max(m2 & 0x7FFFu, (m2 >> 16) & 0x7FFFu);
     };
-    // eight values' largest finite magnitude; NaN and infinities are left out
-    auto magnitude = [](const uint4& w) -> float {
-        const uint32_t a[4] = {w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu, w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu};
-        const uint32_t m2 = __vmaxu2(__vmaxu2(a[0], a[1]), __vmaxu2(a[2], a[3]));
-        uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-        if (m >= 0x7F80u) {
-            m = 0;
+    auto largest_finite = [](const uint4& w) -> uint32_t {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if ((a[i] & 0xFFFFu) < 0x7F80u) m = max(m, a[i] & 0xFFFFu);
-                if ((a[i] >> 16) < 0x7F80u) m = max(m, a[i] >> 16);
-            }
+        for (int i = 0; i < 4; ++i) {
+            if ((u[i] & 0x7FFFu) < 0x7F80u) m = max(m, u[i] & 0x7FFFu);
+            if (((u[i] >> 16) & 0x7FFFu) < 0x7F80u) m = max(m, (u[i] >> 16) & 0x7FFFu);
         }
-        return __uint_as_float(m << 16);
+        return m;
     };
+    const bool single = run_of[begin] == run_of[end - 1] && end - begin <= kAppendHeld;   // one run: a prefill's tile
 
-    for (int z = blockIdx.z; z < 2; z += gridDim.z) {
+    for (int item = blockIdx.y, odd = 0; item < 2 * p.H; item += gridDim.y, odd ^= 1) {
+        const int h = item >> 1, z = item & 1;
+        auto row_address = [&](long long s) {
+            return ((((s >> p.log2_ps) * p.H + h) << p.log2_ps) + (s & ps_mask)) * D;
+        };
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(z ? p.v : p.k) + h * D + c * 8;
         const long long stride = z ? p.v_stride : p.k_stride;
         uint8_t* cache = static_cast<uint8_t*>(z ? p.vc : p.kc);
@@ -371,24 +411,43 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
         auto load = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(src + (t0 + i) * stride)); };
         auto run_at = [&](int i) { return i < end ? run_of[i] : -1; };
         auto join = [&](int run, const uint4& w) {
-            float a = run >= 0 ? magnitude(w) : 0.0f;
-#pragma unroll
-            for (int o = C::LPR / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            if (run >= 0 && c == 0) atomicMax(&run_max[run], __float_as_uint(a));
+            uint32_t a = run >= 0 ? largest(w) : 0u;
+            if (a >= 0x7F80u) {
+                a = largest_finite(w);
+                run_odd[run] = 1;
+            }
+            const unsigned row_lanes = C::LPR == 32 ? 0xffffffffu : ((1u << C::LPR) - 1) << (lane & ~(C::LPR - 1));
+            a = __reduce_max_sync(row_lanes, a);
+            if (run >= 0 && c == 0) atomicMax(&run_max[run], a << 16);
         };
         uint4 x[C::HELD];
 #pragma unroll
         for (int k = 0; k < C::HELD; ++k) {
             const int i = begin + k * C::RPP + row_in_pass;
+            x[k] = make_uint4(0, 0, 0, 0);
             if (run_at(i) >= 0) x[k] = load(i);
         }
+        if (single) {
+            uint32_t a = 0;
 #pragma unroll
-        for (int k = 0; k < C::HELD; ++k) join(run_at(begin + k * C::RPP + row_in_pass), x[k]);
-        for (int i0 = begin + kAppendHeld; i0 < end; i0 += C::RPP) {
-            const int i = i0 + row_in_pass, run = run_at(i);
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (run >= 0) w = load(i);
-            join(run, w);
+            for (int k = 0; k < C::HELD; ++k) a = max(a, largest(x[k]));
+            if (a >= 0x7F80u) {
+                a = 0;
+#pragma unroll
+                for (int k = 0; k < C::HELD; ++k) a = max(a, largest_finite(x[k]));
+                run_odd[run_of[begin]] = 1;
+            }
+            a = __reduce_max_sync(0xffffffffu, a);
+            if (lane == 0) atomicMax(&run_max[run_of[begin]], a << 16);
+        } else {
+#pragma unroll
+            for (int k = 0; k < C::HELD; ++k) join(run_at(begin + k * C::RPP + row_in_pass), x[k]);
+            for (int i0 = begin + kAppendHeld; i0 < end; i0 += C::RPP) {
+                const int i = i0 + row_in_pass, run = run_at(i);
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (run >= 0) w = load(i);
+                join(run, w);
+            }
         }
         __syncthreads();
         if (tid < tile && run_of[tid] == tid) {
@@ -396,42 +455,48 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
             const int row = (int)(s0 & (block - 1));
             float* sc = scales + ((((s0 >> p.log2_ps) * p.H + h) << (p.log2_ps - p.log2_blk)) +
                                   ((s0 & ps_mask) >> p.log2_blk));
+            const bool finite = run_odd[tid] == 0;
             float need = __fdiv_rn(__uint_as_float(run_max[tid]), kE5M2 ? 57344.0f : 448.0f);
             if (p.pow2) need = pow2_at_least(need);
             const float old = row > 0 ? *sc : 0.0f;
             const float s = fmaxf(old, need);
             run_old[tid] = old;
-            run_scale[tid] = s;
+            run_scale[tid] = s > 0.0f ? s : 1.0f;
+            run_inv[tid] = finite && s > 1e-30f && s < 1e30f ? __frcp_rn(s) : 0.0f;
             if (row == 0 || s > old) *sc = s;
-            if (row > 0 && s > old) grown[atomicAdd(&num_grown, 1)] = tid;
+            if (row > 0 && s > old) grown[atomicAdd(&num_grown[odd], 1)] = tid;
+            run_max[tid] = 0;                        // for the next head
+            run_odd[tid] = 0;
         }
         __syncthreads();
-        auto write = [&](int i, int run, const uint4& w) {
-            const float s = run_scale[run] > 0.0f ? run_scale[run] : 1.0f;
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-            float2 v[4];
-            const uint32_t m2 = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu),
-                                         __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
-            const bool plain = max(m2 & 0xFFFFu, m2 >> 16) < 0x7F80u && s > 1e-30f && s < 1e30f;
-            const float2 y = make_float2(__frcp_rn(s), __frcp_rn(s)), neg = make_float2(-s, -s);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 a = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xFFFF0000u));
-                v[k] = plain ? div2_by_scale(a, neg, y) : make_float2(__fdiv_rn(a.x, s), __fdiv_rn(a.y, s));
+        if (tid == 0) num_grown[odd ^ 1] = 0;
+        auto write = [&](uint8_t* to, float s, float inv, const uint4& w) {
+            if (inv == 0.0f) {
+                *reinterpret_cast<uint2*>(to) = divide8<kE5M2>(w, s);
+                return;
             }
-            *reinterpret_cast<uint2*>(cache + row_address(slots[i]) + c * 8) =
-                make_uint2(pack4_fp8<kE5M2>(v[0].x, v[0].y, v[1].x, v[1].y),
-                           pack4_fp8<kE5M2>(v[2].x, v[2].y, v[3].x, v[3].y));
+            *reinterpret_cast<uint2*>(to) =
+                make_uint2(quotient4<kE5M2>(w.x, w.y, s, inv), quotient4<kE5M2>(w.z, w.w, s, inv));
         };
+        if (single) {                                // the run's rows follow one another in the cache
+            const int run = run_of[begin];
+            const float s = run_scale[run], inv = run_inv[run];
+            uint8_t* to = cache + row_address(slots[run]) + row_in_pass * D + c * 8;
 #pragma unroll
-        for (int k = 0; k < C::HELD; ++k) {
-            const int i = begin + k * C::RPP + row_in_pass, run = run_at(i);
-            if (run >= 0) write(i, run, x[k]);
+            for (int k = 0; k < C::HELD; ++k)
+                if (begin + k * C::RPP + row_in_pass < end) write(to + k * C::RPP * D, s, inv, x[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < C::HELD; ++k) {
+                const int i = begin + k * C::RPP + row_in_pass, run = run_at(i);
+                if (run >= 0) write(cache + row_address(slots[i]) + c * 8, run_scale[run], run_inv[run], x[k]);
+            }
         }
         for (int i = begin + kAppendHeld + row_in_pass; i < end; i += C::RPP)
-            if (run_of[i] >= 0) write(i, run_of[i], load(i));
+            if (run_of[i] >= 0)
+                write(cache + row_address(slots[i]) + c * 8, run_scale[run_of[i]], run_inv[run_of[i]], load(i));
         // blocks whose scale grew: their earlier rows, one warp a block
-        for (int k = warp; k < num_grown; k += C::THREADS / 32) {
+        for (int k = warp; k < num_grown[odd]; k += C::THREADS / 32) {
             const int run = grown[k];
             const int row = (int)(slots[run] & (block - 1));
             const float old = run_old[run], s = run_scale[run];
@@ -443,12 +508,6 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
                                            __fdiv_rn(b.x * old, s), __fdiv_rn(b.y * old, s));
             }
         }
-        if (z + gridDim.z < 2) {
-            __syncthreads();
-            if (tid < kAppendWindow) run_max[tid] = 0;
-            if (tid == 0) num_grown = 0;
-            __syncthreads();
-        }
     }
 }
 
@@ -457,8 +516,10 @@ static cudaError_t launch_append_fp8_d(const AppendParams& p, bool e5m2, cudaStr
 {
     const int block = 1 << p.log2_blk, tile = block < 64 ? 64 : block;
     const long long tiles = ((long long)p.T + tile - 1) / tile;
-    // K and V in CTAs of their own while there are few, else one after the other
-    const dim3 grid((unsigned)tiles, p.H, tiles * p.H <= 2 * p.sm_count ? 2 : 1);
+    // a head of K or V per CTA while there are few, else about twelve CTAs per SM, each with
+    // several of its tile's heads
+    const long long groups = (12LL * p.sm_count + tiles - 1) / tiles;
+    const dim3 grid((unsigned)tiles, groups < 2 * p.H ? (unsigned)groups : 2 * p.H);
     constexpr int threads = AppendCfg<D>::THREADS;
     if (e5m2) cache_append_fp8_kernel<D, true><<<grid, threads, 0, stream>>>(p);
     else cache_append_fp8_kernel<D, false><<<grid, threads, 0, stream>>>(p);
