@@ -151,12 +151,29 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n)
         const int ps = int_arg(a[5], "page_size"), T = int_arg(a[6], "num_tokens");
         if (T < 0) value_error("num_tokens must not be negative");
         const c10::cuda::CUDAGuard guard(dev);
-        const Tensor seq_out = output(a[7], {B}, at::kInt, dev, "seq_lens_out");
-        const Tensor count_out = output(a[8], {1}, at::kInt, dev, "free_count_out");
-        const Tensor cu = output(a[9], {B + 1}, at::kInt, dev, "cu_new");
-        const Tensor slots = output(a[10], {T}, at::kLong, dev, "slot_map");
-        const Tensor pos = output(a[11], {T}, at::kInt, dev, "positions");
-        const Tensor served = output(a[12], {B}, at::kInt, dev, "served");
+        // new outputs share one allocation, each from a 16-byte boundary on
+        auto room = [](int64_t bytes) { return (bytes + 15) / 16 * 16; };
+        Tensor whole;
+        int64_t used = 0;
+        auto out = [&](PyObject* given, int64_t count, at::ScalarType dtype, const char* name) {
+            if (given != Py_None) return exact(given, {count}, dtype, dev, name);
+            if (!whole.defined())
+                whole = at::empty({room(8 * T) + room(4 * T) + 2 * room(4 * B) + room(4 * B + 4) + 16},
+                                  at::TensorOptions().dtype(at::kByte).device(dev));
+            const int64_t size = (int64_t)c10::elementSize(dtype);
+            Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+                c10::Storage(whole.storage()), whole.key_set(), c10::scalarTypeToTypeMeta(dtype));
+            t.unsafeGetTensorImpl()->set_storage_offset(used / size);
+            t.unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(&count, 1));
+            used += room(count * size);
+            return t;
+        };
+        const Tensor seq_out = out(a[7], B, at::kInt, "seq_lens_out");
+        const Tensor count_out = out(a[8], 1, at::kInt, "free_count_out");
+        const Tensor cu = out(a[9], B + 1, at::kInt, "cu_new");
+        const Tensor slots = out(a[10], T, at::kLong, "slot_map");
+        const Tensor pos = out(a[11], T, at::kInt, "positions");
+        const Tensor served = out(a[12], B, at::kInt, "served");
         auto ints = [](const Tensor& t) { return static_cast<int*>(t.data_ptr()); };
         const attn_status_t st =
             f_plan(ints(new_lens), ints(seq_lens), ints(table), ints(pages), ints(count), ints(seq_out),

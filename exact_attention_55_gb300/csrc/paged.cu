@@ -38,9 +38,10 @@ namespace cg = cooperative_groups;
 // table entry another thread writes.
 constexpr int kPlanMaxThreads = 1024;
 
-__device__ __forceinline__ long long plan_block_scan(long long x, long long* warp_sum, long long* total)
+// Exclusive sum over the block's threads and the total; every thread calls it.  `sums` is a
+// scan's own, one per warp.
+__device__ __forceinline__ long long plan_block_scan(long long x, long long* sums, long long* total)
 {
-    // exclusive sum over the block's threads; every thread calls it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     long long inc = x;
 #pragma unroll
@@ -48,35 +49,39 @@ __device__ __forceinline__ long long plan_block_scan(long long x, long long* war
         const long long y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
     }
-    __syncthreads();   // the previous scan's warp sums have been read
-    if (lane == 31) warp_sum[warp] = inc;
+    if (lane == 31) sums[warp] = inc;
     __syncthreads();
-    long long before = 0, all = 0;
-    for (int w = 0; w < warps; ++w) {
-        const long long s = warp_sum[w];
-        if (w < warp) before += s;
-        all += s;
+    long long all = lane < warps ? sums[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all += y;
     }
-    *total = all;
-    return before + inc - x;
+    *total = __shfl_sync(0xffffffffu, all, 31);
+    const long long before = __shfl_sync(0xffffffffu, all, (warp + 31) & 31);
+    return (warp ? before : 0) + inc - x;
 }
 
-// The last index i in [0, n) with a[i] <= x, for a non-decreasing with a[0] <= x.
-__device__ __forceinline__ int last_not_above(const int* a, int n, int x)
+// For each x[k] the last index i in [0, n) with a[i] <= x[k], for a non-decreasing from
+// a[0] <= x[k] on; `top` is the largest power of two below n (0 for n = 1).
+template <int K>
+__device__ __forceinline__ void last_not_above(const int* a, int n, int top, const int (&x)[K], int (&at)[K])
 {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a[mid] <= x) lo = mid;
-        else hi = mid;
-    }
-    return lo;
+#pragma unroll
+    for (int k = 0; k < K; ++k) at[k] = 0;
+    for (int step = top; step > 0; step >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int next = at[k] + step;
+            if (next < n && a[next] <= x[k]) at[k] = next;
+        }
 }
 
 __global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanParams p)
 {
     extern __shared__ int sm_plan[];
-    __shared__ long long warp_sum[kPlanMaxThreads / 32];
+    __shared__ long long sums[2][kPlanMaxThreads / 32];
+    __shared__ int taken_s;
     int* start = sm_plan;               // first packed row of the request, at most num_tokens
     int* base = sm_plan + p.B;          // pages taken before it
     int* len = sm_plan + 2 * p.B;       // cached length, or its complement when not served
@@ -86,34 +91,32 @@ __global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanP
     const long long cap = (long long)p.max_pages << p.log2_ps;   // fits an int
     const int free = min(max(*p.free_count, 0), p.free_capacity);
     const int per = (p.B + nt - 1) / nt, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    if (tid == 0) taken_s = 0;
 
-    auto request = [&](int b, long long& n, int& L) {
-        n = max(p.new_lens[b], 0);
-        L = (int)min((long long)max(p.seq_lens[b], 0), cap);
-    };
-    long long n, tokens = 0, total, taken_all;
-    int L;
+    // the thread's own requests: their counts in start and lengths in len until they are replaced
+    long long tokens = 0, total, all;
     for (int b = b0; b < b1; ++b) {
-        request(b, n, L);
+        const int n = max(p.new_lens[b], 0);
+        start[b] = n;
+        len[b] = (int)min((long long)max(p.seq_lens[b], 0), cap);
         tokens += n;
     }
-    const long long first = plan_block_scan(tokens, warp_sum, &total);
-    auto pages_needed = [&](long long end, long long nn, int LL) -> long long {
-        if (LL + nn > cap || end > p.num_tokens) return -1;      // does not fit
-        return ((LL + nn + ps - 1) >> p.log2_ps) - ((LL + ps - 1) >> p.log2_ps);
+    const long long first = plan_block_scan(tokens, sums[0], &total);
+    auto pages_needed = [&](long long end, long long n, long long L) -> long long {
+        if (L + n > cap || end > p.num_tokens) return -1;        // does not fit
+        return ((L + n + ps - 1) >> p.log2_ps) - ((L + ps - 1) >> p.log2_ps);
     };
     long long need_sum = 0, end = first;
     for (int b = b0; b < b1; ++b) {
-        request(b, n, L);
-        end += n;
-        const long long need = pages_needed(end, n, L);
+        end += start[b];
+        const long long need = pages_needed(end, start[b], len[b]);
         need_sum += need > 0 ? need : 0;
     }
-    const long long need_first = plan_block_scan(need_sum, warp_sum, &taken_all);
-    long long at = need_first, granted = 0;
+    long long at = plan_block_scan(need_sum, sums[1], &all);
+    int taken = 0;
     end = first;
     for (int b = b0; b < b1; ++b) {
-        request(b, n, L);
+        const int n = start[b], L = len[b];
         start[b] = (int)min(end, (long long)p.num_tokens);
         end += n;
         const long long need = pages_needed(end, n, L);
@@ -122,16 +125,44 @@ __global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanP
         len[b] = ok ? L : ~L;
         if (need > 0) {
             at += need;
-            if (ok) granted += need;
+            if (ok) taken = (int)at;              // the pages served are the first ones
         }
     }
-    long long taken;
-    plan_block_scan(granted, warp_sum, &taken);   // also: every thread's entries are written
+    taken = (int)__reduce_max_sync(0xffffffffu, (unsigned)taken);
+    if ((tid & 31) == 0 && taken > 0) atomicMax(&taken_s, taken);
     __syncthreads();
     cluster.sync();                               // every CTA has read the lengths
+    taken = taken_s;
 
     const int rank = (int)cluster.block_rank() * nt + tid, threads = (int)cluster.num_blocks() * nt;
     const int rows = (int)min(total, (long long)p.num_tokens);   // packed rows in use
+    const int top = p.B > 1 ? 1 << (31 - __clz(p.B - 1)) : 0;
+    constexpr int K = 4;                          // tokens a thread looks up together
+    for (long long t0 = rank; t0 < p.num_tokens; t0 += (long long)K * threads) {
+        int t[K], b[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) t[k] = (int)min(t0 + (long long)k * threads, 0x7fffffffLL);
+        last_not_above(start, p.B, top, t, b);
+        int pos[K], id[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int L = len[b[k]];
+            pos[k] = -1;
+            id[k] = -1;
+            if (t[k] < rows && L >= 0) {
+                pos[k] = L + t[k] - start[b[k]];
+                const int page = pos[k] >> p.log2_ps, old = (L + ps - 1) >> p.log2_ps;
+                id[k] = page < old ? p.page_table[(size_t)b[k] * p.max_pages + page]
+                                   : p.free_pages[free - 1 - (base[b[k]] + page - old)];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (t[k] < p.num_tokens) {
+                p.slot_map[t[k]] = id[k] < 0 ? -1 : ((long long)id[k] << p.log2_ps) + (pos[k] & (ps - 1));
+                p.positions[t[k]] = pos[k];
+            }
+    }
     for (int b = rank; b < p.B; b += threads) {
         const int next = b + 1 < p.B ? start[b + 1] : rows;
         const bool ok = len[b] >= 0;
@@ -140,36 +171,24 @@ __global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanP
         p.served[b] = ok ? 1 : 0;
         p.seq_lens_out[b] = ok ? len[b] + (next - start[b]) : ~len[b];
     }
-    if (rank == 0) *p.free_count_out = free - (int)taken;
-    for (int k = rank; k < (int)taken; k += threads) {
-        const int b = last_not_above(base, p.B, k);
-        const int page = ((len[b] + ps - 1) >> p.log2_ps) + k - base[b];
-        p.page_table[(size_t)b * p.max_pages + page] = p.free_pages[free - 1 - k];
-    }
-    for (int t = rank; t < p.num_tokens; t += threads) {
-        long long slot = -1;
-        int pos = -1;
-        if (t < rows) {
-            const int b = last_not_above(start, p.B, t);
-            if (len[b] >= 0) {
-                pos = len[b] + t - start[b];
-                const int page = pos >> p.log2_ps, old = (len[b] + ps - 1) >> p.log2_ps;
-                const int id = page < old ? p.page_table[(size_t)b * p.max_pages + page]
-                                          : p.free_pages[free - 1 - (base[b] + page - old)];
-                slot = id < 0 ? -1 : ((long long)id << p.log2_ps) + (pos & (ps - 1));
-            }
-        }
-        p.slot_map[t] = slot;
-        p.positions[t] = pos;
+    if (rank == 0) *p.free_count_out = free - taken;
+    for (int k = rank; k < taken; k += threads) {
+        const int x[1] = {k};
+        int b[1];
+        last_not_above(base, p.B, top, x, b);
+        const int page = ((len[b[0]] + ps - 1) >> p.log2_ps) + k - base[b[0]];
+        p.page_table[(size_t)b[0] * p.max_pages + page] = p.free_pages[free - 1 - k];
     }
 }
 
 cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream)
 {
     const int smem = 3 * p.B * (int)sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         200 * 1024);
-    if (e != cudaSuccess) return e;
+    if (smem > 47 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   200 * 1024);
+        if (e != cudaSuccess) return e;
+    }
     const int items = p.num_tokens > p.B ? p.num_tokens : p.B;
     int ctas = (items + 4095) / 4096;
     ctas = ctas >= 8 ? 8 : ctas >= 4 ? 4 : ctas >= 2 ? 2 : 1;
@@ -421,16 +440,28 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
             if (run >= 0 && c == 0) atomicMax(&run_max[run], a << 16);
         };
         uint4 x[C::HELD];
+        auto load_rows = [&](int from) {             // 128 rows, their loads in flight together
 #pragma unroll
-        for (int k = 0; k < C::HELD; ++k) {
-            const int i = begin + k * C::RPP + row_in_pass;
-            x[k] = make_uint4(0, 0, 0, 0);
-            if (run_at(i) >= 0) x[k] = load(i);
-        }
+            for (int k = 0; k < C::HELD; ++k) {
+                const int i = from + k * C::RPP;
+                x[k] = make_uint4(0, 0, 0, 0);
+                if (run_at(i) >= 0) x[k] = load(i);
+            }
+        };
+        const int row0 = begin + row_in_pass;
         if (single) {
-            uint32_t a = 0;
+            const __nv_bfloat16* from = src + (t0 + row0) * stride;
+            const long long step = C::RPP * stride;
 #pragma unroll
-            for (int k = 0; k < C::HELD; ++k) a = max(a, largest(x[k]));
+            for (int k = 0; k < C::HELD; ++k) {
+                x[k] = make_uint4(0, 0, 0, 0);
+                if (row0 + k * C::RPP < end) x[k] = __ldcs(reinterpret_cast<const uint4*>(from + k * step));
+            }
+            uint32_t m2 = 0;
+#pragma unroll
+            for (int k = 0; k < C::HELD; ++k)
+                m2 = max_abs_bf16x2(m2, max_abs_bf16x2(max_abs_bf16x2(x[k].x, x[k].y), max_abs_bf16x2(x[k].z, x[k].w)));
+            uint32_t a = max(m2 & 0x7FFFu, (m2 >> 16) & 0x7FFFu);
             if (a >= 0x7F80u) {
                 a = 0;
 #pragma unroll
@@ -440,13 +471,10 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
             a = __reduce_max_sync(0xffffffffu, a);
             if (lane == 0) atomicMax(&run_max[run_of[begin]], a << 16);
         } else {
+            for (int from = row0; from - row_in_pass < end; from += kAppendHeld) {
+                load_rows(from);
 #pragma unroll
-            for (int k = 0; k < C::HELD; ++k) join(run_at(begin + k * C::RPP + row_in_pass), x[k]);
-            for (int i0 = begin + kAppendHeld; i0 < end; i0 += C::RPP) {
-                const int i = i0 + row_in_pass, run = run_at(i);
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (run >= 0) w = load(i);
-                join(run, w);
+                for (int k = 0; k < C::HELD; ++k) join(run_at(from + k * C::RPP), x[k]);
             }
         }
         __syncthreads();
@@ -484,17 +512,18 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
             uint8_t* to = cache + row_address(slots[run]) + row_in_pass * D + c * 8;
 #pragma unroll
             for (int k = 0; k < C::HELD; ++k)
-                if (begin + k * C::RPP + row_in_pass < end) write(to + k * C::RPP * D, s, inv, x[k]);
+                if (row0 + k * C::RPP < end) write(to + k * C::RPP * D, s, inv, x[k]);
         } else {
+            const int held = (end - begin - 1) / kAppendHeld * kAppendHeld;   // the rows loaded last
+            for (int from = held; from >= 0; from -= kAppendHeld) {
+                if (from != held) load_rows(row0 + from);
 #pragma unroll
-            for (int k = 0; k < C::HELD; ++k) {
-                const int i = begin + k * C::RPP + row_in_pass, run = run_at(i);
-                if (run >= 0) write(cache + row_address(slots[i]) + c * 8, run_scale[run], run_inv[run], x[k]);
+                for (int k = 0; k < C::HELD; ++k) {
+                    const int i = row0 + from + k * C::RPP, run = run_at(i);
+                    if (run >= 0) write(cache + row_address(slots[i]) + c * 8, run_scale[run], run_inv[run], x[k]);
+                }
             }
         }
-        for (int i = begin + kAppendHeld + row_in_pass; i < end; i += C::RPP)
-            if (run_of[i] >= 0)
-                write(cache + row_address(slots[i]) + c * 8, run_scale[run_of[i]], run_inv[run_of[i]], load(i));
         // blocks whose scale grew: their earlier rows, one warp a block
         for (int k = warp; k < num_grown[odd]; k += C::THREADS / 32) {
             const int run = grown[k];
@@ -516,9 +545,10 @@ static cudaError_t launch_append_fp8_d(const AppendParams& p, bool e5m2, cudaStr
 {
     const int block = 1 << p.log2_blk, tile = block < 64 ? 64 : block;
     const long long tiles = ((long long)p.T + tile - 1) / tile;
-    // a head of K or V per CTA while there are few, else about twelve CTAs per SM, each with
-    // several of its tile's heads
-    const long long groups = (12LL * p.sm_count + tiles - 1) / tiles;
+    // a head of K or V per CTA while there are few, else about 36 CTAs per SM, each with
+    // several of its tile's heads (31850 tokens of 16 heads, d 128: 8 per SM 103.0 us, 12 90.6,
+    // 24 78.1, 36 73.2, 60 76.5)
+    const long long groups = (36LL * p.sm_count + tiles - 1) / tiles;
     const dim3 grid((unsigned)tiles, groups < 2 * p.H ? (unsigned)groups : 2 * p.H);
     constexpr int threads = AppendCfg<D>::THREADS;
     if (e5m2) cache_append_fp8_kernel<D, true><<<grid, threads, 0, stream>>>(p);
