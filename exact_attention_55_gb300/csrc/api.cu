@@ -30,6 +30,7 @@ cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append_fp8(const AppendParams& p, bool e5m2, cudaStream_t stream);
 int decode_fp8_row_tiles(int rows, int d);
+int decode_fp8_ctas_per_sm(int rows, int d);
 cudaError_t launch_decode_fp8(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeFp8Params& p,
                               int d, bool e5m2, cudaStream_t stream);
 cudaError_t launch_bwd(const BwdMaps& m, const BwdParams& p, int d, int sm_count, cudaStream_t stream);
@@ -1035,7 +1036,8 @@ static void decode_fp8_grid(int rows, int d, int sm_count, int* ranges, int* row
 {
     const int per = 8 * decode_fp8_row_tiles(rows, d);
     *row_groups = (rows + per - 1) / per;
-    *ranges = 2 * sm_count / *row_groups > 1 ? 2 * sm_count / *row_groups : 1;
+    const int ctas = decode_fp8_ctas_per_sm(rows, d) * sm_count;
+    *ranges = ctas / *row_groups > 1 ? ctas / *row_groups : 1;
 }
 
 static size_t decode_fp8_ws_bytes(int rows, int d, int ranges, int row_groups)

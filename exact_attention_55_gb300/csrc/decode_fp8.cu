@@ -68,7 +68,8 @@ struct Dec8Cfg {
     static constexpr int Q_FRAGS = NT * (D / 16) * 32;    // 8 bytes each, two heads' worth
     static constexpr int PAD = 4;
     static constexpr int MERGE = kD8Warps * 8 * (D + PAD) * 4;
-    static constexpr int CAP = 112 * 1024;                // two CTAs per SM
+    static constexpr int CTAS = NT == 1 && D <= 128 ? 3 : 2;   // per SM
+    static constexpr int CAP = (CTAS == 3 ? 74 : 112) * 1024;
     static constexpr int FIXED = 1024 + 2 * Q_FRAGS * 8 + MERGE + 2048;   // 1024: alignment
     static constexpr int FIT = (CAP - FIXED) / STAGE;
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
@@ -241,7 +242,7 @@ __device__ __forceinline__ void dec8_timeout(const DecodeFp8Params& p, int* abor
 }
 
 template <int D, bool kE5M2, int NT>
-__global__ void __launch_bounds__(kD8Threads, 2)
+__global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const DecodeFp8Params p)
 {
@@ -273,6 +274,11 @@ __global__ void __launch_bounds__(kD8Threads, 2)
         mbar_init(smem_u32(&sh->meet), kD8Warps);
         sh->abort_flag = 0;
         fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // what ran before has written its results
+    if (threadIdx.x == 0) {
         if (!per_unit) todo[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
     const int x = blockIdx.x / p.row_groups, rg = blockIdx.x - x * p.row_groups, row0 = rg * C::ROWS;
@@ -325,10 +331,6 @@ __global__ void __launch_bounds__(kD8Threads, 2)
 
     if (warp == kD8Warps) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            tma_prefetch_desc(&tmK);
-            tma_prefetch_desc(&tmV);
-        }
         const uint64_t pol = l2_policy_evict_first();
         const int g = lane >> 2, t = lane & 3;
         const int log2_r = p.log2_ps < 6 ? p.log2_ps : 6;       // rows per TMA box: a page, or 64
@@ -795,11 +797,26 @@ __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(c
     if (x1 - x0 < 4) {
         for (int i = blockIdx.y * kD8CombineThreads + tid; i < rows * (D / 4); i += gridDim.y * kD8CombineThreads) {
             const int r = i / (D / 4), col = i - r * (D / 4);
-            float M = NEG_INF, l = 0.0f;
-            for (int x = x0; x <= x1; ++x) M = fmaxf(M, part_of(x)[C::ROWS * D + r]);
-            const float mb = M == NEG_INF ? 0.0f : M;
+            float m[4], sum[4];
+            float4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float* w = part_of(min(x0 + k, x1));
+                m[k] = x0 + k <= x1 ? w[C::ROWS * D + r] : NEG_INF;
+                sum[k] = w[C::ROWS * D + C::ROWS + r];
+                v[k] = *reinterpret_cast<const float4*>(w + r * D + col * 4);
+            }
+            const float M = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), mb = M == NEG_INF ? 0.0f : M;
             float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int x = x0; x <= x1; ++x) add(x, r, col, mb, a, l);
+            float l = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (x0 + k > x1) break;
+                const float fac = ex2(m[k] - mb);
+                l = fmaf(fac, sum[k], l);
+                a.x = fmaf(fac, v[k].x, a.x), a.y = fmaf(fac, v[k].y, a.y);
+                a.z = fmaf(fac, v[k].z, a.z), a.w = fmaf(fac, v[k].w, a.w);
+            }
             finish(r, col, a, l, mb);
         }
         return;
@@ -842,6 +859,7 @@ __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(c
 // Query rows of a CTA, in eights.  More rows under one key head go to more CTAs, which read
 // the same tiles at the same time (the second read comes from L2).
 int decode_fp8_row_tiles(int rows, int d) { return rows <= 8 || d == 256 ? 1 : 2; }
+int decode_fp8_ctas_per_sm(int rows, int d) { return rows <= 8 && d <= 128 ? 3 : 2; }
 
 template <int D, bool kE5M2, int NT>
 static cudaError_t launch_decode_fp8_n(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeFp8Params& p,
@@ -851,22 +869,25 @@ static cudaError_t launch_decode_fp8_n(const CUtensorMap& mk, const CUtensorMap&
     auto kernel = decode_fp8_kernel<D, kE5M2, NT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    kernel<<<p.ranges * p.row_groups, kD8Threads, C::SMEM, stream>>>(mk, mv, p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3(p.ranges * p.row_groups);
+    cfg.blockDim = dim3(kD8Threads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
+    if (e != cudaSuccess) return e;
     // as many CTAs for a unit as it has parts on average, up to one for 64 columns of a row
     const long long units = (long long)p.B * p.Hkv * p.row_groups, ctas = p.ranges * p.row_groups;
     const int items = (p.rows < C::ROWS ? p.rows : C::ROWS) * (D / 64);
     const int share = units < ctas ? (int)(4 * ctas / units) : 2;
     cfg.gridDim = dim3((unsigned)(units < ctas ? units : ctas), share < items ? share : items);
     cfg.blockDim = dim3(kD8CombineThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, decode_fp8_combine_kernel<D, NT>, p);
 }
 
