@@ -43,6 +43,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_params.h"
 #include "paged_params.h"
@@ -760,15 +761,17 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
 // Joins the parts of a unit that several ranges shared: with M the largest part maximum,
 // O = sum_x 2^(M_x - M) a_x / sum_x 2^(M_x - M) l_x.  grid.x: the units, or where there are
 // more of them the ranges (each leaves at most one unit to its successors); grid.y shares
-// a unit's rows and columns.  Few parts (the usual batch): a thread joins one float4 of one
-// row.  Many (one long sequence): 64 columns of a row at a time, eight threads a float4.
+// a unit's rows and columns.  Latency-bound: a thread has all its parts' loads in flight
+// together.  Up to eight parts (the usual batch), a thread joins one float4 of one row;
+// more (one long sequence), 32 columns of a row at a time, sixteen threads a float4.
 template <int D, int NT>
 __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(const DecodeFp8Params p)
 {
     using C = Dec8Cfg<D, NT>;
-    constexpr int COLS = 16, GROUPS = kD8CombineThreads / COLS, SLICES = D / 64;
+    constexpr int FEW = 8, MANY = 10;                        // parts of a thread
+    constexpr int COLS = 8, GROUPS = kD8CombineThreads / COLS, SLICES = D / 32;
     __shared__ float4 sm_a[GROUPS][COLS];
-    __shared__ float sm_m[kD8CombineThreads / 32], sm_l[GROUPS];
+    __shared__ float2 sm_ml[GROUPS];
     const float NEG_INF = -__int_as_float(0x7f800000);
     const int tid = threadIdx.x, ctas = p.ranges * p.row_groups;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -780,77 +783,78 @@ __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(c
     auto part_of = [&](int x) {
         return p.ws + 4 * ctas + (size_t)(2 * (x * p.row_groups + rg) + (x == x0 ? 1 : 0)) * C::PART;
     };
-    auto finish = [&](int r, int col, float4 a, float sum, float mb) {
+    auto finish = [&](int r, int col, float4 a, float sum, float M) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (row0 + r) * D)[col] =
             make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-        if (col == 0) p.lse[row0 + r] = sum == 0.0f ? NEG_INF : (mb + __log2f(sum)) * 0.69314718055994531f;
+        if (col == 0)
+            p.lse[row0 + r] = sum == 0.0f ? NEG_INF : ((M == NEG_INF ? 0.0f : M) + __log2f(sum)) * 0.69314718055994531f;
     };
-    auto add = [&](int x, int r, int col, float mb, float4& a, float& l) {
-        const float* w = part_of(x);
-        const float fac = ex2(w[C::ROWS * D + r] - mb);
-        const float4 v = *reinterpret_cast<const float4*>(w + r * D + col * 4);
-        l = fmaf(fac, w[C::ROWS * D + C::ROWS + r], l);
-        a.x = fmaf(fac, v.x, a.x), a.y = fmaf(fac, v.y, a.y);
-        a.z = fmaf(fac, v.z, a.z), a.w = fmaf(fac, v.w, a.w);
+    // (M, l, a) += K parts x, x + step, ... up to x1, of row r
+    auto join = [&](auto K, int x, int step, int r, int col, float& M, float& l, float4& a) {
+        constexpr int k_parts = decltype(K)::value;
+        float m[k_parts], sum[k_parts];
+        float4 v[k_parts];
+#pragma unroll
+        for (int k = 0; k < k_parts; ++k) {
+            m[k] = NEG_INF;
+            if (x + k * step > x1) continue;
+            const float* w = part_of(x + k * step);
+            m[k] = w[C::ROWS * D + r];
+            sum[k] = w[C::ROWS * D + C::ROWS + r];
+            v[k] = *reinterpret_cast<const float4*>(w + r * D + col * 4);
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < k_parts; ++k) top = fmaxf(top, m[k]);
+        const float mb = top == NEG_INF ? 0.0f : top, f = ex2(M - mb);
+        M = top;
+        l *= f;
+        a.x *= f, a.y *= f, a.z *= f, a.w *= f;
+#pragma unroll
+        for (int k = 0; k < k_parts; ++k) {
+            if (x + k * step > x1) continue;
+            const float fac = ex2(m[k] - mb);
+            l = fmaf(fac, sum[k], l);
+            a.x = fmaf(fac, v[k].x, a.x), a.y = fmaf(fac, v[k].y, a.y);
+            a.z = fmaf(fac, v[k].z, a.z), a.w = fmaf(fac, v[k].w, a.w);
+        }
     };
-    if (x1 - x0 < 4) {
+    if (x1 - x0 < FEW) {
         for (int i = blockIdx.y * kD8CombineThreads + tid; i < rows * (D / 4); i += gridDim.y * kD8CombineThreads) {
             const int r = i / (D / 4), col = i - r * (D / 4);
-            float m[4], sum[4];
-            float4 v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float* w = part_of(min(x0 + k, x1));
-                m[k] = x0 + k <= x1 ? w[C::ROWS * D + r] : NEG_INF;
-                sum[k] = w[C::ROWS * D + C::ROWS + r];
-                v[k] = *reinterpret_cast<const float4*>(w + r * D + col * 4);
-            }
-            const float M = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), mb = M == NEG_INF ? 0.0f : M;
+            float M = NEG_INF, l = 0.0f;
             float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float l = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (x0 + k > x1) break;
-                const float fac = ex2(m[k] - mb);
-                l = fmaf(fac, sum[k], l);
-                a.x = fmaf(fac, v[k].x, a.x), a.y = fmaf(fac, v[k].y, a.y);
-                a.z = fmaf(fac, v[k].z, a.z), a.w = fmaf(fac, v[k].w, a.w);
-            }
-            finish(r, col, a, l, mb);
+            join(std::integral_constant<int, FEW>{}, x0, 1, r, col, M, l, a);
+            finish(r, col, a, l, M);
         }
         return;
     }
     const int grp = tid / COLS;
     for (int i = blockIdx.y; i < rows * SLICES; i += gridDim.y) {
         const int r = i / SLICES, col = (i - r * SLICES) * COLS + tid % COLS;
-        float M = NEG_INF;
-        for (int x = x0 + tid; x <= x1; x += kD8CombineThreads) M = fmaxf(M, part_of(x)[C::ROWS * D + r]);
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-        if ((tid & 31) == 0) sm_m[tid >> 5] = M;
-        __syncthreads();
-        M = sm_m[0];
-#pragma unroll
-        for (int w = 1; w < kD8CombineThreads / 32; ++w) M = fmaxf(M, sm_m[w]);
-        const float mb = M == NEG_INF ? 0.0f : M;
+        float M = NEG_INF, l = 0.0f;
         float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float l = 0.0f;
-#pragma unroll 8
-        for (int x = x0 + grp; x <= x1; x += GROUPS) add(x, r, col, mb, a, l);
+        for (int x = x0 + grp; x <= x1; x += GROUPS * MANY)
+            join(std::integral_constant<int, MANY>{}, x, GROUPS, r, col, M, l, a);
         sm_a[grp][tid % COLS] = a;
-        if (tid % COLS == 0) sm_l[grp] = l;
+        if (tid % COLS == 0) sm_ml[grp] = make_float2(M, l);
         __syncthreads();
         if (tid < COLS) {
-            float sum = 0.0f;
+            float top = NEG_INF, sum = 0.0f;
             a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < GROUPS; ++k) top = fmaxf(top, sm_ml[k].x);
+            const float mb = top == NEG_INF ? 0.0f : top;
 #pragma unroll
             for (int k = 0; k < GROUPS; ++k) {
                 const float4 v = sm_a[k][tid];
-                a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-                sum += sm_l[k];
+                const float fac = ex2(sm_ml[k].x - mb);
+                sum = fmaf(fac, sm_ml[k].y, sum);
+                a.x = fmaf(fac, v.x, a.x), a.y = fmaf(fac, v.y, a.y);
+                a.z = fmaf(fac, v.z, a.z), a.w = fmaf(fac, v.w, a.w);
             }
-            finish(r, col, a, sum, mb);
+            finish(r, col, a, sum, top);
         }
         __syncthreads();
     }
@@ -881,11 +885,14 @@ static cudaError_t launch_decode_fp8_n(const CUtensorMap& mk, const CUtensorMap&
     cfg.dynamicSmemBytes = C::SMEM;
     e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
     if (e != cudaSuccess) return e;
-    // as many CTAs for a unit as it has parts on average, up to one for 64 columns of a row
+    // a unit's float4s over its CTAs, and four CTAs a part of the average unit while that is
+    // more, up to one for 32 columns of a row
     const long long units = (long long)p.B * p.Hkv * p.row_groups, ctas = p.ranges * p.row_groups;
-    const int items = (p.rows < C::ROWS ? p.rows : C::ROWS) * (D / 64);
-    const int share = units < ctas ? (int)(4 * ctas / units) : 2;
-    cfg.gridDim = dim3((unsigned)(units < ctas ? units : ctas), share < items ? share : items);
+    const int rows = p.rows < C::ROWS ? p.rows : C::ROWS, items = rows * (D / 32);
+    const int least = (rows * (D / 4) + kD8CombineThreads - 1) / kD8CombineThreads;
+    int share = units < ctas ? (int)(4 * ctas / units) : least;
+    share = share > items ? items : share < least ? least : share;
+    cfg.gridDim = dim3((unsigned)(units < ctas ? units : ctas), share);
     cfg.blockDim = dim3(kD8CombineThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, decode_fp8_combine_kernel<D, NT>, p);
