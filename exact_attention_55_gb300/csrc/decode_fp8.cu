@@ -67,16 +67,15 @@ struct Dec8Cfg {
     static constexpr int STAGE = 2 * HALF;
     static constexpr bool Q_REGS = NT * D <= 128;         // query fragments held in registers
     static constexpr int Q_FRAGS = NT * (D / 16) * 32;    // 8 bytes each, two heads' worth
-    static constexpr int PAD = 4;
-    static constexpr int MERGE = kD8Warps * 8 * (D + PAD) * 4;
     static constexpr int CTAS = NT == 1 && D <= 128 ? 3 : 2;   // per SM
     static constexpr int CAP = (CTAS == 3 ? 74 : 112) * 1024;
-    static constexpr int FIXED = 1024 + 2 * Q_FRAGS * 8 + MERGE + 2048;   // 1024: alignment
+    static constexpr int FIXED = 1024 + 2 * Q_FRAGS * 8 + 2048;   // 1024: alignment
     static constexpr int FIT = (CAP - FIXED) / STAGE;
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
     static constexpr int PART = ROWS * (D + 2);           // floats of a part: O, maxima, sums
     static_assert(STAGES >= 2, "ring");
+    static_assert(STAGE == kD8Warps * 8 * D * 4, "a head's last stage holds the warps' O for joining");
 };
 
 template <int D, int NT>
@@ -251,8 +250,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint2* qs = reinterpret_cast<uint2*>(smem + C::STAGES * C::STAGE);       // [2][Q_FRAGS]
-    float* merge = reinterpret_cast<float*>(qs + 2 * C::Q_FRAGS);
-    auto* sh = reinterpret_cast<Dec8Shared<D, NT>*>(merge + C::MERGE / 4);
+    auto* sh = reinterpret_cast<Dec8Shared<D, NT>*>(qs + 2 * C::Q_FRAGS);
     static_assert(sizeof(Dec8Shared<D, NT>) <= 2048, "shared memory");
     const volatile int* abort_flag = &sh->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -446,7 +444,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
         const int g = lane >> 2, t = lane & 3;
         int stage = 0, q_slot = 0;
         uint32_t parity = 0, q_parity = 0, meet_parity = 0;
-        bool ok = true, merged = false;
+        bool ok = true;
         auto wait_all = [&](uint64_t* bar, uint32_t par) {
             const bool r = mbar_wait(smem_u32(bar), par, abort_flag, p.timeout_ns);
             ok = __all_sync(0xffffffffu, r);
@@ -674,6 +672,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                         }
                     }
                 }
+                if (k == k1 - 1) break;                          // the last stage is kept for the joining
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh->empty[stage]));
                 if (++stage == C::STAGES) {
@@ -690,21 +689,23 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                 q_parity ^= 1;
             }
 
-            // ---- join the four warps, eight rows at a time
+            // ---- join the four warps, eight rows at a time, in the last tile's stage: warp w's
+            // row r, float4 c at ((w * 8 + r) * D / 4 + (c ^ (r / 2 & 3))), which keeps the
+            // writes below to two lanes a bank
             const bool whole = k1 - k0 == seq.n;
             float* part = p.ws + 4 * gridDim.x + (size_t)(2 * blockIdx.x + (k0 == 0 ? 1 : 0)) * C::PART;
+            float4* area = reinterpret_cast<float4*>(smem + stage * C::STAGE);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                if (merged && !meet()) break;                    // the areas have been read
-                merged = true;
+                if (!meet()) break;                              // the tile, or the rows before, have been read
                 // value d of acc[..][i][h]: group g holds CB/8 consecutive ones of a column box
                 constexpr int VT = C::CB / 16;                   // products per column box
-                float* area = merge + warp * 8 * (D + C::PAD) + g * (C::CB / 8);
 #pragma unroll
                 for (int i = 0; i < D / 16; i += 2)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<float4*>(area + (2 * t + h) * (D + C::PAD) + (i / VT) * C::CB + (i % VT) * 2) =
+                        area[(warp * 8 + 2 * t + h) * (D / 4) +
+                             (((i / VT) * (C::CB / 4) + g * (C::CB / 32) + (i % VT) / 2) ^ t)] =
                             make_float4(acc[nt][i][h], acc[nt][i][h + 2], acc[nt][i + 1][h], acc[nt][i + 1][h + 2]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
 #pragma unroll
                     for (int w = 0; w < kD8Warps; ++w) {
                         const float fac = ex2(sh->m[w][r] - mb);     // ex2(-inf) = 0
-                        const float4 u = *reinterpret_cast<const float4*>(merge + (w * 8 + r8) * (D + C::PAD) + d4 * 4);
+                        const float4 u = area[(w * 8 + r8) * (D / 4) + (d4 ^ (r8 >> 1))];
                         sum = fmaf(sh->l[w][r], fac, sum);
                         v.x = fmaf(u.x, fac, v.x), v.y = fmaf(u.y, fac, v.y);
                         v.z = fmaf(u.z, fac, v.z), v.w = fmaf(u.w, fac, v.w);
@@ -747,6 +748,13 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                 }
             }
             if (!ok) break;
+            fence_proxy_async_smem();                            // TMA writes the stage next
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh->empty[stage]));
+            if (++stage == C::STAGES) {
+                stage = 0;
+                parity ^= 1;
+            }
             if (k0 == 0 && threadIdx.x == 0 && (per_unit || !whole))   // the unit's first part names the last
                 todo[per_unit ? (b * p.Hkv + hk) * p.row_groups + rg : blockIdx.x] =
                     whole ? make_int4(-1, 0, 0, 0)
