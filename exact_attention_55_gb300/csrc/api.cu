@@ -911,6 +911,7 @@ extern "C" attn_status_t attn_bwd_bf16(const void* q, const void* k, const void*
 // ------------------------------------------------------------------ paged 8-bit cache
 namespace {
 
+constexpr int kDecodeWholeKeys = 512;
 constexpr int kPlanMaxRequests = 16384;   // three ints of shared memory per request
 
 bool page_size_ok(int page_size, int least)
@@ -1118,6 +1119,8 @@ extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cach
     p.window = window > 0 ? window : 0;
     p.c_log2 = (float)((double)scale * 1.4426950408889634);
     p.ws = static_cast<float*>(workspace);
+    // a table of at most kDecodeWholeKeys keys: a head is one CTA's, and no kernel joins parts
+    p.whole = (long long)max_pages * page_size <= kDecodeWholeKeys ? 1 : 0;
     p.ranges = ranges;
     p.row_groups = row_groups;
     p.status = dev->status;

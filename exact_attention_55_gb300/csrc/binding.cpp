@@ -9,8 +9,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -71,17 +71,30 @@ const Tensor& exact(PyObject* o, std::initializer_list<int64_t> shape, at::Scala
 Tensor output(PyObject* o, std::initializer_list<int64_t> shape, at::ScalarType dtype, at::Device dev, const char* name)
 {
     if (o != Py_None) return exact(o, shape, dtype, dev, name);
-    return at::empty(at::IntArrayRef(shape), at::TensorOptions().dtype(dtype).device(dev));
+    return at::detail::empty_cuda(at::IntArrayRef(shape), dtype, dev, c10::nullopt);
 }
 
-// The stream of a call: its handle, or None for the device's current one.
-void* stream_of(PyObject* o, at::Device dev)
-{
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-    void* s = PyLong_AsVoidPtr(o);
-    if (PyErr_Occurred()) throw Refusal{nullptr, ""};
-    return s;
-}
+// Makes a call's device and stream current while it allocates and launches: the given
+// stream's handle, or None for the device's current one.  What a call allocates (outputs,
+// a workspace that goes back when it returns) belongs to the stream it runs on, so nobody
+// on another stream can be given that memory while the call's kernels are in flight.
+struct On {
+    c10::cuda::OptionalCUDAGuard device;
+    c10::cuda::OptionalCUDAStreamGuard stream;
+    void* handle;
+
+    On(PyObject* given, at::Device dev)
+    {
+        if (given == Py_None) {
+            device.set_device(dev);
+            handle = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+            return;
+        }
+        handle = PyLong_AsVoidPtr(given);
+        if (PyErr_Occurred()) throw Refusal{nullptr, ""};
+        stream.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), dev.index()));
+    }
+};
 
 int int_arg(PyObject* o, const char* name)
 {
@@ -150,7 +163,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Tensor& count = exact(a[4], {1}, at::kInt, dev, "free_count");
         const int ps = int_arg(a[5], "page_size"), T = int_arg(a[6], "num_tokens");
         if (T < 0) value_error("num_tokens must not be negative");
-        const c10::cuda::CUDAGuard guard(dev);
+        const On on(a[13], dev);
         // new outputs share one allocation, each from a 16-byte boundary on
         auto room = [](int64_t bytes) { return (bytes + 15) / 16 * 16; };
         Tensor whole;
@@ -158,8 +171,8 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n)
         auto out = [&](PyObject* given, int64_t count, at::ScalarType dtype, const char* name) {
             if (given != Py_None) return exact(given, {count}, dtype, dev, name);
             if (!whole.defined())
-                whole = at::empty({room(8 * T) + room(4 * T) + 2 * room(4 * B) + room(4 * B + 4) + 16},
-                                  at::TensorOptions().dtype(at::kByte).device(dev));
+                whole = at::detail::empty_cuda({room(8 * T) + room(4 * T) + 2 * room(4 * B) + room(4 * B + 4) + 16},
+                                               at::kByte, dev, c10::nullopt);
             const int64_t size = (int64_t)c10::elementSize(dtype);
             Tensor t = at::detail::make_tensor<c10::TensorImpl>(
                 c10::Storage(whole.storage()), whole.key_set(), c10::scalarTypeToTypeMeta(dtype));
@@ -179,7 +192,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n)
             f_plan(ints(new_lens), ints(seq_lens), ints(table), ints(pages), ints(count), ints(seq_out),
                    ints(count_out), ints(cu), static_cast<long long*>(slots.data_ptr()), ints(pos), ints(served),
                    size_arg(B, "B"), ps, size_arg(width, "max_pages"), size_arg(pages.numel(), "free_pages"), T,
-                   stream_of(a[13], dev));
+                   on.handle);
         if (st != ATTN_OK) return status(st);
         return tuple_of({seq_out, count_out, cu, slots, pos, served});
     });
@@ -237,9 +250,9 @@ PyObject* append_bf16(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded(n, 6, [&]() -> PyObject* {
         const Append p = append_args(a, a[4], false);
-        const c10::cuda::CUDAGuard guard(p.dev);
+        const On on(a[5], p.dev);
         return status(f_append_bf16(ptr(a[0]), ptr(a[1]), ptr(a[2]), ptr(a[3]), static_cast<long long*>(ptr(a[4])),
-                                    p.T, p.H, p.d, p.k_stride, p.v_stride, p.ps, p.pages, stream_of(a[5], p.dev)));
+                                    p.T, p.H, p.d, p.k_stride, p.v_stride, p.ps, p.pages, on.handle));
     });
 }
 
@@ -268,10 +281,10 @@ PyObject* append_fp8(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Append p = append_args(a, a[6], true);
         const int format = int_arg(a[7], "format");
         const int block = block_of(a[2], a[3], a[4], a[5], format, p.dev);
-        const c10::cuda::CUDAGuard guard(p.dev);
+        const On on(a[8], p.dev);
         return status(f_append_fp8(ptr(a[0]), ptr(a[1]), ptr(a[2]), ptr(a[3]), static_cast<float*>(ptr(a[4])),
                                    static_cast<float*>(ptr(a[5])), static_cast<long long*>(ptr(a[6])), p.T, p.H, p.d,
-                                   p.k_stride, p.v_stride, p.ps, p.pages, block, format, stream_of(a[8], p.dev)));
+                                   p.k_stride, p.v_stride, p.ps, p.pages, block, format, on.handle));
     });
 }
 
@@ -304,15 +317,21 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n)
         }
         const int window = int_arg(a[9], "window");
         const int h = size_arg(H, "H"), hkv = size_arg(kc.size(1), "Hkv"), nqi = size_arg(nq, "nq"), di = size_arg(d, "d");
-        const c10::cuda::CUDAGuard guard(dev);
-        Tensor ws;
+        const On on(a[13], dev);
+        // without a workspace of the caller's: the stream's allocator lends one for the call
+        c10::DataPtr lent;
+        void* ws = nullptr;
+        size_t ws_bytes = 0;
         if (a[10] == Py_None) {
-            const int64_t bytes = (int64_t)f_decode_ws(h, hkv, nqi, di);
-            ws = at::empty({bytes > 16 ? bytes : 16}, at::TensorOptions().dtype(at::kByte).device(dev));
+            ws_bytes = f_decode_ws(h, hkv, nqi, di);
+            lent = c10::cuda::CUDACachingAllocator::get()->allocate(ws_bytes);
+            ws = lent.get();
         } else {
-            ws = tensor(a[10], "workspace");
-            if (ws.device() != dev || !ws.is_contiguous())
+            const Tensor& given = tensor(a[10], "workspace");
+            if (given.device() != dev || !given.is_contiguous())
                 type_error("workspace must be a contiguous CUDA tensor on " + dev.str());
+            ws = given.data_ptr();
+            ws_bytes = (size_t)given.nbytes();
         }
         const Tensor o = output(a[11], {B, H, nq, d}, at::kBFloat16, dev, "o");
         const Tensor lse = output(a[12], {B, H, nq}, at::kFloat, dev, "lse");
@@ -321,7 +340,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n)
             static_cast<int*>(table.data_ptr()), static_cast<int*>(lens.data_ptr()), o.data_ptr(),
             static_cast<float*>(lse.data_ptr()), size_arg(B, "B"), h, hkv, nqi, di, size_arg(kc.size(2), "page_size"),
             size_arg(kc.size(0), "num_pages"), size_arg(table.size(1), "max_pages"), block, format, scale, window,
-            ws.data_ptr(), (size_t)ws.nbytes(), stream_of(a[13], dev));
+            ws, ws_bytes, on.handle);
         if (st != ATTN_OK) return status(st);
         return tuple_of({o, lse});
     });

@@ -125,6 +125,9 @@ struct Dec8Line {
     __device__ __forceinline__ int owner(long long at) const { return (int)(((at + 1) * X - 1) / cost); }
 };
 
+// What a sequence's units cover of the line: their tiles, or 1 where units are not split.
+__device__ __forceinline__ int dec8_span(const DecodeFp8Params& p, int n) { return p.whole ? min(n, 1) : n; }
+
 // Finds the sequence that range x starts in (its number and the cost before it).  All
 // threads of the main kernel call it.
 template <class Shared>
@@ -135,7 +138,7 @@ __device__ __forceinline__ Dec8Line dec8_line(const DecodeFp8Params& p, Shared* 
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     long long mine = 0, seqs = 0;
     for (int b = b0; b < b1; ++b) {
-        const int n = dec8_seq(p, b).n;
+        const int n = dec8_span(p, dec8_seq(p, b).n);
         mine += n;
         seqs += n > 0;
     }
@@ -169,7 +172,7 @@ __device__ __forceinline__ Dec8Line dec8_line(const DecodeFp8Params& p, Shared* 
         long long s0 = (before + before_s * line.unit_cost) * p.Hkv;
         if (s0 <= at && at < s0 + (mine + seqs * line.unit_cost) * p.Hkv)
             for (int b = b0; b < b1; ++b) {
-                const int n = dec8_seq(p, b).n;
+                const int n = dec8_span(p, dec8_seq(p, b).n);
                 const long long len = n > 0 ? (long long)(n + line.unit_cost) * p.Hkv : 0;
                 if (s0 <= at && at < s0 + len) {
                     sh->b0 = b;
@@ -303,23 +306,25 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
     const long long a = line.cut(x), e = line.cut(x + 1);
     int b = sh->b0;
     Dec8Seq seq = dec8_seq(p, b);
-    int hk = (int)((a - sh->first) / (seq.n + line.unit_cost));
-    long long s0 = sh->first + (long long)hk * (seq.n + line.unit_cost);
+    int span = dec8_span(p, seq.n), hk = (int)((a - sh->first) / (span + line.unit_cost));
+    long long s0 = sh->first + (long long)hk * (span + line.unit_cost);
     // the unit's tiles of this range: [k0, k1)
     int k0 = 0, k1 = 0;
     auto take = [&]() {
         k0 = (int)max(0LL, a - s0 - line.unit_cost);
-        k1 = (int)max((long long)k0, min((long long)seq.n, e - s0 - line.unit_cost));
+        k1 = (int)max((long long)k0, min((long long)span, e - s0 - line.unit_cost));
+        if (p.whole && k1 > k0) k1 = seq.n;
     };
     // to the next unit with tiles of this range; false when there is none
     auto next_unit = [&]() -> bool {
         do {
-            s0 += seq.n + line.unit_cost;
+            s0 += span + line.unit_cost;
             if (s0 + line.unit_cost >= e) return false;
             if (++hk == p.Hkv) {
                 hk = 0;
                 do seq = dec8_seq(p, ++b);
                 while (seq.n == 0);
+                span = dec8_span(p, seq.n);
             }
             take();
         } while (k1 <= k0);
@@ -755,7 +760,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                 stage = 0;
                 parity ^= 1;
             }
-            if (k0 == 0 && threadIdx.x == 0 && (per_unit || !whole))   // the unit's first part names the last
+            if (k0 == 0 && threadIdx.x == 0 && !p.whole && (per_unit || !whole))   // the unit's first part names the last
                 todo[per_unit ? (b * p.Hkv + hk) * p.row_groups + rg : blockIdx.x] =
                     whole ? make_int4(-1, 0, 0, 0)
                           : make_int4(x, line.owner(s0 + line.unit_cost + seq.n - 1), rg, (int)unit_row);
@@ -893,6 +898,7 @@ static cudaError_t launch_decode_fp8_n(const CUtensorMap& mk, const CUtensorMap&
     cfg.dynamicSmemBytes = C::SMEM;
     e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
     if (e != cudaSuccess) return e;
+    if (p.whole) return cudaSuccess;
     // a unit's float4s over its CTAs, and four CTAs a part of the average unit while that is
     // more, up to one for 32 columns of a row
     const long long units = (long long)p.B * p.Hkv * p.row_groups, ctas = p.ranges * p.row_groups;

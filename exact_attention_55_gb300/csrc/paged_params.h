@@ -56,6 +56,7 @@ struct DecodeFp8Params {
     int window;
     float c_log2;           // softmax scale * log2(e)
     float* ws;              // per CTA: int4 for the joining kernel; then two parts per CTA
+    int whole;              // 1: no unit is split over ranges (short tables), nothing to join
     int ranges;             // CTAs of one row group: at most this many ranges of tiles
     int row_groups;         // groups of query rows, each a CTA's share
     int* status;            // device status word (bounded waits)

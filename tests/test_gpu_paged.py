@@ -514,6 +514,28 @@ def test_calls_on_other_streams(fa):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_workspace_belongs_to_the_calls_stream(fa):
+    """Calls on a given stream without a workspace, while the current stream allocates and
+    overwrites blocks of the same sizes: nobody else gets a workspace that is in use."""
+    rng = np.random.default_rng(23)
+    lens, Hkv, d = [30000, 5], 2, 128
+    kc, vc, ks, vs, table = ref.make_cache(rng, lens, Hkv, d, 64, 64, "e4m3")
+    q = torch.randn(2, 8, 1, d, generator=torch.Generator().manual_seed(1)).bfloat16()
+    args = [q.cuda()] + [cuda(a) for a in (kc, vc, ks, vs, table, np.array(lens, np.int32))]
+    want = fa.attn_decode_fp8_paged(*args)
+    torch.cuda.synchronize()
+    nbytes = fa.attn_decode_fp8_workspace_bytes(8, Hkv, 1, d)
+    s = torch.cuda.Stream()
+    outs = []
+    for _ in range(30):
+        outs.append(fa.attn_decode_fp8_paged(*args, stream=s))
+        for _ in range(3):
+            torch.empty(nbytes // 4, device="cuda").fill_(float("nan"))
+    torch.cuda.synchronize()
+    for o, lse in outs:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
 def test_refusals(fa):
     """What the binding refuses on the device: types, shapes, a cache of the other format."""
     q = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
