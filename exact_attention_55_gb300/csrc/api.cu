@@ -912,6 +912,7 @@ extern "C" attn_status_t attn_bwd_bf16(const void* q, const void* k, const void*
 namespace {
 
 constexpr int kDecodeWholeKeys = 512;
+constexpr int kDecodeFp8MaxBatch = (1 << 19) - 1;   // the kernel packs a count of sequences into 19 bits
 constexpr int kPlanMaxRequests = 16384;   // three ints of shared memory per request
 
 bool page_size_ok(int page_size, int least)
@@ -1077,7 +1078,8 @@ extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cach
     if (nq > 8 || !page_size_ok(page_size, 16) || !block_ok(block, page_size))
         return ATTN_ERR_UNSUPPORTED;
     if ((long long)max_pages * page_size > 0x7fffffffLL ||
-        (long long)num_pages * Hkv > 0x7fffffffLL || (long long)B * H > 0x7fffffffLL / nq)
+        (long long)num_pages * Hkv > 0x7fffffffLL || (long long)B * H > 0x7fffffffLL / nq ||
+        B > kDecodeFp8MaxBatch)
         return ATTN_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) ||
         !aligned(lse, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||

@@ -87,7 +87,7 @@ struct alignas(16) Dec8Shared {
     float scale[C::STAGES][8];         // K scales of the tile's four 16-key parts, then V's
     float rowc[2][C::ROWS];            // per query row: softmax scale over its fragments' factor
     float m[kD8Warps][C::ROWS], l[kD8Warps][C::ROWS];
-    long long sum[kD8Threads / 32][2]; // set-up: tiles and sequences of each warp's share
+    long long sum[kD8Threads / 32];    // set-up: tiles and sequences of each warp's share
     long long first;                   // cost before sequence b0
     int b0;
     int abort_flag;
@@ -108,6 +108,13 @@ __device__ __forceinline__ Dec8Seq dec8_seq(const DecodeFp8Params& p, int b)
     return s;
 }
 
+// a / b for a >= 0 and 0 < b < 2^32, in 32 bits where a fits (the usual case, a third of the time).
+__device__ __forceinline__ long long dec8_div(long long a, long long b)
+{
+    if ((a >> 32) == 0) return (unsigned)a / (unsigned)b;
+    return a / b;
+}
+
 // The line that the ranges are cut from: `tiles` in all, `cost` long; a unit (sequence, key
 // head) of n tiles covers n + unit_cost of it, its tiles at the end; x cuts it at x cost / X.
 struct Dec8Line {
@@ -121,7 +128,7 @@ struct Dec8Line {
         cost = tiles + seqs * p.Hkv * unit_cost;
         X = tiles < p.ranges ? tiles : p.ranges;
     }
-    __device__ __forceinline__ long long cut(int x) const { return x * cost / X; }
+    __device__ __forceinline__ long long cut(int x) const { return dec8_div(x * cost, X); }
     __device__ __forceinline__ int owner(long long at) const { return (int)(((at + 1) * X - 1) / cost); }
 };
 
@@ -136,36 +143,30 @@ __device__ __forceinline__ Dec8Line dec8_line(const DecodeFp8Params& p, Shared* 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + kD8Threads - 1) / kD8Threads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    long long mine = 0, seqs = 0;
+    // tiles in the lower 44 bits (at most 2^25 a sequence), sequences that have any above
+    constexpr int shift = 44;
+    constexpr long long mask = (1LL << shift) - 1;
+    long long both = 0;
     for (int b = b0; b < b1; ++b) {
         const int n = dec8_span(p, dec8_seq(p, b).n);
-        mine += n;
-        seqs += n > 0;
+        both += n + ((long long)(n > 0) << shift);
     }
-    long long inc = mine, inc_s = seqs;
+    long long inc = both;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o), z = __shfl_up_sync(0xffffffffu, inc_s, o);
-        if (lane >= o) {
-            inc += y;
-            inc_s += z;
-        }
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
     }
-    if (lane == 31) {
-        sh->sum[warp][0] = inc;
-        sh->sum[warp][1] = inc_s;
-    }
+    if (lane == 31) sh->sum[warp] = inc;
     __syncthreads();
-    long long before = inc - mine, before_s = inc_s - seqs, total = 0, total_s = 0;
+    long long before2 = inc - both, total2 = 0;
 #pragma unroll
     for (int w = 0; w < kD8Threads / 32; ++w) {
-        if (w < warp) {
-            before += sh->sum[w][0];
-            before_s += sh->sum[w][1];
-        }
-        total += sh->sum[w][0];
-        total_s += sh->sum[w][1];
+        if (w < warp) before2 += sh->sum[w];
+        total2 += sh->sum[w];
     }
+    const long long mine = both & mask, seqs = both >> shift, before = before2 & mask, before_s = before2 >> shift;
+    const long long total = total2 & mask, total_s = total2 >> shift;
     const Dec8Line line(p, total, total_s);
     if (x < line.X) {
         const long long at = line.cut(x);
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
     const long long a = line.cut(x), e = line.cut(x + 1);
     int b = sh->b0;
     Dec8Seq seq = dec8_seq(p, b);
-    int span = dec8_span(p, seq.n), hk = (int)((a - sh->first) / (span + line.unit_cost));
+    int span = dec8_span(p, seq.n), hk = (int)dec8_div(a - sh->first, span + line.unit_cost);
     long long s0 = sh->first + (long long)hk * (span + line.unit_cost);
     // the unit's tiles of this range: [k0, k1)
     int k0 = 0, k1 = 0;

@@ -445,7 +445,7 @@ attn_status_t attn_cache_append_fp8(const void* k, const void* v, void* k_cache,
  *   page_table, seq_lens, max_pages, num_pages : as attn_decode_bf16_paged
  *   o, lse     : bf16 [B, H, nq, d], float [B, H, nq], written; a query that sees no key
  *                gets O = 0, LSE = -inf
- *   d in {64, 128, 256}
+ *   d in {64, 128, 256}; B < 2^19 (else ATTN_ERR_UNSUPPORTED)
  *   workspace  : device memory of attn_decode_fp8_workspace_bytes(...) bytes, 16-byte
  *                aligned (may be NULL when that is 0); its contents before and after do
  *                not matter.  Calls that may overlap need one each.
