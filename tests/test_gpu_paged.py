@@ -302,6 +302,113 @@ def test_decode_fp8_long_and_ragged(fa):
     check_decode(fa, [9001] * 3, 3, 3, 1, 64, 16, 16, "e5m2", seed=13)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("nq,group", [(1, 3), (2, 4), (4, 4), (3, 8), (8, 7)])
+def test_decode_fp8_split_heads(fa, d, nq, group):
+    """Heads of more keys than one CTA keeps whole, under any number of query rows."""
+    check_decode(fa, [1500, 2, 700, 385], 2 * group, 2, nq, d, 64, 32, "e4m3", seed=d + group)
+    check_decode(fa, [2100], group, 1, nq, d, 64, 32, "e5m2", window=999, seed=d + nq)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_decode_fp8_random_cases(fa, seed):
+    rng = np.random.default_rng(1000 + seed)
+    ps = int(rng.choice([16, 32, 64, 128]))
+    block = int(rng.choice([b for b in (16, 32, 64, 128) if b <= ps]))
+    B, Hkv, group = int(rng.integers(1, 9)), int(rng.integers(1, 5)), int(rng.choice([1, 1, 2, 4, 6, 16]))
+    hi = int(np.exp(rng.uniform(0, np.log(1800))))
+    check_decode(fa, list(rng.integers(0, hi + 1, B)), Hkv * group, Hkv, int(rng.integers(1, 9)),
+                 int(rng.choice([64, 128, 256])), ps, block, FORMATS[seed % 3],
+                 window=int(rng.choice([0, 0, rng.integers(1, hi + 2), 2 ** 31 - 1])), seed=seed)
+
+
+def test_caches_beyond_32_bit_offsets(fa):
+    """Pages whose bytes start past 2^32 in caches of 5 GB: rows appended there, then read."""
+    pages, Hkv, ps, d = 41000, 8, 128, 128
+    rng = np.random.default_rng(24)
+    kc, vc = (torch.empty((pages, Hkv, ps, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty((pages, Hkv, 1), device="cuda") for _ in range(2))
+    own = np.array([pages - 1, 33000, 3, pages - 2], np.int32)
+    L = 4 * ps - 5
+    slots = own[np.arange(L) // ps].astype(np.int64) * ps + np.arange(L) % ps
+    k, v = rows_of(rng, L, Hkv, d), rows_of(rng, L, Hkv, d)
+    fa.attn_cache_append_fp8(k.cuda(), v.cuda(), kc, vc, ks, vs, cuda(slots))
+    small = [np.zeros((4, Hkv, ps, d), np.uint8), np.zeros((4, Hkv, ps, d), np.uint8),
+             np.zeros((4, Hkv, 1), np.float32), np.zeros((4, Hkv, 1), np.float32)]
+    ref.append_fp8(k.float().numpy(), small[0], small[2], np.arange(L), "e4m3")
+    ref.append_fp8(v.float().numpy(), small[1], small[3], np.arange(L), "e4m3")
+    at = torch.from_numpy(own).long().cuda()
+    for got, want in zip((ks, vs), small[2:]):
+        np.testing.assert_array_equal(got[at].cpu().numpy(), want)
+    for got, want in zip((kc, vc), small):
+        got = got[at].transpose(1, 2).reshape(4 * ps, Hkv, d)[:L].cpu().numpy()
+        np.testing.assert_array_equal(got, want.transpose(0, 2, 1, 3).reshape(4 * ps, Hkv, d)[:L])
+    q = torch.from_numpy(rng.standard_normal((1, 16, 1, d)).astype(np.float32)).bfloat16()
+    o, lse = fa.attn_decode_fp8_paged(q.cuda(), kc, vc, ks, vs, cuda(own[None]), cuda(np.array([L], np.int32)), scale=0.1)
+    table = np.arange(4, dtype=np.int32)[None]
+    compare_decode(o, lse, ref.decode_fp8(q.double().numpy(), small[0], small[1], small[2], small[3], table, [L], "e4m3", 0.1))
+    del kc, vc
+    kb, vb = (torch.empty((pages, Hkv, ps, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    fa.attn_cache_append_bf16(k.cuda(), v.cuda(), kb, vb, cuda(slots))
+    for got, want in ((kb, k), (vb, v)):
+        assert torch.equal(got[at].transpose(1, 2).reshape(4 * ps, Hkv, d)[:L].cpu(), want)
+
+
+def test_a_slot_named_twice_stays_in_its_block(fa):
+    """Tokens that name one block out of order leave that block unspecified and no other."""
+    rng = np.random.default_rng(25)
+    slots = np.array([5, 5, 5, 40, 41, 2, 7, 70, -1, 71], np.int64)
+    H, d, ps = 2, 64, 32
+    k, v = rows_of(rng, len(slots), H, d), rows_of(rng, len(slots), H, d)
+    codes = [rng.integers(0, 100, (4, H, ps, d)).astype(np.uint8) for _ in range(2)]
+    scales = [np.full((4, H, 1), 0.01, np.float32) for _ in range(2)]
+    dev = [cuda(a) for a in codes + scales]
+    fa.attn_cache_append_fp8(k.cuda(), v.cuda(), *dev, cuda(slots))
+    torch.cuda.synchronize()
+    for x, c, s in ((k, codes[0], scales[0]), (v, codes[1], scales[1])):
+        ref.append_fp8(x.float().numpy(), c, s, slots, "e4m3")
+    for got, want in zip(dev, codes + scales):
+        np.testing.assert_array_equal(got.cpu().numpy()[1:], want[1:])
+    kb = torch.zeros(4, H, ps, d, dtype=torch.bfloat16, device="cuda")
+    vb = torch.zeros_like(kb)
+    fa.attn_cache_append_bf16(k.cuda(), v.cuda(), kb, vb, cuda(slots))
+    row = kb[0, :, 5].cpu()
+    assert any(torch.equal(row[0], k[i, 0]) for i in range(3)) and torch.equal(kb[1, :, 8].cpu(), k[3])
+
+
+def test_decode_fp8_workspace_and_outputs(fa):
+    """A workspace of exactly the bytes asked for, whatever it holds; a smaller one is refused;
+    given outputs are the ones returned."""
+    rng = np.random.default_rng(26)
+    lens, Hkv, d = [3000, 0, 700], 2, 128
+    kc, vc, ks, vs, table = ref.make_cache(rng, lens, Hkv, d, 64, 64, "e4m3")
+    args = [torch.randn(3, 8, 2, d).bfloat16().cuda()] + [cuda(a) for a in (kc, vc, ks, vs, table, np.array(lens, np.int32))]
+    want = fa.attn_decode_fp8_paged(*args)
+    need = fa.attn_decode_fp8_workspace_bytes(8, Hkv, 2, d)
+    for fill in (float("nan"), 0.0, 1e30):
+        ws = torch.full((need // 4,), fill, device="cuda")
+        o, lse = torch.full_like(want[0], 7), torch.full_like(want[1], 7)
+        got = fa.attn_decode_fp8_paged(*args, workspace=ws, o=o, lse=lse)
+        assert got[0] is o and got[1] is lse
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    with pytest.raises(fa.AttnError):
+        fa.attn_decode_fp8_paged(*args, workspace=torch.empty(need // 4 - 4, device="cuda"))
+    assert fa.attn_get_device_status() == fa.ATTN_OK
+
+
+def test_append_of_nothing(fa):
+    x = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    none = torch.zeros(0, dtype=torch.int64, device="cuda")
+    c, s = torch.full((2, 2, 16, 64), 9, dtype=torch.uint8, device="cuda"), torch.ones(2, 2, 1, device="cuda")
+    fa.attn_cache_append_fp8(x, x, c, c, s, s, none)
+    fa.attn_cache_append_bf16(x, x, c.bfloat16(), c.bfloat16(), none)
+    gone = torch.full((3,), -1, dtype=torch.int64, device="cuda")
+    fa.attn_cache_append_fp8(torch.ones(3, 2, 64, dtype=torch.bfloat16, device="cuda"),
+                             torch.ones(3, 2, 64, dtype=torch.bfloat16, device="cuda"), c, c, s, s, gone)
+    torch.cuda.synchronize()
+    assert (c == 9).all() and (s == 1).all()
+
+
 @pytest.mark.parametrize("qmul", [0.0, 1e-30, 1e-4, 300.0, 1e30])
 def test_decode_fp8_query_magnitudes(fa, qmul):
     """Queries far outside fp16's range keep their scores (softmax scale chosen to match)."""
