@@ -36,6 +36,7 @@ UNITS = [
     ("quant_fp8", "quant_fp8.cu", []),
     ("decode", "decode.cu", []),
     ("decode_tc", "decode_tc.cu", []),
+    ("decode_fp8_wide", "decode_fp8_wide.cu", []),
     ("decode_fp8", "decode_fp8.cu", []),
     ("paged", "paged.cu", []),
     ("attn_bwd", "attn_bwd.cu", []),

@@ -29,10 +29,11 @@ cudaError_t launch_decode_tc(const CUtensorMap& mq, const CUtensorMap& mk, const
 cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append_fp8(const AppendParams& p, bool e5m2, cudaStream_t stream);
-int decode_fp8_row_tiles(int rows, int d);
-int decode_fp8_ctas_per_sm(int rows, int d);
 cudaError_t launch_decode_fp8(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeFp8Params& p,
-                              int d, bool e5m2, cudaStream_t stream);
+                              int d, bool e5m2, int cta_rows, cudaStream_t stream);
+cudaError_t launch_decode_fp8_wide(const CUtensorMap& mk, const CUtensorMap& mv,
+                                   const DecodeFp8Params& p, int d, bool e5m2, int cta_rows,
+                                   cudaStream_t stream);
 cudaError_t launch_bwd(const BwdMaps& m, const BwdParams& p, int d, int sm_count, cudaStream_t stream);
 
 // One status word per device: kernels write kStatusTimeout here when they give up.
@@ -1036,19 +1037,34 @@ extern "C" attn_status_t attn_cache_append_fp8(const void* k, const void* v, voi
                ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// The grid of an 8-bit decoding step: two CTAs per SM, shared out among the groups of rows.
-static void decode_fp8_grid(int rows, int d, int sm_count, int* ranges, int* row_groups)
+// How an 8-bit decoding step of `rows` query rows per key head runs: the kernel, its rows per
+// CTA, and its grid, all resident at once.
+struct DecodeFp8Plan {
+    bool wide;       // decode_fp8_wide.cu (tcgen05, up to 128 rows a CTA) or decode_fp8.cu
+    int cta_rows, ranges, row_groups;
+};
+
+static DecodeFp8Plan decode_fp8_plan(int rows, int d, int sm_count)
 {
-    const int per = 8 * decode_fp8_row_tiles(rows, d);
-    *row_groups = (rows + per - 1) / per;
-    const int ctas = decode_fp8_ctas_per_sm(rows, d) * sm_count;
-    *ranges = ctas / *row_groups > 1 ? ctas / *row_groups : 1;
+    DecodeFp8Plan plan;
+    plan.wide = rows > (d == 256 ? 8 : 16);
+    int ctas;
+    if (plan.wide) {
+        plan.cta_rows = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+        ctas = sm_count;
+    } else {
+        plan.cta_rows = rows <= 8 ? 8 : 16;
+        ctas = (rows <= 8 && d <= 128 ? 3 : 2) * sm_count;
+    }
+    plan.row_groups = (rows + plan.cta_rows - 1) / plan.cta_rows;
+    plan.ranges = ctas / plan.row_groups > 1 ? ctas / plan.row_groups : 1;
+    return plan;
 }
 
-static size_t decode_fp8_ws_bytes(int rows, int d, int ranges, int row_groups)
+static size_t decode_fp8_ws_bytes(const DecodeFp8Plan& plan, int d)
 {
     // per CTA: what the joining kernel has to do (16 bytes), and two parts
-    return (size_t)ranges * row_groups * (4 + 2 * 8 * decode_fp8_row_tiles(rows, d) * (d + 2)) * sizeof(float);
+    return (size_t)plan.ranges * plan.row_groups * (4 + 2 * plan.cta_rows * (d + 2)) * sizeof(float);
 }
 
 extern "C" size_t attn_decode_fp8_workspace_bytes(int H, int Hkv, int nq, int d)
@@ -1057,9 +1073,7 @@ extern "C" size_t attn_decode_fp8_workspace_bytes(int H, int Hkv, int nq, int d)
     if (d != 64 && d != 128 && d != 256) return 0;
     DeviceInfo* dev = nullptr;
     if (H / Hkv > 0x7fffffff / 8 || device_info(&dev) != ATTN_OK) return 0;
-    int ranges = 1, row_groups = 1;
-    decode_fp8_grid(H / Hkv * nq, d, dev->sm_count, &ranges, &row_groups);
-    return decode_fp8_ws_bytes(H / Hkv * nq, d, ranges, row_groups);
+    return decode_fp8_ws_bytes(decode_fp8_plan(H / Hkv * nq, d, dev->sm_count), d);
 }
 
 extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cache,
@@ -1092,9 +1106,8 @@ extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cach
     const attn_status_t st = device_info(&dev);
     if (st != ATTN_OK) return st;
     const int rows = H / Hkv * nq;
-    int ranges = 1, row_groups = 1;
-    decode_fp8_grid(rows, d, dev->sm_count, &ranges, &row_groups);
-    if (decode_fp8_ws_bytes(rows, d, ranges, row_groups) > (workspace ? workspace_bytes : 0))
+    const DecodeFp8Plan plan = decode_fp8_plan(rows, d, dev->sm_count);
+    if (decode_fp8_ws_bytes(plan, d) > (workspace ? workspace_bytes : 0))
         return ATTN_ERR_INVALID_ARG;
     // the caches as (d, page_size, pages * Hkv), boxes of one page or 64 rows of a larger one
     alignas(64) CUtensorMap mk, mv;
@@ -1126,11 +1139,13 @@ extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cach
     p.c_log2 = (float)((double)scale * 1.4426950408889634);
     p.ws = static_cast<float*>(workspace);
     p.whole = (long long)max_pages * page_size <= kDecodeWholeKeys ? 1 : 0;
-    p.ranges = ranges;
-    p.row_groups = row_groups;
+    p.ranges = plan.ranges;
+    p.row_groups = plan.row_groups;
     p.status = dev->status;
     p.timeout_ns = kWaitTimeoutNs;
-    return launch_decode_fp8(mk, mv, p, d, format == ATTN_FP8_E5M2, static_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess
-               ? ATTN_OK : ATTN_ERR_CUDA;
+    const bool e5m2 = format == ATTN_FP8_E5M2;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t err = plan.wide ? launch_decode_fp8_wide(mk, mv, p, d, e5m2, plan.cta_rows, cs)
+                                      : launch_decode_fp8(mk, mv, p, d, e5m2, plan.cta_rows, cs);
+    return err == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

@@ -37,17 +37,7 @@
 // before the product, and a NaN value at a key that only some rows see is replaced by 0
 // there and added back as NaN to the rows that do (keep_nan), so what stale rows and pages
 // hold never reaches O.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-
-#include <cstdint>
-#include <type_traits>
-
-#include "attn_params.h"
-#include "paged_params.h"
-#include "ptx.cuh"
+#include "decode_fp8.cuh"
 
 namespace gb300 {
 
@@ -55,8 +45,6 @@ constexpr int kD8Tile = 64;            // keys of a tile, 16 per consumer warp
 constexpr int kD8Warps = 4;            // consumer warps
 constexpr int kD8Threads = (kD8Warps + 1) * 32;
 constexpr float kD8Tau = 8.0f;         // the running maximum is raised when passed by this (log2)
-constexpr int kD8UnitCost = 4;         // tiles a head's start and end are worth
-constexpr int kD8CombineThreads = 128;
 
 template <int D, int NT>
 struct Dec8Cfg {
@@ -73,7 +61,6 @@ struct Dec8Cfg {
     static constexpr int FIT = (CAP - FIXED) / STAGE;
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
-    static constexpr int PART = ROWS * (D + 2);           // floats of a part: O, maxima, sums
     static_assert(STAGES >= 2, "ring");
     static_assert(STAGE == kD8Warps * 8 * D * 4, "a head's last stage holds the warps' O for joining");
 };
@@ -87,120 +74,9 @@ struct alignas(16) Dec8Shared {
     float scale[C::STAGES][8];         // K scales of the tile's four 16-key parts, then V's
     float rowc[2][C::ROWS];            // per query row: softmax scale over its fragments' factor
     float m[kD8Warps][C::ROWS], l[kD8Warps][C::ROWS];
-    long long sum[kD8Threads / 32];    // set-up: tiles and sequences of each warp's share
-    long long first;                   // cost before sequence b0
-    int b0;
+    Dec8Setup<kD8Threads> setup;
     int abort_flag;
 };
-
-// Tiles of sequence b: [t0, t0 + n) of 64 keys, of which keys lo .. L-1 may be seen.
-struct Dec8Seq {
-    int L, lo, t0, n;
-};
-
-__device__ __forceinline__ Dec8Seq dec8_seq(const DecodeFp8Params& p, int b)
-{
-    Dec8Seq s;
-    s.L = min(max(__ldg(p.seq_lens + b), 0), p.max_pages << p.log2_ps);
-    s.lo = p.window > 0 ? max(0, s.L - p.nq - p.window) : 0;
-    s.t0 = s.lo / kD8Tile;
-    s.n = (int)(((unsigned)s.L + kD8Tile - 1) / kD8Tile) - s.t0;
-    return s;
-}
-
-// a / b for a >= 0 and 0 < b < 2^32, in 32 bits where a fits (the usual case, a third of the time).
-__device__ __forceinline__ long long dec8_div(long long a, long long b)
-{
-    if ((a >> 32) == 0) return (unsigned)a / (unsigned)b;
-    return a / b;
-}
-
-// The line that the ranges are cut from: `tiles` in all, `cost` long; a unit (sequence, key
-// head) of n tiles covers n + unit_cost of it, its tiles at the end; x cuts it at x cost / X.
-struct Dec8Line {
-    long long tiles, cost, X;
-    int unit_cost;
-
-    __device__ __forceinline__ Dec8Line(const DecodeFp8Params& p, long long seq_tiles, long long seqs)
-    {
-        tiles = seq_tiles * p.Hkv;
-        unit_cost = tiles <= p.ranges ? 0 : kD8UnitCost;   // few tiles: one per range
-        cost = tiles + seqs * p.Hkv * unit_cost;
-        X = tiles < p.ranges ? tiles : p.ranges;
-    }
-    __device__ __forceinline__ long long cut(int x) const { return dec8_div(x * cost, X); }
-    __device__ __forceinline__ int owner(long long at) const { return (int)(((at + 1) * X - 1) / cost); }
-};
-
-// What a sequence's units cover of the line: their tiles, or 1 where units are not split.
-__device__ __forceinline__ int dec8_span(const DecodeFp8Params& p, int n) { return p.whole ? min(n, 1) : n; }
-
-// Finds the sequence that range x starts in (its number and the cost before it).  All
-// threads of the main kernel call it.
-template <class Shared>
-__device__ __forceinline__ Dec8Line dec8_line(const DecodeFp8Params& p, Shared* sh, int x)
-{
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.B + kD8Threads - 1) / kD8Threads;
-    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    // tiles in the lower 44 bits (at most 2^25 a sequence), sequences that have any above
-    constexpr int shift = 44;
-    constexpr long long mask = (1LL << shift) - 1;
-    long long both = 0;
-    for (int b = b0; b < b1; ++b) {
-        const int n = dec8_span(p, dec8_seq(p, b).n);
-        both += n + ((long long)(n > 0) << shift);
-    }
-    long long inc = both;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    if (lane == 31) sh->sum[warp] = inc;
-    __syncthreads();
-    long long before2 = inc - both, total2 = 0;
-#pragma unroll
-    for (int w = 0; w < kD8Threads / 32; ++w) {
-        if (w < warp) before2 += sh->sum[w];
-        total2 += sh->sum[w];
-    }
-    const long long mine = both & mask, seqs = both >> shift, before = before2 & mask, before_s = before2 >> shift;
-    const long long total = total2 & mask, total_s = total2 >> shift;
-    const Dec8Line line(p, total, total_s);
-    if (x < line.X) {
-        const long long at = line.cut(x);
-        long long s0 = (before + before_s * line.unit_cost) * p.Hkv;
-        if (s0 <= at && at < s0 + (mine + seqs * line.unit_cost) * p.Hkv)
-            for (int b = b0; b < b1; ++b) {
-                const int n = dec8_span(p, dec8_seq(p, b).n);
-                const long long len = n > 0 ? (long long)(n + line.unit_cost) * p.Hkv : 0;
-                if (s0 <= at && at < s0 + len) {
-                    sh->b0 = b;
-                    sh->first = s0;
-                }
-                s0 += len;
-            }
-    }
-    __syncthreads();
-    return line;
-}
-
-template <bool kE5M2>
-__device__ __forceinline__ uint32_t dec8_half2(uint32_t two)   // codes in bits 0-15 -> f16x2, exact
-{
-    uint32_t h;
-    if constexpr (kE5M2) asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-    else asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-    return h;
-}
-
-// 0x80 in every byte of w whose code is not finite (E5M2: infinities too).
-template <bool kE5M2>
-__device__ __forceinline__ uint32_t dec8_nonfinite(uint32_t w)
-{
-    return (kE5M2 ? (w & 0x7C7C7C7Cu) + 0x04040404u : (w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-}
 
 __device__ __forceinline__ void dec8_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1)
@@ -218,33 +94,6 @@ __device__ __forceinline__ uint32_t dec8_transpose(uint32_t x)   // 8x8 of 16-bi
     return y;
 }
 
-__device__ __forceinline__ uint32_t dec8_pack_half2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint4 dec8_lds128(uint32_t a)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-
-__device__ __forceinline__ uint2 dec8_lds64(uint32_t a)
-{
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-
-__device__ __forceinline__ void dec8_timeout(const DecodeFp8Params& p, int* abort_flag)
-{
-    atomicExch(p.status, kStatusTimeout);
-    *reinterpret_cast<volatile int*>(abort_flag) = 1;
-}
-
 template <int D, bool kE5M2, int NT>
 __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -259,10 +108,6 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
     const volatile int* abort_flag = &sh->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float NEG_INF = -__int_as_float(0x7f800000);
-    // what the combine kernel finds: an entry per unit, or where there are more units than CTAs
-    // one per CTA, for the one unit that it may begin and not end
-    const bool per_unit = (long long)p.B * p.Hkv * p.row_groups <= gridDim.x;
-    int4* todo = reinterpret_cast<int4*>(p.ws);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (threadIdx.x == 0) {
@@ -281,58 +126,14 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
         tma_prefetch_desc(&tmV);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");   // what ran before has written its results
-    if (threadIdx.x == 0) {
-        if (!per_unit) todo[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    }
+    if (threadIdx.x == 0 && !dec8_per_unit(p)) reinterpret_cast<int4*>(p.ws)[blockIdx.x] = make_int4(-1, 0, 0, 0);
     const int x = blockIdx.x / p.row_groups, rg = blockIdx.x - x * p.row_groups, row0 = rg * C::ROWS;
-    const Dec8Line line = dec8_line(p, sh, x);
-    // sequences without a key: O = 0, LSE = -inf
-    auto write_empty = [&](int threads) {
-        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-            if (dec8_seq(p, b).n > 0) continue;
-            const size_t r0 = (size_t)b * p.Hkv * p.rows, rows = (size_t)p.Hkv * p.rows;
-            uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + r0 * D);
-            for (size_t i = threadIdx.x; i < rows * (D / 8); i += threads) o[i] = make_uint4(0, 0, 0, 0);
-            for (size_t i = threadIdx.x; i < rows; i += threads) p.lse[r0 + i] = NEG_INF;
-            if (per_unit)
-                for (int i = threadIdx.x; i < p.Hkv * p.row_groups; i += threads)
-                    todo[b * p.Hkv * p.row_groups + i] = make_int4(-1, 0, 0, 0);
-        }
-    };
+    const Dec8Line line = dec8_line<kD8Tile>(p, sh->setup, x);
     if (x >= line.X) {
-        write_empty(kD8Threads);
+        dec8_write_empty<kD8Tile, D>(p, kD8Threads);
         return;
     }
-    // this CTA's range [a, e) of the line; unit (b, hk) starts at s0 and has seq.n tiles
-    const long long a = line.cut(x), e = line.cut(x + 1);
-    int b = sh->b0;
-    Dec8Seq seq = dec8_seq(p, b);
-    int span = dec8_span(p, seq.n), hk = (int)dec8_div(a - sh->first, span + line.unit_cost);
-    long long s0 = sh->first + (long long)hk * (span + line.unit_cost);
-    // the unit's tiles of this range: [k0, k1)
-    int k0 = 0, k1 = 0;
-    auto take = [&]() {
-        k0 = (int)max(0LL, a - s0 - line.unit_cost);
-        k1 = (int)max((long long)k0, min((long long)span, e - s0 - line.unit_cost));
-        if (p.whole && k1 > k0) k1 = seq.n;
-    };
-    // to the next unit with tiles of this range; false when there is none
-    auto next_unit = [&]() -> bool {
-        do {
-            s0 += span + line.unit_cost;
-            if (s0 + line.unit_cost >= e) return false;
-            if (++hk == p.Hkv) {
-                hk = 0;
-                do seq = dec8_seq(p, ++b);
-                while (seq.n == 0);
-                span = dec8_span(p, seq.n);
-            }
-            take();
-        } while (k1 <= k0);
-        return true;
-    };
-    take();
-    bool more = k1 > k0 || next_unit();
+    Dec8Walk<kD8Tile> w(p, line, sh->setup, x);
 
     if (warp == kD8Warps) {
         // ------------------------------------------------------------ producer
@@ -350,11 +151,11 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
             ok = __shfl_sync(0xffffffffu, r, 0) != 0;
             return ok;
         };
-        while (more && ok) {
+        while (w.more && ok) {
             // this head's queries: lane (g, t) holds row 8 nt + g, 16-byte pieces of its share of d
             constexpr int PER = D / 8;                           // words of a row in a lane
-            uint32_t w[NT][PER];
-            const size_t unit_row = ((size_t)b * p.Hkv + hk) * p.rows + row0;
+            uint32_t qw[NT][PER];
+            const size_t unit_row = ((size_t)w.b * p.Hkv + w.hk) * p.rows + row0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -366,13 +167,13 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                         if (row0 + r < p.rows)
                             u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
                                                                      (unit_row + r) * D + c * C::CB + t * (C::CB / 4) + v * 8));
-                        w[nt][o] = u.x, w[nt][o + 1] = u.y, w[nt][o + 2] = u.z, w[nt][o + 3] = u.w;
+                        qw[nt][o] = u.x, qw[nt][o + 1] = u.y, qw[nt][o + 2] = u.z, qw[nt][o + 3] = u.w;
                     }
-            const int* ptab = p.page_table + (size_t)b * p.max_pages;
+            const int* ptab = p.page_table + (size_t)w.b * p.max_pages;
             int held = 0, pg = 0;                                // 32 boxes' pages from box `held` on
-            for (int k = k0; k < k1 && ok; ++k) {
-                const int key0 = (seq.t0 + k) * kD8Tile, box0 = key0 >> log2_r;
-                if (k == k0 || box0 - held >= 32) {
+            for (int k = w.k0; k < w.k1 && ok; ++k) {
+                const int key0 = (w.seq.t0 + k) * kD8Tile, box0 = key0 >> log2_r;
+                if (k == w.k0 || box0 - held >= 32) {
                     held = box0;
                     const long long key = (long long)(box0 + lane) << log2_r;
                     const int pi = (int)min(key >> p.log2_ps, (long long)p.max_pages - 1);
@@ -391,11 +192,11 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
 #pragma unroll
                     for (int c = 0; c < C::NCB; ++c)
                         tma_load_3d(dst + c * kD8Tile * C::CB, is_v ? &tmV : &tmK, fb, c * C::CB,
-                                    (key0 + (box << log2_r)) & ps_mask, pg_box * p.Hkv + hk, pol);
+                                    (key0 + (box << log2_r)) & ps_mask, pg_box * p.Hkv + w.hk, pol);
                 }
                 if (lane < 8) {
                     const int key = key0 + (lane & 3) * 16;
-                    const size_t at = (((size_t)pg_part * p.Hkv + hk) << (p.log2_ps - p.log2_blk)) +
+                    const size_t at = (((size_t)pg_part * p.Hkv + w.hk) << (p.log2_ps - p.log2_blk)) +
                                       ((key & ps_mask) >> p.log2_blk);
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n\t"
                                  "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%2];" ::"r"(
@@ -408,7 +209,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                     stage = 0;
                     parity ^= 1;
                 }
-                if (k > k0) continue;
+                if (k > w.k0) continue;
                 // fragments: a row scaled by a power of two so that its largest value is just
                 // below 2^15 in fp16; what is 2^-38 of that and less is rounded
                 if (!wait_lane0(&sh->q_empty[q_slot], q_parity)) break;
@@ -416,7 +217,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                 for (int nt = 0; nt < NT; ++nt) {
                     uint32_t big = 0;
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) big = max(big, max((w[nt][i] << 16) & 0x7FFF0000u, w[nt][i] & 0x7FFF0000u));
+                    for (int i = 0; i < PER; ++i) big = max(big, max((qw[nt][i] << 16) & 0x7FFF0000u, qw[nt][i] & 0x7FFF0000u));
                     big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
                     big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
                     const int ex = max((int)(big >> 23), 15) - 14;   // biased exponent of the factor's inverse
@@ -424,7 +225,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                     if (t == 0) sh->rowc[q_slot][nt * 8 + g] = __int_as_float(ex << 23) * p.c_log2;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
-                        const uint32_t u = w[nt][2 * i], v = w[nt][2 * i + 1];
+                        const uint32_t u = qw[nt][2 * i], v = qw[nt][2 * i + 1];
                         qs[q_slot * C::Q_FRAGS + (nt * (D / 16) + i) * 32 + lane] = make_uint2(
                             dec8_pack_half2(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xFFFF0000u) * down),
                             dec8_pack_half2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down));
@@ -437,7 +238,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                     q_parity ^= 1;
                 }
             }
-            if (ok) more = next_unit();
+            if (ok) w.next(p);
         }
         if (!ok && lane == 0) dec8_timeout(p, &sh->abort_flag);
         // every copy issued lands before shared memory is released
@@ -463,8 +264,8 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
             meet_parity ^= 1;
             return r;
         };
-        while (more) {
-            const size_t unit_row = ((size_t)b * p.Hkv + hk) * p.rows + row0;
+        while (w.more) {
+            const size_t unit_row = ((size_t)w.b * p.Hkv + w.hk) * p.rows + row0;
             if (!wait_all(&sh->q_full[q_slot], q_parity)) break;
             const uint2* frag = qs + q_slot * C::Q_FRAGS + lane;
             uint2 qf[C::Q_REGS ? NT * (D / 16) : 1];
@@ -527,13 +328,13 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                 }
             };
 
-            for (int k = k0; k < k1; ++k) {
-                const int key0 = (seq.t0 + k) * kD8Tile + warp * 16;
+            for (int k = w.k0; k < w.k1; ++k) {
+                const int key0 = (w.seq.t0 + k) * kD8Tile + warp * 16;
                 if (!wait_all(&sh->full[stage], parity)) break;
                 // this warp's keys: some row sees one of them; all rows see all of them
-                const bool any = key0 < seq.L && key0 + 15 >= seq.lo;
-                const bool edge = key0 + 15 > seq.L - p.nq ||
-                                  (p.window > 0 && key0 < seq.L - 1 - p.window);
+                const bool any = key0 < w.seq.L && key0 + 15 >= w.seq.lo;
+                const bool edge = key0 + 15 > w.seq.L - p.nq ||
+                                  (p.window > 0 && key0 < w.seq.L - 1 - p.window);
                 const uint32_t kb = smem_u32(smem + stage * C::STAGE), vb = kb + C::HALF;
                 if (any) {
                     // ---- S^T = K Q^T: keys key0 + g (+ 8) by rows 8 nt + 2 t (+ 1)
@@ -568,12 +369,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                     }
                     // ---- scales, mask, running maximum, weights
                     const float ksc = sh->scale[stage][warp], vsc = sh->scale[stage][4 + warp];
-                    // vs = f 2^e with e at most 60 below the largest so far (a scale of 0 has
-                    // f = 0): 2^-e stays in range and every key counts in l
-                    const int ve = min(max((int)((__float_as_uint(vsc) >> 23) & 0xFF) - 127, v_top - 60), 126);
-                    v_top = max(v_top, ve);
-                    const float vf = vsc * __int_as_float((127 - ve) << 23), vinv = __int_as_float((127 - ve) << 23);
-                    const float vef = (float)ve;
+                    const Dec8ValueScale vs(vsc, v_top);
                     float xs[NT][4];
                     bool raise = false;
 #pragma unroll
@@ -581,7 +377,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                         const float k0 = ksc * rowc[nt][0], k1 = ksc * rowc[nt][1];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            xs[nt][e] = fmaf(s[nt][0][e] + s[nt][1][e], (e & 1) ? k1 : k0, vef);
+                            xs[nt][e] = fmaf(s[nt][0][e] + s[nt][1][e], (e & 1) ? k1 : k0, vs.e);
                         }
                     }
                     if (edge) {
@@ -590,7 +386,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const int key = key0 + g + (e & 2) * 4;
-                                const int last = seq.L - p.nq + (row0 + nt * 8 + 2 * t + (e & 1)) % p.nq;
+                                const int last = w.seq.L - p.nq + (row0 + nt * 8 + 2 * t + (e & 1)) % p.nq;
                                 if (key > last || (p.window > 0 && key < last - p.window)) xs[nt][e] = NEG_INF;
                             }
                     }
@@ -622,16 +418,16 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                     uint32_t pb[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float w[4];
+                        float wt[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float mm = m[nt][e & 1];
-                            w[e] = ex2(xs[nt][e] - (mm == NEG_INF ? 0.0f : mm));
+                            wt[e] = ex2(xs[nt][e] - (mm == NEG_INF ? 0.0f : mm));
                         }
-                        l[nt][0] = fmaf(w[0] + w[2], vinv, l[nt][0]);
-                        l[nt][1] = fmaf(w[1] + w[3], vinv, l[nt][1]);
-                        pb[nt][0] = dec8_transpose(dec8_pack_half2(w[0] * vf, w[1] * vf));
-                        pb[nt][1] = dec8_transpose(dec8_pack_half2(w[2] * vf, w[3] * vf));
+                        l[nt][0] = fmaf(wt[0] + wt[2], vs.inv, l[nt][0]);
+                        l[nt][1] = fmaf(wt[1] + wt[3], vs.inv, l[nt][1]);
+                        pb[nt][0] = dec8_transpose(dec8_pack_half2(wt[0] * vs.f, wt[1] * vs.f));
+                        pb[nt][1] = dec8_transpose(dec8_pack_half2(wt[2] * vs.f, wt[3] * vs.f));
                     }
                     // ---- O^T += V^T P^T: this lane's keys 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
@@ -654,7 +450,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const int key = key0 + 2 * t + (k & 1) + (k & 2) * 4;
-                                const bool out = key >= seq.L || key < seq.lo;
+                                const bool out = key >= w.seq.L || key < w.seq.lo;
 #pragma unroll
                                 for (int i = 0; i < VW; ++i) {
                                     v[k][i] = out ? 0u : v[k][i];
@@ -678,7 +474,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                         }
                     }
                 }
-                if (k == k1 - 1) break;                          // the last stage is kept for the joining
+                if (k == w.k1 - 1) break;                          // the last stage is kept for the joining
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh->empty[stage]));
                 if (++stage == C::STAGES) {
@@ -698,8 +494,8 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
             // ---- join the four warps, eight rows at a time, in the last tile's stage: warp w's
             // row r, float4 c at ((w * 8 + r) * D / 4 + (c ^ (r / 2 & 3))), which keeps the
             // writes below to two lanes a bank
-            const bool whole = k1 - k0 == seq.n;
-            float* part = p.ws + 4 * gridDim.x + (size_t)(2 * blockIdx.x + (k0 == 0 ? 1 : 0)) * C::PART;
+            const bool whole = w.whole();
+            float* part = dec8_my_part<C::ROWS, D>(p, w.k0 == 0);
             float4* area = reinterpret_cast<float4*>(smem + stage * C::STAGE);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -761,123 +557,13 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                 stage = 0;
                 parity ^= 1;
             }
-            if (k0 == 0 && threadIdx.x == 0 && !p.whole && (per_unit || !whole))   // the unit's first part names the last
-                todo[per_unit ? (b * p.Hkv + hk) * p.row_groups + rg : blockIdx.x] =
-                    whole ? make_int4(-1, 0, 0, 0)
-                          : make_int4(x, line.owner(s0 + line.unit_cost + seq.n - 1), rg, (int)unit_row);
-            more = next_unit();
+            if (threadIdx.x == 0) dec8_name_parts(p, w, line, x, rg, unit_row);
+            w.next(p);
         }
         if (!ok) dec8_timeout(p, &sh->abort_flag);
-        else write_empty(kD8Warps * 32);
+        else dec8_write_empty<kD8Tile, D>(p, kD8Warps * 32);
     }
 }
-
-// Joins the parts of a unit that several ranges shared: with M the largest part maximum,
-// O = sum_x 2^(M_x - M) a_x / sum_x 2^(M_x - M) l_x.  grid.x: the units, or where there are
-// more of them the ranges (each leaves at most one unit to its successors); grid.y shares
-// a unit's rows and columns.  Latency-bound: a thread has all its parts' loads in flight
-// together.  Up to eight parts (the usual batch), a thread joins one float4 of one row;
-// more (one long sequence), 32 columns of a row at a time, sixteen threads a float4.
-template <int D, int NT>
-__global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(const DecodeFp8Params p)
-{
-    using C = Dec8Cfg<D, NT>;
-    constexpr int FEW = 8, MANY = 10;                        // parts of a thread
-    constexpr int COLS = 8, GROUPS = kD8CombineThreads / COLS, SLICES = D / 32;
-    __shared__ float4 sm_a[GROUPS][COLS];
-    __shared__ float2 sm_ml[GROUPS];
-    const float NEG_INF = -__int_as_float(0x7f800000);
-    const int tid = threadIdx.x, ctas = p.ranges * p.row_groups;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 todo = reinterpret_cast<const int4*>(p.ws)[blockIdx.x];
-    const int x0 = todo.x, x1 = min(todo.y, p.ranges - 1), rg = todo.z;
-    if (x0 < 0) return;
-    const size_t row0 = (size_t)todo.w;
-    const int rows = min(C::ROWS, p.rows - rg * C::ROWS);
-    auto part_of = [&](int x) {
-        return p.ws + 4 * ctas + (size_t)(2 * (x * p.row_groups + rg) + (x == x0 ? 1 : 0)) * C::PART;
-    };
-    auto finish = [&](int r, int col, float4 a, float sum, float M) {
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (row0 + r) * D)[col] =
-            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-        if (col == 0)
-            p.lse[row0 + r] = sum == 0.0f ? NEG_INF : ((M == NEG_INF ? 0.0f : M) + __log2f(sum)) * 0.69314718055994531f;
-    };
-    // (M, l, a) += K parts x, x + step, ... up to x1, of row r
-    auto join = [&](auto K, int x, int step, int r, int col, float& M, float& l, float4& a) {
-        constexpr int k_parts = decltype(K)::value;
-        float m[k_parts], sum[k_parts];
-        float4 v[k_parts];
-#pragma unroll
-        for (int k = 0; k < k_parts; ++k) {
-            m[k] = NEG_INF;
-            if (x + k * step > x1) continue;
-            const float* w = part_of(x + k * step);
-            m[k] = w[C::ROWS * D + r];
-            sum[k] = w[C::ROWS * D + C::ROWS + r];
-            v[k] = *reinterpret_cast<const float4*>(w + r * D + col * 4);
-        }
-        float top = M;
-#pragma unroll
-        for (int k = 0; k < k_parts; ++k) top = fmaxf(top, m[k]);
-        const float mb = top == NEG_INF ? 0.0f : top, f = ex2(M - mb);
-        M = top;
-        l *= f;
-        a.x *= f, a.y *= f, a.z *= f, a.w *= f;
-#pragma unroll
-        for (int k = 0; k < k_parts; ++k) {
-            if (x + k * step > x1) continue;
-            const float fac = ex2(m[k] - mb);
-            l = fmaf(fac, sum[k], l);
-            a.x = fmaf(fac, v[k].x, a.x), a.y = fmaf(fac, v[k].y, a.y);
-            a.z = fmaf(fac, v[k].z, a.z), a.w = fmaf(fac, v[k].w, a.w);
-        }
-    };
-    if (x1 - x0 < FEW) {
-        for (int i = blockIdx.y * kD8CombineThreads + tid; i < rows * (D / 4); i += gridDim.y * kD8CombineThreads) {
-            const int r = i / (D / 4), col = i - r * (D / 4);
-            float M = NEG_INF, l = 0.0f;
-            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            join(std::integral_constant<int, FEW>{}, x0, 1, r, col, M, l, a);
-            finish(r, col, a, l, M);
-        }
-        return;
-    }
-    const int grp = tid / COLS;
-    for (int i = blockIdx.y; i < rows * SLICES; i += gridDim.y) {
-        const int r = i / SLICES, col = (i - r * SLICES) * COLS + tid % COLS;
-        float M = NEG_INF, l = 0.0f;
-        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int x = x0 + grp; x <= x1; x += GROUPS * MANY)
-            join(std::integral_constant<int, MANY>{}, x, GROUPS, r, col, M, l, a);
-        sm_a[grp][tid % COLS] = a;
-        if (tid % COLS == 0) sm_ml[grp] = make_float2(M, l);
-        __syncthreads();
-        if (tid < COLS) {
-            float top = NEG_INF, sum = 0.0f;
-            a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < GROUPS; ++k) top = fmaxf(top, sm_ml[k].x);
-            const float mb = top == NEG_INF ? 0.0f : top;
-#pragma unroll
-            for (int k = 0; k < GROUPS; ++k) {
-                const float4 v = sm_a[k][tid];
-                const float fac = ex2(sm_ml[k].x - mb);
-                sum = fmaf(fac, sm_ml[k].y, sum);
-                a.x = fmaf(fac, v.x, a.x), a.y = fmaf(fac, v.y, a.y);
-                a.z = fmaf(fac, v.z, a.z), a.w = fmaf(fac, v.w, a.w);
-            }
-            finish(r, col, a, sum, top);
-        }
-        __syncthreads();
-    }
-}
-
-// Query rows of a CTA, in eights.  More rows under one key head go to more CTAs, which read
-// the same tiles at the same time (the second read comes from L2).
-int decode_fp8_row_tiles(int rows, int d) { return rows <= 8 || d == 256 ? 1 : 2; }
-int decode_fp8_ctas_per_sm(int rows, int d) { return rows <= 8 && d <= 128 ? 3 : 2; }
 
 template <int D, bool kE5M2, int NT>
 static cudaError_t launch_decode_fp8_n(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeFp8Params& p,
@@ -899,36 +585,31 @@ static cudaError_t launch_decode_fp8_n(const CUtensorMap& mk, const CUtensorMap&
     cfg.dynamicSmemBytes = C::SMEM;
     e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
     if (e != cudaSuccess) return e;
-    if (p.whole) return cudaSuccess;
-    // a unit's float4s over its CTAs, and four CTAs a part of the average unit while that is
-    // more, up to one for 32 columns of a row
-    const long long units = (long long)p.B * p.Hkv * p.row_groups, ctas = p.ranges * p.row_groups;
-    const int rows = p.rows < C::ROWS ? p.rows : C::ROWS, items = rows * (D / 32);
-    const int least = (rows * (D / 4) + kD8CombineThreads - 1) / kD8CombineThreads;
-    int share = units < ctas ? (int)(4 * ctas / units) : least;
-    share = share > items ? items : share < least ? least : share;
-    cfg.gridDim = dim3((unsigned)(units < ctas ? units : ctas), share);
-    cfg.blockDim = dim3(kD8CombineThreads);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, decode_fp8_combine_kernel<D, NT>, p);
+    return launch_decode_fp8_combine<D, C::ROWS>(p, cfg);
 }
 
 template <int D, bool kE5M2>
 static cudaError_t launch_decode_fp8_d(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeFp8Params& p,
-                                       cudaStream_t stream)
+                                       int cta_rows, cudaStream_t stream)
 {
     if constexpr (D < 256)
-        if (decode_fp8_row_tiles(p.rows, D) == 2) return launch_decode_fp8_n<D, kE5M2, 2>(mk, mv, p, stream);
+        if (cta_rows == 16) return launch_decode_fp8_n<D, kE5M2, 2>(mk, mv, p, stream);
     return launch_decode_fp8_n<D, kE5M2, 1>(mk, mv, p, stream);
 }
 
 cudaError_t launch_decode_fp8(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeFp8Params& p, int d,
-                              bool e5m2, cudaStream_t stream)
+                              bool e5m2, int cta_rows, cudaStream_t stream)
 {
     switch (d) {
-    case 64: return e5m2 ? launch_decode_fp8_d<64, true>(mk, mv, p, stream) : launch_decode_fp8_d<64, false>(mk, mv, p, stream);
-    case 128: return e5m2 ? launch_decode_fp8_d<128, true>(mk, mv, p, stream) : launch_decode_fp8_d<128, false>(mk, mv, p, stream);
-    case 256: return e5m2 ? launch_decode_fp8_d<256, true>(mk, mv, p, stream) : launch_decode_fp8_d<256, false>(mk, mv, p, stream);
+    case 64:
+        return e5m2 ? launch_decode_fp8_d<64, true>(mk, mv, p, cta_rows, stream)
+                    : launch_decode_fp8_d<64, false>(mk, mv, p, cta_rows, stream);
+    case 128:
+        return e5m2 ? launch_decode_fp8_d<128, true>(mk, mv, p, cta_rows, stream)
+                    : launch_decode_fp8_d<128, false>(mk, mv, p, cta_rows, stream);
+    case 256:
+        return e5m2 ? launch_decode_fp8_d<256, true>(mk, mv, p, cta_rows, stream)
+                    : launch_decode_fp8_d<256, false>(mk, mv, p, cta_rows, stream);
     default: return cudaErrorInvalidValue;
     }
 }

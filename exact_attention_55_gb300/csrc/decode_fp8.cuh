@@ -1,0 +1,398 @@
+// decode_fp8.cuh -- what the two decoding kernels over an 8-bit paged cache share: how the
+// work is cut into ranges, how a CTA walks its range, conversions, and the joining of parts.
+//
+// The tiles (TILE keys of one key head) of all sequences form one line that is cut into
+// equal ranges, one per resident CTA, so a ragged batch and a single long sequence both keep
+// every SM busy to the end.  A unit (sequence, key head) counts a few tiles more than it has,
+// what starting and ending it costs.  A range may end inside a unit; its part (O not yet
+// divided, running maxima, sums) then goes to the workspace, and decode_fp8_combine_kernel,
+// launched as a dependent of the main grid, joins a unit's parts.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "attn_params.h"
+#include "paged_params.h"
+#include "ptx.cuh"
+
+namespace gb300 {
+
+constexpr int kD8UnitCost = 4;         // tiles a unit's start and end are worth
+constexpr int kD8CombineThreads = 128;
+
+// Floats of a part: O [rows][d], maxima [rows], sums [rows].
+__host__ __device__ constexpr int dec8_part(int rows, int d) { return rows * (d + 2); }
+
+// Tiles of a sequence: [t0, t0 + n), of whose keys lo .. L-1 may be seen.
+struct Dec8Seq {
+    int L, lo, t0, n;
+};
+
+template <int TILE>
+__device__ __forceinline__ Dec8Seq dec8_seq(const DecodeFp8Params& p, int b)
+{
+    Dec8Seq s;
+    s.L = min(max(__ldg(p.seq_lens + b), 0), p.max_pages << p.log2_ps);
+    s.lo = p.window > 0 ? max(0, s.L - p.nq - p.window) : 0;
+    s.t0 = s.lo / TILE;
+    s.n = (int)(((unsigned)s.L + TILE - 1) / TILE) - s.t0;
+    return s;
+}
+
+// a / b for a >= 0 and 0 < b < 2^32, in 32 bits where a fits (the usual case, a third of the time).
+__device__ __forceinline__ long long dec8_div(long long a, long long b)
+{
+    if ((a >> 32) == 0) return (unsigned)a / (unsigned)b;
+    return a / b;
+}
+
+// The line: `tiles` in all, `cost` long; a unit of n tiles covers n + unit_cost of it, its
+// tiles at the end; range x is [cut(x), cut(x + 1)) of X.  Where units are not split
+// (p.whole) each counts as one tile.
+struct Dec8Line {
+    long long tiles, cost, X;
+    int unit_cost;
+
+    __device__ __forceinline__ Dec8Line(const DecodeFp8Params& p, long long seq_tiles, long long seqs)
+    {
+        tiles = seq_tiles * p.Hkv;
+        unit_cost = tiles <= p.ranges ? 0 : kD8UnitCost;   // few tiles: one per range
+        cost = tiles + seqs * p.Hkv * unit_cost;
+        X = tiles < p.ranges ? tiles : p.ranges;
+    }
+    __device__ __forceinline__ long long cut(int x) const { return dec8_div(x * cost, X); }
+    __device__ __forceinline__ int owner(long long at) const { return (int)(((at + 1) * X - 1) / cost); }
+};
+
+__device__ __forceinline__ int dec8_span(const DecodeFp8Params& p, int n) { return p.whole ? min(n, 1) : n; }
+
+// What the set-up leaves in shared memory.
+template <int THREADS>
+struct Dec8Setup {
+    long long sum[THREADS / 32];       // tiles and sequences of each warp's share
+    long long first;                   // cost before sequence b0
+    int b0;                            // the sequence that the range starts in
+};
+
+// The line, and the sequence that range x starts in.  All threads call it.
+template <int TILE, int THREADS>
+__device__ __forceinline__ Dec8Line dec8_line(const DecodeFp8Params& p, Dec8Setup<THREADS>& sh, int x)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.B + THREADS - 1) / THREADS;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    // tiles in the lower 44 bits (at most 2^25 a sequence), sequences that have any above
+    constexpr int shift = 44;
+    constexpr long long mask = (1LL << shift) - 1;
+    long long both = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int n = dec8_span(p, dec8_seq<TILE>(p, b).n);
+        both += n + ((long long)(n > 0) << shift);
+    }
+    long long inc = both;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) sh.sum[warp] = inc;
+    __syncthreads();
+    long long before2 = inc - both, total2 = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before2 += sh.sum[w];
+        total2 += sh.sum[w];
+    }
+    const long long mine = both & mask, seqs = both >> shift, before = before2 & mask, before_s = before2 >> shift;
+    const Dec8Line line(p, total2 & mask, total2 >> shift);
+    if (x < line.X) {
+        const long long at = line.cut(x);
+        long long s0 = (before + before_s * line.unit_cost) * p.Hkv;
+        if (s0 <= at && at < s0 + (mine + seqs * line.unit_cost) * p.Hkv)
+            for (int b = b0; b < b1; ++b) {
+                const int n = dec8_span(p, dec8_seq<TILE>(p, b).n);
+                const long long len = n > 0 ? (long long)(n + line.unit_cost) * p.Hkv : 0;
+                if (s0 <= at && at < s0 + len) {
+                    sh.b0 = b;
+                    sh.first = s0;
+                }
+                s0 += len;
+            }
+    }
+    __syncthreads();
+    return line;
+}
+
+// A CTA's walk over its range [a, e): unit (b, hk), which starts at s0 of the line, and the
+// unit's tiles that are this range's, [k0, k1).
+template <int TILE>
+struct Dec8Walk {
+    Dec8Seq seq;
+    long long a, e, s0;
+    int b, hk, span, unit_cost, k0, k1;
+    bool more;
+
+    template <int THREADS>
+    __device__ __forceinline__ Dec8Walk(const DecodeFp8Params& p, const Dec8Line& line, const Dec8Setup<THREADS>& sh, int x)
+        : a(line.cut(x)), e(line.cut(x + 1)), b(sh.b0), unit_cost(line.unit_cost)
+    {
+        seq = dec8_seq<TILE>(p, b);
+        span = dec8_span(p, seq.n);
+        hk = (int)dec8_div(a - sh.first, span + unit_cost);
+        s0 = sh.first + (long long)hk * (span + unit_cost);
+        take(p);
+        more = k1 > k0 || next(p);
+    }
+    __device__ __forceinline__ void take(const DecodeFp8Params& p)
+    {
+        k0 = (int)max(0LL, a - s0 - unit_cost);
+        k1 = (int)max((long long)k0, min((long long)span, e - s0 - unit_cost));
+        if (p.whole && k1 > k0) k1 = seq.n;
+    }
+    // to the next unit with tiles of this range; false, and the end of the walk, if there is none
+    __device__ __forceinline__ bool next(const DecodeFp8Params& p)
+    {
+        do {
+            s0 += span + unit_cost;
+            if (s0 + unit_cost >= e) return more = false;
+            if (++hk == p.Hkv) {
+                hk = 0;
+                do seq = dec8_seq<TILE>(p, ++b);
+                while (seq.n == 0);
+                span = dec8_span(p, seq.n);
+            }
+            take(p);
+        } while (k1 <= k0);
+        return more = true;
+    }
+    __device__ __forceinline__ bool whole() const { return k1 - k0 == seq.n; }
+    // the range that has the unit's last tile
+    __device__ __forceinline__ int last_owner(const Dec8Line& line) const { return line.owner(s0 + unit_cost + seq.n - 1); }
+};
+
+// What the combine kernel finds at the workspace's start: an entry per unit (and row group),
+// or where there are more units than CTAs one per CTA, for the one unit that it may begin and
+// not end.  (first range, last range, row group, first row), or a negative first range.
+__device__ __forceinline__ bool dec8_per_unit(const DecodeFp8Params& p)
+{
+    return (long long)p.B * p.Hkv * p.row_groups <= p.ranges * p.row_groups;
+}
+
+template <int TILE>
+__device__ __forceinline__ void dec8_name_parts(const DecodeFp8Params& p, const Dec8Walk<TILE>& w, const Dec8Line& line,
+                                                int x, int rg, size_t unit_row)
+{
+    if (w.k0 != 0 || p.whole) return;
+    const bool per_unit = dec8_per_unit(p);
+    if (!per_unit && w.whole()) return;
+    reinterpret_cast<int4*>(p.ws)[per_unit ? (w.b * p.Hkv + w.hk) * p.row_groups + rg : blockIdx.x] =
+        w.whole() ? make_int4(-1, 0, 0, 0) : make_int4(x, w.last_owner(line), rg, (int)unit_row);
+}
+
+// This CTA's part of the unit it is on.
+template <int ROWS, int D>
+__device__ __forceinline__ float* dec8_my_part(const DecodeFp8Params& p, bool first)
+{
+    return p.ws + 4 * (size_t)(p.ranges * p.row_groups) + (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * dec8_part(ROWS, D);
+}
+
+// Sequences without a key: O = 0, LSE = -inf, nothing to join.  The CTAs share them.
+template <int TILE, int D>
+__device__ __forceinline__ void dec8_write_empty(const DecodeFp8Params& p, int threads)
+{
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        if (dec8_seq<TILE>(p, b).n > 0) continue;
+        const size_t r0 = (size_t)b * p.Hkv * p.rows, rows = (size_t)p.Hkv * p.rows;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + r0 * D);
+        for (size_t i = threadIdx.x; i < rows * (D / 8); i += threads) o[i] = make_uint4(0, 0, 0, 0);
+        for (size_t i = threadIdx.x; i < rows; i += threads) p.lse[r0 + i] = -__int_as_float(0x7f800000);
+        if (dec8_per_unit(p))
+            for (int i = threadIdx.x; i < p.Hkv * p.row_groups; i += threads)
+                reinterpret_cast<int4*>(p.ws)[b * p.Hkv * p.row_groups + i] = make_int4(-1, 0, 0, 0);
+    }
+}
+
+// The value scale of 16 keys as f 2^e with e at most 60 below the largest so far (a scale of 0
+// has f = 0): 2^-e stays in range, and every key counts in the sum of weights.
+struct Dec8ValueScale {
+    float e, f, inv;   // exponent, factor, 2^-e
+    __device__ __forceinline__ Dec8ValueScale(float s, int& top)
+    {
+        const int x = min(max((int)((__float_as_uint(s) >> 23) & 0xFF) - 127, top - 60), 126);
+        top = max(top, x);
+        inv = __int_as_float((127 - x) << 23);
+        f = s * inv;
+        e = (float)x;
+    }
+};
+
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t dec8_half2(uint32_t two)   // codes in bits 0-15 -> f16x2, exact
+{
+    uint32_t h;
+    if constexpr (kE5M2) asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    else asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    return h;
+}
+
+// 0x80 in every byte of w whose code is not finite (E5M2: infinities too).
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t dec8_nonfinite(uint32_t w)
+{
+    return (kE5M2 ? (w & 0x7C7C7C7Cu) + 0x04040404u : (w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+__device__ __forceinline__ uint32_t dec8_pack_half2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint4 dec8_lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint2 dec8_lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ void dec8_timeout(const DecodeFp8Params& p, int* abort_flag)
+{
+    atomicExch(p.status, kStatusTimeout);
+    *reinterpret_cast<volatile int*>(abort_flag) = 1;
+}
+
+// Joins the parts of a unit that several ranges shared: with M the largest part maximum,
+// O = sum_x 2^(M_x - M) a_x / sum_x 2^(M_x - M) l_x.  grid.x: the units, or where there are
+// more of them the ranges (each leaves at most one unit to its successors); grid.y shares
+// a unit's rows and columns.  Latency-bound: a thread has all its parts' loads in flight
+// together.  Up to eight parts (the usual batch), a thread joins one float4 of one row;
+// more (one long sequence), 32 columns of a row at a time, sixteen threads a float4.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(const DecodeFp8Params p)
+{
+    constexpr int PART = dec8_part(ROWS, D);
+    constexpr int FEW = 8, MANY = 10;                        // parts of a thread
+    constexpr int COLS = 8, GROUPS = kD8CombineThreads / COLS, SLICES = D / 32;
+    __shared__ float4 sm_a[GROUPS][COLS];
+    __shared__ float2 sm_ml[GROUPS];
+    const float NEG_INF = -__int_as_float(0x7f800000);
+    const int tid = threadIdx.x, ctas = p.ranges * p.row_groups;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 todo = reinterpret_cast<const int4*>(p.ws)[blockIdx.x];
+    const int x0 = todo.x, x1 = min(todo.y, p.ranges - 1), rg = todo.z;
+    if (x0 < 0) return;
+    const size_t row0 = (size_t)todo.w;
+    const int rows = min(ROWS, p.rows - rg * ROWS);
+    auto part_of = [&](int x) {
+        return p.ws + 4 * ctas + (size_t)(2 * (x * p.row_groups + rg) + (x == x0 ? 1 : 0)) * PART;
+    };
+    auto finish = [&](int r, int col, float4 a, float sum, float M) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (row0 + r) * D)[col] =
+            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        if (col == 0)
+            p.lse[row0 + r] = sum == 0.0f ? NEG_INF : ((M == NEG_INF ? 0.0f : M) + __log2f(sum)) * 0.69314718055994531f;
+    };
+    // (M, l, a) += K parts x, x + step, ... up to x1, of row r
+    auto join = [&](auto K, int x, int step, int r, int col, float& M, float& l, float4& a) {
+        constexpr int k_parts = decltype(K)::value;
+        float m[k_parts], sum[k_parts];
+        float4 v[k_parts];
+#pragma unroll
+        for (int k = 0; k < k_parts; ++k) {
+            m[k] = NEG_INF;
+            if (x + k * step > x1) continue;
+            const float* w = part_of(x + k * step);
+            m[k] = w[ROWS * D + r];
+            sum[k] = w[ROWS * D + ROWS + r];
+            v[k] = *reinterpret_cast<const float4*>(w + r * D + col * 4);
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < k_parts; ++k) top = fmaxf(top, m[k]);
+        const float mb = top == NEG_INF ? 0.0f : top, f = ex2(M - mb);
+        M = top;
+        l *= f;
+        a.x *= f, a.y *= f, a.z *= f, a.w *= f;
+#pragma unroll
+        for (int k = 0; k < k_parts; ++k) {
+            if (x + k * step > x1) continue;
+            const float fac = ex2(m[k] - mb);
+            l = fmaf(fac, sum[k], l);
+            a.x = fmaf(fac, v[k].x, a.x), a.y = fmaf(fac, v[k].y, a.y);
+            a.z = fmaf(fac, v[k].z, a.z), a.w = fmaf(fac, v[k].w, a.w);
+        }
+    };
+    if (x1 - x0 < FEW) {
+        for (int i = blockIdx.y * kD8CombineThreads + tid; i < rows * (D / 4); i += gridDim.y * kD8CombineThreads) {
+            const int r = i / (D / 4), col = i - r * (D / 4);
+            float M = NEG_INF, l = 0.0f;
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            join(std::integral_constant<int, FEW>{}, x0, 1, r, col, M, l, a);
+            finish(r, col, a, l, M);
+        }
+        return;
+    }
+    const int grp = tid / COLS;
+    for (int i = blockIdx.y; i < rows * SLICES; i += gridDim.y) {
+        const int r = i / SLICES, col = (i - r * SLICES) * COLS + tid % COLS;
+        float M = NEG_INF, l = 0.0f;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int x = x0 + grp; x <= x1; x += GROUPS * MANY)
+            join(std::integral_constant<int, MANY>{}, x, GROUPS, r, col, M, l, a);
+        sm_a[grp][tid % COLS] = a;
+        if (tid % COLS == 0) sm_ml[grp] = make_float2(M, l);
+        __syncthreads();
+        if (tid < COLS) {
+            float top = NEG_INF, sum = 0.0f;
+            a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < GROUPS; ++k) top = fmaxf(top, sm_ml[k].x);
+            const float mb = top == NEG_INF ? 0.0f : top;
+#pragma unroll
+            for (int k = 0; k < GROUPS; ++k) {
+                const float4 v = sm_a[k][tid];
+                const float fac = ex2(sm_ml[k].x - mb);
+                sum = fmaf(fac, sm_ml[k].y, sum);
+                a.x = fmaf(fac, v.x, a.x), a.y = fmaf(fac, v.y, a.y);
+                a.z = fmaf(fac, v.z, a.z), a.w = fmaf(fac, v.w, a.w);
+            }
+            finish(r, col, a, sum, top);
+        }
+        __syncthreads();
+    }
+}
+
+// The joining launch of a main grid whose CTAs take ROWS rows.
+template <int D, int ROWS>
+cudaError_t launch_decode_fp8_combine(const DecodeFp8Params& p, cudaLaunchConfig_t& cfg)
+{
+    if (p.whole) return cudaSuccess;
+    // a unit's float4s over its CTAs, and four CTAs a part of the average unit while that is
+    // more, up to one for 32 columns of a row
+    const long long units = (long long)p.B * p.Hkv * p.row_groups, ctas = p.ranges * p.row_groups;
+    const int rows = p.rows < ROWS ? p.rows : ROWS, items = rows * (D / 32);
+    const int least = (rows * (D / 4) + kD8CombineThreads - 1) / kD8CombineThreads;
+    int share = units < ctas ? (int)(4 * ctas / units) : least;
+    share = share > items ? items : share < least ? least : share;
+    cfg.gridDim = dim3((unsigned)(units < ctas ? units : ctas), share);
+    cfg.blockDim = dim3(kD8CombineThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, decode_fp8_combine_kernel<D, ROWS>, p);
+}
+
+}  // namespace gb300
