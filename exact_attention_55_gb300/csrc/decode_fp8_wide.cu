@@ -275,38 +275,59 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
             constexpr bool kE5M2 = decltype(fmt)::value;
             constexpr int CPR = C::CB / 16;                      // chunks of a row in a column box
             const bool edge = is_v && (key0 + C::TILE > w.seq.L - p.nq + 1 || key0 < w.seq.lo + p.nq - 1);
+            constexpr int N = C::HALF / 16 / 128;                // chunks of a thread
+            // chunk i is (box, row, c); all of a thread's have the same c and, box aside, rows
+            // 128 / CPR apart, so that their swizzles agree
+            const int c = ct % CPR, first = ct / CPR;
+            constexpr int STEP = 128 / CPR, PER_BOX = C::TILE / STEP;
+            const int sw_in = C::CB == 128 ? c ^ (first & 7) : c ^ ((first >> 1) & 3);
+            const uint32_t in = from + first * C::CB + sw_in * 16;
+            uint4 u[N];
 #pragma unroll
-            for (int i = 0; i < C::HALF / 16 / 128; ++i) {
-                const int idx = i * 128 + ct, box = idx / (C::TILE * CPR), rem = idx - box * C::TILE * CPR;
-                const int row = rem / CPR, c = rem % CPR, dc = box * CPR + c;
-                const int sw = C::CB == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
-                uint4 u = dec8_lds128(from + box * C::TILE * C::CB + row * C::CB + sw * 16);
-                if (edge) {
-                    const int key = key0 + row;
-                    if (key >= w.seq.L || key < w.seq.lo) u = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < N; ++i)
+                u[i] = dec8_lds128(in + (i / PER_BOX) * C::TILE * C::CB + (i % PER_BOX) * STEP * C::CB);
+            if (edge) {
+#pragma unroll 1
+                for (int i = 0; i < N; ++i) {
+                    const int key = key0 + first + (i % PER_BOX) * STEP;
+                    uint4 v = u[0];
+#pragma unroll
+                    for (int k = 1; k < N; ++k)
+                        if (k == i) v = u[k];
+                    if (key >= w.seq.L || key < w.seq.lo) v = make_uint4(0, 0, 0, 0);
                     const int partly = dec8_partly(p, w.seq, key);
-                    if (partly >= 0 && (dec8_nonfinite<kE5M2>(u.x) | dec8_nonfinite<kE5M2>(u.y) |
-                                        dec8_nonfinite<kE5M2>(u.z) | dec8_nonfinite<kE5M2>(u.w))) {
+                    if (partly >= 0 && (dec8_nonfinite<kE5M2>(v.x) | dec8_nonfinite<kE5M2>(v.y) |
+                                        dec8_nonfinite<kE5M2>(v.z) | dec8_nonfinite<kE5M2>(v.w))) {
                         atomicOr(&sh->nan_keys[uc & 3], 1u << partly);
-                        u.x &= ~((dec8_nonfinite<kE5M2>(u.x) >> 7) * 0xFFu);
-                        u.y &= ~((dec8_nonfinite<kE5M2>(u.y) >> 7) * 0xFFu);
-                        u.z &= ~((dec8_nonfinite<kE5M2>(u.z) >> 7) * 0xFFu);
-                        u.w &= ~((dec8_nonfinite<kE5M2>(u.w) >> 7) * 0xFFu);
+                        v.x &= ~((dec8_nonfinite<kE5M2>(v.x) >> 7) * 0xFFu);
+                        v.y &= ~((dec8_nonfinite<kE5M2>(v.y) >> 7) * 0xFFu);
+                        v.z &= ~((dec8_nonfinite<kE5M2>(v.z) >> 7) * 0xFFu);
+                        v.w &= ~((dec8_nonfinite<kE5M2>(v.w) >> 7) * 0xFFu);
                     }
+#pragma unroll
+                    for (int k = 0; k < N; ++k)
+                        if (k == i) u[k] = v;
                 }
+            }
+            // the two fp16 chunks of code chunk dc = box CPR + c: block dc / 4, chunks 2 (dc % 4) + {0, 1}
+            const int second = C::CB == 128 ? (c >> 2) & 1 : 0;
+            const int q = (c % 4) * 2;
+            const uint32_t row_at = to + first * 128;
+            const uint32_t out0 = row_at + (((q + second) ^ (first & 7)) * 16) + (c / 4) * C::CBW;
+            const uint32_t out1 = row_at + (((q + (second ^ 1)) ^ (first & 7)) * 16) + (c / 4) * C::CBW;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
                 uint4 a, b;
-                a.x = dec8_half2<kE5M2>(u.x & 0xFFFF), a.y = dec8_half2<kE5M2>(u.x >> 16);
-                a.z = dec8_half2<kE5M2>(u.y & 0xFFFF), a.w = dec8_half2<kE5M2>(u.y >> 16);
-                b.x = dec8_half2<kE5M2>(u.z & 0xFFFF), b.y = dec8_half2<kE5M2>(u.z >> 16);
-                b.z = dec8_half2<kE5M2>(u.w & 0xFFFF), b.w = dec8_half2<kE5M2>(u.w >> 16);
-                const int second = C::CB == 128 ? (c >> 2) & 1 : 0;
-                const uint32_t line_at = to + (dc / 4) * C::CBW + row * 128;
+                a.x = dec8_half2<kE5M2>(u[i].x & 0xFFFF), a.y = dec8_half2<kE5M2>(u[i].x >> 16);
+                a.z = dec8_half2<kE5M2>(u[i].y & 0xFFFF), a.w = dec8_half2<kE5M2>(u[i].y >> 16);
+                b.x = dec8_half2<kE5M2>(u[i].z & 0xFFFF), b.y = dec8_half2<kE5M2>(u[i].z >> 16);
+                b.z = dec8_half2<kE5M2>(u[i].w & 0xFFFF), b.w = dec8_half2<kE5M2>(u[i].w >> 16);
                 const uint4 v0 = second ? b : a, v1 = second ? a : b;
-                const int q0 = (dc % 4) * 2 + second, q1 = (dc % 4) * 2 + (second ^ 1);
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(line_at + ((q0 ^ (row & 7)) * 16)),
-                             "r"(v0.x), "r"(v0.y), "r"(v0.z), "r"(v0.w) : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(line_at + ((q1 ^ (row & 7)) * 16)),
-                             "r"(v1.x), "r"(v1.y), "r"(v1.z), "r"(v1.w) : "memory");
+                const uint32_t at = (i / PER_BOX) * (CPR / 4) * C::CBW + (i % PER_BOX) * STEP * 128;
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(out0 + at), "r"(v0.x), "r"(v0.y), "r"(v0.z),
+                             "r"(v0.w) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(out1 + at), "r"(v1.x), "r"(v1.y), "r"(v1.z),
+                             "r"(v1.w) : "memory");
             }
         };
         while (w.more && ok) {
