@@ -7,11 +7,12 @@
 // From about 16 rows on the register products of that kernel, not the cache's bytes, set the
 // time (each 16 rows take the conversions and the tile's read again).  Here both products are
 // tcgen05.mma with M = 128 rows, so up to 128 rows cost one pass over the cache:
-//   * warp 8 streams K and V halves of a tile (128 keys; 64 at d = 256) through a TMA ring,
+//   * warp 12 streams K and V halves of a tile (128 keys; 64 at d = 256) through a TMA ring,
 //     the blocks' scales beside them by cp.async;
-//   * warps 4-7 convert a half's codes to fp16 (exact) into the K-major (K) or MN-major (V)
-//     swizzled operand, writing zeros for keys outside the sequence and the window;
-//   * warp 9 issues S = Q K^T and O += P V, with Q and P (fp16) read from tensor memory, so
+//   * warps 4-7 (K) and 8-11 (V) convert a half's codes to fp16 (exact) into the K-major (K)
+//     or MN-major (V) swizzled operand, with zeros for V outside the sequence and the window;
+//   * warps 13 and 14 issue S = Q K^T and O += P V (neither waits for the other's operands),
+//     with Q and P (fp16) read from tensor memory, so
 //     the products' shared-memory traffic is the tile alone: per 32 KB of codes 32 + 64 + 64 KB
 //     are read, written and read again, under the time that HBM takes to deliver them;
 //   * warps 0-3 own 32 rows each: softmax, P, rescaling of O when a maximum is passed by 2^8.
@@ -25,7 +26,12 @@
 namespace gb300 {
 
 constexpr float kD8WideTau = 8.0f;
-constexpr int kD8WideThreads = 320;
+constexpr int kD8WideThreads = 512;    // warpgroups: softmax, K converters, V converters, and the warps below
+constexpr int kD8WideProducer = 12, kD8WideMmaS = 13, kD8WideMmaPV = 14;
+// registers of a thread after the split; the block starts with 512 x 128 = 65536
+constexpr int kD8WideSoftmaxRegs = 208, kD8WideConvertRegs = 96, kD8WideControlRegs = 112;
+static_assert(128 * (kD8WideSoftmaxRegs + 2 * kD8WideConvertRegs + kD8WideControlRegs) <= 512 * 128,
+              "the split draws on the registers the block was launched with");
 
 template <int D, int COPIES>
 struct Dec8WideCfg {
@@ -58,7 +64,7 @@ struct alignas(16) Dec8WideShared {
     uint64_t sc_full[C::SC_RING], sc_empty[C::SC_RING];
     uint64_t k16_full[2], k16_empty[2], v16_full[2], v16_empty[2];
     uint64_t s_full[2], s_empty[2];
-    uint64_t q_full, q_empty, p_full, pv_done, o_empty, meet, drain;
+    uint64_t q_full, q_empty, p_full, pv_done, o_empty, meet, drain[2];
     float scale[C::SC_RING][2 * C::PARTS];
     float m[128], l[128];
     uint32_t nan_keys[4];              // per unit in flight: partly seen keys with a NaN value
@@ -117,7 +123,8 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
         mbar_init(smem_u32(&sh->pv_done), 1);
         mbar_init(smem_u32(&sh->o_empty), 4);
         mbar_init(smem_u32(&sh->meet), 4);
-        mbar_init(smem_u32(&sh->drain), 1);
+        mbar_init(smem_u32(&sh->drain[0]), 1);
+        mbar_init(smem_u32(&sh->drain[1]), 1);
         for (int s = 0; s < 4; ++s) sh->nan_keys[s] = 0;
         sh->abort_flag = 0;
         fence_mbar_init();
@@ -133,7 +140,7 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
         return;
     }
     Walk w(p, line, sh->setup, x);
-    if (warp == 9) {
+    if (warp == kD8WideMmaS) {
         tmem_alloc(smem_u32(&sh->tmem_base), C::TMEM_COLS);
         tmem_relinquish();
     }
@@ -152,7 +159,8 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(bar));
     };
 
-    if (warp == 8) {
+    if (warp >= kD8WideProducer) regs_decrease<kD8WideControlRegs>();
+    if (warp == kD8WideProducer) {
         // ------------------------------------------------------------ producer
         const uint64_t pol = l2_policy_evict_first();
         const int log2_r = p.log2_ps < 6 ? p.log2_ps : 6;       // rows per TMA box: a page, or 64
@@ -217,79 +225,93 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
-    } else if (warp == 9) {
-        // ------------------------------------------------------------ MMA issuer
-        constexpr uint32_t idesc_s = idesc_f32acc(0, 0, 128, C::TILE);   // fp16, K-major B
-        constexpr uint32_t idesc_o = idesc_f32acc(0, 1, 128, D);         // fp16, MN-major B
+    } else if (warp == kD8WideMmaS) {
+        // ------------------------------------------------------------ S(t) = Q K(t)^T
+        constexpr uint32_t idesc = idesc_f32acc(0, 0, 128, C::TILE);     // fp16, K-major B
         const uint64_t k_desc = sdesc_sw128(smem_u32(k16), 16, 1024);
-        const uint64_t v_desc = sdesc_sw128(smem_u32(v16), C::CBW, 1024);
-        uint32_t t = 0, uc = 0;                                  // tiles, units
+        uint32_t t = 0, uc = 0;
         while (w.more && ok) {
-            const int n = w.k1 - w.k0;
             if (!wait_all(&sh->q_full, uc & 1)) break;
-            for (int j = 0; j <= n && ok; ++j) {
-                if (j < n) {                                     // S(j) = Q K(j)^T
-                    const uint32_t i = t + j, slot = i & 1, sb = C::S_BUFS == 2 ? slot : 0;
-                    if (!wait_all(&sh->k16_full[slot], (i >> 1) & 1)) break;
-                    if (!wait_all(&sh->s_empty[sb], ((i / C::S_BUFS) & 1) ^ 1)) break;
-                    tc_fence_after_sync();
+            for (int k = w.k0; k < w.k1; ++k, ++t) {
+                const uint32_t slot = t & 1, sb = C::S_BUFS == 2 ? slot : 0;
+                if (!wait_all(&sh->k16_full[slot], (t >> 1) & 1)) break;
+                if (!wait_all(&sh->s_empty[sb], ((t / C::S_BUFS) & 1) ^ 1)) break;
+                tc_fence_after_sync();
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (slot * C::F16 + ((kk * 32) / 128) * C::CBW + (kk * 32) % 128) >> 4;
-                        mma_ts_warp<false>(tmem + sb * C::TILE, tmem + C::Q_COL + kk * 8, k_desc + off, idesc_s, kk > 0);
-                    }
-                    mma_commit_warp(smem_u32(&sh->s_full[sb]));
-                    mma_commit_warp(smem_u32(&sh->k16_empty[slot]));
-                    if (j == n - 1) mma_commit_warp(smem_u32(&sh->q_empty));
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (slot * C::F16 + ((kk * 32) / 128) * C::CBW + (kk * 32) % 128) >> 4;
+                    mma_ts_warp<false>(tmem + sb * C::TILE, tmem + C::Q_COL + kk * 8, k_desc + off, idesc, kk > 0);
                 }
-                if (j > 0) {                                     // O (+)= P(j-1) V(j-1)
-                    const uint32_t i = t + j - 1, slot = i & 1;
-                    if (!wait_all(&sh->v16_full[slot], (i >> 1) & 1)) break;
-                    if (!wait_all(&sh->p_full, i & 1)) break;
-                    if (j == 1 && !wait_all(&sh->o_empty, (uc & 1) ^ 1)) break;
-                    tc_fence_after_sync();
-#pragma unroll
-                    for (int kk = 0; kk < C::TILE / 16; ++kk)
-                        mma_ts_warp<false>(tmem + C::O_COL, tmem + C::P_COL + kk * 8,
-                                           v_desc + ((slot * C::F16 + kk * 16 * 128) >> 4), idesc_o, kk > 0 || j > 1);
-                    mma_commit_warp(smem_u32(&sh->pv_done));
-                    mma_commit_warp(smem_u32(&sh->v16_empty[slot]));
-                }
+                mma_commit_warp(smem_u32(&sh->s_full[sb]));
+                mma_commit_warp(smem_u32(&sh->k16_empty[slot]));
             }
             if (!ok) break;
-            t += n;
+            mma_commit_warp(smem_u32(&sh->q_empty));
             ++uc;
             w.next(p);
         }
         if (!ok && lane == 0) dec8_timeout(p, &sh->abort_flag);
-        mma_commit_warp(smem_u32(&sh->drain));
-        mbar_wait(smem_u32(&sh->drain), 0, nullptr, kCleanupTimeoutNs);
+        mma_commit_warp(smem_u32(&sh->drain[0]));
+        mbar_wait(smem_u32(&sh->drain[0]), 0, nullptr, kCleanupTimeoutNs);
         __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp == kD8WideMmaPV) {
+        // ------------------------------------------------------------ O (+)= P(t) V(t)
+        constexpr uint32_t idesc = idesc_f32acc(0, 1, 128, D);           // fp16, MN-major B
+        const uint64_t v_desc = sdesc_sw128(smem_u32(v16), C::CBW, 1024);
+        uint32_t t = 0, uc = 0;
+        while (w.more && ok) {
+            if (!wait_all(&sh->o_empty, (uc & 1) ^ 1)) break;            // the unit before has been read
+            for (int k = w.k0; k < w.k1; ++k, ++t) {
+                const uint32_t slot = t & 1;
+                if (!wait_all(&sh->v16_full[slot], (t >> 1) & 1)) break;
+                if (!wait_all(&sh->p_full, t & 1)) break;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int kk = 0; kk < C::TILE / 16; ++kk)
+                    mma_ts_warp<false>(tmem + C::O_COL, tmem + C::P_COL + kk * 8,
+                                       v_desc + ((slot * C::F16 + kk * 16 * 128) >> 4), idesc, kk > 0 || k > w.k0);
+                mma_commit_warp(smem_u32(&sh->pv_done));
+                mma_commit_warp(smem_u32(&sh->v16_empty[slot]));
+            }
+            if (!ok) break;
+            ++uc;
+            w.next(p);
+        }
+        if (!ok && lane == 0) dec8_timeout(p, &sh->abort_flag);
+        mma_commit_warp(smem_u32(&sh->drain[1]));
+        mbar_wait(smem_u32(&sh->drain[1]), 0, nullptr, kCleanupTimeoutNs);
+        __syncwarp();
+    } else if (warp >= 4 && warp < kD8WideProducer) {
         // ------------------------------------------------------------ converters
-        const int ct = threadIdx.x - 128;
-        uint32_t h = 0, t = 0, uc = 0;
-        // one half: code chunks of 16 to two fp16 chunks; eight lanes take the chunks of a row
-        // (two rows at d = 64), half of them their second chunk first: no bank conflicts
-        auto convert = [&](auto fmt, uint32_t from, uint32_t to, bool is_v, int key0) {
+        regs_decrease<kD8WideConvertRegs>();
+        const bool is_v = warp >= 8;                             // K halves, or V halves
+        const int ct = threadIdx.x & 127;
+        uint64_t* full16 = is_v ? sh->v16_full : sh->k16_full;
+        uint64_t* empty16 = is_v ? sh->v16_empty : sh->k16_empty;
+        const uint32_t to0 = smem_u32(is_v ? v16 : k16);
+        uint32_t h = is_v ? 1 : 0, t = 0, uc = 0;
+        // One half: chunks of 16 codes to two chunks of 8 fp16.  Eight lanes take four chunks of
+        // two rows, r and r ^ 5 (r and r + 1 at d = 64): under the 128-byte swizzles of both
+        // sides (64-byte at d = 64) they read and write all banks once.
+        auto convert = [&](auto fmt, uint32_t from, uint32_t to, int key0) {
             constexpr bool kE5M2 = decltype(fmt)::value;
-            constexpr int CPR = C::CB / 16;                      // chunks of a row in a column box
-            const bool edge = is_v && (key0 + C::TILE > w.seq.L - p.nq + 1 || key0 < w.seq.lo + p.nq - 1);
             constexpr int N = C::HALF / 16 / 128;                // chunks of a thread
-            // chunk i is (box, row, c); all of a thread's have the same c and, box aside, rows
-            // 128 / CPR apart, so that their swizzles agree
-            const int c = ct % CPR, first = ct / CPR;
-            constexpr int STEP = 128 / CPR, PER_BOX = C::TILE / STEP;
-            const int sw_in = C::CB == 128 ? c ^ (first & 7) : c ^ ((first >> 1) & 3);
-            const uint32_t in = from + first * C::CB + sw_in * 16;
+            const bool edge = is_v && (key0 + C::TILE > w.seq.L - p.nq + 1 || key0 < w.seq.lo + p.nq - 1);
+            // chunk i of the thread: quad i % Q of four chunks in row first + (i / Q) * 32
+            constexpr int Q = D / 64;
+            const int l5 = ct & 31, c = l5 & 3;
+            const int first = (ct >> 5) * 8 + (C::CB == 128 ? (l5 >> 3) ^ ((l5 & 4) ? 5 : 0) : l5 >> 2);
             uint4 u[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                u[i] = dec8_lds128(in + (i / PER_BOX) * C::TILE * C::CB + (i % PER_BOX) * STEP * C::CB);
+            for (int i = 0; i < N; ++i) {
+                const int quad = i % Q, row = first + (i / Q) * 32;
+                const int ch = C::CB == 128 ? ((quad & 1) * 4 + c) ^ (first & 7) : c ^ ((first >> 1) & 3);
+                u[i] = dec8_lds128(from + (quad >> 1) * C::TILE * C::CB + row * C::CB + ch * 16);
+            }
             if (edge) {
 #pragma unroll 1
                 for (int i = 0; i < N; ++i) {
-                    const int key = key0 + first + (i % PER_BOX) * STEP;
+                    const int key = key0 + first + (i / Q) * 32;
                     uint4 v = u[0];
 #pragma unroll
                     for (int k = 1; k < N; ++k)
@@ -309,51 +331,41 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                         if (k == i) u[k] = v;
                 }
             }
-            // the two fp16 chunks of code chunk dc = box CPR + c: block dc / 4, chunks 2 (dc % 4) + {0, 1}
-            const int second = C::CB == 128 ? (c >> 2) & 1 : 0;
-            const int q = (c % 4) * 2;
-            const uint32_t row_at = to + first * 128;
-            const uint32_t out0 = row_at + (((q + second) ^ (first & 7)) * 16) + (c / 4) * C::CBW;
-            const uint32_t out1 = row_at + (((q + (second ^ 1)) ^ (first & 7)) * 16) + (c / 4) * C::CBW;
+            // quad q of a row is the 128-byte fp16 block q, chunk c of it the chunks 2c and 2c + 1
+            const uint32_t out0 = to + first * 128 + (((2 * c) ^ (first & 7)) * 16);
+            const uint32_t out1 = to + first * 128 + (((2 * c + 1) ^ (first & 7)) * 16);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                uint4 a, b;
-                a.x = dec8_half2<kE5M2>(u[i].x & 0xFFFF), a.y = dec8_half2<kE5M2>(u[i].x >> 16);
-                a.z = dec8_half2<kE5M2>(u[i].y & 0xFFFF), a.w = dec8_half2<kE5M2>(u[i].y >> 16);
-                b.x = dec8_half2<kE5M2>(u[i].z & 0xFFFF), b.y = dec8_half2<kE5M2>(u[i].z >> 16);
-                b.z = dec8_half2<kE5M2>(u[i].w & 0xFFFF), b.w = dec8_half2<kE5M2>(u[i].w >> 16);
-                const uint4 v0 = second ? b : a, v1 = second ? a : b;
-                const uint32_t at = (i / PER_BOX) * (CPR / 4) * C::CBW + (i % PER_BOX) * STEP * 128;
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(out0 + at), "r"(v0.x), "r"(v0.y), "r"(v0.z),
-                             "r"(v0.w) : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(out1 + at), "r"(v1.x), "r"(v1.y), "r"(v1.z),
-                             "r"(v1.w) : "memory");
+                const uint32_t at = (i % Q) * C::CBW + (i / Q) * 32 * 128;
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(out0 + at),
+                             "r"(dec8_half2<kE5M2>(u[i].x & 0xFFFF)), "r"(dec8_half2<kE5M2>(u[i].x >> 16)),
+                             "r"(dec8_half2<kE5M2>(u[i].y & 0xFFFF)), "r"(dec8_half2<kE5M2>(u[i].y >> 16)) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(out1 + at),
+                             "r"(dec8_half2<kE5M2>(u[i].z & 0xFFFF)), "r"(dec8_half2<kE5M2>(u[i].z >> 16)),
+                             "r"(dec8_half2<kE5M2>(u[i].w & 0xFFFF)), "r"(dec8_half2<kE5M2>(u[i].w >> 16)) : "memory");
             }
         };
         while (w.more && ok) {
-            for (int k = w.k0; k < w.k1 && ok; ++k, ++t) {
+            for (int k = w.k0; k < w.k1; ++k, ++t, h += 2) {
+                const uint32_t slot = t & 1, s = h % C::RING;
+                if (!wait_all(&sh->kv_full[s], (h / C::RING) & 1)) break;
+                if (!wait_all(&empty16[slot], ((t >> 1) & 1) ^ 1)) break;
+                const uint32_t from = smem_u32(ring + s * C::HALF), to = to0 + slot * C::F16;
                 const int key0 = (w.seq.t0 + k) * C::TILE;
-                const uint32_t slot = t & 1, par = (t >> 1) & 1;
-#pragma unroll 1
-                for (int which = 0; which < 2; ++which, ++h) {
-                    const uint32_t s = h % C::RING;
-                    if (!wait_all(&sh->kv_full[s], (h / C::RING) & 1)) break;
-                    if (!wait_all(which ? &sh->v16_empty[slot] : &sh->k16_empty[slot], par ^ 1)) break;
-                    const uint32_t from = smem_u32(ring + s * C::HALF), to = smem_u32((which ? v16 : k16) + slot * C::F16);
-                    if (e5m2) convert(std::true_type{}, from, to, which != 0, key0);
-                    else convert(std::false_type{}, from, to, which != 0, key0);
-                    fence_proxy_async_smem();
-                    arrive(&sh->kv_empty[s]);
-                    arrive(which ? &sh->v16_full[slot] : &sh->k16_full[slot]);
-                }
+                if (e5m2) convert(std::true_type{}, from, to, key0);
+                else convert(std::false_type{}, from, to, key0);
+                fence_proxy_async_smem();
+                arrive(&sh->kv_empty[s]);
+                arrive(&full16[slot]);
             }
             if (!ok) break;
             ++uc;
             w.next(p);
         }
         if (!ok && lane == 0) dec8_timeout(p, &sh->abort_flag);
-    } else {
+    } else if (warp < 4) {
         // ------------------------------------------------------------ softmax, 32 rows a warp
+        regs_increase<kD8WideSoftmaxRegs>();
         constexpr int GROUPS = 4 / COPIES;                       // warps that hold the rows once
         const int copy = warp / GROUPS, row = (warp % GROUPS) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
@@ -423,49 +435,64 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                 const uint32_t sb = C::S_BUFS == 2 ? t & 1 : 0, sc = t % C::SC_RING;
                 if (!wait_all(&sh->s_full[sb], (t / C::S_BUFS) & 1)) break;
                 tc_fence_after_sync();
-                uint32_t sr[C::KEYS];
-                const uint32_t from = lanes + sb * C::TILE + copy * C::KEYS;
-                if constexpr (C::KEYS >= 32) {
+                const uint32_t from = lanes + sb * C::TILE + copy * C::KEYS, to = lanes + C::P_COL + copy * (C::KEYS / 2);
+                // scores in pieces of at most 64 keys; with 128 they are read once for the maximum
+                // and again for the weights
+                constexpr int PIECE = C::KEYS < 64 ? C::KEYS : 64, BLOCKS = C::KEYS / 16;
+                uint32_t sr[PIECE];
+                float* s = reinterpret_cast<float*>(sr);
+                auto load = [&](int at) {
+                    if constexpr (PIECE >= 32) {
 #pragma unroll
-                    for (int c = 0; c < C::KEYS / 32; ++c) tmem_ld32p(from + c * 32, sr + c * 32);
-                    tmem_wait_ld_only();
+                        for (int c = 0; c < PIECE / 32; ++c) tmem_ld32p(from + at + c * 32, sr + c * 32);
+                        tmem_wait_ld_only();
 #pragma unroll
-                    for (int c = 0; c < C::KEYS / 32; ++c) reg_fence32(sr + c * 32);
-                } else {
-                    tmem_ld16(from, sr);
-                    tmem_wait_ld16(sr);
+                        for (int c = 0; c < PIECE / 32; ++c) reg_fence32(sr + c * 32);
+                    } else {
+                        tmem_ld16(from + at, sr);
+                        tmem_wait_ld16(sr);
+                    }
+                };
+                load(0);
+                if constexpr (C::KEYS == PIECE) {
+                    tc_fence_before_sync();
+                    arrive(&sh->s_empty[sb]);
                 }
-                tc_fence_before_sync();
-                arrive(&sh->s_empty[sb]);
                 if (!wait_all(&sh->sc_full[sc], (t / C::SC_RING) & 1)) break;
                 const bool edge = key0 + C::KEYS - 1 > w.seq.L - p.nq ||
                                   (p.window > 0 && key0 < w.seq.L - 1 - p.window);
-                float* s = reinterpret_cast<float*>(sr);
-                float vf[C::KEYS / 16], vinv[C::KEYS / 16];
+                float kf[BLOCKS], ve[BLOCKS], vf[BLOCKS], vinv[BLOCKS];
 #pragma unroll
-                for (int b = 0; b < C::KEYS / 16; ++b) {
-                    float ks = sh->scale[sc][copy * (C::KEYS / 16) + b] * rowc;
-                    float vsc = sh->scale[sc][C::PARTS + copy * (C::KEYS / 16) + b];
+                for (int b = 0; b < BLOCKS; ++b) {
+                    kf[b] = sh->scale[sc][copy * BLOCKS + b] * rowc;
+                    float vsc = sh->scale[sc][C::PARTS + copy * BLOCKS + b];
                     if (edge) {
                         const int kb = key0 + b * 16;
-                        if (kb >= w.seq.L || kb + 15 < w.seq.lo) ks = vsc = 0.0f;   // nobody's: whatever its scales are
+                        if (kb >= w.seq.L || kb + 15 < w.seq.lo) kf[b] = vsc = 0.0f;   // nobody's: whatever its scales are
                     }
                     const Dec8ValueScale vs(vsc, v_top);
+                    ve[b] = vs.e;
                     vf[b] = vs.f;
                     vinv[b] = vs.inv;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[b * 16 + i] = fmaf(s[b * 16 + i], ks, vs.e);
                 }
                 arrive(&sh->sc_empty[sc]);
-                if (edge) {
+                auto scale_and_mask = [&](int at) {
 #pragma unroll
-                    for (int i = 0; i < C::KEYS; ++i)
-                        if (key0 + i > last || key0 + i < oldest) s[i] = NEG_INF;
+                    for (int i = 0; i < PIECE; ++i) s[i] = fmaf(s[i], kf[(at + i) / 16], ve[(at + i) / 16]);
+                    if (edge) {
+#pragma unroll
+                        for (int i = 0; i < PIECE; ++i)
+                            if (key0 + at + i > last || key0 + at + i < oldest) s[i] = NEG_INF;
+                    }
+                };
+                float mx = NEG_INF;
+#pragma unroll
+                for (int at = 0; at < C::KEYS; at += PIECE) {
+                    if (at > 0) load(at);
+                    scale_and_mask(at);
+#pragma unroll
+                    for (int i = 0; i < PIECE; i += 2) mx = fmax3(mx, s[i], s[i + 1]);
                 }
-                float mx = s[0];
-#pragma unroll
-                for (int i = 1; i + 1 < C::KEYS; i += 2) mx = fmax3(mx, s[i], s[i + 1]);
-                mx = fmaxf(mx, s[C::KEYS - 1]);
                 const bool raise = mx > m + kD8WideTau;
                 const float al = raise ? ex2(m - mx) : 1.0f;     // ex2(-inf) = 0
                 if (raise) {
@@ -490,27 +517,36 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                     }
                 }
 #pragma unroll
-                for (int b = 0; b < C::KEYS / 16; ++b) {
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float w0 = ex2(s[b * 16 + 2 * i] - mb), w1 = ex2(s[b * 16 + 2 * i + 1] - mb);
-                        sum += w0 + w1;
-                        sr[b * 8 + i] = dec8_pack_half2(w0 * vf[b], w1 * vf[b]);
+                for (int at = 0; at < C::KEYS; at += PIECE) {
+                    if constexpr (C::KEYS > PIECE) {
+                        load(at);
+                        scale_and_mask(at);
                     }
-                    l = fmaf(sum, vinv[b], l);
+#pragma unroll
+                    for (int b = 0; b < PIECE / 16; ++b) {
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float w0 = ex2(s[b * 16 + 2 * i] - mb), w1 = ex2(s[b * 16 + 2 * i + 1] - mb);
+                            sum += w0 + w1;
+                            sr[b * 8 + i] = dec8_pack_half2(w0 * vf[at / 16 + b], w1 * vf[at / 16 + b]);
+                        }
+                        l = fmaf(sum, vinv[at / 16 + b], l);
+                    }
+                    if constexpr (PIECE == 64) {
+                        tmem_st32p(to + at / 2, sr);
+                    } else if constexpr (PIECE == 32) {
+                        tmem_st16p(to, sr);
+                    } else {
+                        uint32_t f[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = sr[i];
+                        tmem_st8(to, f);
+                    }
                 }
-                const uint32_t to = lanes + C::P_COL + copy * (C::KEYS / 2);
-                if constexpr (C::KEYS >= 64) {
-#pragma unroll
-                    for (int c = 0; c < C::KEYS / 64; ++c) tmem_st32p(to + c * 32, sr + c * 32);
-                } else if constexpr (C::KEYS == 32) {
-                    tmem_st16p(to, sr);
-                } else {
-                    uint32_t f[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = sr[i];
-                    tmem_st8(to, f);
+                if constexpr (C::KEYS > PIECE) {
+                    tc_fence_before_sync();
+                    arrive(&sh->s_empty[sb]);
                 }
                 tmem_wait_st();
                 tc_fence_before_sync();
@@ -632,7 +668,7 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 9) tmem_dealloc(tmem, C::TMEM_COLS);
+    if (warp == kD8WideMmaS) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
 template <int D, int COPIES>
