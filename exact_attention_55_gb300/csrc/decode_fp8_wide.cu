@@ -45,7 +45,7 @@ struct Dec8WideCfg {
     static constexpr int F16 = 2 * HALF;                  // a half as fp16
     static constexpr int CBW = TILE * 128;                // 128-byte column block of an fp16 half
     static constexpr int PARTS = TILE / 16;               // 16-key parts, one scale each
-    static constexpr int SC_RING = 4;
+    static constexpr int SC_RING = 8;                     // tiles whose scales are held (see the producer)
     static constexpr int S_BUFS = D == 256 ? 1 : 2;
     static constexpr int Q_COL = S_BUFS * TILE;           // tensor memory: S, Q, P, O
     static constexpr int P_COL = Q_COL + D / 2;
@@ -61,7 +61,6 @@ template <int D, int COPIES>
 struct alignas(16) Dec8WideShared {
     using C = Dec8WideCfg<D, COPIES>;
     uint64_t kv_full[C::RING], kv_empty[C::RING];
-    uint64_t sc_full[C::SC_RING], sc_empty[C::SC_RING];
     uint64_t k16_full[2], k16_empty[2], v16_full[2], v16_empty[2];
     uint64_t s_full[2], s_empty[2];
     uint64_t q_full, q_empty, p_full, pv_done, o_empty, meet, drain[2];
@@ -102,12 +101,8 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::RING; ++s) {
-            mbar_init(smem_u32(&sh->kv_full[s]), 1);
+            mbar_init(smem_u32(&sh->kv_full[s]), 1 + 2 * C::PARTS);   // the bytes, lanes' scales
             mbar_init(smem_u32(&sh->kv_empty[s]), 4);
-        }
-        for (int s = 0; s < C::SC_RING; ++s) {
-            mbar_init(smem_u32(&sh->sc_full[s]), 2 * C::PARTS);
-            mbar_init(smem_u32(&sh->sc_empty[s]), 4);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sh->k16_full[s]), 4);
@@ -187,17 +182,6 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                 const int pg_box = __shfl_sync(0xffffffffu, pg, box0 - held + (lane & (nbox - 1)));
                 const int part_key = key0 + (lane & (C::PARTS - 1)) * 16;
                 const int pg_part = __shfl_sync(0xffffffffu, pg, (part_key >> log2_r) - held);
-                const uint32_t sc = t % C::SC_RING;
-                if (!wait_lane0(&sh->sc_empty[sc], ((t / C::SC_RING) & 1) ^ 1)) break;
-                if (lane < 2 * C::PARTS) {
-                    const size_t at = (((size_t)pg_part * p.Hkv + w.hk) << (p.log2_ps - p.log2_blk)) +
-                                      ((part_key & ps_mask) >> p.log2_blk);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n\t"
-                                 "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%2];" ::"r"(
-                                     smem_u32(&sh->scale[sc][lane])),
-                                 "l"((lane < C::PARTS ? p.ks : p.vs) + at), "r"(smem_u32(&sh->sc_full[sc]))
-                                 : "memory");
-                }
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {        // K, then V
                     const uint32_t s = h % C::RING;
@@ -205,6 +189,19 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                     const uint32_t fb = smem_u32(&sh->kv_full[s]);
                     if (lane == 0) mbar_arrive_expect_tx(fb, C::HALF);
                     __syncwarp();
+                    // The tile's scales complete on the barrier of its K half, so whoever has seen
+                    // S of the tile may read them.  Their place is free: the half that makes room
+                    // for this one was converted, so S two tiles after the one whose scales it
+                    // held (eight tiles back) has begun, and the softmax reads a tile's scales
+                    // before it gives up that tile's S.
+                    const size_t at = (((size_t)pg_part * p.Hkv + w.hk) << (p.log2_ps - p.log2_blk)) +
+                                      ((part_key & ps_mask) >> p.log2_blk);
+                    if (which == 0 && lane < 2 * C::PARTS)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                                         smem_u32(&sh->scale[t % C::SC_RING][lane])),
+                                     "l"((lane < C::PARTS ? p.ks : p.vs) + at) : "memory");
+                    if (lane < 2 * C::PARTS)
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
                     if (lane < nbox) {
                         const uint32_t dst = smem_u32(ring + s * C::HALF) + (lane << log2_r) * C::CB;
 #pragma unroll
@@ -454,11 +451,6 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                     }
                 };
                 load(0);
-                if constexpr (C::KEYS == PIECE) {
-                    tc_fence_before_sync();
-                    arrive(&sh->s_empty[sb]);
-                }
-                if (!wait_all(&sh->sc_full[sc], (t / C::SC_RING) & 1)) break;
                 const bool edge = key0 + C::KEYS - 1 > w.seq.L - p.nq ||
                                   (p.window > 0 && key0 < w.seq.L - 1 - p.window);
                 float kf[BLOCKS], ve[BLOCKS], vf[BLOCKS], vinv[BLOCKS];
@@ -475,10 +467,17 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                     vf[b] = vs.f;
                     vinv[b] = vs.inv;
                 }
-                arrive(&sh->sc_empty[sc]);
+                if constexpr (C::KEYS == PIECE) {
+                    tc_fence_before_sync();
+                    arrive(&sh->s_empty[sb]);
+                }
                 auto scale_and_mask = [&](int at) {
 #pragma unroll
-                    for (int i = 0; i < PIECE; ++i) s[i] = fmaf(s[i], kf[(at + i) / 16], ve[(at + i) / 16]);
+                    for (int i = 0; i < PIECE; i += 2) {
+                        const int b = (at + i) / 16;
+                        const float2 v = __ffma2_rn(make_float2(s[i], s[i + 1]), make_float2(kf[b], kf[b]), make_float2(ve[b], ve[b]));
+                        s[i] = v.x, s[i + 1] = v.y;
+                    }
                     if (edge) {
 #pragma unroll
                         for (int i = 0; i < PIECE; ++i)
@@ -524,14 +523,17 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                     }
 #pragma unroll
                     for (int b = 0; b < PIECE / 16; ++b) {
-                        float sum = 0.0f;
+                        float2 sum = make_float2(0.0f, 0.0f);
+                        const float2 down = make_float2(-mb, -mb), f = make_float2(vf[at / 16 + b], vf[at / 16 + b]);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float w0 = ex2(s[b * 16 + 2 * i] - mb), w1 = ex2(s[b * 16 + 2 * i + 1] - mb);
-                            sum += w0 + w1;
-                            sr[b * 8 + i] = dec8_pack_half2(w0 * vf[at / 16 + b], w1 * vf[at / 16 + b]);
+                            const float2 d = __fadd2_rn(make_float2(s[b * 16 + 2 * i], s[b * 16 + 2 * i + 1]), down);
+                            const float2 e = make_float2(ex2(d.x), ex2(d.y));
+                            sum = __fadd2_rn(sum, e);
+                            const float2 g = __fmul2_rn(e, f);
+                            sr[b * 8 + i] = dec8_pack_half2(g.x, g.y);
                         }
-                        l = fmaf(sum, vinv[at / 16 + b], l);
+                        l = fmaf(sum.x + sum.y, vinv[at / 16 + b], l);
                     }
                     if constexpr (PIECE == 64) {
                         tmem_st32p(to + at / 2, sr);
