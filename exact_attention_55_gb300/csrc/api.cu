@@ -1044,21 +1044,35 @@ struct DecodeFp8Plan {
     int cta_rows, ranges, row_groups;
 };
 
-static DecodeFp8Plan decode_fp8_plan(int rows, int d, int sm_count)
+static DecodeFp8Plan decode_fp8_plan(bool wide, int rows, int d, int sm_count)
 {
     DecodeFp8Plan plan;
-    plan.wide = rows > (d == 256 ? 8 : 16);
+    plan.wide = wide;
     int ctas;
-    if (plan.wide) {
+    if (wide) {
         plan.cta_rows = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
         ctas = sm_count;
     } else {
-        plan.cta_rows = rows <= 8 ? 8 : 16;
+        plan.cta_rows = rows <= 8 || d == 256 ? 8 : 16;
         ctas = (rows <= 8 && d <= 128 ? 3 : 2) * sm_count;
     }
     plan.row_groups = (rows + plan.cta_rows - 1) / plan.cta_rows;
     plan.ranges = ctas / plan.row_groups > 1 ? ctas / plan.row_groups : 1;
     return plan;
+}
+
+// The narrow kernel's time grows with its row groups (16 rows each; 8 at d = 256), the wide
+// one's hardly with the rows, but it starts and ends later by what about 16 tiles of 64 keys
+// per SM cost.  `keys`: the most a sequence of the step can have.  Measured narrow against
+// wide, 8 key heads, us: d 128, 32 rows, 2 x 4096 keys 18.8 / 21.4, 4 x 4096 21.5 / 22.2,
+// 8 x 4096 33.0 / 30.4, 16 x 8192 102 / 69; 48 rows, 2 x 4096 18.4 / 24.0, 4 x 4096
+// 27.2 / 23.5; d 256, 16 rows, 16 x 8192 116 / 118, 32 rows 219 / 126.
+static bool decode_fp8_is_wide(int rows, int d, long long heads, long long keys, int sm_count)
+{
+    if (rows <= 16) return false;
+    const long long tiles = heads * ((keys + 63) / 64);
+    const int groups = (rows + (d == 256 ? 7 : 15)) / (d == 256 ? 8 : 16);
+    return d == 256 ? tiles * (groups - 2) >= 27LL * sm_count : tiles * (groups - 1) >= 16LL * sm_count;
 }
 
 static size_t decode_fp8_ws_bytes(const DecodeFp8Plan& plan, int d)
@@ -1073,7 +1087,12 @@ extern "C" size_t attn_decode_fp8_workspace_bytes(int H, int Hkv, int nq, int d)
     if (d != 64 && d != 128 && d != 256) return 0;
     DeviceInfo* dev = nullptr;
     if (H / Hkv > 0x7fffffff / 8 || device_info(&dev) != ATTN_OK) return 0;
-    return decode_fp8_ws_bytes(decode_fp8_plan(H / Hkv * nq, d, dev->sm_count), d);
+    // whichever kernel a call will take
+    const int rows = H / Hkv * nq;
+    const size_t narrow = decode_fp8_ws_bytes(decode_fp8_plan(false, rows, d, dev->sm_count), d);
+    if (rows <= 16) return narrow;
+    const size_t wide = decode_fp8_ws_bytes(decode_fp8_plan(true, rows, d, dev->sm_count), d);
+    return narrow > wide ? narrow : wide;
 }
 
 extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cache,
@@ -1106,7 +1125,10 @@ extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cach
     const attn_status_t st = device_info(&dev);
     if (st != ATTN_OK) return st;
     const int rows = H / Hkv * nq;
-    const DecodeFp8Plan plan = decode_fp8_plan(rows, d, dev->sm_count);
+    long long keys = (long long)max_pages * page_size;
+    if (window > 0 && (long long)window + nq < keys) keys = (long long)window + nq;
+    const bool wide = decode_fp8_is_wide(rows, d, (long long)B * Hkv, keys, dev->sm_count);
+    const DecodeFp8Plan plan = decode_fp8_plan(wide, rows, d, dev->sm_count);
     if (decode_fp8_ws_bytes(plan, d) > (workspace ? workspace_bytes : 0))
         return ATTN_ERR_INVALID_ARG;
     // the caches as (d, page_size, pages * Hkv), boxes of one page or 64 rows of a larger one

@@ -451,8 +451,11 @@ attn_status_t attn_cache_append_fp8(const void* k, const void* v, void* k_cache,
  *                not matter.  Calls that may overlap need one each.
  * What the cache holds at keys a query does not see (rows behind the sequence, pages
  * behind it or before its window) never reaches that query's outputs, NaN codes and
- * scales included.  The queries and the codes enter the products exactly; scores, sums and
- * O are fp32, the weights of the second product are rounded to fp16.
+ * scales included (an E5M2 code of infinity in V counts as NaN at keys that only some of
+ * the queries see).  The queries and the codes enter the products exactly; scores, sums and O
+ * are fp32, the weights of the second product (softmax times V scale, relative to the row's
+ * largest) are rounded to fp16.  A V scale below 2^-60 of the sequence's largest, or of 1,
+ * counts as that in "largest": only a softmax that sits on such blocks loses digits of O.
  * HBM-bound: every key and value code that a query sees is read once per call.
  */
 size_t attn_decode_fp8_workspace_bytes(int H, int Hkv, int nq, int d);

@@ -103,7 +103,12 @@ def decode_fp8(q, kc, vc, ks, vs, table, lens, fmt, scale, window=0):
         ds = d 2^-23 max_j scale ks_j sum|q k8| + 2^-21 (1 + max|s|)
         moves a weight by ds and the normalised result by 2 ds;
       weights in fp16: half a step, 2^-11 of each, and below fp16's normal numbers
-        2^-25 of the largest weight (times 2, as a scale's mantissa is split off);
+        2^-25 of the largest weight (times 2, as a scale's mantissa is split off).  The
+        kernels take weights relative to max_j p_j 2^e_j, where e_j is the exponent of vs_j
+        but at least 60 below that of the largest scale (and of 1), so that a block with the
+        scale 0 still counts in the sum; the largest weight is therefore
+        max_j p_j max(vs_j, 2^-60 max(1, largest vs)), not max_j p_j vs_j: a row whose softmax
+        sits on blocks of scale 0 has its fp16 step there;
       sums of n weights in fp32 by 16s: 2^-22 n / 16;
       O in bf16: 2^-8 of the value.
     """
@@ -140,8 +145,9 @@ def decode_fp8(q, kc, vc, ks, vs, table, lens, fmt, scale, window=0):
                 n = last + 1 - first
                 w = p * vsc[j]
                 avg = w @ np.abs(V8[j])
+                w_max = (p * np.maximum(vsc[j], 2.0 ** -60 * max(1.0, vsc[j].max()))).max()
                 o_tol[b, h, i] = (2.0 ** -8 * np.abs(o[b, h, i]) + avg * (2.0 ** -11 + 2 * ds + 2.0 ** -22 * n / 16)
-                                  + 2.0 ** -24 * w.max() * np.abs(V8[j]).sum(0) + 1e-30)
+                                  + 2.0 ** -24 * w_max * np.abs(V8[j]).sum(0) + 1e-30)
                 lse_tol[b, h, i] = ds + 2.0 ** -22 * (n / 16 + abs(lse[b, h, i]))
     return o, lse, o_tol, lse_tol
 

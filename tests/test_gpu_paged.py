@@ -227,9 +227,21 @@ def test_append_fp8_unusual_values(fa, fmt):
 
 
 # ------------------------------------------------------------------ decoding
-def check_decode(fa, lens, H, Hkv, nq, d, ps, block, fmt, window=0, seed=0, qmul=1.0, stale=True, scale=None):
+# Many query rows under one key head go to a kernel of their own (tcgen05) once the step is
+# large; how large it is follows from the table's width, so a table of this many keys, most of
+# its entries unused, brings short sequences there too.
+WIDE_TABLE = 1 << 18
+
+
+def widen(table, ps, keys=WIDE_TABLE):
+    return np.concatenate([table, np.full((len(table), keys // ps), -1, np.int32)], 1)
+
+
+def check_decode(fa, lens, H, Hkv, nq, d, ps, block, fmt, window=0, seed=0, qmul=1.0, stale=True, scale=None, wide=False):
     rng = np.random.default_rng(seed)
     kc, vc, ks, vs, table = ref.make_cache(rng, lens, Hkv, d, ps, block, fmt, stale=stale)
+    if wide:
+        table = widen(table, ps)
     q = (torch.from_numpy(rng.standard_normal((len(lens), H, nq, d)).astype(np.float32)) * qmul).bfloat16()
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     o, lse = fa.attn_decode_fp8_paged(q.cuda(), cuda(kc), cuda(vc), cuda(ks), cuda(vs), cuda(table),
@@ -293,6 +305,72 @@ def test_decode_fp8_window(fa, window, nq):
 def test_decode_fp8_many_query_heads(fa, rows, d):
     """One key head under any number of query heads."""
     check_decode(fa, [300, 64, 5], rows, 1, 1, d, 64, 64, "e4m3", seed=rows)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [17, 31, 32, 33, 64, 65, 100, 128, 129, 300])
+def test_decode_fp8_wide_rows(fa, rows, d):
+    """The kernel for many rows: 32, 64 and 128 rows a CTA, more in groups, some not full."""
+    check_decode(fa, [300, 0, 64, 5, 1], rows, 1, 1, d, 64, 64, "e4m3", seed=rows, wide=True)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("nq,group", [(1, 20), (2, 16), (3, 16), (4, 8), (8, 5), (8, 16)])
+def test_decode_fp8_wide(fa, d, fmt, nq, group):
+    check_decode(fa, LENS + [1000], 2 * group, 2, nq, d, 32, 16, fmt, seed=d + nq, wide=True)
+
+
+@pytest.mark.parametrize("ps,block", [(16, 16), (64, 16), (128, 128), (256, 64), (1024, 128)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_decode_fp8_wide_page_sizes(fa, ps, block, d):
+    check_decode(fa, [700, 33, 1025, 0, 1], 3 * 12, 3, 2, d, ps, block, "e4m3", seed=ps + block, wide=True)
+
+
+@pytest.mark.parametrize("window", [1, 16, 100, 127, 500])
+@pytest.mark.parametrize("nq,group", [(1, 32), (4, 16), (8, 16)])
+def test_decode_fp8_wide_window(fa, window, nq, group):
+    """Windows in the kernel for many rows (enough sequences for it), freed pages before them."""
+    B, d, ps, block = 60, 64, 32, 16
+    rng = np.random.default_rng(window + nq)
+    lens = [int(n) for n in rng.integers(0, 900, B)]
+    heads = -(-2432 // (B * -(-(window + nq) // 64) * (nq * group // 16 - 1)))
+    kc, vc, ks, vs, table = ref.make_cache(rng, lens, heads, d, ps, block, "e4m3")
+    for b, L in enumerate(lens):
+        lo = max(0, L - nq - window)
+        for t in range(lo):
+            kc[table[b, t // ps], :, t % ps], vc[table[b, t // ps], :, t % ps] = 0x7F, 0xFF
+        for blk in range(lo // block):
+            ks[table[b, blk * block // ps], :, blk % (ps // block)] = np.nan
+            vs[table[b, blk * block // ps], :, blk % (ps // block)] = np.inf
+        table[b, :lo // ps] = -1
+    q = torch.from_numpy(rng.standard_normal((B, heads * group, nq, d)).astype(np.float32)).bfloat16()
+    o, lse = fa.attn_decode_fp8_paged(q.cuda(), cuda(kc), cuda(vc), cuda(ks), cuda(vs), cuda(table),
+                                      cuda(np.array(lens, np.int32)), scale=0.125, window=window)
+    assert fa.attn_get_device_status() == fa.ATTN_OK
+    some = sorted(set(rng.integers(0, B, 12).tolist()) | {int(np.argmin(lens))})   # the reference is slow
+    hs = [0, heads * group - 1, group // 2]
+    kv = [0, heads - 1]
+    want = [ref.decode_fp8(q[some][:, [h]].double().numpy(), kc[:, [h // group]], vc[:, [h // group]],
+                           ks[:, [h // group]], vs[:, [h // group]], table[some], [lens[b] for b in some],
+                           "e4m3", 0.125, window) for h in hs]
+    assert kv[0] == hs[0] // group and kv[1] == hs[1] // group
+    for h, w in zip(hs, want):
+        compare_decode(o[some][:, [h]], lse[some][:, [h]], w)
+
+
+def test_decode_fp8_wide_short_tables(fa):
+    """Many short sequences under many rows: no head is split, nothing is joined."""
+    rng = np.random.default_rng(30)
+    lens = [int(n) for n in rng.integers(0, 385, 40)]
+    check_decode(fa, lens, 64, 4, 8, 64, 64, 64, "e4m3", seed=31)
+
+
+def test_decode_fp8_wide_long(fa):
+    """Parts of long and short sequences, several CTAs on each, joined."""
+    check_decode(fa, [20001, 3, 7000, 1, 129], 32, 1, 1, 128, 64, 64, "e4m3_pow2", seed=32, wide=True)
+    check_decode(fa, [9000], 20, 1, 4, 256, 128, 128, "e5m2", seed=33, wide=True)
+    check_decode(fa, [5000] * 3, 64, 2, 1, 64, 16, 16, "e4m3", seed=34, wide=True)
 
 
 def test_decode_fp8_long_and_ragged(fa):
@@ -410,18 +488,22 @@ def test_append_of_nothing(fa):
 
 
 @pytest.mark.parametrize("qmul", [0.0, 1e-30, 1e-4, 300.0, 1e30])
-def test_decode_fp8_query_magnitudes(fa, qmul):
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_fp8_query_magnitudes(fa, qmul, wide):
     """Queries far outside fp16's range keep their scores (softmax scale chosen to match)."""
-    check_decode(fa, [100, 17], 4, 2, 2, 128, 32, 32, "e4m3", qmul=qmul, seed=14,
-                 scale=0.1 / max(qmul, 1e-30) if qmul else 0.1)
+    check_decode(fa, [100, 17], 48 if wide else 4, 2, 2, 128, 32, 32, "e4m3", qmul=qmul, seed=14,
+                 scale=0.1 / max(qmul, 1e-30) if qmul else 0.1, wide=wide)
 
 
-def test_decode_fp8_query_rows_of_mixed_magnitude(fa):
+@pytest.mark.parametrize("H", [4, 40])
+def test_decode_fp8_query_rows_of_mixed_magnitude(fa, H):
     """Within a row: values down to 2^-20 of the row's largest still count."""
     rng = np.random.default_rng(15)
     d, lens = 128, [200]
     kc, vc, ks, vs, table = ref.make_cache(rng, lens, 1, d, 32, 32, "e4m3")
-    q = rng.standard_normal((1, 4, 1, d)).astype(np.float32)
+    if H > 16:
+        table = widen(table, 32)
+    q = rng.standard_normal((1, H, 1, d)).astype(np.float32)
     q[..., 1:] *= np.exp2(-rng.integers(0, 21, d - 1)).astype(np.float32)
     q = torch.from_numpy(q).bfloat16()
     o, lse = fa.attn_decode_fp8_paged(q.cuda(), cuda(kc), cuda(vc), cuda(ks), cuda(vs), cuda(table),
@@ -429,16 +511,19 @@ def test_decode_fp8_query_rows_of_mixed_magnitude(fa):
     compare_decode(o, lse, ref.decode_fp8(q.double().numpy(), kc, vc, ks, vs, table, lens, "e4m3", 0.3))
 
 
-def test_decode_fp8_scales_far_apart(fa):
+@pytest.mark.parametrize("H", [4, 40, 200])
+def test_decode_fp8_scales_far_apart(fa, H):
     """Blocks whose scales lie 2^40 apart, zero scales among them, in K and in V."""
     rng = np.random.default_rng(16)
     d, lens, fmt = 64, [300, 70], "e4m3"
     kc, vc, ks, vs, table = ref.make_cache(rng, lens, 2, d, 32, 16, fmt)
+    if H > 16:
+        table = widen(table, 32)
     ks[:], vs[:] = np.nan_to_num(ks, nan=0.01), np.nan_to_num(vs, nan=0.01)
     vs *= np.exp2(rng.integers(-20, 21, vs.shape)).astype(np.float32)
     vs[rng.random(vs.shape) < 0.2] = 0
     ks[rng.random(ks.shape) < 0.2] = 0
-    q = torch.from_numpy(rng.standard_normal((2, 4, 1, d)).astype(np.float32)).bfloat16()
+    q = torch.from_numpy(rng.standard_normal((2, H, 1, d)).astype(np.float32)).bfloat16()
     o, lse = fa.attn_decode_fp8_paged(q.cuda(), cuda(kc), cuda(vc), cuda(ks), cuda(vs), cuda(table),
                                       cuda(np.array(lens, np.int32)), scale=0.125)
     compare_decode(o, lse, ref.decode_fp8(q.double().numpy(), kc, vc, ks, vs, table, lens, fmt, 0.125))
@@ -446,17 +531,20 @@ def test_decode_fp8_scales_far_apart(fa):
 
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_decode_fp8_nan_at_a_key_only_later_queries_see(fa, fmt, d):
+@pytest.mark.parametrize("H", [2, 10, 20, 40])
+def test_decode_fp8_nan_at_a_key_only_later_queries_see(fa, fmt, d, H):
     """A NaN value at the newest token reaches the last query alone (and there only its own
     coordinate); a NaN key reaches every query that sees it."""
     rng = np.random.default_rng(17)
     lens, nq, ps = [70, 64], 3, 32
     kc, vc, ks, vs, table = ref.make_cache(rng, lens, 1, d, ps, 32, fmt)
+    if H > 2:
+        table = widen(table, ps)
     clean = (vc.copy(), kc.copy())
     for b, L in enumerate(lens):
         vc[table[b, (L - 1) // ps], 0, (L - 1) % ps, 7] = 0x7F
     kc[table[1, (lens[1] - 2) // ps], 0, (lens[1] - 2) % ps, 3] = 0xFF
-    q = torch.from_numpy(rng.standard_normal((2, 2, nq, d)).astype(np.float32)).bfloat16()
+    q = torch.from_numpy(rng.standard_normal((2, H, nq, d)).astype(np.float32)).bfloat16()
     o, lse = fa.attn_decode_fp8_paged(q.cuda(), cuda(kc), cuda(vc), cuda(ks), cuda(vs), cuda(table),
                                       cuda(np.array(lens, np.int32)), fmt=fmt, scale=0.1)
     want = ref.decode_fp8(q.double().numpy(), clean[1], clean[0], ks, vs, table, lens, fmt, 0.1)
@@ -603,9 +691,11 @@ def test_calls_on_other_streams(fa):
     takes the stream it is given."""
     rng = np.random.default_rng(22)
     cases = []
-    for seed, (H, Hkv, d) in enumerate([(4, 2, 64), (8, 1, 128), (3, 3, 256)]):
+    for seed, (H, Hkv, d) in enumerate([(4, 2, 64), (8, 1, 128), (3, 3, 256), (40, 1, 128)]):
         lens = [3000, 17, 900]
         kc, vc, ks, vs, table = ref.make_cache(rng, lens, Hkv, d, 32, 32, "e4m3")
+        if H > 16:
+            table = widen(table, 32)
         q = torch.randn(3, H, 1, d, generator=torch.Generator().manual_seed(seed)).bfloat16()
         cases.append([t.cuda() if isinstance(t, torch.Tensor) else cuda(t)
                       for t in (q, kc, vc, ks, vs, table, np.array(lens, np.int32))])
