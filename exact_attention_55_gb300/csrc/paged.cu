@@ -11,6 +11,7 @@
 
 #include <cstdint>
 
+#include "fp8_scale.cuh"
 #include "paged_params.h"
 #include "ptx.cuh"
 

@@ -466,27 +466,4 @@ __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi)
     return r;
 }
 
-// RN(x / s) for two values at once, s > 0 finite and the quotients normal, from
-// y = RN(1/s) and s_neg = -s: q = RN(x y), r = x - q s (exact), RN(q + r y).
-__device__ __forceinline__ float2 div2_by_scale(float2 x, float2 s_neg, float2 y)
-{
-    const float2 q = __fmul2_rn(x, y);
-    const float2 r = __ffma2_rn(q, s_neg, x);  // x - q s, exact
-    const float2 c = __ffma2_rn(r, y, q);
-    // c equals q when r == 0, except that q = -0 (x = -0) would come back as +0;
-    // the quotient's sign is x's in every case
-    return make_float2(copysignf(c.x, x.x), copysignf(c.y, x.y));
-}
-
-// The smallest power of two >= s (s > 0 finite), normal or subnormal.
-__device__ __forceinline__ float pow2_at_least(float s)
-{
-    const uint32_t b = __float_as_uint(s);
-    if ((b & 0x7F800000u) == 0) {  // subnormal: 2^k >= m * 2^-149 from m's highest bit
-        const uint32_t m = b & 0x7FFFFFu;
-        return __uint_as_float((m & (m - 1)) == 0 ? m : (1u << (32 - __clz(m))));
-    }
-    return (b & 0x7FFFFFu) == 0 ? s : __uint_as_float((b & 0x7F800000u) + 0x00800000u);
-}
-
 }  // namespace gb300

@@ -45,6 +45,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_params.h"
+#include "fp8_scale.cuh"
 #include "ptx.cuh"
 
 namespace gb300 {
@@ -76,6 +77,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
             dst),
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
+}
+
+// RN(x / s) for two values at once, s > 0 finite and the quotients normal, from
+// y = RN(1/s) and s_neg = -s: q = RN(x y), r = x - q s (exact), RN(q + r y).
+__device__ __forceinline__ float2 div2_by_scale(float2 x, float2 s_neg, float2 y)
+{
+    const float2 q = __fmul2_rn(x, y);
+    const float2 r = __ffma2_rn(q, s_neg, x);  // x - q s, exact
+    const float2 c = __ffma2_rn(r, y, q);
+    // c equals q when r == 0, except that q = -0 (x = -0) would come back as +0;
+    // the quotient's sign is x's in every case
+    return make_float2(copysignf(c.x, x.x), copysignf(c.y, x.y));
 }
 
 // a + b and a - b of two pairs, each rounded once (a - b as fma(b, -1, a)).
