@@ -41,7 +41,6 @@
 
 namespace gb300 {
 
-constexpr int kD8Tile = 64;            // keys of a tile, 16 per consumer warp
 constexpr int kD8Warps = 4;            // consumer warps
 constexpr int kD8Threads = (kD8Warps + 1) * 32;
 constexpr float kD8Tau = 8.0f;         // the running maximum is raised when passed by this (log2)
@@ -51,7 +50,9 @@ struct Dec8Cfg {
     static constexpr int ROWS = 8 * NT;                   // query rows of a CTA
     static constexpr int CB = D < 128 ? D : 128;          // bytes of a row in one TMA box
     static constexpr int NCB = D / CB;                    // column boxes of a row
-    static constexpr int HALF = kD8Tile * D;              // K or V of a tile
+    static constexpr int G = D == 64 ? 2 : 1;             // 16-key groups of a warp in a tile
+    static constexpr int TILE = 64 * G;                   // keys of a tile
+    static constexpr int HALF = TILE * D;                 // K or V of a tile
     static constexpr int STAGE = 2 * HALF;
     static constexpr bool Q_REGS = NT * D <= 128;         // query fragments held in registers
     static constexpr int Q_FRAGS = NT * (D / 16) * 32;    // 8 bytes each, two heads' worth
@@ -62,7 +63,7 @@ struct Dec8Cfg {
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
     static_assert(STAGES >= 2, "ring");
-    static_assert(STAGE == kD8Warps * 8 * D * 4, "a head's last stage holds the warps' O for joining");
+    static_assert(STAGE >= kD8Warps * 8 * D * 4, "a head's last stage holds the warps' O for joining");
 };
 
 template <int D, int NT>
@@ -71,7 +72,7 @@ struct alignas(16) Dec8Shared {
     uint64_t full[C::STAGES], empty[C::STAGES];
     uint64_t q_full[2], q_empty[2];
     uint64_t meet;                     // the consumer warps' barrier
-    float scale[C::STAGES][8];         // K scales of the tile's four 16-key parts, then V's
+    float scale[C::STAGES][8 * C::G];  // K scales of the tile's 16-key parts, then V's
     float rowc[2][C::ROWS];            // per query row: softmax scale over its fragments' factor
     float m[kD8Warps][C::ROWS], l[kD8Warps][C::ROWS];
     Dec8Setup<kD8Threads> setup;
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(smem_u32(&sh->full[s]), 9);        // lane 0's bytes, eight lanes' scales
+            mbar_init(smem_u32(&sh->full[s]), 1 + 8 * C::G);   // lane 0's bytes, lanes' scales
             mbar_init(smem_u32(&sh->empty[s]), kD8Warps);
         }
         for (int s = 0; s < 2; ++s) {
@@ -128,19 +129,19 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
     asm volatile("griddepcontrol.wait;" ::: "memory");   // what ran before has written its results
     if (threadIdx.x == 0 && !dec8_per_unit(p)) reinterpret_cast<int4*>(p.ws)[blockIdx.x] = make_int4(-1, 0, 0, 0);
     const int x = blockIdx.x / p.row_groups, rg = blockIdx.x - x * p.row_groups, row0 = rg * C::ROWS;
-    const Dec8Line line = dec8_line<kD8Tile>(p, sh->setup, x);
+    const Dec8Line line = dec8_line<C::TILE>(p, sh->setup, x);
     if (x >= line.X) {
-        dec8_write_empty<kD8Tile, D>(p, kD8Threads);
+        dec8_write_empty<C::TILE, D>(p, kD8Threads);
         return;
     }
-    Dec8Walk<kD8Tile> w(p, line, sh->setup, x);
+    Dec8Walk<C::TILE> w(p, line, sh->setup, x);
 
     if (warp == kD8Warps) {
         // ------------------------------------------------------------ producer
         const uint64_t pol = l2_policy_evict_first();
         const int g = lane >> 2, t = lane & 3;
         const int log2_r = p.log2_ps < 6 ? p.log2_ps : 6;       // rows per TMA box: a page, or 64
-        const int nbox = kD8Tile >> log2_r;
+        const int nbox = C::TILE >> log2_r;
         const int ps_mask = (1 << p.log2_ps) - 1;
         int stage = 0, filled = 0, q_slot = 0;
         uint32_t parity = 1, q_parity = 1;
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
             const int* ptab = p.page_table + (size_t)w.b * p.max_pages;
             int held = 0, pg = 0;                                // 32 boxes' pages from box `held` on
             for (int k = w.k0; k < w.k1 && ok; ++k) {
-                const int key0 = (w.seq.t0 + k) * kD8Tile, box0 = key0 >> log2_r;
+                const int key0 = (w.seq.t0 + k) * C::TILE, box0 = key0 >> log2_r;
                 if (k == w.k0 || box0 - held >= 32) {
                     held = box0;
                     const long long key = (long long)(box0 + lane) << log2_r;
@@ -184,24 +185,24 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                 if (lane == 0) mbar_arrive_expect_tx(fb, C::STAGE);
                 __syncwarp();
                 const int pg_box = __shfl_sync(0xffffffffu, pg, box0 - held + (lane & (nbox - 1)));
-                const int pg_part = __shfl_sync(0xffffffffu, pg, ((key0 + (lane & 3) * 16) >> log2_r) - held);
+                const int pg_part = __shfl_sync(0xffffffffu, pg, ((key0 + (lane & (4 * C::G - 1)) * 16) >> log2_r) - held);
                 if (lane < 2 * nbox) {
                     const bool is_v = lane >= nbox;
                     const int box = lane & (nbox - 1);
                     const uint32_t dst = smem_u32(smem + stage * C::STAGE + (is_v ? C::HALF : 0)) + (box << log2_r) * C::CB;
 #pragma unroll
                     for (int c = 0; c < C::NCB; ++c)
-                        tma_load_3d(dst + c * kD8Tile * C::CB, is_v ? &tmV : &tmK, fb, c * C::CB,
+                        tma_load_3d(dst + c * C::TILE * C::CB, is_v ? &tmV : &tmK, fb, c * C::CB,
                                     (key0 + (box << log2_r)) & ps_mask, pg_box * p.Hkv + w.hk, pol);
                 }
-                if (lane < 8) {
-                    const int key = key0 + (lane & 3) * 16;
+                if (lane < 8 * C::G) {
+                    const int key = key0 + (lane & (4 * C::G - 1)) * 16;
                     const size_t at = (((size_t)pg_part * p.Hkv + w.hk) << (p.log2_ps - p.log2_blk)) +
                                       ((key & ps_mask) >> p.log2_blk);
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n\t"
                                  "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%2];" ::"r"(
                                      smem_u32(&sh->scale[stage][lane])),
-                                 "l"((lane < 4 ? p.ks : p.vs) + at), "r"(fb)
+                                 "l"((lane < 4 * C::G ? p.ks : p.vs) + at), "r"(fb)
                                  : "memory");
                 }
                 ++filled;
@@ -329,79 +330,95 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
             };
 
             for (int k = w.k0; k < w.k1; ++k) {
-                const int key0 = (w.seq.t0 + k) * kD8Tile + warp * 16;
+                const int key0 = (w.seq.t0 + k) * C::TILE + warp * 16 * C::G;
                 if (!wait_all(&sh->full[stage], parity)) break;
                 // this warp's keys: some row sees one of them; all rows see all of them
-                const bool any = key0 < w.seq.L && key0 + 15 >= w.seq.lo;
-                const bool edge = key0 + 15 > w.seq.L - p.nq ||
+                const bool any = key0 < w.seq.L && key0 + 16 * C::G - 1 >= w.seq.lo;
+                const bool edge = key0 + 16 * C::G - 1 > w.seq.L - p.nq ||
                                   (p.window > 0 && key0 < w.seq.L - 1 - p.window);
-                const uint32_t kb = smem_u32(smem + stage * C::STAGE), vb = kb + C::HALF;
+                const uint32_t kb = smem_u32(smem + stage * C::STAGE) + warp * 16 * C::G * C::CB, vb = kb + C::HALF;
                 if (any) {
-                    // ---- S^T = K Q^T: keys key0 + g (+ 8) by rows 8 nt + 2 t (+ 1)
-                    float s[NT][2][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[nt][0][e] = s[nt][1][e] = 0.0f;
+                    // ---- S^T = K Q^T: keys key0 + 16 u + g (+ 8) by rows 8 nt + 2 t (+ 1)
+                    float s[C::G][NT][2][4];
                     constexpr int KW = C::CB / 16;               // k-steps (words of a lane) per column box
 #pragma unroll
-                    for (int c = 0; c < C::NCB; ++c) {
-                        uint32_t lo[KW], hi[KW];
-                        const uint32_t ra = kb + c * kD8Tile * C::CB + (warp * 16 + g) * C::CB, rb = ra + 8 * C::CB;
+                    for (int u = 0; u < C::G; ++u) {
 #pragma unroll
-                        for (int v = 0; v < KW / 4; ++v) {
-                            const int ch = C::CB == 128 ? ((2 * t + v) ^ g) : (t ^ ((g >> 1) & 3));
-                            const uint4 a = dec8_lds128(ra + ch * 16), d = dec8_lds128(rb + ch * 16);
-                            lo[4 * v] = a.x, lo[4 * v + 1] = a.y, lo[4 * v + 2] = a.z, lo[4 * v + 3] = a.w;
-                            hi[4 * v] = d.x, hi[4 * v + 1] = d.y, hi[4 * v + 2] = d.z, hi[4 * v + 3] = d.w;
-                        }
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < KW; ++i) {
-                            const uint32_t a0 = dec8_half2<kE5M2>(lo[i] & 0xFFFF), a2 = dec8_half2<kE5M2>(lo[i] >> 16);
-                            const uint32_t a1 = dec8_half2<kE5M2>(hi[i] & 0xFFFF), a3 = dec8_half2<kE5M2>(hi[i] >> 16);
+                            for (int e = 0; e < 4; ++e) s[u][nt][0][e] = s[u][nt][1][e] = 0.0f;
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const int at = nt * (D / 16) + c * KW + i;
-                                const uint2 q2 = C::Q_REGS ? qf[C::Q_REGS ? at : 0] : frag[at * 32];
-                                dec8_mma(s[nt][i & 1], a0, a1, a2, a3, q2.x, q2.y);
+                        for (int c = 0; c < C::NCB; ++c) {
+                            uint32_t lo[KW], hi[KW];
+                            const uint32_t ra = kb + c * C::TILE * C::CB + (u * 16 + g) * C::CB, rb = ra + 8 * C::CB;
+#pragma unroll
+                            for (int v = 0; v < KW / 4; ++v) {
+                                const int ch = C::CB == 128 ? ((2 * t + v) ^ g) : (t ^ ((g >> 1) & 3));
+                                const uint4 a = dec8_lds128(ra + ch * 16), d = dec8_lds128(rb + ch * 16);
+                                lo[4 * v] = a.x, lo[4 * v + 1] = a.y, lo[4 * v + 2] = a.z, lo[4 * v + 3] = a.w;
+                                hi[4 * v] = d.x, hi[4 * v + 1] = d.y, hi[4 * v + 2] = d.z, hi[4 * v + 3] = d.w;
+                            }
+#pragma unroll
+                            for (int i = 0; i < KW; ++i) {
+                                const uint32_t a0 = dec8_half2<kE5M2>(lo[i] & 0xFFFF), a2 = dec8_half2<kE5M2>(lo[i] >> 16);
+                                const uint32_t a1 = dec8_half2<kE5M2>(hi[i] & 0xFFFF), a3 = dec8_half2<kE5M2>(hi[i] >> 16);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    const int at = nt * (D / 16) + c * KW + i;
+                                    const uint2 q2 = C::Q_REGS ? qf[C::Q_REGS ? at : 0] : frag[at * 32];
+                                    dec8_mma(s[u][nt][i & 1], a0, a1, a2, a3, q2.x, q2.y);
+                                }
                             }
                         }
                     }
                     // ---- scales, mask, running maximum, weights
-                    const float ksc = sh->scale[stage][warp], vsc = sh->scale[stage][4 + warp];
-                    const Dec8ValueScale vs(vsc, v_top);
-                    float xs[NT][4];
+                    float vf[C::G], vinv[C::G], xs[C::G][NT][4];
                     bool raise = false;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float k0 = ksc * rowc[nt][0], k1 = ksc * rowc[nt][1];
+                    for (int u = 0; u < C::G; ++u) {
+                        float ksc = sh->scale[stage][warp * C::G + u], vsc = sh->scale[stage][(4 + warp) * C::G + u];
+                        if (C::G > 1 && edge && (key0 + u * 16 >= w.seq.L || key0 + u * 16 + 15 < w.seq.lo))
+                            ksc = vsc = 0.0f;                    // nobody's keys: whatever their scales are
+                        const Dec8ValueScale vs(vsc, v_top);
+                        vf[u] = vs.f;
+                        vinv[u] = vs.inv;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            xs[nt][e] = fmaf(s[nt][0][e] + s[nt][1][e], (e & 1) ? k1 : k0, vs.e);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float k0 = ksc * rowc[nt][0], k1 = ksc * rowc[nt][1];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                xs[u][nt][e] = fmaf(s[u][nt][0][e] + s[u][nt][1][e], (e & 1) ? k1 : k0, vs.e);
                         }
                     }
                     if (edge) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int u = 0; u < C::G; ++u)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int key = key0 + g + (e & 2) * 4;
-                                const int last = w.seq.L - p.nq + (row0 + nt * 8 + 2 * t + (e & 1)) % p.nq;
-                                if (key > last || (p.window > 0 && key < last - p.window)) xs[nt][e] = NEG_INF;
-                            }
-                    }
+                            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        raise |= fmaxf(xs[nt][0], xs[nt][2]) > m[nt][0] + kD8Tau ||
-                                 fmaxf(xs[nt][1], xs[nt][3]) > m[nt][1] + kD8Tau;
+                                for (int e = 0; e < 4; ++e) {
+                                    const int key = key0 + u * 16 + g + (e & 2) * 4;
+                                    const int last = w.seq.L - p.nq + (row0 + nt * 8 + 2 * t + (e & 1)) % p.nq;
+                                    if (key > last || (p.window > 0 && key < last - p.window)) xs[u][nt][e] = NEG_INF;
+                                }
                     }
+                    float top[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            top[nt][e] = fmaxf(xs[0][nt][e], xs[0][nt][e + 2]);
+#pragma unroll
+                            for (int u = 1; u < C::G; ++u) top[nt][e] = fmax3(top[nt][e], xs[u][nt][e], xs[u][nt][e + 2]);
+                            raise |= top[nt][e] > m[nt][e] + kD8Tau;
+                        }
                     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             float al[2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                float mx = fmaxf(xs[nt][e], xs[nt][e + 2]);
+                                float mx = top[nt][e];
 #pragma unroll
                                 for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                                 mx = fmaxf(mx, m[nt][e]);
@@ -415,49 +432,52 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                                 for (int e = 0; e < 4; ++e) acc[nt][i][e] *= al[e & 1];
                         }
                     }
-                    uint32_t pb[NT][2];
+                    uint32_t pb[C::G][NT][2];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float wt[4];
+                    for (int u = 0; u < C::G; ++u)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float mm = m[nt][e & 1];
-                            wt[e] = ex2(xs[nt][e] - (mm == NEG_INF ? 0.0f : mm));
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float wt[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float mm = m[nt][e & 1];
+                                wt[e] = ex2(xs[u][nt][e] - (mm == NEG_INF ? 0.0f : mm));
+                            }
+                            l[nt][0] = fmaf(wt[0] + wt[2], vinv[u], l[nt][0]);
+                            l[nt][1] = fmaf(wt[1] + wt[3], vinv[u], l[nt][1]);
+                            pb[u][nt][0] = dec8_transpose(dec8_pack_half2(wt[0] * vf[u], wt[1] * vf[u]));
+                            pb[u][nt][1] = dec8_transpose(dec8_pack_half2(wt[2] * vf[u], wt[3] * vf[u]));
                         }
-                        l[nt][0] = fmaf(wt[0] + wt[2], vs.inv, l[nt][0]);
-                        l[nt][1] = fmaf(wt[1] + wt[3], vs.inv, l[nt][1]);
-                        pb[nt][0] = dec8_transpose(dec8_pack_half2(wt[0] * vs.f, wt[1] * vs.f));
-                        pb[nt][1] = dec8_transpose(dec8_pack_half2(wt[2] * vs.f, wt[3] * vs.f));
-                    }
                     // ---- O^T += V^T P^T: this lane's keys 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
-                    for (int c = 0; c < C::NCB; ++c) {
+                    for (int uc = 0; uc < C::G * C::NCB; ++uc) {
+                        const int u = uc / C::NCB, c = uc % C::NCB;
                         uint32_t v[4][VW];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int kr = 2 * t + (k & 1) + (k & 2) * 4;
-                            const uint32_t ra = vb + c * kD8Tile * C::CB + (warp * 16 + kr) * C::CB;
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            const int kr = 2 * t + (k4 & 1) + (k4 & 2) * 4;
+                            const uint32_t ra = vb + c * C::TILE * C::CB + (u * 16 + kr) * C::CB;
                             if constexpr (C::CB == 128) {
-                                const uint4 u = dec8_lds128(ra + ((g ^ (kr & 7)) * 16));
-                                v[k][0] = u.x, v[k][1] = u.y, v[k][2] = u.z, v[k][3] = u.w;
+                                const uint4 r = dec8_lds128(ra + ((g ^ (kr & 7)) * 16));
+                                v[k4][0] = r.x, v[k4][1] = r.y, v[k4][2] = r.z, v[k4][3] = r.w;
                             } else {
-                                const uint2 u = dec8_lds64(ra + (((g >> 1) ^ ((kr >> 1) & 3)) * 16) + (g & 1) * 8);
-                                v[k][0] = u.x, v[k][1] = u.y;
+                                const uint2 r = dec8_lds64(ra + (((g >> 1) ^ ((kr >> 1) & 3)) * 16) + (g & 1) * 8);
+                                v[k4][0] = r.x, v[k4][1] = r.y;
                             }
                         }
                         if (edge) {
                             uint32_t odd = 0;                    // non-finite codes among this lane's
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int key = key0 + 2 * t + (k & 1) + (k & 2) * 4;
+                            for (int k4 = 0; k4 < 4; ++k4) {
+                                const int key = key0 + u * 16 + 2 * t + (k4 & 1) + (k4 & 2) * 4;
                                 const bool out = key >= w.seq.L || key < w.seq.lo;
 #pragma unroll
                                 for (int i = 0; i < VW; ++i) {
-                                    v[k][i] = out ? 0u : v[k][i];
-                                    odd |= dec8_nonfinite<kE5M2>(v[k][i]);
+                                    v[k4][i] = out ? 0u : v[k4][i];
+                                    odd |= dec8_nonfinite<kE5M2>(v[k4][i]);
                                 }
                             }
-                            if (__any_sync(0xffffffffu, odd != 0)) keep_nan(c, v, xs);
+                            if (__any_sync(0xffffffffu, odd != 0)) keep_nan(c, v, xs[u]);
                         }
 #pragma unroll
                         for (int i = 0; i < VW; ++i) {
@@ -469,7 +489,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                                 const uint32_t a2 = dec8_half2<kE5M2>(d & 0xFFFF), a3 = dec8_half2<kE5M2>(d >> 16);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
-                                    dec8_mma(acc[nt][(c * VW + i) * 2 + h], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                                    dec8_mma(acc[nt][(c * VW + i) * 2 + h], a0, a1, a2, a3, pb[u][nt][0], pb[u][nt][1]);
                             }
                         }
                     }
@@ -561,7 +581,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
             w.next(p);
         }
         if (!ok) dec8_timeout(p, &sh->abort_flag);
-        else dec8_write_empty<kD8Tile, D>(p, kD8Warps * 32);
+        else dec8_write_empty<C::TILE, D>(p, kD8Warps * 32);
     }
 }
 
