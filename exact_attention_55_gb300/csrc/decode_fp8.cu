@@ -13,23 +13,23 @@
 // Taking the maximum over what a key adds to O, not over its score alone, keeps the fp16
 // weights w f at or below a small constant whatever the blocks' scales are.
 //
-// HBM-bound: a byte of the cache is used by 2 * rows FLOP and half the rows' weight of a
-// conversion.  The design is about keeping the loads in flight and the work even:
-//   * The tiles (64 keys of one head) of all sequences form one line that is cut into equal
-//     ranges, one per resident CTA (two per SM), so a ragged batch and a single long sequence
-//     both keep every SM busy to the end.  A head counts kD8UnitCost tiles more than it has,
-//     what starting and joining it costs.  A range may end inside a head; its part then goes
-//     to the workspace and decode_fp8_combine_kernel, launched as a dependent of the main
-//     grid, joins the parts.
+// This kernel takes up to 16 query rows per key head (8 at d = 256) in one pass over the
+// cache, and more in several; decode_fp8_wide.cu takes many rows of a large step.  HBM-bound:
+// a byte of the cache is used by 2 * rows FLOP and half a conversion.  The design is about
+// keeping the loads in flight and the work even:
+//   * The work is cut into equal ranges, one per resident CTA (decode_fp8.cuh).  Up to 8 rows
+//     three CTAs fit an SM (two: 85.5 for 84.7 us at B16 H16 L8192 d128, 36.3 for 35.3 on
+//     a ragged batch of 48).
 //   * Warp 4 walks the range ahead of the others: TMA boxes (one per page or 64 rows) into a
 //     ring of stages, the blocks' scales beside them by cp.async on the same barrier, and the
 //     next head's queries as product fragments.
-//   * Warps 0-3 take 16 keys of each tile.  The codes are exact in fp16 and a query row
-//     scaled by a power of two is too, so S^T = K Q^T and O^T += V^T P^T run as
-//     mma.m16n8k16 fp16 with fp32 sums: 16 keys (or 16 values of d) by 8 query rows, which
-//     wastes nothing down to 8 rows and needs no per-row padding to 128.  An m64+ tcgen05
-//     tile would want its operands in one type (the queries split into two E4M3 parts) and
-//     the probabilities through shared memory for a product that HBM bounds anyway.
+//   * Warps 0-3 take 16 keys of each tile (32 at d = 64, where 16 are too little work per
+//     barrier: 29.4 for 25.6 us, 8 rows, 16 x 8 heads x 8192 keys).  The codes are exact in
+//     fp16 and a query row scaled by a power of two is too, so S^T = K Q^T and O^T += V^T P^T
+//     run as mma.m16n8k16 fp16 with fp32 sums: 16 keys (or 16 values of d) by 8 query rows,
+//     operands straight from registers.  A tcgen05 tile would be at least 64 rows high and
+//     want converted tiles in shared memory; up to 16 rows that costs more than it saves
+//     (53.8 here, 63.8 us there at 16 rows, d 128).
 //   * The order of d inside a product is free, so a lane takes 16 consecutive bytes of a row
 //     (no bank conflicts under TMA's swizzle) and uses them as four k-steps; for V, byte
 //     permutes pair two keys before the conversion.
@@ -37,6 +37,13 @@
 // before the product, and a NaN value at a key that only some rows see is replaced by 0
 // there and added back as NaN to the rows that do (keep_nan), so what stale rows and pages
 // hold never reaches O.
+//
+// Measured: B16 H16 L8192 d128, one new token: 84.5 us = 6.35 TB/s, 93 % of the measured copy
+// rate; what is left is the start (lengths, table, first boxes: 4 us until the first tile is
+// there) and the spread of the CTAs' ends (65 to 78 us for equal ranges).  48 sequences of 37
+// to 9000 keys, 32 over 8 heads: 32.6 us = 5.2 TB/s, the same start, 1 us to join a CTA's warps
+// and 2-3 us for the joining launch.  An instruction count of 264 per 16 keys of d 128 keeps the issue
+// slots at 38 %; with the masks inside the common path it was 485 and 109 us.
 #include "decode_fp8.cuh"
 
 namespace gb300 {

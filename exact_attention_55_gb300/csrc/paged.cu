@@ -35,8 +35,10 @@ namespace cg = cooperative_groups;
 // Every CTA scans all requests for itself into shared memory, the cluster meets once (the
 // lengths and the free count may be overwritten in place after that), and then its
 // threads share the tokens, pages and requests.  A token finds its request by bisection
-// of the ends; a page that the step takes is read from the free stack, never from the
-// table entry another thread writes.
+// of the ends, four tokens at a time; a page that the step takes is read from the free stack,
+// never from the table entry another thread writes.  Measured: 16 requests of one token 3.5
+// us, 1024 requests with 33 thousand tokens 8.4 us (11.7 with a third scan and lookups one by
+// one), of which a launch is about 2 and the dependent reads of lengths and pages 2.
 constexpr int kPlanMaxThreads = 1024;
 
 // Exclusive sum over the block's threads and the total; every thread calls it.  `sums` is a
@@ -214,6 +216,9 @@ cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream)
 // skipped.  HBM-bound: each row is read once and written once.  A CTA takes kTokens tokens of
 // K or V, all heads; a token's heads are one run of memory on the input side, so a thread
 // copies the same 16-byte piece of each token, the loads of its tokens in flight together.
+// Measured: 16000 tokens of 16 heads, d 128, as columns of a wider matrix 41.7 us = 6.3 TB/s
+// read and written (54.0 with a 16-byte piece a thread and divisions for its place); a step
+// of 16 tokens 1.7 us.
 template <int kTokens>
 __global__ void __launch_bounds__(256) cache_append_bf16_kernel(const AppendParams p)
 {
@@ -245,7 +250,8 @@ __global__ void __launch_bounds__(256) cache_append_bf16_kernel(const AppendPara
 
 cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream)
 {
-    // one token a CTA while that is what spreads the work, else four
+    // one token a CTA while that is what spreads the work, else four (one against four, us: 16
+    // tokens 1.5 / 1.8, 256 1.7 / 1.8, 1024 of 16 heads 3.2 / 3.4, 2048 4.9 / 4.5, 8192 20.2 / 15.9)
     if (p.T <= 1024) cache_append_bf16_kernel<1><<<dim3(p.T, 2), 256, 0, stream>>>(p);
     else cache_append_bf16_kernel<4><<<dim3((unsigned)(((long long)p.T + 3) / 4), 2), 256, 0, stream>>>(p);
     return cudaGetLastError();
@@ -271,7 +277,12 @@ cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream)
 // them (what a tile holds unless short runs and one of a whole block meet in it; rows past
 // that are read again).  The quotient is formed from the reciprocal with one residual
 // correction, as in the block quantiser; values that this cannot take (infinities, scales
-// near fp32's limits) go through the division itself.
+// near fp32's limits) go through the division itself.  A tile that is one run, as in a
+// prefill, takes a path without per-row bookkeeping.  Measured: 31850 tokens of 16 heads,
+// d 128, blocks of 128: 73.5 us = 5.3 TB/s read and written (the rows read twice and divided
+// one by one 143; several runs' bookkeeping for every tile 91), then bound by issue (8
+// values cost about 45 instructions) as much as by HBM; a step of 61 tokens 5.5 us, four
+// dependent reads (slots, rows, scale, launch) long.
 constexpr int kAppendWindow = 256;     // tokens a CTA looks at: tile + block - 1 < 256
 constexpr int kAppendHeld = 128;       // rows held in registers
 
