@@ -39,11 +39,12 @@
 // hold never reaches O.
 //
 // Measured: B16 H16 L8192 d128, one new token: 84.5 us = 6.35 TB/s, 93 % of the measured copy
-// rate; what is left is the start (lengths, table, first boxes: 4 us until the first tile is
-// there) and the spread of the CTAs' ends (65 to 78 us for equal ranges).  48 sequences of 37
-// to 9000 keys, 32 over 8 heads: 32.6 us = 5.2 TB/s, the same start, 1 us to join a CTA's warps
-// and 2-3 us for the joining launch.  An instruction count of 264 per 16 keys of d 128 keeps the issue
-// slots at 38 %; with the masks inside the common path it was 485 and 109 us.
+// rate; what is left is the start (lengths, table, first boxes: the first tile is there after 4
+// us) and the spread of the CTAs' ends (equal ranges end within 13 us of each other: HBM does
+// not serve all SMs alike).  48 sequences of 37 to 9000 keys, 32 over 8 heads: 32.6 us = 5.2
+// TB/s; beside the same start, 1 us to join a CTA's warps and 2-3 us for the joining launch.
+// The common path is 264 instructions per warp and 16 keys (with masks and NaN handling inside
+// it 485, and 109.5 us for the first case), which keeps the issue slots 43 % busy.
 #include "decode_fp8.cuh"
 
 namespace gb300 {

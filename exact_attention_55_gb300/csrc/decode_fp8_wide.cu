@@ -24,11 +24,11 @@
 //
 // Measured, 16 sequences x 8 key heads x 8192 keys, d 128 (39.5 us at the copy rate): 32 rows
 // 69 us, 64 rows 77, 128 rows 155 (102, 187 and 364 in passes of 16 rows); d 256, 128 rows 152
-// (79).  The products take 1030 cycles of a tile's about 1700 (32 rows); what bounds it is the
-// chain of a softmax warp (S, maximum, weights, P: about 1300 cycles, the SM's issue slots
-// shared with eight converting warps), at 128 rows its 128 keys a thread.  One warp issuing
-// both products left the tensor core idle at every wait (75.5 for 73.0 us), one warpgroup
-// converting K and V in turn was 84.5.
+// (842).  Neither HBM (48 %) nor the tensor pipe (44 %) bounds it, but the chain of a softmax
+// warp per tile (S arrives, maximum, weights, P leaves), whose warps share the issue slots with
+// the eight that convert; at 128 rows each of its threads has all of a tile's 128 keys.  Loading and
+// converting in one warpgroup each for K and V, and S and P V issued by two warps, each cut
+// that chain (32 rows: 112.6, 84.5, 73.0 us).
 #include "decode_fp8.cuh"
 
 namespace gb300 {

@@ -280,9 +280,10 @@ cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream)
 // near fp32's limits) go through the division itself.  A tile that is one run, as in a
 // prefill, takes a path without per-row bookkeeping.  Measured: 31850 tokens of 16 heads,
 // d 128, blocks of 128: 73.5 us = 5.3 TB/s read and written (the rows read twice and divided
-// one by one 143; several runs' bookkeeping for every tile 91), then bound by issue (8
-// values cost about 45 instructions) as much as by HBM; a step of 61 tokens 5.5 us, four
-// dependent reads (slots, rows, scale, launch) long.
+// one by one 143, the bookkeeping of several runs for every tile 142).  The issue slots are 68 %
+// busy (100 instructions per warp and 8 values a lane, half of them the quotients) and HBM 60
+// %, in turns: a tile's loads, its maximum and its codes follow one another, four CTAs an SM.
+// A step of 61 tokens takes 5.5 us, four dependent reads (slots, rows, scale, launch) long.
 constexpr int kAppendWindow = 256;     // tokens a CTA looks at: tile + block - 1 < 256
 constexpr int kAppendHeld = 128;       // rows held in registers
 
