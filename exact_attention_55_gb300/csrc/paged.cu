@@ -37,7 +37,7 @@ namespace cg = cooperative_groups;
 // threads share the tokens, pages and requests.  A token finds its request by bisection
 // of the ends, four tokens at a time; a page that the step takes is read from the free stack,
 // never from the table entry another thread writes.  Measured: 16 requests of one token 3.5
-// us, 1024 requests with 33 thousand tokens 8.4 us (11.7 with a third scan and lookups one by
+// us, 1024 requests with 29 thousand tokens 8.4 us (11.7 with a third scan and lookups one by
 // one), of which a launch is about 2 and the dependent reads of lengths and pages 2.
 constexpr int kPlanMaxThreads = 1024;
 
@@ -216,7 +216,7 @@ cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream)
 // skipped.  HBM-bound: each row is read once and written once.  A CTA takes kTokens tokens of
 // K or V, all heads; a token's heads are one run of memory on the input side, so a thread
 // copies the same 16-byte piece of each token, the loads of its tokens in flight together.
-// Measured: 16000 tokens of 16 heads, d 128, as columns of a wider matrix 41.7 us = 6.3 TB/s
+// Measured: 16006 tokens of 16 heads, d 128, as columns of a wider matrix 41.7 us = 6.6 TB/s
 // read and written (54.0 with a 16-byte piece a thread and divisions for its place); a step
 // of 16 tokens 1.7 us.
 template <int kTokens>
@@ -278,8 +278,8 @@ cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream)
 // that are read again).  The quotient is formed from the reciprocal with one residual
 // correction, as in the block quantiser; values that this cannot take (infinities, scales
 // near fp32's limits) go through the division itself.  A tile that is one run, as in a
-// prefill, takes a path without per-row bookkeeping.  Measured: 31850 tokens of 16 heads,
-// d 128, blocks of 128: 73.5 us = 5.3 TB/s read and written (the rows read twice and divided
+// prefill, takes a path without per-row bookkeeping.  Measured: 31826 tokens of 16 heads,
+// d 128, blocks of 128: 73.5 us = 5.4 TB/s read and written (the rows read twice and divided
 // one by one 143, the bookkeeping of several runs for every tile 142).  The issue slots are 68 %
 // busy (100 instructions per warp and 8 values a lane, half of them the quotients) and HBM 60
 // %, in turns: a tile's loads, its maximum and its codes follow one another, four CTAs an SM.
@@ -559,7 +559,7 @@ static cudaError_t launch_append_fp8_d(const AppendParams& p, bool e5m2, cudaStr
     const int block = 1 << p.log2_blk, tile = block < 64 ? 64 : block;
     const long long tiles = ((long long)p.T + tile - 1) / tile;
     // a head of K or V per CTA while there are few, else about 36 CTAs per SM, each with
-    // several of its tile's heads (31850 tokens of 16 heads, d 128: 8 per SM 103.0 us, 12 90.6,
+    // several of its tile's heads (31826 tokens of 16 heads, d 128: 8 per SM 103.0 us, 12 90.6,
     // 24 78.1, 36 73.2, 60 76.5)
     const long long groups = (36LL * p.sm_count + tiles - 1) / tiles;
     const dim3 grid((unsigned)tiles, groups < 2 * p.H ? (unsigned)groups : 2 * p.H);

@@ -452,8 +452,9 @@ attn_status_t attn_cache_append_fp8(const void* k, const void* v, void* k_cache,
  * What the cache holds at keys a query does not see (rows behind the sequence, pages
  * behind it or before its window) never reaches that query's outputs, NaN codes and
  * scales included (an E5M2 code of infinity in V counts as NaN at keys that only some of
- * the queries see).  The queries and the codes enter the products exactly; scores, sums and O
- * are fp32, the weights of the second product (softmax times V scale, relative to the row's
+ * the queries see).  The queries and the codes enter the products exactly (a query element
+ * below 2^-32 of its row's largest is off by at most 2^-39 of that); scores, sums and O are
+ * fp32, the weights of the second product (softmax times V scale, relative to the row's
  * largest) are rounded to fp16.  A V scale below 2^-60 of the sequence's largest, or of 1,
  * counts as that in "largest": only a softmax that sits on such blocks loses digits of O.
  * HBM-bound: every key and value code that a query sees is read once per call.
