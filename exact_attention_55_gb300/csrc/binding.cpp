@@ -171,7 +171,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n)
         auto out = [&](PyObject* given, int64_t count, at::ScalarType dtype, const char* name) {
             if (given != Py_None) return exact(given, {count}, dtype, dev, name);
             if (!whole.defined())
-                whole = at::detail::empty_cuda({room(8 * T) + room(4 * T) + 2 * room(4 * B) + room(4 * B + 4) + 16},
+                whole = at::detail::empty_cuda({room(8LL * T) + room(4LL * T) + 2 * room(4 * B) + room(4 * B + 4) + 16},
                                                at::kByte, dev, c10::nullopt);
             const int64_t size = (int64_t)c10::elementSize(dtype);
             Tensor t = at::detail::make_tensor<c10::TensorImpl>(

@@ -81,6 +81,20 @@ def test_plan_of_long_requests(fa):
     check_plan(fa, (new, seq, table, stack, np.array([-4], np.int32), 64, 41352))
 
 
+def test_plan_of_very_many_rows(fa):
+    """2^28 and more packed rows: the outputs' one allocation is sized in 64 bits."""
+    T, i32 = (1 << 28) + 7, dict(dtype=torch.int32, device="cuda")
+    new, lens = torch.tensor([3, 0, 2], **i32), torch.tensor([5, 1, 16], **i32)
+    table = torch.tensor([[4, -1], [2, -1], [1, -1]], **i32)
+    out = fa.attn_paged_plan(new, lens, table, torch.tensor([7, 9], **i32), torch.tensor([2], **i32), 16, T)
+    seq, left, cu, slots, pos, served = out
+    assert seq.tolist() == [8, 1, 18] and left.tolist() == [1] and cu.tolist() == [0, 3, 3, 5]
+    assert served.tolist() == [1, 1, 1] and table[2].tolist() == [1, 9]
+    assert slots[:5].tolist() == [4 * 16 + 5, 4 * 16 + 6, 4 * 16 + 7, 9 * 16, 9 * 16 + 1]
+    assert pos[:5].tolist() == [5, 6, 7, 16, 17]
+    assert slots.numel() == pos.numel() == T and (slots[5:] == -1).all() and (pos[5:] == -1).all()
+
+
 def test_plan_in_place_and_again(fa):
     """seq_lens and free_count may be their own outputs; steps follow one another."""
     rng = np.random.default_rng(4)
