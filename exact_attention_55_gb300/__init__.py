@@ -42,7 +42,8 @@ __all__ = [
     "ATTN_FP8_E4M3_POW2",
     "attn_status_string", "attn_get_device_status", "attn_selftest_wait_timeout",
     "attn_selftest_fwd_withheld_load", "attn_selftest_quant_withheld_load",
-    "attn_selftest_bwd_withheld_load", "attn_selftest_fp8_convert", "EXPORTED_SYMBOLS",
+    "attn_selftest_bwd_withheld_load", "attn_selftest_decode_fp8_withheld_load",
+    "attn_selftest_fp8_convert", "EXPORTED_SYMBOLS",
 ]
 
 ATTN_OK = 0
@@ -72,7 +73,7 @@ EXPORTED_SYMBOLS = (
     "attn_fwd_schedule", "attn_status_string", "attn_get_device_status",
     "attn_selftest_wait_timeout", "attn_selftest_fwd_withheld_load",
     "attn_selftest_quant_withheld_load", "attn_selftest_bwd_withheld_load",
-    "attn_selftest_fp8_convert",
+    "attn_selftest_decode_fp8_withheld_load", "attn_selftest_fp8_convert",
 )
 
 _lock = threading.Lock()
@@ -165,6 +166,9 @@ def load_library(path: str | None = None):
         lib.attn_selftest_bwd_withheld_load.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                                         ctypes.c_size_t, i, i, i, i, i, i, u64, vp]
         lib.attn_selftest_bwd_withheld_load.restype = i
+        lib.attn_selftest_decode_fp8_withheld_load.argtypes = (
+            [vp] * 9 + [i] * 10 + [vp, ctypes.c_size_t, i, u64, vp])
+        lib.attn_selftest_decode_fp8_withheld_load.restype = i
         lib.attn_selftest_fp8_convert.argtypes = [ctypes.c_uint, ctypes.c_size_t, i, vp, vp]
         lib.attn_selftest_fp8_convert.restype = i
         if _binding is None:
@@ -681,6 +685,24 @@ def attn_selftest_bwd_withheld_load(q, k, v, o, dout, lse, dq, dk, dv, workspace
         workspace.numel() * workspace.element_size(), B, H, N, d, int(bool(causal)),
         int(withheld), int(timeout_ns), _stream_handle(stream))
     _raise_if(st, "attn_selftest_bwd_withheld_load")
+
+
+def attn_selftest_decode_fp8_withheld_load(q, k_cache, v_cache, k_scales, v_scales, page_table,
+                                           seq_lens, o, lse, workspace, fmt="e4m3",
+                                           withheld: int = 1, timeout_ns: int = 20_000_000,
+                                           stream=None) -> None:
+    """Run the 8-bit decoding step with load `withheld` of every CTA never issued and every
+    wait bounded by timeout_ns (it records ATTN_ERR_TIMEOUT)."""
+    B, H, nq, d = q.shape
+    num_pages, Hkv, page_size, _ = k_cache.shape
+    st = load_library().attn_selftest_decode_fp8_withheld_load(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+        v_scales.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+        lse.data_ptr(), B, H, Hkv, nq, d, page_size, num_pages, page_table.shape[1],
+        page_size // k_scales.shape[2], _fp8_format(fmt), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), int(withheld), int(timeout_ns),
+        _stream_handle(stream))
+    _raise_if(st, "attn_selftest_decode_fp8_withheld_load")
 
 
 def attn_selftest_fp8_convert(first: int, count: int, fmt="e4m3", codes=None, stream=None):

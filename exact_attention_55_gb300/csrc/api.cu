@@ -1095,14 +1095,13 @@ extern "C" size_t attn_decode_fp8_workspace_bytes(int H, int Hkv, int nq, int d)
     return narrow > wide ? narrow : wide;
 }
 
-extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cache,
-                                               const void* v_cache, const float* k_scales,
-                                               const float* v_scales, const int* page_table,
-                                               const int* seq_lens, void* o, float* lse, int B,
-                                               int H, int Hkv, int nq, int d, int page_size,
-                                               int num_pages, int max_pages, int block, int format,
-                                               float scale, int window, void* workspace,
-                                               size_t workspace_bytes, void* stream)
+// withhold: 0, or n: the n-th load of each CTA is never issued (a diagnostic of the abort path)
+static attn_status_t decode_fp8(
+    const void* q, const void* k_cache, const void* v_cache,
+    const float* k_scales, const float* v_scales, const int* page_table, const int* seq_lens,
+    void* o, float* lse, int B, int H, int Hkv, int nq, int d, int page_size, int num_pages,
+    int max_pages, int block, int format, float scale, int window, void* workspace,
+    size_t workspace_bytes, void* stream, unsigned long long timeout_ns, int withhold)
 {
     if (!q || !k_cache || !v_cache || !k_scales || !v_scales || !page_table || !seq_lens || !o || !lse)
         return ATTN_ERR_INVALID_ARG;
@@ -1164,10 +1163,36 @@ extern "C" attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cach
     p.ranges = plan.ranges;
     p.row_groups = plan.row_groups;
     p.status = dev->status;
-    p.timeout_ns = kWaitTimeoutNs;
+    p.timeout_ns = timeout_ns;
+    p.withhold = (unsigned)withhold;
     const bool e5m2 = format == ATTN_FP8_E5M2;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const cudaError_t err = plan.wide ? launch_decode_fp8_wide(mk, mv, p, d, e5m2, plan.cta_rows, cs)
                                       : launch_decode_fp8(mk, mv, p, d, e5m2, plan.cta_rows, cs);
     return err == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" attn_status_t attn_decode_fp8_paged(
+    const void* q, const void* k_cache, const void* v_cache,
+    const float* k_scales, const float* v_scales, const int* page_table, const int* seq_lens,
+    void* o, float* lse, int B, int H, int Hkv, int nq, int d, int page_size, int num_pages,
+    int max_pages, int block, int format, float scale, int window, void* workspace,
+    size_t workspace_bytes, void* stream)
+{
+    return decode_fp8(q, k_cache, v_cache, k_scales, v_scales, page_table, seq_lens, o, lse, B, H, Hkv, nq,
+                      d, page_size, num_pages, max_pages, block, format, scale, window,
+                      workspace, workspace_bytes, stream, kWaitTimeoutNs, 0);
+}
+
+extern "C" attn_status_t attn_selftest_decode_fp8_withheld_load(
+    const void* q, const void* k_cache, const void* v_cache,
+    const float* k_scales, const float* v_scales, const int* page_table, const int* seq_lens,
+    void* o, float* lse, int B, int H, int Hkv, int nq, int d, int page_size, int num_pages,
+    int max_pages, int block, int format, void* workspace, size_t workspace_bytes,
+    int withheld, unsigned long long timeout_ns, void* stream)
+{
+    if (!selftest_args_ok(withheld, timeout_ns)) return ATTN_ERR_INVALID_ARG;
+    return decode_fp8(q, k_cache, v_cache, k_scales, v_scales, page_table, seq_lens, o, lse, B, H, Hkv, nq,
+                      d, page_size, num_pages, max_pages, block, format, 1.0f / sqrtf((float)d),
+                      0, workspace, workspace_bytes, stream, timeout_ns, withheld + 1);
 }

@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
         const int log2_r = p.log2_ps < 6 ? p.log2_ps : 6;       // rows per TMA box: a page, or 64
         const int nbox = C::TILE >> log2_r;
         const int ps_mask = (1 << p.log2_ps) - 1;
-        int stage = 0, filled = 0, q_slot = 0;
-        uint32_t parity = 1, q_parity = 1;
+        int stage = 0, q_slot = 0;
+        uint32_t filled = 0, parity = 1, q_parity = 1;
         bool ok = true;
         auto wait_lane0 = [&](uint64_t* bar, uint32_t par) {
             int r = 1;
@@ -190,11 +190,12 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                 }
                 if (!wait_lane0(&sh->empty[stage], parity)) break;
                 const uint32_t fb = smem_u32(&sh->full[stage]);
-                if (lane == 0) mbar_arrive_expect_tx(fb, C::STAGE);
+                const bool issue = ++filled != p.withhold;
+                if (lane == 0 && issue) mbar_arrive_expect_tx(fb, C::STAGE);
                 __syncwarp();
                 const int pg_box = __shfl_sync(0xffffffffu, pg, box0 - held + (lane & (nbox - 1)));
                 const int pg_part = __shfl_sync(0xffffffffu, pg, ((key0 + (lane & (4 * C::G - 1)) * 16) >> log2_r) - held);
-                if (lane < 2 * nbox) {
+                if (lane < 2 * nbox && issue) {
                     const bool is_v = lane >= nbox;
                     const int box = lane & (nbox - 1);
                     const uint32_t dst = smem_u32(smem + stage * C::STAGE + (is_v ? C::HALF : 0)) + (box << log2_r) * C::CB;
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                         tma_load_3d(dst + c * C::TILE * C::CB, is_v ? &tmV : &tmK, fb, c * C::CB,
                                     (key0 + (box << log2_r)) & ps_mask, pg_box * p.Hkv + w.hk, pol);
                 }
-                if (lane < 8 * C::G) {
+                if (lane < 8 * C::G && issue) {
                     const int key = key0 + (lane & (4 * C::G - 1)) * 16;
                     const size_t at = (((size_t)pg_part * p.Hkv + w.hk) << (p.log2_ps - p.log2_blk)) +
                                       ((key & ps_mask) >> p.log2_blk);
@@ -213,7 +214,6 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                                  "l"((lane < 4 * C::G ? p.ks : p.vs) + at), "r"(fb)
                                  : "memory");
                 }
-                ++filled;
                 if (++stage == C::STAGES) {
                     stage = 0;
                     parity ^= 1;
@@ -252,8 +252,9 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
         if (!ok && lane == 0) dec8_timeout(p, &sh->abort_flag);
         // every copy issued lands before shared memory is released
         if (lane == 0)
-            for (int k = filled < C::STAGES ? 0 : filled - C::STAGES; k < filled; ++k)
-                mbar_wait(smem_u32(&sh->full[k % C::STAGES]), (k / C::STAGES) & 1, nullptr, kCleanupTimeoutNs);
+            for (uint32_t k = filled < C::STAGES ? 0 : filled - C::STAGES; k < filled; ++k)
+                if (k + 1 != p.withhold)
+                    mbar_wait(smem_u32(&sh->full[k % C::STAGES]), (k / C::STAGES) & 1, nullptr, kCleanupTimeoutNs);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ consumers

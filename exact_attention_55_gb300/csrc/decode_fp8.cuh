@@ -89,6 +89,10 @@ __device__ __forceinline__ Dec8Line dec8_line(const DecodeFp8Params& p, Dec8Setu
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + THREADS - 1) / THREADS;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    if (tid == 0) {                    // lengths that change under the call find no start: stay inside
+        sh.b0 = 0;
+        sh.first = 0;
+    }
     // tiles in the lower 44 bits (at most 2^25 a sequence), sequences that have any above
     constexpr int shift = 44;
     constexpr long long mask = (1LL << shift) - 1;
@@ -146,7 +150,7 @@ struct Dec8Walk {
     {
         seq = dec8_seq<TILE>(p, b);
         span = dec8_span(p, seq.n);
-        hk = (int)dec8_div(a - sh.first, span + unit_cost);
+        hk = min((int)dec8_div(a - sh.first, max(span + unit_cost, 1)), p.Hkv - 1);
         s0 = sh.first + (long long)hk * (span + unit_cost);
         take(p);
         more = k1 > k0 || next(p);
@@ -165,8 +169,10 @@ struct Dec8Walk {
             if (s0 + unit_cost >= e) return more = false;
             if (++hk == p.Hkv) {
                 hk = 0;
-                do seq = dec8_seq<TILE>(p, ++b);
-                while (seq.n == 0);
+                do {
+                    if (b + 1 >= p.B) return more = false;   // only if the lengths change under the call
+                    seq = dec8_seq<TILE>(p, ++b);
+                } while (seq.n == 0);
                 span = dec8_span(p, seq.n);
             }
             take(p);
@@ -296,9 +302,11 @@ __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 todo = reinterpret_cast<const int4*>(p.ws)[blockIdx.x];
     const int x0 = todo.x, x1 = min(todo.y, p.ranges - 1), rg = todo.z;
-    if (x0 < 0) return;
+    // a main grid that gave up on a wait leaves entries unwritten: whatever they hold, stay inside
+    if (x0 < 0 || rg < 0 || rg >= p.row_groups || todo.w < 0) return;
     const size_t row0 = (size_t)todo.w;
     const int rows = min(ROWS, p.rows - rg * ROWS);
+    if (row0 + rows > (size_t)p.B * p.Hkv * p.rows) return;
     auto part_of = [&](int x) {
         return p.ws + 4 * ctas + (size_t)(2 * (x * p.row_groups + rg) + (x == x0 ? 1 : 0)) * PART;
     };

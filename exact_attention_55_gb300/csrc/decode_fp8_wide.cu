@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                     const uint32_t s = h % C::RING;
                     if (!wait_lane0(&sh->kv_empty[s], ((h / C::RING) & 1) ^ 1)) break;
                     const uint32_t fb = smem_u32(&sh->kv_full[s]);
+                    if (++h == p.withhold) continue;
                     if (lane == 0) mbar_arrive_expect_tx(fb, C::HALF);
                     __syncwarp();
                     // The tile's scales complete on the barrier of its K half, so whoever has seen
@@ -217,7 +218,6 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                             tma_load_3d(dst + c * C::TILE * C::CB, which ? &tmV : &tmK, fb, c * C::CB,
                                         (key0 + (lane << log2_r)) & ps_mask, pg_box * p.Hkv + w.hk, pol);
                     }
-                    ++h;
                 }
             }
             if (ok) w.next(p);
@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
         // every copy issued lands before shared memory is released
         if (lane == 0) {
             for (uint32_t k = h < C::RING ? 0 : h - C::RING; k < h; ++k)
-                mbar_wait(smem_u32(&sh->kv_full[k % C::RING]), (k / C::RING) & 1, nullptr, kCleanupTimeoutNs);
+                if (k + 1 != p.withhold)
+                    mbar_wait(smem_u32(&sh->kv_full[k % C::RING]), (k / C::RING) & 1, nullptr, kCleanupTimeoutNs);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
         auto convert = [&](auto fmt, uint32_t from, uint32_t to, int key0) {
             constexpr bool kE5M2 = decltype(fmt)::value;
             constexpr int N = C::HALF / 16 / 128;                // chunks of a thread
-            const bool edge = is_v && (key0 + C::TILE > w.seq.L - p.nq + 1 || key0 < w.seq.lo + p.nq - 1);
+            const bool edge = is_v && (key0 + (C::TILE - 1) > w.seq.L - p.nq || key0 < w.seq.lo + p.nq - 1);
             // chunk i of the thread: quad i % Q of four chunks in row first + (i / Q) * 32
             constexpr int Q = D / 64;
             const int l5 = ct & 31, c = l5 & 3;

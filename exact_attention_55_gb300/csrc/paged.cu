@@ -216,7 +216,7 @@ cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream)
 // skipped.  HBM-bound: each row is read once and written once.  A CTA takes kTokens tokens of
 // K or V, all heads; a token's heads are one run of memory on the input side, so a thread
 // copies the same 16-byte piece of each token, the loads of its tokens in flight together.
-// Measured: 16006 tokens of 16 heads, d 128, as columns of a wider matrix 41.7 us = 6.6 TB/s
+// Measured: 16006 tokens of 16 heads, d 128, as columns of a wider matrix 41.7 us = 6.3 TB/s
 // read and written (54.0 with a 16-byte piece a thread and divisions for its place); a step
 // of 16 tokens 1.7 us.
 template <int kTokens>
@@ -279,7 +279,7 @@ cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream)
 // correction, as in the block quantiser; values that this cannot take (infinities, scales
 // near fp32's limits) go through the division itself.  A tile that is one run, as in a
 // prefill, takes a path without per-row bookkeeping.  Measured: 31826 tokens of 16 heads,
-// d 128, blocks of 128: 73.5 us = 5.4 TB/s read and written (the rows read twice and divided
+// d 128, blocks of 128: 73.5 us = 5.3 TB/s read and written (the rows read twice and divided
 // one by one 143, the bookkeeping of several runs for every tile 142).  The issue slots are 68 %
 // busy (100 instructions per warp and 8 values a lane, half of them the quotients) and HBM 60
 // %, in turns: a tile's loads, its maximum and its codes follow one another, four CTAs an SM.

@@ -61,6 +61,7 @@ struct DecodeFp8Params {
     int row_groups;         // groups of query rows, each a CTA's share
     int* status;            // device status word (bounded waits)
     unsigned long long timeout_ns;
+    unsigned withhold;      // 0, or n: each CTA's n-th load is never issued (failure tests)
 };
 
 }  // namespace gb300

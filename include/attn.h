@@ -451,8 +451,8 @@ attn_status_t attn_cache_append_fp8(const void* k, const void* v, void* k_cache,
  *                not matter.  Calls that may overlap need one each.
  * What the cache holds at keys a query does not see (rows behind the sequence, pages
  * behind it or before its window) never reaches that query's outputs, NaN codes and
- * scales included (an E5M2 code of infinity in V counts as NaN at keys that only some of
- * the queries see).  The queries and the codes enter the products exactly (a query element
+ * scales included.  An E5M2 code of infinity in V, which the append never writes, counts as
+ * NaN where only some of the queries see its key, or several share it.  The queries and the codes enter the products exactly (a query element
  * below 2^-32 of its row's largest is off by at most 2^-39 of that); scores, sums and O are
  * fp32, the weights of the second product (softmax times V scale, relative to the row's
  * largest) are rounded to fp16.  A V scale below 2^-60 of the sequence's largest, or of 1,
@@ -492,14 +492,15 @@ attn_status_t attn_selftest_wait_timeout(unsigned long long timeout_ns, void* st
 
 /*
  * attn_selftest_fwd_withheld_load, attn_selftest_quant_withheld_load,
- * attn_selftest_bwd_withheld_load -- diagnostics for the abort path of the real
+ * attn_selftest_bwd_withheld_load, attn_selftest_decode_fp8_withheld_load -- diagnostics for the abort path of the real
  * kernels (no page describes them: they test this library's failure detection).
  * Each runs the production kernel of attn_fwd_bf16 (scale 1/sqrt(d), no window),
- * of attn_quantize_fp8_blockwise (E4M3, block 128) or of attn_bwd_bf16 on the
- * given tensors, with two differences: every wait is bounded by `timeout_ns`
+ * of attn_quantize_fp8_blockwise (E4M3, block 128), of attn_bwd_bf16 or of
+ * attn_decode_fp8_paged (scale 1/sqrt(d), no window) on the given tensors, with two differences: every wait is bounded by `timeout_ns`
  * instead of the usual 4 s, and in every CTA the load with index `withheld`
- * (0-based, counted over that CTA's K/V tiles, its 128-row blocks, or its
- * backward ring tiles) is never issued.  The waits on it run out; the CTA raises
+ * (0-based, counted over that CTA's K/V tiles, its 128-row blocks, its
+ * backward ring tiles, or its cache tiles, K and V counted apart above 16 rows per
+ * key head) is never issued.  The waits on it run out; the CTA raises
  * its abort flag, lets the copies and MMAs it already issued finish, frees its
  * tensor memory and exits, and ATTN_ERR_TIMEOUT is recorded for
  * attn_get_device_status().  The outputs are then unspecified; the context stays
@@ -521,6 +522,12 @@ attn_status_t attn_selftest_bwd_withheld_load(const void* q, const void* k, cons
                                               size_t workspace_bytes, int B, int H, int N, int d,
                                               int causal, int withheld,
                                               unsigned long long timeout_ns, void* stream);
+attn_status_t attn_selftest_decode_fp8_withheld_load(
+    const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
+    const float* v_scales, const int* page_table, const int* seq_lens, void* o, float* lse, int B,
+    int H, int Hkv, int nq, int d, int page_size, int num_pages, int max_pages, int block,
+    int format, void* workspace, size_t workspace_bytes, int withheld,
+    unsigned long long timeout_ns, void* stream);
 
 /*
  * attn_selftest_fp8_convert -- diagnostic: the device's FP8 conversion (the one the

@@ -587,6 +587,38 @@ def test_decode_fp8_bad_page_numbers_stay_inside(fa):
     check_decode(fa, [100, 40], 2, 2, 1, 64, 32, 32, "e4m3", seed=19)
 
 
+@pytest.mark.parametrize("withheld", [0, 3])
+@pytest.mark.parametrize("d,group,nq", [(64, 1, 1), (128, 8, 1), (128, 16, 1), (256, 1, 2),     # narrow
+                                        (64, 8, 4), (128, 8, 4), (128, 8, 8), (256, 16, 8)])    # wide
+@pytest.mark.parametrize("B,L", [(5, 8000), (70, 1000)])       # fewer units than CTAs, and more
+def test_decode_fp8_kernels_abort_on_a_withheld_load(fa, B, L, d, group, nq, withheld):
+    """One load of every CTA is never issued: the bounded waits on it run out, the status says
+    so, the joining kernel stays inside whatever the workspace held, and the next call is
+    right."""
+    g = torch.Generator(device="cuda").manual_seed(withheld + d)
+    Hkv, ps = 8, 64
+    width = -(-L // ps)
+    kc, vc = (torch.randint(0, 0x78, (B * width, Hkv, ps, d), dtype=torch.uint8, device="cuda", generator=g) for _ in range(2))
+    ks, vs = (torch.rand(B * width, Hkv, 1, device="cuda", generator=g) * 0.01 for _ in range(2))
+    table = torch.randperm(B * width, device="cuda", generator=g).to(torch.int32).view(B, width)
+    if group * nq > 16:
+        table = cuda(widen(table.cpu().numpy(), ps))
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    lens[B // 2] = 0
+    q = torch.randn(B, group * Hkv, nq, d, device="cuda", generator=g).bfloat16()
+    o1, lse1 = fa.attn_decode_fp8_paged(q, kc, vc, ks, vs, table, lens)
+    assert fa.attn_get_device_status() == fa.ATTN_OK
+    need = fa.attn_decode_fp8_workspace_bytes(group * Hkv, Hkv, nq, d)
+    ws = torch.randint(0, 6, (need // 4,), dtype=torch.int32, device="cuda", generator=g)
+    ws[::5] = torch.randint(-2 ** 31, 2 ** 31 - 1, ws[::5].shape, dtype=torch.int32, device="cuda", generator=g)
+    fa.attn_selftest_decode_fp8_withheld_load(q, kc, vc, ks, vs, table, lens, torch.empty_like(o1),
+                                              torch.empty_like(lse1), ws, withheld=withheld)
+    assert fa.attn_get_device_status() == fa.ATTN_ERR_TIMEOUT
+    o2, lse2 = fa.attn_decode_fp8_paged(q, kc, vc, ks, vs, table, lens)
+    assert fa.attn_get_device_status() == fa.ATTN_OK
+    assert torch.equal(o1, o2) and torch.equal(lse1, lse2)
+
+
 # ------------------------------------------------------------------ together
 def serve(fa, fmt, steps, seed=0, graph=False):
     """A small serving loop: a prefill step, then decoding steps; returns the outputs of every

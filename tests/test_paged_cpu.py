@@ -82,6 +82,12 @@ def test_decode_fp8_argument_errors(lib, change, expected):
     assert lib.attn_decode_fp8_paged(*args, None) == expected
 
 
+@pytest.mark.parametrize("withheld,limit,expected", [(-1, 10 ** 6, 1), (0, 0, 1), (0, 3 * 10 ** 9, 1)])
+def test_decode_fp8_selftest_argument_errors(lib, withheld, limit, expected):
+    args = DECODE[:19] + DECODE[21:] + [withheld, limit]
+    assert lib.attn_selftest_decode_fp8_withheld_load(*args, None) == expected
+
+
 def test_binding_refuses_cpu_tensors():
     import exact_attention_55_gb300 as fa
     i = torch.zeros(2, dtype=torch.int32)
