@@ -135,53 +135,59 @@ __device__ __forceinline__ Dec8Line dec8_line(const DecodeFp8Params& p, Dec8Setu
     return line;
 }
 
-// A CTA's walk over its range [a, e): unit (b, hk), which starts at s0 of the line, and the
-// unit's tiles that are this range's, [k0, k1).
+// A CTA's walk over its range: unit (b, hk), which starts `at` behind the range's start (or
+// before it: negative), and the unit's tiles that are this range's, [k0, k1).  A range is
+// taken as at most 2^30 long (2^36 keys).  Lengths that change under the call can lead it
+// astray, but not out of the tensors.
 template <int TILE>
 struct Dec8Walk {
     Dec8Seq seq;
-    long long a, e, s0;
-    int b, hk, span, unit_cost, k0, k1;
+    int len, at, b, hk, span, unit_cost, k0, k1;
     bool more;
 
     template <int THREADS>
     __device__ __forceinline__ Dec8Walk(const DecodeFp8Params& p, const Dec8Line& line, const Dec8Setup<THREADS>& sh, int x)
-        : a(line.cut(x)), e(line.cut(x + 1)), b(sh.b0), unit_cost(line.unit_cost)
+        : b(sh.b0), unit_cost(line.unit_cost)
     {
+        const long long a = line.cut(x);
+        len = (int)min(line.cut(x + 1) - a, 1LL << 30);
         seq = dec8_seq<TILE>(p, b);
         span = dec8_span(p, seq.n);
-        hk = min((int)dec8_div(a - sh.first, max(span + unit_cost, 1)), p.Hkv - 1);
-        s0 = sh.first + (long long)hk * (span + unit_cost);
+        hk = (int)min((unsigned)dec8_div(a - sh.first, span + unit_cost), (unsigned)(p.Hkv - 1));
+        at = (int)(sh.first + (long long)hk * (span + unit_cost) - a);
         take(p);
         more = k1 > k0 || next(p);
     }
     __device__ __forceinline__ void take(const DecodeFp8Params& p)
     {
-        k0 = (int)max(0LL, a - s0 - unit_cost);
-        k1 = (int)max((long long)k0, min((long long)span, e - s0 - unit_cost));
+        k0 = max(0, -at - unit_cost);
+        k1 = max(k0, min(span, len - at - unit_cost));
         if (p.whole && k1 > k0) k1 = seq.n;
     }
     // to the next unit with tiles of this range; false, and the end of the walk, if there is none
     __device__ __forceinline__ bool next(const DecodeFp8Params& p)
     {
         do {
-            s0 += span + unit_cost;
-            if (s0 + unit_cost >= e) return more = false;
+            at += span + unit_cost;
+            if (at + unit_cost >= len) return more = false;
             if (++hk == p.Hkv) {
                 hk = 0;
                 do {
-                    if (b + 1 >= p.B) return more = false;   // only if the lengths change under the call
-                    seq = dec8_seq<TILE>(p, ++b);
-                } while (seq.n == 0);
+                    b = min(b + 1, p.B - 1);
+                    seq = dec8_seq<TILE>(p, b);
+                } while (seq.n == 0 && b < p.B - 1);
                 span = dec8_span(p, seq.n);
             }
             take(p);
-        } while (k1 <= k0);
-        return more = true;
+        } while (k1 <= k0 && span > 0);
+        return more = k1 > k0;
     }
     __device__ __forceinline__ bool whole() const { return k1 - k0 == seq.n; }
-    // the range that has the unit's last tile
-    __device__ __forceinline__ int last_owner(const Dec8Line& line) const { return line.owner(s0 + unit_cost + seq.n - 1); }
+    // the range that has the unit's last tile, as range x sees it
+    __device__ __forceinline__ int last_owner(const Dec8Line& line, int x) const
+    {
+        return line.owner(line.cut(x) + at + unit_cost + seq.n - 1);
+    }
 };
 
 // What the combine kernel finds at the workspace's start: an entry per unit (and row group),
@@ -200,7 +206,7 @@ __device__ __forceinline__ void dec8_name_parts(const DecodeFp8Params& p, const 
     const bool per_unit = dec8_per_unit(p);
     if (!per_unit && w.whole()) return;
     reinterpret_cast<int4*>(p.ws)[per_unit ? (w.b * p.Hkv + w.hk) * p.row_groups + rg : blockIdx.x] =
-        w.whole() ? make_int4(-1, 0, 0, 0) : make_int4(x, w.last_owner(line), rg, (int)unit_row);
+        w.whole() ? make_int4(-1, 0, 0, 0) : make_int4(x, w.last_owner(line, x), rg, (int)unit_row);
 }
 
 // This CTA's part of the unit it is on.

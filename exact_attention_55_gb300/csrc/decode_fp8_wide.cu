@@ -23,7 +23,7 @@
 // converted as 0 and noted; the rows that see it get their NaN when the unit is written.
 //
 // Measured, 16 sequences x 8 key heads x 8192 keys, d 128 (39.5 us at the copy rate): 32 rows
-// 69 us, 64 rows 77, 128 rows 155 (102, 187 and 364 in passes of 16 rows); d 256, 128 rows 152
+// 69 us, 64 rows 76, 128 rows 156 (102, 187 and 364 in passes of 16 rows); d 256, 128 rows 150
 // (842).  Neither HBM (48 %) nor the tensor pipe (44 %) bounds it, but the chain of a softmax
 // warp per tile (S arrives, maximum, weights, P leaves), whose warps share the issue slots with
 // the eight that convert; at 128 rows each of its threads has all of a tile's 128 keys.  Loading and
@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                     const uint32_t s = h % C::RING;
                     if (!wait_lane0(&sh->kv_empty[s], ((h / C::RING) & 1) ^ 1)) break;
                     const uint32_t fb = smem_u32(&sh->kv_full[s]);
-                    if (++h == p.withhold) continue;
-                    if (lane == 0) mbar_arrive_expect_tx(fb, C::HALF);
+                    const bool issue = ++h != p.withhold;
+                    if (lane == 0 && issue) mbar_arrive_expect_tx(fb, C::HALF);
                     __syncwarp();
                     // The tile's scales complete on the barrier of its K half, so whoever has seen
                     // S of the tile may read them.  Their place is free: the half that makes room
@@ -205,13 +205,13 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                     // before it gives up that tile's S.
                     const size_t at = (((size_t)pg_part * p.Hkv + w.hk) << (p.log2_ps - p.log2_blk)) +
                                       ((part_key & ps_mask) >> p.log2_blk);
-                    if (which == 0 && lane < 2 * C::PARTS)
+                    if (which == 0 && lane < 2 * C::PARTS && issue)
                         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
                                          smem_u32(&sh->scale[t % C::SC_RING][lane])),
                                      "l"((lane < C::PARTS ? p.ks : p.vs) + at) : "memory");
-                    if (lane < 2 * C::PARTS)
+                    if (lane < 2 * C::PARTS && issue)
                         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
-                    if (lane < nbox) {
+                    if (lane < nbox && issue) {
                         const uint32_t dst = smem_u32(ring + s * C::HALF) + (lane << log2_r) * C::CB;
 #pragma unroll
                         for (int c = 0; c < C::NCB; ++c)
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                 load(0);
                 const bool edge = key0 + C::KEYS - 1 > w.seq.L - p.nq ||
                                   (p.window > 0 && key0 < w.seq.L - 1 - p.window);
-                float kf[BLOCKS], ve[BLOCKS], vf[BLOCKS], vinv[BLOCKS];
+                float kf[BLOCKS], ve[BLOCKS], vf[BLOCKS];
 #pragma unroll
                 for (int b = 0; b < BLOCKS; ++b) {
                     kf[b] = sh->scale[sc][copy * BLOCKS + b] * rowc;
@@ -474,7 +474,6 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                     const Dec8ValueScale vs(vsc, v_top);
                     ve[b] = vs.e;
                     vf[b] = vs.f;
-                    vinv[b] = vs.inv;
                 }
                 if constexpr (C::KEYS == PIECE) {
                     tc_fence_before_sync();
@@ -542,7 +541,7 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                             const float2 g = __fmul2_rn(e, f);
                             sr[b * 8 + i] = dec8_pack_half2(g.x, g.y);
                         }
-                        l = fmaf(sum.x + sum.y, vinv[at / 16 + b], l);
+                        l = fmaf(sum.x + sum.y, __int_as_float((127 - (int)ve[at / 16 + b]) << 23), l);
                     }
                     if constexpr (PIECE == 64) {
                         tmem_st32p(to + at / 2, sr);
