@@ -36,7 +36,7 @@ namespace cg = cooperative_groups;
 // lengths and the free count may be overwritten in place after that), and then its
 // threads share the tokens, pages and requests.  A token finds its request by bisection
 // of the ends, four tokens at a time; a page that the step takes is read from the free stack,
-// never from the table entry another thread writes.  Measured: 16 requests of one token 3.5
+// never from the table entry another thread writes.  Measured: 16 requests of one token 3.3
 // us, 1024 requests with 29 thousand tokens 8.4 us (11.7 with a third scan and lookups one by
 // one), of which a launch is about 2 and the dependent reads of lengths and pages 2.
 constexpr int kPlanMaxThreads = 1024;
@@ -206,7 +206,7 @@ cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream)
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, paged_plan_kernel, p);
 }
 
@@ -283,7 +283,8 @@ cudaError_t launch_cache_append_bf16(const AppendParams& p, cudaStream_t stream)
 // one by one 143, the bookkeeping of several runs for every tile 142).  The issue slots are 68 %
 // busy (100 instructions per warp and 8 values a lane, half of them the quotients) and HBM 60
 // %, in turns: a tile's loads, its maximum and its codes follow one another, four CTAs an SM.
-// A step of 61 tokens takes 5.5 us, four dependent reads (slots, rows, scale, launch) long.
+// A step of 61 tokens takes 4.6 us, three dependent reads (slots, rows or scale, launch) long, and 7
+// where one block in ten grows.
 constexpr int kAppendWindow = 256;     // tokens a CTA looks at: tile + block - 1 < 256
 constexpr int kAppendHeld = 128;       // rows held in registers
 
@@ -344,6 +345,59 @@ __device__ __noinline__ uint2 divide8(uint4 w, float s)
     return make_uint2(out[0], out[1]);
 }
 
+// Codes of (code * old) / s, products and quotients IEEE fp32, for four codes.  The quotient by
+// the reciprocal, corrected by its residual twice: after the first time it is within one ulp,
+// where the residual is exact, and with y = RN(1 / s) the second correction rounds to the
+// quotient itself (Markstein 1990).  Finite codes; 1e-24 < s < 1e30 keeps the residual of every
+// quotient that is not rounded to 0 above fp32's smallest step.
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float old, float s, float y)
+{
+    const float2 o = make_float2(old, old), n = make_float2(-s, -s), y2 = make_float2(y, y);
+    const float2 a = __fmul2_rn(unpack2_fp8<kE5M2>(w & 0xFFFFu), o), b = __fmul2_rn(unpack2_fp8<kE5M2>(w >> 16), o);
+    float2 qa = __fmul2_rn(a, y2), qb = __fmul2_rn(b, y2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        qa = __ffma2_rn(__ffma2_rn(qa, n, a), y2, qa);
+        qb = __ffma2_rn(__ffma2_rn(qb, n, b), y2, qb);
+    }
+    return pack4_fp8<kE5M2>(qa.x, qa.y, qb.x, qb.y) | (w & 0x80808080u);
+}
+
+// Four codes by division: scales near fp32's limits, codes that are not finite.
+template <bool kE5M2>
+__device__ __noinline__ uint32_t redivide4(uint32_t w, float old, float s)
+{
+    const float2 a = unpack2_fp8<kE5M2>(w & 0xFFFFu), b = unpack2_fp8<kE5M2>(w >> 16);
+    return pack4_fp8<kE5M2>(__fdiv_rn(a.x * old, s), __fdiv_rn(a.y * old, s), __fdiv_rn(b.x * old, s),
+                            __fdiv_rn(b.y * old, s));
+}
+
+// The earlier rows (n pieces of 16 codes) of a block whose scale grew from old to s, by the
+// CTA; out of line: few blocks grow.  (A warp a block, four codes a lane and IEEE divisions, took
+// 346 us where every block of 64 tokens and 8 heads grew under 60 rows; a code of 0 alone sends a
+// division down its long path.)
+template <bool kE5M2>
+__device__ __noinline__ void requantise(uint4* codes, int n, float old, float s)
+{
+    const float y = s > 1e-24f && s < 1e30f ? __frcp_rn(s) : 0.0f;
+    for (int at = threadIdx.x; at < n; at += blockDim.x) {
+        const uint4 u = codes[at];
+        uint32_t w[4] = {u.x, u.y, u.z, u.w}, odd = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            odd |= kE5M2 ? (w[k] & 0x7C7C7C7Cu) + 0x04040404u : (w[k] & 0x7F7F7F7Fu) + 0x01010101u;
+        if (y == 0.0f || (odd & 0x80808080u)) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = redivide4<kE5M2>(w[k], old, s);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = rescale4<kE5M2>(w[k], old, s, y);
+        }
+        codes[at] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 template <int D> struct AppendCfg {
     static constexpr int LPR = D / 8;                       // lanes of a row, 8 values each
     static constexpr int THREADS = D == 256 ? 512 : 256;
@@ -365,7 +419,7 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
     __shared__ int grown[kAppendWindow];
     __shared__ int num_grown[2], warp_last[kAppendWindow / 32], first_row, end_row;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int block = 1 << p.log2_blk, tile = block < 64 ? 64 : block, ps_mask = (1 << p.log2_ps) - 1;
+    const int block = 1 << p.log2_blk, tile = p.tile, ps_mask = (1 << p.log2_ps) - 1;
     const long long t0 = (long long)blockIdx.x * tile;
     const int window = (int)min((long long)(tile + block - 1), p.T - t0);
 
@@ -452,6 +506,15 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
             a = __reduce_max_sync(row_lanes, a);
             if (run >= 0 && c == 0) atomicMax(&run_max[run], a << 16);
         };
+        // a run's first thread: where its scale is, read while the rows arrive
+        float* sc = nullptr;
+        float old = 0.0f;
+        if (tid < tile && run_of[tid] == tid) {
+            const long long s0 = slots[tid];
+            sc = scales + ((((s0 >> p.log2_ps) * p.H + h) << (p.log2_ps - p.log2_blk)) +
+                           ((s0 & ps_mask) >> p.log2_blk));
+            if ((s0 & (block - 1)) > 0) old = *sc;
+        }
         uint4 x[C::HELD];
         auto load_rows = [&](int from) {             // 128 rows, their loads in flight together
 #pragma unroll
@@ -491,15 +554,11 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
             }
         }
         __syncthreads();
-        if (tid < tile && run_of[tid] == tid) {
-            const long long s0 = slots[tid];
-            const int row = (int)(s0 & (block - 1));
-            float* sc = scales + ((((s0 >> p.log2_ps) * p.H + h) << (p.log2_ps - p.log2_blk)) +
-                                  ((s0 & ps_mask) >> p.log2_blk));
+        if (sc) {
+            const int row = (int)(slots[tid] & (block - 1));
             const bool finite = run_odd[tid] == 0;
             float need = __fdiv_rn(__uint_as_float(run_max[tid]), kE5M2 ? 57344.0f : 448.0f);
             if (p.pow2) need = pow2_at_least(need);
-            const float old = row > 0 ? *sc : 0.0f;
             const float s = fmaxf(old, need);
             run_old[tid] = old;
             run_scale[tid] = s > 0.0f ? s : 1.0f;
@@ -537,26 +596,28 @@ __global__ void __launch_bounds__(AppendCfg<D>::THREADS, D == 256 ? 2 : 4)
                 }
             }
         }
-        // blocks whose scale grew: their earlier rows, one warp a block
-        for (int k = warp; k < num_grown[odd]; k += C::THREADS / 32) {
+        // blocks whose scale grew: their earlier rows
+        for (int k = 0; k < num_grown[odd]; ++k) {
             const int run = grown[k];
             const int row = (int)(slots[run] & (block - 1));
-            const float old = run_old[run], s = run_scale[run];
-            uint32_t* base = reinterpret_cast<uint32_t*>(cache + row_address(slots[run] - row));
-            for (int w = lane; w < row * (D / 4); w += 32) {
-                const uint32_t codes = base[w];
-                const float2 a = unpack2_fp8<kE5M2>(codes & 0xFFFFu), b = unpack2_fp8<kE5M2>(codes >> 16);
-                base[w] = pack4_fp8<kE5M2>(__fdiv_rn(a.x * old, s), __fdiv_rn(a.y * old, s),
-                                           __fdiv_rn(b.x * old, s), __fdiv_rn(b.y * old, s));
-            }
+            requantise<kE5M2>(reinterpret_cast<uint4*>(cache + row_address(slots[run] - row)), row * (D / 16),
+                              run_old[run], run_scale[run]);
         }
     }
 }
 
 template <int D>
-static cudaError_t launch_append_fp8_d(const AppendParams& p, bool e5m2, cudaStream_t stream)
+static cudaError_t launch_append_fp8_d(AppendParams p, bool e5m2, cudaStream_t stream)
 {
-    const int block = 1 << p.log2_blk, tile = block < 64 ? 64 : block;
+    const int block = 1 << p.log2_blk;
+    // small steps take small tiles while the grid is one wave: a tile's tokens are mostly runs of
+    // their own, whose blocks may each have earlier rows to requantise (64 tokens of 8 heads, every
+    // block growing under 60 rows: 64 tokens a tile 27, 8 11.8, 4 9.0 us; one in ten 15, 7.3, 6.8;
+    // none 5.1, 4.1, 4.2)
+    int tile = 8;
+    while (tile < 64 && ((long long)p.T + tile - 1) / tile * 2 * p.H > 4LL * p.sm_count) tile *= 2;
+    if (tile == 64 && block > 64) tile = block;
+    p.tile = tile;
     const long long tiles = ((long long)p.T + tile - 1) / tile;
     // a head of K or V per CTA while there are few, else about 36 CTAs per SM, each with
     // several of its tile's heads (31826 tokens of 16 heads, d 128: 8 per SM 103.0 us, 12 90.6,

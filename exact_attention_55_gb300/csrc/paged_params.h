@@ -33,6 +33,7 @@ struct AppendParams {
     long long k_stride, v_stride;  // elements
     long long num_slots;    // num_pages << log2_ps
     int T, H, d;
+    int tile;               // tokens whose runs a CTA takes (8-bit caches; the launcher's)
     int log2_ps, log2_blk;
     int pow2;               // scales are rounded up to powers of two
     int sm_count;

@@ -421,7 +421,7 @@ attn_status_t attn_cache_append_bf16(const void* k, const void* v, void* k_cache
  *   k_scales, v_scales : float [num_pages, Hkv, page_size / block]
  *   block  : 16, 32, 64 or 128, at most page_size; page_size a power of two, 16 .. 65536
  *   format : an attn_fp8_format_t, the same in every call on a cache
- * The tokens of one block must be consecutive in the call, in ascending slots, as
+ * The tokens of one block must be consecutive in the call, in ascending slots, none skipped, as
  * attn_paged_plan packs them; otherwise that block's rows and scale are unspecified (no
  * other block's are).
  */
