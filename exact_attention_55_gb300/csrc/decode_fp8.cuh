@@ -26,7 +26,7 @@ namespace gb300 {
 // Tiles a unit's start and end are worth (48 ragged sequences of 8 key heads: 1 36.1, 2 34.6,
 // 4 35.3, 6 35.7, 10 37.7 us; 32 windowed heads 23.8, 22.9, 21.2, 22.3, 23.0).
 constexpr int kD8UnitCost = 4;
-constexpr int kD8CombineThreads = 128;
+constexpr int kD8CombineThreads = 128, kD8CombineFew = 8;
 
 // Floats of a part: O [rows][d], maxima [rows], sums [rows].
 __host__ __device__ constexpr int dec8_part(int rows, int d) { return rows * (d + 2); }
@@ -293,13 +293,14 @@ __device__ __forceinline__ void dec8_timeout(const DecodeFp8Params& p, int* abor
 // O = sum_x 2^(M_x - M) a_x / sum_x 2^(M_x - M) l_x.  grid.x: the units, or where there are
 // more of them the ranges (each leaves at most one unit to its successors); grid.y shares
 // a unit's rows and columns.  Latency-bound: a thread has all its parts' loads in flight
-// together.  Up to eight parts (the usual batch), a thread joins one float4 of one row;
-// more (one long sequence), 32 columns of a row at a time, sixteen threads a float4.
+// together.  Up to few_max parts (the usual batch, or many rows) a thread joins one float4 of
+// one row, eight parts at a time; more (one long sequence), 32 columns of a row at a time,
+// sixteen threads a float4.  few_max is where both take the same number of rounds.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(const DecodeFp8Params p)
+__global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(const DecodeFp8Params p, const int few_max)
 {
     constexpr int PART = dec8_part(ROWS, D);
-    constexpr int FEW = 8, MANY = 10;                        // parts of a thread
+    constexpr int FEW = kD8CombineFew, MANY = 10;            // parts of a thread at a time
     constexpr int COLS = 8, GROUPS = kD8CombineThreads / COLS, SLICES = D / 32;
     __shared__ float4 sm_a[GROUPS][COLS];
     __shared__ float2 sm_ml[GROUPS];
@@ -353,12 +354,12 @@ __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(c
             a.z = fmaf(fac, v[k].z, a.z), a.w = fmaf(fac, v[k].w, a.w);
         }
     };
-    if (x1 - x0 < FEW) {
+    if (x1 - x0 < few_max) {
         for (int i = blockIdx.y * kD8CombineThreads + tid; i < rows * (D / 4); i += gridDim.y * kD8CombineThreads) {
             const int r = i / (D / 4), col = i - r * (D / 4);
             float M = NEG_INF, l = 0.0f;
             float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            join(std::integral_constant<int, FEW>{}, x0, 1, r, col, M, l, a);
+            for (int x = x0; x <= x1; x += FEW) join(std::integral_constant<int, FEW>{}, x, 1, r, col, M, l, a);
             finish(r, col, a, l, M);
         }
         return;
@@ -408,7 +409,9 @@ cudaError_t launch_decode_fp8_combine(const DecodeFp8Params& p, cudaLaunchConfig
     cfg.gridDim = dim3((unsigned)(units < ctas ? units : ctas), share);
     cfg.blockDim = dim3(kD8CombineThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, decode_fp8_combine_kernel<D, ROWS>, p);
+    const int few_rounds = (least + share - 1) / share, many_rounds = (items + share - 1) / share;
+    const int few_max = kD8CombineFew * (many_rounds > few_rounds ? many_rounds / few_rounds : 1);
+    return cudaLaunchKernelEx(&cfg, decode_fp8_combine_kernel<D, ROWS>, p, few_max);
 }
 
 }  // namespace gb300
