@@ -293,9 +293,11 @@ __device__ __forceinline__ void dec8_timeout(const DecodeFp8Params& p, int* abor
 // O = sum_x 2^(M_x - M) a_x / sum_x 2^(M_x - M) l_x.  grid.x: the units, or where there are
 // more of them the ranges (each leaves at most one unit to its successors); grid.y shares
 // a unit's rows and columns.  Latency-bound: a thread has all its parts' loads in flight
-// together.  Up to few_max parts (the usual batch, or many rows) a thread joins one float4 of
-// one row, eight parts at a time; more (one long sequence), 32 columns of a row at a time,
-// sixteen threads a float4.  few_max is where both take the same number of rounds.
+// together.  Up to few_max parts (the usual batch) a thread joins one float4 of one row;
+// more (one long sequence), 32 columns of a row at a time, sixteen threads a float4.  few_max
+// is eight, or with the wide kernel's many rows, eight parts at a time, where both ways take
+// the same number of rounds (8 x 8000 keys under 64 heads, d 256: 34.3 for 29.6 us without;
+// with up to 16 rows the rounds' loop only cost 0.4 us of 20).
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(const DecodeFp8Params p, const int few_max)
 {
@@ -354,12 +356,15 @@ __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(c
             a.z = fmaf(fac, v[k].z, a.z), a.w = fmaf(fac, v[k].w, a.w);
         }
     };
-    if (x1 - x0 < few_max) {
+    if (x1 - x0 < (ROWS > 16 ? few_max : FEW)) {
         for (int i = blockIdx.y * kD8CombineThreads + tid; i < rows * (D / 4); i += gridDim.y * kD8CombineThreads) {
             const int r = i / (D / 4), col = i - r * (D / 4);
             float M = NEG_INF, l = 0.0f;
             float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int x = x0; x <= x1; x += FEW) join(std::integral_constant<int, FEW>{}, x, 1, r, col, M, l, a);
+            if constexpr (ROWS > 16)
+                for (int x = x0; x <= x1; x += FEW) join(std::integral_constant<int, FEW>{}, x, 1, r, col, M, l, a);
+            else
+                join(std::integral_constant<int, FEW>{}, x0, 1, r, col, M, l, a);
             finish(r, col, a, l, M);
         }
         return;
@@ -410,7 +415,7 @@ cudaError_t launch_decode_fp8_combine(const DecodeFp8Params& p, cudaLaunchConfig
     cfg.blockDim = dim3(kD8CombineThreads);
     cfg.dynamicSmemBytes = 0;
     const int few_rounds = (least + share - 1) / share, many_rounds = (items + share - 1) / share;
-    const int few_max = kD8CombineFew * (many_rounds > few_rounds ? many_rounds / few_rounds : 1);
+    const int few_max = kD8CombineFew * (many_rounds > few_rounds ? many_rounds / few_rounds : 1);   // used above 16 rows
     return cudaLaunchKernelEx(&cfg, decode_fp8_combine_kernel<D, ROWS>, p, few_max);
 }
 

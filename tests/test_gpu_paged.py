@@ -431,6 +431,12 @@ def test_decode_fp8_wide_short_tables(fa):
     check_decode(fa, lens, 64, 4, 8, 64, 64, 64, "e4m3", seed=31)
 
 
+@pytest.mark.parametrize("d,H", [(256, 64), (128, 48), (64, 128)])
+def test_decode_fp8_wide_many_parts(fa, d, H):
+    """A few sequences over one key head: each unit's many rows come in many parts."""
+    check_decode(fa, [2600, 3100, 1, 2900, 3000, 700, 2750, 3090], H, 1, 1, d, 64, 64, "e4m3", seed=d, wide=True)
+
+
 def test_decode_fp8_wide_long(fa):
     """Parts of long and short sequences, several CTAs on each, joined."""
     check_decode(fa, [20001, 3, 7000, 1, 129], 32, 1, 1, 128, 64, 64, "e4m3_pow2", seed=32, wide=True)
