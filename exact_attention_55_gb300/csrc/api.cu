@@ -1160,7 +1160,9 @@ static attn_status_t decode_fp8(
     p.c_log2 = (float)((double)scale * 1.4426950408889634);
     p.ws = static_cast<float*>(workspace);
     p.whole = (long long)max_pages * page_size <= kDecodeWholeKeys ? 1 : 0;
-    p.ranges = plan.ranges;
+    // no more CTAs than there can be units, or tiles (64 keys or more, one more for a window's ends)
+    const long long most = (long long)B * Hkv * (p.whole ? 1 : keys / 64 + 2);
+    p.ranges = plan.ranges < most ? plan.ranges : (int)most;
     p.row_groups = plan.row_groups;
     p.status = dev->status;
     p.timeout_ns = timeout_ns;
