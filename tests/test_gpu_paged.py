@@ -816,6 +816,30 @@ def test_calls_on_other_streams(fa):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_decode_fp8_kernels_side_by_side(fa):
+    """Narrow and wide kernels of several head sizes on streams of their own, in flight together,
+    give what each gives alone; so do two calls of one kind."""
+    rng = np.random.default_rng(90)
+    calls = []
+    for d, H, nq, wide in ((64, 32, 4, True), (128, 16, 4, True), (128, 16, 4, True), (256, 32, 8, True),
+                           (128, 8, 1, False), (64, 2, 8, False), (256, 8, 1, False), (128, 8, 1, False)):
+        lens = [int(n) for n in rng.integers(1, 6000, 12)]
+        kc, vc, ks, vs, table = ref.make_cache(rng, lens, 2, d, 64, 64, "e4m3", stale=False)
+        if wide:
+            table = widen(table, 64)
+        q = torch.from_numpy(rng.standard_normal((len(lens), H, nq, d)).astype(np.float32)).bfloat16().cuda()
+        calls.append((q, *(cuda(a) for a in (kc, vc, ks, vs, table, np.array(lens, np.int32)))))
+    alone = [fa.attn_decode_fp8_paged(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        got = [fa.attn_decode_fp8_paged(*c, stream=st) for c, st in zip(calls, streams) for _ in range(2)]
+        torch.cuda.synchronize()
+        for i, (o, lse) in enumerate(got):
+            assert torch.equal(o, alone[i // 2][0]) and torch.equal(lse, alone[i // 2][1])
+    assert fa.attn_get_device_status() == fa.ATTN_OK
+
+
 def test_workspace_belongs_to_the_calls_stream(fa):
     """Calls on a given stream without a workspace, while the current stream allocates and
     overwrites blocks of the same sizes: nobody else gets a workspace that is in use."""
