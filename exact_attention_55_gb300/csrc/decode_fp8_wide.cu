@@ -23,7 +23,7 @@
 // converted as 0 and noted; the rows that see it get their NaN when the unit is written.
 //
 // Measured, 16 sequences x 8 key heads x 8192 keys, d 128 (39.5 us at the copy rate): 32 rows
-// 69 us, 64 rows 76, 128 rows 156 (102, 187 and 364 in passes of 16 rows); d 256, 128 rows 150
+// 68 us, 64 rows 77, 128 rows 157 (102, 187 and 364 in passes of 16 rows); d 256, 128 rows 153
 // (842).  Neither HBM (48 %) nor the tensor pipe (44 %) bounds it, but the chain of a softmax
 // warp per tile (S arrives, maximum, weights, P leaves), whose warps share the issue slots with
 // the eight that convert; at 128 rows each of its threads has all of a tile's 128 keys.  Loading and
@@ -386,28 +386,39 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
         };
         // The unit's query row into tensor memory as fp16, scaled by a power of two so that its
         // largest value is just below 2^15; returns the softmax scale over that factor.
+        // Held in registers between the two (HOLD) the row costs one latency instead of D / 32; us, held
+        // and read twice: 32 rows d 128 68.0 / 70.1, d 256 124.9 / 128.2, 64 rows d 256 135.5 / 142.4, but
+        // 64 rows d 128 91 / 76, 128 rows d 128 179 / 156, d 256 173 / 151 (the loop's registers).
         auto put_q = [&](uint32_t unit) -> float {
+            constexpr bool HOLD = COPIES == 4 || (COPIES == 2 && D == 256);
             const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
                                                             (((size_t)w.b * p.Hkv + w.hk) * p.rows + row0 + (live ? row : 0)) * D);
             uint32_t big = 0;
-#pragma unroll 8
-            for (int i = 0; i < D / 8; ++i) {
-                const uint4 u = __ldg(q + i);
+            auto largest = [&](const uint4& u) {
                 big = max(max(big, max((u.x << 16) & 0x7FFF0000u, u.x & 0x7FFF0000u)),
                           max(max((u.y << 16) & 0x7FFF0000u, u.y & 0x7FFF0000u),
                               max(max((u.z << 16) & 0x7FFF0000u, u.z & 0x7FFF0000u),
                                   max((u.w << 16) & 0x7FFF0000u, u.w & 0x7FFF0000u))));
+            };
+            uint4 held[HOLD ? D / 8 : 1];
+            if constexpr (HOLD) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) held[i] = __ldg(q + i);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) largest(held[i]);
+            } else {
+#pragma unroll 8
+                for (int i = 0; i < D / 8; ++i) largest(__ldg(q + i));
             }
             const int ex = max((int)(big >> 23), 15) - 14;       // biased exponent of the factor's inverse
             const float down = live ? __int_as_float((254 - ex) << 23) : 0.0f;
             if (!wait_all(&sh->q_empty, (unit & 1) ^ 1)) return 0.0f;
             tc_fence_after_sync();
-#pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
+            auto put = [&](int c) {                              // 64 of the row's values
                 uint32_t f[32];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint4 u = __ldg(q + c * 8 + i);
+                    const uint4 u = HOLD ? held[HOLD ? c * 8 + i : 0] : __ldg(q + c * 8 + i);
                     const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -416,6 +427,13 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                                             : 0u;
                 }
                 tmem_st32p(lanes + C::Q_COL + c * 32, f);
+            };
+            if constexpr (HOLD) {
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) put(c);
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) put(c);
             }
             tmem_wait_st();
             tc_fence_before_sync();
