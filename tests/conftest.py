@@ -15,6 +15,14 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: CPU test that takes more than a few seconds")
 
 
+@pytest.fixture(scope="session", autouse=True)
+def _vector_math_initialised():
+    """torch's float64 logarithm and exponential on several threads at their very first use were
+    off by 1e-10 in about one process of ten; once one thread has used them they are not."""
+    import torch
+    torch.logsumexp(torch.zeros(2, 3, 45, 45, dtype=torch.float64), -1)
+
+
 def require_gpu():
     import torch
     if not torch.cuda.is_available():
