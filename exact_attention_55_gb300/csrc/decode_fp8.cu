@@ -8,10 +8,11 @@
 // Row r = g * nq + i of key head hk is query i of head hk * G + g, at position L - nq + i;
 // it sees keys max(0, position - window) .. position (window 0: all of them).  With key
 // scales ks and value scales vs = f 2^e (1 <= f < 2), in log2 units:
-//   s_j = c ks_j (q . k8_j),   w_j = 2^(s_j + e_j - M),   M = running max of s_j + e_j,
+//   s_j = c ks_j (q . k8_j),   w_j = 2^(s_j + e_j - M),   M = running max of s_j + e_j, less 6,
 //   l = sum w_j 2^-e_j,   a = sum (w_j f_j) v8_j,   O = a / l,   LSE = ln2 (M + log2 l).
 // Taking the maximum over what a key adds to O, not over its score alone, keeps the fp16
-// weights w f at or below a small constant whatever the blocks' scales are.
+// weights w f below 2^15 whatever the blocks' scales are; the 6 keeps those of light keys above
+// fp16's smallest step (kD8Room).
 //
 // This kernel takes up to 16 query rows per key head (8 at d = 256) in one pass over the
 // cache, and more in several; decode_fp8_wide.cu takes many rows of a large step.  HBM-bound:
@@ -51,7 +52,6 @@ namespace gb300 {
 
 constexpr int kD8Warps = 4;            // consumer warps
 constexpr int kD8Threads = (kD8Warps + 1) * 32;
-constexpr float kD8Tau = 8.0f;         // the running maximum is raised when passed by this (log2)
 
 template <int D, int NT>
 struct Dec8Cfg {
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                             }
                         }
                     }
-                    // ---- scales, mask, running maximum, weights
+                    // ---- scales, mask, running base, weights
                     float vf[C::G], vinv[C::G], xs[C::G][NT][4];
                     bool raise = false;
 #pragma unroll
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                             top[nt][e] = fmaxf(xs[0][nt][e], xs[0][nt][e + 2]);
 #pragma unroll
                             for (int u = 1; u < C::G; ++u) top[nt][e] = fmax3(top[nt][e], xs[u][nt][e], xs[u][nt][e + 2]);
-                            raise |= top[nt][e] > m[nt][e] + kD8Tau;
+                            raise |= top[nt][e] > m[nt][e] + (kD8Room + kD8Tau);
                         }
                     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                                 float mx = top[nt][e];
 #pragma unroll
                                 for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                                mx = fmaxf(mx, m[nt][e]);
+                                mx = fmaxf(mx - kD8Room, m[nt][e]);
                                 al[e] = mx == NEG_INF ? 1.0f : ex2(m[nt][e] - mx);
                                 m[nt][e] = mx;
                                 l[nt][e] *= al[e];
@@ -567,8 +567,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (unit_row + r) * D + d4 * 4) =
                             make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-                        if (d4 == 0)
-                            p.lse[unit_row + r] = sum == 0.0f ? NEG_INF : (mb + __log2f(sum)) * 0.69314718055994531f;
+                        if (d4 == 0) p.lse[unit_row + r] = dec8_lse(M, sum);
                     } else {
                         *reinterpret_cast<float4*>(part + r * D + d4 * 4) = v;
                         if (d4 == 0) {

@@ -5,7 +5,7 @@
 // equal ranges, one per resident CTA, so a ragged batch and a single long sequence both keep
 // every SM busy to the end.  A unit (sequence, key head) counts a few tiles more than it has,
 // what starting and ending it costs.  A range may end inside a unit; its part (O not yet
-// divided, running maxima, sums) then goes to the workspace, and decode_fp8_combine_kernel,
+// divided, the weights' bases, sums) then goes to the workspace, and decode_fp8_combine_kernel,
 // launched as a dependent of the main grid, joins a unit's parts.
 #pragma once
 
@@ -28,7 +28,14 @@ namespace gb300 {
 constexpr int kD8UnitCost = 4;
 constexpr int kD8CombineThreads = 128, kD8CombineFew = 8;
 
-// Floats of a part: O [rows][d], maxima [rows], sums [rows].
+// Weights are stored in fp16 relative to a base that lies kD8Room (log2) under the row's largest
+// when it is set, and is set again when a key passes that largest by more than kD8Tau: a stored
+// weight w f is below 2^(6 + 7) * 4 = 2^15, and fp16's smallest step lies 2^-30 under the
+// largest weight.  (With the base at the largest itself, 2^-24: beside one heavy key without a
+// value, 131072 light ones of 2^-25 each, 0.4 % of O, were lost, at 2^-24.4 they counted a third too much.)
+constexpr float kD8Room = 6.0f, kD8Tau = 7.0f;
+
+// Floats of a part: O [rows][d], bases [rows], sums [rows].
 __host__ __device__ constexpr int dec8_part(int rows, int d) { return rows * (d + 2); }
 
 // Tiles of a sequence: [t0, t0 + n), of whose keys lo .. L-1 may be seen.
@@ -289,7 +296,17 @@ __device__ __forceinline__ void dec8_timeout(const DecodeFp8Params& p, int* abor
     *reinterpret_cast<volatile int*>(abort_flag) = 1;
 }
 
-// Joins the parts of a unit that several ranges shared: with M the largest part maximum,
+// LSE from the base of a row's weights and their sum; the logarithm is taken of the sum relative
+// to the largest weight, near 1 for few keys.
+__device__ __forceinline__ float dec8_lse(float base, float sum)
+{
+    constexpr float down = 1.0f / (1 << (int)kD8Room);
+    if (sum == 0.0f) return -__int_as_float(0x7f800000);
+    const float m = base == -__int_as_float(0x7f800000) ? 0.0f : base;
+    return (m + kD8Room + __log2f(sum * down)) * 0.69314718055994531f;
+}
+
+// Joins the parts of a unit that several ranges shared: with M the largest part base,
 // O = sum_x 2^(M_x - M) a_x / sum_x 2^(M_x - M) l_x.  grid.x: the units, or where there are
 // more of them the ranges (each leaves at most one unit to its successors); grid.y shares
 // a unit's rows and columns.  Latency-bound: a thread has all its parts' loads in flight
@@ -323,8 +340,7 @@ __global__ void __launch_bounds__(kD8CombineThreads) decode_fp8_combine_kernel(c
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (row0 + r) * D)[col] =
             make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-        if (col == 0)
-            p.lse[row0 + r] = sum == 0.0f ? NEG_INF : ((M == NEG_INF ? 0.0f : M) + __log2f(sum)) * 0.69314718055994531f;
+        if (col == 0) p.lse[row0 + r] = dec8_lse(M, sum);
     };
     // (M, l, a) += K parts x, x + step, ... up to x1, of row r
     auto join = [&](auto K, int x, int step, int r, int col, float& M, float& l, float4& a) {

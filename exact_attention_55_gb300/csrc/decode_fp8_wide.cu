@@ -2,7 +2,7 @@
 // query rows under one key head: wide groups, several new tokens, or both.
 //
 // Same definition and scales as decode_fp8.cu:
-//   s_j = c ks_j (q . k8_j),   vs = f 2^e,   w_j = 2^(s_j + e_j - M),
+//   s_j = c ks_j (q . k8_j),   vs = f 2^e,   w_j = 2^(s_j + e_j - M),   M = running max less 6,
 //   l = sum w_j 2^-e_j,   a = sum (w_j f_j) v8_j,   O = a / l,   LSE = ln2 (M + log2 l).
 // From about 16 rows on the register products of that kernel, not the cache's bytes, set the
 // time (each 16 rows take the conversions and the tile's read again).  Here both products are
@@ -15,7 +15,7 @@
 //     with Q and P (fp16) read from tensor memory, so
 //     the products' shared-memory traffic is the tile alone: per 32 KB of codes 32 + 64 + 64 KB
 //     are read, written and read again, under the time that HBM takes to deliver them;
-//   * warps 0-3 own 32 rows each: softmax, P, rescaling of O when a maximum is passed by 2^8.
+//   * warps 0-3 own 32 rows each: softmax, P, rescaling of O when a maximum is passed by 2^7.
 // With 64 rows or fewer the rows are copied to the other warps' lanes and each copy takes its
 // share of the tile's keys (its P is zero elsewhere), so all four warps work; the copies'
 // results are joined through shared memory at the end of a unit.
@@ -33,7 +33,6 @@
 
 namespace gb300 {
 
-constexpr float kD8WideTau = 8.0f;
 constexpr int kD8WideThreads = 512;    // warpgroups: softmax, K converters, V converters, and the warps below
 constexpr int kD8WideProducer = 12, kD8WideMmaS = 13, kD8WideMmaPV = 14;
 // registers of a thread after the split; the block starts with 512 x 128 = 65536
@@ -518,11 +517,11 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
 #pragma unroll
                     for (int i = 0; i < PIECE; i += 2) mx = fmax3(mx, s[i], s[i + 1]);
                 }
-                const bool raise = mx > m + kD8WideTau;
-                const float al = raise ? ex2(m - mx) : 1.0f;     // ex2(-inf) = 0
+                const bool raise = mx > m + (kD8Room + kD8Tau);
+                const float al = raise ? ex2(m - (mx - kD8Room)) : 1.0f;     // ex2(-inf) = 0
                 if (raise) {
                     l *= al;
-                    m = mx;
+                    m = mx - kD8Room;
                 }
                 const float mb = m == NEG_INF ? 0.0f : m;
                 if (k > w.k0) {
@@ -620,9 +619,7 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (unit_row + r) * D + d4 * 4) =
                         make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-                    if (d4 == 0)
-                        p.lse[unit_row + r] = sum == 0.0f ? NEG_INF
-                                                          : ((top == NEG_INF ? 0.0f : top) + __log2f(sum)) * 0.69314718055994531f;
+                    if (d4 == 0) p.lse[unit_row + r] = dec8_lse(top, sum);
                 } else {
                     *reinterpret_cast<float4*>(part + r * D + d4 * 4) = v;
                     if (d4 == 0) {

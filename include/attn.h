@@ -452,11 +452,14 @@ attn_status_t attn_cache_append_fp8(const void* k, const void* v, void* k_cache,
  * What the cache holds at keys a query does not see (rows behind the sequence, pages
  * behind it or before its window) never reaches that query's outputs, NaN codes and
  * scales included.  An E5M2 code of infinity in V, which the append never writes, counts as
- * NaN where only some of the queries see its key, or several share it.  The queries and the codes enter the products exactly (a query element
- * below 2^-32 of its row's largest is off by at most 2^-39 of that); scores, sums and O are
- * fp32, the weights of the second product (softmax times V scale, relative to the row's
- * largest) are rounded to fp16.  A V scale below 2^-60 of the sequence's largest, or of 1,
- * counts as that in "largest": only a softmax that sits on such blocks loses digits of O.
+ * NaN where only some of the queries see its key, or several share it.  The queries and the
+ * codes enter the products exactly (a query element below 2^-32 of its row's largest is off
+ * by at most 2^-39 of that); scores, sums and O are fp32.  The weights of the second product
+ * (softmax times V scale) are rounded to fp16: each is off by at most 2^-11 of itself, or,
+ * where that is more, by 2^-31 of the row's largest, so that a key below 2^-31 of the largest
+ * may add nothing to O (131072 such keys beside the largest: at most 2^-14 of it).  A V scale
+ * below 2^-60 of the sequence's largest, or of 1, counts as that in "largest": only a
+ * softmax that sits on such blocks loses digits of O.
  * HBM-bound: every key and value code that a query sees is read once per call.
  */
 size_t attn_decode_fp8_workspace_bytes(int H, int Hkv, int nq, int d);
