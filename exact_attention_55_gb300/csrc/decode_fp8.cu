@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                         const int r = nt * 8 + g, o = (c * (C::CB / 32) + v) * 4;
                         uint4 u = make_uint4(0, 0, 0, 0);
                         if (row0 + r < p.rows)
-                            u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                                     (unit_row + r) * D + c * C::CB + t * (C::CB / 4) + v * 8));
+                            u = dec8_ld(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (unit_row + r) * D +
+                                                                       c * C::CB + t * (C::CB / 4) + v * 8));
                         qw[nt][o] = u.x, qw[nt][o + 1] = u.y, qw[nt][o + 2] = u.z, qw[nt][o + 3] = u.w;
                     }
             const int* ptab = p.page_table + (size_t)w.b * p.max_pages;
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kD8Threads, Dec8Cfg<D, NT>::CTAS)
                     held = box0;
                     const long long key = (long long)(box0 + lane) << log2_r;
                     const int pi = (int)min(key >> p.log2_ps, (long long)p.max_pages - 1);
-                    pg = min(max(__ldg(ptab + pi), 0), p.num_pages - 1);
+                    pg = min(max(dec8_ld(ptab + pi), 0), p.num_pages - 1);
                 }
                 if (!wait_lane0(&sh->empty[stage], parity)) break;
                 const uint32_t fb = smem_u32(&sh->full[stage]);

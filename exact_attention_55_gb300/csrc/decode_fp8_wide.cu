@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                     held = box0;
                     const long long key = (long long)(box0 + lane) << log2_r;
                     const int pi = (int)min(key >> p.log2_ps, (long long)p.max_pages - 1);
-                    pg = min(max(__ldg(ptab + pi), 0), p.num_pages - 1);
+                    pg = min(max(dec8_ld(ptab + pi), 0), p.num_pages - 1);
                 }
                 const int pg_box = __shfl_sync(0xffffffffu, pg, box0 - held + (lane & (nbox - 1)));
                 const int part_key = key0 + (lane & (C::PARTS - 1)) * 16;
@@ -402,12 +402,12 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
             uint4 held[HOLD ? D / 8 : 1];
             if constexpr (HOLD) {
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) held[i] = __ldg(q + i);
+                for (int i = 0; i < D / 8; ++i) held[i] = dec8_ld(q + i);
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) largest(held[i]);
             } else {
 #pragma unroll 8
-                for (int i = 0; i < D / 8; ++i) largest(__ldg(q + i));
+                for (int i = 0; i < D / 8; ++i) largest(dec8_ld(q + i));
             }
             const int ex = max((int)(big >> 23), 15) - 14;       // biased exponent of the factor's inverse
             const float down = live ? __int_as_float((254 - ex) << 23) : 0.0f;
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                 uint32_t f[32];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint4 u = HOLD ? held[HOLD ? c * 8 + i : 0] : __ldg(q + c * 8 + i);
+                    const uint4 u = HOLD ? held[HOLD ? c * 8 + i : 0] : dec8_ld(q + c * 8 + i);
                     const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -600,11 +600,11 @@ __global__ void __launch_bounds__(kD8WideThreads, 1)
                 for (uint32_t left = nan_keys; left; left &= left - 1) {
                     const int i = __ffs(left) - 1, key = i < 7 ? u.seq.L - p.nq + 1 + i : u.seq.lo + i - 7;
                     if (key > newest || (p.window > 0 && key < newest - p.window)) continue;
-                    const int page = min(max(__ldg(p.page_table + (size_t)u.b * p.max_pages + (key >> p.log2_ps)), 0),
+                    const int page = min(max(dec8_ld(p.page_table + (size_t)u.b * p.max_pages + (key >> p.log2_ps)), 0),
                                          p.num_pages - 1);
                     const uint8_t* at = p.vc + (((((size_t)page * p.Hkv + u.hk) << p.log2_ps) +
                                                  (key & ((1 << p.log2_ps) - 1))) * D + d4 * 4);
-                    const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(at));
+                    const uint32_t codes = (uint32_t)dec8_ld(reinterpret_cast<const int*>(at));
                     const uint32_t bad = e5m2 ? dec8_nonfinite<true>(codes) : dec8_nonfinite<false>(codes);
                     const float nan = __int_as_float(0x7fc00000);
                     if (bad & 0x80u) v.x = nan;
