@@ -4,8 +4,8 @@ The functions below carry the C entry points' names (``include/attn.h``) and do
 argument marshalling only: every arithmetic step runs in the CUDA library
 ``_build/libgb300attn.so``.  PyTorch supplies device memory and the stream.  The
 paged-cache calls of a serving step are marshalled natively (``csrc/binding.cpp``),
-the others through ctypes.  There is no fallback: if a library is missing or fails
-to load, every call raises.
+the others through ctypes.  There is no fallback: if the library is missing or fails
+to load, every call raises; if the native binding does, the calls that go through it.
 
     import exact_attention_55_gb300 as fa
     o, lse = fa.attn_fwd_bf16(q, k, v, causal=True)          # q, k, v: cuda bf16 [B,H,N,d]
@@ -92,9 +92,8 @@ def library_path() -> str:
 
 
 def load_library(path: str | None = None):
-    """Load (once) and return the ctypes handle of the CUDA library, with the native binding
-    of the paged-cache calls.  Raises if either is absent."""
-    global _lib, _binding
+    """Load (once) and return the ctypes handle of the CUDA library.  Raises if absent."""
+    global _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -171,12 +170,6 @@ def load_library(path: str | None = None):
         lib.attn_selftest_decode_fp8_withheld_load.restype = i
         lib.attn_selftest_fp8_convert.argtypes = [ctypes.c_uint, ctypes.c_size_t, i, vp, vp]
         lib.attn_selftest_fp8_convert.restype = i
-        if _binding is None:
-            binding = _build.load_binding()
-            binding.bind(*(ctypes.cast(getattr(lib, name), vp).value for name in (
-                "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
-                "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes")))
-            _binding = binding
         _lib = lib
         return lib
 
@@ -417,9 +410,19 @@ def attn_decode_bf16_paged_noalloc(q, k_cache, v_cache, page_table, seq_lens,
 
 
 def _native():
-    """The native binding of the paged-cache calls (checks, outputs and the C call in one step)."""
+    """The native binding of the paged-cache calls (checks, outputs and the C call in one step),
+    loaded by the first of them: it is built against the installed PyTorch, which the other
+    calls do not depend on."""
+    global _binding
     if _binding is None:
-        load_library()
+        lib = load_library()
+        with _lock:
+            if _binding is None:
+                binding = _build.load_binding()
+                binding.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+                    "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
+                    "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes")))
+                _binding = binding
     return _binding
 
 

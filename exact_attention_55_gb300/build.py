@@ -112,7 +112,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(UNITS) + 1) as ex:
         binding = ex.submit(_compile_binding)
         results = list(ex.map(compile_unit, UNITS))
-        binding.result()
     if verbose:
         for obj, log in results:
             print(f"== {os.path.basename(obj)}\n{log}")
@@ -123,6 +122,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    binding.result()                       # the library is there even if this raises
     return LIB_PATH
 
 
