@@ -5,11 +5,13 @@ Every translation unit is compiled for sm_103a only
 one shared library with the CUDA runtime linked statically.  The kernel file
 ``attn_fwd_inst.cu`` is compiled once per (head dim, operand type) pair.  Beside it,
 ``csrc/binding.cpp`` becomes a Python extension against the installed PyTorch
-(``_build/_gb300attn_binding.so``): host code only, compiled by the host compiler.
+(``_build/_gb300attn_binding.so``): host code only, compiled by the host compiler.  What it
+was built against (PyTorch and Python versions) is kept in a file beside it; another one makes it stale.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import importlib.machinery
 import importlib.util
 import os
@@ -63,6 +65,25 @@ def _sources_mtime() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
+def _abi() -> str:
+    """What the binding's binary interface depends on."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def _binding_abi_path() -> str:
+    return BINDING_PATH + ".abi"
+
+
+def _binding_abi() -> str:
+    """What the binding on disk was built against ("" if unknown)."""
+    try:
+        with open(_binding_abi_path(), encoding="utf-8") as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def _compile_binding() -> None:
     import torch
     root = os.path.dirname(torch.__file__)
@@ -76,14 +97,23 @@ def _compile_binding() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr}")
+    # the versions last: a run that ends in between leaves a binding that counts as stale
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(_binding_abi_path())
     os.replace(tmp, BINDING_PATH)
+    with open(tmp, "w", encoding="utf-8") as f:
+        f.write(_abi())
+    os.replace(tmp, _binding_abi_path())
 
 
 def load_binding():
-    """The native binding's module; raises if it is not built."""
+    """The native binding's module; raises if it is not built, or for another PyTorch or Python."""
     if not os.path.exists(BINDING_PATH):
         raise RuntimeError(f"binding not built: {BINDING_PATH} is missing "
                            "(run exact_attention_55_gb300.build.build())")
+    if _binding_abi() != _abi():
+        raise RuntimeError(f"{BINDING_PATH} was built against {_binding_abi() or 'an unknown PyTorch'}, here is "
+                           f"{_abi()} (run exact_attention_55_gb300.build.build())")
     loader = importlib.machinery.ExtensionFileLoader(BINDING_NAME, BINDING_PATH)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader(BINDING_NAME, loader))
     loader.exec_module(module)
@@ -92,8 +122,12 @@ def load_binding():
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if stale) and return the path of the shared library."""
-    built = (LIB_PATH, BINDING_PATH)
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _sources_mtime() for p in built):
+    def fresh(path):
+        return not force and os.path.exists(path) and os.path.getmtime(path) >= _sources_mtime()
+
+    if fresh(LIB_PATH):
+        if not (fresh(BINDING_PATH) and _binding_abi() == _abi()):
+            _compile_binding()
         return LIB_PATH
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()

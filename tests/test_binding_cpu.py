@@ -26,6 +26,7 @@ def test_without_the_binding_only_its_own_calls_raise(tmp_path, content):
     path = tmp_path / "binding.so"
     if content is not None:
         path.write_bytes(content)
+        (tmp_path / "binding.so.abi").write_text(build._abi())
     run(f"""
         import torch
         from exact_attention_55_gb300 import build
@@ -73,3 +74,36 @@ def test_the_library_is_linked_before_the_binding_may_fail(monkeypatch, tmp_path
     with pytest.raises(RuntimeError, match="binding"):
         build.build()
     assert lib.exists()
+
+
+def test_a_binding_for_another_pytorch_is_stale(monkeypatch, tmp_path):
+    """build() compiles the binding again, and only it; loading it before that says why not."""
+    lib, path = tmp_path / "lib.so", tmp_path / "binding.so"
+    lib.write_bytes(b"")
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "LIB_PATH", str(lib))
+    monkeypatch.setattr(build, "BINDING_PATH", str(path))
+    real, calls = subprocess.run, []
+
+    def compiler(cmd, **kw):
+        if cmd[0] != "g++":
+            return real(cmd, **kw)
+        calls.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "wb") as f:
+            f.write(b"")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    monkeypatch.setattr(build, "_nvcc", lambda: "/usr/local/cuda/bin/nvcc")
+    build.build()
+    build.build()
+    assert len(calls) == 1                               # built once, then up to date
+    import torch
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "99.0.1+cu990")
+        with pytest.raises(RuntimeError, match="built against torch .*99.0.1"):
+            build.load_binding()
+        build.build()
+        build.build()
+    assert len(calls) == 2
+    build.build()                                        # and back
+    assert len(calls) == 3
