@@ -17,6 +17,11 @@ to load, every call raises; if the native binding does, the calls that go throug
     lens, free, cu, slots, pos, ok = fa.attn_paged_plan(new, lens, table, pages, free, 64, T)
     fa.attn_cache_append_fp8(k, v, kc8, vc8, ks, vs, slots)  # k, v: [T, Hkv, d], 8-bit paged cache
     o, lse = fa.attn_decode_fp8_paged(q1, kc8, vc8, ks, vs, table, lens)
+
+A call enqueues its kernels on ``stream`` (default: the current one).  New outputs are allocated on
+the current stream; those of ``attn_paged_plan`` and ``attn_decode_fp8_paged`` on the call's own
+stream and recorded for the current one.  Either way the caller orders the two streams, and
+records an output (``Tensor.record_stream``) for any third stream that reads it.
 """
 from __future__ import annotations
 
@@ -443,7 +448,9 @@ def attn_paged_plan(new_lens, seq_lens, page_table, free_pages, free_count, page
     updated in place; free_pages: int32 stack of free pages of which free_count (int32 [1])
     are left; num_tokens: packed rows of the step, at least the sum of new_lens.  Returns
     (seq_lens_out, free_count_out, cu_new, slot_map int64 [num_tokens], positions, served).
-    seq_lens_out may be seq_lens and free_count_out free_count (in place)."""
+    seq_lens_out may be seq_lens and free_count_out free_count (in place).  The new outputs of a
+    call share one allocation, which any of them keeps alive: pass tensors of your own for
+    those that outlive the step."""
     r = _native().plan(new_lens, seq_lens, page_table, free_pages, free_count, page_size, num_tokens,
                        seq_lens_out, free_count_out, cu_new, slot_map, positions, served,
                        _stream_on(stream, new_lens))

@@ -67,20 +67,16 @@ const Tensor& exact(PyObject* o, std::initializer_list<int64_t> shape, at::Scala
     return t;
 }
 
-// The caller's output, checked, or a new one.
-Tensor output(PyObject* o, std::initializer_list<int64_t> shape, at::ScalarType dtype, at::Device dev, const char* name)
-{
-    if (o != Py_None) return exact(o, shape, dtype, dev, name);
-    return at::detail::empty_cuda(at::IntArrayRef(shape), dtype, dev, c10::nullopt);
-}
-
 // Makes a call's device and stream current while it allocates and launches: the given
 // stream's handle, or None for the device's current one.  What a call allocates (outputs,
 // a workspace that goes back when it returns) belongs to the stream it runs on, so nobody
-// on another stream can be given that memory while the call's kernels are in flight.
+// on another stream can be given that memory while the call's kernels are in flight.  An output
+// of a call on a given stream is recorded for the current one too: its caller may read it there,
+// after the usual wait, and drop it.
 struct On {
     c10::cuda::OptionalCUDAGuard device;
     c10::cuda::OptionalCUDAStreamGuard stream;
+    c10::optional<c10::cuda::CUDAStream> callers;      // the current stream, where it is another one
     void* handle;
 
     On(PyObject* given, at::Device dev)
@@ -92,7 +88,24 @@ struct On {
         }
         handle = PyLong_AsVoidPtr(given);
         if (PyErr_Occurred()) throw Refusal{nullptr, ""};
+        const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(dev.index());
+        if (current.stream() != handle) callers = current;
         stream.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), dev.index()));
+    }
+
+    Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, at::Device dev) const
+    {
+        Tensor t = at::detail::empty_cuda(shape, dtype, dev, c10::nullopt);
+        if (callers) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *callers);
+        return t;
+    }
+
+    // The caller's output, checked, or a new one.
+    Tensor output(PyObject* o, std::initializer_list<int64_t> shape, at::ScalarType dtype, at::Device dev,
+                  const char* name) const
+    {
+        if (o != Py_None) return exact(o, shape, dtype, dev, name);
+        return empty(at::IntArrayRef(shape), dtype, dev);
     }
 };
 
@@ -171,8 +184,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n)
         auto out = [&](PyObject* given, int64_t count, at::ScalarType dtype, const char* name) {
             if (given != Py_None) return exact(given, {count}, dtype, dev, name);
             if (!whole.defined())
-                whole = at::detail::empty_cuda({room(8LL * T) + room(4LL * T) + 2 * room(4 * B) + room(4 * B + 4) + 16},
-                                               at::kByte, dev, c10::nullopt);
+                whole = on.empty({room(8LL * T) + room(4LL * T) + 2 * room(4 * B) + room(4 * B + 4) + 16}, at::kByte, dev);
             const int64_t size = (int64_t)c10::elementSize(dtype);
             Tensor t = at::detail::make_tensor<c10::TensorImpl>(
                 c10::Storage(whole.storage()), whole.key_set(), c10::scalarTypeToTypeMeta(dtype));
@@ -333,8 +345,8 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n)
             ws = given.data_ptr();
             ws_bytes = (size_t)given.nbytes();
         }
-        const Tensor o = output(a[11], {B, H, nq, d}, at::kBFloat16, dev, "o");
-        const Tensor lse = output(a[12], {B, H, nq}, at::kFloat, dev, "lse");
+        const Tensor o = on.output(a[11], {B, H, nq, d}, at::kBFloat16, dev, "o");
+        const Tensor lse = on.output(a[12], {B, H, nq}, at::kFloat, dev, "lse");
         const attn_status_t st = f_decode(
             q.data_ptr(), kc.data_ptr(), vc.data_ptr(), static_cast<float*>(ptr(a[3])), static_cast<float*>(ptr(a[4])),
             static_cast<int*>(table.data_ptr()), static_cast<int*>(lens.data_ptr()), o.data_ptr(),
