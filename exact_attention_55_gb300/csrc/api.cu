@@ -913,8 +913,10 @@ extern "C" attn_status_t attn_bwd_bf16(const void* q, const void* k, const void*
 namespace {
 
 // Tables of at most this many keys: a head's tiles stay with one CTA and the joining launch is
-// left out.  Measured for 1 to 256 sequences, whole against split: 128 keys 4.7-30.3 against
-// 6.8-33.2 us, 256 keys 5.5-44.2 against 6.9-47.5, 512 keys 7.3-72.3 against 6.9-75.4.
+// left out.  Measured whole against split, 8 key heads, for 1 / 16 / 256 sequences, us: d 128, 4 rows,
+// 320 keys 7.2 / 7.6, 8.1 / 9.9, 31.6 / 33.0; 384 keys 7.6 / 7.7, 8.9 / 10.0, 35.5 / 36.7; 448 keys 8.2 / 7.6,
+// 9.4 / 10.3, 39.8 / 40.5; d 256, 8 rows, 320 keys 9.0 / 8.6, 10.4 / 12.5, 55.7 / 57.8; 448 keys 10.3 / 8.6,
+// 12.1 / 13.5, 73.5 / 74.7; d 64, 4 rows, 512 keys 6.7 / 7.7, 7.7 / 9.2, 27.1 / 28.5.
 constexpr int kDecodeWholeKeys = 384;
 constexpr int kDecodeFp8MaxBatch = (1 << 19) - 1;   // the kernel packs a count of sequences into 19 bits
 constexpr int kPlanMaxRequests = 16384;   // three ints of shared memory per request
@@ -1063,10 +1065,14 @@ static DecodeFp8Plan decode_fp8_plan(bool wide, int rows, int d, int sm_count)
 
 // The narrow kernel's time grows with its row groups (16 rows each; 8 at d = 256), the wide
 // one's hardly with the rows, but it starts and ends later by what about 16 tiles of 64 keys
-// per SM cost.  `keys`: the most a sequence of the step can have.  Measured narrow against
-// wide, 8 key heads, us: d 128, 32 rows, 2 x 4096 keys 18.8 / 21.4, 4 x 4096 21.5 / 22.2,
-// 8 x 4096 33.0 / 30.4, 16 x 8192 102 / 69; 48 rows, 2 x 4096 18.4 / 24.0, 4 x 4096
-// 27.2 / 23.5; d 256, 16 rows, 16 x 8192 116 / 118, 32 rows 219 / 126.
+// per SM cost.  `keys`: the most a sequence of the step can have, by the table's width or the
+// window.  Measured narrow against wide, 8 key heads, us: d 128, 32 rows, 2 x 4096 keys
+// 18.8 / 21.4, 4 x 4096 20.7 / 20.9, 8 x 4096 33.0 / 30.4, 16 x 4096 55.3 / 44.6, 16 x 8192 102 / 68;
+// 48 rows, 2 x 4096 18.4 / 24.0, 4 x 4096 26.2 / 23.5; d 256, 16 rows, 16 x 8192 116 / 118, 32 rows
+// 219 / 125; d 64, where a tile is 128 keys, 32 rows 16 x 4096 32.8 / 34.1, 48 rows 43.8 / 38.6.
+// The lengths are on the device, so a step of short sequences under a wide table takes what the
+// table's width would want (16384 keys, 32 rows, 16 sequences of 256 and 1024 keys: d 128
+// 14.4 / 16.2 and 23.1 / 25.6, d 256 19.7 / 31.6 and 38.9 / 44.0; of one sequence 9 to 20).
 static bool decode_fp8_is_wide(int rows, int d, long long heads, long long keys, int sm_count)
 {
     if (rows <= 16) return false;

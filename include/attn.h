@@ -460,7 +460,12 @@ attn_status_t attn_cache_append_fp8(const void* k, const void* v, void* k_cache,
  * may add nothing to O (131072 such keys beside the largest: at most 2^-14 of it).  A V scale
  * below 2^-60 of the sequence's largest, or of 1, counts as that in "largest": only a
  * softmax that sits on such blocks loses digits of O.
- * HBM-bound: every key and value code that a query sees is read once per call.
+ * One pass over the cache serves 16 query rows of a key head (rows: H / Hkv * nq; 8 at d = 256),
+ * or 128 where a step of more than 16 rows is large; it is HBM-bound up to 8 rows.  Which
+ * of the two kernels a step takes goes by its rows, d, B * Hkv and the table's width, max_pages *
+ * page_size (or the window), since the lengths are on the device: tables much wider than the
+ * longest sequence may take the kernel that is slower for the step (by 2 to 12 us), and a
+ * table of another width may change O and LSE by their roundings.
  */
 size_t attn_decode_fp8_workspace_bytes(int H, int Hkv, int nq, int d);
 attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cache, const void* v_cache,
@@ -495,11 +500,13 @@ attn_status_t attn_selftest_wait_timeout(unsigned long long timeout_ns, void* st
 
 /*
  * attn_selftest_fwd_withheld_load, attn_selftest_quant_withheld_load,
- * attn_selftest_bwd_withheld_load, attn_selftest_decode_fp8_withheld_load -- diagnostics for the abort path of the real
- * kernels (no page describes them: they test this library's failure detection).
+ * attn_selftest_bwd_withheld_load, attn_selftest_decode_fp8_withheld_load -- diagnostics for
+ * the abort path of the real kernels (no page describes them: they test this library's
+ * failure detection).
  * Each runs the production kernel of attn_fwd_bf16 (scale 1/sqrt(d), no window),
  * of attn_quantize_fp8_blockwise (E4M3, block 128), of attn_bwd_bf16 or of
- * attn_decode_fp8_paged (scale 1/sqrt(d), no window) on the given tensors, with two differences: every wait is bounded by `timeout_ns`
+ * attn_decode_fp8_paged (scale 1/sqrt(d), no window) on the given tensors, with two
+ * differences: every wait is bounded by `timeout_ns`
  * instead of the usual 4 s, and in every CTA the load with index `withheld`
  * (0-based, counted over that CTA's K/V tiles, its 128-row blocks, its
  * backward ring tiles, or its cache tiles, K and V counted apart above 16 rows per
