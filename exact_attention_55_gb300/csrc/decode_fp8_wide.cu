@@ -24,7 +24,7 @@
 //
 // Measured, 16 sequences x 8 key heads x 8192 keys, d 128 (39.5 us at the copy rate): 32 rows
 // 68 us, 64 rows 77, 128 rows 160 (102, 187 and 364 in passes of 16 rows); d 256, 128 rows 154
-// (842).  Neither HBM (48 %) nor the tensor pipe (44 %) bounds it, but the chain of a softmax
+// (842).  Neither HBM (46 %) nor the tensor pipe (45 %) bounds it, but the chain of a softmax
 // warp per tile (S arrives, maximum, weights, P leaves), whose warps share the issue slots with
 // the eight that convert; at 128 rows each of its threads has all of a tile's 128 keys.  Loading and
 // converting in one warpgroup each for K and V, and S and P V issued by two warps, each cut
