@@ -41,6 +41,7 @@ __all__ = [
     "attn_decode_workspace_bytes",
     "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
     "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes",
+    "attn_rope_bf16", "attn_diff_fwd_bf16", "attn_diff_fwd_bf16_varlen",
     "attn_quantize_fp8_blockwise", "attn_quantize_fp8_hadamard", "attn_fwd_fp8",
     "attn_quantize_fp8_blockwise_fmt", "attn_fwd_fp8_fmt", "attn_fwd_fp8_blocks",
     "attn_fp8_qk_block_rows", "attn_fwd_schedule", "ATTN_FP8_E4M3", "ATTN_FP8_E5M2",
@@ -72,6 +73,7 @@ EXPORTED_SYMBOLS = (
     "attn_decode_bf16_paged_noalloc", "attn_decode_workspace_bytes",
     "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
     "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes",
+    "attn_rope_bf16", "attn_diff_fwd_bf16", "attn_diff_fwd_bf16_varlen",
     "attn_quantize_fp8_blockwise", "attn_quantize_fp8_blockwise_fmt",
     "attn_quantize_fp8_hadamard",
     "attn_fwd_fp8", "attn_fwd_fp8_fmt", "attn_fwd_fp8_blocks", "attn_fp8_qk_block_rows",
@@ -139,6 +141,12 @@ def load_library(path: str | None = None):
         lib.attn_decode_fp8_workspace_bytes.restype = ctypes.c_size_t
         lib.attn_decode_fp8_paged.argtypes = ([vp] * 9 + [i] * 10 + [f, i, vp, ctypes.c_size_t, vp])
         lib.attn_decode_fp8_paged.restype = i
+        lib.attn_rope_bf16.argtypes = [vp] * 8 + [i] * 9 + [vp]
+        lib.attn_rope_bf16.restype = i
+        lib.attn_diff_fwd_bf16.argtypes = [vp] * 7 + [i] * 5 + [f, i, i, vp]
+        lib.attn_diff_fwd_bf16.restype = i
+        lib.attn_diff_fwd_bf16_varlen.argtypes = [vp] * 8 + [i] * 6 + [f, i, i, vp]
+        lib.attn_diff_fwd_bf16_varlen.restype = i
         lib.attn_quantize_fp8_blockwise.argtypes = [vp, vp, vp, i, i, i, i, i, vp]
         lib.attn_quantize_fp8_blockwise.restype = i
         lib.attn_quantize_fp8_hadamard.argtypes = [vp, vp, vp, i, i, i, i, i, vp]
@@ -415,8 +423,8 @@ def attn_decode_bf16_paged_noalloc(q, k_cache, v_cache, page_table, seq_lens,
 
 
 def _native():
-    """The native binding of the paged-cache calls (checks, outputs and the C call in one step),
-    loaded by the first of them: it is built against the installed PyTorch, which the other
+    """The native binding of the paged-cache calls, of rotary positions and of differential
+    attention (checks, outputs and the C call in one step), loaded by the first of them: it is built against the installed PyTorch, which the other
     calls do not depend on."""
     global _binding
     if _binding is None:
@@ -426,7 +434,8 @@ def _native():
                 binding = _build.load_binding()
                 binding.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
                     "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
-                    "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes")))
+                    "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes", "attn_rope_bf16",
+                    "attn_diff_fwd_bf16", "attn_diff_fwd_bf16_varlen")))
                 _binding = binding
     return _binding
 
@@ -498,6 +507,52 @@ def attn_decode_fp8_paged(q, k_cache, v_cache, k_scales, v_scales, page_table, s
                          _fp8_format(fmt), scale, window, workspace, o, lse, _stream_on(stream, q))
     if type(r) is int:
         raise AttnError(r, "attn_decode_fp8_paged")
+    return r
+
+
+def attn_rope_bf16(q, k, positions, inv_freq, axis=None, interleaved: bool = False,
+                   inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions of queries and keys.  q, k: bf16 [T, H, d] or [B, H, N, d] (k may be None;
+    tokens and heads may be strided, so columns of one projection are fine); positions: int32
+    [T] or [axes, T] ([B, N] or [axes, B, N]), a token with a negative position on axis 0 is
+    left as it is; inv_freq: float32 [rot / 2], radians per position; axis: int32 [rot / 2],
+    each pair's axis (None: 0).  Pairs are (i, rot/2 + i), or (2i, 2i + 1) when interleaved.
+    inverse=True turns back: the gradient of the call.  Returns (q_out, k_out), which may be
+    given, q and k themselves too."""
+    r = _native().rope(q, k, positions, inv_freq, axis, int(bool(interleaved)), int(bool(inverse)),
+                       q_out, k_out, _stream_on(stream, q))
+    if type(r) is int:
+        raise AttnError(r, "attn_rope_bf16")
+    return r
+
+
+def attn_diff_fwd_bf16(q, k, v, lam, scale: float | None = None, causal: bool = False,
+                       window: int = 0, save_o2: bool = False, o=None, lse=None, o2=None,
+                       stream=None):
+    """Differential attention: O = (softmax(S_1) - lam softmax(S_2)) V for every head, S_m =
+    scale Q_m K_m^T + mask.  q: bf16 [B, 2H, N, d], head h's maps at 2h and 2h + 1; k: bf16
+    [B, 2Hkv, N, d]; v: bf16 [B, Hkv, N, 2d], H a multiple of Hkv; lam: float32 [H].  Returns
+    (O [B, H, N, 2d], the natural-log LSE [B, 2H, N], O_2): O_2 = softmax(S_2) V is what
+    attn_diff_bwd_bf16 needs, None unless save_o2 or o2 asks for it."""
+    r = _native().diff_fwd(q, k, v, lam, None, 0, scale, int(bool(causal)), window,
+                           int(bool(save_o2)), o, lse, o2, _stream_on(stream, q))
+    if type(r) is int:
+        raise AttnError(r, "attn_diff_fwd_bf16")
+    return r
+
+
+def attn_diff_fwd_bf16_varlen(q, k, v, lam, cu_seqlens, max_seqlen: int,
+                              scale: float | None = None, causal: bool = False, window: int = 0,
+                              save_o2: bool = False, o=None, lse=None, o2=None, stream=None):
+    """attn_diff_fwd_bf16 over packed sequences: q [T, 2H, d], k [T, 2Hkv, d], v [T, Hkv, 2d];
+    cu_seqlens int32 [S + 1] on the same device; max_seqlen >= every length.  Returns
+    (O [T, H, 2d], LSE [2H, T], O_2 or None)."""
+    if cu_seqlens is None:
+        raise TypeError("cu_seqlens must be an int32 [S + 1] tensor")
+    r = _native().diff_fwd(q, k, v, lam, cu_seqlens, max_seqlen, scale, int(bool(causal)), window,
+                           int(bool(save_o2)), o, lse, o2, _stream_on(stream, q))
+    if type(r) is int:
+        raise AttnError(r, "attn_diff_fwd_bf16_varlen")
     return r
 
 

@@ -42,6 +42,9 @@ UNITS = [
     ("decode_fp8", "decode_fp8.cu", []),
     ("paged", "paged.cu", []),
     ("attn_bwd", "attn_bwd.cu", []),
+    ("diff_fwd", "diff_fwd.cu", []),
+    ("rope", "rope.cu", []),
+    ("api_diff", "api_diff.cu", []),
     ("fwd_bf16_d64", "attn_fwd_inst.cu", ["-DGB300_ATTN_D=64", "-DGB300_ATTN_F8=0"]),
     ("fwd_bf16_d128", "attn_fwd_inst.cu", ["-DGB300_ATTN_D=128", "-DGB300_ATTN_F8=0"]),
     ("fwd_bf16_d256", "attn_fwd_inst.cu", ["-DGB300_ATTN_D=256", "-DGB300_ATTN_F8=0"]),

@@ -14,6 +14,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/attn.h"
+#include "api_internal.h"
 #include "attn_fwd.cuh"
 #include "attn_params.h"
 #include "paged_params.h"
@@ -65,18 +66,12 @@ __global__ void wait_timeout_kernel(int* status, unsigned long long timeout_ns)
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr unsigned long long kWaitTimeoutNs = 4000000000ull;  // 4 s per mbarrier wait
-
-struct DeviceInfo {
-    bool ready = false;
-    int sm_count = 0;
-    int* status = nullptr;
-    float* decode_scratch = nullptr;
-};
 
 std::mutex g_mutex;
 DeviceInfo g_devices[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+}  // namespace
 
 // Per-device facts, looked up once with that device current.
 attn_status_t device_info(DeviceInfo** out)
@@ -111,7 +106,20 @@ attn_status_t device_info(DeviceInfo** out)
     return ATTN_OK;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool encode_rows(CUtensorMap* m, const void* base, int cols, long long rows, long long row_stride,
+                 long long heads, long long head_stride, int box_rows)
+{
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)heads};
+    cuuint64_t strides[2] = {(cuuint64_t)row_stride * 2, (cuuint64_t)head_stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    cuuint32_t estride[3] = {1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                          estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+namespace {
 
 // 3-D map over a [BH, N, d] tensor: dims (d, N, BH) innermost first, 128-byte
 // swizzled boxes of (128 bytes of d) x box_rows x 1.  Rows past N read as zero.
@@ -146,6 +154,8 @@ bool encode_3d_packed(CUtensorMap* m, const void* base, CUtensorMapDataType dt, 
     return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
 // How the batched forward's CTAs walk the work: 0 complementary pairs, 1 single units
 // with a plain stride, 2 single units in rotated rounds.  Pairs balance a causal mask.  Without one the units of a head cost
 // the same, and single units end in fewer rounds whenever whole pairs leave part of the
@@ -167,6 +177,8 @@ int single_unit_walk(int causal, int window, int N, long long pairs, int sm_coun
     if (window > 0) return unit_times <= pair_times ? 2 : 0;
     return unit_times < pair_times ? 1 : 0;
 }
+
+namespace {
 
 template <int D>
 attn_status_t run_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,

@@ -1,0 +1,163 @@
+// api_diff.cu -- the C ABI of rotary positions and of differential attention: argument checks,
+// tensor maps and launches.
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/attn.h"
+#include "api_internal.h"
+#include "diff_params.h"
+
+using namespace gb300;
+
+// ------------------------------------------------------------------ rotary positions
+extern "C" attn_status_t attn_rope_bf16(const void* q, const void* k, void* q_out, void* k_out,
+                                        const int* positions, const float* inv_freq, const int* axis,
+                                        const long long* strides, int B, int N, int Hq, int Hk, int d, int rot,
+                                        int axes, int interleaved, int inverse, void* stream)
+{
+    if (B < 0 || N < 0 || Hq < 1 || Hk < 0 || axes < 1 || !strides) return ATTN_ERR_INVALID_ARG;
+    if (d < 16 || d > 256 || d % 16 != 0 || rot < 16 || rot > d || rot % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)B * N > 0x7fffffffLL || Hq > 65535 || Hk > 65535 || axes > 65535) return ATTN_ERR_UNSUPPORTED;
+    if (B == 0 || N == 0) return ATTN_OK;
+    if (!q || !q_out || !positions || !inv_freq || (Hk > 0 && (!k || !k_out))) return ATTN_ERR_INVALID_ARG;
+    const int tensors = Hk > 0 ? 4 : 2;      // q, q_out, k, k_out
+    const void* at[4] = {q, q_out, k, k_out};
+    for (int i = 0; i < tensors; ++i) {
+        if (!aligned(at[i], 16)) return ATTN_ERR_MISALIGNED;
+        for (int s = 0; s < 3; ++s)
+            if (strides[3 * i + s] % 8 != 0) return ATTN_ERR_MISALIGNED;
+    }
+    if (!aligned(positions, 4) || !aligned(inv_freq, 4) || !aligned(axis, 4)) return ATTN_ERR_MISALIGNED;
+    DeviceInfo* dev = nullptr;
+    const attn_status_t st = device_info(&dev);
+    if (st != ATTN_OK) return st;
+    RopeParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.q = {q, q_out, strides[0], strides[1], strides[2], strides[3], strides[4], strides[5]};
+    if (Hk > 0) p.k = {k, k_out, strides[6], strides[7], strides[8], strides[9], strides[10], strides[11]};
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.axis = axis;
+    p.tokens = B * N;
+    p.N = N;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.d = d;
+    p.rot = rot;
+    p.axes = axes;
+    p.interleaved = interleaved ? 1 : 0;
+    p.inverse = inverse ? 1 : 0;
+    return launch_rope(p, dev->sm_count, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ differential attention
+namespace {
+
+constexpr int kDiffMaxRows = 0x7fffff00;   // a last tile's rows stay in int
+
+// What every entry point below checks of its sizes.
+attn_status_t diff_sizes(int H, int Hkv, int d, float scale)
+{
+    if (H < 1 || Hkv < 1 || H % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+// Maps over q [.., 2H, .., d], k [.., 2Hkv, .., d] and v or o [.., heads, .., 2d], batched (T < 0: [B, heads, N,
+// width]) or packed [T, heads, width].
+bool diff_map(CUtensorMap* m, const void* base, int width, int heads, int B, int N, int T, int box_rows)
+{
+    if (T < 0)
+        return encode_rows(m, base, width, N, width, (long long)B * heads, (long long)N * width, box_rows);
+    return encode_rows(m, base, width, T, (long long)heads * width, heads, width, box_rows);
+}
+
+struct DiffShape {
+    int B, H, Hkv, N, d;          // packed: N the longest sequence
+    const int* cu_seqlens;        // packed layout, else null
+    int num_seqs, T;              // T < 0: batched
+    float scale;
+    int causal, window;
+};
+
+attn_status_t diff_fwd(const void* q, const void* k, const void* v, const float* lam, void* o, float* lse, void* o2,
+                       const DiffShape& s, void* stream, unsigned long long timeout_ns, int withhold)
+{
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(o2, 16) ||
+        !aligned(lam, 4) || !aligned(lse, 4) || !aligned(s.cu_seqlens, 4))
+        return ATTN_ERR_MISALIGNED;
+    if (s.N > kDiffMaxRows || s.T > kDiffMaxRows || s.H > 65535) return ATTN_ERR_UNSUPPORTED;
+    const bool packed = s.T >= 0;
+    const int parts = s.d / 64;
+    const long long heads = (packed ? (long long)s.num_seqs : (long long)s.B) * s.H * parts;
+    const long long blocks = ((long long)s.N + 127) / 128, pairs = heads * ((blocks + 1) / 2);
+    DeviceInfo* dev = nullptr;
+    const attn_status_t st = device_info(&dev);
+    if (st != ATTN_OK) return st;
+    // sub-unit indices, and a walk's step past the last one, stay in int; so do head coordinates
+    if (2 * pairs + 4LL * dev->sm_count > 0x7fffffffLL || 2 * heads > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+    alignas(64) DiffFwdMaps m;
+    if (!diff_map(&m.q, q, s.d, 2 * s.H, s.B, s.N, s.T, 128) ||
+        !diff_map(&m.k, k, s.d, 2 * s.Hkv, s.B, s.N, s.T, 128) ||
+        !diff_map(&m.v, v, 2 * s.d, s.Hkv, s.B, s.N, s.T, 128))
+        return ATTN_ERR_CUDA;
+    DiffFwdParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.f.o = o;
+    p.f.lse = lse;
+    p.f.status = dev->status;
+    p.f.BH = (int)heads;
+    p.f.N = s.N;
+    p.f.num_qblk = (int)blocks;
+    p.f.num_units = (int)pairs;
+    p.f.unit_walk = packed ? 0 : single_unit_walk(s.causal, s.window, s.N, pairs, dev->sm_count);
+    p.f.causal = s.causal ? 1 : 0;
+    p.f.window = s.window > 0 && s.window < s.N ? s.window : 0;   // a wider one masks nothing
+    p.f.c_log2 = (float)((double)s.scale * 1.4426950408889634);
+    p.f.timeout_ns = timeout_ns;
+    p.f.withhold_kv = withhold;
+    p.f.cu_seqlens = s.cu_seqlens;
+    p.f.num_seqs = s.num_seqs;
+    p.f.H = s.H * parts;
+    p.f.T = s.T;
+    p.o2 = o2;
+    p.lam = lam;
+    p.H = s.H;
+    p.Hkv = s.Hkv;
+    return launch_diff_fwd(m, p, s.d, dev->sm_count, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK
+                                                                                                       : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" attn_status_t attn_diff_fwd_bf16(const void* q, const void* k, const void* v, const float* lam, void* o,
+                                            float* lse, void* o2, int B, int H, int Hkv, int N, int d, float scale,
+                                            int causal, int window, void* stream)
+{
+    if (B < 1 || N < 1) return ATTN_ERR_INVALID_ARG;
+    const attn_status_t st = diff_sizes(H, Hkv, d, scale);
+    if (st != ATTN_OK) return st;
+    if (!q || !k || !v || !lam || !o || !lse) return ATTN_ERR_INVALID_ARG;
+    return diff_fwd(q, k, v, lam, o, lse, o2, {B, H, Hkv, N, d, nullptr, 0, -1, scale, causal, window}, stream,
+                    kWaitTimeoutNs, 0);
+}
+
+extern "C" attn_status_t attn_diff_fwd_bf16_varlen(const void* q, const void* k, const void* v, const float* lam,
+                                                   void* o, float* lse, void* o2, const int* cu_seqlens, int num_seqs,
+                                                   int max_seqlen, int total_tokens, int H, int Hkv, int d,
+                                                   float scale, int causal, int window, void* stream)
+{
+    if (num_seqs < 1 || total_tokens < 0 || max_seqlen < 0 || max_seqlen > total_tokens) return ATTN_ERR_INVALID_ARG;
+    const attn_status_t st = diff_sizes(H, Hkv, d, scale);
+    if (st != ATTN_OK) return st;
+    if (total_tokens == 0 || max_seqlen == 0) return ATTN_OK;
+    if (!q || !k || !v || !lam || !o || !lse || !cu_seqlens) return ATTN_ERR_INVALID_ARG;
+    return diff_fwd(q, k, v, lam, o, lse, o2,
+                    {1, H, Hkv, max_seqlen, d, cu_seqlens, num_seqs, total_tokens, scale, causal, window}, stream,
+                    kWaitTimeoutNs, 0);
+}

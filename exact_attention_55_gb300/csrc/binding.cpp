@@ -38,6 +38,9 @@ decltype(&attn_cache_append_bf16) f_append_bf16;
 decltype(&attn_cache_append_fp8) f_append_fp8;
 decltype(&attn_decode_fp8_paged) f_decode;
 decltype(&attn_decode_fp8_workspace_bytes) f_decode_ws;
+decltype(&attn_rope_bf16) f_rope;
+decltype(&attn_diff_fwd_bf16) f_diff_fwd;
+decltype(&attn_diff_fwd_bf16_varlen) f_diff_fwd_varlen;
 
 const Tensor& tensor(PyObject* o, const char* name)
 {
@@ -358,12 +361,205 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
-// The addresses of the five C functions, in the order below.
+// ------------------------------------------------------------------ rotary positions
+
+// bf16 rows of q or k: [T, H, d] or [B, H, N, d], elements of a row contiguous.
+void check_rows(const Tensor& t, at::Device dev, const char* name)
+{
+    if (t.scalar_type() != at::kBFloat16 || t.device() != dev || (t.dim() != 3 && t.dim() != 4))
+        type_error(std::string(name) + " must be a bf16 [T, H, d] or [B, H, N, d] tensor on " + dev.str());
+    if (t.size(-1) > 1 && t.stride(-1) != 1) value_error(std::string(name) + ": a row's elements must be contiguous");
+}
+
+// Strides of batch, token and head; that of a single index does not matter.
+void row_strides(const Tensor& t, bool written, const char* name, long long* out)
+{
+    const int dims[3] = {t.dim() == 4 ? 0 : -1, t.dim() == 4 ? 2 : 0, 1};
+    for (int i = 0; i < 3; ++i) {
+        const bool one = dims[i] < 0 || t.size(dims[i]) <= 1;
+        out[i] = one ? 0 : (long long)t.stride(dims[i]);
+        if (written && !one && out[i] == 0) value_error(std::string(name) + " has several indices at one place");
+    }
+}
+
+// q, k or None, positions, inv_freq, axis or None, interleaved, inverse, q_out, k_out, stream
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 10, [&]() -> PyObject* {
+        const Tensor& q = cuda_tensor(a[0], "q");
+        const at::Device dev = q.device();
+        check_rows(q, dev, "q");
+        const bool keys = a[1] != Py_None, batched = q.dim() == 4;
+        const int64_t B = batched ? q.size(0) : 1, N = q.size(batched ? 2 : 0), d = q.size(-1);
+        int64_t hk = 0;
+        if (keys) {
+            const Tensor& k = tensor(a[1], "k");
+            check_rows(k, dev, "k");
+            if (k.dim() != q.dim() || (batched && k.size(0) != B) || k.size(batched ? 2 : 0) != N || k.size(-1) != d)
+                value_error("k must have q's tokens and d");
+            hk = k.size(1);
+        }
+        const Tensor& pos = tensor(a[2], "positions");
+        const int64_t lead = batched ? 2 : 1;
+        if (pos.dim() != lead && pos.dim() != lead + 1)
+            type_error(std::string("positions must be int32 ") + (batched ? "[B, N] or [axes, B, N]" : "[T] or [axes, T]"));
+        const int64_t axes = pos.dim() == lead ? 1 : pos.size(0);
+        if (batched && pos.dim() == 3) exact(a[2], {axes, B, N}, at::kInt, dev, "positions");
+        else if (batched) exact(a[2], {B, N}, at::kInt, dev, "positions");
+        else if (pos.dim() == 2) exact(a[2], {axes, N}, at::kInt, dev, "positions");
+        else exact(a[2], {N}, at::kInt, dev, "positions");
+        const Tensor& freq = tensor(a[3], "inv_freq");
+        if (freq.dim() != 1) type_error("inv_freq must be a float32 [rot / 2] tensor");
+        exact(a[3], {freq.numel()}, at::kFloat, dev, "inv_freq");
+        const int* axis = nullptr;
+        if (a[4] != Py_None)
+            axis = static_cast<int*>(exact(a[4], {freq.numel()}, at::kInt, dev, "axis").data_ptr());
+        const int interleaved = int_arg(a[5], "interleaved"), inverse = int_arg(a[6], "inverse");
+        const On on(a[9], dev);
+        auto out = [&](PyObject* given, const Tensor& like, const char* name) {
+            if (given == Py_None) return on.empty(like.sizes(), at::kBFloat16, dev);
+            const Tensor& t = tensor(given, name);
+            check_rows(t, dev, name);
+            if (!t.sizes().equals(like.sizes())) value_error(std::string(name) + " must have its input's shape");
+            return t;
+        };
+        long long strides[12] = {};
+        const Tensor qo = out(a[7], q, "q_out");
+        row_strides(q, false, "q", strides);
+        row_strides(qo, true, "q_out", strides + 3);
+        Tensor ko;
+        if (keys) {
+            const Tensor& k = THPVariable_Unpack(a[1]);
+            ko = out(a[8], k, "k_out");
+            row_strides(k, false, "k", strides + 6);
+            row_strides(ko, true, "k_out", strides + 9);
+        }
+        const attn_status_t st =
+            f_rope(q.data_ptr(), keys ? ptr(a[1]) : nullptr, qo.data_ptr(), keys ? ko.data_ptr() : nullptr,
+                   static_cast<int*>(pos.data_ptr()), static_cast<float*>(freq.data_ptr()), axis, strides,
+                   size_arg(B, "B"), size_arg(N, "N"), size_arg(q.size(1), "Hq"), size_arg(hk, "Hk"), size_arg(d, "d"),
+                   size_arg(2 * freq.numel(), "rot"), size_arg(axes, "axes"), interleaved, inverse, on.handle);
+        if (st != ATTN_OK) return status(st);
+        if (keys) return tuple_of({qo, ko});
+        PyObject* first = THPVariable_Wrap(qo);
+        if (!first) throw Refusal{nullptr, ""};
+        PyObject* pair = PyTuple_Pack(2, first, Py_None);
+        Py_DECREF(first);
+        if (!pair) throw Refusal{nullptr, ""};
+        return pair;
+    });
+}
+
+// ------------------------------------------------------------------ differential attention
+
+float scale_arg(PyObject* o, int64_t d)
+{
+    if (o == Py_None) return (float)(1.0 / std::sqrt((double)(d > 0 ? d : 1)));
+    const float scale = (float)PyFloat_AsDouble(o);
+    if (PyErr_Occurred()) throw Refusal{nullptr, ""};
+    return scale;
+}
+
+// Sizes of q [B, 2H, N, d], k [B, 2Hkv, N, d] and v [B, Hkv, N, 2d], or packed [T, 2H, d], [T, 2Hkv, d] and
+// [T, Hkv, 2d] (B = 1, N = T); checked, as lam [H] is.
+struct Diff {
+    at::Device dev;
+    bool packed;
+    int64_t B, H, Hkv, N, d;
+
+    at::DimVector shape(int64_t heads, int64_t width) const
+    {
+        return packed ? at::DimVector{N, heads, width} : at::DimVector{B, heads, N, width};
+    }
+    at::DimVector lse_shape() const { return packed ? at::DimVector{2 * H, N} : at::DimVector{B, 2 * H, N}; }
+};
+
+const Tensor& of_shape(PyObject* o, const at::DimVector& shape, at::ScalarType dtype, at::Device dev, const char* name)
+{
+    return shape.size() == 4   ? exact(o, {shape[0], shape[1], shape[2], shape[3]}, dtype, dev, name)
+           : shape.size() == 3 ? exact(o, {shape[0], shape[1], shape[2]}, dtype, dev, name)
+                               : exact(o, {shape[0], shape[1]}, dtype, dev, name);
+}
+
+Tensor output_of(const On& on, PyObject* o, const at::DimVector& shape, at::ScalarType dtype, at::Device dev,
+                 const char* name)
+{
+    if (o != Py_None) return of_shape(o, shape, dtype, dev, name);
+    return on.empty(shape, dtype, dev);
+}
+
+Diff diff_args(PyObject* const* a, bool packed)
+{
+    const Tensor& q = cuda_tensor(a[0], "q");
+    const Tensor& k = tensor(a[1], "k");
+    const Tensor& v = tensor(a[2], "v");
+    const at::Device dev = q.device();
+    const int64_t dims = packed ? 3 : 4;
+    for (const Tensor* t : {&q, &k, &v})
+        if (t->scalar_type() != at::kBFloat16 || t->device() != dev || t->dim() != dims || !t->is_contiguous())
+            type_error(std::string("q, k and v must be contiguous bf16 ") + (packed ? "[T, heads, d]" : "[B, heads, N, d]") +
+                       " tensors on " + dev.str());
+    Diff s{dev, packed, packed ? 1 : q.size(0), q.size(1) / 2, v.size(1), q.size(packed ? 0 : 2), q.size(-1)};
+    if (q.size(1) % 2 != 0 || s.H < 1 || s.Hkv < 1 || s.H % s.Hkv != 0)
+        value_error("q must have 2 H heads, H a multiple of v's");
+    of_shape(a[1], s.shape(2 * s.Hkv, s.d), at::kBFloat16, dev, "k");
+    of_shape(a[2], s.shape(s.Hkv, 2 * s.d), at::kBFloat16, dev, "v");
+    exact(a[3], {s.H}, at::kFloat, dev, "lam");
+    return s;
+}
+
+// cu_seqlens [S + 1] of packed rows.
+const Tensor& cu_arg(PyObject* o, at::Device dev)
+{
+    const Tensor& cu = tensor(o, "cu_seqlens");
+    if (cu.dim() != 1 || cu.numel() < 2) type_error("cu_seqlens must be an int32 [S + 1] tensor");
+    return exact(o, {cu.numel()}, at::kInt, dev, "cu_seqlens");
+}
+
+float* floats(const Tensor& t) { return static_cast<float*>(t.data_ptr()); }
+
+// q, k, v, lam, cu_seqlens or None, max_seqlen, scale or None, causal, window, save_o2, o, lse, o2, stream
+PyObject* diff_fwd(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 14, [&]() -> PyObject* {
+        const bool packed = a[4] != Py_None;
+        const Diff s = diff_args(a, packed);
+        const float scale = scale_arg(a[6], s.d);
+        const int causal = int_arg(a[7], "causal"), window = int_arg(a[8], "window");
+        const bool save = int_arg(a[9], "save_o2") != 0 || a[12] != Py_None;
+        const Tensor* cu = packed ? &cu_arg(a[4], s.dev) : nullptr;
+        const int longest = packed ? int_arg(a[5], "max_seqlen") : 0;
+        const On on(a[13], s.dev);
+        const Tensor o = output_of(on, a[10], s.shape(s.H, 2 * s.d), at::kBFloat16, s.dev, "o");
+        const Tensor lse = output_of(on, a[11], s.lse_shape(), at::kFloat, s.dev, "lse");
+        Tensor o2;
+        if (save) o2 = output_of(on, a[12], s.shape(s.H, 2 * s.d), at::kBFloat16, s.dev, "o2");
+        const int H = size_arg(s.H, "H"), hkv = size_arg(s.Hkv, "Hkv"), N = size_arg(s.N, "N"), d = size_arg(s.d, "d");
+        void* second = save ? o2.data_ptr() : nullptr;
+        const attn_status_t st =
+            packed ? f_diff_fwd_varlen(ptr(a[0]), ptr(a[1]), ptr(a[2]), static_cast<float*>(ptr(a[3])), o.data_ptr(),
+                                       floats(lse), second, static_cast<int*>(cu->data_ptr()),
+                                       size_arg(cu->numel() - 1, "S"), longest, N, H, hkv, d, scale, causal, window,
+                                       on.handle)
+                   : f_diff_fwd(ptr(a[0]), ptr(a[1]), ptr(a[2]), static_cast<float*>(ptr(a[3])), o.data_ptr(),
+                                floats(lse), second, size_arg(s.B, "B"), H, hkv, N, d, scale, causal, window, on.handle);
+        if (st != ATTN_OK) return status(st);
+        if (save) return tuple_of({o, lse, o2});
+        PyObject* two = tuple_of({o, lse});
+        PyObject* out = PyTuple_Pack(3, PyTuple_GET_ITEM(two, 0), PyTuple_GET_ITEM(two, 1), Py_None);
+        Py_DECREF(two);
+        if (!out) throw Refusal{nullptr, ""};
+        return out;
+    });
+}
+
+// The addresses of the C functions, in the order below.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded(n, 5, [&]() -> PyObject* {
-        void* f[5];
-        for (int i = 0; i < 5; ++i) {
+    constexpr int kCount = 8;
+    return guarded(n, kCount, [&]() -> PyObject* {
+        void* f[kCount];
+        for (int i = 0; i < kCount; ++i) {
             f[i] = PyLong_AsVoidPtr(a[i]);
             if (PyErr_Occurred()) throw Refusal{nullptr, ""};
         }
@@ -372,6 +568,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
         f_append_fp8 = reinterpret_cast<decltype(f_append_fp8)>(f[2]);
         f_decode = reinterpret_cast<decltype(f_decode)>(f[3]);
         f_decode_ws = reinterpret_cast<decltype(f_decode_ws)>(f[4]);
+        f_rope = reinterpret_cast<decltype(f_rope)>(f[5]);
+        f_diff_fwd = reinterpret_cast<decltype(f_diff_fwd)>(f[6]);
+        f_diff_fwd_varlen = reinterpret_cast<decltype(f_diff_fwd_varlen)>(f[7]);
         Py_RETURN_NONE;
     });
 }
@@ -384,7 +583,8 @@ PyMethodDef method(const char* name)
 
 PyMethodDef methods[] = {method<bind>("bind"),           method<plan>("plan"),
                          method<append_bf16>("append_bf16"), method<append_fp8>("append_fp8"),
-                         method<decode>("decode"),       {nullptr, nullptr, 0, nullptr}};
+                         method<decode>("decode"),       method<rope>("rope"),
+                         method<diff_fwd>("diff_fwd"),   {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gb300attn_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -476,6 +476,70 @@ attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cache, const vo
                                     int format, float scale, int window, void* workspace,
                                     size_t workspace_bytes, void* stream);
 
+/*
+ * attn_rope_bf16 -- rotary positions of queries and keys, on one or several axes.
+ *
+ * The pages describe attention on q and k as given; a model with rotary positions turns them
+ * first, in the forward pass and, by the opposite angle, their gradients in the backward pass.
+ * Pair i < rot / 2 of a row is elements (i, rot/2 + i), or (2i, 2i + 1) when interleaved != 0:
+ *     angle = positions[axis[i]][token] * inv_freq[i]   (negated when inverse != 0)
+ *     (x, y) -> (x cos(angle) - y sin(angle), x sin(angle) + y cos(angle))
+ * and elements rot .. d-1 are copied.  Axes are, say, one for text, or time, height and width of
+ * images and video, each with its run of pairs, or pairs in turn: `axis` says which.
+ *   q, k        : const bf16, rows of d elements; token (b, n) of head h at
+ *                 b * batch + n * token + h * head elements, by the strides below
+ *   q_out, k_out : bf16, written, with strides of their own; each may be its input (in place),
+ *                 and overlaps nothing else.  Hk = 0: no keys (k, k_out may be null)
+ *   positions   : const int32 [axes, B, N].  A token whose position on axis 0 is negative is
+ *                 padding (attn_paged_plan's -1): its rows are copied as they are.  On the other
+ *                 axes negative positions turn backwards
+ *   inv_freq    : const float [rot / 2], radians per position; finite (else the pair is NaN).
+ *                 The angle is computed from its fp32 value exactly to 2^-32 of a turn, plus
+ *                 2^-38 of one at position 2^20 and frequencies up to 1
+ *   axis        : const int32 [rot / 2], clamped to [0, axes); null: all pairs on axis 0
+ *   strides     : host array of 12, in elements, multiples of 8: batch, token and head of q, of
+ *                 q_out, of k and of k_out (the last six are not read when Hk = 0)
+ *   d and rot multiples of 16, 16 <= rot <= d <= 256 (else ATTN_ERR_UNSUPPORTED);
+ *   B * N == 0 returns ATTN_OK
+ * Alignment: tensors 16 bytes, positions, inv_freq and axis 4 bytes.  HBM-bound.
+ */
+attn_status_t attn_rope_bf16(const void* q, const void* k, void* q_out, void* k_out,
+                             const int* positions, const float* inv_freq, const int* axis,
+                             const long long* strides, int B, int N, int Hq, int Hk, int d, int rot,
+                             int axes, int interleaved, int inverse, void* stream);
+
+/*
+ * attn_diff_fwd_bf16 -- differential attention: the difference of two softmax maps.
+ *
+ * [YT] §1.2 fuses mask, softmax and both matmuls of one map; here a head has two, with query
+ * heads 2h and 2h + 1, a pair of key heads, one value head of width 2d, and a learned weight:
+ *     S_m = scale * Q_m K_m^T + mask,  P_m = softmax(S_m)  (m = 1, 2)
+ *     O = (P_1 - lam[h] P_2) V,  LSE_m = natural log-sum-exp of S_m,  O_2 = P_2 V
+ * Heads h share key pair and value head h / (H / Hkv).
+ *   q    : const bf16 [B, 2H, N, d]
+ *   k    : const bf16 [B, 2Hkv, N, d];  v : const bf16 [B, Hkv, N, 2d]
+ *   lam  : const float [H] on the device
+ *   o    : bf16 [B, H, N, 2d], written;  lse : float [B, 2H, N], written
+ *   o2   : bf16 [B, H, N, 2d], written, or null: the second map's output, for the backward pass
+ *   H a multiple of Hkv;  d in {64, 128} (else ATTN_ERR_UNSUPPORTED)
+ *   scale, causal, window as attn_fwd_bf16
+ * Scores, sums and outputs are fp32 until the last rounding; P_1 and P_2 are rounded to bf16, each
+ * relative to its row's running maximum, for the product with V.  Every row of v has to be finite
+ * (a masked key in a tile enters as 0 * v).
+ *
+ * attn_diff_fwd_bf16_varlen -- the same over packed sequences, as attn_fwd_bf16_varlen: q
+ * [T, 2H, d], k [T, 2Hkv, d], v [T, Hkv, 2d], o and o2 [T, H, 2d], lse [2H, T].  Tokens outside
+ * every sequence may hold anything, NaN too, and their outputs are not written.
+ */
+attn_status_t attn_diff_fwd_bf16(const void* q, const void* k, const void* v, const float* lam,
+                                 void* o, float* lse, void* o2, int B, int H, int Hkv, int N, int d,
+                                 float scale, int causal, int window, void* stream);
+attn_status_t attn_diff_fwd_bf16_varlen(const void* q, const void* k, const void* v,
+                                        const float* lam, void* o, float* lse, void* o2,
+                                        const int* cu_seqlens, int num_seqs, int max_seqlen,
+                                        int total_tokens, int H, int Hkv, int d, float scale,
+                                        int causal, int window, void* stream);
+
 /* Static English text for a status code (never NULL). */
 const char* attn_status_string(attn_status_t status);
 
