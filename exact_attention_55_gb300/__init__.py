@@ -42,6 +42,7 @@ __all__ = [
     "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
     "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes",
     "attn_rope_bf16", "attn_diff_fwd_bf16", "attn_diff_fwd_bf16_varlen",
+    "attn_diff_bwd_bf16", "attn_diff_bwd_bf16_varlen", "attn_diff_bwd_workspace_bytes",
     "attn_quantize_fp8_blockwise", "attn_quantize_fp8_hadamard", "attn_fwd_fp8",
     "attn_quantize_fp8_blockwise_fmt", "attn_fwd_fp8_fmt", "attn_fwd_fp8_blocks",
     "attn_fp8_qk_block_rows", "attn_fwd_schedule", "ATTN_FP8_E4M3", "ATTN_FP8_E5M2",
@@ -74,6 +75,7 @@ EXPORTED_SYMBOLS = (
     "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
     "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes",
     "attn_rope_bf16", "attn_diff_fwd_bf16", "attn_diff_fwd_bf16_varlen",
+    "attn_diff_bwd_bf16", "attn_diff_bwd_bf16_varlen", "attn_diff_bwd_workspace_bytes",
     "attn_quantize_fp8_blockwise", "attn_quantize_fp8_blockwise_fmt",
     "attn_quantize_fp8_hadamard",
     "attn_fwd_fp8", "attn_fwd_fp8_fmt", "attn_fwd_fp8_blocks", "attn_fp8_qk_block_rows",
@@ -147,6 +149,13 @@ def load_library(path: str | None = None):
         lib.attn_diff_fwd_bf16.restype = i
         lib.attn_diff_fwd_bf16_varlen.argtypes = [vp] * 8 + [i] * 6 + [f, i, i, vp]
         lib.attn_diff_fwd_bf16_varlen.restype = i
+        lib.attn_diff_bwd_workspace_bytes.argtypes = [i, i, i]
+        lib.attn_diff_bwd_workspace_bytes.restype = ctypes.c_size_t
+        lib.attn_diff_bwd_bf16.argtypes = [vp] * 13 + [ctypes.c_size_t] + [i] * 5 + [f, i, i, vp]
+        lib.attn_diff_bwd_bf16.restype = i
+        lib.attn_diff_bwd_bf16_varlen.argtypes = ([vp] * 13 + [ctypes.c_size_t, vp] + [i] * 6
+                                                  + [f, i, i, vp])
+        lib.attn_diff_bwd_bf16_varlen.restype = i
         lib.attn_quantize_fp8_blockwise.argtypes = [vp, vp, vp, i, i, i, i, i, vp]
         lib.attn_quantize_fp8_blockwise.restype = i
         lib.attn_quantize_fp8_hadamard.argtypes = [vp, vp, vp, i, i, i, i, i, vp]
@@ -435,7 +444,8 @@ def _native():
                 binding.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
                     "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
                     "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes", "attn_rope_bf16",
-                    "attn_diff_fwd_bf16", "attn_diff_fwd_bf16_varlen")))
+                    "attn_diff_fwd_bf16", "attn_diff_fwd_bf16_varlen", "attn_diff_bwd_bf16",
+                    "attn_diff_bwd_bf16_varlen", "attn_diff_bwd_workspace_bytes")))
                 _binding = binding
     return _binding
 
@@ -553,6 +563,37 @@ def attn_diff_fwd_bf16_varlen(q, k, v, lam, cu_seqlens, max_seqlen: int,
                            int(bool(save_o2)), o, lse, o2, _stream_on(stream, q))
     if type(r) is int:
         raise AttnError(r, "attn_diff_fwd_bf16_varlen")
+    return r
+
+
+def attn_diff_bwd_workspace_bytes(B: int, H: int, N: int) -> int:
+    """Workspace bytes attn_diff_bwd_bf16 needs (packed sequences: B = 1, N = T)."""
+    return int(load_library().attn_diff_bwd_workspace_bytes(int(B), int(H), int(N)))
+
+
+def attn_diff_bwd_bf16(q, k, v, lam, o, o2, dout, lse, scale: float | None = None,
+                       causal: bool = False, window: int = 0, dq=None, dk=None, dv=None, dlam=None,
+                       workspace=None, stream=None):
+    """Backward pass of attn_diff_fwd_bf16 (same scale and mask) for the upstream gradient dout:
+    returns (dQ, dK, dV, dlam float32 [H]), given the forward's o, o2 (save_o2=True) and lse."""
+    r = _native().diff_bwd(q, k, v, lam, o, o2, dout, lse, None, 0, scale, int(bool(causal)), window,
+                           dq, dk, dv, dlam, workspace, _stream_on(stream, q))
+    if type(r) is int:
+        raise AttnError(r, "attn_diff_bwd_bf16")
+    return r
+
+
+def attn_diff_bwd_bf16_varlen(q, k, v, lam, o, o2, dout, lse, cu_seqlens, max_seqlen: int,
+                              scale: float | None = None, causal: bool = False, window: int = 0,
+                              dq=None, dk=None, dv=None, dlam=None, workspace=None, stream=None):
+    """attn_diff_bwd_bf16 over packed sequences, given attn_diff_fwd_bf16_varlen's o, o2 and lse."""
+    if cu_seqlens is None:
+        raise TypeError("cu_seqlens must be an int32 [S + 1] tensor")
+    r = _native().diff_bwd(q, k, v, lam, o, o2, dout, lse, cu_seqlens, max_seqlen, scale,
+                           int(bool(causal)), window, dq, dk, dv, dlam, workspace,
+                           _stream_on(stream, q))
+    if type(r) is int:
+        raise AttnError(r, "attn_diff_bwd_bf16_varlen")
     return r
 
 

@@ -42,6 +42,7 @@ UNITS = [
     ("decode_fp8", "decode_fp8.cu", []),
     ("paged", "paged.cu", []),
     ("attn_bwd", "attn_bwd.cu", []),
+    ("diff_bwd", "diff_bwd.cu", []),
     ("diff_fwd", "diff_fwd.cu", []),
     ("rope", "rope.cu", []),
     ("api_diff", "api_diff.cu", []),

@@ -133,6 +133,66 @@ attn_status_t diff_fwd(const void* q, const void* k, const void* v, const float*
                                                                                                        : ATTN_ERR_CUDA;
 }
 
+// The workspace: two counters in 16 bytes, then D_1 and D_2 of every row, laid out as the LSE.
+constexpr size_t kDiffBwdHead = 16;
+
+attn_status_t diff_bwd(const void* q, const void* k, const void* v, const float* lam, const void* o, const void* o2,
+                       const void* dout, const float* lse, void* dq, void* dk, void* dv, float* dlam, void* workspace,
+                       const DiffShape& s, void* stream, unsigned long long timeout_ns, int withhold)
+{
+    for (const void* t : {q, k, v, o, o2, dout, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                          static_cast<const void*>(dv), static_cast<const void*>(workspace)})
+        if (!aligned(t, 16)) return ATTN_ERR_MISALIGNED;
+    if (!aligned(lam, 4) || !aligned(lse, 4) || !aligned(dlam, 4) || !aligned(s.cu_seqlens, 4))
+        return ATTN_ERR_MISALIGNED;
+    if (s.N > kDiffMaxRows || s.T > kDiffMaxRows || s.H > 65535) return ATTN_ERR_UNSUPPORTED;
+    const bool packed = s.T >= 0;
+    const int seqs = packed ? s.num_seqs : s.B;
+    const long long tiles = ((long long)s.N + 127) / 128, units = tiles * seqs * 2 * s.H;
+    DeviceInfo* dev = nullptr;
+    const attn_status_t st = device_info(&dev);
+    if (st != ATTN_OK) return st;
+    // unit numbers, the counter's last value and the rows of the first kernel's grid stay in int
+    const long long rows = (packed ? (long long)s.T : (long long)s.B * s.N) * s.H;
+    if (units + 4LL * dev->sm_count > 0x7fffffffLL || rows / 8 > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+    alignas(64) DiffBwdMaps m;
+    if (!diff_map(&m.q, q, s.d, 2 * s.H, s.B, s.N, s.T, 128) || !diff_map(&m.q64, q, s.d, 2 * s.H, s.B, s.N, s.T, 64) ||
+        !diff_map(&m.dout, dout, 2 * s.d, s.H, s.B, s.N, s.T, 128) ||
+        !diff_map(&m.dout64, dout, 2 * s.d, s.H, s.B, s.N, s.T, 64) ||
+        !diff_map(&m.k, k, s.d, 2 * s.Hkv, s.B, s.N, s.T, 128) || !diff_map(&m.v, v, 2 * s.d, s.Hkv, s.B, s.N, s.T, 128) ||
+        !diff_map(&m.k64, k, s.d, 2 * s.Hkv, s.B, s.N, s.T, 64) || !diff_map(&m.v64, v, 2 * s.d, s.Hkv, s.B, s.N, s.T, 64))
+        return ATTN_ERR_CUDA;
+    DiffBwdParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.o = o;
+    p.o2 = o2;
+    p.dout = dout;
+    p.lse = lse;
+    p.lam = lam;
+    p.next = static_cast<int*>(workspace);
+    p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kDiffBwdHead);
+    p.dlam = dlam;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.status = dev->status;
+    p.B = seqs;
+    p.H = s.H;
+    p.Hkv = s.Hkv;
+    p.N = s.N;
+    p.nt = (int)tiles;
+    p.causal = s.causal ? 1 : 0;
+    p.window = s.window > 0 && s.window < s.N ? s.window : 0;
+    p.c_log2 = (float)((double)s.scale * 1.4426950408889634);
+    p.scale = s.scale;
+    p.timeout_ns = timeout_ns;
+    p.withhold = withhold;
+    p.cu_seqlens = s.cu_seqlens;
+    p.T = s.T;
+    return launch_diff_bwd(m, p, s.d, dev->sm_count, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK
+                                                                                                       : ATTN_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" attn_status_t attn_diff_fwd_bf16(const void* q, const void* k, const void* v, const float* lam, void* o,
@@ -158,6 +218,52 @@ extern "C" attn_status_t attn_diff_fwd_bf16_varlen(const void* q, const void* k,
     if (total_tokens == 0 || max_seqlen == 0) return ATTN_OK;
     if (!q || !k || !v || !lam || !o || !lse || !cu_seqlens) return ATTN_ERR_INVALID_ARG;
     return diff_fwd(q, k, v, lam, o, lse, o2,
+                    {1, H, Hkv, max_seqlen, d, cu_seqlens, num_seqs, total_tokens, scale, causal, window}, stream,
+                    kWaitTimeoutNs, 0);
+}
+
+extern "C" size_t attn_diff_bwd_workspace_bytes(int B, int H, int N)
+{
+    if (B < 1 || H < 1 || N < 1) return 0;
+    return kDiffBwdHead + (size_t)B * H * N * 2 * sizeof(float);
+}
+
+extern "C" attn_status_t attn_diff_bwd_bf16(const void* q, const void* k, const void* v, const float* lam,
+                                            const void* o, const void* o2, const void* dout, const float* lse, void* dq,
+                                            void* dk, void* dv, float* dlam, void* workspace, size_t workspace_bytes,
+                                            int B, int H, int Hkv, int N, int d, float scale, int causal, int window,
+                                            void* stream)
+{
+    if (B < 1 || N < 1) return ATTN_ERR_INVALID_ARG;
+    const attn_status_t st = diff_sizes(H, Hkv, d, scale);
+    if (st != ATTN_OK) return st;
+    if (!q || !k || !v || !lam || !o || !o2 || !dout || !lse || !dq || !dk || !dv || !dlam || !workspace)
+        return ATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < attn_diff_bwd_workspace_bytes(B, H, N)) return ATTN_ERR_INVALID_ARG;
+    return diff_bwd(q, k, v, lam, o, o2, dout, lse, dq, dk, dv, dlam, workspace,
+                    {B, H, Hkv, N, d, nullptr, 0, -1, scale, causal, window}, stream, kWaitTimeoutNs, 0);
+}
+
+extern "C" attn_status_t attn_diff_bwd_bf16_varlen(const void* q, const void* k, const void* v, const float* lam,
+                                                   const void* o, const void* o2, const void* dout, const float* lse,
+                                                   void* dq, void* dk, void* dv, float* dlam, void* workspace,
+                                                   size_t workspace_bytes, const int* cu_seqlens, int num_seqs,
+                                                   int max_seqlen, int total_tokens, int H, int Hkv, int d, float scale,
+                                                   int causal, int window, void* stream)
+{
+    if (num_seqs < 1 || total_tokens < 0 || max_seqlen < 0 || max_seqlen > total_tokens) return ATTN_ERR_INVALID_ARG;
+    const attn_status_t st = diff_sizes(H, Hkv, d, scale);
+    if (st != ATTN_OK) return st;
+    if (!dlam) return ATTN_ERR_INVALID_ARG;
+    if (total_tokens == 0 || max_seqlen == 0) {          // no rows: the sum over them is 0
+        if (!aligned(dlam, 4)) return ATTN_ERR_MISALIGNED;
+        return cudaMemsetAsync(dlam, 0, (size_t)H * sizeof(float), static_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? ATTN_OK : ATTN_ERR_CUDA;
+    }
+    if (!q || !k || !v || !lam || !o || !o2 || !dout || !lse || !dq || !dk || !dv || !workspace || !cu_seqlens)
+        return ATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < attn_diff_bwd_workspace_bytes(1, H, total_tokens)) return ATTN_ERR_INVALID_ARG;
+    return diff_bwd(q, k, v, lam, o, o2, dout, lse, dq, dk, dv, dlam, workspace,
                     {1, H, Hkv, max_seqlen, d, cu_seqlens, num_seqs, total_tokens, scale, causal, window}, stream,
                     kWaitTimeoutNs, 0);
 }

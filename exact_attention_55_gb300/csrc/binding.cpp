@@ -41,6 +41,9 @@ decltype(&attn_decode_fp8_workspace_bytes) f_decode_ws;
 decltype(&attn_rope_bf16) f_rope;
 decltype(&attn_diff_fwd_bf16) f_diff_fwd;
 decltype(&attn_diff_fwd_bf16_varlen) f_diff_fwd_varlen;
+decltype(&attn_diff_bwd_bf16) f_diff_bwd;
+decltype(&attn_diff_bwd_bf16_varlen) f_diff_bwd_varlen;
+decltype(&attn_diff_bwd_workspace_bytes) f_diff_bwd_ws;
 
 const Tensor& tensor(PyObject* o, const char* name)
 {
@@ -553,10 +556,70 @@ PyObject* diff_fwd(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// A workspace of the caller's, or one that the stream's allocator lends for the call.
+struct Workspace {
+    c10::DataPtr lent;
+    void* ptr;
+    size_t bytes;
+
+    Workspace(PyObject* given, size_t needed, at::Device dev)
+    {
+        if (given == Py_None) {
+            bytes = needed;
+            lent = c10::cuda::CUDACachingAllocator::get()->allocate(needed);
+            ptr = lent.get();
+            return;
+        }
+        const Tensor& t = tensor(given, "workspace");
+        if (t.device() != dev || !t.is_contiguous()) type_error("workspace must be a contiguous CUDA tensor on " + dev.str());
+        ptr = t.data_ptr();
+        bytes = (size_t)t.nbytes();
+    }
+};
+
+// q, k, v, lam, o, o2, dout, lse, cu_seqlens or None, max_seqlen, scale or None, causal, window, dq, dk, dv,
+// dlam, workspace, stream
+PyObject* diff_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 19, [&]() -> PyObject* {
+        const bool packed = a[8] != Py_None;
+        const Diff s = diff_args(a, packed);
+        const at::DimVector out = s.shape(s.H, 2 * s.d);
+        of_shape(a[4], out, at::kBFloat16, s.dev, "o");
+        of_shape(a[5], out, at::kBFloat16, s.dev, "o2");
+        of_shape(a[6], out, at::kBFloat16, s.dev, "dout");
+        of_shape(a[7], s.lse_shape(), at::kFloat, s.dev, "lse");
+        const Tensor* cu = packed ? &cu_arg(a[8], s.dev) : nullptr;
+        const int longest = packed ? int_arg(a[9], "max_seqlen") : 0;
+        const float scale = scale_arg(a[10], s.d);
+        const int causal = int_arg(a[11], "causal"), window = int_arg(a[12], "window");
+        const int B = size_arg(s.B, "B"), H = size_arg(s.H, "H"), hkv = size_arg(s.Hkv, "Hkv");
+        const int N = size_arg(s.N, "N"), d = size_arg(s.d, "d");
+        const On on(a[18], s.dev);
+        const Tensor dq = output_of(on, a[13], s.shape(2 * s.H, s.d), at::kBFloat16, s.dev, "dq");
+        const Tensor dk = output_of(on, a[14], s.shape(2 * s.Hkv, s.d), at::kBFloat16, s.dev, "dk");
+        const Tensor dv = output_of(on, a[15], s.shape(s.Hkv, 2 * s.d), at::kBFloat16, s.dev, "dv");
+        const Tensor dlam = on.output(a[16], {s.H}, at::kFloat, s.dev, "dlam");
+        const Workspace ws(a[17], f_diff_bwd_ws(B, H, N), s.dev);
+        auto bf = [&](int i) { return ptr(a[i]); };
+        float *lam = static_cast<float*>(bf(3)), *lse = static_cast<float*>(bf(7));
+        const attn_status_t st =
+            packed ? f_diff_bwd_varlen(bf(0), bf(1), bf(2), lam, bf(4), bf(5), bf(6), lse, dq.data_ptr(), dk.data_ptr(),
+                                       dv.data_ptr(), floats(dlam), ws.ptr, ws.bytes, static_cast<int*>(cu->data_ptr()),
+                                       size_arg(cu->numel() - 1, "S"), longest, N, H, hkv, d, scale, causal, window,
+                                       on.handle)
+                   : f_diff_bwd(bf(0), bf(1), bf(2), lam, bf(4), bf(5), bf(6), lse, dq.data_ptr(), dk.data_ptr(),
+                                dv.data_ptr(), floats(dlam), ws.ptr, ws.bytes, B, H, hkv, N, d, scale, causal, window,
+                                on.handle);
+        if (st != ATTN_OK) return status(st);
+        return tuple_of({dq, dk, dv, dlam});
+    });
+}
+
 // The addresses of the C functions, in the order below.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    constexpr int kCount = 8;
+    constexpr int kCount = 11;
     return guarded(n, kCount, [&]() -> PyObject* {
         void* f[kCount];
         for (int i = 0; i < kCount; ++i) {
@@ -571,6 +634,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
         f_rope = reinterpret_cast<decltype(f_rope)>(f[5]);
         f_diff_fwd = reinterpret_cast<decltype(f_diff_fwd)>(f[6]);
         f_diff_fwd_varlen = reinterpret_cast<decltype(f_diff_fwd_varlen)>(f[7]);
+        f_diff_bwd = reinterpret_cast<decltype(f_diff_bwd)>(f[8]);
+        f_diff_bwd_varlen = reinterpret_cast<decltype(f_diff_bwd_varlen)>(f[9]);
+        f_diff_bwd_ws = reinterpret_cast<decltype(f_diff_bwd_ws)>(f[10]);
         Py_RETURN_NONE;
     });
 }
@@ -584,7 +650,8 @@ PyMethodDef method(const char* name)
 PyMethodDef methods[] = {method<bind>("bind"),           method<plan>("plan"),
                          method<append_bf16>("append_bf16"), method<append_fp8>("append_fp8"),
                          method<decode>("decode"),       method<rope>("rope"),
-                         method<diff_fwd>("diff_fwd"),   {nullptr, nullptr, 0, nullptr}};
+                         method<diff_fwd>("diff_fwd"),   method<diff_bwd>("diff_bwd"),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gb300attn_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -43,8 +43,40 @@ struct DiffFwdMaps {
     CUtensorMap q, k, v;    // 128-row boxes of 64 columns
 };
 
+// Backward pass of differential attention.  Packed layout: B sequences' offsets in cu_seqlens, N the
+// longest.
+struct DiffBwdParams {
+    const void* o;          // bf16 [B, H, N, 2d] or [T, H, 2d], as the forward pass wrote them
+    const void* o2;
+    const void* dout;
+    const float* lse;       // fp32 [B, 2H, N] or [2H, T]
+    const float* lam;       // fp32 [H]
+    float* delta;           // fp32, laid out as lse: dO . O_1 and dO . O_2 of every row
+    float* dlam;            // fp32 [H]
+    void* dq;               // bf16 [B, 2H, N, d] or [T, 2H, d]
+    void* dk;               // bf16 [B, 2Hkv, N, d] or [T, 2Hkv, d]
+    void* dv;               // bf16 [B, Hkv, N, 2d] or [T, Hkv, 2d]
+    int* next;              // [2]: the next unit of each pass, 0 before the first
+    int* status;
+    int B, H, Hkv, N;
+    int nt;                 // 128-row tiles of N rows
+    int causal, window;
+    float c_log2, scale;
+    unsigned long long timeout_ns;
+    int withhold;           // 0, or n: each CTA's n-th ring load is never issued (failure tests)
+    const int* cu_seqlens;  // int32 [B + 1], or null: batched
+    int T;
+};
+
+struct DiffBwdMaps {
+    CUtensorMap q, k, v, dout;      // 128-row boxes of 64 columns
+    CUtensorMap q64, k64, v64, dout64;   // 64-row boxes
+};
+
 cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_diff_fwd(const DiffFwdMaps& m, const DiffFwdParams& p, int d, int sm_count,
+                            cudaStream_t stream);
+cudaError_t launch_diff_bwd(const DiffBwdMaps& m, const DiffBwdParams& p, int d, int sm_count,
                             cudaStream_t stream);
 
 }  // namespace gb300

@@ -540,6 +540,44 @@ attn_status_t attn_diff_fwd_bf16_varlen(const void* q, const void* k, const void
                                         int total_tokens, int H, int Hkv, int d, float scale,
                                         int causal, int window, void* stream);
 
+/*
+ * attn_diff_bwd_bf16 -- backward pass of attn_diff_fwd_bf16: dQ, dK, dV and d lam for an upstream
+ * dO ([YT] §2.3.2, as attn_bwd_bf16).
+ *
+ * With P_m = exp(scale * Q_m K_m^T + mask - LSE_m), f_1 = 1, f_2 = -lam[h] and, per row,
+ * D_1 = dO . (O + lam[h] O_2), D_2 = dO . O_2:
+ *     dP = dO V^T,  dS_m = f_m P_m * (dP - D_m),
+ *     dQ_m = scale * dS_m K_m,  dK_m = scale * dS_m^T Q_m,  dV = (f_1 P_1 + f_2 P_2)^T dO,
+ *     dlam[h] = - sum over the rows of D_2
+ * with dK and dV summed over the heads that share them, all sums in fp32, in a fixed order.
+ *   q, k, v, lam : as the forward call;  o, o2, lse : as it wrote them (o2 is needed)
+ *   dout         : const bf16, laid out as o
+ *   dq, dk, dv   : bf16, laid out as q, k and v, written;  dlam : float [H], written
+ *   workspace    : 16-byte aligned device memory of at least
+ *                  attn_diff_bwd_workspace_bytes(B, H, N) bytes; its contents do not matter.
+ *                  Calls that may overlap need one each
+ *   sizes, scale, causal, window as the forward call
+ * Finite inputs are expected at every row, masked ones too, as in the forward pass.
+ *
+ * attn_diff_bwd_bf16_varlen -- the same over packed sequences, as attn_diff_fwd_bf16_varlen, with a
+ * workspace of attn_diff_bwd_workspace_bytes(1, H, T) bytes.  Tokens outside every sequence may
+ * hold anything; their gradients are not written and do not count in dlam.  T == 0 or
+ * max_seqlen == 0: dlam = 0, nothing else.
+ */
+size_t attn_diff_bwd_workspace_bytes(int B, int H, int N);
+attn_status_t attn_diff_bwd_bf16(const void* q, const void* k, const void* v, const float* lam,
+                                 const void* o, const void* o2, const void* dout, const float* lse,
+                                 void* dq, void* dk, void* dv, float* dlam, void* workspace,
+                                 size_t workspace_bytes, int B, int H, int Hkv, int N, int d,
+                                 float scale, int causal, int window, void* stream);
+attn_status_t attn_diff_bwd_bf16_varlen(const void* q, const void* k, const void* v,
+                                        const float* lam, const void* o, const void* o2,
+                                        const void* dout, const float* lse, void* dq, void* dk,
+                                        void* dv, float* dlam, void* workspace,
+                                        size_t workspace_bytes, const int* cu_seqlens, int num_seqs,
+                                        int max_seqlen, int total_tokens, int H, int Hkv, int d,
+                                        float scale, int causal, int window, void* stream);
+
 /* Static English text for a status code (never NULL). */
 const char* attn_status_string(attn_status_t status);
 

@@ -77,6 +77,46 @@ def forward(q, k, v, lam, scale, ok):
     return dict(o=o, o2=o2, lse=lse, p=p, o_bound=bound, o2_bound=bound2, lse_bound=bound_lse)
 
 
+def backward(q, k, v, lam, o, o2, dout, lse, scale, ok, rounded=0.0):
+    """One sequence's gradients by the formulas on what the forward pass saved (any precision), and their
+    bounds.  `rounded`: how far o and o2 are from the definition's, relative (HALF where the kernels'
+    own are compared with gradients of the definition)."""
+    q, k, v, lam, o, o2, dout, lse = (t.double() for t in (q, k, v, lam, o, o2, dout, lse))
+    H, Hkv, n, d = q.shape[0] // 2, k.shape[0] // 2, q.shape[1], q.shape[2]
+    G = H // Hkv
+    kk = k.view(Hkv, 2, -1, d).repeat_interleave(G, 0)              # [H, 2, m, d]
+    qq, vv = q.view(H, 2, n, d), v.repeat_interleave(G, 0)
+    w = lam[:, None, None]
+    s = (qq @ kk.transpose(2, 3) * scale).masked_fill(~ok, -math.inf)
+    p = torch.exp(s - lse.view(H, 2, n, 1)) * torch.stack((torch.ones_like(w), -w), 1)
+    dot2 = (dout * o2).sum(2, keepdim=True)
+    dot = torch.stack(((dout * o).sum(2, keepdim=True) + w * dot2, dot2), 1)    # [H, 2, n, 1]
+    dp = (dout @ vv.transpose(1, 2))[:, None]
+    ds = p * (dp - dot)
+    heads = lambda t: t.view(Hkv, G, *t.shape[1:]).sum(1)
+    dq = (ds @ kk * scale).flatten(0, 1)
+    dk = heads(ds.transpose(2, 3) @ qq * scale).flatten(0, 1)
+    dv = heads((p.sum(1)).transpose(1, 2) @ dout)
+    dlam = -dot2.sum((1, 2))
+    # A weight is off by its score's error (fp32 sums of d products) and 2^-20 for the fp32 LSE, the
+    # exponential and its argument; dP - D by fp32 sums of 2d products and what o and o2 are off;
+    # what enters the products is rounded once to bf16; their sums are fp32 (2^-12: 2^12 terms).
+    err = ((qq.abs() @ kk.abs().transpose(2, 3) * scale).masked_fill(~ok, 0.0).amax((1, 2, 3)) * d * 2.0 ** -23
+           + 2.0 ** -20 + lse.view(H, -1).abs().amax(1) * 2.0 ** -23)[:, None, None, None]
+    size2 = (dout.abs() * o2.abs()).sum(2, keepdim=True)
+    size1 = (dout.abs() * o.abs()).sum(2, keepdim=True) + w.abs() * size2
+    size = torch.stack((size1, size2), 1)
+    off = 2 * d * 2.0 ** -24 * ((dout.abs() @ vv.abs().transpose(1, 2))[:, None] + size) + rounded * size
+    rel = HALF + 2.0 ** -12 + err
+    eds = rel * ds.abs() + p.abs() * (1 + HALF) * off
+    ep = rel * p.abs()
+    bq = (eds @ kk.abs() * scale).flatten(0, 1) + HALF * dq.abs()
+    bk = heads(eds.transpose(2, 3) @ qq.abs() * scale).flatten(0, 1) + HALF * dk.abs()
+    bv = heads(ep.sum(1).transpose(1, 2) @ dout.abs()) + HALF * dv.abs()
+    blam = (rounded + 2.0 ** -16) * size2.sum((1, 2))
+    return (dq, dk, dv, dlam), (bq, bk, bv, blam)
+
+
 def check(got, want, bound, name):
     """|got - want| <= bound everywhere; infinities equal."""
     got = got.detach().cpu().double()
