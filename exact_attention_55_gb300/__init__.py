@@ -43,6 +43,7 @@ __all__ = [
     "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes",
     "attn_rope_bf16", "attn_diff_fwd_bf16", "attn_diff_fwd_bf16_varlen",
     "attn_diff_bwd_bf16", "attn_diff_bwd_bf16_varlen", "attn_diff_bwd_workspace_bytes",
+    "attn_diff_decode_bf16_paged", "attn_diff_decode_workspace_bytes",
     "attn_quantize_fp8_blockwise", "attn_quantize_fp8_hadamard", "attn_fwd_fp8",
     "attn_quantize_fp8_blockwise_fmt", "attn_fwd_fp8_fmt", "attn_fwd_fp8_blocks",
     "attn_fp8_qk_block_rows", "attn_fwd_schedule", "ATTN_FP8_E4M3", "ATTN_FP8_E5M2",
@@ -76,6 +77,7 @@ EXPORTED_SYMBOLS = (
     "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes",
     "attn_rope_bf16", "attn_diff_fwd_bf16", "attn_diff_fwd_bf16_varlen",
     "attn_diff_bwd_bf16", "attn_diff_bwd_bf16_varlen", "attn_diff_bwd_workspace_bytes",
+    "attn_diff_decode_bf16_paged", "attn_diff_decode_workspace_bytes",
     "attn_quantize_fp8_blockwise", "attn_quantize_fp8_blockwise_fmt",
     "attn_quantize_fp8_hadamard",
     "attn_fwd_fp8", "attn_fwd_fp8_fmt", "attn_fwd_fp8_blocks", "attn_fp8_qk_block_rows",
@@ -156,6 +158,10 @@ def load_library(path: str | None = None):
         lib.attn_diff_bwd_bf16_varlen.argtypes = ([vp] * 13 + [ctypes.c_size_t, vp] + [i] * 6
                                                   + [f, i, i, vp])
         lib.attn_diff_bwd_bf16_varlen.restype = i
+        lib.attn_diff_decode_workspace_bytes.argtypes = [i, i, i, i]
+        lib.attn_diff_decode_workspace_bytes.restype = ctypes.c_size_t
+        lib.attn_diff_decode_bf16_paged.argtypes = [vp] * 8 + [i] * 8 + [f, i, vp, ctypes.c_size_t, vp]
+        lib.attn_diff_decode_bf16_paged.restype = i
         lib.attn_quantize_fp8_blockwise.argtypes = [vp, vp, vp, i, i, i, i, i, vp]
         lib.attn_quantize_fp8_blockwise.restype = i
         lib.attn_quantize_fp8_hadamard.argtypes = [vp, vp, vp, i, i, i, i, i, vp]
@@ -445,7 +451,8 @@ def _native():
                     "attn_paged_plan", "attn_cache_append_bf16", "attn_cache_append_fp8",
                     "attn_decode_fp8_paged", "attn_decode_fp8_workspace_bytes", "attn_rope_bf16",
                     "attn_diff_fwd_bf16", "attn_diff_fwd_bf16_varlen", "attn_diff_bwd_bf16",
-                    "attn_diff_bwd_bf16_varlen", "attn_diff_bwd_workspace_bytes")))
+                    "attn_diff_bwd_bf16_varlen", "attn_diff_bwd_workspace_bytes",
+                    "attn_diff_decode_bf16_paged", "attn_diff_decode_workspace_bytes")))
                 _binding = binding
     return _binding
 
@@ -594,6 +601,27 @@ def attn_diff_bwd_bf16_varlen(q, k, v, lam, o, o2, dout, lse, cu_seqlens, max_se
                            _stream_on(stream, q))
     if type(r) is int:
         raise AttnError(r, "attn_diff_bwd_bf16_varlen")
+    return r
+
+
+def attn_diff_decode_workspace_bytes(H: int, Hkv: int, nq: int, d: int) -> int:
+    """Workspace bytes attn_diff_decode_bf16_paged needs on the current device."""
+    return int(load_library().attn_diff_decode_workspace_bytes(int(H), int(Hkv), int(nq), int(d)))
+
+
+def attn_diff_decode_bf16_paged(q, k_cache, v_cache, lam, page_table, seq_lens,
+                                scale: float | None = None, window: int = 0, workspace=None, o=None,
+                                lse=None, stream=None):
+    """One decoding step of differential attention.  q: bf16 [B, 2H, nq, d] (the nq newest tokens,
+    nq <= 8); k_cache, v_cache: bf16 [num_pages, 2Hkv, page_size, d], as attn_cache_append_bf16
+    fills them from k [T, 2Hkv, d] and v.view(T, 2 * Hkv, d); lam: float32 [H]; page_table int32
+    [B, max_pages], seq_lens int32 [B] (the new tokens included); window > 0: a query sees the
+    last window + 1 keys.  Returns O [B, H, nq, 2d] and the natural-log LSE [B, 2H, nq].  A
+    workspace of attn_diff_decode_workspace_bytes(...) is allocated when none is given."""
+    r = _native().diff_decode(q, k_cache, v_cache, lam, page_table, seq_lens, scale, window, workspace,
+                              o, lse, _stream_on(stream, q))
+    if type(r) is int:
+        raise AttnError(r, "attn_diff_decode_bf16_paged")
     return r
 
 

@@ -43,6 +43,7 @@ UNITS = [
     ("paged", "paged.cu", []),
     ("attn_bwd", "attn_bwd.cu", []),
     ("diff_bwd", "diff_bwd.cu", []),
+    ("diff_decode", "diff_decode.cu", []),
     ("diff_fwd", "diff_fwd.cu", []),
     ("rope", "rope.cu", []),
     ("api_diff", "api_diff.cu", []),

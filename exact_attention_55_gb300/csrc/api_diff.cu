@@ -267,3 +267,109 @@ extern "C" attn_status_t attn_diff_bwd_bf16_varlen(const void* q, const void* k,
                     {1, H, Hkv, max_seqlen, d, cu_seqlens, num_seqs, total_tokens, scale, causal, window}, stream,
                     kWaitTimeoutNs, 0);
 }
+
+// ------------------------------------------------------------------ decoding over a paged cache
+namespace {
+
+// Tables of at most this many keys: a pair's tiles stay with one CTA and nothing is joined.
+constexpr int kDiffDecodeWholeKeys = 384;
+constexpr int kDiffDecodeMaxBatch = (1 << 19) - 1;   // decode_fp8.cuh packs a count of sequences into 19 bits
+
+struct DiffDecodePlan {
+    int cta_rows, ranges, row_groups;
+};
+
+DiffDecodePlan diff_decode_plan(int rows, int d, int sm_count)
+{
+    DiffDecodePlan plan;
+    plan.cta_rows = diff_decode_rows(rows, d);
+    plan.row_groups = (rows + plan.cta_rows - 1) / plan.cta_rows;
+    const int ctas = diff_decode_ctas(d) * sm_count;
+    plan.ranges = ctas / plan.row_groups > 1 ? ctas / plan.row_groups : 1;
+    return plan;
+}
+
+size_t diff_decode_ws_bytes(const DiffDecodePlan& plan, int d)
+{
+    // per CTA: what the joining kernel has to do (16 bytes), and two parts of both maps
+    return (size_t)plan.ranges * plan.row_groups * (4 + 2 * (2 * plan.cta_rows) * (2 * d + 2)) * sizeof(float);
+}
+
+attn_status_t diff_decode(const void* q, const void* k_cache, const void* v_cache, const float* lam,
+                          const int* page_table, const int* seq_lens, void* o, float* lse, int B, int H, int Hkv, int nq,
+                          int d, int page_size, int num_pages, int max_pages, float scale, int window, void* workspace,
+                          size_t workspace_bytes, void* stream, unsigned long long timeout_ns, int withhold)
+{
+    if (!q || !k_cache || !v_cache || !lam || !page_table || !seq_lens || !o || !lse) return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || nq < 1 || num_pages < 1 || max_pages < 1) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = diff_sizes(H, Hkv, d, scale);
+    if (st != ATTN_OK) return st;
+    if (nq > 8 || page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0)
+        return ATTN_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page_size > 0x7fffffffLL || (long long)num_pages * Hkv > 0x7fffffffLL / 2 || H > 65535 ||
+        (long long)B * H > 0x7fffffffLL / 2 / nq || B > kDiffDecodeMaxBatch)
+        return ATTN_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lam, 4) ||
+        !aligned(lse, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 16))
+        return ATTN_ERR_MISALIGNED;
+    DeviceInfo* dev = nullptr;
+    st = device_info(&dev);
+    if (st != ATTN_OK) return st;
+    const int rows = H / Hkv * nq;
+    const DiffDecodePlan plan = diff_decode_plan(rows, d, dev->sm_count);
+    if (diff_decode_ws_bytes(plan, d) > (workspace ? workspace_bytes : 0)) return ATTN_ERR_INVALID_ARG;
+    // the caches as (d, page_size, pages * 2 Hkv), boxes of one page or 64 rows of a larger one
+    alignas(64) CUtensorMap mk, mv;
+    const int box = page_size < 64 ? page_size : 64;
+    const long long heads = 2LL * num_pages * Hkv;
+    if (!encode_rows(&mk, k_cache, d, page_size, d, heads, (long long)page_size * d, box) ||
+        !encode_rows(&mv, v_cache, d, page_size, d, heads, (long long)page_size * d, box))
+        return ATTN_ERR_CUDA;
+    DiffDecodeParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.w.q = q;
+    p.w.page_table = page_table;
+    p.w.seq_lens = seq_lens;
+    p.w.o = o;
+    p.w.lse = lse;
+    p.w.B = B;
+    p.w.Hkv = Hkv;
+    p.w.nq = nq;
+    p.w.rows = rows;
+    while ((1 << p.w.log2_ps) < page_size) ++p.w.log2_ps;
+    p.w.num_pages = num_pages;
+    p.w.max_pages = max_pages;
+    p.w.window = window > 0 && window < max_pages * page_size ? window : 0;   // a wider one hides nothing
+    p.w.c_log2 = (float)((double)scale * 1.4426950408889634);
+    p.w.ws = static_cast<float*>(workspace);
+    p.w.whole = max_pages * page_size <= kDiffDecodeWholeKeys ? 1 : 0;
+    p.w.ranges = plan.ranges;
+    p.w.row_groups = plan.row_groups;
+    p.w.status = dev->status;
+    p.w.timeout_ns = timeout_ns;
+    p.w.withhold = (unsigned)withhold;
+    p.lam = lam;
+    p.H = H;
+    return launch_diff_decode(mk, mv, p, d, plan.cta_rows, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" size_t attn_diff_decode_workspace_bytes(int H, int Hkv, int nq, int d)
+{
+    if (H < 1 || Hkv < 1 || nq < 1 || nq > 8 || H % Hkv != 0 || H > 65535 || (d != 64 && d != 128)) return 0;
+    DeviceInfo* dev = nullptr;
+    if (device_info(&dev) != ATTN_OK) return 0;
+    return diff_decode_ws_bytes(diff_decode_plan(H / Hkv * nq, d, dev->sm_count), d);
+}
+
+extern "C" attn_status_t attn_diff_decode_bf16_paged(const void* q, const void* k_cache, const void* v_cache,
+                                                     const float* lam, const int* page_table, const int* seq_lens,
+                                                     void* o, float* lse, int B, int H, int Hkv, int nq, int d,
+                                                     int page_size, int num_pages, int max_pages, float scale,
+                                                     int window, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return diff_decode(q, k_cache, v_cache, lam, page_table, seq_lens, o, lse, B, H, Hkv, nq, d, page_size, num_pages,
+                       max_pages, scale, window, workspace, workspace_bytes, stream, kWaitTimeoutNs, 0);
+}

@@ -44,6 +44,8 @@ decltype(&attn_diff_fwd_bf16_varlen) f_diff_fwd_varlen;
 decltype(&attn_diff_bwd_bf16) f_diff_bwd;
 decltype(&attn_diff_bwd_bf16_varlen) f_diff_bwd_varlen;
 decltype(&attn_diff_bwd_workspace_bytes) f_diff_bwd_ws;
+decltype(&attn_diff_decode_bf16_paged) f_diff_decode;
+decltype(&attn_diff_decode_workspace_bytes) f_diff_decode_ws;
 
 const Tensor& tensor(PyObject* o, const char* name)
 {
@@ -616,10 +618,47 @@ PyObject* diff_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// q, k_cache, v_cache, lam, page_table, seq_lens, scale or None, window, workspace, o, lse, stream
+PyObject* diff_decode(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 12, [&]() -> PyObject* {
+        const Tensor& q = cuda_tensor(a[0], "q");
+        const at::Device dev = q.device();
+        if (q.scalar_type() != at::kBFloat16) type_error("q must be bf16");
+        if (q.dim() != 4 || !q.is_contiguous()) value_error("q must be a contiguous [B, 2H, nq, d] tensor");
+        const int64_t B = q.size(0), H = q.size(1) / 2, nq = q.size(2), d = q.size(3);
+        const Tensor& kc = tensor(a[1], "k_cache");
+        const Tensor& vc = tensor(a[2], "v_cache");
+        check_cache(kc, dev, false, "k_cache");
+        check_cache(vc, dev, false, "v_cache");
+        if (!vc.sizes().equals(kc.sizes()) || kc.size(3) != d || kc.size(1) % 2 != 0 || q.size(1) % 2 != 0)
+            value_error("q must be [B, 2H, nq, d] and the caches [num_pages, 2Hkv, page_size, d]");
+        exact(a[3], {H}, at::kFloat, dev, "lam");
+        const Tensor& table = tensor(a[4], "page_table");
+        if (table.dim() != 2) type_error("page_table must be an int32 [B, max_pages] tensor");
+        exact(a[4], {B, table.size(1)}, at::kInt, dev, "page_table");
+        exact(a[5], {B}, at::kInt, dev, "seq_lens");
+        const float scale = scale_arg(a[6], d);
+        const int window = int_arg(a[7], "window");
+        const int h = size_arg(H, "H"), hkv = size_arg(kc.size(1) / 2, "Hkv"), nqi = size_arg(nq, "nq"), di = size_arg(d, "d");
+        const On on(a[11], dev);
+        const Workspace ws(a[8], a[8] == Py_None ? f_diff_decode_ws(h, hkv, nqi, di) : 0, dev);
+        const Tensor o = on.output(a[9], {B, H, nq, 2 * d}, at::kBFloat16, dev, "o");
+        const Tensor lse = on.output(a[10], {B, 2 * H, nq}, at::kFloat, dev, "lse");
+        const attn_status_t st = f_diff_decode(
+            q.data_ptr(), kc.data_ptr(), vc.data_ptr(), static_cast<float*>(ptr(a[3])), static_cast<int*>(ptr(a[4])),
+            static_cast<int*>(ptr(a[5])), o.data_ptr(), floats(lse), size_arg(B, "B"), h, hkv, nqi, di,
+            size_arg(kc.size(2), "page_size"), size_arg(kc.size(0), "num_pages"), size_arg(table.size(1), "max_pages"),
+            scale, window, ws.ptr, ws.bytes, on.handle);
+        if (st != ATTN_OK) return status(st);
+        return tuple_of({o, lse});
+    });
+}
+
 // The addresses of the C functions, in the order below.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    constexpr int kCount = 11;
+    constexpr int kCount = 13;
     return guarded(n, kCount, [&]() -> PyObject* {
         void* f[kCount];
         for (int i = 0; i < kCount; ++i) {
@@ -637,6 +676,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
         f_diff_bwd = reinterpret_cast<decltype(f_diff_bwd)>(f[8]);
         f_diff_bwd_varlen = reinterpret_cast<decltype(f_diff_bwd_varlen)>(f[9]);
         f_diff_bwd_ws = reinterpret_cast<decltype(f_diff_bwd_ws)>(f[10]);
+        f_diff_decode = reinterpret_cast<decltype(f_diff_decode)>(f[11]);
+        f_diff_decode_ws = reinterpret_cast<decltype(f_diff_decode_ws)>(f[12]);
         Py_RETURN_NONE;
     });
 }
@@ -651,7 +692,7 @@ PyMethodDef methods[] = {method<bind>("bind"),           method<plan>("plan"),
                          method<append_bf16>("append_bf16"), method<append_fp8>("append_fp8"),
                          method<decode>("decode"),       method<rope>("rope"),
                          method<diff_fwd>("diff_fwd"),   method<diff_bwd>("diff_bwd"),
-                         {nullptr, nullptr, 0, nullptr}};
+                         method<diff_decode>("diff_decode"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gb300attn_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_params.h"
+#include "paged_params.h"
 
 namespace gb300 {
 
@@ -73,10 +74,25 @@ struct DiffBwdMaps {
     CUtensorMap q64, k64, v64, dout64;   // 64-row boxes
 };
 
+// One decoding step of differential attention over a paged bf16 cache.  w holds what the cut of the work
+// needs (decode_fp8.cuh), with w.Hkv key pairs and w.rows = H / Hkv * nq query rows of each map; its
+// scales and 8-bit caches are not used.
+struct DiffDecodeParams {
+    DecodeFp8Params w;      // w.q: bf16 [B, 2H, nq, d]; w.o: [B, H, nq, 2d]; w.lse: [B, 2H, nq]
+    const float* lam;       // fp32 [H]
+    int H;
+};
+
+// Rows of each map that a CTA takes, and CTAs of an SM.
+constexpr int diff_decode_rows(int rows, int d) { return rows <= 4 ? 4 : rows <= 8 || d == 128 ? 8 : 16; }
+constexpr int diff_decode_ctas(int d) { return d == 64 ? 2 : 1; }
+
 cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_diff_fwd(const DiffFwdMaps& m, const DiffFwdParams& p, int d, int sm_count,
                             cudaStream_t stream);
 cudaError_t launch_diff_bwd(const DiffBwdMaps& m, const DiffBwdParams& p, int d, int sm_count,
                             cudaStream_t stream);
+cudaError_t launch_diff_decode(const CUtensorMap& mk, const CUtensorMap& mv, const DiffDecodeParams& p, int d,
+                               int cta_rows, cudaStream_t stream);
 
 }  // namespace gb300

@@ -578,6 +578,38 @@ attn_status_t attn_diff_bwd_bf16_varlen(const void* q, const void* k, const void
                                         int max_seqlen, int total_tokens, int H, int Hkv, int d,
                                         float scale, int causal, int window, void* stream);
 
+/*
+ * attn_diff_decode_bf16_paged -- one decoding step of differential attention over a paged KV cache.
+ *
+ * [JJ] §3 总结; [WGC] 局限性与后续方向 item 2, as attn_decode_bf16_paged, with attn_diff_fwd_bf16's
+ * two maps.  The caches are what attn_cache_append_bf16 writes with 2 Hkv heads from k [T, 2Hkv, d]
+ * and v [T, Hkv, 2d] seen as [T, 2Hkv, d]: K heads 2g, 2g + 1 are key pair g, V heads 2g, 2g + 1 the
+ * halves of value head g.  For sequence b with seq_lens[b] = L, query i is the token at position
+ * p = L - nq + i and attends to keys 0 .. p, or max(0, p - window) .. p when window > 0.
+ *   q          : const bf16 [B, 2H, nq, d]; 1 <= nq <= 8;  lam : const float [H] on the device
+ *   k_cache, v_cache : const bf16 [num_pages, 2Hkv, page_size, d]; H a multiple of Hkv
+ *   page_table, seq_lens, max_pages, num_pages : as attn_decode_bf16_paged
+ *   o, lse     : bf16 [B, H, nq, 2d], float [B, 2H, nq], written; a query that sees no key gets
+ *                O = 0, LSE = -inf
+ *   d in {64, 128}; page_size a power of two, 16 .. 65536; B < 2^19 (else ATTN_ERR_UNSUPPORTED)
+ *   workspace  : device memory of attn_diff_decode_workspace_bytes(...) bytes, 16-byte aligned;
+ *                its contents before and after do not matter.  Calls that may overlap need one
+ *                each
+ * What the cache holds at keys a query does not see (rows behind the sequence, pages behind it or
+ * before its window) never reaches that query's outputs, NaN included; an infinity in V counts as
+ * NaN where only some of the queries that share a tile see its key.  Scores, sums and O are fp32;
+ * the weights are rounded to bf16.  One pass over the cache serves H / Hkv * nq <= 16 rows of a
+ * map (8 at d = 128); it is HBM-bound.  A table of another width may change O and LSE by their
+ * roundings.
+ */
+size_t attn_diff_decode_workspace_bytes(int H, int Hkv, int nq, int d);
+attn_status_t attn_diff_decode_bf16_paged(const void* q, const void* k_cache, const void* v_cache,
+                                          const float* lam, const int* page_table,
+                                          const int* seq_lens, void* o, float* lse, int B, int H,
+                                          int Hkv, int nq, int d, int page_size, int num_pages,
+                                          int max_pages, float scale, int window, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
 /* Static English text for a status code (never NULL). */
 const char* attn_status_string(attn_status_t status);
 
