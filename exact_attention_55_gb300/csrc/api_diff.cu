@@ -133,8 +133,10 @@ attn_status_t diff_fwd(const void* q, const void* k, const void* v, const float*
                                                                                                        : ATTN_ERR_CUDA;
 }
 
-// The workspace: two counters in 16 bytes, then D_1 and D_2 of every row, laid out as the LSE.
-constexpr size_t kDiffBwdHead = 16;
+// The workspace: three counters in 16 bytes, the table of packed sequences, then D_1 and D_2 of every row,
+// laid out as the LSE.
+constexpr size_t kDiffBwdHead = 2048;
+static_assert(16 + sizeof(SortTab) <= kDiffBwdHead, "workspace");
 
 attn_status_t diff_bwd(const void* q, const void* k, const void* v, const float* lam, const void* o, const void* o2,
                        const void* dout, const float* lse, void* dq, void* dk, void* dv, float* dlam, void* workspace,
@@ -159,8 +161,7 @@ attn_status_t diff_bwd(const void* q, const void* k, const void* v, const float*
     if (!diff_map(&m.q, q, s.d, 2 * s.H, s.B, s.N, s.T, 128) || !diff_map(&m.q64, q, s.d, 2 * s.H, s.B, s.N, s.T, 64) ||
         !diff_map(&m.dout, dout, 2 * s.d, s.H, s.B, s.N, s.T, 128) ||
         !diff_map(&m.dout64, dout, 2 * s.d, s.H, s.B, s.N, s.T, 64) ||
-        !diff_map(&m.k, k, s.d, 2 * s.Hkv, s.B, s.N, s.T, 128) || !diff_map(&m.v, v, 2 * s.d, s.Hkv, s.B, s.N, s.T, 128) ||
-        !diff_map(&m.k64, k, s.d, 2 * s.Hkv, s.B, s.N, s.T, 64) || !diff_map(&m.v64, v, 2 * s.d, s.Hkv, s.B, s.N, s.T, 64))
+        !diff_map(&m.k, k, s.d, 2 * s.Hkv, s.B, s.N, s.T, 128) || !diff_map(&m.v, v, 2 * s.d, s.Hkv, s.B, s.N, s.T, 128))
         return ATTN_ERR_CUDA;
     DiffBwdParams p;
     std::memset(&p, 0, sizeof(p));
@@ -170,6 +171,7 @@ attn_status_t diff_bwd(const void* q, const void* k, const void* v, const float*
     p.lse = lse;
     p.lam = lam;
     p.next = static_cast<int*>(workspace);
+    if (packed && seqs <= kSortMaxSeqs) p.tab = reinterpret_cast<SortTab*>(static_cast<uint8_t*>(workspace) + 16);
     p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kDiffBwdHead);
     p.dlam = dlam;
     p.dq = dq;

@@ -8,22 +8,43 @@
 //     d lam = - sum over the head's rows of D_2.
 // Heads that share a key pair and value head add up in its dK and dV.
 //
-// Three launches, no floating-point atomics:
-//   diff_dot_kernel            D_1 and D_2 of every row, one warp a row;
-//   diff_bwd_kernel<D, true>   (dQ pass) a unit is 128 query rows of one map: in steps of 128 keys
-//                              (64 at d = 128), S = Q K_j^T and dP = dO V_j^T into TMEM, the compute warps turn
-//                              them into dS (bf16, over S), then dQ += dS K_j;
-//   diff_bwd_kernel<D, false>  (dK/dV pass) a unit is 128 keys of a key pair, taken as two items, one
-//                              a map: in steps of 64 queries over every head that reads it, the
-//                              transposed products, then dV += P^T dO_i and dK += dS^T Q_i.  dV
-//                              stays in TMEM from the first item to the second.
-// dP is computed for each map: 28 d products per pair of tokens where 20 d would do if both maps'
-// scores, dP and accumulators fitted TMEM at once (640 and 704 columns of 512 in the dK/dV pass).
-// The structure of each pass, its roles and its waits are those of attn_bwd.cu, with two
-// differences.  Units are handed out by a counter, the costliest first, because shared heads
-// leave few of them (128 key tiles for 152 SMs in an 8192-token step with two key pairs).
-// And what lies behind a packed sequence never enters a product: masked entries are selected
-// away before dP can make them NaN, and the rows of the operands become 0.
+// Four launches, no floating-point atomics:
+//   diff_dot_kernel              D_1 and D_2 of every row, one warp a row;
+//   diff_bwd_kernel<D, kPassDK>  a unit is 128 keys of one map: in steps of 128 queries, over every
+//                                head that reads them, S^T = K Q_i^T and dP^T = V dO_i^T into TMEM,
+//                                the compute warps turn them into dS^T (bf16, over S^T), then
+//                                dK += dS^T Q_i;
+//   diff_bwd_kernel<D, kPassDV>  a unit is 128 keys of a pair: both maps' S^T, of which the compute
+//                                warps make (P_1 - lam P_2)^T, rounded once, then dV += it dO_i;
+//   diff_bwd_kernel<D, kPassDQ>  a unit is 128 query rows of one map: in steps of 128 keys, S = Q K_j^T
+//                                and dP = dO V_j^T, then dQ += dS K_j.
+// (The dV pass takes 64 queries a step at d = 128.)
+// 40 d products per pair of tokens where 20 d would do: dP is computed for each map and again for dQ,
+// the scores three times.  Both maps' scores, dP and accumulators together want 640 columns of
+// TMEM (d = 64; it has 512), and more shared memory than there is beside a ring.
+//
+// A step has two products of its own, S (Q K^T of the map; dV: of map 1) and X (dP; dV: map 2's
+// scores), and one accumulation that waits for the compute warps.  S has two TMEM buffers and X one, which
+// the compute warps release as soon as they have loaded it, so the MMA warp issues X(j), the
+// accumulation of step j - 1, then S(j + 1), and the tensor pipe works on X(j) and S(j + 1) while both
+// compute warpgroups (half of the columns each) turn steps j - 1 and j.
+//
+// What this was measured against, on 4 x 8 heads x 4096 tokens of d = 64, causal, all passes:
+// steps of 64 columns with three TMEM buffers and a warpgroup each 1140 us, with quick waits 894.
+// The tensor pipe was busy for a quarter of it: its queue holds about 8 MMAs, and a wait, even for what
+// has long happened, took the issuing warp 150-200 cycles (one lane or all polling in a loop; 60-120
+// with one attempt by all lanes first), so few large MMAs and few waits a column are what counts.
+// A 128 x 64 x 16 product of two shared-memory operands takes 48 cycles instead of 32: it reads
+// 6 KB of the 128 bytes a cycle there are.
+//
+// The three passes do not depend on one another, and each is launched as a dependent that starts
+// when all CTAs of the one before have started: its CTAs take the SMs that run out of units.
+// Each waits for the one before at its end, so that the last one's end is the end of all.
+// Units are handed out by a counter, the costliest first: shared heads leave few of them (128 key
+// tiles for 152 SMs in an 8192-token step with two key pairs).
+//
+// What lies behind a packed sequence never enters a product: masked entries are selected away
+// before dP can make them NaN, and the rows of the operands become 0.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -36,80 +57,89 @@
 
 namespace gb300 {
 
-template <int D, bool kDQ>
+enum : int { kPassDK = 0, kPassDV = 1, kPassDQ = 2 };   // in the order of their launches
+
+template <int D, int kPass>
 struct DiffBwdCfg {
+    static constexpr bool DQ = kPass == kPassDQ, DV = kPass == kPassDV;
     static constexpr int BT = 128;                 // rows of a unit's tile
-    // Columns of a step.  dQ pass at d = 128: a step of 128 keys would want K_{j-1}, K_j and V_j (128 KB)
-    // beside Q and dO (96 KB), which leaves no room to load ahead.
-    static constexpr int BC = kDQ && D == 64 ? 128 : 64;
+    static constexpr int BC = DV && D == 128 ? 64 : 128, HC = BC / 2;   // columns of a step, of a warpgroup
     static constexpr int NCB = D / 64;             // 64-column blocks of a row of d
     static constexpr int FIX_CB = BT * 128;        // bytes of one, fixed tiles
     static constexpr int RING_CB = BC * 128;       // and ring tiles
-    static constexpr int FIX_BYTES = 3 * NCB * FIX_CB;      // d columns (Q or K), then 2d (dO or V)
-    static constexpr int SLOT = NCB * RING_CB;              // d columns of a step
-    static constexpr int STEP_SLOTS = 3;                    // K and V's halves, or Q and dO's
-    static constexpr int SMEM_CAP = 227 * 1024;
-    // after the barriers, dK/dV: the warps' LSE and D, float [8][2][32]; then the schedule table
-    static constexpr int MAX_SLOTS = 12;
-    static constexpr int COL_OFF = 512;
-    static constexpr int TAB_OFF = kDQ ? COL_OFF : COL_OFF + 2048;
-    static constexpr int BAR_BYTES = (TAB_OFF + (int)sizeof(SortTab) + 15) / 16 * 16;
-    static constexpr int NSLOT_FIT = (SMEM_CAP - BAR_BYTES - 1024 - FIX_BYTES) / SLOT;
-    static constexpr int NSLOT = NSLOT_FIT < MAX_SLOTS ? NSLOT_FIT : MAX_SLOTS;
-    static constexpr int SMEM_BYTES = 1024 + FIX_BYTES + NSLOT * SLOT + BAR_BYTES;
-    // TMEM.  dQ pass: S of step h at 128 (h & 1), dP at 256, dQ at 384.  dK/dV pass: step buffers of
-    // S^T (64 columns) and dP^T (64), two at d = 64 and one at d = 128, dV at 256, dK behind it
-    // or (d = 128) before it.
-    static constexpr int NB = kDQ || D == 64 ? 2 : 1;
-    static constexpr int DP_OFF = kDQ ? 256 : 64;
-    static constexpr int DQ_COL = 384, DV_COL = 256, DK_COL = D == 64 ? 384 : 128;
-    static constexpr int COMPUTE_WARPS = 8, NUM_THREADS = 384, PRODUCER_WARP = 8, MMA_WARP = 9, SUM_WARP = 10;
+    static constexpr int FIX_PARTS = DV ? 2 : 3;   // of d columns: K_1 and K_2; Q or K, then dO or V
+    static constexpr int FIX_BYTES = FIX_PARTS * NCB * FIX_CB;
+    // Three rings.  S: Q or K of the map (dV: Q_1), which the accumulation reads too.  X: dO or V in parts of
+    // d columns (dV: Q_2).  dV alone: A, dO for the accumulation.
+    static constexpr int S_BYTES = NCB * RING_CB, X_BYTES = NCB * RING_CB, A_BYTES = DV ? 2 * NCB * RING_CB : 0;
+    static constexpr int X_PARTS = DV ? 1 : 2;
+    static constexpr int NS = D == 64 ? 3 : DV ? 3 : 2, NX = D == 64 ? (DV ? 2 : 6) : 2, NACC = DV ? 2 : 1;   // slots
+    // TMEM: S of step h at (h & 1) BC (then dS or the weights, packed), X behind both, the accumulator
+    static constexpr int ACC = DV ? 2 * D : D;
+    static constexpr int X_COL = 2 * BC, ACC_COL = 512 - (ACC > 128 ? 256 : 128);
+    static constexpr int COMPUTE_WARPS = 8, PRODUCER_WARP = 8, MMA_WARP = 9, SUM_WARP = 10, NUM_THREADS = 384;
     static constexpr int REG_COMPUTE = 208, REG_CONTROL = 88;
     static constexpr int REG_POOL = 256 * REG_COMPUTE + 128 * REG_CONTROL;
+    // Shared memory: fixed tiles, rings, barriers, two steps' column values (LSE, D, factor).  At d = 128 it
+    // is full to 600 bytes, so there is none to spend on alignment: the tiles start where it starts.
+    static constexpr int RING_BYTES = NS * S_BYTES + NX * X_BYTES + (DV ? NACC * A_BYTES : 0);
+    static constexpr int COL_OFF = 384, COL_FLOATS = 2 * BC + 4;
+    static constexpr int SMEM_BYTES = FIX_BYTES + RING_BYTES + COL_OFF + (DQ ? 0 : 2 * COL_FLOATS * 4);
+    static constexpr int COLUMN_WARP = 11;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
     static_assert(D == 64 || D == 128, "head dim");
-    // dQ pass: V_j's second half waits for a slot while K_{j-1}, five before it, is still held
-    static_assert(NSLOT >= (kDQ ? 6 : 3), "ring too small");
-    static_assert(SMEM_BYTES <= SMEM_CAP, "shared memory");
+    static_assert(X_COL + BC <= ACC_COL && ACC_COL + ACC <= 512, "TMEM");
 };
-
-struct alignas(16) DiffBwdBars {
-    uint64_t fix_full, fix_empty;
-    uint64_t ring_full[12], ring_empty[12];
-    uint64_t s_full[2], p_full[2];
-    uint64_t dp_free;
-    uint64_t acc_done, acc_empty;
-    uint64_t unit_full[2], unit_empty[2];
-    uint64_t drain;
-    int unit[2];                                   // the units handed out, -1 at the end
-    uint32_t tmem_base;
-    int abort_flag;
-};
-static_assert(sizeof(DiffBwdBars) <= 512, "barrier block");
 
 // One unit: tile t (128 rows) of a head, or of a key pair, of one sequence.
 struct DiffBwdUnit {
     int t, N, y0;      // tile, rows of the sequence, its first token (packed)
-    int b, z;          // batch entry (packed: 0); dQ pass: 2 h + map, dK/dV pass: key pair
+    int b, z;          // batch entry (packed: 0); 2 h + map, 2 g + map, or (dV) the key pair g
+    int lo, n;         // its steps: from column block lo on, n of them
+    int more;          // 0: there is none
 };
 
-__device__ __forceinline__ int diff_bwd_units(const DiffBwdParams& p, int heads, const SortTab* tab)
+struct alignas(16) DiffBwdBars {
+    uint64_t fix_full, fix_empty;
+    uint64_t s_in_full[3], s_in_empty[3], x_in_full[6], x_in_empty[6], a_in_full[2], a_in_empty[2];   // rings
+    uint64_t s_full, p_full, x_free;               // one phase a step
+    uint64_t acc_done, acc_empty;
+    uint64_t unit_full[2], unit_empty[2];
+    uint64_t col_full[2], col_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(DiffBwdBars) + 2 * sizeof(DiffBwdUnit) <= 384, "barrier block");
+constexpr int kDiffBwdUnitOff = 320;               // the two units handed out
+static_assert(sizeof(DiffBwdBars) <= kDiffBwdUnitOff, "barrier block");
+
+// Units of a pass over `heads` heads (of q, of k, or key pairs).
+__device__ __forceinline__ int diff_bwd_units(const DiffBwdParams& p, int heads)
 {
-    return tab != nullptr ? tab->total : p.nt * p.B * heads;
+    if (p.tab == nullptr) return p.nt * p.B * heads;
+    return __ldcg(&p.tab->total) * heads;
 }
 
 // Unit u, costliest first under a causal mask: a query tile t meets t + 1 key tiles, a key tile nt - t
-// query tiles.  Batched: rank by rank over all heads; packed, from the table: the longest sequence
-// first.  More sequences than the table holds: slots laid out for the longest one; false where
-// a sequence is shorter.
+// query tiles.  Batched: rank by rank over all heads; packed, from the table of sorted sequences that
+// the first kernel left: the longest sequence first.  More sequences than the table holds: slots laid out
+// for the longest one; false where a sequence is shorter.
 template <bool kDQ, bool kPacked>
-__device__ __forceinline__ bool diff_bwd_unit(const DiffBwdParams& p, int u, int heads, const SortTab* tab, DiffBwdUnit& w)
+__device__ __forceinline__ bool diff_bwd_unit(const DiffBwdParams& p, int u, int heads, DiffBwdUnit& w)
 {
     int rank, seq;
-    if (kPacked && tab != nullptr) {
-        int rem;
-        sorted_pair(tab, p.B, u, seq, rem);
-        rank = rem / heads;
-        w.z = rem - rank * heads;
+    if (kPacked && p.tab != nullptr) {
+        const int tile = u / heads;                // over all sequences, in the table's order
+        w.z = u - tile * heads;
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (__ldcg(p.tab->prefix + mid) <= tile) lo = mid;
+            else hi = mid - 1;
+        }
+        seq = __ldcg(p.tab->seq + lo);
+        rank = tile - __ldcg(p.tab->prefix + lo);
     } else {
         rank = u / (p.B * heads);
         const int rem = u - rank * (p.B * heads);
@@ -175,12 +205,28 @@ __device__ __forceinline__ size_t diff_bwd_row(const DiffBwdParams& p, const Dif
     return kPacked ? (size_t)(w.y0 + r) * heads + z : ((size_t)w.b * heads + z) * p.N + r;
 }
 
-// D_1 and D_2 in fp32, one warp a row; the units' counters start at 0.
+// A value that all lanes share, by a reduction, whose result the compiler knows to be uniform: what an
+// MMA's descriptors are computed from then stays in uniform registers.
+__device__ __forceinline__ int diff_uniform(int v) { return (int)__reduce_or_sync(0xffffffffu, (unsigned)v); }
+
+// What the kernel ahead wrote, and what may still be in a cache of an SM that ran before: from L2.
+__device__ __forceinline__ float diff_ld(const float* p) { return __ldcg(p); }
+
+// D_1 and D_2 in fp32, one warp a row; the units' counters start at 0, and the table of packed sequences
+// is sorted (tiles of 128 rows before each sequence).
 template <int D>
 __global__ void __launch_bounds__(256) diff_dot_kernel(const DiffBwdParams p)
 {
     constexpr int E = 2 * D / 32;
-    if (blockIdx.x == 0 && threadIdx.x < 2) p.next[threadIdx.x] = 0;
+    __shared__ SortTab tab;
+    if (blockIdx.x == 0) {
+        if (threadIdx.x < 3) p.next[threadIdx.x] = 0;
+        if (p.tab != nullptr) {
+            build_sort_tab<64>(p.cu_seqlens, p.B, p.T, 1, &tab);      // pairs of 64 rows: tiles
+            for (int i = threadIdx.x; i < (int)(sizeof(SortTab) / 4); i += 256)
+                reinterpret_cast<int*>(p.tab)[i] = reinterpret_cast<const int*>(&tab)[i];
+        }
+    }
     const bool packed = p.cu_seqlens != nullptr;
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const long long rows = packed ? (long long)p.T * p.H : (long long)p.B * p.H * p.N;
@@ -191,7 +237,7 @@ __global__ void __launch_bounds__(256) diff_dot_kernel(const DiffBwdParams p)
     if (packed) {
         const long long t = row / p.H;
         h = (int)(row - t * p.H);
-        if (t < __ldg(p.cu_seqlens) || t >= __ldg(p.cu_seqlens + p.B)) return;   // outside every sequence
+        if (t < __ldcg(p.cu_seqlens) || t >= __ldcg(p.cu_seqlens + p.B)) return;   // outside every sequence
         at = (size_t)(2 * h) * p.T + t;
         step = (size_t)p.T;
     } else {
@@ -229,7 +275,7 @@ __global__ void __launch_bounds__(256) diff_dot_kernel(const DiffBwdParams p)
         b += __shfl_xor_sync(0xffffffffu, b, s);
     }
     if (lane == 0) {
-        p.delta[at] = fmaf(__ldg(p.lam + h), b, a);
+        p.delta[at] = fmaf(__ldcg(p.lam + h), b, a);
         p.delta[at + step] = b;
     }
 }
@@ -245,8 +291,8 @@ __device__ __forceinline__ void diff_dlam(const DiffBwdParams& p, int lane)
             const float* d;
             long long n;
             if (p.cu_seqlens) {
-                const int t0 = min(max(__ldg(p.cu_seqlens), 0), p.T);
-                n = min(max(__ldg(p.cu_seqlens + p.B), t0), p.T) - t0;
+                const int t0 = min(max(__ldcg(p.cu_seqlens), 0), p.T);
+                n = min(max(__ldcg(p.cu_seqlens + p.B), t0), p.T) - t0;
                 d = p.delta + (size_t)(2 * h + 1) * p.T + t0;
             } else {
                 n = p.N;
@@ -255,7 +301,7 @@ __device__ __forceinline__ void diff_dlam(const DiffBwdParams& p, int lane)
             for (long long i = lane; i < n; i += 256) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    if (i + 32 * k < n) acc[k] += d[i + 32 * k];
+                    if (i + 32 * k < n) acc[k] += diff_ld(d + i + 32 * k);
             }
         }
         float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
@@ -265,38 +311,49 @@ __device__ __forceinline__ void diff_dlam(const DiffBwdParams& p, int lane)
     }
 }
 
-// One pass.  Maps: dQ pass fixed Q and dO, ring K and V; dK/dV pass fixed K and V, ring Q and dO.
-template <int D, bool kDQ, bool kPacked>
-__global__ void __launch_bounds__(DiffBwdCfg<D, kDQ>::NUM_THREADS, 1)
+// One pass.  Maps: dK pass fixed K and V, ring Q and dO; dV pass fixed K, ring Q and dO; dQ pass fixed Q
+// and dO, ring K and V.
+template <int D, int kPass, bool kPacked>
+__global__ void __launch_bounds__(DiffBwdCfg<D, kPass>::NUM_THREADS, 1)
     diff_bwd_kernel(const __grid_constant__ CUtensorMap tmFixA, const __grid_constant__ CUtensorMap tmFixB,
                     const __grid_constant__ CUtensorMap tmRingA, const __grid_constant__ CUtensorMap tmRingB,
                     const DiffBwdParams p)
 {
-    using C = DiffBwdCfg<D, kDQ>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    using C = DiffBwdCfg<D, kPass>;
+    constexpr bool kDQ = C::DQ, kDV = C::DV;
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* fix = smem;
-    uint8_t* ring = smem + C::FIX_BYTES;
-    auto* bars = reinterpret_cast<DiffBwdBars*>(ring + C::NSLOT * C::SLOT);
+    uint8_t* ring_s = smem + C::FIX_BYTES;
+    uint8_t* ring_x = ring_s + C::NS * C::S_BYTES;
+    uint8_t* ring_a = ring_x + C::NX * C::X_BYTES;         // dV only
+    uint8_t* tail = smem + C::FIX_BYTES + C::RING_BYTES;
+    DiffBwdBars* bars = reinterpret_cast<DiffBwdBars*>(tail);
+    DiffBwdUnit* handed = reinterpret_cast<DiffBwdUnit*>(tail + kDiffBwdUnitOff);
+    float* columns = reinterpret_cast<float*>(tail + C::COL_OFF);
     const volatile int* abort_flag = &bars->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int heads = kDQ ? 2 * p.H : p.Hkv, G = p.H / p.Hkv;
-    const int items = kDQ ? 1 : 2;
+    const int heads = kDQ ? 2 * p.H : kDV ? p.Hkv : 2 * p.Hkv, G = p.H / p.Hkv;
+    if ((smem_u32(smem) & 1023) != 0) {                    // no kernel of this file has static shared memory
+        if (threadIdx.x == 0) atomicExch(p.status, kStatusTimeout);
+        return;
+    }
 
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bars->fix_full), 1);
         mbar_init(smem_u32(&bars->fix_empty), 1);
-        for (int s = 0; s < C::NSLOT; ++s) {
-            mbar_init(smem_u32(&bars->ring_full[s]), 1);
-            mbar_init(smem_u32(&bars->ring_empty[s]), 1);
+        for (int s = 0; s < C::NS; ++s) mbar_init(smem_u32(&bars->s_in_full[s]), 1), mbar_init(smem_u32(&bars->s_in_empty[s]), 1);
+        for (int s = 0; s < C::NX; ++s) mbar_init(smem_u32(&bars->x_in_full[s]), 1), mbar_init(smem_u32(&bars->x_in_empty[s]), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&bars->a_in_full[s]), 1);
+            mbar_init(smem_u32(&bars->a_in_empty[s]), 1);
+            mbar_init(smem_u32(&bars->unit_full[s]), 1);
+            mbar_init(smem_u32(&bars->unit_empty[s]), C::COMPUTE_WARPS + (kDQ ? 1 : 2));
+            mbar_init(smem_u32(&bars->col_full[s]), 1);
+            mbar_init(smem_u32(&bars->col_empty[s]), C::COMPUTE_WARPS);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_u32(&bars->s_full[b]), 1);
-            mbar_init(smem_u32(&bars->p_full[b]), C::COMPUTE_WARPS);
-            mbar_init(smem_u32(&bars->unit_full[b]), 1);
-            mbar_init(smem_u32(&bars->unit_empty[b]), C::COMPUTE_WARPS + 1);
-        }
-        mbar_init(smem_u32(&bars->dp_free), C::COMPUTE_WARPS);
+        mbar_init(smem_u32(&bars->s_full), 1);
+        mbar_init(smem_u32(&bars->p_full), C::COMPUTE_WARPS);
+        mbar_init(smem_u32(&bars->x_free), C::COMPUTE_WARPS);
         mbar_init(smem_u32(&bars->acc_done), 1);
         mbar_init(smem_u32(&bars->acc_empty), C::COMPUTE_WARPS);
         mbar_init(smem_u32(&bars->drain), 1);
@@ -307,150 +364,169 @@ __global__ void __launch_bounds__(DiffBwdCfg<D, kDQ>::NUM_THREADS, 1)
         tmem_alloc(smem_u32(&bars->tmem_base), 512);
         tmem_relinquish();
     }
+    // The first pass waits for the dot products and the counters; the others' CTAs start when every CTA
+    // of the pass before has come this far, and find them written.
+    if constexpr (kPass == kPassDK) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = bars->tmem_base;
-    const SortTab* tab = nullptr;
-    if constexpr (kPacked) {
-        if (p.B <= kSortMaxSeqs) {
-            SortTab* t = reinterpret_cast<SortTab*>(reinterpret_cast<uint8_t*>(bars) + C::TAB_OFF);
-            build_sort_tab<64>(p.cu_seqlens, p.B, p.T, heads, t);   // pairs of 64 rows: tiles
-            tab = t;
-        }
-    }
-    const int total = diff_bwd_units(p, heads, tab);
     auto timed_out = [&]() {
         atomicExch(p.status, kStatusTimeout);
         *reinterpret_cast<volatile int*>(&bars->abort_flag) = 1;
     };
-    // A consumer warp's next unit (all lanes); -1 at the end or after an abort.
-    auto take_unit = [&](uint32_t& n, bool& ok) -> int {
+    // A warp's wait: all lanes try once, which is the usual case; else they poll until the limit.
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const uint32_t a = smem_u32(bar);
+        if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+        return __all_sync(0xffffffffu, mbar_wait(a, parity, abort_flag, p.timeout_ns));
+    };
+    // A consumer warp's next unit (all lanes); false at the end or after an abort.
+    auto take_unit = [&](uint32_t& n, bool& ok, DiffBwdUnit& w) -> bool {
         const uint32_t b = n & 1;
-        const bool r = mbar_wait(smem_u32(&bars->unit_full[b]), (n >> 1) & 1, abort_flag, p.timeout_ns);
-        if (!__all_sync(0xffffffffu, r)) {
+        if (!warp_wait(&bars->unit_full[b], (n >> 1) & 1)) {
             ok = false;
-            return -1;
+            return false;
         }
-        const int u = *reinterpret_cast<volatile int*>(&bars->unit[b]);
+        const volatile DiffBwdUnit* u = handed + b;
+        w.t = diff_uniform(u->t), w.N = diff_uniform(u->N), w.y0 = diff_uniform(u->y0), w.b = diff_uniform(u->b);
+        w.z = diff_uniform(u->z), w.lo = diff_uniform(u->lo), w.n = diff_uniform(u->n), w.more = diff_uniform(u->more);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->unit_empty[b]));
         ++n;
-        return u;
+        return w.more != 0;
     };
 
     if (warp == C::PRODUCER_WARP) {
         regs_decrease<C::REG_CONTROL>();
         if (lane == 0) {
             const uint64_t pol_fix = l2_policy_evict_first(), pol_ring = l2_policy_evict_last();
-            uint32_t rc = 0, fixed = 0, given = 0;
+            uint32_t ns = 0, nx = 0, na = 0, issued = 0, lost_s = 0, lost_x = 0, lost_a = 0, fixed = 0, given = 0;
+            const int total = diff_bwd_units(p, heads);
             int walk = (int)blockIdx.x;
             bool ok = true;
-            // the next ring slot gets d columns from `col` on of `row` of a map
-            auto load = [&](const CUtensorMap* map, int col, int row, int head) {
+            // the next slot of a ring: `blocks` blocks of 64 columns from `col` on of heads `head`, ...; a withheld
+            // one is neither armed nor loaded (test hook)
+            auto load = [&](uint8_t* base, uint64_t* full, uint64_t* empty, uint32_t slots, uint32_t& n, uint32_t& lost,
+                            const CUtensorMap* map, auto blocks_tag, int col, int row, int head) {
+                constexpr int blocks = decltype(blocks_tag)::value;
                 if (!ok) return;
-                const uint32_t slot = rc % C::NSLOT;
-                if (!mbar_wait(smem_u32(&bars->ring_empty[slot]), ((rc / C::NSLOT) & 1) ^ 1, abort_flag, p.timeout_ns)) {
+                const uint32_t slot = n % slots;
+                if (!mbar_wait(smem_u32(&empty[slot]), ((n / slots) & 1) ^ 1, abort_flag, p.timeout_ns)) {
                     ok = false;
                     return;
                 }
-                if (++rc == (uint32_t)p.withhold) return;      // test hook: never arrives
-                const uint32_t rb = smem_u32(&bars->ring_full[slot]);
-                mbar_arrive_expect_tx(rb, C::SLOT);
+                ++n;
+                if (++issued == (uint32_t)p.withhold) {
+                    lost = n;
+                    return;
+                }
+                const uint32_t fb = smem_u32(&full[slot]);
+                mbar_arrive_expect_tx(fb, blocks * C::RING_CB);
 #pragma unroll
-                for (int cb = 0; cb < C::NCB; ++cb)
-                    tma_load_3d(smem_u32(ring + slot * C::SLOT + cb * C::RING_CB), map, rb, col + cb * 64, row, head,
-                                pol_ring);
+                for (int i = 0; i < blocks; ++i)
+                    tma_load_3d(smem_u32(base + (slot * blocks + i) * C::RING_CB), map, fb, col + i * 64, row, head, pol_ring);
             };
+            using One = std::integral_constant<int, C::NCB>;
+            using Two = std::integral_constant<int, 2 * C::NCB>;
             while (ok) {
                 DiffBwdUnit w;
                 int u;
-                if (!kPacked || tab != nullptr) {
-                    u = atomicAdd(p.next + (kDQ ? 0 : 1), 1);
+                if (!kPacked || p.tab != nullptr) {
+                    u = atomicAdd(p.next + kPass, 1);
                 } else {                       // slots with gaps: walked without the counter
                     u = walk;
                     walk += gridDim.x;
                 }
-                const bool more = u < total;
-                if (more && !diff_bwd_unit<kDQ, kPacked>(p, u, heads, tab, w)) continue;
+                w.more = u < total ? 1 : 0;
+                if (w.more && !diff_bwd_unit<kDQ, kPacked>(p, u, heads, w)) continue;
+                int hi = 0;
+                w.lo = 0;
+                if (w.more) diff_bwd_steps<kDQ, C::BC>(p, w, w.lo, hi);
+                const int per = hi - w.lo, group = kDQ ? 1 : G;       // steps of a head, heads
+                w.n = group * per;
                 const uint32_t b = given & 1;
                 if (!mbar_wait(smem_u32(&bars->unit_empty[b]), ((given >> 1) & 1) ^ 1, abort_flag, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
-                *reinterpret_cast<volatile int*>(&bars->unit[b]) = more ? u : -1;
+                volatile DiffBwdUnit* v = handed + b;
+                v->t = w.t, v->N = w.N, v->y0 = w.y0, v->b = w.b, v->z = w.z, v->lo = w.lo, v->n = w.n, v->more = w.more;
                 mbar_arrive(smem_u32(&bars->unit_full[b]));
                 ++given;
-                if (!more) break;
-                int lo, hi;
-                diff_bwd_steps<kDQ, C::BC>(p, w, lo, hi);
-                for (int m = 0; m < items && ok; ++m) {
-                    if (!mbar_wait(smem_u32(&bars->fix_empty), (fixed & 1) ^ 1, abort_flag, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = smem_u32(&bars->fix_full);
-                    mbar_arrive_expect_tx(fb, C::FIX_BYTES);
-                    ++fixed;
-                    const int row = w.y0 + w.t * 128;
-                    const int za = kDQ ? w.b * 2 * p.H + w.z : w.b * 2 * p.Hkv + 2 * w.z + m;
-                    const int zb = kDQ ? w.b * p.H + (w.z >> 1) : w.b * p.Hkv + w.z;
+                if (!w.more) break;
+                if (!mbar_wait(smem_u32(&bars->fix_empty), (fixed & 1) ^ 1, abort_flag, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = smem_u32(&bars->fix_full);
+                mbar_arrive_expect_tx(fb, C::FIX_BYTES);
+                ++fixed;
+                // parts of d columns: Q, K or K_1; then dO, V, or K_2
+                const int row = w.y0 + w.t * 128;
+                const int za = w.b * heads * (kDV ? 2 : 1) + w.z * (kDV ? 2 : 1);
+                const int zb = kDV ? za + 1 : kDQ ? w.b * p.H + (w.z >> 1) : w.b * p.Hkv + (w.z >> 1);
 #pragma unroll
-                    for (int cb = 0; cb < 3 * C::NCB; ++cb) {
-                        const bool first = cb < C::NCB;
-                        tma_load_3d(smem_u32(fix + cb * C::FIX_CB), first ? &tmFixA : &tmFixB, fb,
-                                    (first ? cb : cb - C::NCB) * 64, row, first ? za : zb, pol_fix);
-                    }
+                for (int cb = 0; cb < C::FIX_PARTS * C::NCB; ++cb) {
+                    const bool first = cb < C::NCB;
+                    tma_load_3d(smem_u32(fix + cb * C::FIX_CB), first || kDV ? &tmFixA : &tmFixB, fb,
+                                (first ? cb : cb - C::NCB) * 64, row, first ? za : zb, pol_fix);
+                }
+                for (int i = 0; i < group; ++i) {
+                    int zs, zx;                // heads of S's operand, and of X's (dV: of dO)
                     if constexpr (kDQ) {
-                        const int g = (w.z >> 1) / G, zk = w.b * 2 * p.Hkv + 2 * g + (w.z & 1), zv = w.b * p.Hkv + g;
-                        for (int j = lo; j < hi && ok; ++j) {
-                            load(&tmRingA, 0, w.y0 + j * C::BC, zk);
-                            load(&tmRingB, 0, w.y0 + j * C::BC, zv);
-                            load(&tmRingB, D, w.y0 + j * C::BC, zv);
-                        }
+                        const int g = (w.z >> 1) / G;
+                        zs = w.b * 2 * p.Hkv + 2 * g + (w.z & 1);
+                        zx = w.b * p.Hkv + g;
                     } else {
-                        for (int i = 0; i < G; ++i) {
-                            const int h = w.z * G + i, zq = w.b * 2 * p.H + 2 * h + m, zo = w.b * p.H + h;
-                            for (int s = lo; s < hi && ok; ++s) {
-                                load(&tmRingA, 0, w.y0 + s * C::BC, zq);
-                                load(&tmRingB, 0, w.y0 + s * C::BC, zo);
-                                load(&tmRingB, D, w.y0 + s * C::BC, zo);
-                            }
+                        const int h = (kDV ? w.z : w.z >> 1) * G + i;
+                        zs = w.b * 2 * p.H + 2 * h + (kDV ? 0 : w.z & 1);
+                        zx = w.b * p.H + h;
+                    }
+                    for (int s = w.lo; s < hi && ok; ++s) {
+                        const int r = w.y0 + s * C::BC;
+                        load(ring_s, bars->s_in_full, bars->s_in_empty, C::NS, ns, lost_s, &tmRingA, One{}, 0, r, zs);
+                        if constexpr (kDV) {
+                            load(ring_x, bars->x_in_full, bars->x_in_empty, C::NX, nx, lost_x, &tmRingA, One{}, 0, r, zs + 1);
+                            load(ring_a, bars->a_in_full, bars->a_in_empty, C::NACC, na, lost_a, &tmRingB, Two{}, 0, r, zx);
+                        } else {
+                            load(ring_x, bars->x_in_full, bars->x_in_empty, C::NX, nx, lost_x, &tmRingB, One{}, 0, r, zx);
+                            load(ring_x, bars->x_in_full, bars->x_in_empty, C::NX, nx, lost_x, &tmRingB, One{}, D, r, zx);
                         }
                     }
                 }
             }
             if (!ok) timed_out();
             // every copy issued lands before shared memory is released
-            const uint32_t n = rc < C::NSLOT ? rc : C::NSLOT;
-            for (uint32_t k = rc - n; k < rc; ++k) {
-                if (k + 1 == (uint32_t)p.withhold) continue;
-                mbar_wait(smem_u32(&bars->ring_full[k % C::NSLOT]), (k / C::NSLOT) & 1, nullptr, kCleanupTimeoutNs);
-            }
+            auto landed = [&](uint64_t* full, uint32_t slots, uint32_t n, uint32_t lost) {
+                for (uint32_t k = n < slots ? 0 : n - slots; k < n; ++k)
+                    if (k + 1 != lost)
+                        mbar_wait(smem_u32(&full[k % slots]), (k / slots) & 1, nullptr, kCleanupTimeoutNs);
+            };
+            landed(bars->s_in_full, C::NS, ns, lost_s);
+            landed(bars->x_in_full, C::NX, nx, lost_x);
+            if constexpr (kDV) landed(bars->a_in_full, C::NACC, na, lost_a);
             if (fixed > 0) mbar_wait(smem_u32(&bars->fix_full), (fixed - 1) & 1, nullptr, kCleanupTimeoutNs);
         }
     } else if (warp == C::MMA_WARP) {
         regs_decrease<C::REG_CONTROL>();
-        constexpr uint32_t idesc_kk = idesc_f32acc(1, 0, 128, C::BC);  // both K-major
-        constexpr uint32_t idesc_acc = idesc_f32acc(1, 1, 128, D);     // B MN-major
+        constexpr uint32_t idesc_kk = idesc_f32acc(1, 0, 128, C::BC);      // both K-major
+        constexpr uint32_t idesc_acc = idesc_f32acc(1, 1, 128, C::ACC);    // B MN-major
         const uint64_t fix_k = sdesc_sw128(smem_u32(fix), 16, 1024);
-        const uint64_t ring_k = sdesc_sw128(smem_u32(ring), 16, 1024);
-        const uint64_t ring_mn = sdesc_sw128(smem_u32(ring), C::RING_CB, 1024);
-        uint32_t rc = 0, items_done = 0, hs = 0, units = 0;
+        const uint64_t s_k = sdesc_sw128(smem_u32(ring_s), 16, 1024), x_k = sdesc_sw128(smem_u32(ring_x), 16, 1024);
+        const uint64_t acc_mn = sdesc_sw128(smem_u32(kDV ? ring_a : ring_s), C::RING_CB, 1024);
+        uint32_t units_done = 0, h = 0, units = 0;      // h: steps so far
+        uint32_t xs = 0;                                // slots of X's ring so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-            bool r = ok && mbar_wait(smem_u32(bar), parity, abort_flag, p.timeout_ns);
-            r = __all_sync(0xffffffffu, r);
-            if (!r) ok = false;
-            return r;
+            ok = ok && warp_wait(bar, parity);
+            return ok;
         };
         auto commit = [&](uint64_t* bar) { mma_commit_warp(smem_u32(bar)); };
-        auto slot = [&](uint32_t n) { return n % C::NSLOT; };
-        auto full = [&](uint32_t n) -> bool { return wait(&bars->ring_full[slot(n)], (n / C::NSLOT) & 1); };
-        // d_col (+)= A B^T over d columns: fixed part `part` (0: Q or K; 1, 2: halves of dO or V), ring tile n
-        auto mm_kk = [&](uint32_t d_col, int part, uint32_t n, bool accumulate) {
+        // d_col (+)= A B^T over d columns: fixed tiles from part `part` on, ring tile b0
+        auto mm_kk = [&](uint32_t d_col, int part, uint64_t b0, bool accumulate) {
             const uint64_t a0 = fix_k + (uint64_t)((part * C::NCB * C::FIX_CB) >> 4);
-            const uint64_t b0 = ring_k + (uint64_t)((slot(n) * C::SLOT) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const int byte = kk * 32;
@@ -459,177 +535,109 @@ __global__ void __launch_bounds__(DiffBwdCfg<D, kDQ>::NUM_THREADS, 1)
                                    (kk > 0 || accumulate) ? 1u : 0u);
             }
         };
-        // acc_col (+)= A (TMEM, packed to bf16 by both warpgroups, each over the first half of its
-        // columns) times ring tile n as MN-major
-        auto mm_acc = [&](uint32_t acc_col, uint32_t a_col, uint32_t n, bool accumulate) {
-            const uint64_t b0 = ring_mn + (uint64_t)((slot(n) * C::SLOT) >> 4);
-            constexpr int PER = C::BC / 32;                            // k-steps of a warpgroup
-#pragma unroll
-            for (int kk = 0; kk < C::BC / 16; ++kk)
-                mma_ts_warp<false>(tmem + acc_col, tmem + a_col + (kk / PER) * (C::BC / 2) + (kk % PER) * 8,
-                                   b0 + (uint64_t)((kk * 16 * 128) >> 4), idesc_acc, (kk > 0 || accumulate) ? 1u : 0u);
-        };
-        // packed rows behind the sequence become 0 in ring tile n, whose first row is `row`
-        auto clear_tail = [&](const DiffBwdUnit& w, int row, uint32_t n) {
+        // packed rows behind the sequence become 0 in a slot that starts at column `c` of the unit's columns
+        auto clear_tail = [&](const DiffBwdUnit& w, int c, uint8_t* t, int blocks) {
             if constexpr (kPacked) {
-                const int live = w.N - row;
+                const int live = w.N - c;
                 if (live >= C::BC) return;
-                uint8_t* t = ring + slot(n) * C::SLOT;
                 for (int o = live * 128 + lane * 16; o < C::RING_CB; o += 512)
-#pragma unroll
-                    for (int cb = 0; cb < C::NCB; ++cb)
-                        *reinterpret_cast<uint4*>(t + cb * C::RING_CB + o) = make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < blocks; ++i)
+                        *reinterpret_cast<uint4*>(t + i * C::RING_CB + o) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
                 __syncwarp();
             }
         };
-        while (ok) {
-            const int u = take_unit(units, ok);
-            if (u < 0) break;
-            DiffBwdUnit w;
-            diff_bwd_unit<kDQ, kPacked>(p, u, heads, tab, w);
-            int lo, hi;
-            diff_bwd_steps<kDQ, C::BC>(p, w, lo, hi);
-            if constexpr (kDQ) {
-                // Step j: dP(j) once the compute warps have read dP(j-1), the accumulation of step
-                // j-1, S(j+1) into the other buffer.  Ring: K_j, V_j's halves, K_{j+1}, ...
-                const uint32_t r0 = rc, h0 = hs;
-                auto nk = [&](int j) { return r0 + 3u * (uint32_t)(j - lo); };
-                if (!wait(&bars->fix_full, items_done & 1)) break;
-                if (!full(nk(lo))) break;
-                clear_tail(w, lo * C::BC, nk(lo));
+        DiffBwdUnit w;
+        while (take_unit(units, ok, w)) {
+            const int per = kDQ ? w.n : w.n / G;
+            if (!wait(&bars->fix_full, units_done & 1)) break;
+            const uint32_t h0 = h;
+            auto column = [&](int x) { return (w.lo + x % per) * C::BC; };
+            // S of step x (number h): buffer h & 1 was last read by the accumulation of step h - 2
+            auto issue_s = [&](int x) -> bool {
+                const uint32_t hx = h0 + (uint32_t)x, slot = hx % C::NS;
+                if (!wait(&bars->s_in_full[slot], (hx / C::NS) & 1)) return false;
+                clear_tail(w, column(x), ring_s + slot * C::S_BYTES, C::NCB);
                 tc_fence_after_sync();
-                mm_kk((h0 & 1) * 128, 0, nk(lo), false);
-                bool started = false;
-                for (int j = lo; j < hi && ok; ++j) {
-                    const uint32_t hj = h0 + (uint32_t)(j - lo), nv = nk(j) + 1;
-                    if (!full(nv) || !full(nv + 1)) break;
-                    if (hj > 0 && !wait(&bars->dp_free, (hj - 1) & 1)) break;
+                mm_kk((hx & 1) * C::BC, 0, s_k + (uint64_t)((slot * C::S_BYTES) >> 4), false);
+                if (kDV) commit(&bars->s_in_empty[slot]);
+                return true;
+            };
+            // the accumulation of step x: dS or the weights from TMEM, packed by both warpgroups over the first
+            // half of their columns of S
+            auto issue_acc = [&](int x) -> bool {
+                const uint32_t hx = h0 + (uint32_t)x, slot = hx % (kDV ? C::NACC : C::NS);
+                if (x == 0 && !wait(&bars->acc_empty, (units_done & 1) ^ 1)) return false;
+                if constexpr (kDV) {
+                    if (!wait(&bars->a_in_full[slot], (hx / C::NACC) & 1)) return false;
+                    clear_tail(w, column(x), ring_a + slot * C::A_BYTES, 2 * C::NCB);
                     tc_fence_after_sync();
-                    mm_kk(C::DP_OFF, 1, nv, false);
-                    commit(&bars->ring_empty[slot(nv)]);
-                    mm_kk(C::DP_OFF, 2, nv + 1, true);
-                    commit(&bars->ring_empty[slot(nv + 1)]);
-                    if (j == hi - 1) commit(&bars->fix_empty);
-                    if (j > lo) {
-                        // s_full of this step before the accumulation of the last, and only when that
-                        // one's p_full was seen: no barrier runs a phase ahead
-                        if (!wait(&bars->p_full[0], (hj - 1) & 1)) break;
-                        commit(&bars->s_full[0]);
-                        if (!started && !wait(&bars->acc_empty, (items_done & 1) ^ 1)) break;
-                        tc_fence_after_sync();
-                        mm_acc(C::DQ_COL, ((hj - 1) & 1) * 128, nk(j - 1), started);
-                        started = true;
-                        commit(&bars->ring_empty[slot(nk(j - 1))]);
-                    } else {
-                        commit(&bars->s_full[0]);
-                    }
-                    if (j + 1 < hi) {
-                        if (!full(nk(j + 1))) break;
-                        clear_tail(w, (j + 1) * C::BC, nk(j + 1));
-                        tc_fence_after_sync();
-                        mm_kk(((hj + 1) & 1) * 128, 0, nk(j + 1), false);
-                    }
                 }
-                if (!ok) break;
-                const uint32_t hl = h0 + (uint32_t)(hi - 1 - lo);
-                if (!wait(&bars->p_full[0], hl & 1)) break;
-                if (!started && !wait(&bars->acc_empty, (items_done & 1) ^ 1)) break;
-                tc_fence_after_sync();
-                mm_acc(C::DQ_COL, (hl & 1) * 128, nk(hi - 1), started);
-                commit(&bars->ring_empty[slot(nk(hi - 1))]);
-                commit(&bars->acc_done);
-                rc = nk(hi);
-                hs = h0 + (uint32_t)(hi - lo);
-                ++items_done;
-            } else {
-                const int ns = hi - lo, n = G * ns;
-                for (int m = 0; m < 2 && ok; ++m) {
-                    if (!wait(&bars->fix_full, items_done & 1)) break;
-                    // the accumulations of step h of this item (number x), from ring position r on
-                    auto issue_acc = [&](uint32_t h, uint32_t r, int x) -> bool {
-                        const uint32_t buf = (h % C::NB) * 128;
-                        if (!wait(&bars->p_full[h % C::NB], (h / C::NB) & 1)) return false;
-                        if (x == 0 && !wait(&bars->acc_empty, (items_done & 1) ^ 1)) return false;
-                        tc_fence_after_sync();
-                        mm_acc(C::DV_COL, buf, r + 1, m > 0 || x > 0);                   // dV += P^T dO
-                        mm_acc(C::DV_COL + D, buf, r + 2, m > 0 || x > 0);
-                        commit(&bars->ring_empty[slot(r + 1)]);
-                        commit(&bars->ring_empty[slot(r + 2)]);
-                        mm_acc(C::DK_COL, buf + C::DP_OFF, r, x > 0);                    // dK += dS^T Q
-                        commit(&bars->ring_empty[slot(r)]);
-                        return true;
-                    };
-                    for (int x = 0; x < n; ++x) {
-                        if (C::NB == 1 && x > 0 && !issue_acc(hs - 1, rc - 3, x - 1)) break;
-                        if (!full(rc) || !full(rc + 1) || !full(rc + 2)) break;
-                        const int row = (lo + x % ns) * C::BC;
-                        clear_tail(w, row, rc);
-                        clear_tail(w, row, rc + 1);
-                        clear_tail(w, row, rc + 2);
-                        tc_fence_after_sync();
-                        const uint32_t buf = (hs % C::NB) * 128;
-                        mm_kk(buf, 0, rc, false);                                        // S^T
-                        mm_kk(buf + C::DP_OFF, 1, rc + 1, false);                        // dP^T
-                        mm_kk(buf + C::DP_OFF, 2, rc + 2, true);
-                        commit(&bars->s_full[hs % C::NB]);
-                        if (x == n - 1) commit(&bars->fix_empty);
-                        if (C::NB == 2 && x > 0 && !issue_acc(hs - 1, rc - 3, x - 1)) break;
-                        ++hs;
-                        rc += 3;
-                    }
-                    if (!ok) break;
-                    if (!issue_acc(hs - 1, rc - 3, n - 1)) break;
-                    commit(&bars->acc_done);
-                    ++items_done;
+                const uint64_t t = acc_mn + (uint64_t)((slot * (kDV ? C::A_BYTES : C::S_BYTES)) >> 4);
+                constexpr int PER = C::HC / 16;         // k-steps of a warpgroup
+#pragma unroll
+                for (int kk = 0; kk < C::BC / 16; ++kk)
+                    mma_ts_warp<false>(tmem + C::ACC_COL, tmem + (hx & 1) * C::BC + (kk / PER) * C::HC + (kk % PER) * 8,
+                                       t + (uint64_t)((kk * 16 * 128) >> 4), idesc_acc, (kk > 0 || x > 0) ? 1u : 0u);
+                commit(kDV ? &bars->a_in_empty[slot] : &bars->s_in_empty[slot]);
+                return true;
+            };
+            if (!issue_s(0)) break;
+            for (int x = 0; x < w.n && ok; ++x) {
+                const uint32_t hx = h0 + (uint32_t)x;
+                // X of this step, in parts of d columns, once the compute warps have read the last one
+                if (hx > 0 && !wait(&bars->x_free, (hx - 1) & 1)) break;
+                bool there = true;
+#pragma unroll
+                for (int part = 0; part < C::X_PARTS; ++part, ++xs) {
+                    const uint32_t slot = xs % C::NX;
+                    there = there && wait(&bars->x_in_full[slot], (xs / C::NX) & 1);
+                    if (!there) break;
+                    tc_fence_after_sync();
+                    mm_kk(C::X_COL, 1 + part, x_k + (uint64_t)((slot * C::X_BYTES) >> 4), part > 0);
+                    commit(&bars->x_in_empty[slot]);
                 }
+                if (!there) break;
+                if (x == w.n - 1) commit(&bars->fix_empty);     // S of this step was issued before
+                // s_full of this step before the accumulation of the last, and only when that one's p_full was
+                // seen: no barrier runs a phase ahead
+                if (x > 0) {
+                    if (!wait(&bars->p_full, (hx - 1) & 1)) break;
+                    commit(&bars->s_full);
+                    tc_fence_after_sync();
+                    if (!issue_acc(x - 1)) break;
+                } else {
+                    commit(&bars->s_full);
+                }
+                if (x + 1 < w.n && !issue_s(x + 1)) break;
             }
+            if (!ok) break;
+            h = h0 + (uint32_t)w.n;
+            if (!wait(&bars->p_full, (h - 1) & 1)) break;
+            tc_fence_after_sync();
+            if (!issue_acc(w.n - 1)) break;
+            commit(&bars->acc_done);
+            ++units_done;
         }
         if (!ok && lane == 0) timed_out();
         commit(&bars->drain);
         mbar_wait(smem_u32(&bars->drain), 0, nullptr, kCleanupTimeoutNs);
         __syncwarp();
     } else if (warp < C::COMPUTE_WARPS) {
-        // both warpgroups work on every step, warpgroup wg on its half of the columns
+        // both warpgroups work on every step, warpgroup wg on its half of the columns, a thread one row
         regs_increase<C::REG_COMPUTE>();
         const int wg = warp >> 2, trow = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-        const float LOG2E = 1.4426950408889634f;
-        uint32_t h = 0, units = 0, items_done = 0;
+        constexpr float LOG2E = 1.4426950408889634f;
+        const float2 c2 = make_float2(p.c_log2, p.c_log2);
+        uint32_t h = 0, units = 0, units_done = 0;
         bool ok = true;
         auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-            bool r = ok && mbar_wait(smem_u32(bar), parity, abort_flag, p.timeout_ns);
-            r = __all_sync(0xffffffffu, r);
-            if (!r) ok = false;
-            return r;
+            ok = ok && warp_wait(bar, parity);
+            return ok;
         };
-        // `cols` accumulator columns from `col` on, times f, to a row of bf16
-        auto write = [&](auto cols_tag, uint32_t col, float f, __nv_bfloat16* out, bool valid) {
-            constexpr int cols = decltype(cols_tag)::value;
-#pragma unroll
-            for (int ch = 0; ch < cols / 32; ++ch) {
-                uint32_t r[32];
-                tmem_ld32(tmem + lane_addr + col + ch * 32, r);
-                tmem_wait_ld(r);
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    pk[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
-                if (valid) {
-                    uint4* dst = reinterpret_cast<uint4*>(out + ch * 32);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
-                }
-            }
-        };
-        while (ok) {
-            const int u = take_unit(units, ok);
-            if (u < 0) break;
-            DiffBwdUnit w;
-            diff_bwd_unit<kDQ, kPacked>(p, u, heads, tab, w);
-            int lo, hi;
-            diff_bwd_steps<kDQ, C::BC>(p, w, lo, hi);
+        DiffBwdUnit w;
+        while (take_unit(units, ok, w)) {
             const int my = w.t * 128 + trow;            // this thread's row (query or key)
             const bool valid = my < w.N;
             // The columns that the mask allows for this row are [m_lo, m_hi]; a row behind the sequence
@@ -645,209 +653,222 @@ __global__ void __launch_bounds__(DiffBwdCfg<D, kDQ>::NUM_THREADS, 1)
             m_hi = min(m_hi, w.N - 1);
             m_lo = min(m_lo, m_hi);
             const uint32_t m_span = (uint32_t)(m_hi - m_lo);
+            const int per = kDQ ? w.n : w.n / G;
+            // what this row needs (dQ): minus its LSE (log2 units) and minus its D
+            float2 row_l = make_float2(0.0f, 0.0f), row_d = row_l;
             if constexpr (kDQ) {
-                const size_t vec = diff_bwd_vec<kPacked>(p, w, w.z);
-                const float lse2 = valid ? __ldg(p.lse + vec + my) * LOG2E : 0.0f;
-                const float dlt = valid ? __ldg(p.delta + vec + my) : 0.0f;
-                const uint32_t h0 = h;
-                h = h0 + (uint32_t)(hi - lo);
-                for (int j = lo; j < hi; ++j) {
-                    const uint32_t hj = h0 + (uint32_t)(j - lo);
-                    constexpr int HC = C::BC / 2;       // this warpgroup's keys
-                    const int c0 = j * C::BC + wg * HC;
-                    if (!wait_all(&bars->s_full[0], hj & 1)) break;
-                    tc_fence_after_sync();
-                    const uint32_t sb = tmem + lane_addr + (hj & 1) * 128 + (uint32_t)(wg * HC);
-                    const uint32_t db = tmem + lane_addr + C::DP_OFF + (uint32_t)(wg * HC);
-                    uint32_t sra[HC], dra[HC];
-#pragma unroll
-                    for (int ch = 0; ch < HC; ch += 32) {
-                        tmem_ld32p(sb + ch, sra + ch);
-                        tmem_ld32p(db + ch, dra + ch);
-                    }
-                    tmem_wait_ld_only();
-#pragma unroll
-                    for (int ch = 0; ch < HC; ch += 32) {
-                        reg_fence32(sra + ch);
-                        reg_fence32(dra + ch);
-                    }
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bars->dp_free));
-                    auto step = [&](auto masked_tag) {
-                        constexpr bool kMasked = decltype(masked_tag)::value;
-#pragma unroll
-                        for (int ch = 0; ch < HC / 32; ++ch) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float ds[2];
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const int i = ch * 32 + 2 * e + k;
-                                    const float pr = ex2(fmaf(__uint_as_float(sra[i]), p.c_log2, -lse2));
-                                    ds[k] = pr * (__uint_as_float(dra[i]) - dlt);
-                                    if constexpr (kMasked) {
-                                        const uint32_t off = (uint32_t)(c0 - m_lo) + (uint32_t)i;
-                                        ds[k] = off <= m_span ? ds[k] : 0.0f;
-                                    }
-                                }
-                                pk[e] = pack_bf16x2(ds[0], ds[1]);
-                            }
-                            tmem_st16p(sb + ch * 16, pk);
-                        }
-                    };
-                    if (diff_bwd_full(p, w.N, w.t * 128, 128, j * C::BC, C::BC)) step(std::false_type{});
-                    else step(std::true_type{});
-                    tmem_wait_st();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[0]));
-                }
-                if (!ok) break;
-                if (!wait_all(&bars->acc_done, items_done & 1)) break;
+                const size_t at = diff_bwd_vec<kPacked>(p, w, w.z) + (valid ? my : 0);
+                row_l.x = row_l.y = -diff_ld(p.lse + at) * LOG2E;
+                row_d.x = row_d.y = -diff_ld(p.delta + at);
+            }
+            int s = w.lo;
+            for (int x = 0; x < w.n; ++x) {
+                const uint32_t hx = h++;
+                const int c0 = s * C::BC;
+                if (++s == w.lo + per) s = w.lo;
+                const float* col = columns + (hx & 1) * C::COL_FLOATS;
+                if (!kDQ && !wait_all(&bars->col_full[hx & 1], (hx >> 1) & 1)) break;
+                if (!wait_all(&bars->s_full, hx & 1)) break;
                 tc_fence_after_sync();
-                const float f = (w.z & 1) ? -p.scale * __ldg(p.lam + (w.z >> 1)) : p.scale;
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dq) +
-                                     diff_bwd_row<kPacked>(p, w, 2 * p.H, w.z, my) * D + wg * (D / 2);
-                write(std::integral_constant<int, D / 2>{}, C::DQ_COL + wg * (D / 2), f, out, valid);
+                const uint32_t sb = tmem + lane_addr + (hx & 1) * C::BC + (uint32_t)(wg * C::HC);
+                const uint32_t xb = tmem + lane_addr + C::X_COL + (uint32_t)(wg * C::HC);
+                uint32_t a[C::HC], b[C::HC];
+#pragma unroll
+                for (int ch = 0; ch < C::HC; ch += 32) {
+                    tmem_ld32p(xb + ch, b + ch);
+                    tmem_ld32p(sb + ch, a + ch);
+                }
+                tmem_wait_ld_only();
+#pragma unroll
+                for (int ch = 0; ch < C::HC; ch += 32) {
+                    reg_fence32(b + ch);
+                    reg_fence32(a + ch);
+                }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->acc_empty));
-                ++items_done;
-            } else {
-                float* my_lse2 = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + C::COL_OFF) + warp * 64;
-                float* my_delta = my_lse2 + 32;
-                const int ns = hi - lo, n = G * ns;
-                for (int m = 0; m < 2 && ok; ++m) {
-                    // this lane's column of the next step: LSE (log2 units) and D
-                    float nl = 0.0f, nd = 0.0f;
-                    auto col_load = [&](int head, int s) {
-                        const size_t at = diff_bwd_vec<kPacked>(p, w, 2 * (w.z * G + head) + m) +
-                                          min(s * C::BC + wg * 32 + lane, w.N - 1);
-                        nl = __ldg(p.lse + at) * LOG2E;
-                        nd = __ldg(p.delta + at);
-                    };
-                    col_load(0, lo);
-                    int head = 0, s = lo;
-                    float f = m ? -__ldg(p.lam + w.z * G) : 1.0f;
-                    for (int x = 0; x < n; ++x) {
-                        __syncwarp();                   // the last step's values have been read
-                        my_lse2[lane] = nl;
-                        my_delta[lane] = nd;
-                        __syncwarp();
-                        const int c0 = s * C::BC + wg * 32;
-                        const float fx = f;
-                        const bool open = diff_bwd_full(p, w.N, s * C::BC, C::BC, w.t * 128, 128);
-                        if (++s == hi) {
-                            s = lo;
-                            ++head;
-                            if (m && head < G) f = -__ldg(p.lam + w.z * G + head);
-                        }
-                        if (head < G) col_load(head, s);
-                        const uint32_t hx = h++;
-                        if (!wait_all(&bars->s_full[hx % C::NB], (hx / C::NB) & 1)) break;
-                        tc_fence_after_sync();
-                        const uint32_t sb = tmem + lane_addr + (hx % C::NB) * 128 + (uint32_t)wg * 32;
-                        uint32_t sr[32], dr[32];
-                        tmem_ld32p(sb, sr);
-                        tmem_ld32p(sb + C::DP_OFF, dr);
-                        tmem_wait_ld_only();
-                        reg_fence32(sr);
-                        reg_fence32(dr);
-                        auto step = [&](auto masked_tag) {
-                            constexpr bool kMasked = decltype(masked_tag)::value;
-                            uint32_t pp[16], pd[16];
+                if (lane == 0) mbar_arrive(smem_u32(&bars->x_free));
+                auto step = [&](auto masked_tag) {
+                    constexpr bool kMasked = decltype(masked_tag)::value;
+                    float2 f2 = make_float2(1.0f, 1.0f);
+                    if constexpr (!kDQ) f2.x = f2.y = col[2 * C::BC];
 #pragma unroll
-                            for (int e4 = 0; e4 < 8; ++e4) {
-                                const float4 l4 = *reinterpret_cast<const float4*>(my_lse2 + 4 * e4);
-                                const float4 d4 = *reinterpret_cast<const float4*>(my_delta + 4 * e4);
-                                const float l[4] = {l4.x, l4.y, l4.z, l4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
-                                float pv[4], ds[4];
+                    for (int ch = 0; ch < C::HC / 32; ++ch) {
+                        uint32_t pk[16];
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const int i = 4 * e4 + k;
-                                    pv[k] = fx * ex2(fmaf(__uint_as_float(sr[i]), p.c_log2, -l[k]));
-                                    ds[k] = pv[k] * (__uint_as_float(dr[i]) - d[k]);
-                                    if constexpr (kMasked) {
-                                        const uint32_t off = (uint32_t)(c0 - m_lo) + (uint32_t)i;
-                                        pv[k] = off <= m_span ? pv[k] : 0.0f;
-                                        ds[k] = off <= m_span ? ds[k] : 0.0f;
-                                    }
-                                }
-                                pp[2 * e4] = pack_bf16x2(pv[0], pv[1]);
-                                pp[2 * e4 + 1] = pack_bf16x2(pv[2], pv[3]);
-                                pd[2 * e4] = pack_bf16x2(ds[0], ds[1]);
-                                pd[2 * e4 + 1] = pack_bf16x2(ds[2], ds[3]);
+                        for (int e4 = 0; e4 < 8; ++e4) {
+                            float4 l4, d4;
+                            if constexpr (!kDQ) {
+                                l4 = *reinterpret_cast<const float4*>(col + wg * C::HC + ch * 32 + 4 * e4);
+                                d4 = *reinterpret_cast<const float4*>(col + C::BC + wg * C::HC + ch * 32 + 4 * e4);
                             }
-                            tmem_st16p(sb, pp);                 // P^T over S^T
-                            tmem_st16p(sb + C::DP_OFF, pd);     // dS^T over dP^T
-                        };
-                        if (open) step(std::false_type{});
-                        else step(std::true_type{});
-                        tmem_wait_st();
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[hx % C::NB]));
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int e = ch * 32 + 4 * e4 + 2 * k;
+                                const float2 l = kDQ ? row_l : k ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
+                                const float2 d = kDQ ? row_d : k ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y);
+                                const float2 va = make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1]));
+                                const float2 vb = make_float2(__uint_as_float(b[e]), __uint_as_float(b[e + 1]));
+                                const float2 xa = __ffma2_rn(va, c2, l);
+                                float2 pa = make_float2(ex2(xa.x), ex2(xa.y)), r;
+                                if constexpr (kDV) {
+                                    const float2 xv = __ffma2_rn(vb, c2, d);
+                                    r = __ffma2_rn(make_float2(ex2(xv.x), ex2(xv.y)), f2, pa);
+                                } else {
+                                    if constexpr (!kDQ) pa = __fmul2_rn(pa, f2);
+                                    r = __fmul2_rn(pa, __fadd2_rn(vb, d));
+                                }
+                                if constexpr (kMasked) {
+                                    const uint32_t off = (uint32_t)(c0 + wg * C::HC - m_lo) + (uint32_t)e;
+                                    r.x = off <= m_span ? r.x : 0.0f;
+                                    r.y = off + 1u <= m_span ? r.y : 0.0f;
+                                }
+                                pk[2 * e4 + k] = pack_bf16x2(r.x, r.y);
+                            }
+                        }
+                        tmem_st16p(sb + ch * 16, pk);           // over S, already loaded
                     }
-                    if (!ok) break;
-                    if (!wait_all(&bars->acc_done, items_done & 1)) break;
-                    tc_fence_after_sync();
-                    __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) +
-                                        diff_bwd_row<kPacked>(p, w, 2 * p.Hkv, 2 * w.z + m, my) * D + wg * (D / 2);
-                    write(std::integral_constant<int, D / 2>{}, C::DK_COL + wg * (D / 2), p.scale, dk, valid);
-                    if (m == 1) {
-                        __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) +
-                                            diff_bwd_row<kPacked>(p, w, p.Hkv, w.z, my) * (2 * D) + wg * D;
-                        write(std::integral_constant<int, D>{}, C::DV_COL + wg * D, 1.0f, dv, valid);
-                    }
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bars->acc_empty));
-                    ++items_done;
+                };
+                if (diff_bwd_full(p, w.N, kDQ ? w.t * 128 : c0, kDQ ? 128 : C::BC, kDQ ? c0 : w.t * 128, kDQ ? C::BC : 128))
+                    step(std::false_type{});
+                else
+                    step(std::true_type{});
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bars->p_full));
+                    if (!kDQ) mbar_arrive(smem_u32(&bars->col_empty[hx & 1]));
                 }
             }
+            if (!ok) break;
+            if (!wait_all(&bars->acc_done, units_done & 1)) break;
+            tc_fence_after_sync();
+            // each warpgroup writes half of the accumulator's columns
+            float f = kDV ? 1.0f : p.scale;
+            __nv_bfloat16* out;
+            if constexpr (kDQ) {
+                if (w.z & 1) f *= -diff_ld(p.lam + (w.z >> 1));
+                out = static_cast<__nv_bfloat16*>(p.dq);
+            } else {
+                out = static_cast<__nv_bfloat16*>(kDV ? p.dv : p.dk);
+            }
+            out += diff_bwd_row<kPacked>(p, w, heads, w.z, my) * C::ACC + wg * (C::ACC / 2);
+#pragma unroll
+            for (int ch = 0; ch < C::ACC / 64; ++ch) {
+                uint32_t r[32];
+                tmem_ld32(tmem + lane_addr + C::ACC_COL + wg * (C::ACC / 2) + ch * 32, r);
+                tmem_wait_ld(r);
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    pk[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
+                if (valid) {
+                    uint4* dst = reinterpret_cast<uint4*>(out + ch * 32);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->acc_empty));
+            ++units_done;
         }
         if (!ok) timed_out();
         tmem_wait_st();
     } else {
         regs_decrease<C::REG_CONTROL>();
-        if (!kDQ && warp == C::SUM_WARP) diff_dlam(p, lane);
+        if (!kDQ && warp == C::COLUMN_WARP) {
+            // what the columns of a step need: minus the LSE (log2 units) of the map and minus D, or minus both
+            // maps' LSE (dV), and the factor of the weights (of map 2), a step ahead of the compute warps
+            constexpr int PER = C::BC / 32;             // columns of a lane
+            constexpr float LOG2E = 1.4426950408889634f;
+            uint32_t h = 0, units = 0;
+            bool ok = true;
+            DiffBwdUnit w;
+            while (take_unit(units, ok, w)) {
+                const int per = w.n / G;
+                int head = 0, s = w.lo;
+                for (int x = 0; x < w.n && ok; ++x, ++h) {
+                    const int hq = (kDV ? w.z : w.z >> 1) * G + head;
+                    const size_t at = diff_bwd_vec<kPacked>(p, w, 2 * hq + (kDV ? 0 : w.z & 1));
+                    const size_t other = kPacked ? (size_t)p.T : (size_t)p.N;     // from map 1 to map 2
+                    float l[PER], d[PER];
+#pragma unroll
+                    for (int k = 0; k < PER; ++k) {
+                        const int q = min(s * C::BC + k * 32 + lane, w.N - 1);
+                        l[k] = -diff_ld(p.lse + at + q) * LOG2E;
+                        d[k] = kDV ? -diff_ld(p.lse + at + other + q) * LOG2E : -diff_ld(p.delta + at + q);
+                    }
+                    const float f = kDV || (w.z & 1) ? -diff_ld(p.lam + hq) : 1.0f;
+                    if (++s == w.lo + per) {
+                        s = w.lo;
+                        ++head;
+                    }
+                    ok = warp_wait(&bars->col_empty[h & 1], ((h >> 1) & 1) ^ 1);
+                    if (!ok) break;
+                    float* col = columns + (h & 1) * C::COL_FLOATS;
+#pragma unroll
+                    for (int k = 0; k < PER; ++k) {
+                        col[k * 32 + lane] = l[k];
+                        col[C::BC + k * 32 + lane] = d[k];
+                    }
+                    if (lane == 0) col[2 * C::BC] = f;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars->col_full[h & 1]));
+                }
+            }
+            if (!ok) timed_out();
+        }
+        if (kPass == kPassDK && warp == C::SUM_WARP) diff_dlam(p, lane);
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     if (warp == C::MMA_WARP) tmem_dealloc(tmem, 512);
+    // the last pass's end is the end of all
+    if constexpr (kPass != kPassDK) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// One pass, as a dependent of what was launched before it.
+template <int D, int kPass, bool kPacked>
+static cudaError_t launch_diff_bwd_pass(const DiffBwdMaps& m, const DiffBwdParams& p, int heads, int sm_count,
+                                        cudaStream_t stream)
+{
+    using C = DiffBwdCfg<D, kPass>;
+    auto kernel = diff_bwd_kernel<D, kPass, kPacked>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    // setmaxnreg.inc would wait forever if the launch pool were smaller than the split
+    cudaFuncAttributes attr;
+    if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
+    if (attr.numRegs * C::NUM_THREADS < C::REG_POOL) return cudaErrorInvalidConfiguration;
+    const long long units = (long long)p.nt * p.B * heads;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute dep[1];
+    dep[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    dep[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = dep;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3((unsigned)(units < sm_count ? units : sm_count));
+    cfg.blockDim = dim3(C::NUM_THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    if constexpr (C::DQ) return cudaLaunchKernelEx(&cfg, kernel, m.q, m.dout, m.k, m.v, p);
+    else if constexpr (C::BC == 64) return cudaLaunchKernelEx(&cfg, kernel, m.k, m.v, m.q64, m.dout64, p);
+    else return cudaLaunchKernelEx(&cfg, kernel, m.k, m.v, m.q, m.dout, p);
 }
 
 template <int D, bool kPacked>
 static cudaError_t launch_diff_bwd_t(const DiffBwdMaps& m, const DiffBwdParams& p, int sm_count, cudaStream_t stream)
 {
-    using CQ = DiffBwdCfg<D, true>;
-    using CK = DiffBwdCfg<D, false>;
     const long long rows = kPacked ? (long long)p.T * p.H : (long long)p.B * p.H * p.N;
     diff_dot_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    auto kq = diff_bwd_kernel<D, true, kPacked>;
-    auto kk = diff_bwd_kernel<D, false, kPacked>;
-    if ((e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, CQ::SMEM_BYTES)) != cudaSuccess)
-        return e;
-    if ((e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, CK::SMEM_BYTES)) != cudaSuccess)
-        return e;
-    // setmaxnreg.inc would wait forever if the launch pool were smaller than the split
-    for (const void* f : {reinterpret_cast<const void*>(kq), reinterpret_cast<const void*>(kk)}) {
-        cudaFuncAttributes attr;
-        if ((e = cudaFuncGetAttributes(&attr, f)) != cudaSuccess) return e;
-        if (attr.numRegs * CQ::NUM_THREADS < CQ::REG_POOL) return cudaErrorInvalidConfiguration;
-    }
-    const long long tiles = (long long)p.nt * p.B;
-    auto grid = [&](int heads) { return (int)(tiles * heads < sm_count ? tiles * heads : sm_count); };
-    kq<<<grid(2 * p.H), CQ::NUM_THREADS, CQ::SMEM_BYTES, stream>>>(m.q, m.dout, CQ::BC == 64 ? m.k64 : m.k,
-                                                                       CQ::BC == 64 ? m.v64 : m.v, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    kk<<<grid(p.Hkv), CK::NUM_THREADS, CK::SMEM_BYTES, stream>>>(m.k, m.v, m.q64, m.dout64, p);
-    return cudaGetLastError();
+    if ((e = launch_diff_bwd_pass<D, kPassDK, kPacked>(m, p, 2 * p.Hkv, sm_count, stream)) != cudaSuccess) return e;
+    if ((e = launch_diff_bwd_pass<D, kPassDV, kPacked>(m, p, p.Hkv, sm_count, stream)) != cudaSuccess) return e;
+    return launch_diff_bwd_pass<D, kPassDQ, kPacked>(m, p, 2 * p.H, sm_count, stream);
 }
 
 cudaError_t launch_diff_bwd(const DiffBwdMaps& m, const DiffBwdParams& p, int d, int sm_count, cudaStream_t stream)

@@ -9,6 +9,7 @@
 
 #include "attn_params.h"
 #include "paged_params.h"
+#include "sched.cuh"
 
 namespace gb300 {
 
@@ -57,7 +58,8 @@ struct DiffBwdParams {
     void* dq;               // bf16 [B, 2H, N, d] or [T, 2H, d]
     void* dk;               // bf16 [B, 2Hkv, N, d] or [T, 2Hkv, d]
     void* dv;               // bf16 [B, Hkv, N, 2d] or [T, Hkv, 2d]
-    int* next;              // [2]: the next unit of each pass, 0 before the first
+    int* next;              // [3]: the next unit of each pass, 0 before the first
+    SortTab* tab;           // packed: the sequences by length, with the 128-row tiles before each; or null
     int* status;
     int B, H, Hkv, N;
     int nt;                 // 128-row tiles of N rows
@@ -71,7 +73,7 @@ struct DiffBwdParams {
 
 struct DiffBwdMaps {
     CUtensorMap q, k, v, dout;      // 128-row boxes of 64 columns
-    CUtensorMap q64, k64, v64, dout64;   // 64-row boxes
+    CUtensorMap q64, dout64;        // 64-row boxes
 };
 
 // One decoding step of differential attention over a paged bf16 cache.  w holds what the cut of the work
