@@ -20,10 +20,14 @@
 //     (0 | q_2) in the same accumulator, and V is multiplied once for both.  Otherwise the columns
 //     of a product are one map's, and V's fragments are used for both.
 //     A tcgen05 tile would be at least 64 rows high, mostly empty.
-// Scores, weights' sums and O are fp32; a weight, relative to a running maximum that it may pass by
-// 2^8, is rounded to bf16.  Keys that a row does not see have weight 0, value rows outside every
+// Scores, weights' sums and O are fp32.  A weight, relative to a running maximum that it may pass by
+// 2^8, enters as two bf16 numbers, what it rounds to and the rest, off by 2^-17 of it (one of them
+// would double O's error, 0.0017 to 0.0026 relative at 16 x 8 heads x 8192 keys; the second product
+// hides behind the loads).  Keys that a row does not see have weight 0, value rows outside every
 // row's range become 0, and a NaN or infinite value at a key that only some rows see is taken out
 // of the product and reaches those rows as NaN (keep_nan).
+#include <cmath>
+
 #include "decode_fp8.cuh"
 #include "diff_params.h"
 
@@ -385,7 +389,7 @@ __global__ void __launch_bounds__(kDdThreads, DdCfg<D, NT>::CTAS)
                                 for (int e = 0; e < 4; ++e) acc[nt][i][e] *= al[e & 1];
                         }
                     }
-                    uint32_t pb[NT][2];
+                    uint32_t pb[NT][2], pl[NT][2];                 // the weights in bf16, and what that leaves
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float wt[4];
@@ -396,8 +400,13 @@ __global__ void __launch_bounds__(kDdThreads, DdCfg<D, NT>::CTAS)
                         }
                         l[nt][0] += wt[0] + wt[2];
                         l[nt][1] += wt[1] + wt[3];
-                        pb[nt][0] = dd_transpose(pack_bf16x2(wt[0], wt[1]));
-                        pb[nt][1] = dd_transpose(pack_bf16x2(wt[2], wt[3]));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t hi = pack_bf16x2(wt[2 * h], wt[2 * h + 1]);
+                            pb[nt][h] = dd_transpose(hi);
+                            pl[nt][h] = dd_transpose(pack_bf16x2(wt[2 * h] - __uint_as_float(hi << 16),
+                                                                 wt[2 * h + 1] - __uint_as_float(hi & 0xFFFF0000u)));
+                        }
                     }
                     // ---- O^T += V^T P^T, this lane's keys 2t, 2t+1 and 2t+8, 2t+9 of 16
                     if (!edge) {
@@ -406,7 +415,10 @@ __global__ void __launch_bounds__(kDdThreads, DdCfg<D, NT>::CTAS)
                             uint32_t a[4];
                             dd_ldmatrix<true>(a, frag_at(base, 2 + i / (D / 16), i % (D / 16), v_row, v_ch));
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) dd_mma(acc[nt][i], a, pb[nt][0], pb[nt][1]);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                dd_mma(acc[nt][i], a, pb[nt][0], pb[nt][1]);
+                                dd_mma(acc[nt][i], a, pl[nt][0], pl[nt][1]);
+                            }
                         }
                     } else {
                         uint32_t live[2], seen[NT][2];
@@ -434,7 +446,10 @@ __global__ void __launch_bounds__(kDdThreads, DdCfg<D, NT>::CTAS)
                                 odd[e] &= 0x3F803F80u;                       // 1 where it was not finite
                             }
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) dd_mma(acc[nt][i], a, pb[nt][0], pb[nt][1]);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                dd_mma(acc[nt][i], a, pb[nt][0], pb[nt][1]);
+                                dd_mma(acc[nt][i], a, pl[nt][0], pl[nt][1]);
+                            }
                             if (__any_sync(0xffffffffu, (odd[0] | odd[1] | odd[2] | odd[3]) != 0)) {
                                 // keep_nan: O becomes NaN where a row sees such a value
 #pragma unroll
@@ -583,14 +598,42 @@ __global__ void __launch_bounds__(kDdThreads, DdCfg<D, NT>::CTAS)
 
 // Joins the parts of a unit that several ranges shared and subtracts the maps.  grid.x: the units, or
 // where there are more of them the CTAs (each leaves at most one unit to its successors); grid.y shares a
-// unit's rows and slices of 32 value columns.  Sixteen threads take a float4 of both maps from every
-// sixteenth part, with their loads in flight together, then one adds them up in order.
-constexpr int kDdJoinThreads = 128;
+// unit's rows and columns.  Up to eight parts, the usual batch: a thread joins a float4 of both maps from
+// all of them, with their loads in flight together.  More, one long sequence: sixteen threads take every
+// sixteenth part, then one adds them up in order.
+constexpr int kDdJoinThreads = 128, kDdFew = 8;
+
+struct DdSum {
+    float m, l;
+    float4 v;
+
+    __device__ __forceinline__ DdSum() : m(-INFINITY), l(0.0f), v(make_float4(0.0f, 0.0f, 0.0f, 0.0f)) {}
+
+    // Adds kParts parts (m, l, v) at once; absent ones have m = -inf and zeros.
+    template <int kParts>
+    __device__ __forceinline__ void add(const float (&pm)[kParts], const float (&pl)[kParts], const float4 (&pv)[kParts])
+    {
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) top = fmaxf(top, pm[k]);
+        const float mb = top == -__int_as_float(0x7f800000) ? 0.0f : top, f = ex2(m - mb);
+        m = top;
+        l *= f;
+        v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+            const float fac = ex2(pm[k] - mb);
+            l = fmaf(fac, pl[k], l);
+            v.x = fmaf(fac, pv[k].x, v.x), v.y = fmaf(fac, pv[k].y, v.y);
+            v.z = fmaf(fac, pv[k].z, v.z), v.w = fmaf(fac, pv[k].w, v.w);
+        }
+    }
+};
 
 template <int D, int COLS>
 __global__ void __launch_bounds__(kDdJoinThreads) diff_decode_join_kernel(const DiffDecodeParams p)
 {
-    constexpr int RC = COLS / 2, PART = dec8_part(COLS, 2 * D), SLICES = 2 * D / 32;
+    constexpr int RC = COLS / 2, PART = dec8_part(COLS, 2 * D), SLICES = 2 * D / 32, VEC = 2 * D / 4;
     constexpr int VECS = 8, GROUPS = kDdJoinThreads / VECS, FLY = 5;
     __shared__ float4 sm_v[2][GROUPS][VECS];
     __shared__ float2 sm_ml[2][GROUPS];
@@ -604,81 +647,71 @@ __global__ void __launch_bounds__(kDdJoinThreads) diff_decode_join_kernel(const 
     if (x0 < 0 || rg < 0 || rg >= pw.row_groups || todo.w < 0 || todo.w >= (long long)pw.B * pw.Hkv) return;
     const int rows = min(RC, pw.rows - rg * RC);
     const size_t row0 = (size_t)todo.w * pw.rows + rg * RC;
-    auto part_of = [&](int x) {
-        return pw.ws + 4 * ctas + (size_t)(2 * (x * pw.row_groups + rg) + (x == x0 ? 1 : 0)) * PART;
-    };
-    for (int item = blockIdx.y; item < rows * SLICES; item += gridDim.y) {
-        const int r = item / SLICES, v4 = (item - r * SLICES) * VECS + vec;
-        float M[2] = {NEG_INF, NEG_INF}, l[2] = {0.0f, 0.0f};
-        float4 a[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-        for (int xb = x0 + grp; xb <= x1; xb += FLY * GROUPS) {
-            float m[2][FLY], s[2][FLY];
-            float4 v[2][FLY];
+    // up to kParts parts x, x + step, ... of row r's map mp and float4 v4
+    auto gather = [&](auto parts_tag, int x, int step, int r, int v4, DdSum (&sum)[2]) {
+        constexpr int kParts = decltype(parts_tag)::value;
+        float m[2][kParts], l[2][kParts];
+        float4 v[2][kParts];
 #pragma unroll
-            for (int k = 0; k < FLY; ++k) {
-                const int x = xb + k * GROUPS;
-#pragma unroll
-                for (int mp = 0; mp < 2; ++mp) {
-                    m[mp][k] = NEG_INF;
-                    s[mp][k] = 0.0f;
-                    v[mp][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (x > x1) continue;
-                    const float* w = part_of(x);
-                    const int col = mp * RC + r;
-                    m[mp][k] = w[COLS * 2 * D + col];
-                    s[mp][k] = w[COLS * 2 * D + COLS + col];
-                    v[mp][k] = *reinterpret_cast<const float4*>(w + col * (2 * D) + v4 * 4);
-                }
-            }
+        for (int k = 0; k < kParts; ++k)
 #pragma unroll
             for (int mp = 0; mp < 2; ++mp) {
-                float top = M[mp];
-#pragma unroll
-                for (int k = 0; k < FLY; ++k) top = fmaxf(top, m[mp][k]);
-                const float mb = top == NEG_INF ? 0.0f : top, f = ex2(M[mp] - mb);
-                M[mp] = top;
-                l[mp] *= f;
-                a[mp].x *= f, a[mp].y *= f, a[mp].z *= f, a[mp].w *= f;
-#pragma unroll
-                for (int k = 0; k < FLY; ++k) {
-                    const float fac = ex2(m[mp][k] - mb);
-                    l[mp] = fmaf(fac, s[mp][k], l[mp]);
-                    a[mp].x = fmaf(fac, v[mp][k].x, a[mp].x), a[mp].y = fmaf(fac, v[mp][k].y, a[mp].y);
-                    a[mp].z = fmaf(fac, v[mp][k].z, a[mp].z), a[mp].w = fmaf(fac, v[mp][k].w, a[mp].w);
-                }
+                m[mp][k] = NEG_INF;
+                l[mp][k] = 0.0f;
+                v[mp][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const int at = x + k * step, col = mp * RC + r;
+                if (at > x1) continue;
+                const float* w = pw.ws + 4 * ctas + (size_t)(2 * (at * pw.row_groups + rg) + (at == x0 ? 1 : 0)) * PART;
+                m[mp][k] = w[COLS * 2 * D + col];
+                l[mp][k] = w[COLS * 2 * D + COLS + col];
+                v[mp][k] = *reinterpret_cast<const float4*>(w + col * (2 * D) + v4 * 4);
             }
+        sum[0].add(m[0], l[0], v[0]);
+        sum[1].add(m[1], l[1], v[1]);
+    };
+    auto finish = [&](int r, int v4, const DdSum (&sum)[2]) {
+        const size_t row = row0 + r;
+        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(pw.o) + row * (2 * D))[v4] =
+            dd_out(sum[0].v, sum[0].l, sum[1].v, sum[1].l, dd_lam(p, row));
+        if (v4 == 0) {
+            pw.lse[dd_qrow(row, pw.nq, 0)] = dd_lse(sum[0].m, sum[0].l);
+            pw.lse[dd_qrow(row, pw.nq, 1)] = dd_lse(sum[1].m, sum[1].l);
         }
+    };
+    if (x1 - x0 < kDdFew) {
+        for (int i = blockIdx.y * kDdJoinThreads + tid; i < rows * VEC; i += gridDim.y * kDdJoinThreads) {
+            DdSum sum[2];
+            const int r = i / VEC;
+            gather(std::integral_constant<int, kDdFew>{}, x0, 1, r, i - r * VEC, sum);
+            finish(r, i - r * VEC, sum);
+        }
+        return;
+    }
+    for (int item = blockIdx.y; item < rows * SLICES; item += gridDim.y) {
+        const int r = item / SLICES, v4 = (item - r * SLICES) * VECS + vec;
+        DdSum sum[2];
+        for (int x = x0 + grp; x <= x1; x += FLY * GROUPS)
+            gather(std::integral_constant<int, FLY>{}, x, GROUPS, r, v4, sum);
 #pragma unroll
         for (int mp = 0; mp < 2; ++mp) {
-            sm_v[mp][grp][vec] = a[mp];
-            if (vec == 0) sm_ml[mp][grp] = make_float2(M[mp], l[mp]);
+            sm_v[mp][grp][vec] = sum[mp].v;
+            if (vec == 0) sm_ml[mp][grp] = make_float2(sum[mp].m, sum[mp].l);
         }
         __syncthreads();
         if (tid < VECS) {
-            const int groups = min(GROUPS, x1 - x0 + 1);
+            DdSum all[2];
 #pragma unroll
             for (int mp = 0; mp < 2; ++mp) {
-                float top = NEG_INF;
-                for (int k = 0; k < groups; ++k) top = fmaxf(top, sm_ml[mp][k].x);
-                const float mb = top == NEG_INF ? 0.0f : top;
-                M[mp] = top;
-                l[mp] = 0.0f;
-                a[mp] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int k = 0; k < groups; ++k) {
-                    const float4 v = sm_v[mp][k][tid];
-                    const float fac = ex2(sm_ml[mp][k].x - mb);
-                    l[mp] = fmaf(fac, sm_ml[mp][k].y, l[mp]);
-                    a[mp].x = fmaf(fac, v.x, a[mp].x), a[mp].y = fmaf(fac, v.y, a[mp].y);
-                    a[mp].z = fmaf(fac, v.z, a[mp].z), a[mp].w = fmaf(fac, v.w, a[mp].w);
+                float m[GROUPS], l[GROUPS];
+                float4 v[GROUPS];
+#pragma unroll
+                for (int k = 0; k < GROUPS; ++k) {
+                    m[k] = sm_ml[mp][k].x, l[k] = sm_ml[mp][k].y;
+                    v[k] = sm_v[mp][k][tid];
                 }
+                all[mp].add(m, l, v);
             }
-            const size_t row = row0 + r;
-            reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(pw.o) + row * (2 * D))[v4] =
-                dd_out(a[0], l[0], a[1], l[1], dd_lam(p, row));
-            if (v4 == 0) {
-                pw.lse[dd_qrow(row, pw.nq, 0)] = dd_lse(M[0], l[0]);
-                pw.lse[dd_qrow(row, pw.nq, 1)] = dd_lse(M[1], l[1]);
-            }
+            finish(r, v4, all);
         }
         __syncthreads();
     }
@@ -705,8 +738,13 @@ static cudaError_t launch_diff_decode_n(const CUtensorMap& mk, const CUtensorMap
     if ((e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, p)) != cudaSuccess) return e;
     if (p.w.whole) return cudaSuccess;
     const long long units = (long long)p.w.B * p.w.Hkv * p.w.row_groups, ctas = (long long)p.w.ranges * p.w.row_groups;
-    const int items = (p.w.rows < C::RC ? p.w.rows : C::RC) * (2 * D / 32);
-    cfg.gridDim = dim3((unsigned)(units < ctas ? units : ctas), (unsigned)items);
+    // a unit's float4s over its CTAs, and four CTAs a part of the average unit while that is more, up to one
+    // for 32 columns of a row
+    const int rows = p.w.rows < C::RC ? p.w.rows : C::RC, items = rows * (2 * D / 32);
+    const int least = (rows * (2 * D / 4) + kDdJoinThreads - 1) / kDdJoinThreads;
+    long long share = units < ctas ? 4 * ctas / units : least;
+    share = share > items ? items : share < least ? least : share;
+    cfg.gridDim = dim3((unsigned)(units < ctas ? units : ctas), (unsigned)share);
     cfg.blockDim = dim3(kDdJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, diff_decode_join_kernel<D, C::COLS>, p);

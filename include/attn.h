@@ -598,7 +598,7 @@ attn_status_t attn_diff_bwd_bf16_varlen(const void* q, const void* k, const void
  * What the cache holds at keys a query does not see (rows behind the sequence, pages behind it or
  * before its window) never reaches that query's outputs, NaN included; an infinity in V counts as
  * NaN where only some of the queries that share a tile see its key.  Scores, sums and O are fp32;
- * the weights are rounded to bf16.  One pass over the cache serves H / Hkv * nq <= 16 rows of a
+ * the weights are off by at most 2^-17 of themselves.  One pass over the cache serves H / Hkv * nq <= 16 rows of a
  * map (8 at d = 128); it is HBM-bound.  A table of another width may change O and LSE by their
  * roundings.
  */
