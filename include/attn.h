@@ -499,7 +499,7 @@ attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cache, const vo
  *   axis        : const int32 [rot / 2], clamped to [0, axes); null: all pairs on axis 0
  *   strides     : host array of 12, in elements, multiples of 8: batch, token and head of q, of
  *                 q_out, of k and of k_out (the last six are not read when Hk = 0)
- *   d and rot multiples of 16, 16 <= rot <= d <= 256 (else ATTN_ERR_UNSUPPORTED);
+ *   d and rot multiples of 16, 16 <= rot <= d <= 256, axes <= 255 (else ATTN_ERR_UNSUPPORTED);
  *   B * N == 0 returns ATTN_OK
  * Alignment: tensors 16 bytes, positions, inv_freq and axis 4 bytes.  HBM-bound.
  */
