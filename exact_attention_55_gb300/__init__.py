@@ -51,7 +51,8 @@ __all__ = [
     "attn_status_string", "attn_get_device_status", "attn_selftest_wait_timeout",
     "attn_selftest_fwd_withheld_load", "attn_selftest_quant_withheld_load",
     "attn_selftest_bwd_withheld_load", "attn_selftest_decode_fp8_withheld_load",
-    "attn_selftest_fp8_convert", "EXPORTED_SYMBOLS",
+    "attn_selftest_diff_fwd_withheld_load", "attn_selftest_diff_bwd_withheld_load",
+    "attn_selftest_diff_decode_withheld_load", "attn_selftest_fp8_convert", "EXPORTED_SYMBOLS",
 ]
 
 ATTN_OK = 0
@@ -84,7 +85,9 @@ EXPORTED_SYMBOLS = (
     "attn_fwd_schedule", "attn_status_string", "attn_get_device_status",
     "attn_selftest_wait_timeout", "attn_selftest_fwd_withheld_load",
     "attn_selftest_quant_withheld_load", "attn_selftest_bwd_withheld_load",
-    "attn_selftest_decode_fp8_withheld_load", "attn_selftest_fp8_convert",
+    "attn_selftest_decode_fp8_withheld_load", "attn_selftest_diff_fwd_withheld_load",
+    "attn_selftest_diff_bwd_withheld_load", "attn_selftest_diff_decode_withheld_load",
+    "attn_selftest_fp8_convert",
 )
 
 _lock = threading.Lock()
@@ -196,6 +199,14 @@ def load_library(path: str | None = None):
         lib.attn_selftest_decode_fp8_withheld_load.argtypes = (
             [vp] * 9 + [i] * 10 + [vp, ctypes.c_size_t, i, u64, vp])
         lib.attn_selftest_decode_fp8_withheld_load.restype = i
+        lib.attn_selftest_diff_fwd_withheld_load.argtypes = [vp] * 6 + [i] * 7 + [u64, vp]
+        lib.attn_selftest_diff_fwd_withheld_load.restype = i
+        lib.attn_selftest_diff_bwd_withheld_load.argtypes = (
+            [vp] * 13 + [ctypes.c_size_t] + [i] * 7 + [u64, vp])
+        lib.attn_selftest_diff_bwd_withheld_load.restype = i
+        lib.attn_selftest_diff_decode_withheld_load.argtypes = (
+            [vp] * 8 + [i] * 8 + [vp, ctypes.c_size_t, i, u64, vp])
+        lib.attn_selftest_diff_decode_withheld_load.restype = i
         lib.attn_selftest_fp8_convert.argtypes = [ctypes.c_uint, ctypes.c_size_t, i, vp, vp]
         lib.attn_selftest_fp8_convert.restype = i
         _lib = lib
@@ -837,6 +848,47 @@ def attn_selftest_decode_fp8_withheld_load(q, k_cache, v_cache, k_scales, v_scal
         workspace.numel() * workspace.element_size(), int(withheld), int(timeout_ns),
         _stream_handle(stream))
     _raise_if(st, "attn_selftest_decode_fp8_withheld_load")
+
+
+def attn_selftest_diff_fwd_withheld_load(q, k, v, lam, o, lse, causal: bool = False,
+                                         withheld: int = 2, timeout_ns: int = 20_000_000,
+                                         stream=None) -> None:
+    """Run differential attention's forward kernel with ring load `withheld` of every CTA never
+    issued and every wait bounded by timeout_ns (it records ATTN_ERR_TIMEOUT)."""
+    B, H2, N, d = q.shape
+    st = load_library().attn_selftest_diff_fwd_withheld_load(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), o.data_ptr(), lse.data_ptr(), B,
+        H2 // 2, v.shape[1], N, d, int(bool(causal)), int(withheld), int(timeout_ns),
+        _stream_handle(stream))
+    _raise_if(st, "attn_selftest_diff_fwd_withheld_load")
+
+
+def attn_selftest_diff_bwd_withheld_load(q, k, v, lam, o, o2, dout, lse, dq, dk, dv, dlam, workspace,
+                                         causal: bool = False, withheld: int = 2,
+                                         timeout_ns: int = 20_000_000, stream=None) -> None:
+    """Run differential attention's backward kernels with ring load `withheld` of every CTA never
+    issued and every wait bounded by timeout_ns (they record ATTN_ERR_TIMEOUT)."""
+    B, H2, N, d = q.shape
+    st = load_library().attn_selftest_diff_bwd_withheld_load(
+        *(t.data_ptr() for t in (q, k, v, lam, o, o2, dout, lse, dq, dk, dv, dlam, workspace)),
+        workspace.numel() * workspace.element_size(), B, H2 // 2, v.shape[1], N, d,
+        int(bool(causal)), int(withheld), int(timeout_ns), _stream_handle(stream))
+    _raise_if(st, "attn_selftest_diff_bwd_withheld_load")
+
+
+def attn_selftest_diff_decode_withheld_load(q, k_cache, v_cache, lam, page_table, seq_lens, o, lse,
+                                            workspace, withheld: int = 1,
+                                            timeout_ns: int = 20_000_000, stream=None) -> None:
+    """Run differential attention's decoding step with load `withheld` of every CTA never issued and
+    every wait bounded by timeout_ns (it records ATTN_ERR_TIMEOUT)."""
+    B, H2, nq, d = q.shape
+    num_pages, heads, page_size, _ = k_cache.shape
+    st = load_library().attn_selftest_diff_decode_withheld_load(
+        *(t.data_ptr() for t in (q, k_cache, v_cache, lam, page_table, seq_lens, o, lse)), B, H2 // 2,
+        heads // 2, nq, d, page_size, num_pages, page_table.shape[1], workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), int(withheld), int(timeout_ns),
+        _stream_handle(stream))
+    _raise_if(st, "attn_selftest_diff_decode_withheld_load")
 
 
 def attn_selftest_fp8_convert(first: int, count: int, fmt="e4m3", codes=None, stream=None):

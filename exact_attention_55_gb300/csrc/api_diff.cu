@@ -375,3 +375,51 @@ extern "C" attn_status_t attn_diff_decode_bf16_paged(const void* q, const void* 
     return diff_decode(q, k_cache, v_cache, lam, page_table, seq_lens, o, lse, B, H, Hkv, nq, d, page_size, num_pages,
                        max_pages, scale, window, workspace, workspace_bytes, stream, kWaitTimeoutNs, 0);
 }
+
+// ------------------------------------------------------------------ abort paths
+// The production kernels with one load withheld and a short limit on every wait.
+static bool selftest_ok(int withheld, unsigned long long timeout_ns)
+{
+    return withheld >= 0 && withheld < 0x7ffffffe && timeout_ns > 0 && timeout_ns <= 2000000000ull;
+}
+
+extern "C" attn_status_t attn_selftest_diff_fwd_withheld_load(const void* q, const void* k, const void* v,
+                                                             const float* lam, void* o, float* lse, int B, int H,
+                                                             int Hkv, int N, int d, int causal, int withheld,
+                                                             unsigned long long timeout_ns, void* stream)
+{
+    if (!selftest_ok(withheld, timeout_ns) || B < 1 || N < 1) return ATTN_ERR_INVALID_ARG;
+    const attn_status_t st = diff_sizes(H, Hkv, d, 1.0f);
+    if (st != ATTN_OK) return st;
+    if (!q || !k || !v || !lam || !o || !lse) return ATTN_ERR_INVALID_ARG;
+    return diff_fwd(q, k, v, lam, o, lse, nullptr,
+                    {B, H, Hkv, N, d, nullptr, 0, -1, 1.0f / std::sqrt((float)d), causal, 0}, stream, timeout_ns,
+                    withheld + 1);
+}
+
+extern "C" attn_status_t attn_selftest_diff_bwd_withheld_load(
+    const void* q, const void* k, const void* v, const float* lam, const void* o, const void* o2, const void* dout,
+    const float* lse, void* dq, void* dk, void* dv, float* dlam, void* workspace, size_t workspace_bytes, int B, int H,
+    int Hkv, int N, int d, int causal, int withheld, unsigned long long timeout_ns, void* stream)
+{
+    if (!selftest_ok(withheld, timeout_ns) || B < 1 || N < 1) return ATTN_ERR_INVALID_ARG;
+    const attn_status_t st = diff_sizes(H, Hkv, d, 1.0f);
+    if (st != ATTN_OK) return st;
+    if (!q || !k || !v || !lam || !o || !o2 || !dout || !lse || !dq || !dk || !dv || !dlam || !workspace ||
+        workspace_bytes < attn_diff_bwd_workspace_bytes(B, H, N))
+        return ATTN_ERR_INVALID_ARG;
+    return diff_bwd(q, k, v, lam, o, o2, dout, lse, dq, dk, dv, dlam, workspace,
+                    {B, H, Hkv, N, d, nullptr, 0, -1, 1.0f / std::sqrt((float)d), causal, 0}, stream, timeout_ns,
+                    withheld + 1);
+}
+
+extern "C" attn_status_t attn_selftest_diff_decode_withheld_load(
+    const void* q, const void* k_cache, const void* v_cache, const float* lam, const int* page_table,
+    const int* seq_lens, void* o, float* lse, int B, int H, int Hkv, int nq, int d, int page_size, int num_pages,
+    int max_pages, void* workspace, size_t workspace_bytes, int withheld, unsigned long long timeout_ns, void* stream)
+{
+    if (!selftest_ok(withheld, timeout_ns) || d < 1) return ATTN_ERR_INVALID_ARG;
+    return diff_decode(q, k_cache, v_cache, lam, page_table, seq_lens, o, lse, B, H, Hkv, nq, d, page_size, num_pages,
+                       max_pages, 1.0f / std::sqrt((float)d), 0, workspace, workspace_bytes, stream, timeout_ns,
+                       withheld + 1);
+}

@@ -674,6 +674,29 @@ attn_status_t attn_selftest_decode_fp8_withheld_load(
     unsigned long long timeout_ns, void* stream);
 
 /*
+ * attn_selftest_diff_fwd_withheld_load, attn_selftest_diff_bwd_withheld_load,
+ * attn_selftest_diff_decode_withheld_load -- the same diagnostics for the kernels of
+ * attn_diff_fwd_bf16, attn_diff_bwd_bf16 and attn_diff_decode_bf16_paged (scale 1/sqrt(d), no
+ * window): in every CTA (of each of the backward's passes) load `withheld` of its ring is never
+ * issued.
+ */
+attn_status_t attn_selftest_diff_fwd_withheld_load(const void* q, const void* k, const void* v,
+                                                   const float* lam, void* o, float* lse, int B,
+                                                   int H, int Hkv, int N, int d, int causal,
+                                                   int withheld, unsigned long long timeout_ns,
+                                                   void* stream);
+attn_status_t attn_selftest_diff_bwd_withheld_load(
+    const void* q, const void* k, const void* v, const float* lam, const void* o, const void* o2,
+    const void* dout, const float* lse, void* dq, void* dk, void* dv, float* dlam, void* workspace,
+    size_t workspace_bytes, int B, int H, int Hkv, int N, int d, int causal, int withheld,
+    unsigned long long timeout_ns, void* stream);
+attn_status_t attn_selftest_diff_decode_withheld_load(
+    const void* q, const void* k_cache, const void* v_cache, const float* lam,
+    const int* page_table, const int* seq_lens, void* o, float* lse, int B, int H, int Hkv, int nq,
+    int d, int page_size, int num_pages, int max_pages, void* workspace, size_t workspace_bytes,
+    int withheld, unsigned long long timeout_ns, void* stream);
+
+/*
  * attn_selftest_fp8_convert -- diagnostic: the device's FP8 conversion (the one the
  * quantisers use: round to nearest even, saturating to the format's largest finite
  * value) applied to the fp32 bit patterns first .. first + count - 1, so that a test
