@@ -450,8 +450,8 @@ def attn_decode_bf16_paged_noalloc(q, k_cache, v_cache, page_table, seq_lens,
 
 def _native():
     """The native binding of the paged-cache calls, of rotary positions and of differential
-    attention (checks, outputs and the C call in one step), loaded by the first of them: it is built against the installed PyTorch, which the other
-    calls do not depend on."""
+    attention (checks, outputs and the C call in one step), loaded by the first of them: it is
+    built against the installed PyTorch, which the other calls do not depend on."""
     global _binding
     if _binding is None:
         lib = load_library()

@@ -22,6 +22,9 @@ extern "C" attn_status_t attn_rope_bf16(const void* q, const void* k, void* q_ou
     if (B < 0 || N < 0 || Hq < 1 || Hk < 0 || axes < 1 || !strides) return ATTN_ERR_INVALID_ARG;
     if (d < 16 || d > 256 || d % 16 != 0 || rot < 16 || rot > d || rot % 16 != 0) return ATTN_ERR_UNSUPPORTED;
     if ((long long)B * N > 0x7fffffffLL || Hq > 65535 || Hk > 65535 || axes > 255) return ATTN_ERR_UNSUPPORTED;
+    // the threads of the longest launch (rope.cu), eight heads each, stay in 32 bits
+    const int heads = Hq + Hk, each = heads < 8 ? heads : 8;
+    if (((long long)B * N * ((heads + each - 1) / each) * (d / 16)) > 0xffffff00LL) return ATTN_ERR_UNSUPPORTED;
     if (B == 0 || N == 0) return ATTN_OK;
     if (!q || !q_out || !positions || !inv_freq || (Hk > 0 && (!k || !k_out))) return ATTN_ERR_INVALID_ARG;
     const int tensors = Hk > 0 ? 4 : 2;      // q, q_out, k, k_out

@@ -37,7 +37,7 @@ struct DiffFwdCfg {
     static constexpr int Q_BYTES = 2 * (D / 64) * CB;    // both maps' queries
     static constexpr int SLOT = 2 * CB;                  // 32 KB: both maps' keys (d 64) or one's, or V
     static constexpr int KSLOTS = D / 64;                // ring slots of a step's keys
-    static constexpr int BAR_BYTES = 4096;
+    static constexpr int BAR_BYTES = 5120;
     static constexpr int SMEM_CAP = 227 * 1024;
     static constexpr int NSLOT = (SMEM_CAP - BAR_BYTES - 1024 - Q_BYTES) / SLOT;
     static constexpr int SMEM_BYTES = 1024 + Q_BYTES + NSLOT * SLOT + BAR_BYTES;
@@ -61,11 +61,12 @@ struct alignas(16) DiffFwdBars {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
-    float inv[2][128];       // 1 / sum of the maps' rows
+    float inv[2][2][128];    // 1 / sum of the maps' rows, by the parity of the unit: one map's warps may be a
+                             // unit ahead of the other's
 };
-constexpr int kDiffTabOffset = 2048;
+constexpr int kDiffTabOffset = 3072;
 static_assert(sizeof(DiffFwdBars) <= kDiffTabOffset, "barrier block");
-static_assert(kDiffTabOffset + sizeof(SortTab) <= 4096, "schedule table");
+static_assert(kDiffTabOffset + sizeof(SortTab) <= 5120, "schedule table");
 
 // Where a unit's rows live.
 struct DiffAt {
@@ -458,14 +459,14 @@ __global__ void __launch_bounds__(DiffFwdCfg<D, PK>::NUM_THREADS, 1)
             if (!ok) break;
             // ---- the maps' sums change hands, then each warpgroup writes 64 columns of the difference
             const DiffAt at = diff_at<C>(dp, w);
-            bars->inv[grp][row_in_tile] = l > 0.0f ? 1.0f / l : 0.0f;
+            bars->inv[uc & 1][grp][row_in_tile] = l > 0.0f ? 1.0f / l : 0.0f;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->sums_full));
             if (!wait_all(&bars->sums_full, uc & 1)) break;
             if (!wait_all(&bars->pv_done[0], uc & 1)) break;
             if (!wait_all(&bars->pv_done[1], uc & 1)) break;
             tc_fence_after_sync();
-            const float inv1 = bars->inv[0][row_in_tile], inv2 = bars->inv[1][row_in_tile];
+            const float inv1 = bars->inv[uc & 1][0][row_in_tile], inv2 = bars->inv[uc & 1][1][row_in_tile];
             const float lam = __ldg(dp.lam + at.h);
             const size_t orow = at.out_row + (size_t)row * at.out_step;
             const size_t ocol = orow * (2 * D) + at.part * C::DV + grp * 64;

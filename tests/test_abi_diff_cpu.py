@@ -29,7 +29,7 @@ def changed(args, change):
     ({0: 0}, 1), ({2: 0}, 1), ({4: 0}, 1), ({5: 0}, 1), ({1: 0}, 1), ({3: 0}, 1),
     ({10: 0}, 1), ({11: -1}, 1), ({14: 0}, 1), ({8: -1}, 1),
     ({12: 72}, 2), ({12: 272}, 2), ({13: 24}, 2), ({13: 80}, 2), ({13: 0}, 2), ({14: 256}, 2),
-    ({8: 70000, 9: 70000}, 2),
+    ({8: 70000, 9: 70000}, 2), ({9: 1 << 28, 10: 1, 11: 0, 12: 256}, 2),
     ({0: P + 8}, 3), ({3: P + 2}, 3), ({4: P + 2}, 3), ({5: P + 1}, 3), ({6: P + 2}, 3),
 ])
 def test_rope_arguments(lib, change, expected):

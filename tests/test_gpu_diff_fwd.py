@@ -140,6 +140,22 @@ def test_more_sequences_than_the_table():
             ref.check(o[s].transpose(0, 1), want["o"], want["o_bound"], "o")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_units_of_one_step(d):
+    """Several units a CTA with a single step each, where the two maps' warps are furthest apart: the same bits
+    however the units fall on the CTAs."""
+    m = fa()
+    B, H, N = 96, 8, 100
+    q, k, v = make((B, 2 * H, N, d), 20).cuda(), make((B, 2 * H, N, d), 21).cuda(), make((B, H, N, 2 * d), 22).cuda()
+    lam = weights(H).cuda()
+    o, lse, _ = m.attn_diff_fwd_bf16(q, k, v, lam, causal=True)
+    for b in range(0, B, 19):
+        one = slice(b, b + 1)
+        o1, lse1, _ = m.attn_diff_fwd_bf16(q[one], k[one], v[one], lam, causal=True)
+        assert torch.equal(o[one], o1) and torch.equal(lse[one], lse1)
+    compare(m, q[:1].cpu(), k[:1].cpu(), v[:1].cpu(), lam.cpu(), True, 0, None)
+
+
 def test_window_wider_than_the_sequence():
     m = fa()
     q, k, v = (make(s, i).cuda() for i, s in enumerate([(1, 2, 200, 64), (1, 2, 200, 64), (1, 1, 200, 128)]))
