@@ -45,6 +45,7 @@ UNITS = [
     ("diff_bwd", "diff_bwd.cu", []),
     ("diff_decode", "diff_decode.cu", []),
     ("diff_fwd", "diff_fwd.cu", []),
+    ("diff_fwd_wide", "diff_fwd_wide.cu", []),
     ("rope", "rope.cu", []),
     ("api_diff", "api_diff.cu", []),
     ("fwd_bf16_d64", "attn_fwd_inst.cu", ["-DGB300_ATTN_D=64", "-DGB300_ATTN_F8=0"]),

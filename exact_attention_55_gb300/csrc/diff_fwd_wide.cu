@@ -1,0 +1,688 @@
+// diff_fwd_wide.cu -- forward pass of differential attention at d = 128 in two launches: the rows'
+// log-sum-exps, then one product with both maps' weights.
+//
+//     L_m = log sum exp(scale Q_m K_m^T + mask),   O = (exp(S_1 - L_1) - lam exp(S_2 - L_2)) V
+//
+// A value head of 256 columns leaves no room in TMEM for the two accumulators of diff_fwd.cu, which
+// therefore takes each half of it with scores of its own: 16 d products per pair of tokens (two scores of
+// 2 d and two products of 2 d for each half).  With the L_m known the maps' weights are subtracted before the
+// product, and one accumulator of 256 columns takes it: 4 d products for the L_m, 4 d for the scores
+// again, 4 d for O: 12 d, with as many exponentials, and no rescaling in the second launch.
+// Measured, 16 heads over 4 key pairs, 16384 tokens, causal: 3020 us in one launch, 2435 in two.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "attn_fwd.cuh"
+#include "diff_params.h"
+
+namespace gb300 {
+
+// ------------------------------------------------------------------ log-sum-exps
+// A unit is 256 query rows of one map, as two tiles with a warpgroup each that share the stream of key tiles; each
+// tile's scores have two TMEM buffers.
+template <bool PK>
+struct DiffLseCfg {
+    static constexpr bool PACKED = PK;
+    static constexpr int BM = 128, NQ = 2, BN = 128, D = 128;
+    static constexpr int CB = 128 * 128;                 // 64 columns of a 128-row tile
+    static constexpr int TILE = 2 * CB;
+    static constexpr int NSLOT = 4;
+    static constexpr int TAB_OFF = 256, BAR_BYTES = 2048 + 256;
+    static constexpr int SMEM_BYTES = 1024 + (NQ + NSLOT) * TILE + BAR_BYTES;
+    static constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, NUM_THREADS = 384;
+    static constexpr int REG_SOFTMAX = 208, REG_CONTROL = 88;
+    static constexpr int REG_POOL = 256 * REG_SOFTMAX + 128 * REG_CONTROL;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    static_assert(TAB_OFF + sizeof(SortTab) <= BAR_BYTES, "schedule table");
+};
+
+struct alignas(16) DiffLseBars {
+    uint64_t q_full, q_empty;
+    uint64_t k_full[4], k_empty[4];
+    uint64_t s_full[2][2], s_free[2][2];                 // tile, buffer
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(DiffLseBars) <= 256, "barrier block");
+
+// Keys [lo, hi] that row r may use; both grow with r.
+__device__ __forceinline__ void diff_key_bounds(const FwdParams& p, int N, int r, int& lo, int& hi)
+{
+    lo = 0;
+    hi = N - 1;
+    if (p.causal) hi = min(hi, r);
+    if (p.window > 0) {
+        lo = r - p.window;
+        if (!p.causal) hi = min(hi, r + p.window);
+    }
+}
+
+// Some row of [a, a + 128) may not use some key of [c0, c0 + 128).
+__device__ __forceinline__ bool diff_edge(const FwdParams& p, int N, int a, int c0)
+{
+    return (c0 + 128 > N) || (p.causal && c0 + 127 > a) ||
+           (p.window > 0 && (c0 < a + 127 - p.window || (!p.causal && c0 + 127 > a + p.window)));
+}
+
+template <bool PK>
+__global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
+    diff_lse_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const DiffFwdParams dp)
+{
+    using C = DiffLseCfg<PK>;
+    constexpr int D = C::D;
+    const FwdParams& p = dp.f;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* ring_smem = q_smem + C::NQ * C::TILE;
+    DiffLseBars* bars = reinterpret_cast<DiffLseBars*>(ring_smem + C::NSLOT * C::TILE);
+    const volatile int* abort_flag = &bars->abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const SortTab* tab = nullptr;
+    if constexpr (C::PACKED) {
+        if (p.num_seqs <= kSortMaxSeqs) {
+            SortTab* t = reinterpret_cast<SortTab*>(reinterpret_cast<uint8_t*>(bars) + C::TAB_OFF);
+            build_sort_tab<C::NQ * C::BM>(p.cu_seqlens, p.num_seqs, p.T, p.H, t);
+            tab = t;
+        }
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bars->q_full), 1);
+        mbar_init(smem_u32(&bars->q_empty), 1);
+        for (int s = 0; s < C::NSLOT; ++s) {
+            mbar_init(smem_u32(&bars->k_full[s]), 1);
+            mbar_init(smem_u32(&bars->k_empty[s]), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_u32(&bars->s_full[i >> 1][i & 1]), 1);
+            mbar_init(smem_u32(&bars->s_free[i >> 1][i & 1]), 4);
+        }
+        mbar_init(smem_u32(&bars->drain), 1);
+        bars->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::MMA_WARP) {
+        tmem_alloc(smem_u32(&bars->tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = bars->tmem_base;
+    auto timed_out = [&]() {
+        atomicExch(p.status, kStatusTimeout);
+        *reinterpret_cast<volatile int*>(&bars->abort_flag) = 1;
+    };
+    // all lanes try once, which is the usual case; else they poll until the limit
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const uint32_t a = smem_u32(bar);
+        if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+        return __all_sync(0xffffffffu, mbar_wait(a, parity, abort_flag, p.timeout_ns));
+    };
+
+    if (warp == C::PRODUCER_WARP) {
+        regs_decrease<C::REG_CONTROL>();
+        if (lane == 0) {
+            const uint64_t pol_q = l2_policy_evict_first(), pol_k = l2_policy_evict_last();
+            uint32_t ring = 0, uc = 0;
+            bool ok = true;
+            for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
+                Unit w;
+                if (!unit_of<C>(su, p, w, tab)) continue;
+                if (!mbar_wait(smem_u32(&bars->q_empty), (uc & 1) ^ 1, abort_flag, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t qb = smem_u32(&bars->q_full);
+                mbar_arrive_expect_tx(qb, C::NQ * C::TILE);
+#pragma unroll
+                for (int i = 0; i < 2 * C::NQ; ++i)
+                    tma_load_3d(smem_u32(q_smem + i * C::CB), &tmQ, qb, (i & 1) * 64, w.y0 + w.q0 + (i >> 1) * C::BM, w.z,
+                                pol_q);
+                ++uc;
+                // map z = 2 h + m (behind 2 H b) reads the keys 2 (h / G) + m (behind 2 Hkv b)
+                const int G = dp.H / dp.Hkv, b = C::PACKED ? 0 : w.z / (2 * dp.H), zz = w.z - b * 2 * dp.H;
+                const int zk = 2 * (b * dp.Hkv + (zz >> 1) / G) + (zz & 1);
+                for (int jj = 0; jj < w.n; ++jj) {
+                    const uint32_t slot = ring % C::NSLOT;
+                    if (!mbar_wait(smem_u32(&bars->k_empty[slot]), ((ring / C::NSLOT) & 1) ^ 1, abort_flag, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (++ring == (uint32_t)p.withhold_kv) continue;      // test hook: never arrives
+                    const uint32_t fb = smem_u32(&bars->k_full[slot]);
+                    mbar_arrive_expect_tx(fb, C::TILE);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        tma_load_3d(smem_u32(ring_smem + slot * C::TILE + c * C::CB), &tmK, fb, c * 64,
+                                    w.y0 + (w.t0 + jj) * C::BN, zk, pol_k);
+                }
+            }
+            if (!ok) timed_out();
+            // every copy issued lands before shared memory is released
+            for (uint32_t k = ring < C::NSLOT ? 0 : ring - C::NSLOT; k < ring; ++k)
+                if (k + 1 != (uint32_t)p.withhold_kv)
+                    mbar_wait(smem_u32(&bars->k_full[k % C::NSLOT]), (k / C::NSLOT) & 1, nullptr, kCleanupTimeoutNs);
+            if (uc > 0) mbar_wait(smem_u32(&bars->q_full), (uc - 1) & 1, nullptr, kCleanupTimeoutNs);
+        }
+    } else if (warp == C::MMA_WARP) {
+        regs_decrease<C::REG_CONTROL>();
+        constexpr uint32_t idesc = idesc_f32acc(1, 0, C::BM, C::BN);
+        const uint64_t q_desc = sdesc_sw128(smem_u32(q_smem), 16, 1024), k_desc = sdesc_sw128(smem_u32(ring_smem), 16, 1024);
+        uint32_t ring = 0, uc = 0, count[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+            ok = ok && warp_wait(bar, parity);
+            return ok;
+        };
+        for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
+            Unit w;
+            if (!unit_of<C>(su, p, w, tab)) continue;
+            int L[2], R[2];
+            tile_steps<C>(w, 0, p, L[0], R[0]);
+            tile_steps<C>(w, 1, p, L[1], R[1]);
+            if (!wait(&bars->q_full, uc & 1)) break;
+            for (int jj = 0; jj < w.n && ok; ++jj, ++ring) {
+                const uint32_t slot = ring % C::NSLOT;
+                if (!wait(&bars->k_full[slot], (ring / C::NSLOT) & 1)) break;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (jj < L[i] || jj >= R[i]) continue;
+                    const uint32_t n = count[i]++, b = n & 1;
+                    if (!wait(&bars->s_free[i][b], ((n >> 1) & 1) ^ 1)) break;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk / 4) * C::CB + (kk % 4) * 32) >> 4;
+                        mma_ss_warp<false>(tmem + (2 * i + b) * C::BN, q_desc + ((i * C::TILE) >> 4) + off,
+                                           k_desc + ((slot * C::TILE) >> 4) + off, idesc, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit_warp(smem_u32(&bars->s_full[i][b]));
+                }
+                if (!ok) break;
+                mma_commit_warp(smem_u32(&bars->k_empty[slot]));
+            }
+            if (!ok) break;
+            mma_commit_warp(smem_u32(&bars->q_empty));
+            ++uc;
+        }
+        if (!ok && lane == 0) timed_out();
+        mma_commit_warp(smem_u32(&bars->drain));
+        mbar_wait(smem_u32(&bars->drain), 0, nullptr, kCleanupTimeoutNs);
+        __syncwarp();
+    } else if (warp < 8) {
+        regs_increase<C::REG_SOFTMAX>();
+        const int grp = warp >> 2, wq = warp & 3;
+        const uint32_t lane_addr = (uint32_t)(wq * 32) << 16;
+        const float NEG_INF = -__int_as_float(0x7f800000), c = p.c_log2;
+        uint32_t count = 0;
+        bool ok = true;
+        for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
+            Unit w;
+            if (!unit_of<C>(su, p, w, tab)) continue;
+            int L, R;
+            tile_steps<C>(w, grp, p, L, R);
+            const int a = w.q0 + grp * C::BM, row = a + wq * 32 + lane;
+            int jlo, jhi;
+            diff_key_bounds(p, w.N, row, jlo, jhi);
+            // a row behind the sequence sees what the last one sees, and stores nothing
+            if (jlo > jhi) jlo = jhi;
+            const uint32_t span = (uint32_t)(jhi - jlo);
+            float m_used = NEG_INF;
+            float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            for (int jj = L; jj < R; ++jj) {
+                const int c0 = (w.t0 + jj) * C::BN;
+                const uint32_t b = count & 1;
+                ok = warp_wait(&bars->s_full[grp][b], (count >> 1) & 1);
+                ++count;
+                if (!ok) break;
+                tc_fence_after_sync();
+                uint32_t sr[C::BN];
+#pragma unroll
+                for (int ch = 0; ch < C::BN / 32; ++ch) tmem_ld32p(tmem + lane_addr + (2 * grp + b) * C::BN + ch * 32, sr + ch * 32);
+                tmem_wait_ld_only();
+#pragma unroll
+                for (int ch = 0; ch < C::BN / 32; ++ch) reg_fence32(sr + ch * 32);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[grp][b]));
+                float* s = reinterpret_cast<float*>(sr);
+                if (diff_edge(p, w.N, a, c0)) {
+                    const uint32_t base = (uint32_t)(c0 - jlo);
+#pragma unroll
+                    for (int e = 0; e < C::BN; ++e)
+                        if (base + (uint32_t)e > span) s[e] = NEG_INF;
+                }
+                float mx[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float m = s[k];
+#pragma unroll
+                    for (int u = 1; u + 1 < C::BN / 8; u += 2) m = fmax3(m, s[k + 8 * u], s[k + 8 * u + 8]);
+                    mx[k] = fmaxf(m, s[k + 8 * (C::BN / 8 - 1)]);
+                }
+                const float m_cand =
+                    fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * c;
+                if (m_cand > m_used) {                    // exact: a thread's own sums are all there is to rescale
+                    const float alpha = ex2(m_used - m_cand);    // ex2(-inf) = 0
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[k] = __fmul2_rn(acc[k], make_float2(alpha, alpha));
+                    m_used = m_cand;
+                }
+                const float mb = m_used == NEG_INF ? 0.0f : m_used;
+                const float2 c2 = make_float2(c, c), b2 = make_float2(-mb, -mb);
+#pragma unroll
+                for (int e = 0; e < C::BN / 2; ++e) {
+                    const float2 x = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), c2, b2);
+                    acc[e & 3] = __fadd2_rn(acc[e & 3], make_float2(ex2(x.x), ex2(x.y)));
+                }
+            }
+            if (!ok) break;
+            const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+            const float l = (a01.x + a01.y) + (a23.x + a23.y);
+            if (row < w.N) {
+                const size_t at = C::PACKED ? (size_t)w.z * p.T + w.y0 : (size_t)w.z * p.N;
+                p.lse[at + row] = (l > 0.0f ? m_used + __log2f(l) : NEG_INF) * 0.69314718055994531f;
+            }
+        }
+        if (!ok) timed_out();
+    } else {
+        regs_decrease<C::REG_CONTROL>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == C::MMA_WARP) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ the output
+// A unit is 128 query rows of a head.  A step's scores of both maps (128 keys) fill 256 TMEM columns,
+// which the compute warps load at once and give back; they take half of the keys of both maps each and put the
+// difference of the weights, rounded once, into shared memory.  The MMA warp issues the next step's scores
+// before the product with it, so the tensor pipe works on both while the weights are made.  K and V stream
+// through one ring in pieces of 16 KB (64 columns of a map's keys; 32 keys of V), each given back as soon as
+// its products are done: it holds one step.
+template <bool PK>
+struct DiffOutCfg {
+    static constexpr bool PACKED = PK;
+    static constexpr int BM = 128, NQ = 1, BN = 128, D = 128;
+    static constexpr int CB = 128 * 128;
+    static constexpr int Q_BYTES = 4 * CB, W_BYTES = 2 * CB, NSLOT = 8;
+    static constexpr int V_KEYS = 32, V_CB = V_KEYS * 128;          // keys of a piece of V, bytes of 64 of its columns
+    static constexpr int TAB_OFF = 384, BAR_BYTES = 384 + 1792;
+    static constexpr int SMEM_BYTES = Q_BYTES + W_BYTES + NSLOT * CB + BAR_BYTES;   // no room for alignment
+    static constexpr int O_COL = 256;
+    static constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, NUM_THREADS = 384;
+    static constexpr int REG_COMPUTE = 208, REG_CONTROL = 88;
+    static constexpr int REG_POOL = 256 * REG_COMPUTE + 128 * REG_CONTROL;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    static_assert(TAB_OFF + sizeof(SortTab) <= BAR_BYTES, "schedule table");
+};
+
+struct alignas(16) DiffOutBars {
+    uint64_t q_full, q_empty;
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t s_full, s_free, w_full, w_free, o_full, o_empty;
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(DiffOutBars) <= 384, "barrier block");
+
+template <bool PK>
+__global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
+    diff_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const DiffFwdParams dp)
+{
+    using C = DiffOutCfg<PK>;
+    const FwdParams& p = dp.f;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* q_smem = smem;
+    uint8_t* w_smem = smem + C::Q_BYTES;
+    uint8_t* ring_smem = w_smem + C::W_BYTES;
+    DiffOutBars* bars = reinterpret_cast<DiffOutBars*>(ring_smem + C::NSLOT * C::CB);
+    const volatile int* abort_flag = &bars->abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((smem_u32(smem) & 1023) != 0) {                    // no kernel of this file has static shared memory
+        if (threadIdx.x == 0) atomicExch(p.status, kStatusTimeout);
+        return;
+    }
+
+    const SortTab* tab = nullptr;
+    if constexpr (C::PACKED) {
+        if (p.num_seqs <= kSortMaxSeqs) {
+            SortTab* t = reinterpret_cast<SortTab*>(reinterpret_cast<uint8_t*>(bars) + C::TAB_OFF);
+            build_sort_tab<C::BM>(p.cu_seqlens, p.num_seqs, p.T, p.H, t);
+            tab = t;
+        }
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bars->q_full), 1);
+        mbar_init(smem_u32(&bars->q_empty), 1);
+        for (int s = 0; s < C::NSLOT; ++s) {
+            mbar_init(smem_u32(&bars->kv_full[s]), 1);
+            mbar_init(smem_u32(&bars->kv_empty[s]), 1);
+        }
+        mbar_init(smem_u32(&bars->s_full), 1);
+        mbar_init(smem_u32(&bars->s_free), 8);
+        mbar_init(smem_u32(&bars->w_full), 8);
+        mbar_init(smem_u32(&bars->w_free), 1);
+        mbar_init(smem_u32(&bars->o_full), 1);
+        mbar_init(smem_u32(&bars->o_empty), 8);
+        mbar_init(smem_u32(&bars->drain), 1);
+        bars->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::MMA_WARP) {
+        tmem_alloc(smem_u32(&bars->tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = bars->tmem_base;
+    const int G = dp.H / dp.Hkv;
+    auto timed_out = [&]() {
+        atomicExch(p.status, kStatusTimeout);
+        *reinterpret_cast<volatile int*>(&bars->abort_flag) = 1;
+    };
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const uint32_t a = smem_u32(bar);
+        if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+        return __all_sync(0xffffffffu, mbar_wait(a, parity, abort_flag, p.timeout_ns));
+    };
+
+    if (warp == C::PRODUCER_WARP) {
+        regs_decrease<C::REG_CONTROL>();
+        if (lane == 0) {
+            const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
+            uint32_t ring = 0, uc = 0;
+            bool ok = true;
+            // the next slot, free and armed; false: stop, or (withheld) not armed
+            auto ready = [&](uint32_t& slot) -> bool {
+                slot = ring % C::NSLOT;
+                if (!ok) return false;
+                if (!mbar_wait(smem_u32(&bars->kv_empty[slot]), ((ring / C::NSLOT) & 1) ^ 1, abort_flag, p.timeout_ns)) {
+                    ok = false;
+                    return false;
+                }
+                if (++ring == (uint32_t)p.withhold_kv) return false;      // test hook: never arrives
+                mbar_arrive_expect_tx(smem_u32(&bars->kv_full[slot]), C::CB);
+                return true;
+            };
+            for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
+                Unit w;
+                if (!unit_of<C>(su, p, w, tab)) continue;
+                // heads of q (map 1), of V, of k (map 1)
+                const int b = C::PACKED ? 0 : w.z / dp.H, zv = b * dp.Hkv + (w.z - b * dp.H) / G, zk = 2 * zv;
+                if (!mbar_wait(smem_u32(&bars->q_empty), (uc & 1) ^ 1, abort_flag, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t qb = smem_u32(&bars->q_full);
+                mbar_arrive_expect_tx(qb, C::Q_BYTES);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tma_load_3d(smem_u32(q_smem + i * C::CB), &tmQ, qb, (i & 1) * 64, w.y0 + w.q0, 2 * w.z + (i >> 1), pol_q);
+                ++uc;
+                // in the order of their use: K of a step before V of the step before
+                for (int x = -1; x < w.n && ok; ++x) {
+                    uint32_t slot;
+                    if (x + 1 < w.n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (ready(slot))
+                                tma_load_3d(smem_u32(ring_smem + slot * C::CB), &tmK, smem_u32(&bars->kv_full[slot]),
+                                            (i & 1) * 64, w.y0 + (w.t0 + x + 1) * C::BN, zk + (i >> 1), pol_kv);
+                    if (x >= 0)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (ready(slot))
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    tma_load_3d(smem_u32(ring_smem + slot * C::CB + c * C::V_CB), &tmV,
+                                                smem_u32(&bars->kv_full[slot]), c * 64,
+                                                w.y0 + (w.t0 + x) * C::BN + i * C::V_KEYS, zv, pol_kv);
+                }
+            }
+            if (!ok) timed_out();
+            // every copy issued lands before shared memory is released
+            for (uint32_t k = ring < C::NSLOT ? 0 : ring - C::NSLOT; k < ring; ++k)
+                if (k + 1 != (uint32_t)p.withhold_kv)
+                    mbar_wait(smem_u32(&bars->kv_full[k % C::NSLOT]), (k / C::NSLOT) & 1, nullptr, kCleanupTimeoutNs);
+            if (uc > 0) mbar_wait(smem_u32(&bars->q_full), (uc - 1) & 1, nullptr, kCleanupTimeoutNs);
+        }
+    } else if (warp == C::MMA_WARP) {
+        regs_decrease<C::REG_CONTROL>();
+        constexpr uint32_t idesc_s = idesc_f32acc(1, 0, C::BM, C::BN), idesc_o = idesc_f32acc(1, 1, C::BM, 2 * C::D);
+        const uint64_t q_desc = sdesc_sw128(smem_u32(q_smem), 16, 1024), w_desc = sdesc_sw128(smem_u32(w_smem), 16, 1024);
+        const uint64_t k_desc = sdesc_sw128(smem_u32(ring_smem), 16, 1024);
+        const uint64_t v_desc = sdesc_sw128(smem_u32(ring_smem), C::V_CB, 1024);
+        uint32_t ring = 0, uc = 0, scores = 0, products = 0;       // steps whose S and whose product were issued
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+            ok = ok && warp_wait(bar, parity);
+            return ok;
+        };
+        auto commit = [&](uint64_t* bar) { mma_commit_warp(smem_u32(bar)); };
+        auto full = [&](uint32_t n) -> bool { return wait(&bars->kv_full[n % C::NSLOT], (n / C::NSLOT) & 1); };
+        auto issue_s = [&]() -> bool {
+            if (scores > 0 && !wait(&bars->s_free, (scores - 1) & 1)) return false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i, ++ring) {
+                const uint32_t slot = ring % C::NSLOT;
+                if (!full(ring)) return false;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ss_warp<false>(tmem + (i >> 1) * C::BN, q_desc + ((i * C::CB + kk * 32) >> 4),
+                                       k_desc + ((slot * C::CB + kk * 32) >> 4), idesc_s, (i & 1) || kk > 0 ? 1u : 0u);
+                commit(&bars->kv_empty[slot]);
+            }
+            commit(&bars->s_full);
+            ++scores;
+            return true;
+        };
+        // packed rows behind the sequence become 0: a weight of 0 times a NaN would be one
+        auto clear_tail = [&](int live, uint8_t* v) {
+            if constexpr (C::PACKED) {
+                if (live >= C::V_KEYS) return;
+                for (int o = max(live, 0) * 128 + lane * 16; o < C::V_CB; o += 512)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(v + c * C::V_CB + o) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+        };
+        auto issue_product = [&](const Unit& w, int x) -> bool {
+            if (x == 0 && !wait(&bars->o_empty, (uc & 1) ^ 1)) return false;
+            if (!wait(&bars->w_full, products & 1)) return false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i, ++ring) {
+                const uint32_t slot = ring % C::NSLOT;
+                if (!full(ring)) return false;
+                clear_tail(w.N - (w.t0 + x) * C::BN - i * C::V_KEYS, ring_smem + slot * C::CB);
+                tc_fence_after_sync();
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                    mma_ss_warp<false>(tmem + C::O_COL, w_desc + (((i >> 1) * C::CB + (i & 1) * 64 + kk * 32) >> 4),
+                                       v_desc + ((slot * C::CB + kk * 16 * 128) >> 4), idesc_o,
+                                       x > 0 || i > 0 || kk > 0 ? 1u : 0u);
+                commit(&bars->kv_empty[slot]);
+            }
+            commit(&bars->w_free);
+            ++products;
+            return true;
+        };
+        for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
+            Unit w;
+            if (!unit_of<C>(su, p, w, tab)) continue;
+            if (!wait(&bars->q_full, uc & 1)) break;
+            if (!issue_s()) break;
+            for (int x = 0; x < w.n; ++x) {
+                if (x + 1 < w.n && !issue_s()) break;
+                if (x + 2 == w.n || w.n == 1) commit(&bars->q_empty);     // behind the unit's last scores
+                if (!issue_product(w, x)) break;
+            }
+            if (!ok) break;
+            commit(&bars->o_full);
+            ++uc;
+        }
+        if (!ok && lane == 0) timed_out();
+        commit(&bars->drain);
+        mbar_wait(smem_u32(&bars->drain), 0, nullptr, kCleanupTimeoutNs);
+        __syncwarp();
+    } else if (warp < 8) {
+        // both warpgroups work on every step, warpgroup wg on its half of the keys, a thread one row
+        regs_increase<C::REG_COMPUTE>();
+        constexpr int HC = C::BN / 2;
+        constexpr float LOG2E = 1.4426950408889634f;
+        const int wg = warp >> 2, trow = (warp & 3) * 32 + lane;
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const float NEG_INF = -__int_as_float(0x7f800000);
+        const float2 c2 = make_float2(p.c_log2, p.c_log2);
+        uint8_t* w_row = w_smem + wg * C::CB + trow * 128;
+        uint32_t h = 0, uc = 0;
+        bool ok = true;
+        auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+            ok = ok && warp_wait(bar, parity);
+            return ok;
+        };
+        for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
+            Unit w;
+            if (!unit_of<C>(su, p, w, tab)) continue;
+            const int row = w.q0 + trow, head = C::PACKED ? w.z : w.z % dp.H;
+            const bool valid = row < w.N;
+            int jlo, jhi;
+            diff_key_bounds(p, w.N, row, jlo, jhi);
+            if (jlo > jhi) jlo = jhi;                     // a row behind the sequence, which is not stored
+            const uint32_t span = (uint32_t)(jhi - jlo);
+            // minus the LSE of both maps (log2 units); a row whose every score is -inf has weights 0
+            float2 l1 = make_float2(0.0f, 0.0f), l2 = l1;
+            {
+                const size_t at = (C::PACKED ? (size_t)(2 * w.z) * p.T + w.y0 : (size_t)(2 * w.z) * p.N) + (valid ? row : 0);
+                const size_t step = C::PACKED ? (size_t)p.T : (size_t)p.N;
+                const float a = __ldcg(p.lse + at), b = __ldcg(p.lse + at + step);
+                l1.x = l1.y = a == NEG_INF ? 0.0f : -a * LOG2E;
+                l2.x = l2.y = b == NEG_INF ? 0.0f : -b * LOG2E;
+            }
+            const float lam = __ldg(dp.lam + head);
+            const float2 f2 = make_float2(-lam, -lam);
+            for (int x = 0; x < w.n; ++x, ++h) {
+                const int c0 = (w.t0 + x) * C::BN;
+                if (!wait_all(&bars->s_full, h & 1)) break;
+                tc_fence_after_sync();
+                uint32_t a[HC], b[HC];
+#pragma unroll
+                for (int ch = 0; ch < HC; ch += 32) {
+                    tmem_ld32p(tmem + lane_addr + wg * HC + ch, a + ch);
+                    tmem_ld32p(tmem + lane_addr + C::BN + wg * HC + ch, b + ch);
+                }
+                tmem_wait_ld_only();
+#pragma unroll
+                for (int ch = 0; ch < HC; ch += 32) {
+                    reg_fence32(a + ch);
+                    reg_fence32(b + ch);
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->s_free));
+                uint32_t pk[HC / 2];
+                auto weigh = [&](auto masked_tag) {
+                    constexpr bool kMasked = decltype(masked_tag)::value;
+                    const uint32_t first = (uint32_t)(c0 + wg * HC - jlo);
+#pragma unroll
+                    for (int e = 0; e < HC; e += 2) {
+                        const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])), c2, l1);
+                        const float2 x2 = __ffma2_rn(make_float2(__uint_as_float(b[e]), __uint_as_float(b[e + 1])), c2, l2);
+                        float2 r = __ffma2_rn(make_float2(ex2(x2.x), ex2(x2.y)), f2, make_float2(ex2(x1.x), ex2(x1.y)));
+                        if constexpr (kMasked) {
+                            r.x = first + (uint32_t)e <= span ? r.x : 0.0f;
+                            r.y = first + (uint32_t)e + 1u <= span ? r.y : 0.0f;
+                        }
+                        pk[e / 2] = pack_bf16x2(r.x, r.y);
+                    }
+                };
+                if (diff_edge(p, w.N, w.q0, c0)) weigh(std::true_type{});
+                else weigh(std::false_type{});
+                // the product of the step before has read the weights
+                if (h > 0 && !wait_all(&bars->w_free, (h - 1) & 1)) break;
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                    *reinterpret_cast<uint4*>(w_row + ((v ^ (trow & 7)) << 4)) =
+                        make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->w_full));
+            }
+            if (!ok) break;
+            if (!wait_all(&bars->o_full, uc & 1)) break;
+            tc_fence_after_sync();
+            // each warpgroup writes half of the head's columns
+            const size_t orow = C::PACKED ? (size_t)(w.y0 + row) * p.H + w.z : (size_t)w.z * p.N + row;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + orow * (2 * C::D) + wg * C::D;
+#pragma unroll
+            for (int ch = 0; ch < C::D / 32; ++ch) {
+                uint32_t r[32];
+                tmem_ld32(tmem + lane_addr + C::O_COL + wg * C::D + ch * 32, r);
+                tmem_wait_ld(r);
+                if (!valid) continue;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        pk[e] = pack_bf16x2(__uint_as_float(r[8 * v + 2 * e]), __uint_as_float(r[8 * v + 2 * e + 1]));
+                    reinterpret_cast<uint4*>(out + ch * 32)[v] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->o_empty));
+            ++uc;
+        }
+        if (!ok) timed_out();
+    } else {
+        regs_decrease<C::REG_CONTROL>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == C::MMA_WARP) tmem_dealloc(tmem, 512);
+}
+
+template <class C, class Kernel, class... Args>
+static cudaError_t launch_one(Kernel kernel, FwdParams& f, int sm_count, cudaStream_t stream, const Args&... args)
+{
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    // setmaxnreg.inc would wait forever if the launch pool were smaller than the split
+    cudaFuncAttributes attr;
+    if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
+    if (attr.numRegs * C::NUM_THREADS < C::REG_POOL) return cudaErrorInvalidConfiguration;
+    const int grid = fwd_grid(f, sm_count);
+    set_fwd_walk(f, grid);
+    kernel<<<grid, C::NUM_THREADS, C::SMEM_BYTES, stream>>>(args...);
+    return cudaGetLastError();
+}
+
+template <bool PK>
+static cudaError_t launch_wide(const DiffFwdMaps& m, DiffFwdParams& lse, DiffFwdParams& out, int sm_count, cudaStream_t stream)
+{
+    const cudaError_t e = launch_one<DiffLseCfg<PK>>(diff_lse_kernel<PK>, lse.f, sm_count, stream, m.q, m.k, lse);
+    if (e != cudaSuccess) return e;
+    return launch_one<DiffOutCfg<PK>>(diff_out_kernel<PK>, out.f, sm_count, stream, m.q, m.k, m.v32, out);
+}
+
+cudaError_t launch_diff_fwd_wide(const DiffFwdMaps& m, DiffFwdParams lse, DiffFwdParams out, int sm_count,
+                                 cudaStream_t stream)
+{
+    return out.f.cu_seqlens != nullptr ? launch_wide<true>(m, lse, out, sm_count, stream)
+                                       : launch_wide<false>(m, lse, out, sm_count, stream);
+}
+
+}  // namespace gb300
