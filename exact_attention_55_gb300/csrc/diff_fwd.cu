@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(DiffFwdCfg<D, PK>::NUM_THREADS, 1)
             if (lane == 0) mbar_arrive(smem_u32(&bars->o_empty));
             if (row < w.N && at.part == 0)
                 p.lse[at.lse + grp * at.lse_step + row] =
-                    (l > 0.0f ? m_used + __log2f(l) : NEG_INF) * 0.69314718055994531f;
+                    (l == 0.0f ? NEG_INF : m_used + __log2f(l)) * 0.69314718055994531f;   // NaN stays one
             ++uc;
         }
         if (!ok) timed_out();

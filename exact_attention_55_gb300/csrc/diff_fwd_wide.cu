@@ -8,7 +8,7 @@
 // 2 d and two products of 2 d for each half).  With the L_m known the maps' weights are subtracted before the
 // product, and one accumulator of 256 columns takes it: 4 d products for the L_m, 4 d for the scores
 // again, 4 d for O: 12 d, with as many exponentials, and no rescaling in the second launch.
-// Measured, 16 heads over 4 key pairs, 16384 tokens, causal: 3020 us in one launch, 2435 in two.
+// Measured, 16 heads over 4 key pairs, 16384 tokens, causal: 3020 us in one launch, 2270 in two (780 + 1440).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -20,8 +20,9 @@
 namespace gb300 {
 
 // ------------------------------------------------------------------ log-sum-exps
-// A unit is 256 query rows of one map, as two tiles with a warpgroup each that share the stream of key tiles; each
-// tile's scores have two TMEM buffers.
+// A unit is 256 query rows of one map, as two tiles that share the stream of key tiles; each tile's scores have
+// two TMEM buffers, and two warpgroups that take half of the keys each and join their sums at the end (one
+// warpgroup a tile left the schedulers two warps, and half of their slots empty).
 template <bool PK>
 struct DiffLseCfg {
     static constexpr bool PACKED = PK;
@@ -29,11 +30,11 @@ struct DiffLseCfg {
     static constexpr int CB = 128 * 128;                 // 64 columns of a 128-row tile
     static constexpr int TILE = 2 * CB;
     static constexpr int NSLOT = 4;
-    static constexpr int TAB_OFF = 256, BAR_BYTES = 2048 + 256;
+    static constexpr int TAB_OFF = 2560, BAR_BYTES = TAB_OFF + 2048;
     static constexpr int SMEM_BYTES = 1024 + (NQ + NSLOT) * TILE + BAR_BYTES;
-    static constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, NUM_THREADS = 384;
-    static constexpr int REG_SOFTMAX = 208, REG_CONTROL = 88;
-    static constexpr int REG_POOL = 256 * REG_SOFTMAX + 128 * REG_CONTROL;
+    static constexpr int COMPUTE_WARPS = 16, PRODUCER_WARP = 16, MMA_WARP = 17, NUM_THREADS = 640;
+    static constexpr int REG_SOFTMAX = 104, REG_CONTROL = 64;
+    static constexpr int REG_POOL = 512 * REG_SOFTMAX + 128 * REG_CONTROL;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
     static_assert(TAB_OFF + sizeof(SortTab) <= BAR_BYTES, "schedule table");
 };
@@ -42,11 +43,13 @@ struct alignas(16) DiffLseBars {
     uint64_t q_full, q_empty;
     uint64_t k_full[4], k_empty[4];
     uint64_t s_full[2][2], s_free[2][2];                 // tile, buffer
+    uint64_t half_full[2], half_free[2];                 // tile
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
+    float2 half[2][128];                                 // maximum and sum of the second half's keys
 };
-static_assert(sizeof(DiffLseBars) <= 256, "barrier block");
+static_assert(sizeof(DiffLseBars) <= 2560, "barrier block");
 
 // Keys [lo, hi] that row r may use; both grow with r.
 __device__ __forceinline__ void diff_key_bounds(const FwdParams& p, int N, int r, int& lo, int& hi)
@@ -99,7 +102,11 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(smem_u32(&bars->s_full[i >> 1][i & 1]), 1);
-            mbar_init(smem_u32(&bars->s_free[i >> 1][i & 1]), 4);
+            mbar_init(smem_u32(&bars->s_free[i >> 1][i & 1]), 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars->half_full[i]), 4);
+            mbar_init(smem_u32(&bars->half_free[i]), 4);
         }
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort_flag = 0;
@@ -214,60 +221,59 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
         mma_commit_warp(smem_u32(&bars->drain));
         mbar_wait(smem_u32(&bars->drain), 0, nullptr, kCleanupTimeoutNs);
         __syncwarp();
-    } else if (warp < 8) {
+    } else if (warp < C::COMPUTE_WARPS) {
         regs_increase<C::REG_SOFTMAX>();
-        const int grp = warp >> 2, wq = warp & 3;
-        const uint32_t lane_addr = (uint32_t)(wq * 32) << 16;
+        constexpr int HC = C::BN / 2;
+        const int tile = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3, trow = wq * 32 + lane;
+        const uint32_t s_addr = tmem + ((uint32_t)(wq * 32) << 16) + 2 * tile * C::BN + half * HC;
         const float NEG_INF = -__int_as_float(0x7f800000), c = p.c_log2;
-        uint32_t count = 0;
+        uint32_t count = 0, uc = 0;
         bool ok = true;
         for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
             Unit w;
             if (!unit_of<C>(su, p, w, tab)) continue;
             int L, R;
-            tile_steps<C>(w, grp, p, L, R);
-            const int a = w.q0 + grp * C::BM, row = a + wq * 32 + lane;
+            tile_steps<C>(w, tile, p, L, R);
+            const int a = w.q0 + tile * C::BM, row = a + trow;
             int jlo, jhi;
             diff_key_bounds(p, w.N, row, jlo, jhi);
-            // a row behind the sequence sees what the last one sees, and stores nothing
-            if (jlo > jhi) jlo = jhi;
+            if (jlo > jhi) jlo = jhi;                     // a row behind the sequence, which is not stored
             const uint32_t span = (uint32_t)(jhi - jlo);
             float m_used = NEG_INF;
             float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             for (int jj = L; jj < R; ++jj) {
                 const int c0 = (w.t0 + jj) * C::BN;
                 const uint32_t b = count & 1;
-                ok = warp_wait(&bars->s_full[grp][b], (count >> 1) & 1);
+                ok = warp_wait(&bars->s_full[tile][b], (count >> 1) & 1);
                 ++count;
                 if (!ok) break;
                 tc_fence_after_sync();
-                uint32_t sr[C::BN];
+                uint32_t sr[HC];
 #pragma unroll
-                for (int ch = 0; ch < C::BN / 32; ++ch) tmem_ld32p(tmem + lane_addr + (2 * grp + b) * C::BN + ch * 32, sr + ch * 32);
+                for (int ch = 0; ch < HC; ch += 32) tmem_ld32p(s_addr + b * C::BN + ch, sr + ch);
                 tmem_wait_ld_only();
 #pragma unroll
-                for (int ch = 0; ch < C::BN / 32; ++ch) reg_fence32(sr + ch * 32);
+                for (int ch = 0; ch < HC; ch += 32) reg_fence32(sr + ch);
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[grp][b]));
+                if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[tile][b]));
                 float* s = reinterpret_cast<float*>(sr);
                 if (diff_edge(p, w.N, a, c0)) {
-                    const uint32_t base = (uint32_t)(c0 - jlo);
+                    const uint32_t first = (uint32_t)(c0 + half * HC - jlo);
 #pragma unroll
-                    for (int e = 0; e < C::BN; ++e)
-                        if (base + (uint32_t)e > span) s[e] = NEG_INF;
+                    for (int e = 0; e < HC; ++e)
+                        if (first + (uint32_t)e > span) s[e] = NEG_INF;
                 }
-                float mx[8];
+                float mx[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     float m = s[k];
 #pragma unroll
-                    for (int u = 1; u + 1 < C::BN / 8; u += 2) m = fmax3(m, s[k + 8 * u], s[k + 8 * u + 8]);
-                    mx[k] = fmaxf(m, s[k + 8 * (C::BN / 8 - 1)]);
+                    for (int u = 1; u + 1 < HC / 4; u += 2) m = fmax3(m, s[k + 4 * u], s[k + 4 * u + 4]);
+                    mx[k] = fmaxf(m, s[k + 4 * (HC / 4 - 1)]);
                 }
-                const float m_cand =
-                    fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * c;
-                if (m_cand > m_used) {                    // exact: a thread's own sums are all there is to rescale
+                const float m_cand = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * c;
+                if (m_cand > m_used) {                    // a thread's own sums are all there is to rescale
                     const float alpha = ex2(m_used - m_cand);    // ex2(-inf) = 0
 #pragma unroll
                     for (int k = 0; k < 4; ++k) acc[k] = __fmul2_rn(acc[k], make_float2(alpha, alpha));
@@ -276,18 +282,35 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
                 const float mb = m_used == NEG_INF ? 0.0f : m_used;
                 const float2 c2 = make_float2(c, c), b2 = make_float2(-mb, -mb);
 #pragma unroll
-                for (int e = 0; e < C::BN / 2; ++e) {
+                for (int e = 0; e < HC / 2; ++e) {
                     const float2 x = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), c2, b2);
                     acc[e & 3] = __fadd2_rn(acc[e & 3], make_float2(ex2(x.x), ex2(x.y)));
                 }
             }
             if (!ok) break;
             const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
-            const float l = (a01.x + a01.y) + (a23.x + a23.y);
-            if (row < w.N) {
-                const size_t at = C::PACKED ? (size_t)w.z * p.T + w.y0 : (size_t)w.z * p.N;
-                p.lse[at + row] = (l > 0.0f ? m_used + __log2f(l) : NEG_INF) * 0.69314718055994531f;
+            float l = (a01.x + a01.y) + (a23.x + a23.y);
+            if (half == 1) {
+                ok = warp_wait(&bars->half_free[tile], (uc & 1) ^ 1);
+                if (!ok) break;
+                bars->half[tile][trow] = make_float2(m_used, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->half_full[tile]));
+            } else {
+                ok = warp_wait(&bars->half_full[tile], uc & 1);
+                if (!ok) break;
+                const float2 o = bars->half[tile][trow];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->half_free[tile]));
+                const float top = fmaxf(m_used, o.x), mb = top == NEG_INF ? 0.0f : top;
+                l = fmaf(l, ex2(m_used - mb), o.y * ex2(o.x - mb));
+                if (row < w.N) {
+                    const size_t at = C::PACKED ? (size_t)w.z * p.T + w.y0 : (size_t)w.z * p.N;
+                    // a sum that is NaN stays one
+                    p.lse[at + row] = (l == 0.0f ? NEG_INF : top + __log2f(l)) * 0.69314718055994531f;
+                }
             }
+            ++uc;
         }
         if (!ok) timed_out();
     } else {
