@@ -108,7 +108,8 @@ attn_status_t diff_fwd(const void* q, const void* k, const void* v, const float*
     if (!diff_map(&m.q, q, s.d, 2 * s.H, s.B, s.N, s.T, 128) ||
         !diff_map(&m.k, k, s.d, 2 * s.Hkv, s.B, s.N, s.T, 128) ||
         !diff_map(&m.v, v, 2 * s.d, s.Hkv, s.B, s.N, s.T, 128) ||
-        !diff_map(&m.v32, v, 2 * s.d, s.Hkv, s.B, s.N, s.T, 32))
+        !diff_map(&m.k64, k, s.d, 2 * s.Hkv, s.B, s.N, s.T, 64) ||
+        !diff_map(&m.v64, v, 2 * s.d, s.Hkv, s.B, s.N, s.T, 64))
         return ATTN_ERR_CUDA;
     DiffFwdParams p;
     std::memset(&p, 0, sizeof(p));
@@ -135,16 +136,17 @@ attn_status_t diff_fwd(const void* q, const void* k, const void* v, const float*
     p.Hkv = s.Hkv;
     cudaError_t e;
     if (s.d == 128 && !o2) {
-        auto shape = [&](int heads_of, int rows) {     // heads of one sequence, rows of a query block
+        auto shape = [&](int heads_of, int walkers) {     // heads of one sequence; CTAs or pairs of them
             DiffFwdParams r = p;
             r.f.H = heads_of;
             r.f.BH = (packed ? s.num_seqs : s.B) * heads_of;
-            r.f.num_qblk = (int)(((long long)s.N + rows - 1) / rows);
+            r.f.num_qblk = (int)(((long long)s.N + 255) / 256);
             r.f.num_units = r.f.BH * ((r.f.num_qblk + 1) / 2);
-            r.f.unit_walk = packed ? 0 : single_unit_walk(s.causal, s.window, s.N, r.f.num_units, dev->sm_count);
+            r.f.unit_walk = packed ? 0 : single_unit_walk(s.causal, s.window, s.N, r.f.num_units, walkers);
             return r;
         };
-        e = launch_diff_fwd_wide(m, shape(2 * s.H, 256), shape(s.H, 128), dev->sm_count, static_cast<cudaStream_t>(stream));
+        e = launch_diff_fwd_wide(m, shape(2 * s.H, dev->sm_count), shape(s.H, dev->sm_count / 2), dev->sm_count,
+                                 static_cast<cudaStream_t>(stream));
     } else {
         e = launch_diff_fwd(m, p, s.d, dev->sm_count, static_cast<cudaStream_t>(stream));
     }

@@ -8,7 +8,7 @@
 // 2 d and two products of 2 d for each half).  With the L_m known the maps' weights are subtracted before the
 // product, and one accumulator of 256 columns takes it: 4 d products for the L_m, 4 d for the scores
 // again, 4 d for O: 12 d, with as many exponentials, and no rescaling in the second launch.
-// Measured, 16 heads over 4 key pairs, 16384 tokens, causal: 3020 us in one launch, 2270 in two (780 + 1440).
+// Measured, 16 heads over 4 key pairs, 16384 tokens, causal: 3020 us in one launch, 2435 in two.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -323,21 +323,24 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
 }
 
 // ------------------------------------------------------------------ the output
-// A unit is 128 query rows of a head.  A step's scores of both maps (128 keys) fill 256 TMEM columns,
-// which the compute warps load at once and give back; they take half of the keys of both maps each and put the
-// difference of the weights, rounded once, into shared memory.  The MMA warp issues the next step's scores
-// before the product with it, so the tensor pipe works on both while the weights are made.  K and V stream
-// through one ring in pieces of 16 KB (64 columns of a map's keys; 32 keys of V), each given back as soon as
-// its products are done: it holds one step.
+// A unit is 256 query rows of a head for a cluster of two CTAs: each has 128 of them, in its registers and TMEM,
+// and half of every tile of K (64 keys) and V (128 columns), which the paired products (cta_group::2) of both
+// read.  A step's scores of both maps (128 keys) fill 256 TMEM columns, which the compute warps load at once and
+// give back; they take half of the keys of both maps each and put the difference of the weights, rounded once, into
+// shared memory.  CTA 0's MMA warp issues the next step's scores before the product with it, so the tensor pipes
+// work on both while the weights are made; CTA 1's tells it what has landed there.
+//
+// By itself a CTA would move 384 KB of shared memory a step (operands of 16 128 x 128 and 8 128 x 256 products of 16,
+// what TMA and the compute warps write): 3072 cycles at 128 bytes each, for 2048 of products.  A pair's CTA
+// moves 256 KB.
 template <bool PK>
 struct DiffOutCfg {
     static constexpr bool PACKED = PK;
-    static constexpr int BM = 128, NQ = 1, BN = 128, D = 128;
-    static constexpr int CB = 128 * 128;
-    static constexpr int Q_BYTES = 4 * CB, W_BYTES = 2 * CB, NSLOT = 8;
-    static constexpr int V_KEYS = 32, V_CB = V_KEYS * 128;          // keys of a piece of V, bytes of 64 of its columns
+    static constexpr int BM = 128, NQ = 2, BN = 128, D = 128;
+    static constexpr int CB = 128 * 128, HB = 64 * 128;              // 64 columns of 128 rows, of 64
+    static constexpr int Q_BYTES = 4 * CB, W_BYTES = 2 * CB, SLOT = 2 * HB, NSLOT = 8;
     static constexpr int TAB_OFF = 384, BAR_BYTES = 384 + 1792;
-    static constexpr int SMEM_BYTES = Q_BYTES + W_BYTES + NSLOT * CB + BAR_BYTES;   // no room for alignment
+    static constexpr int SMEM_BYTES = Q_BYTES + W_BYTES + NSLOT * SLOT + BAR_BYTES;   // no room for alignment
     static constexpr int O_COL = 256;
     static constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, NUM_THREADS = 384;
     static constexpr int REG_COMPUTE = 208, REG_CONTROL = 88;
@@ -349,12 +352,69 @@ struct DiffOutCfg {
 struct alignas(16) DiffOutBars {
     uint64_t q_full, q_empty;
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t s_full, s_free, w_full, w_free, o_full, o_empty;
+    uint64_t s_full, s_free, w_full, w_free, o_full, o_empty;      // s_free, w_full and o_empty: CTA 0's count both
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
 };
 static_assert(sizeof(DiffOutBars) <= 384, "barrier block");
+
+// The walk of attn_fwd.cuh by clusters: cluster c of G.
+template <class C>
+__device__ __forceinline__ int pair_first_sub(const FwdParams& p, int c)
+{
+    return C::PACKED ? 2 * c : c * p.walk_first;
+}
+template <class C>
+__device__ __forceinline__ int pair_next_sub(int s, const FwdParams& p, const SortTab* tab, int c, int G)
+{
+    if constexpr (C::PACKED) {
+        if (!(s & 1)) return s + 1;
+        if (tab == nullptr) return s + 2 * G - 1;
+        const int r = (s >> 1) / G + 1;                    // snake order, as snake_next_sub
+        return 2 * (r * G + ((r & 1) ? G - 1 - c : c));
+    } else {
+        return s + 1 + (((s + p.walk_a) % p.walk_m == 0) ? 0 : p.walk_step);
+    }
+}
+
+__device__ __forceinline__ uint32_t pair_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void pair_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// One arrival on CTA 0's barrier at this place.  No thread reads what the other CTA's threads wrote: operands pass from
+// TMA, or behind their writers' proxy fences, to the tensor cores, and TMEM behind its fences.  So the order within
+// the CTA is enough (a release to the cluster took the compute warps a memory barrier at each: 1440 us became 2130).
+__device__ __forceinline__ void pair_arrive(uint64_t* bar)
+{
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void pair_mma_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+// One arrival on the barrier at this place in both CTAs when the products issued so far are done.
+__device__ __forceinline__ void pair_commit_warp(uint64_t* bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
 
 template <bool PK>
 __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
@@ -367,9 +427,10 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
     uint8_t* q_smem = smem;
     uint8_t* w_smem = smem + C::Q_BYTES;
     uint8_t* ring_smem = w_smem + C::W_BYTES;
-    DiffOutBars* bars = reinterpret_cast<DiffOutBars*>(ring_smem + C::NSLOT * C::CB);
+    DiffOutBars* bars = reinterpret_cast<DiffOutBars*>(ring_smem + C::NSLOT * C::SLOT);
     const volatile int* abort_flag = &bars->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)pair_rank(), cid = (int)blockIdx.x / 2, clusters = (int)gridDim.x / 2;
     if ((smem_u32(smem) & 1023) != 0) {                    // no kernel of this file has static shared memory
         if (threadIdx.x == 0) atomicExch(p.status, kStatusTimeout);
         return;
@@ -379,33 +440,37 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
     if constexpr (C::PACKED) {
         if (p.num_seqs <= kSortMaxSeqs) {
             SortTab* t = reinterpret_cast<SortTab*>(reinterpret_cast<uint8_t*>(bars) + C::TAB_OFF);
-            build_sort_tab<C::BM>(p.cu_seqlens, p.num_seqs, p.T, p.H, t);
+            build_sort_tab<C::NQ * C::BM>(p.cu_seqlens, p.num_seqs, p.T, p.H, t);
             tab = t;
         }
     }
     if (threadIdx.x == 0) {
-        mbar_init(smem_u32(&bars->q_full), 1);
+        // CTA 0's full barriers count its own copies and CTA 1's word that its have landed
+        const uint32_t sides = rank == 0 ? 2 : 1;
+        mbar_init(smem_u32(&bars->q_full), sides);
         mbar_init(smem_u32(&bars->q_empty), 1);
         for (int s = 0; s < C::NSLOT; ++s) {
-            mbar_init(smem_u32(&bars->kv_full[s]), 1);
+            mbar_init(smem_u32(&bars->kv_full[s]), sides);
             mbar_init(smem_u32(&bars->kv_empty[s]), 1);
         }
         mbar_init(smem_u32(&bars->s_full), 1);
-        mbar_init(smem_u32(&bars->s_free), 8);
-        mbar_init(smem_u32(&bars->w_full), 8);
+        mbar_init(smem_u32(&bars->s_free), 16);
+        mbar_init(smem_u32(&bars->w_full), 16);
         mbar_init(smem_u32(&bars->w_free), 1);
         mbar_init(smem_u32(&bars->o_full), 1);
-        mbar_init(smem_u32(&bars->o_empty), 8);
+        mbar_init(smem_u32(&bars->o_empty), 16);
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == C::MMA_WARP) {
-        tmem_alloc(smem_u32(&bars->tmem_base), 512);
-        tmem_relinquish();
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bars->tmem_base))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before_sync();
     __syncthreads();
+    pair_sync();                                           // both CTAs' barriers are there
     tc_fence_after_sync();
     const uint32_t tmem = bars->tmem_base;
     const int G = dp.H / dp.Hkv;
@@ -434,10 +499,10 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
                     return false;
                 }
                 if (++ring == (uint32_t)p.withhold_kv) return false;      // test hook: never arrives
-                mbar_arrive_expect_tx(smem_u32(&bars->kv_full[slot]), C::CB);
+                mbar_arrive_expect_tx(smem_u32(&bars->kv_full[slot]), C::SLOT);
                 return true;
             };
-            for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
+            for (int su = pair_first_sub<C>(p, cid); su < num_subs(p, tab) && ok; su = pair_next_sub<C>(su, p, tab, cid, clusters)) {
                 Unit w;
                 if (!unit_of<C>(su, p, w, tab)) continue;
                 // heads of q (map 1), of V, of k (map 1)
@@ -450,114 +515,141 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
                 mbar_arrive_expect_tx(qb, C::Q_BYTES);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    tma_load_3d(smem_u32(q_smem + i * C::CB), &tmQ, qb, (i & 1) * 64, w.y0 + w.q0, 2 * w.z + (i >> 1), pol_q);
+                    tma_load_3d(smem_u32(q_smem + i * C::CB), &tmQ, qb, (i & 1) * 64, w.y0 + w.q0 + rank * C::BM,
+                                2 * w.z + (i >> 1), pol_q);
                 ++uc;
-                // in the order of their use: K of a step before V of the step before
+                // in the order of their use: K of a step (a slot a map) before V of the step before (64 keys a slot)
                 for (int x = -1; x < w.n && ok; ++x) {
                     uint32_t slot;
                     if (x + 1 < w.n)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < 2; ++i)
                             if (ready(slot))
-                                tma_load_3d(smem_u32(ring_smem + slot * C::CB), &tmK, smem_u32(&bars->kv_full[slot]),
-                                            (i & 1) * 64, w.y0 + (w.t0 + x + 1) * C::BN, zk + (i >> 1), pol_kv);
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    tma_load_3d(smem_u32(ring_smem + slot * C::SLOT + c * C::HB), &tmK,
+                                                smem_u32(&bars->kv_full[slot]), c * 64,
+                                                w.y0 + (w.t0 + x + 1) * C::BN + rank * 64, zk + i, pol_kv);
                     if (x >= 0)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < 2; ++i)
                             if (ready(slot))
 #pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    tma_load_3d(smem_u32(ring_smem + slot * C::CB + c * C::V_CB), &tmV,
-                                                smem_u32(&bars->kv_full[slot]), c * 64,
-                                                w.y0 + (w.t0 + x) * C::BN + i * C::V_KEYS, zv, pol_kv);
+                                for (int c = 0; c < 2; ++c)
+                                    tma_load_3d(smem_u32(ring_smem + slot * C::SLOT + c * C::HB), &tmV,
+                                                smem_u32(&bars->kv_full[slot]), rank * 128 + c * 64,
+                                                w.y0 + (w.t0 + x) * C::BN + i * 64, zv, pol_kv);
                 }
             }
             if (!ok) timed_out();
-            // every copy issued lands before shared memory is released
+            // every copy issued lands before shared memory is released (after an abort the other CTA's word may not
+            // come: a millisecond is enough for the copies)
+            const unsigned long long limit = ok ? kCleanupTimeoutNs : 1000000ull;
             for (uint32_t k = ring < C::NSLOT ? 0 : ring - C::NSLOT; k < ring; ++k)
                 if (k + 1 != (uint32_t)p.withhold_kv)
-                    mbar_wait(smem_u32(&bars->kv_full[k % C::NSLOT]), (k / C::NSLOT) & 1, nullptr, kCleanupTimeoutNs);
-            if (uc > 0) mbar_wait(smem_u32(&bars->q_full), (uc - 1) & 1, nullptr, kCleanupTimeoutNs);
+                    mbar_wait(smem_u32(&bars->kv_full[k % C::NSLOT]), (k / C::NSLOT) & 1, nullptr, limit);
+            if (uc > 0) mbar_wait(smem_u32(&bars->q_full), (uc - 1) & 1, nullptr, limit);
         }
     } else if (warp == C::MMA_WARP) {
         regs_decrease<C::REG_CONTROL>();
-        constexpr uint32_t idesc_s = idesc_f32acc(1, 0, C::BM, C::BN), idesc_o = idesc_f32acc(1, 1, C::BM, 2 * C::D);
+        constexpr uint32_t idesc_s = idesc_f32acc(1, 0, 2 * C::BM, C::BN), idesc_o = idesc_f32acc(1, 1, 2 * C::BM, 2 * C::D);
         const uint64_t q_desc = sdesc_sw128(smem_u32(q_smem), 16, 1024), w_desc = sdesc_sw128(smem_u32(w_smem), 16, 1024);
         const uint64_t k_desc = sdesc_sw128(smem_u32(ring_smem), 16, 1024);
-        const uint64_t v_desc = sdesc_sw128(smem_u32(ring_smem), C::V_CB, 1024);
+        const uint64_t v_desc = sdesc_sw128(smem_u32(ring_smem), C::HB, 1024);
         uint32_t ring = 0, uc = 0, scores = 0, products = 0;       // steps whose S and whose product were issued
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
             ok = ok && warp_wait(bar, parity);
             return ok;
         };
-        auto commit = [&](uint64_t* bar) { mma_commit_warp(smem_u32(bar)); };
         auto full = [&](uint32_t n) -> bool { return wait(&bars->kv_full[n % C::NSLOT], (n / C::NSLOT) & 1); };
+        // packed rows behind the sequence become 0: a weight of 0 times a NaN would be one
+        auto clear_tail = [&](int live, uint8_t* v) {
+            if constexpr (C::PACKED) {
+                if (live >= 64) return;
+                for (int o = max(live, 0) * 128 + lane * 16; o < C::HB; o += 512)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) *reinterpret_cast<uint4*>(v + c * C::HB + o) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+        };
         auto issue_s = [&]() -> bool {
             if (scores > 0 && !wait(&bars->s_free, (scores - 1) & 1)) return false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i, ++ring) {
+            for (int i = 0; i < 2; ++i, ++ring) {
                 const uint32_t slot = ring % C::NSLOT;
                 if (!full(ring)) return false;
                 tc_fence_after_sync();
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ss_warp<false>(tmem + (i >> 1) * C::BN, q_desc + ((i * C::CB + kk * 32) >> 4),
-                                       k_desc + ((slot * C::CB + kk * 32) >> 4), idesc_s, (i & 1) || kk > 0 ? 1u : 0u);
-                commit(&bars->kv_empty[slot]);
+                for (int kk = 0; kk < C::D / 16; ++kk)
+                    pair_mma_warp(tmem + i * C::BN, q_desc + (((2 * i + kk / 4) * C::CB + (kk % 4) * 32) >> 4),
+                                  k_desc + ((slot * C::SLOT + (kk / 4) * C::HB + (kk % 4) * 32) >> 4), idesc_s,
+                                  kk > 0 ? 1u : 0u);
+                pair_commit_warp(&bars->kv_empty[slot]);
             }
-            commit(&bars->s_full);
+            pair_commit_warp(&bars->s_full);
             ++scores;
             return true;
-        };
-        // packed rows behind the sequence become 0: a weight of 0 times a NaN would be one
-        auto clear_tail = [&](int live, uint8_t* v) {
-            if constexpr (C::PACKED) {
-                if (live >= C::V_KEYS) return;
-                for (int o = max(live, 0) * 128 + lane * 16; o < C::V_CB; o += 512)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(v + c * C::V_CB + o) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
         };
         auto issue_product = [&](const Unit& w, int x) -> bool {
             if (x == 0 && !wait(&bars->o_empty, (uc & 1) ^ 1)) return false;
             if (!wait(&bars->w_full, products & 1)) return false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i, ++ring) {
+            for (int i = 0; i < 2; ++i, ++ring) {
                 const uint32_t slot = ring % C::NSLOT;
                 if (!full(ring)) return false;
-                clear_tail(w.N - (w.t0 + x) * C::BN - i * C::V_KEYS, ring_smem + slot * C::CB);
+                clear_tail(w.N - (w.t0 + x) * C::BN - i * 64, ring_smem + slot * C::SLOT);
                 tc_fence_after_sync();
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
-                    mma_ss_warp<false>(tmem + C::O_COL, w_desc + (((i >> 1) * C::CB + (i & 1) * 64 + kk * 32) >> 4),
-                                       v_desc + ((slot * C::CB + kk * 16 * 128) >> 4), idesc_o,
-                                       x > 0 || i > 0 || kk > 0 ? 1u : 0u);
-                commit(&bars->kv_empty[slot]);
+                for (int kk = 0; kk < 4; ++kk)
+                    pair_mma_warp(tmem + C::O_COL, w_desc + ((i * C::CB + kk * 32) >> 4),
+                                  v_desc + ((slot * C::SLOT + kk * 16 * 128) >> 4), idesc_o, x > 0 || i > 0 || kk > 0 ? 1u : 0u);
+                pair_commit_warp(&bars->kv_empty[slot]);
             }
-            commit(&bars->w_free);
+            pair_commit_warp(&bars->w_free);
             ++products;
             return true;
         };
-        for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
+        // CTA 1: a slot that has landed
+        auto pass_on = [&](uint64_t* bar) {
+            __syncwarp();
+            if (lane == 0) pair_arrive(bar);
+        };
+        for (int su = pair_first_sub<C>(p, cid); su < num_subs(p, tab) && ok; su = pair_next_sub<C>(su, p, tab, cid, clusters)) {
             Unit w;
             if (!unit_of<C>(su, p, w, tab)) continue;
             if (!wait(&bars->q_full, uc & 1)) break;
-            if (!issue_s()) break;
-            for (int x = 0; x < w.n; ++x) {
-                if (x + 1 < w.n && !issue_s()) break;
-                if (x + 2 == w.n || w.n == 1) commit(&bars->q_empty);     // behind the unit's last scores
-                if (!issue_product(w, x)) break;
+            if (rank == 0) {
+                if (!issue_s()) break;
+                for (int x = 0; x < w.n; ++x) {
+                    if (x + 1 < w.n && !issue_s()) break;
+                    if (x + 2 == w.n || w.n == 1) pair_commit_warp(&bars->q_empty);   // behind the unit's last scores
+                    if (!issue_product(w, x)) break;
+                }
+                if (!ok) break;
+                pair_commit_warp(&bars->o_full);
+            } else {
+                pass_on(&bars->q_full);
+                for (int x = -1; x < w.n && ok; ++x) {
+                    if (x + 1 < w.n)
+                        for (int i = 0; i < 2 && ok; ++i, ++ring)
+                            if (full(ring)) pass_on(&bars->kv_full[ring % C::NSLOT]);
+                    if (x >= 0)
+                        for (int i = 0; i < 2 && ok; ++i, ++ring)
+                            if (full(ring)) {
+                                clear_tail(w.N - (w.t0 + x) * C::BN - i * 64, ring_smem + (ring % C::NSLOT) * C::SLOT);
+                                pass_on(&bars->kv_full[ring % C::NSLOT]);
+                            }
+                }
             }
-            if (!ok) break;
-            commit(&bars->o_full);
             ++uc;
         }
         if (!ok && lane == 0) timed_out();
-        commit(&bars->drain);
-        mbar_wait(smem_u32(&bars->drain), 0, nullptr, kCleanupTimeoutNs);
+        if (rank == 0) {
+            pair_commit_warp(&bars->drain);
+            mbar_wait(smem_u32(&bars->drain), 0, nullptr, kCleanupTimeoutNs);
+        }
         __syncwarp();
     } else if (warp < 8) {
         // both warpgroups work on every step, warpgroup wg on its half of the keys, a thread one row
@@ -575,10 +667,10 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
             ok = ok && warp_wait(bar, parity);
             return ok;
         };
-        for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
+        for (int su = pair_first_sub<C>(p, cid); su < num_subs(p, tab) && ok; su = pair_next_sub<C>(su, p, tab, cid, clusters)) {
             Unit w;
             if (!unit_of<C>(su, p, w, tab)) continue;
-            const int row = w.q0 + trow, head = C::PACKED ? w.z : w.z % dp.H;
+            const int a0 = w.q0 + rank * C::BM, row = a0 + trow, head = C::PACKED ? w.z : w.z % dp.H;
             const bool valid = row < w.N;
             int jlo, jhi;
             diff_key_bounds(p, w.N, row, jlo, jhi);
@@ -613,7 +705,7 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->s_free));
+                if (lane == 0) pair_arrive(&bars->s_free);
                 uint32_t pk[HC / 2];
                 auto weigh = [&](auto masked_tag) {
                     constexpr bool kMasked = decltype(masked_tag)::value;
@@ -630,7 +722,7 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
                         pk[e / 2] = pack_bf16x2(r.x, r.y);
                     }
                 };
-                if (diff_edge(p, w.N, w.q0, c0)) weigh(std::true_type{});
+                if (diff_edge(p, w.N, a0, c0)) weigh(std::true_type{});
                 else weigh(std::false_type{});
                 // the product of the step before has read the weights
                 if (h > 0 && !wait_all(&bars->w_free, (h - 1) & 1)) break;
@@ -640,7 +732,7 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
                         make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->w_full));
+                if (lane == 0) pair_arrive(&bars->w_full);
             }
             if (!ok) break;
             if (!wait_all(&bars->o_full, uc & 1)) break;
@@ -665,7 +757,7 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
             }
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->o_empty));
+            if (lane == 0) pair_arrive(&bars->o_empty);
             ++uc;
         }
         if (!ok) timed_out();
@@ -674,12 +766,14 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
     }
     tc_fence_before_sync();
     __syncthreads();
+    pair_sync();                                           // nothing of the other CTA's is on its way here
     tc_fence_after_sync();
-    if (warp == C::MMA_WARP) tmem_dealloc(tmem, 512);
+    if (warp == C::MMA_WARP)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 template <class C, class Kernel, class... Args>
-static cudaError_t launch_one(Kernel kernel, FwdParams& f, int sm_count, cudaStream_t stream, const Args&... args)
+static cudaError_t launch_one(Kernel kernel, int cluster, FwdParams& f, int sm_count, cudaStream_t stream, const Args&... args)
 {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
@@ -687,18 +781,28 @@ static cudaError_t launch_one(Kernel kernel, FwdParams& f, int sm_count, cudaStr
     cudaFuncAttributes attr;
     if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
     if (attr.numRegs * C::NUM_THREADS < C::REG_POOL) return cudaErrorInvalidConfiguration;
-    const int grid = fwd_grid(f, sm_count);
+    const int grid = fwd_grid(f, sm_count / cluster);     // CTAs or pairs that walk the units
     set_fwd_walk(f, grid);
-    kernel<<<grid, C::NUM_THREADS, C::SMEM_BYTES, stream>>>(args...);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute pair[1];
+    pair[0].id = cudaLaunchAttributeClusterDimension;
+    pair[0].val.clusterDim.x = cluster;
+    pair[0].val.clusterDim.y = pair[0].val.clusterDim.z = 1;
+    cfg.attrs = pair;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cfg.stream = stream;
+    cfg.gridDim = dim3((unsigned)(grid * cluster));
+    cfg.blockDim = dim3(C::NUM_THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <bool PK>
 static cudaError_t launch_wide(const DiffFwdMaps& m, DiffFwdParams& lse, DiffFwdParams& out, int sm_count, cudaStream_t stream)
 {
-    const cudaError_t e = launch_one<DiffLseCfg<PK>>(diff_lse_kernel<PK>, lse.f, sm_count, stream, m.q, m.k, lse);
+    const cudaError_t e = launch_one<DiffLseCfg<PK>>(diff_lse_kernel<PK>, 1, lse.f, sm_count, stream, m.q, m.k, lse);
     if (e != cudaSuccess) return e;
-    return launch_one<DiffOutCfg<PK>>(diff_out_kernel<PK>, out.f, sm_count, stream, m.q, m.k, m.v32, out);
+    return launch_one<DiffOutCfg<PK>>(diff_out_kernel<PK>, 2, out.f, sm_count, stream, m.q, m.k64, m.v64, out);
 }
 
 cudaError_t launch_diff_fwd_wide(const DiffFwdMaps& m, DiffFwdParams lse, DiffFwdParams out, int sm_count,

@@ -43,7 +43,7 @@ struct DiffFwdParams {
 
 struct DiffFwdMaps {
     CUtensorMap q, k, v;    // 128-row boxes of 64 columns
-    CUtensorMap v32;        // 32-row boxes (launch_diff_fwd_wide)
+    CUtensorMap k64, v64;   // 64-row boxes (launch_diff_fwd_wide)
 };
 
 // Backward pass of differential attention.  Packed layout: B sequences' offsets in cu_seqlens, N the
@@ -93,7 +93,7 @@ constexpr int diff_decode_ctas(int d) { return d == 64 ? 2 : 1; }
 cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_diff_fwd(const DiffFwdMaps& m, const DiffFwdParams& p, int d, int sm_count,
                             cudaStream_t stream);
-// d = 128 without O_2: two launches; lse.f counts maps as heads and has query blocks of 256 rows.
+// d = 128 without O_2: two launches with query blocks of 256 rows; lse.f counts maps as heads.
 cudaError_t launch_diff_fwd_wide(const DiffFwdMaps& m, DiffFwdParams lse, DiffFwdParams out, int sm_count,
                                  cudaStream_t stream);
 cudaError_t launch_diff_bwd(const DiffBwdMaps& m, const DiffBwdParams& p, int d, int sm_count,
