@@ -134,8 +134,15 @@ attn_status_t diff_fwd(const void* q, const void* k, const void* v, const float*
     p.lam = lam;
     p.H = s.H;
     p.Hkv = s.Hkv;
+    // d = 128 without O_2: two launches of 12 d products in place of one of 16 d (diff_fwd_wide.cu), where the one
+    // would take more than a round of the card and sequences (packed: their mean) are longer than a query block
+    // there.  Measured, one against two, causal, 16 heads over 4: 1024 tokens 24 us against 39, 1536 56 against 47,
+    // 4096 228 against 168; 64 x 256 tokens 14.5 against 19, 64 x 384 32 against 30; non-causal 512 12 against 21, 768 27
+    // against 26; a window of 128 1024 tokens 18 against 21, of 512 4096 tokens 89 against 82.
     cudaError_t e;
-    if (s.d == 128 && !o2) {
+    const int mean = packed ? s.T / s.num_seqs : s.N;
+    if (s.d == 128 && !o2 && mean > 256 && (p.f.window == 0 || p.f.window >= 256) &&
+        (p.f.unit_walk ? 2 * pairs : pairs) > dev->sm_count) {
         auto shape = [&](int heads_of, int walkers) {     // heads of one sequence; CTAs or pairs of them
             DiffFwdParams r = p;
             r.f.H = heads_of;

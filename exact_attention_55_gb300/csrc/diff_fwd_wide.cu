@@ -20,18 +20,21 @@
 namespace gb300 {
 
 // ------------------------------------------------------------------ log-sum-exps
-// A unit is 256 query rows of one map, as two tiles that share the stream of key tiles; each tile's scores have
-// two TMEM buffers, and two warpgroups that take half of the keys each and join their sums at the end (one
-// warpgroup a tile left the schedulers two warps, and half of their slots empty).
+// A unit is 256 query rows of one map, as two tiles that share the stream of key tiles.  A step is 256 keys: a
+// 128 x 256 x 16 product of two shared-memory operands reads 12 KB in its 128 cycles, one of 128 x 128 the 8 KB
+// that shared memory has for its 64, with nothing left for TMA.  A tile's scores fill half of TMEM; the
+// tensor pipe works on one tile's while the warps load the other's, two warpgroups a tile with half of the keys
+// each, which join their sums at the end (one warpgroup a tile left the schedulers two warps, and half of their
+// slots empty).
 template <bool PK>
 struct DiffLseCfg {
     static constexpr bool PACKED = PK;
-    static constexpr int BM = 128, NQ = 2, BN = 128, D = 128;
-    static constexpr int CB = 128 * 128;                 // 64 columns of a 128-row tile
-    static constexpr int TILE = 2 * CB;
-    static constexpr int NSLOT = 4;
+    static constexpr int BM = 128, NQ = 2, BN = 256, D = 128;
+    static constexpr int CB = 128 * 128;                 // 64 columns of 128 rows
+    static constexpr int Q_BYTES = 2 * NQ * CB, SLOT = 4 * CB;
+    static constexpr int NSLOT = 2;
     static constexpr int TAB_OFF = 2560, BAR_BYTES = TAB_OFF + 2048;
-    static constexpr int SMEM_BYTES = 1024 + (NQ + NSLOT) * TILE + BAR_BYTES;
+    static constexpr int SMEM_BYTES = 1024 + Q_BYTES + NSLOT * SLOT + BAR_BYTES;
     static constexpr int COMPUTE_WARPS = 16, PRODUCER_WARP = 16, MMA_WARP = 17, NUM_THREADS = 640;
     static constexpr int REG_SOFTMAX = 104, REG_CONTROL = 64;
     static constexpr int REG_POOL = 512 * REG_SOFTMAX + 128 * REG_CONTROL;
@@ -41,8 +44,8 @@ struct DiffLseCfg {
 
 struct alignas(16) DiffLseBars {
     uint64_t q_full, q_empty;
-    uint64_t k_full[4], k_empty[4];
-    uint64_t s_full[2][2], s_free[2][2];                 // tile, buffer
+    uint64_t k_full[2], k_empty[2];
+    uint64_t s_full[2], s_free[2];                       // tile
     uint64_t half_full[2], half_free[2];                 // tile
     uint64_t drain;
     uint32_t tmem_base;
@@ -63,11 +66,12 @@ __device__ __forceinline__ void diff_key_bounds(const FwdParams& p, int N, int r
     }
 }
 
-// Some row of [a, a + 128) may not use some key of [c0, c0 + 128).
+// Some row of [a, a + 128) may not use some key of [c0, c0 + keys).
+template <int keys>
 __device__ __forceinline__ bool diff_edge(const FwdParams& p, int N, int a, int c0)
 {
-    return (c0 + 128 > N) || (p.causal && c0 + 127 > a) ||
-           (p.window > 0 && (c0 < a + 127 - p.window || (!p.causal && c0 + 127 > a + p.window)));
+    return (c0 + keys > N) || (p.causal && c0 + keys - 1 > a) ||
+           (p.window > 0 && (c0 < a + 127 - p.window || (!p.causal && c0 + keys - 1 > a + p.window)));
 }
 
 template <bool PK>
@@ -80,8 +84,8 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
     const FwdParams& p = dp.f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* ring_smem = q_smem + C::NQ * C::TILE;
-    DiffLseBars* bars = reinterpret_cast<DiffLseBars*>(ring_smem + C::NSLOT * C::TILE);
+    uint8_t* ring_smem = q_smem + C::Q_BYTES;
+    DiffLseBars* bars = reinterpret_cast<DiffLseBars*>(ring_smem + C::NSLOT * C::SLOT);
     const volatile int* abort_flag = &bars->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -100,11 +104,9 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
             mbar_init(smem_u32(&bars->k_full[s]), 1);
             mbar_init(smem_u32(&bars->k_empty[s]), 1);
         }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(smem_u32(&bars->s_full[i >> 1][i & 1]), 1);
-            mbar_init(smem_u32(&bars->s_free[i >> 1][i & 1]), 8);
-        }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars->s_full[i]), 1);
+            mbar_init(smem_u32(&bars->s_free[i]), 8);
             mbar_init(smem_u32(&bars->half_full[i]), 4);
             mbar_init(smem_u32(&bars->half_free[i]), 4);
         }
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
                     break;
                 }
                 const uint32_t qb = smem_u32(&bars->q_full);
-                mbar_arrive_expect_tx(qb, C::NQ * C::TILE);
+                mbar_arrive_expect_tx(qb, C::Q_BYTES);
 #pragma unroll
                 for (int i = 0; i < 2 * C::NQ; ++i)
                     tma_load_3d(smem_u32(q_smem + i * C::CB), &tmQ, qb, (i & 1) * 64, w.y0 + w.q0 + (i >> 1) * C::BM, w.z,
@@ -162,11 +164,11 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
                     }
                     if (++ring == (uint32_t)p.withhold_kv) continue;      // test hook: never arrives
                     const uint32_t fb = smem_u32(&bars->k_full[slot]);
-                    mbar_arrive_expect_tx(fb, C::TILE);
+                    mbar_arrive_expect_tx(fb, C::SLOT);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        tma_load_3d(smem_u32(ring_smem + slot * C::TILE + c * C::CB), &tmK, fb, c * 64,
-                                    w.y0 + (w.t0 + jj) * C::BN, zk, pol_k);
+                    for (int c = 0; c < 4; ++c)            // 64 columns of 256 keys, then the other 64
+                        tma_load_3d(smem_u32(ring_smem + slot * C::SLOT + c * C::CB), &tmK, fb, (c >> 1) * 64,
+                                    w.y0 + (w.t0 + jj) * C::BN + (c & 1) * 128, zk, pol_k);
                 }
             }
             if (!ok) timed_out();
@@ -199,16 +201,15 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (jj < L[i] || jj >= R[i]) continue;
-                    const uint32_t n = count[i]++, b = n & 1;
-                    if (!wait(&bars->s_free[i][b], ((n >> 1) & 1) ^ 1)) break;
+                    if (count[i] > 0 && !wait(&bars->s_free[i], (count[i] - 1) & 1)) break;
+                    ++count[i];
                     tc_fence_after_sync();
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk / 4) * C::CB + (kk % 4) * 32) >> 4;
-                        mma_ss_warp<false>(tmem + (2 * i + b) * C::BN, q_desc + ((i * C::TILE) >> 4) + off,
-                                           k_desc + ((slot * C::TILE) >> 4) + off, idesc, kk > 0 ? 1u : 0u);
-                    }
-                    mma_commit_warp(smem_u32(&bars->s_full[i][b]));
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_ss_warp<false>(tmem + i * C::BN, q_desc + (((2 * i + kk / 4) * C::CB + (kk % 4) * 32) >> 4),
+                                           k_desc + ((slot * C::SLOT + (kk / 4) * 2 * C::CB + (kk % 4) * 32) >> 4), idesc,
+                                           kk > 0 ? 1u : 0u);
+                    mma_commit_warp(smem_u32(&bars->s_full[i]));
                 }
                 if (!ok) break;
                 mma_commit_warp(smem_u32(&bars->k_empty[slot]));
@@ -223,9 +224,9 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
         __syncwarp();
     } else if (warp < C::COMPUTE_WARPS) {
         regs_increase<C::REG_SOFTMAX>();
-        constexpr int HC = C::BN / 2;
+        constexpr int HC = C::BN / 2, CH = 64;           // keys of a warpgroup, loaded at once
         const int tile = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3, trow = wq * 32 + lane;
-        const uint32_t s_addr = tmem + ((uint32_t)(wq * 32) << 16) + 2 * tile * C::BN + half * HC;
+        const uint32_t s_addr = tmem + ((uint32_t)(wq * 32) << 16) + tile * C::BN + half * HC;
         const float NEG_INF = -__int_as_float(0x7f800000), c = p.c_log2;
         uint32_t count = 0, uc = 0;
         bool ok = true;
@@ -242,49 +243,54 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
             float m_used = NEG_INF;
             float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             for (int jj = L; jj < R; ++jj) {
-                const int c0 = (w.t0 + jj) * C::BN;
-                const uint32_t b = count & 1;
-                ok = warp_wait(&bars->s_full[tile][b], (count >> 1) & 1);
+                const int c0 = (w.t0 + jj) * C::BN + half * HC;
+                ok = warp_wait(&bars->s_full[tile], count & 1);
                 ++count;
                 if (!ok) break;
                 tc_fence_after_sync();
-                uint32_t sr[HC];
+                const bool edge = diff_edge<HC>(p, w.N, a, c0);
 #pragma unroll
-                for (int ch = 0; ch < HC; ch += 32) tmem_ld32p(s_addr + b * C::BN + ch, sr + ch);
-                tmem_wait_ld_only();
+                for (int part = 0; part < HC / CH; ++part) {
+                    uint32_t sr[CH];
 #pragma unroll
-                for (int ch = 0; ch < HC; ch += 32) reg_fence32(sr + ch);
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[tile][b]));
-                float* s = reinterpret_cast<float*>(sr);
-                if (diff_edge(p, w.N, a, c0)) {
-                    const uint32_t first = (uint32_t)(c0 + half * HC - jlo);
+                    for (int ch = 0; ch < CH; ch += 32) tmem_ld32p(s_addr + part * CH + ch, sr + ch);
+                    tmem_wait_ld_only();
 #pragma unroll
-                    for (int e = 0; e < HC; ++e)
-                        if (first + (uint32_t)e > span) s[e] = NEG_INF;
-                }
-                float mx[4];
+                    for (int ch = 0; ch < CH; ch += 32) reg_fence32(sr + ch);
+                    if (part == HC / CH - 1) {
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[tile]));
+                    }
+                    float* s = reinterpret_cast<float*>(sr);
+                    if (edge) {
+                        const uint32_t first = (uint32_t)(c0 + part * CH - jlo);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float m = s[k];
+                        for (int e = 0; e < CH; ++e)
+                            if (first + (uint32_t)e > span) s[e] = NEG_INF;
+                    }
+                    float mx[4];
 #pragma unroll
-                    for (int u = 1; u + 1 < HC / 4; u += 2) m = fmax3(m, s[k + 4 * u], s[k + 4 * u + 4]);
-                    mx[k] = fmaxf(m, s[k + 4 * (HC / 4 - 1)]);
-                }
-                const float m_cand = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * c;
-                if (m_cand > m_used) {                    // a thread's own sums are all there is to rescale
-                    const float alpha = ex2(m_used - m_cand);    // ex2(-inf) = 0
+                    for (int k = 0; k < 4; ++k) {
+                        float m = s[k];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[k] = __fmul2_rn(acc[k], make_float2(alpha, alpha));
-                    m_used = m_cand;
-                }
-                const float mb = m_used == NEG_INF ? 0.0f : m_used;
-                const float2 c2 = make_float2(c, c), b2 = make_float2(-mb, -mb);
+                        for (int u = 1; u + 1 < CH / 4; u += 2) m = fmax3(m, s[k + 4 * u], s[k + 4 * u + 4]);
+                        mx[k] = fmaxf(m, s[k + 4 * (CH / 4 - 1)]);
+                    }
+                    const float m_cand = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * c;
+                    if (m_cand > m_used) {                // a thread's own sums are all there is to rescale
+                        const float alpha = ex2(m_used - m_cand);    // ex2(-inf) = 0
 #pragma unroll
-                for (int e = 0; e < HC / 2; ++e) {
-                    const float2 x = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), c2, b2);
-                    acc[e & 3] = __fadd2_rn(acc[e & 3], make_float2(ex2(x.x), ex2(x.y)));
+                        for (int k = 0; k < 4; ++k) acc[k] = __fmul2_rn(acc[k], make_float2(alpha, alpha));
+                        m_used = m_cand;
+                    }
+                    const float mb = m_used == NEG_INF ? 0.0f : m_used;
+                    const float2 c2 = make_float2(c, c), b2 = make_float2(-mb, -mb);
+#pragma unroll
+                    for (int e = 0; e < CH / 2; ++e) {
+                        const float2 x = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), c2, b2);
+                        acc[e & 3] = __fadd2_rn(acc[e & 3], make_float2(ex2(x.x), ex2(x.y)));
+                    }
                 }
             }
             if (!ok) break;
@@ -722,7 +728,7 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
                         pk[e / 2] = pack_bf16x2(r.x, r.y);
                     }
                 };
-                if (diff_edge(p, w.N, a0, c0)) weigh(std::true_type{});
+                if (diff_edge<C::BN>(p, w.N, a0, c0)) weigh(std::true_type{});
                 else weigh(std::false_type{});
                 // the product of the step before has read the weights
                 if (h > 0 && !wait_all(&bars->w_free, (h - 1) & 1)) break;
