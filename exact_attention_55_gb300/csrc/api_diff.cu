@@ -1,5 +1,6 @@
 // api_diff.cu -- the C ABI of rotary positions and of differential attention: argument checks,
 // tensor maps and launches.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -134,15 +135,18 @@ attn_status_t diff_fwd(const void* q, const void* k, const void* v, const float*
     p.lam = lam;
     p.H = s.H;
     p.Hkv = s.Hkv;
-    // d = 128 without O_2: two launches of 12 d products in place of one of 16 d (diff_fwd_wide.cu), where the one
-    // would take more than a round of the card and sequences (packed: their mean) are longer than a query block
-    // there.  Measured, one against two, causal, 16 heads over 4: 1024 tokens 24 us against 39, 1536 56 against 47,
-    // 4096 228 against 168; 64 x 256 tokens 14.5 against 19, 64 x 384 32 against 30; non-causal 512 12 against 21, 768 27
-    // against 26; a window of 128 1024 tokens 18 against 21, of 512 4096 tokens 89 against 82.
+    // d = 128 without O_2: two launches of 12 d products in place of one of 16 d (diff_fwd_wide.cu), where the one would
+    // take at least 25 steps of 128 x 128 scores an SM and there are units for every pair of SMs, half of them again.
+    // Measured, one against two, 16 heads over 4: causal 1536 tokens (16 steps) 41 us against 45, 2048 (29) 62
+    // against 54, 4096 198 against 159; 64 x 768 (18) 53 against 59, 64 x 1024 (30) 78 against 71; 4 heads, 4096 tokens
+    // (64 units) 54 against 84; non-causal 64 x 512 (13) 39 against 35, 64 x 768 (30) 75 against 71.
     cudaError_t e;
-    const int mean = packed ? s.T / s.num_seqs : s.N;
-    if (s.d == 128 && !o2 && mean > 256 && (p.f.window == 0 || p.f.window >= 256) &&
-        (p.f.unit_walk ? 2 * pairs : pairs) > dev->sm_count) {
+    const long long mean = packed ? s.T / s.num_seqs : s.N, seqs = packed ? s.num_seqs : s.B;
+    long long keys = s.causal ? mean / 2 + 64 : mean;     // that a row sees, with what its tiles mask
+    if (p.f.window > 0) keys = std::min(keys, (s.causal ? 1LL : 2LL) * p.f.window + 128);
+    const long long steps = heads * ((mean + 127) / 128) * ((keys + 127) / 128);
+    if (s.d == 128 && !o2 && mean > 256 && steps >= 25LL * dev->sm_count &&
+        4 * seqs * s.H * ((mean + 255) / 256) >= 3LL * dev->sm_count) {
         auto shape = [&](int heads_of, int walkers) {     // heads of one sequence; CTAs or pairs of them
             DiffFwdParams r = p;
             r.f.H = heads_of;

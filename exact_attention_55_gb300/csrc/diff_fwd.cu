@@ -24,6 +24,7 @@
 
 #include "attn_fwd.cuh"
 #include "diff_params.h"
+#include "diff_units.cuh"
 
 namespace gb300 {
 
@@ -31,6 +32,7 @@ template <int D, bool PK>
 struct DiffFwdCfg {
     static constexpr bool PACKED = PK;
     static constexpr int BM = 128, NQ = 1, BN = 128;     // a unit: 128 rows of a head, both maps
+    static constexpr int HEAD_DIM = D;
     static constexpr int VH = D / 64;                    // parts of 128 columns of a value head
     static constexpr int DV = 128;                       // value columns of a unit
     static constexpr int CB = 128 * 128;                 // 64 columns of a 128-row tile
@@ -58,10 +60,8 @@ struct alignas(16) DiffFwdBars {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t o_empty, sums_full;
-    uint64_t unit_full[2], unit_empty[2], steal;         // packed: units handed out
+    DiffHand hand;
     uint64_t drain;
-    uint4 stolen;
-    int handed[2];
     uint32_t tmem_base;
     int abort_flag;
     float inv[2][2][128];    // 1 / sum of the maps' rows, by the parity of the unit: one map's warps may be a
@@ -70,54 +70,6 @@ struct alignas(16) DiffFwdBars {
 constexpr int kDiffTabOffset = 3072;
 static_assert(sizeof(DiffFwdBars) <= kDiffTabOffset, "barrier block");
 static_assert(kDiffTabOffset + sizeof(SortTab) <= 5120, "schedule table");
-
-// Packed sequences: a block of the grid a unit, heads x 128-row tiles, the longest sequences' first and each one's
-// costliest first.  Blocks that run take over the work of blocks that were not launched yet, so the
-// costs even out by themselves (pairs dealt out in advance: the busiest SM 15 % above the mean at nine documents of
-// 200 to 5600 tokens x 8 heads).  False: the grid, laid out for the most tiles there can be, has no unit u.
-template <class C>
-__device__ __forceinline__ bool stolen_unit(int u, const FwdParams& p, Unit& w, const SortTab* tab)
-{
-    const int tile = u / p.H;
-    if (tile >= tab->total) return false;
-    int seq, rank, a, b;
-    sorted_pair(tab, p.num_seqs, tile, seq, rank);        // the table counts tiles of one head
-    seq_span(p.cu_seqlens, seq, p.T, a, b);
-    w.z = u - tile * p.H;
-    w.y0 = a;
-    w.N = b - a;
-    w.q0 = ((w.N + C::BM - 1) / C::BM - 1 - rank) * C::BM;
-    const int last = min(w.N, w.q0 + C::BM) - 1;
-    int lo = 0, hi = w.N;
-    if (p.window > 0) lo = max(0, w.q0 - p.window);
-    if (p.causal) hi = last + 1;
-    else if (p.window > 0) hi = min(w.N, last + p.window + 1);
-    w.t0 = lo / C::BN;
-    w.n = (hi + C::BN - 1) / C::BN - w.t0;
-    return true;
-}
-
-// Asks for a block that was not launched; the answer lands in `to` and counts 16 bytes on `bar`.
-__device__ __forceinline__ void steal_request(uint4* to, uint64_t* bar)
-{
-    fence_proxy_async_smem();                             // the last answer was read
-    mbar_arrive_expect_tx(smem_u32(bar), 16);
-    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                     smem_u32(to)),
-                 "r"(smem_u32(bar))
-                 : "memory");
-}
-// The block's number, or -1: there are no more.
-__device__ __forceinline__ int steal_answer(const uint4* from)
-{
-    uint32_t got, x;
-    asm volatile(
-        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tld.shared.b128 r, [%2];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
-        : "=&r"(got), "=&r"(x) : "r"(smem_u32(from)) : "memory");
-    return got ? (int)x : -1;
-}
 
 // Where a unit's rows live.
 struct DiffAt {
@@ -177,7 +129,7 @@ __global__ void __launch_bounds__(DiffFwdCfg<D, PK>::NUM_THREADS, 1)
     if constexpr (C::PACKED) {
         if (p.num_seqs <= kSortMaxSeqs) {
             SortTab* t = reinterpret_cast<SortTab*>(reinterpret_cast<uint8_t*>(bars) + kDiffTabOffset);
-            build_sort_tab<C::BM / 2>(p.cu_seqlens, p.num_seqs, p.T, 1, t);    // pairs of 64 rows: tiles
+            build_diff_tab<C>(p, t);
             tab = t;
         }
     }
@@ -192,10 +144,8 @@ __global__ void __launch_bounds__(DiffFwdCfg<D, PK>::NUM_THREADS, 1)
             mbar_init(smem_u32(&bars->s_full[i]), 1);
             mbar_init(smem_u32(&bars->p_full[i]), 4);
             mbar_init(smem_u32(&bars->pv_done[i]), 1);
-            mbar_init(smem_u32(&bars->unit_full[i]), 1);
-            mbar_init(smem_u32(&bars->unit_empty[i]), C::NUM_SOFTMAX_WARPS + 1);
         }
-        mbar_init(smem_u32(&bars->steal), 1);
+        bars->hand.init(C::NUM_SOFTMAX_WARPS + 1);
         mbar_init(smem_u32(&bars->o_empty), 8);
         mbar_init(smem_u32(&bars->sums_full), 8);
         mbar_init(smem_u32(&bars->drain), 1);
@@ -220,26 +170,7 @@ __global__ void __launch_bounds__(DiffFwdCfg<D, PK>::NUM_THREADS, 1)
         *reinterpret_cast<volatile int*>(&bars->abort_flag) = 1;
     };
 
-    // A consumer warp's next unit (all lanes): the one that the producer handed out, or of the walk.
-    int su = 0;
-    uint32_t units = 0;
-    auto take = [&](Unit& w, bool& ok) -> bool {
-        if (C::PACKED && tab != nullptr) {
-            const uint32_t b = units & 1;
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->unit_full[b]), (units >> 1) & 1, abort_flag, p.timeout_ns));
-            if (!ok) return false;
-            const int u = *reinterpret_cast<const volatile int*>(&bars->handed[b]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->unit_empty[b]));
-            ++units;
-            return u >= 0 && stolen_unit<C>(u, p, w, tab);
-        }
-        while (true) {
-            su = units++ == 0 ? first_sub<C>(p) : next_sub<C>(su, p, tab);
-            if (su >= num_subs(p, tab)) return false;
-            if (unit_of<C>(su, p, w, tab)) return true;
-        }
-    };
+    DiffUnits<C> units(dp, tab, &bars->hand, abort_flag);
 
     if (warp == C::PRODUCER_WARP) {
         // ------------------------------------------------------------ TMA producer
@@ -262,42 +193,8 @@ __global__ void __launch_bounds__(DiffFwdCfg<D, PK>::NUM_THREADS, 1)
                 ++ring;
                 return slot;
             };
-            // the next unit: of the walk, or this block's own and then those of blocks that were not launched.  The one
-            // behind it is asked for at once, and its number handed on.
-            const bool stealing = C::PACKED && tab != nullptr;
-            int mine = (int)blockIdx.x;
-            uint32_t asked = 0, answered = 0;
-            auto answer = [&](unsigned long long limit) -> bool {
-                if (!mbar_wait(smem_u32(&bars->steal), answered & 1, abort_flag, limit)) return false;
-                ++answered;
-                mine = steal_answer(&bars->stolen);
-                return true;
-            };
-            auto give = [&](Unit& w) -> bool {
-                if (!stealing) return take(w, ok);
-                bool there = false;
-                while (ok && !there) {
-                    if (asked > 0 && !answer(p.timeout_ns)) {
-                        ok = false;
-                        return false;
-                    }
-                    if (mine < 0) break;
-                    steal_request(&bars->stolen, &bars->steal);
-                    ++asked;
-                    there = stolen_unit<C>(mine, p, w, tab);
-                }
-                const uint32_t b = units & 1;
-                if (!mbar_wait(smem_u32(&bars->unit_empty[b]), ((units >> 1) & 1) ^ 1, abort_flag, p.timeout_ns)) {
-                    ok = false;
-                    return false;
-                }
-                *reinterpret_cast<volatile int*>(&bars->handed[b]) = mine;
-                mbar_arrive(smem_u32(&bars->unit_full[b]));
-                ++units;
-                return there;
-            };
             Unit w;
-            while (ok && give(w)) {
+            while (ok && units.give(w, ok)) {
                 const DiffAt at = diff_at<C>(dp, w);
                 if (!mbar_wait(smem_u32(&bars->q_empty), (uc & 1) ^ 1, abort_flag, p.timeout_ns)) {
                     ok = false;
@@ -338,13 +235,7 @@ __global__ void __launch_bounds__(DiffFwdCfg<D, PK>::NUM_THREADS, 1)
                 }
             }
             if (!ok) timed_out();
-            // what was asked for lands too; after an abort the blocks that were not launched are not needed
-            while (asked > answered && mbar_wait(smem_u32(&bars->steal), answered & 1, nullptr, kCleanupTimeoutNs)) {
-                ++answered;
-                if (steal_answer(&bars->stolen) < 0) break;
-                steal_request(&bars->stolen, &bars->steal);
-                ++asked;
-            }
+            units.finish(ok);
             // every copy issued lands before shared memory is released
             const uint32_t armed = ring < C::NSLOT ? ring : C::NSLOT;
             for (uint32_t k = ring - armed; k < ring; ++k) {
@@ -406,7 +297,7 @@ __global__ void __launch_bounds__(DiffFwdCfg<D, PK>::NUM_THREADS, 1)
             }
         };
         Unit w;
-        while (ok && take(w, ok)) {
+        while (ok && units.take(w, ok)) {
             if (!wait(&bars->q_full, uc & 1)) break;
             for (int jj = 0; jj <= w.n && ok; ++jj) {
                 // ring positions: V of step jj - 1, keys of step jj behind it
@@ -460,7 +351,7 @@ __global__ void __launch_bounds__(DiffFwdCfg<D, PK>::NUM_THREADS, 1)
             return r;
         };
         Unit w;
-        while (ok && take(w, ok)) {
+        while (ok && units.take(w, ok)) {
             const int a = w.q0, row = a + row_in_tile;
             // keys allowed for row r: [lo, hi]; both grow with r
             auto key_bounds = [&](int r, int& lo, int& hi) {
@@ -645,13 +536,8 @@ static cudaError_t launch_diff_fwd_t(const DiffFwdMaps& m, const DiffFwdParams& 
     if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
     if (attr.numRegs * C::NUM_THREADS < C::REG_POOL) return cudaErrorInvalidConfiguration;
     DiffFwdParams p = given;
-    int grid = fwd_grid(p.f, sm_count);
-    set_fwd_walk(p.f, grid);
-    if (PK && p.f.num_seqs <= kSortMaxSeqs) {             // a block for every unit there can be
-        const long long most = ((long long)p.f.T / C::BM + p.f.num_seqs) * p.f.H;
-        if (most > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-        grid = (int)most;
-    }
+    const int grid = diff_grid<C>(p, sm_count);
+    if (grid < 1) return cudaErrorInvalidConfiguration;
     kernel<<<grid, C::NUM_THREADS, C::SMEM_BYTES, stream>>>(m.q, m.k, m.v, p);
     return cudaGetLastError();
 }

@@ -16,6 +16,7 @@
 
 #include "attn_fwd.cuh"
 #include "diff_params.h"
+#include "diff_units.cuh"
 
 namespace gb300 {
 
@@ -29,7 +30,7 @@ namespace gb300 {
 template <bool PK>
 struct DiffLseCfg {
     static constexpr bool PACKED = PK;
-    static constexpr int BM = 128, NQ = 2, BN = 256, D = 128;
+    static constexpr int BM = 128, NQ = 2, BN = 256, D = 128, HEAD_DIM = D;
     static constexpr int CB = 128 * 128;                 // 64 columns of 128 rows
     static constexpr int Q_BYTES = 2 * NQ * CB, SLOT = 4 * CB;
     static constexpr int NSLOT = 2;
@@ -47,6 +48,7 @@ struct alignas(16) DiffLseBars {
     uint64_t k_full[2], k_empty[2];
     uint64_t s_full[2], s_free[2];                       // tile
     uint64_t half_full[2], half_free[2];                 // tile
+    DiffHand hand;
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
     if constexpr (C::PACKED) {
         if (p.num_seqs <= kSortMaxSeqs) {
             SortTab* t = reinterpret_cast<SortTab*>(reinterpret_cast<uint8_t*>(bars) + C::TAB_OFF);
-            build_sort_tab<C::NQ * C::BM>(p.cu_seqlens, p.num_seqs, p.T, p.H, t);
+            build_diff_tab<C>(p, t);
             tab = t;
         }
     }
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
             mbar_init(smem_u32(&bars->half_full[i]), 4);
             mbar_init(smem_u32(&bars->half_free[i]), 4);
         }
+        bars->hand.init(C::COMPUTE_WARPS + 1);
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort_flag = 0;
         fence_mbar_init();
@@ -133,15 +136,16 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
         return __all_sync(0xffffffffu, mbar_wait(a, parity, abort_flag, p.timeout_ns));
     };
 
+    DiffUnits<C> units(dp, tab, &bars->hand, abort_flag);
+
     if (warp == C::PRODUCER_WARP) {
         regs_decrease<C::REG_CONTROL>();
         if (lane == 0) {
             const uint64_t pol_q = l2_policy_evict_first(), pol_k = l2_policy_evict_last();
             uint32_t ring = 0, uc = 0;
             bool ok = true;
-            for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
-                Unit w;
-                if (!unit_of<C>(su, p, w, tab)) continue;
+            Unit w;
+            while (ok && units.give(w, ok)) {
                 if (!mbar_wait(smem_u32(&bars->q_empty), (uc & 1) ^ 1, abort_flag, p.timeout_ns)) {
                     ok = false;
                     break;
@@ -172,6 +176,7 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
                 }
             }
             if (!ok) timed_out();
+            units.finish(ok);
             // every copy issued lands before shared memory is released
             for (uint32_t k = ring < C::NSLOT ? 0 : ring - C::NSLOT; k < ring; ++k)
                 if (k + 1 != (uint32_t)p.withhold_kv)
@@ -188,9 +193,8 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
             ok = ok && warp_wait(bar, parity);
             return ok;
         };
-        for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
-            Unit w;
-            if (!unit_of<C>(su, p, w, tab)) continue;
+        Unit w;
+        while (ok && units.take(w, ok)) {
             int L[2], R[2];
             tile_steps<C>(w, 0, p, L[0], R[0]);
             tile_steps<C>(w, 1, p, L[1], R[1]);
@@ -230,9 +234,8 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
         const float NEG_INF = -__int_as_float(0x7f800000), c = p.c_log2;
         uint32_t count = 0, uc = 0;
         bool ok = true;
-        for (int su = first_sub<C>(p); su < num_subs(p, tab) && ok; su = next_sub<C>(su, p, tab)) {
-            Unit w;
-            if (!unit_of<C>(su, p, w, tab)) continue;
+        Unit w;
+        while (ok && units.take(w, ok)) {
             int L, R;
             tile_steps<C>(w, tile, p, L, R);
             const int a = w.q0 + tile * C::BM, row = a + trow;
@@ -779,16 +782,15 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
 }
 
 template <class C, class Kernel, class... Args>
-static cudaError_t launch_one(Kernel kernel, int cluster, FwdParams& f, int sm_count, cudaStream_t stream, const Args&... args)
+static cudaError_t launch_one(Kernel kernel, int grid, int cluster, cudaStream_t stream, const Args&... args)
 {
+    if (grid < 1) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     // setmaxnreg.inc would wait forever if the launch pool were smaller than the split
     cudaFuncAttributes attr;
     if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
     if (attr.numRegs * C::NUM_THREADS < C::REG_POOL) return cudaErrorInvalidConfiguration;
-    const int grid = fwd_grid(f, sm_count / cluster);     // CTAs or pairs that walk the units
-    set_fwd_walk(f, grid);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute pair[1];
     pair[0].id = cudaLaunchAttributeClusterDimension;
@@ -797,7 +799,7 @@ static cudaError_t launch_one(Kernel kernel, int cluster, FwdParams& f, int sm_c
     cfg.attrs = pair;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
     cfg.stream = stream;
-    cfg.gridDim = dim3((unsigned)(grid * cluster));
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(C::NUM_THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
@@ -806,9 +808,12 @@ static cudaError_t launch_one(Kernel kernel, int cluster, FwdParams& f, int sm_c
 template <bool PK>
 static cudaError_t launch_wide(const DiffFwdMaps& m, DiffFwdParams& lse, DiffFwdParams& out, int sm_count, cudaStream_t stream)
 {
-    const cudaError_t e = launch_one<DiffLseCfg<PK>>(diff_lse_kernel<PK>, 1, lse.f, sm_count, stream, m.q, m.k, lse);
+    const int grid = diff_grid<DiffLseCfg<PK>>(lse, sm_count);
+    const cudaError_t e = launch_one<DiffLseCfg<PK>>(diff_lse_kernel<PK>, grid, 1, stream, m.q, m.k, lse);
     if (e != cudaSuccess) return e;
-    return launch_one<DiffOutCfg<PK>>(diff_out_kernel<PK>, 2, out.f, sm_count, stream, m.q, m.k64, m.v64, out);
+    const int pairs = fwd_grid(out.f, sm_count / 2);
+    set_fwd_walk(out.f, pairs);
+    return launch_one<DiffOutCfg<PK>>(diff_out_kernel<PK>, 2 * pairs, 2, stream, m.q, m.k64, m.v64, out);
 }
 
 cudaError_t launch_diff_fwd_wide(const DiffFwdMaps& m, DiffFwdParams lse, DiffFwdParams out, int sm_count,

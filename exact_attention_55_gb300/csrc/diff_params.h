@@ -39,6 +39,7 @@ struct DiffFwdParams {
     void* o2;               // the second map's output, laid out as o, or null
     const float* lam;       // fp32 [H]
     int H, Hkv;
+    int group;              // heads (f's) whose units are handed out together, set at launch
 };
 
 struct DiffFwdMaps {

@@ -1,5 +1,5 @@
-"""Differential attention's forward pass at d = 128 without O_2 in its two-launch form (many heads, long
-sequences) against the plain 64-bit form, with the bounds of the one-launch form: the weights' difference is
+"""Differential attention's forward pass at d = 128 without O_2 in its two-launch form (at least 25 steps of
+128 x 128 scores an SM: hundreds of heads here, of which some are checked) against the plain 64-bit form, with the bounds of the one-launch form: the weights' difference is
 rounded once, which is off by no more than its two terms rounded by themselves."""
 import math
 
@@ -44,12 +44,12 @@ def compare(m, q, k, v, lam, causal, window, scale=None, batches=None):
 @pytest.mark.parametrize("N", [257, 300, 383, 384, 385, 512, 640, 769])
 @pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 256), (False, 300)])
 def test_batched(N, causal, window):
-    compare(fa(), *batched(12, 8, 8, N), weights(8), causal, window, batches=(0, 5, 11))
+    compare(fa(), *batched(40, 8, 8, N), weights(8), causal, window, batches=(0, 19, 39))
 
 
 @pytest.mark.parametrize("H,G", [(1, 1), (3, 1), (4, 2), (12, 3)])
 def test_shared_heads(H, G):
-    B = 120 // H
+    B = 204 // H
     compare(fa(), *batched(B, H, G, 400), weights(H), True, 0, 0.2, batches=(0, B // 2, B - 1))
 
 
@@ -62,7 +62,7 @@ def test_many_tiles_and_large_scores():
 
 def test_weights_of_zero_and_of_equal_maps():
     m = fa()
-    q, k, v = batched(12, 8, 8, 300, seed=21)
+    q, k, v = batched(40, 8, 8, 300, seed=21)
     compare(m, q, k, v, torch.zeros(8), True, 0, batches=(3,))
     q[:, 1::2], k[:, 1::2] = q[:, ::2], k[:, ::2]
     o, _, _ = m.attn_diff_fwd_bf16(q.cuda(), k.cuda(), v.cuda(), torch.ones(8).cuda(), causal=True)
@@ -74,7 +74,7 @@ def test_weights_of_zero_and_of_equal_maps():
 def test_packed(lens, causal, window):
     """Rows before the first sequence and behind the last are NaN on the way in, and left as they were."""
     m = fa()
-    H, G, lead, trail = 32, 8, 3, 70
+    H, G, lead, trail = 64, 16, 3, 70
     T = lead + sum(lens) + trail
     q, k, v = make((T, 2 * H, D), 31), make((T, 2 * G, D), 32), make((T, G, 2 * D), 33)
     for t in (q, k, v):
@@ -87,7 +87,7 @@ def test_packed(lens, causal, window):
                                 o=o, lse=lse)
     assert m.attn_get_device_status() == m.ATTN_OK
     assert (o[:lead] == 7).all() and (o[T - trail:] == 7).all() and (lse[:, :lead] == 7).all() and (lse[:, T - trail:] == 7).all()
-    some = [0, 1, 2, 7, 30, 31]                     # value groups of four heads
+    some = [0, 1, 2, 7, 62, 63]                     # value groups of four heads
     for s, n in enumerate(lens):
         if n == 0:
             continue
@@ -103,7 +103,7 @@ def test_packed(lens, causal, window):
 def test_sequences_between_nan():
     """A sequence's neighbours in memory do not reach it."""
     m = fa()
-    H, lens = 40, [300, 333, 400]
+    H, lens = 80, [300, 333, 400]
     T = sum(lens)
     q, k, v = make((T, 2 * H, D), 41).cuda(), make((T, 2 * H, D), 42).cuda(), make((T, H, 2 * D), 43).cuda()
     cu, lam = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda(), weights(H).cuda()
@@ -121,8 +121,8 @@ def test_more_sequences_than_the_table():
     m = fa()
     lens = [257 + 7 * (i % 5) for i in range(230)]
     T = sum(lens)
-    q, k, v = make((T, 2, D), 51), make((T, 2, D), 52), make((T, 1, 2 * D), 53)
-    cu, lam = torch.tensor([0] + lens).cumsum(0).to(torch.int32), weights(1)
+    q, k, v = make((T, 4, D), 51), make((T, 2, D), 52), make((T, 1, 2 * D), 53)
+    cu, lam = torch.tensor([0] + lens).cumsum(0).to(torch.int32), weights(2)
     o, lse, _ = m.attn_diff_fwd_bf16_varlen(q.cuda(), k.cuda(), v.cuda(), lam.cuda(), cu.cuda(), max(lens), causal=True)
     assert m.attn_get_device_status() == m.ATTN_OK
     for s in (0, 1, 100, 228, 229):
@@ -137,13 +137,13 @@ def test_infinite_keys():
     """A key whose scores are -inf for every query has no weight; rows that see no other have an LSE of -inf and
     an output of 0; a NaN score makes its row's output and LSE NaN."""
     m = fa()
-    q, k, v = batched(12, 8, 8, 300, seed=61)
+    q, k, v = batched(40, 8, 8, 300, seed=61)
     q = q.abs() + 0.1
     k[:, :, 0] = -float("inf")
     k[2, 0, 250] = float("nan")
     o, lse, _ = m.attn_diff_fwd_bf16(q.cuda(), k.cuda(), v.cuda(), weights(8).cuda(), causal=True)
     assert not o[:, :, 0].any() and (lse[:, :, 0] == -float("inf")).all()
-    keep = torch.ones(12, 8, 300, dtype=torch.bool)
+    keep = torch.ones(40, 8, 300, dtype=torch.bool)
     keep[2, 0, 250:] = False
     assert torch.equal(o.cpu().isnan().any(-1), ~keep)
     assert lse[2, 0, 250:].isnan().all() and not lse[2, 1].isnan().any()
@@ -154,6 +154,9 @@ def test_same_bits_every_time_streams_and_graph():
     q, k, v = (t.cuda() for t in batched(10, 8, 4, 700, seed=71))
     lam = weights(8).cuda()
     first = m.attn_diff_fwd_bf16(q, k, v, lam, causal=True)[:2]
+    # the one-launch form, which gives O_2 too, rounds the maps' weights one by one
+    one = m.attn_diff_fwd_bf16(q, k, v, lam, causal=True, save_o2=True)[0]
+    assert not torch.equal(one, first[0]) and (one - first[0]).abs().max() < 0.1
     side = [torch.cuda.Stream() for _ in range(2)]
     for s in side:
         s.wait_stream(torch.cuda.current_stream())
@@ -179,8 +182,8 @@ def test_same_bits_every_time_streams_and_graph():
 @pytest.mark.parametrize("withheld", [0, 1, 2, 5])
 def test_withheld_load(withheld):
     m = fa()
-    q, k, v = (t.cuda() for t in batched(1, 40, 40, 600, seed=81))
-    lam = weights(40).cuda()
+    q, k, v = (t.cuda() for t in batched(2, 65, 65, 600, seed=81))
+    lam = weights(65).cuda()
     want = m.attn_diff_fwd_bf16(q, k, v, lam, causal=True)
     assert m.attn_get_device_status() == m.ATTN_OK
     m.attn_selftest_diff_fwd_withheld_load(q, k, v, lam, torch.empty_like(want[0]), torch.empty_like(want[1]), causal=True,
