@@ -29,6 +29,9 @@
 // accumulation of step j - 1, then S(j + 1), and the tensor pipe works on X(j) and S(j + 1) while both
 // compute warpgroups (half of the columns each) turn steps j - 1 and j.
 //
+// Measured, 4 x 8 heads x 4096 tokens of d = 64, causal: 590 us = 582 TFLOP/s of 20 d (1164 executed); a step takes
+// 1630 to 1740 cycles for 1024 of products.  Packed, 8 heads over 2, 8192 tokens of d = 128, window 2047: 375 us.
+//
 // What this was measured against, on 4 x 8 heads x 4096 tokens of d = 64, causal, all passes:
 // steps of 64 columns with three TMEM buffers and a warpgroup each 1140 us, with quick waits 894.
 // The tensor pipe was busy for a quarter of it: its queue holds about 8 MMAs, and a wait, even for what

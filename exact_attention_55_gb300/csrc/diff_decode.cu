@@ -20,6 +20,7 @@
 //     (0 | q_2) in the same accumulator, and V is multiplied once for both.  Otherwise the columns
 //     of a product are one map's, and V's fragments are used for both.
 //     A tcgen05 tile would be at least 64 rows high, mostly empty.
+// Measured, 16 sequences x 8 heads x 8192 keys of d = 128 (1.07 GB): 158.8 us = 6.76 TB/s.
 // Scores, weights' sums and O are fp32.  A weight, relative to a running maximum that it may pass by
 // 2^8, enters as two bf16 numbers, what it rounds to and the rest, off by 2^-17 of it (one of them
 // would double O's error, 0.0017 to 0.0026 relative at 16 x 8 heads x 8192 keys; the second product

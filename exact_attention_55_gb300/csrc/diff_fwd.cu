@@ -17,8 +17,11 @@
 // unit takes one half of its columns and the scores are computed for each half: 16 d products
 // per pair of tokens instead of 12 d.  (Each half reads the same q and k from L2.)
 //
-// Several heads may read one pair of key heads (H / Hkv): their units are neighbours in the
-// walk, so they share its tiles in L2.
+// Several heads may read one pair of key heads (H / Hkv): their units are handed out together
+// (diff_units.cuh), so they share its tiles in L2.
+//
+// Measured, one sequence of 16384 tokens, 8 heads over 4 of d = 64, causal, with O_2: 650 us = 1269 TFLOP/s of 12 d;
+// a step of both maps takes about 2900 cycles for 1536 of products, which the softmax warps need for its 32768 scores.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

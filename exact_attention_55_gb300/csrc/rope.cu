@@ -16,7 +16,7 @@
 // Bound by memory: 4 bytes of traffic an element against half a multiplication.  A thread turns the
 // same eight pairs (two 16-byte pieces of a row) of up to eight heads of its token, so an angle's
 // instructions are shared by them; neighbouring threads take neighbouring pieces and heads.  Measured,
-// 8191 tokens of 32 + 8 heads of d 128 on three axes: 33.8 us = 4.97 TB/s (36.8 with sincospif, 38.9
+// 8191 tokens of 32 + 8 heads of d 128 on three axes: 33.2 us = 5.05 TB/s (36.8 with sincospif, 38.9
 // with a block's angles shared through shared memory, 41 with several tokens a thread and their
 // frequencies kept); blocks of 64 threads end more evenly than of 128 (34.8) or 256 (36.7).
 #include <cuda_bf16.h>
