@@ -35,7 +35,7 @@ template <int D, bool PK>
 struct DiffFwdCfg {
     static constexpr bool PACKED = PK;
     static constexpr int BM = 128, NQ = 1, BN = 128;     // a unit: 128 rows of a head, both maps
-    static constexpr int HEAD_DIM = D;
+    static constexpr int HEAD_DIM = D, CLUSTER = 1;
     static constexpr int VH = D / 64;                    // parts of 128 columns of a value head
     static constexpr int DV = 128;                       // value columns of a unit
     static constexpr int CB = 128 * 128;                 // 64 columns of a 128-row tile

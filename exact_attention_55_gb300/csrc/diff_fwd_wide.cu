@@ -8,7 +8,8 @@
 // 2 d and two products of 2 d for each half).  With the L_m known the maps' weights are subtracted before the
 // product, and one accumulator of 256 columns takes it: 4 d products for the L_m, 4 d for the scores
 // again, 4 d for O: 12 d, with as many exponentials, and no rescaling in the second launch.
-// Measured, 16 heads over 4 key pairs, 16384 tokens, causal: 3020 us in one launch, 2435 in two.
+// Measured, 16 heads over 4 key pairs, 16384 tokens, causal: 3020 us in one launch, 2035 in two
+// (1620 TFLOP/s of 12 d).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,7 +31,7 @@ namespace gb300 {
 template <bool PK>
 struct DiffLseCfg {
     static constexpr bool PACKED = PK;
-    static constexpr int BM = 128, NQ = 2, BN = 256, D = 128, HEAD_DIM = D;
+    static constexpr int BM = 128, NQ = 2, BN = 256, D = 128, HEAD_DIM = D, CLUSTER = 1;
     static constexpr int CB = 128 * 128;                 // 64 columns of 128 rows
     static constexpr int Q_BYTES = 2 * NQ * CB, SLOT = 4 * CB;
     static constexpr int NSLOT = 2;
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
 template <bool PK>
 struct DiffOutCfg {
     static constexpr bool PACKED = PK;
-    static constexpr int BM = 128, NQ = 2, BN = 128, D = 128;
+    static constexpr int BM = 128, NQ = 2, BN = 128, D = 128, HEAD_DIM = D, CLUSTER = 2;
     static constexpr int CB = 128 * 128, HB = 64 * 128;              // 64 columns of 128 rows, of 64
     static constexpr int Q_BYTES = 4 * CB, W_BYTES = 2 * CB, SLOT = 2 * HB, NSLOT = 8;
     static constexpr int TAB_OFF = 384, BAR_BYTES = 384 + 1792;
@@ -362,49 +363,16 @@ struct alignas(16) DiffOutBars {
     uint64_t q_full, q_empty;
     uint64_t kv_full[8], kv_empty[8];
     uint64_t s_full, s_free, w_full, w_free, o_full, o_empty;      // s_free, w_full and o_empty: CTA 0's count both
+    DiffHand hand;
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
 };
 static_assert(sizeof(DiffOutBars) <= 384, "barrier block");
 
-// The walk of attn_fwd.cuh by clusters: cluster c of G.
-template <class C>
-__device__ __forceinline__ int pair_first_sub(const FwdParams& p, int c)
-{
-    return C::PACKED ? 2 * c : c * p.walk_first;
-}
-template <class C>
-__device__ __forceinline__ int pair_next_sub(int s, const FwdParams& p, const SortTab* tab, int c, int G)
-{
-    if constexpr (C::PACKED) {
-        if (!(s & 1)) return s + 1;
-        if (tab == nullptr) return s + 2 * G - 1;
-        const int r = (s >> 1) / G + 1;                    // snake order, as snake_next_sub
-        return 2 * (r * G + ((r & 1) ? G - 1 - c : c));
-    } else {
-        return s + 1 + (((s + p.walk_a) % p.walk_m == 0) ? 0 : p.walk_step);
-    }
-}
-
-__device__ __forceinline__ uint32_t pair_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void pair_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// One arrival on CTA 0's barrier at this place.  No thread reads what the other CTA's threads wrote: operands pass from
-// TMA, or behind their writers' proxy fences, to the tensor cores, and TMEM behind its fences.  So the order within
-// the CTA is enough (a release to the cluster took the compute warps a memory barrier at each: 1440 us became 2130).
-__device__ __forceinline__ void pair_arrive(uint64_t* bar)
-{
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void pair_mma_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               uint32_t accumulate)
@@ -439,7 +407,7 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
     DiffOutBars* bars = reinterpret_cast<DiffOutBars*>(ring_smem + C::NSLOT * C::SLOT);
     const volatile int* abort_flag = &bars->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)pair_rank(), cid = (int)blockIdx.x / 2, clusters = (int)gridDim.x / 2;
+    const int rank = (int)pair_rank();
     if ((smem_u32(smem) & 1023) != 0) {                    // no kernel of this file has static shared memory
         if (threadIdx.x == 0) atomicExch(p.status, kStatusTimeout);
         return;
@@ -449,7 +417,7 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
     if constexpr (C::PACKED) {
         if (p.num_seqs <= kSortMaxSeqs) {
             SortTab* t = reinterpret_cast<SortTab*>(reinterpret_cast<uint8_t*>(bars) + C::TAB_OFF);
-            build_sort_tab<C::NQ * C::BM>(p.cu_seqlens, p.num_seqs, p.T, p.H, t);
+            build_diff_tab<C>(p, t);
             tab = t;
         }
     }
@@ -468,6 +436,7 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
         mbar_init(smem_u32(&bars->w_free), 1);
         mbar_init(smem_u32(&bars->o_full), 1);
         mbar_init(smem_u32(&bars->o_empty), 16);
+        bars->hand.init(9);                                // the MMA warp and the compute warps
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort_flag = 0;
         fence_mbar_init();
@@ -493,6 +462,8 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
         return __all_sync(0xffffffffu, mbar_wait(a, parity, abort_flag, p.timeout_ns));
     };
 
+    DiffUnits<C> units(dp, tab, &bars->hand, abort_flag);
+
     if (warp == C::PRODUCER_WARP) {
         regs_decrease<C::REG_CONTROL>();
         if (lane == 0) {
@@ -511,9 +482,8 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
                 mbar_arrive_expect_tx(smem_u32(&bars->kv_full[slot]), C::SLOT);
                 return true;
             };
-            for (int su = pair_first_sub<C>(p, cid); su < num_subs(p, tab) && ok; su = pair_next_sub<C>(su, p, tab, cid, clusters)) {
-                Unit w;
-                if (!unit_of<C>(su, p, w, tab)) continue;
+            Unit w;
+            while (ok && units.give(w, ok)) {
                 // heads of q (map 1), of V, of k (map 1)
                 const int b = C::PACKED ? 0 : w.z / dp.H, zv = b * dp.Hkv + (w.z - b * dp.H) / G, zk = 2 * zv;
                 if (!mbar_wait(smem_u32(&bars->q_empty), (uc & 1) ^ 1, abort_flag, p.timeout_ns)) {
@@ -551,6 +521,7 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
                 }
             }
             if (!ok) timed_out();
+            units.finish(ok);
             // every copy issued lands before shared memory is released (after an abort the other CTA's word may not
             // come: a millisecond is enough for the copies)
             const unsigned long long limit = ok ? kCleanupTimeoutNs : 1000000ull;
@@ -625,9 +596,8 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
             __syncwarp();
             if (lane == 0) pair_arrive(bar);
         };
-        for (int su = pair_first_sub<C>(p, cid); su < num_subs(p, tab) && ok; su = pair_next_sub<C>(su, p, tab, cid, clusters)) {
-            Unit w;
-            if (!unit_of<C>(su, p, w, tab)) continue;
+        Unit w;
+        while (ok && units.take(w, ok)) {
             if (!wait(&bars->q_full, uc & 1)) break;
             if (rank == 0) {
                 if (!issue_s()) break;
@@ -676,9 +646,8 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
             ok = ok && warp_wait(bar, parity);
             return ok;
         };
-        for (int su = pair_first_sub<C>(p, cid); su < num_subs(p, tab) && ok; su = pair_next_sub<C>(su, p, tab, cid, clusters)) {
-            Unit w;
-            if (!unit_of<C>(su, p, w, tab)) continue;
+        Unit w;
+        while (ok && units.take(w, ok)) {
             const int a0 = w.q0 + rank * C::BM, row = a0 + trow, head = C::PACKED ? w.z : w.z % dp.H;
             const bool valid = row < w.N;
             int jlo, jhi;
@@ -811,9 +780,8 @@ static cudaError_t launch_wide(const DiffFwdMaps& m, DiffFwdParams& lse, DiffFwd
     const int grid = diff_grid<DiffLseCfg<PK>>(lse, sm_count);
     const cudaError_t e = launch_one<DiffLseCfg<PK>>(diff_lse_kernel<PK>, grid, 1, stream, m.q, m.k, lse);
     if (e != cudaSuccess) return e;
-    const int pairs = fwd_grid(out.f, sm_count / 2);
-    set_fwd_walk(out.f, pairs);
-    return launch_one<DiffOutCfg<PK>>(diff_out_kernel<PK>, 2 * pairs, 2, stream, m.q, m.k64, m.v64, out);
+    const int pairs = diff_grid<DiffOutCfg<PK>>(out, sm_count);
+    return launch_one<DiffOutCfg<PK>>(diff_out_kernel<PK>, pairs, 2, stream, m.q, m.k64, m.v64, out);
 }
 
 cudaError_t launch_diff_fwd_wide(const DiffFwdMaps& m, DiffFwdParams lse, DiffFwdParams out, int sm_count,

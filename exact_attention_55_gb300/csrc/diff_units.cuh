@@ -10,6 +10,8 @@
 // Order: the longest sequence first; within it groups of heads whose keys and values fit in L2 together; in a
 // group the costliest rows first under a causal mask, of all its heads, so that the last units are short.
 // Packed calls with more sequences than the sorted table holds walk pairs as attn_fwd.cuh does.
+//
+// With CLUSTER = 2 a unit is a cluster's: CTA 0 asks for both, and the answer lands in both.
 #pragma once
 
 #include "attn_fwd.cuh"
@@ -20,7 +22,7 @@ namespace gb300 {
 // The hand-over of units from a block's producer, in shared memory.
 struct alignas(16) DiffHand {
     uint4 stolen;
-    uint64_t full[2], empty[2], steal;
+    uint64_t full[2], empty[2], steal, ready;              // ready: CTA 1 can take an answer
     int unit[2];
 
     __device__ __forceinline__ void init(int consumer_warps)
@@ -30,6 +32,7 @@ struct alignas(16) DiffHand {
             mbar_init(smem_u32(&empty[i]), consumer_warps);
         }
         mbar_init(smem_u32(&steal), 1);
+        mbar_init(smem_u32(&ready), 1);
     }
 };
 
@@ -81,17 +84,59 @@ __device__ __forceinline__ bool diff_unit(int u, const DiffFwdParams& dp, Unit& 
     return true;
 }
 
-// Asks for a block that was not launched; the answer lands in `to` and counts 16 bytes on `bar`.
+// The walk of attn_fwd.cuh by clusters: cluster c of G.
+template <class C>
+__device__ __forceinline__ int pair_first_sub(const FwdParams& p, int c)
+{
+    return C::PACKED ? 2 * c : c * p.walk_first;
+}
+template <class C>
+__device__ __forceinline__ int pair_next_sub(int s, const FwdParams& p, const SortTab* tab, int c, int G)
+{
+    if constexpr (C::PACKED) {
+        if (!(s & 1)) return s + 1;
+        if (tab == nullptr) return s + 2 * G - 1;
+        const int r = (s >> 1) / G + 1;                    // snake order, as snake_next_sub
+        return 2 * (r * G + ((r & 1) ? G - 1 - c : c));
+    } else {
+        return s + 1 + (((s + p.walk_a) % p.walk_m == 0) ? 0 : p.walk_step);
+    }
+}
+
+__device__ __forceinline__ uint32_t pair_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// One arrival on CTA 0's barrier at this place.  No thread reads what the other CTA's threads wrote: operands pass from
+// TMA, or behind their writers' proxy fences, to the tensor cores, and TMEM behind its fences.  So the order within
+// the CTA is enough (a release to the cluster took the compute warps a memory barrier at each: 1440 us became 2130).
+__device__ __forceinline__ void pair_arrive(uint64_t* bar)
+{
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)) : "memory");
+}
+// Asks for a block (cluster) that was not launched; the answer lands in `to`, with kBoth of both CTAs, and counts 16
+// bytes on `bar`.
+template <bool kBoth>
 __device__ __forceinline__ void steal_request(uint4* to, uint64_t* bar)
 {
-    fence_proxy_async_smem();                             // the last answer was read
-    mbar_arrive_expect_tx(smem_u32(bar), 16);
-    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                     smem_u32(to)),
-                 "r"(smem_u32(bar))
-                 : "memory");
+    if constexpr (kBoth)
+        asm volatile(
+            "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 "
+            "[%0], [%1];" ::"r"(smem_u32(to)),
+            "r"(smem_u32(bar))
+            : "memory");
+    else
+        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                         smem_u32(to)),
+                     "r"(smem_u32(bar))
+                     : "memory");
 }
-// The block's number, or -1: there are no more, and none may be asked for again.
+// The number of the block (cluster), or -1: there are no more, and none may be asked for again.
+template <int kCluster>
 __device__ __forceinline__ int steal_answer(const uint4* from)
 {
     uint32_t got, x;
@@ -100,7 +145,7 @@ __device__ __forceinline__ int steal_answer(const uint4* from)
         "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
         "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
         : "=&r"(got), "=&r"(x) : "r"(smem_u32(from)) : "memory");
-    return got ? (int)x : -1;
+    return got ? (int)x / kCluster : -1;
 }
 
 // One role's way through the units of its block.
@@ -113,17 +158,23 @@ struct DiffUnits {
     bool walks;                     // pairs dealt out in advance
     int su = 0, mine;
     uint32_t units = 0, asked = 0, answered = 0;
+    static constexpr bool kPair = C::CLUSTER == 2;
 
     __device__ __forceinline__ DiffUnits(const DiffFwdParams& dp, const SortTab* tab, DiffHand* hand,
                                          const volatile int* abort_flag)
-        : dp(dp), tab(tab), hand(hand), abort_flag(abort_flag), walks(C::PACKED && tab == nullptr), mine((int)blockIdx.x)
+        : dp(dp), tab(tab), hand(hand), abort_flag(abort_flag), walks(C::PACKED && tab == nullptr), mine((int)blockIdx.x / C::CLUSTER)
     {
     }
 
     __device__ __forceinline__ bool walk(Unit& w)
     {
         while (true) {
-            su = units++ == 0 ? first_sub<C>(dp.f) : next_sub<C>(su, dp.f, tab);
+            if constexpr (kPair) {
+                const int c = (int)blockIdx.x / 2, G = (int)gridDim.x / 2;
+                su = units++ == 0 ? pair_first_sub<C>(dp.f, c) : pair_next_sub<C>(su, dp.f, tab, c, G);
+            } else {
+                su = units++ == 0 ? first_sub<C>(dp.f) : next_sub<C>(su, dp.f, tab);
+            }
             if (su >= num_subs(dp.f, tab)) return false;
             if (unit_of<C>(su, dp.f, w, tab)) return true;
         }
@@ -143,6 +194,27 @@ struct DiffUnits {
         return u >= 0 && diff_unit<C>(u, dp, w, tab);
     }
 
+    __device__ __forceinline__ bool ask(bool& ok)
+    {
+        fence_proxy_async_smem();                         // the last answer was read
+        mbar_arrive_expect_tx(smem_u32(&hand->steal), 16);
+        ++asked;
+        if constexpr (kPair) {
+            if (pair_rank() != 0) {
+                pair_arrive(&hand->ready);
+                return true;
+            }
+            if (!mbar_wait(smem_u32(&hand->ready), (asked - 1) & 1, abort_flag, dp.f.timeout_ns)) {
+                --asked;                                  // was not sent
+                ok = false;
+                mine = -1;
+                return false;
+            }
+        }
+        steal_request<kPair>(&hand->stolen, &hand->steal);
+        return true;
+    }
+
     // The producer's (one lane): this block's own, then those of blocks that were not launched.  It asks for one when
     // the loads of the last are issued (asked for before them, a block with a long unit took a second at once, which
     // others would have come to sooner).
@@ -152,14 +224,13 @@ struct DiffUnits {
         bool there = false;
         for (bool first = units == 0; !there; first = false) {
             if (!first) {
-                steal_request(&hand->stolen, &hand->steal);
-                ++asked;
+                if (!ask(ok)) return false;
                 if (!mbar_wait(smem_u32(&hand->steal), answered & 1, abort_flag, dp.f.timeout_ns)) {
                     ok = false;
                     return false;
                 }
                 ++answered;
-                mine = steal_answer(&hand->stolen);
+                mine = steal_answer<C::CLUSTER>(&hand->stolen);
             }
             if (mine < 0) break;
             there = diff_unit<C>(mine, dp, w, tab);
@@ -176,18 +247,24 @@ struct DiffUnits {
     }
 
     // The producer's end: what was asked for lands, and after an abort the blocks that were not launched are not
-    // needed either.
+    // needed either (CTA 1's answer may not come then; a millisecond is enough for one that does).
     __device__ __forceinline__ void finish(bool ok)
     {
-        if (walks || (ok && asked == answered)) return;
+        if (walks || ok) return;
+        if (kPair && pair_rank() != 0) {
+            if (asked > answered) mbar_wait(smem_u32(&hand->steal), answered & 1, nullptr, 1000000ull);
+            return;
+        }
         while (mine >= 0) {
             if (asked == answered) {
-                steal_request(&hand->stolen, &hand->steal);
+                fence_proxy_async_smem();
+                mbar_arrive_expect_tx(smem_u32(&hand->steal), 16);
+                steal_request<false>(&hand->stolen, &hand->steal);
                 ++asked;
             }
             if (!mbar_wait(smem_u32(&hand->steal), answered & 1, nullptr, kCleanupTimeoutNs)) return;
             ++answered;
-            mine = steal_answer(&hand->stolen);
+            mine = steal_answer<C::CLUSTER>(&hand->stolen);
         }
     }
 };
@@ -202,14 +279,14 @@ inline int diff_grid(DiffFwdParams& dp, int sm_count)
     const long long fit = kGroupBytes / (per_token * p.N), pairs = fit < 1 ? 1 : fit > dp.Hkv ? dp.Hkv : fit;
     dp.group = (int)pairs * (p.H / dp.Hkv);               // heads (maps, parts) of so many key pairs
     if (C::PACKED && p.num_seqs > kSortMaxSeqs) {
-        const int grid = fwd_grid(p, sm_count);
+        const int grid = fwd_grid(p, sm_count / C::CLUSTER);
         set_fwd_walk(p, grid);
-        return grid;
+        return grid * C::CLUSTER;
     }
     constexpr int ROWS = C::NQ * C::BM;
     const long long units =
         C::PACKED ? ((long long)p.T / ROWS + p.num_seqs) * p.H : (long long)(p.BH / p.H) * p.num_qblk * p.H;
-    return units <= 0x7fffffffLL ? (int)units : 0;
+    return units * C::CLUSTER <= 0x7fffffffLL ? (int)units * C::CLUSTER : 0;
 }
 
 }  // namespace gb300

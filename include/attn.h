@@ -524,8 +524,9 @@ attn_status_t attn_rope_bf16(const void* q, const void* k, void* q_out, void* k_
  *   H a multiple of Hkv;  d in {64, 128} (else ATTN_ERR_UNSUPPORTED)
  *   scale, causal, window as attn_fwd_bf16
  * Scores, sums and outputs are fp32 until the last rounding; P_1 and P_2 are rounded to bf16, each
- * relative to its row's running maximum, for the product with V.  Every row of v has to be finite
- * (a masked key in a tile enters as 0 * v).
+ * relative to its row's running maximum, for the product with V, or at d = 128 without o2, in
+ * calls of enough work, their difference once: outputs with and without o2 may differ by these
+ * roundings.  Every row of v has to be finite (a masked key in a tile enters as 0 * v).
  *
  * attn_diff_fwd_bf16_varlen -- the same over packed sequences, as attn_fwd_bf16_varlen: q
  * [T, 2H, d], k [T, 2Hkv, d], v [T, Hkv, 2d], o and o2 [T, H, 2d], lse [2H, T].  Tokens outside
