@@ -70,7 +70,7 @@ struct alignas(16) DiffFwdBars {
     float inv[2][2][128];    // 1 / sum of the maps' rows, by the parity of the unit: one map's warps may be a
                              // unit ahead of the other's
 };
-constexpr int kDiffTabOffset = 3072;
+constexpr int kDiffTabOffset = 2816;
 static_assert(sizeof(DiffFwdBars) <= kDiffTabOffset, "barrier block");
 static_assert(kDiffTabOffset + sizeof(SortTab) <= 5120, "schedule table");
 

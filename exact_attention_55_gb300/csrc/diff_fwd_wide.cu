@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
 // work on both while the weights are made; CTA 1's tells it what has landed there.
 //
 // By itself a CTA would move 384 KB of shared memory a step (operands of 16 128 x 128 and 8 128 x 256 products of 16,
-// what TMA and the compute warps write): 3072 cycles at 128 bytes each, for 2048 of products.  A pair's CTA
+// what TMA and the compute warps write), at 128 bytes a cycle half as long again as the 2048 cycles of products.  A pair's CTA
 // moves 256 KB.
 template <bool PK>
 struct DiffOutCfg {
