@@ -121,7 +121,6 @@ attn_status_t diff_fwd(const void* q, const void* k, const void* v, const float*
     p.f.N = s.N;
     p.f.num_qblk = (int)blocks;
     p.f.num_units = (int)pairs;
-    p.f.unit_walk = packed ? 0 : single_unit_walk(s.causal, s.window, s.N, pairs, dev->sm_count);
     p.f.causal = s.causal ? 1 : 0;
     p.f.window = s.window > 0 && s.window < s.N ? s.window : 0;   // a wider one masks nothing
     p.f.c_log2 = (float)((double)s.scale * 1.4426950408889634);
@@ -147,17 +146,15 @@ attn_status_t diff_fwd(const void* q, const void* k, const void* v, const float*
     const long long steps = heads * ((mean + 127) / 128) * ((keys + 127) / 128);
     if (s.d == 128 && !o2 && mean > 256 && steps >= 25LL * dev->sm_count &&
         4 * seqs * s.H * ((mean + 255) / 256) >= 3LL * dev->sm_count) {
-        auto shape = [&](int heads_of, int walkers) {     // heads of one sequence; CTAs or pairs of them
+        auto shape = [&](int heads_of) {              // heads of one sequence
             DiffFwdParams r = p;
             r.f.H = heads_of;
             r.f.BH = (packed ? s.num_seqs : s.B) * heads_of;
             r.f.num_qblk = (int)(((long long)s.N + 255) / 256);
             r.f.num_units = r.f.BH * ((r.f.num_qblk + 1) / 2);
-            r.f.unit_walk = packed ? 0 : single_unit_walk(s.causal, s.window, s.N, r.f.num_units, walkers);
             return r;
         };
-        e = launch_diff_fwd_wide(m, shape(2 * s.H, dev->sm_count), shape(s.H, dev->sm_count / 2), dev->sm_count,
-                                 static_cast<cudaStream_t>(stream));
+        e = launch_diff_fwd_wide(m, shape(2 * s.H), shape(s.H), dev->sm_count, static_cast<cudaStream_t>(stream));
     } else {
         e = launch_diff_fwd(m, p, s.d, dev->sm_count, static_cast<cudaStream_t>(stream));
     }

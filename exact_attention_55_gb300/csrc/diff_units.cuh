@@ -84,25 +84,6 @@ __device__ __forceinline__ bool diff_unit(int u, const DiffFwdParams& dp, Unit& 
     return true;
 }
 
-// The walk of attn_fwd.cuh by clusters: cluster c of G.
-template <class C>
-__device__ __forceinline__ int pair_first_sub(const FwdParams& p, int c)
-{
-    return C::PACKED ? 2 * c : c * p.walk_first;
-}
-template <class C>
-__device__ __forceinline__ int pair_next_sub(int s, const FwdParams& p, const SortTab* tab, int c, int G)
-{
-    if constexpr (C::PACKED) {
-        if (!(s & 1)) return s + 1;
-        if (tab == nullptr) return s + 2 * G - 1;
-        const int r = (s >> 1) / G + 1;                    // snake order, as snake_next_sub
-        return 2 * (r * G + ((r & 1) ? G - 1 - c : c));
-    } else {
-        return s + 1 + (((s + p.walk_a) % p.walk_m == 0) ? 0 : p.walk_step);
-    }
-}
-
 __device__ __forceinline__ uint32_t pair_rank()
 {
     uint32_t r;
@@ -168,16 +149,15 @@ struct DiffUnits {
 
     __device__ __forceinline__ bool walk(Unit& w)
     {
-        while (true) {
-            if constexpr (kPair) {
-                const int c = (int)blockIdx.x / 2, G = (int)gridDim.x / 2;
-                su = units++ == 0 ? pair_first_sub<C>(dp.f, c) : pair_next_sub<C>(su, dp.f, tab, c, G);
-            } else {
-                su = units++ == 0 ? first_sub<C>(dp.f) : next_sub<C>(su, dp.f, tab);
+        if constexpr (C::PACKED) {
+            const int c = (int)blockIdx.x / C::CLUSTER, G = (int)gridDim.x / C::CLUSTER;
+            while (true) {
+                su = units++ == 0 ? 2 * c : (su & 1) ? su + 2 * G - 1 : su + 1;
+                if (su >= num_subs(dp.f, nullptr)) return false;
+                if (unit_of<C>(su, dp.f, w, nullptr)) return true;
             }
-            if (su >= num_subs(dp.f, tab)) return false;
-            if (unit_of<C>(su, dp.f, w, tab)) return true;
         }
+        return false;
     }
 
     // A consumer warp's next unit (all lanes).
@@ -278,11 +258,7 @@ inline int diff_grid(DiffFwdParams& dp, int sm_count)
     const long long per_token = 8LL * C::HEAD_DIM;        // bytes of a key pair and its value head
     const long long fit = kGroupBytes / (per_token * p.N), pairs = fit < 1 ? 1 : fit > dp.Hkv ? dp.Hkv : fit;
     dp.group = (int)pairs * (p.H / dp.Hkv);               // heads (maps, parts) of so many key pairs
-    if (C::PACKED && p.num_seqs > kSortMaxSeqs) {
-        const int grid = fwd_grid(p, sm_count / C::CLUSTER);
-        set_fwd_walk(p, grid);
-        return grid * C::CLUSTER;
-    }
+    if (C::PACKED && p.num_seqs > kSortMaxSeqs) return fwd_grid(p, sm_count / C::CLUSTER) * C::CLUSTER;
     constexpr int ROWS = C::NQ * C::BM;
     const long long units =
         C::PACKED ? ((long long)p.T / ROWS + p.num_seqs) * p.H : (long long)(p.BH / p.H) * p.num_qblk * p.H;
