@@ -520,6 +520,11 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
                                                 w.y0 + (w.t0 + x) * C::BN + i * 64, zv, pol_kv);
                 }
             }
+            // CTA 0's commits reach this CTA by themselves, ordered by no barrier of the pair: the last of each has to be
+            // here before shared memory is released (after an abort, the one that the MMA warp waits for)
+            for (uint32_t k = ring < C::NSLOT ? 0 : ring - C::NSLOT; k < ring && ok; ++k)
+                ok = mbar_wait(smem_u32(&bars->kv_empty[k % C::NSLOT]), (k / C::NSLOT) & 1, abort_flag, p.timeout_ns);
+            if (ok && uc > 0) ok = mbar_wait(smem_u32(&bars->q_empty), (uc - 1) & 1, abort_flag, p.timeout_ns);
             if (!ok) timed_out();
             units.finish(ok);
             // every copy issued lands before shared memory is released (after an abort the other CTA's word may not
@@ -625,10 +630,9 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
             ++uc;
         }
         if (!ok && lane == 0) timed_out();
-        if (rank == 0) {
-            pair_commit_warp(&bars->drain);
-            mbar_wait(smem_u32(&bars->drain), 0, nullptr, kCleanupTimeoutNs);
-        }
+        if (rank == 0) pair_commit_warp(&bars->drain);
+        // CTA 1 may have given up first: CTA 0 does when its own waits run out
+        mbar_wait(smem_u32(&bars->drain), 0, nullptr, rank == 0 ? kCleanupTimeoutNs : p.timeout_ns + kCleanupTimeoutNs);
         __syncwarp();
     } else if (warp < 8) {
         // both warpgroups work on every step, warpgroup wg on its half of the keys, a thread one row
@@ -738,13 +742,17 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
             if (lane == 0) pair_arrive(&bars->o_empty);
             ++uc;
         }
+        if (ok && h > 0) wait_all(&bars->w_free, (h - 1) & 1);     // CTA 0's last word on the weights
         if (!ok) timed_out();
     } else {
         regs_decrease<C::REG_CONTROL>();
     }
     tc_fence_before_sync();
     __syncthreads();
-    pair_sync();                                           // nothing of the other CTA's is on its way here
+    // The arrivals of the other CTA's threads are behind this barrier, its commits were waited for above, and its
+    // requests for units are awaited here.
+    pair_sync();
+    if (threadIdx.x == 0) bars->hand.last_answer();
     tc_fence_after_sync();
     if (warp == C::MMA_WARP)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

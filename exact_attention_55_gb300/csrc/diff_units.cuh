@@ -24,15 +24,24 @@ struct alignas(16) DiffHand {
     uint4 stolen;
     uint64_t full[2], empty[2], steal, ready;              // ready: CTA 1 can take an answer
     int unit[2];
+    int owed;                                              // CTA 1: 1 + the parity of an answer that may still come
 
     __device__ __forceinline__ void init(int consumer_warps)
     {
+        owed = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&full[i]), 1);
             mbar_init(smem_u32(&empty[i]), consumer_warps);
         }
         mbar_init(smem_u32(&steal), 1);
         mbar_init(smem_u32(&ready), 1);
+    }
+
+    // CTA 1, once CTA 0 sends no more requests (behind a barrier of both): an answer on its way lands.  One thread; it
+    // comes only after an abort, and a millisecond is enough for it.
+    __device__ __forceinline__ void last_answer()
+    {
+        if (owed != 0) mbar_wait(smem_u32(&steal), (uint32_t)(owed - 1), nullptr, 1000000ull);
     }
 };
 
@@ -227,12 +236,12 @@ struct DiffUnits {
     }
 
     // The producer's end: what was asked for lands, and after an abort the blocks that were not launched are not
-    // needed either (CTA 1's answer may not come then; a millisecond is enough for one that does).
+    // needed either.  CTA 0 may send the request that CTA 1 made ready for after CTA 1 gave up: see last_answer.
     __device__ __forceinline__ void finish(bool ok)
     {
         if (walks || ok) return;
         if (kPair && pair_rank() != 0) {
-            if (asked > answered) mbar_wait(smem_u32(&hand->steal), answered & 1, nullptr, 1000000ull);
+            if (asked > answered) hand->owed = 1 + (int)(answered & 1);
             return;
         }
         while (mine >= 0) {
