@@ -1,13 +1,19 @@
 // diff_fwd_wide.cu -- forward pass of differential attention at d = 128 in two launches: the rows'
-// log-sum-exps, then one product with both maps' weights.
+// largest scores and sums of weights (and the log-sum-exps), then one product with both maps' weights.
 //
-//     L_m = log sum exp(scale Q_m K_m^T + mask),   O = (exp(S_1 - L_1) - lam exp(S_2 - L_2)) V
+//     S_m = scale Q_m K_m^T + mask,  M_m = max S_m,  l_m = sum exp(S_m - M_m),
+//     O = (exp(S_1 - M_1) - lam l_1 / l_2 exp(S_2 - M_2)) V / l_1
 //
 // A value head of 256 columns leaves no room in TMEM for the two accumulators of diff_fwd.cu, which
 // therefore takes each half of it with scores of its own: 16 d products per pair of tokens (two scores of
-// 2 d and two products of 2 d for each half).  With the L_m known the maps' weights are subtracted before the
-// product, and one accumulator of 256 columns takes it: 4 d products for the L_m, 4 d for the scores
+// 2 d and two products of 2 d for each half).  With the sums known the maps' weights are subtracted before the
+// product, and one accumulator of 256 columns takes it: 4 d products for the sums, 4 d for the scores
 // again, 4 d for O: 12 d, with as many exponentials, and no rescaling in the second launch.
+//
+// What passes from the first launch to the second is M_m and l_m, not the log-sum-exp M_m + log l_m: that one is
+// rounded by half a step of its own size, an error of all of a row's weights (3 % where scores are some 2^18), while
+// M_m, whatever its rounding, is the same number in l_m and in the weights.  The four floats of a row and head lie
+// at the start of its output row, which the second launch overwrites when it has used them.
 // Measured, 16 heads over 4 key pairs, 16384 tokens, causal: 3020 us in one launch, 2035 in two
 // (1620 TFLOP/s of 12 d).
 #include <cuda_bf16.h>
@@ -21,7 +27,7 @@
 
 namespace gb300 {
 
-// ------------------------------------------------------------------ log-sum-exps
+// ------------------------------------------------------------------ largest scores and sums
 // A unit is 256 query rows of one map, as two tiles that share the stream of key tiles.  A step is 256 keys: a
 // 128 x 256 x 16 product of two shared-memory operands reads 12 KB in its 128 cycles, one of 128 x 128 the 8 KB
 // that shared memory has for its 64, with nothing left for TMA.  A tile's scores fill half of TMEM; the
@@ -318,6 +324,9 @@ __global__ void __launch_bounds__(DiffLseCfg<PK>::NUM_THREADS, 1)
                     const size_t at = C::PACKED ? (size_t)w.z * p.T + w.y0 : (size_t)w.z * p.N;
                     // a sum that is NaN stays one
                     p.lse[at + row] = (l == 0.0f ? NEG_INF : top + __log2f(l)) * 0.69314718055994531f;
+                    // for the second launch: 16 bytes at the start of the head's output row, 8 of them a map's
+                    const size_t orow = C::PACKED ? (size_t)(w.y0 + row) * dp.H + (w.z >> 1) : (size_t)(w.z >> 1) * p.N + row;
+                    reinterpret_cast<float2*>(static_cast<__nv_bfloat16*>(p.o) + orow * (2 * D))[w.z & 1] = make_float2(mb, l);
                 }
             }
             ++uc;
@@ -638,10 +647,8 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
         // both warpgroups work on every step, warpgroup wg on its half of the keys, a thread one row
         regs_increase<C::REG_COMPUTE>();
         constexpr int HC = C::BN / 2;
-        constexpr float LOG2E = 1.4426950408889634f;
         const int wg = warp >> 2, trow = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-        const float NEG_INF = -__int_as_float(0x7f800000);
         const float2 c2 = make_float2(p.c_log2, p.c_log2);
         uint8_t* w_row = w_smem + wg * C::CB + trow * 128;
         uint32_t h = 0, uc = 0;
@@ -658,17 +665,17 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
             diff_key_bounds(p, w.N, row, jlo, jhi);
             if (jlo > jhi) jlo = jhi;                     // a row behind the sequence, which is not stored
             const uint32_t span = (uint32_t)(jhi - jlo);
-            // minus the LSE of both maps (log2 units); a row whose every score is -inf has weights 0
-            float2 l1 = make_float2(0.0f, 0.0f), l2 = l1;
-            {
-                const size_t at = (C::PACKED ? (size_t)(2 * w.z) * p.T + w.y0 : (size_t)(2 * w.z) * p.N) + (valid ? row : 0);
-                const size_t step = C::PACKED ? (size_t)p.T : (size_t)p.N;
-                const float a = __ldcg(p.lse + at), b = __ldcg(p.lse + at + step);
-                l1.x = l1.y = a == NEG_INF ? 0.0f : -a * LOG2E;
-                l2.x = l2.y = b == NEG_INF ? 0.0f : -b * LOG2E;
-            }
-            const float lam = __ldg(dp.lam + head);
-            const float2 f2 = make_float2(-lam, -lam);
+            // Each warpgroup writes half of the head's columns of this row, behind both warpgroups' last weights, so no
+            // sooner than both have read what the first launch left there.
+            const size_t orow = C::PACKED ? (size_t)(w.y0 + row) * p.H + w.z : (size_t)w.z * p.N + row;
+            __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.o) + orow * (2 * C::D);
+            const float4 sums = valid ? __ldcg(reinterpret_cast<const float4*>(out)) : make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+            // M_1, l_1, M_2, l_2 (log2 units).  A map whose every score is -inf has weights and a sum of 0, and the
+            // other map is left.
+            const float2 m1 = make_float2(-sums.x, -sums.x), m2 = make_float2(-sums.z, -sums.z);
+            const float l1 = sums.y == 0.0f ? 1.0f : sums.y, inv1 = 1.0f / l1;
+            const float f = sums.w == 0.0f ? 0.0f : -__ldg(dp.lam + head) * (l1 / sums.w);
+            const float2 f2 = make_float2(f, f);
             for (int x = 0; x < w.n; ++x, ++h) {
                 const int c0 = (w.t0 + x) * C::BN;
                 if (!wait_all(&bars->s_full, h & 1)) break;
@@ -694,8 +701,8 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
                     const uint32_t first = (uint32_t)(c0 + wg * HC - jlo);
 #pragma unroll
                     for (int e = 0; e < HC; e += 2) {
-                        const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])), c2, l1);
-                        const float2 x2 = __ffma2_rn(make_float2(__uint_as_float(b[e]), __uint_as_float(b[e + 1])), c2, l2);
+                        const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])), c2, m1);
+                        const float2 x2 = __ffma2_rn(make_float2(__uint_as_float(b[e]), __uint_as_float(b[e + 1])), c2, m2);
                         float2 r = __ffma2_rn(make_float2(ex2(x2.x), ex2(x2.y)), f2, make_float2(ex2(x1.x), ex2(x1.y)));
                         if constexpr (kMasked) {
                             r.x = first + (uint32_t)e <= span ? r.x : 0.0f;
@@ -719,9 +726,6 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
             if (!ok) break;
             if (!wait_all(&bars->o_full, uc & 1)) break;
             tc_fence_after_sync();
-            // each warpgroup writes half of the head's columns
-            const size_t orow = C::PACKED ? (size_t)(w.y0 + row) * p.H + w.z : (size_t)w.z * p.N + row;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + orow * (2 * C::D) + wg * C::D;
 #pragma unroll
             for (int ch = 0; ch < C::D / 32; ++ch) {
                 uint32_t r[32];
@@ -733,8 +737,9 @@ __global__ void __launch_bounds__(DiffOutCfg<PK>::NUM_THREADS, 1)
                     uint32_t pk[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        pk[e] = pack_bf16x2(__uint_as_float(r[8 * v + 2 * e]), __uint_as_float(r[8 * v + 2 * e + 1]));
-                    reinterpret_cast<uint4*>(out + ch * 32)[v] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        pk[e] = pack_bf16x2(__uint_as_float(r[8 * v + 2 * e]) * inv1,
+                                            __uint_as_float(r[8 * v + 2 * e + 1]) * inv1);
+                    reinterpret_cast<uint4*>(out + wg * C::D + ch * 32)[v] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 }
             }
             tc_fence_before_sync();
