@@ -17,8 +17,8 @@
 //   * Warps 0-3 take 16 keys of each tile: S^T = K Q^T and O^T += V^T P^T as mma.m16n8k16, with 16
 //     keys (or value columns) by eight query rows.  With up to four rows of a map both maps share
 //     one product's eight columns, map 1 in 0-3 and map 2 in 4-7: K_1 meets (q_1 | 0) and K_2
-//     (0 | q_2) in the same accumulator, and V is multiplied once for both.  Otherwise the columns
-//     of a product are one map's, and V's fragments are used for both.
+//     (0 | q_2), each column takes its own map's sum, and V is multiplied once for both.  Otherwise the
+//     columns of a product are one map's, and V's fragments are used for both.
 //     A tcgen05 tile would be at least 64 rows high, mostly empty.
 // Measured, 16 sequences x 8 heads x 8192 keys of d = 128 (1.07 GB): 158.8 us = 6.76 TB/s.
 // Scores, weights' sums and O are fp32.  A weight, relative to a running maximum that it may pass by
@@ -352,7 +352,12 @@ __global__ void __launch_bounds__(kDdThreads, DdCfg<D, NT>::CTAS)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) xs[nt][e] = (s[nt][0][e] + s[nt][1][e]) * pw.c_log2;
+                            for (int e = 0; e < 4; ++e) {
+                                // one product for both maps: the other map's sums in this column are 0 times its keys, NaN
+                                // where one is not finite
+                                if constexpr (NT == 1) xs[nt][e] = (t >= 2 ? s[0][1][e] : s[0][0][e]) * pw.c_log2;
+                                else xs[nt][e] = (s[nt][0][e] + s[nt][1][e]) * pw.c_log2;
+                            }
                     }
                     if (edge) {
 #pragma unroll
