@@ -102,3 +102,27 @@ def test_rows_without_a_weight_in_one_map():
         # beside the roundings above: scores are fp32 sums of 128 products whose magnitudes add up to less than 2^4, so
         # off by 2^-13, and a weight by that much twice (in itself and in the sum)
         ref.check(o[0], want["o"], (ref.HALF + 2.0 ** -11) * (a + b) + ref.HALF * want["o"].abs(), f"o {name}")
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_uneven_lengths(causal):
+    """One long document beside many short ones, in both forms."""
+    m = fa()
+    lens, H, G = [50, 7, 2500] + [50] * 5, 64, 16
+    T, cu = sum(lens), torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    q, k, v = make((T, 2 * H, D), 96), make((T, 2 * G, D), 97), make((T, G, 2 * D), 98)
+    lam = weights(H)
+    dev = [t.cuda() for t in (q, k, v, lam, cu)]
+    one = m.attn_diff_fwd_bf16_varlen(*dev, max(lens), causal=causal, save_o2=True)
+    two = m.attn_diff_fwd_bf16_varlen(*dev, max(lens), causal=causal)
+    assert m.attn_get_device_status() == m.ATTN_OK
+    assert not torch.equal(one[0], two[0]), "the call without O_2 took one launch"
+    for s, n in enumerate(lens):
+        rows = slice(int(cu[s]), int(cu[s + 1]))
+        for h in (0, 63):
+            g = h // (H // G)
+            want = ref.forward(*(t[rows, a:b].transpose(0, 1) for t, a, b in ((q, 2 * h, 2 * h + 2), (k, 2 * g, 2 * g + 2), (v, g, g + 1))),
+                               lam[h:h + 1], 1 / math.sqrt(D), ref.allowed(n, causal, 0))
+            for name, (o, lse, _) in (("one", one), ("two", two)):
+                ref.check(o[rows, h:h + 1].transpose(0, 1), want["o"], want["o_bound"], f"o {name} {s} {h}")
+                ref.check(lse[2 * h:2 * h + 2, rows], want["lse"], want["lse_bound"], f"lse {name} {s} {h}")
