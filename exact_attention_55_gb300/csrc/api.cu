@@ -154,8 +154,6 @@ bool encode_3d_packed(CUtensorMap* m, const void* base, CUtensorMapDataType dt, 
     return r == CUDA_SUCCESS;
 }
 
-}  // namespace
-
 // How the batched forward's CTAs walk the work: 0 complementary pairs, 1 single units
 // with a plain stride, 2 single units in rotated rounds.  Pairs balance a causal mask.  Without one the units of a head cost
 // the same, and single units end in fewer rounds whenever whole pairs leave part of the
@@ -177,8 +175,6 @@ int single_unit_walk(int causal, int window, int N, long long pairs, int sm_coun
     if (window > 0) return unit_times <= pair_times ? 2 : 0;
     return unit_times < pair_times ? 1 : 0;
 }
-
-namespace {
 
 template <int D>
 attn_status_t run_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,

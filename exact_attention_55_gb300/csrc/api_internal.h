@@ -28,9 +28,6 @@ attn_status_t device_info(DeviceInfo** out);
 bool encode_rows(CUtensorMap* m, const void* base, int cols, long long rows, long long row_stride,
                  long long heads, long long head_stride, int box_rows);
 
-// The walk of a batched forward launch (see there).
-int single_unit_walk(int causal, int window, int N, long long pairs, int sm_count);
-
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace gb300
