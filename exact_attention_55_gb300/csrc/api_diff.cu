@@ -138,7 +138,8 @@ attn_status_t diff_fwd(const void* q, const void* k, const void* v, const float*
     // take at least 25 steps of 128 x 128 scores an SM and there are units for every pair of SMs, half of them again.
     // Measured, one against two, 16 heads over 4: causal 1536 tokens (16 steps) 41 us against 45, 2048 (29) 62
     // against 54, 4096 198 against 159; 64 x 768 (18) 53 against 59, 64 x 1024 (30) 78 against 71; 4 heads, 4096 tokens
-    // (64 units) 54 against 84; non-causal 64 x 512 (13) 39 against 35, 64 x 768 (30) 75 against 71.
+    // (64 units) 54 against 84; non-causal 64 x 512 (13) 39 against 35, 64 x 768 (30) 75 against 71.  So the few short calls without a mask that two
+    // launches would serve better are given up, and so are packed ones whose lengths' mean is short beside their longest.
     cudaError_t e;
     const long long mean = packed ? s.T / s.num_seqs : s.N, seqs = packed ? s.num_seqs : s.B;
     long long keys = s.causal ? mean / 2 + 64 : mean;     // that a row sees, with what its tiles mask

@@ -20,8 +20,9 @@
 //                                and dP = dO V_j^T, then dQ += dS K_j.
 // (The dV pass takes 64 queries a step at d = 128.)
 // 40 d products per pair of tokens where 20 d would do: dP is computed for each map and again for dQ,
-// the scores three times.  Both maps' scores, dP and accumulators together want 640 columns of
-// TMEM (d = 64; it has 512), and more shared memory than there is beside a ring.
+// the scores three times.  dK and dV of both maps in one unit want 640 columns of TMEM (d = 64: scores and
+// dP 384, accumulators 256), of which there are 512.  dK, or dQ, of both maps in one unit would share dP
+// and fit in TMEM (32 d in all); that form was not built.
 //
 // A step has two products of its own, S (Q K^T of the map; dV: of map 1) and X (dP; dV: map 2's
 // scores), and one accumulation that waits for the compute warps.  S has two TMEM buffers and X one, which
@@ -41,7 +42,9 @@
 // 6 KB of the 128 bytes a cycle there are.
 //
 // The three passes do not depend on one another, and each is launched as a dependent that starts
-// when all CTAs of the one before have started: its CTAs take the SMs that run out of units.
+// when all CTAs of the one before have started: its CTAs take the SMs that run out of units.  Against
+// launches one after another: 566 us to 574 (4 x 8 heads x 4096 tokens), 347 to 468 (packed, d = 128, where
+// shared heads leave few units), 14.2 to 24.9 (2 x 4 heads x 300).
 // Each waits for the one before at its end, so that the last one's end is the end of all.
 // Units are handed out by a counter, the costliest first: shared heads leave few of them (128 key
 // tiles for 152 SMs in an 8192-token step with two key pairs).

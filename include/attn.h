@@ -495,7 +495,7 @@ attn_status_t attn_decode_fp8_paged(const void* q, const void* k_cache, const vo
  *                 axes negative positions turn backwards
  *   inv_freq    : const float [rot / 2], radians per position; finite (else the pair is NaN).
  *                 The angle is computed from its fp32 value exactly to 2^-32 of a turn, plus
- *                 2^-38 of one at position 2^20 and frequencies up to 1
+ *                 2^-43 of one at position 2^20 and frequencies up to 1
  *   axis        : const int32 [rot / 2], clamped to [0, axes); null: all pairs on axis 0
  *   strides     : host array of 12, in elements, multiples of 8: batch, token and head of q, of
  *                 q_out, of k and of k_out (the last six are not read when Hk = 0)
@@ -558,7 +558,8 @@ attn_status_t attn_diff_fwd_bf16_varlen(const void* q, const void* k, const void
  *                  attn_diff_bwd_workspace_bytes(B, H, N) bytes; its contents do not matter.
  *                  Calls that may overlap need one each
  *   sizes, scale, causal, window as the forward call
- * Finite inputs are expected at every row, masked ones too, as in the forward pass.
+ * The weights are recomputed from lse as it is given: its rounding to fp32, 2^-24 of |LSE|, is a relative
+ * error of all of a row's weights.  Finite inputs are expected at every row, masked ones too, as in the forward pass.
  *
  * attn_diff_bwd_bf16_varlen -- the same over packed sequences, as attn_diff_fwd_bf16_varlen, with a
  * workspace of attn_diff_bwd_workspace_bytes(1, H, T) bytes.  Tokens outside every sequence may
@@ -597,8 +598,9 @@ attn_status_t attn_diff_bwd_bf16_varlen(const void* q, const void* k, const void
  *                its contents before and after do not matter.  Calls that may overlap need one
  *                each
  * What the cache holds at keys a query does not see (rows behind the sequence, pages behind it or
- * before its window) never reaches that query's outputs, NaN included; an infinity in V counts as
- * NaN where only some of the queries that share a tile see its key.  Scores, sums and O are fp32;
+ * before its window) never reaches that query's outputs, NaN included; an infinity in V at a key that
+ * it sees counts as NaN.  A key that is not finite reaches the LSE of its own map alone, and one whose
+ * score is -inf has no weight in it.  Scores, sums and O are fp32;
  * the weights are off by at most 2^-17 of themselves.  One pass over the cache serves H / Hkv * nq <= 16 rows of a
  * map (8 at d = 128); it is HBM-bound.  A table of another width may change O and LSE by their
  * roundings.
