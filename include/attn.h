@@ -599,7 +599,7 @@ attn_status_t attn_diff_bwd_bf16_varlen(const void* q, const void* k, const void
  *                each
  * What the cache holds at keys a query does not see (rows behind the sequence, pages behind it or
  * before its window) never reaches that query's outputs, NaN included; an infinity in V at a key that
- * it sees counts as NaN.  A key that is not finite reaches the LSE of its own map alone, and one whose
+ * it sees makes its column of O NaN or infinite.  A key that is not finite reaches the LSE of its own map alone, and one whose
  * score is -inf has no weight in it.  Scores, sums and O are fp32;
  * the weights are off by at most 2^-17 of themselves.  One pass over the cache serves H / Hkv * nq <= 16 rows of a
  * map (8 at d = 128); it is HBM-bound.  A table of another width may change O and LSE by their
